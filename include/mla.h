@@ -62,7 +62,7 @@ typedef enum {
   MLA_ERR_UNSUPPORTED = 2,    /* valid request outside the supported modes/shapes */
   MLA_ERR_WORKSPACE = 3,      /* workspace missing or smaller than mla_workspace_size() */
   MLA_ERR_CUDA = 4,           /* a CUDA runtime/driver call failed; message has the error */
-  MLA_ERR_DEVICE_BOUNDS = 5,  /* device status: a block-table entry outside [0, num_pages) */
+  MLA_ERR_DEVICE_BOUNDS = 5,  /* device status: a block-table entry outside [0, num_pages), or no room */
   MLA_ERR_DEVICE_TIMEOUT = 6  /* device status: a bounded wait inside a kernel gave up */
 } mla_status;
 
@@ -70,6 +70,7 @@ typedef enum {
 #define MLA_DEVICE_BAD_PAGE 0x1u     /* a page id outside [0, num_pages) was skipped (token masked) */
 #define MLA_DEVICE_TIMEOUT 0x2u      /* a pipeline wait exceeded its limit; results are invalid */
 #define MLA_DEVICE_BAD_SCHEDULE 0x4u /* the schedule did not match the arguments; results invalid */
+#define MLA_DEVICE_NO_ROOM 0x8u      /* mla_assign_pages ran out of free pages, table columns or slot entries */
 
 /* ABI version of this header (incremented on incompatible change). */
 #define MLA_ABI_VERSION 3
@@ -200,6 +201,78 @@ mla_status mla_fp8_cache_store(const void* x, int num_tokens, const int32_t* inp
                                int block_table_stride, void* kvcache, int num_pages, int page_size,
                                mla_stream_t stream);
 
+/* Pages and slots of one step's new tokens: the block table and the slot map
+ * that the cache writes and the decode calls of the step use, built on the
+ * device from the request lengths.
+ *
+ * Request b has max(cache_lengths[b], 0) cached tokens in the pages of its
+ * block-table row and receives max(new_tokens[b], 0) more.  Pages it lacks
+ * are taken from free_pages, from entry *free_cursor on, in the order of the
+ * requests; they go to the next columns of its row (all other entries of
+ * block_table are left as they are).  Written besides:
+ *   cache_seqlens[b] = cached + new tokens   (the lengths decode takes)
+ *   row_offsets[b]   = new tokens of the requests before b; row_offsets[batch] all
+ *   slot_map[t]      = page * 64 + position % 64 of new token t (tokens in the
+ *                      order of row_offsets), -1 for t past the last token
+ *   *next_cursor     = *free_cursor + the pages taken
+ * cache_seqlens may be cache_lengths itself and next_cursor free_cursor
+ * itself (a decode loop recorded as a graph advances both in place); any
+ * other overlap of an output is refused.
+ *
+ * A page that the free list or the table row has no room for gets table entry
+ * -1 (if the row has the column) and its tokens slot -1; a token past
+ * num_tokens gets no slot; either sets MLA_DEVICE_NO_ROOM.  A page id outside
+ * [0, num_pages) gives its tokens slot -1 and sets MLA_DEVICE_BAD_PAGE.
+ * The cursor is taken as clamped to [0, num_free].  Asynchronous on `stream`;
+ * all memory is the caller's; batch at most 16384. */
+typedef struct {
+  const int32_t* cache_lengths;   /* int32 [batch] */
+  const int32_t* new_tokens;      /* int32 [batch] */
+  int batch;
+  const int32_t* free_pages;      /* int32 [num_free], distinct page ids */
+  int num_free;
+  const int32_t* free_cursor;     /* int32 [1] */
+  int32_t* block_table;           /* int32 [batch, block_table_stride], updated */
+  int block_table_stride;
+  int num_pages;                  /* pages of the cache */
+  int num_tokens;                 /* entries of slot_map */
+  int32_t* cache_seqlens;         /* out: int32 [batch] */
+  int32_t* row_offsets;           /* out: int32 [batch + 1] */
+  int32_t* slot_map;              /* out: int32 [num_tokens] */
+  int32_t* next_cursor;           /* out: int32 [1] */
+} mla_assign_pages_args;
+
+mla_status mla_assign_pages(const mla_assign_pages_args* args, mla_stream_t stream);
+
+/* Cache write through a slot map: token i, its 512 latent values and 64 RoPE
+ * values from two row-strided tensors (rows of separate tensors, or slices of
+ * one wider projection), goes to cache row slot_map[i] = page * 64 + slot.
+ *
+ * Row formats: is_fp8 = 0, bf16 rows of 576 values, copied; is_fp8 = 1, the
+ * 656-byte rows of mla_fp8_cache_store, bit for bit as it writes them; with
+ * kv_scales, 640-byte rows of 512 E4M3 codes and 64 bf16 RoPE values, with
+ * scale = amax / 448 over the token's 512 latent values (1 for an all-zero
+ * token) in kv_scales and code = E4M3 of x / scale (float32 division), rounded
+ * to nearest even and saturated at 448.
+ * A negative slot is padding and is skipped; a slot past the cache is not
+ * written and sets MLA_DEVICE_BAD_PAGE.  Slots that are written must be
+ * distinct: a row named twice may end up with bytes of either token.  Rows
+ * that no slot names are left as they are.  Asynchronous on `stream`. */
+typedef struct {
+  const void* latent;             /* bf16 [num_tokens, 512], 16-byte aligned */
+  int64_t latent_stride;          /* elements between rows: a multiple of 8 */
+  const void* rope;               /* bf16 [num_tokens, 64], 16-byte aligned */
+  int64_t rope_stride;            /* elements between rows: a multiple of 8 */
+  const int32_t* slot_map;        /* int32 [num_tokens] */
+  int num_tokens;                 /* 0: nothing is launched */
+  void* kvcache;                  /* bf16 [num_pages,64,1,576], uint8 [num_pages,64,1,656 or 640], 16-byte aligned */
+  int num_pages, page_size;       /* page_size must be 64 */
+  int is_fp8;
+  float* kv_scales;               /* fp32 [num_pages, 64] for 640-byte rows, else NULL */
+} mla_cache_store_args;
+
+mla_status mla_cache_store(const mla_cache_store_args* args, mla_stream_t stream);
+
 /* Sparse prefill ("flash_mla_sparse_fwd(q, kv, indices, sm_scale)" of the
  * FlashMLA article's usage section): token-level sparse attention with no
  * batch dimension and an unpaged bf16 KV with one head.  For query token i
@@ -233,6 +306,76 @@ mla_status mla_sparse_prefill_workspace_size(int s_q, int h_q, int topk, size_t*
  * caller.  Host-side argument errors return without launching; device-side
  * problems set bits in the device status word (mla_get_device_status). */
 mla_status mla_sparse_prefill(const mla_sparse_prefill_args* args, mla_stream_t stream);
+
+/* Windowed decode: attention over the first `sinks` keys and the last
+ * `window` keys of each element (sinks: first tokens that stay visible when
+ * the window has moved past them).  Query token i of element b sits at
+ * position P_i = cache_seqlens[b] - s_q + i and sees key t < cache_seqlens[b]
+ * if t <= P_i and (t < sinks or t > P_i - window).  Results as mla_decode's;
+ * a row that sees no key gets out = 0 and lse = -inf.  Only the pages that
+ * hold keys some query token sees are read, so the others need no
+ * block-table entry.  A key that no query token of its element sees may hold
+ * anything; one that some of them see must be finite.
+ * Schedule, attention and combine are launched on `stream` by the one call;
+ * device-side problems set bits in the device status word. */
+typedef struct {
+  const void* q;                  /* bf16 [batch, s_q, h_q, 576], 16-byte aligned */
+  int batch, s_q, h_q;            /* s_q * h_q <= 1024 */
+  const void* kvcache;            /* as in mla_decode_args */
+  int num_pages, page_size;       /* page_size must be 64 */
+  const int32_t* block_table;     /* int32 [batch, block_table_stride] */
+  int block_table_stride;
+  const int32_t* cache_seqlens;   /* int32 [batch] */
+  float sm_scale;
+  int window;                     /* >= 1 */
+  int sinks;                      /* >= 0 */
+  int is_fp8;
+  const float* kv_scales;         /* fp32 [num_pages, 64] for 640-byte FP8 rows, else NULL */
+  void* workspace;                /* >= mla_window_decode_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  void* out;                      /* bf16 [batch, s_q, h_q, 512], 16-byte aligned */
+  float* lse;                     /* fp32 [batch, s_q, h_q], base 2 */
+} mla_window_decode_args;
+
+mla_status mla_window_decode_workspace_size(int batch, int h_q, int s_q, int is_fp8, size_t* bytes);
+mla_status mla_window_decode(const mla_window_decode_args* args, mla_stream_t stream);
+
+/* Shared-prefix decode: a batch whose elements share their first tokens (one
+ * system prompt, one document).  Every query row attends to the
+ * *prefix_length tokens of prefix_table and to its element's own
+ * cache_seqlens[b] tokens of block_table row b; with is_causal query token i
+ * sees own keys <= cache_seqlens[b] - s_q + i (and always the whole prefix).
+ * Results as mla_decode's over the two key sets in one softmax.  The prefix
+ * is read and multiplied once for 128 query rows of the whole batch at a
+ * time, whatever elements they belong to.  The prefix may end inside a page;
+ * own tokens start in pages of their own.  With an FP8 cache the prefix is
+ * turned into bf16 rows in the workspace first.  Keys past a length may hold
+ * anything; own keys must be finite.
+ * All launches are made on `stream` by the one call. */
+typedef struct {
+  const void* q;                  /* bf16 [batch, s_q, h_q, 576], 16-byte aligned */
+  int batch, s_q, h_q;            /* s_q * h_q <= 1024 */
+  const void* kvcache;            /* as in mla_decode_args */
+  int num_pages, page_size;       /* page_size must be 64 */
+  const int32_t* prefix_table;    /* int32 [prefix_table_len]: page ids of the prefix */
+  int prefix_table_len;
+  const int32_t* prefix_length;   /* int32 [1], device: tokens of the prefix */
+  const int32_t* block_table;     /* int32 [batch, block_table_stride]: pages of the own tokens */
+  int block_table_stride;
+  const int32_t* cache_seqlens;   /* int32 [batch]: own tokens */
+  float sm_scale;
+  int is_causal;
+  int is_fp8;
+  const float* kv_scales;         /* fp32 [num_pages, 64] for 640-byte FP8 rows, else NULL */
+  void* workspace;                /* >= mla_shared_prefix_decode_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  void* out;                      /* bf16 [batch, s_q, h_q, 512], 16-byte aligned */
+  float* lse;                     /* fp32 [batch, s_q, h_q], base 2 */
+} mla_shared_prefix_decode_args;
+
+mla_status mla_shared_prefix_decode_workspace_size(int batch, int h_q, int s_q, int prefix_table_len, int is_fp8,
+                                                   size_t* bytes);
+mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* args, mla_stream_t stream);
 
 /* FP8 top-k indexer (MAX kernels summary, MLA indexing kernels:
  * mla_fp8_index_top_k): picks, per query token, the topk cached keys that

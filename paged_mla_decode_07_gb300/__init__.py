@@ -27,6 +27,7 @@ D_QK = 576
 D_V = 512
 PAGE_SIZE = 64
 FP8_ROW_BYTES = 656
+MAX_PAGES = (2 ** 31 - 1) // PAGE_SIZE  # slots are int32
 
 MLA_OK = 0
 STATUS_NAMES = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_WORKSPACE",
@@ -34,6 +35,7 @@ STATUS_NAMES = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED",
 DEVICE_BAD_PAGE = 0x1
 DEVICE_TIMEOUT = 0x2
 DEVICE_BAD_SCHEDULE = 0x4
+DEVICE_NO_ROOM = 0x8
 
 _lock = threading.Lock()
 _lib = None
@@ -83,6 +85,53 @@ class IndexTopkArgs(ctypes.Structure):
     ]
 
 
+class AssignPagesArgs(ctypes.Structure):
+    """Mirror of ``mla_assign_pages_args`` in include/mla.h."""
+    _fields_ = [
+        ("cache_lengths", ctypes.c_void_p), ("new_tokens", ctypes.c_void_p), ("batch", ctypes.c_int),
+        ("free_pages", ctypes.c_void_p), ("num_free", ctypes.c_int), ("free_cursor", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("num_tokens", ctypes.c_int), ("cache_seqlens", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p),
+        ("slot_map", ctypes.c_void_p), ("next_cursor", ctypes.c_void_p),
+    ]
+
+
+class CacheStoreArgs(ctypes.Structure):
+    """Mirror of ``mla_cache_store_args`` in include/mla.h."""
+    _fields_ = [
+        ("latent", ctypes.c_void_p), ("latent_stride", ctypes.c_int64), ("rope", ctypes.c_void_p),
+        ("rope_stride", ctypes.c_int64), ("slot_map", ctypes.c_void_p), ("num_tokens", ctypes.c_int),
+        ("kvcache", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("is_fp8", ctypes.c_int), ("kv_scales", ctypes.c_void_p),
+    ]
+
+
+class WindowDecodeArgs(ctypes.Structure):
+    """Mirror of ``mla_window_decode_args`` in include/mla.h."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("batch", ctypes.c_int), ("s_q", ctypes.c_int), ("h_q", ctypes.c_int),
+        ("kvcache", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int),
+        ("cache_seqlens", ctypes.c_void_p), ("sm_scale", ctypes.c_float), ("window", ctypes.c_int),
+        ("sinks", ctypes.c_int), ("is_fp8", ctypes.c_int), ("kv_scales", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+    ]
+
+
+class SharedPrefixDecodeArgs(ctypes.Structure):
+    """Mirror of ``mla_shared_prefix_decode_args`` in include/mla.h."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("batch", ctypes.c_int), ("s_q", ctypes.c_int), ("h_q", ctypes.c_int),
+        ("kvcache", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("prefix_table", ctypes.c_void_p), ("prefix_table_len", ctypes.c_int), ("prefix_length", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int),
+        ("cache_seqlens", ctypes.c_void_p), ("sm_scale", ctypes.c_float), ("is_causal", ctypes.c_int),
+        ("is_fp8", ctypes.c_int), ("kv_scales", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+    ]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -121,6 +170,18 @@ def lib():
             L.mla_index_topk_workspace_size.restype = I
             L.mla_index_topk.argtypes = [ctypes.POINTER(IndexTopkArgs), P]
             L.mla_index_topk.restype = I
+            L.mla_assign_pages.argtypes = [ctypes.POINTER(AssignPagesArgs), P]
+            L.mla_assign_pages.restype = I
+            L.mla_cache_store.argtypes = [ctypes.POINTER(CacheStoreArgs), P]
+            L.mla_cache_store.restype = I
+            L.mla_window_decode_workspace_size.argtypes = [I, I, I, I, ctypes.POINTER(S)]
+            L.mla_window_decode_workspace_size.restype = I
+            L.mla_window_decode.argtypes = [ctypes.POINTER(WindowDecodeArgs), P]
+            L.mla_window_decode.restype = I
+            L.mla_shared_prefix_decode_workspace_size.argtypes = [I, I, I, I, I, ctypes.POINTER(S)]
+            L.mla_shared_prefix_decode_workspace_size.restype = I
+            L.mla_shared_prefix_decode.argtypes = [ctypes.POINTER(SharedPrefixDecodeArgs), P]
+            L.mla_shared_prefix_decode.restype = I
             _lib = L
     return _lib
 
@@ -154,6 +215,62 @@ def _need(t, name, dtype, device=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dimensions (got {tuple(t.shape)})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+class _On:
+    """The device of a call's tensors and the stream it runs on, current while the call allocates
+    and launches: memory that the call allocates then belongs to that stream in torch's allocator,
+    so it is not handed out again while the call's kernels still use it."""
+    __slots__ = ("handle", "ctx")
+
+    def __init__(self, dev, stream):
+        self.ctx = []
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            if stream.device != dev:
+                raise ValueError(f"stream must belong to {dev} (got {stream.device})")
+            self.ctx.append(torch.cuda.stream(stream))
+            self.handle = stream.cuda_stream
+        else:
+            self.handle = torch.cuda.current_stream(dev).cuda_stream
+            if dev.index != torch.cuda.current_device():
+                self.ctx.append(torch.cuda.device(dev))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return ctypes.c_void_p(self.handle)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _cuda_tensor(t, name):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _cache_format(kvcache, kv_scales, dev):
+    """(is_fp8) of a paged cache after checking its type, shape and scales."""
+    if kvcache.dtype == torch.uint8:
+        _need(kvcache, "kvcache", torch.uint8, dev, 4)
+        row = 640 if kv_scales is not None else FP8_ROW_BYTES
+        if kvcache.shape[-1] != row or kvcache.shape[2] != 1:
+            raise ValueError(f"FP8 kvcache must be [pages, page_size, 1, {row}] (got {tuple(kvcache.shape)})")
+        if kv_scales is not None:
+            _need(kv_scales, "kv_scales", torch.float32, dev)
+            if kv_scales.numel() != kvcache.shape[0] * kvcache.shape[1]:
+                raise ValueError("kv_scales must hold one scale per cached token")
+        return True
+    _need(kvcache, "kvcache", torch.bfloat16, dev, 4)
+    if kvcache.shape[-1] != D_QK or kvcache.shape[2] != 1:
+        raise ValueError(f"bf16 kvcache must be [pages, page_size, 1, {D_QK}] (got {tuple(kvcache.shape)})")
+    if kv_scales is not None:
+        raise ValueError("kv_scales given with a bf16 kvcache")
+    return False
 
 
 def metadata_size(batch: int, *, h_q: int, s_q: int, topk: int, is_fp8: bool) -> Tuple[int, int]:
@@ -307,6 +424,82 @@ def fp8_cache_store(x: torch.Tensor, input_row_offsets: torch.Tensor, cache_leng
                                      _stream(stream)))
 
 
+def assign_pages(cache_lengths: torch.Tensor, new_tokens: torch.Tensor, free_pages: torch.Tensor,
+                 free_cursor: torch.Tensor, block_table: torch.Tensor, num_tokens: int,
+                 num_pages: Optional[int] = None, cache_seqlens: Optional[torch.Tensor] = None,
+                 row_offsets: Optional[torch.Tensor] = None, slot_map: Optional[torch.Tensor] = None,
+                 next_cursor: Optional[torch.Tensor] = None, stream=None):
+    """Pages and slots of one step's new tokens (mla_assign_pages).
+
+    cache_lengths, new_tokens int32 [batch]; free_pages int32 [num_free], used from entry free_cursor
+    (int32 [1]) on; block_table int32 [batch, stride], its new entries written in place; num_tokens:
+    the entries of the slot map, the new tokens of all requests or more (a padded step); num_pages:
+    the cache's pages, to check page ids against.  Returns (cache_seqlens int32 [batch], row_offsets
+    int32 [batch + 1], slot_map int32 [num_tokens], next_cursor int32 [1]); cache_seqlens may be
+    given as cache_lengths and next_cursor as free_cursor, to advance them in place.
+    """
+    dev = _cuda_tensor(cache_lengths, "cache_lengths")
+    _need(cache_lengths, "cache_lengths", torch.int32, dev, 1)
+    _need(new_tokens, "new_tokens", torch.int32, dev, 1)
+    _need(free_pages, "free_pages", torch.int32, dev, 1)
+    _need(free_cursor, "free_cursor", torch.int32, dev, 1)
+    _need(block_table, "block_table", torch.int32, dev, 2)
+    batch, num_tokens = cache_lengths.shape[0], int(num_tokens)
+    if new_tokens.shape[0] != batch or block_table.shape[0] != batch or free_cursor.shape[0] != 1:
+        raise ValueError("new_tokens and block_table must have batch rows and free_cursor one entry")
+    if num_tokens < 0:
+        raise ValueError(f"num_tokens must be >= 0 (got {num_tokens})")
+    with _On(dev, stream) as handle:
+        def out(t, name, n):
+            if t is None:
+                return torch.empty(n, dtype=torch.int32, device=dev)
+            _need(t, name, torch.int32, dev, 1)
+            if t.shape[0] != n:
+                raise ValueError(f"{name} must have {n} entries (got {t.shape[0]})")
+            return t
+        cache_seqlens = out(cache_seqlens, "cache_seqlens", batch)
+        row_offsets = out(row_offsets, "row_offsets", batch + 1)
+        slot_map = out(slot_map, "slot_map", num_tokens)
+        next_cursor = out(next_cursor, "next_cursor", 1)
+        a = AssignPagesArgs(cache_lengths.data_ptr(), new_tokens.data_ptr(), batch, free_pages.data_ptr(),
+                            free_pages.shape[0], free_cursor.data_ptr(), block_table.data_ptr(),
+                            block_table.shape[1], MAX_PAGES if num_pages is None else int(num_pages), num_tokens,
+                            cache_seqlens.data_ptr(), row_offsets.data_ptr(), slot_map.data_ptr(),
+                            next_cursor.data_ptr())
+        _check(lib().mla_assign_pages(ctypes.byref(a), handle))
+    return cache_seqlens, row_offsets, slot_map, next_cursor
+
+
+def cache_store(latent: torch.Tensor, rope: torch.Tensor, slot_map: torch.Tensor, kvcache: torch.Tensor,
+                kv_scales: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write new tokens into the cache rows that slot_map names (mla_cache_store).
+
+    latent bf16 [num_tokens, 512] and rope bf16 [num_tokens, 64], each with any row stride that is a
+    multiple of 8 values (so both may be slices of one projection); slot_map int32 [num_tokens]
+    (page * 64 + slot, negative: skipped), the slots distinct; kvcache bf16 [num_pages, 64, 1, 576],
+    uint8 [.., 656] or, with kv_scales fp32 [num_pages, 64], uint8 [.., 640]; written in place.
+    """
+    dev = _cuda_tensor(latent, "latent")
+    n = latent.shape[0] if latent.dim() == 2 else -1
+    for t, name, width in ((latent, "latent", D_V), (rope, "rope", D_QK - D_V)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != dev:
+            raise ValueError(f"{name} must be a bfloat16 tensor on {dev}")
+        if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
+            raise ValueError(f"{name} must be [num_tokens, {width}] (got {tuple(t.shape)})")
+        if t.stride(1) != 1:
+            raise ValueError(f"the values of a row of {name} must be contiguous")
+    _need(slot_map, "slot_map", torch.int32, dev, 1)
+    if slot_map.shape[0] != n:
+        raise ValueError(f"slot_map must have {n} entries (got {slot_map.shape[0]})")
+    is_fp8 = _cache_format(kvcache, kv_scales, dev)
+    a = CacheStoreArgs(latent.data_ptr(), latent.stride(0) if n > 1 else D_V, rope.data_ptr(),
+                       rope.stride(0) if n > 1 else D_V, slot_map.data_ptr(), n, kvcache.data_ptr(),
+                       kvcache.shape[0], kvcache.shape[1], int(is_fp8),
+                       kv_scales.data_ptr() if kv_scales is not None else None)
+    with _On(dev, stream) as handle:
+        _check(lib().mla_cache_store(ctypes.byref(a), handle))
+
+
 def sparse_prefill_workspace_size(s_q: int, h_q: int, topk: int) -> int:
     n = ctypes.c_size_t()
     _check(lib().mla_sparse_prefill_workspace_size(s_q, h_q, topk, ctypes.byref(n)))
@@ -365,6 +558,118 @@ def sparse_prefill(q: torch.Tensor, kv: torch.Tensor, indices: torch.Tensor, sm_
     a.lse = lse.data_ptr()
     _check(lib().mla_sparse_prefill(ctypes.byref(a), _stream(stream)))
     return out.view(s_q, h_q, D_V), lse.view(s_q, h_q)
+
+
+def _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales):
+    """Checks what the decode calls over a paged cache share; returns (device, is_fp8)."""
+    dev = _cuda_tensor(q, "q")
+    _need(q, "q", torch.bfloat16, dev, 4)
+    if q.shape[3] != D_QK:
+        raise ValueError(f"q must have last dimension {D_QK} (got {q.shape[3]})")
+    if not isinstance(kvcache, torch.Tensor):
+        raise ValueError("kvcache must be a torch.Tensor")
+    is_fp8 = _cache_format(kvcache, kv_scales, dev)
+    _need(block_table, "block_table", torch.int32, dev, 2)
+    _need(cache_seqlens, "cache_seqlens", torch.int32, dev, 1)
+    if block_table.shape[0] != q.shape[0] or cache_seqlens.shape[0] != q.shape[0]:
+        raise ValueError("block_table and cache_seqlens must have batch rows")
+    return dev, is_fp8
+
+
+def _outputs(q, out, lse):
+    batch, s_q, h_q, _ = q.shape
+    if out is None:
+        out = torch.empty((batch, s_q, h_q, D_V), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((batch, s_q, h_q), dtype=torch.float32, device=q.device)
+    _need(out, "out", torch.bfloat16, q.device)
+    _need(lse, "lse", torch.float32, q.device)
+    if out.numel() != batch * s_q * h_q * D_V or lse.numel() != batch * s_q * h_q:
+        raise ValueError("out / lse have the wrong size")
+    return out, lse
+
+
+def _scratch(workspace, nbytes, dev):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace
+
+
+def window_decode_workspace_size(batch: int, *, h_q: int, s_q: int, is_fp8: bool) -> int:
+    """Scratch bytes of window_decode."""
+    n = ctypes.c_size_t()
+    _check(lib().mla_window_decode_workspace_size(batch, h_q, s_q, int(bool(is_fp8)), ctypes.byref(n)))
+    return n.value
+
+
+def window_decode(q: torch.Tensor, kvcache: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
+                  sm_scale: float, window: int, sinks: int = 0, kv_scales: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """Decode attention over the first ``sinks`` and the last ``window`` keys (mla_window_decode).
+
+    Arguments as decode()'s; query token i of an element of length L sits at position L - s_q + i and
+    sees key t <= that position if t < sinks or t > position - window.  Returns (out bf16
+    [b, s_q, h_q, 512], lse fp32 [b, s_q, h_q], base 2)."""
+    dev, is_fp8 = _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales)
+    batch, s_q, h_q, _ = q.shape
+    with _On(dev, stream) as handle:
+        out, lse = _outputs(q, out, lse)
+        n = ctypes.c_size_t()
+        if workspace is None:
+            _check(lib().mla_window_decode_workspace_size(batch, h_q, s_q, int(is_fp8), ctypes.byref(n)))
+        workspace = _scratch(workspace, n.value, dev)
+        a = WindowDecodeArgs(q.data_ptr(), batch, s_q, h_q, kvcache.data_ptr(), kvcache.shape[0], kvcache.shape[1],
+                             block_table.data_ptr(), block_table.shape[1], cache_seqlens.data_ptr(), float(sm_scale),
+                             int(window), int(sinks), int(is_fp8),
+                             kv_scales.data_ptr() if kv_scales is not None else None, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr())
+        _check(lib().mla_window_decode(ctypes.byref(a), handle))
+    return out.view(batch, s_q, h_q, D_V), lse.view(batch, s_q, h_q)
+
+
+def shared_prefix_decode_workspace_size(batch: int, *, h_q: int, s_q: int, prefix_table_len: int,
+                                        is_fp8: bool) -> int:
+    """Scratch bytes of shared_prefix_decode."""
+    n = ctypes.c_size_t()
+    _check(lib().mla_shared_prefix_decode_workspace_size(batch, h_q, s_q, prefix_table_len, int(bool(is_fp8)),
+                                                         ctypes.byref(n)))
+    return n.value
+
+
+def shared_prefix_decode(q: torch.Tensor, kvcache: torch.Tensor, prefix_table: torch.Tensor,
+                         prefix_length: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
+                         sm_scale: float, is_causal: bool = False, kv_scales: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """Decode attention of a batch that shares a prefix, read once for the batch (mla_shared_prefix_decode).
+
+    prefix_table int32 [pages] and prefix_length int32 [1] (on the device) name the shared tokens,
+    block_table and cache_seqlens each element's own; every query row attends to both.  Returns (out
+    bf16 [b, s_q, h_q, 512], lse fp32 [b, s_q, h_q], base 2)."""
+    dev, is_fp8 = _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales)
+    _need(prefix_table, "prefix_table", torch.int32, dev, 1)
+    _need(prefix_length, "prefix_length", torch.int32, dev, 1)
+    if prefix_length.shape[0] != 1:
+        raise ValueError("prefix_length must have one entry")
+    batch, s_q, h_q, _ = q.shape
+    with _On(dev, stream) as handle:
+        out, lse = _outputs(q, out, lse)
+        n = ctypes.c_size_t()
+        if workspace is None:
+            _check(lib().mla_shared_prefix_decode_workspace_size(batch, h_q, s_q, prefix_table.shape[0], int(is_fp8),
+                                                                 ctypes.byref(n)))
+        workspace = _scratch(workspace, n.value, dev)
+        a = SharedPrefixDecodeArgs(q.data_ptr(), batch, s_q, h_q, kvcache.data_ptr(), kvcache.shape[0],
+                                   kvcache.shape[1], prefix_table.data_ptr(), prefix_table.shape[0],
+                                   prefix_length.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                                   cache_seqlens.data_ptr(), float(sm_scale), int(bool(is_causal)), int(is_fp8),
+                                   kv_scales.data_ptr() if kv_scales is not None else None, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr())
+        _check(lib().mla_shared_prefix_decode(ctypes.byref(a), handle))
+    return out.view(batch, s_q, h_q, D_V), lse.view(batch, s_q, h_q)
 
 
 def index_topk_workspace_size(num_tokens: int, block_table_stride: int) -> int:

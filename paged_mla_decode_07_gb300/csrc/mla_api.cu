@@ -282,6 +282,130 @@ mla_status prefill_layout(int s_q, int h_q, int topk, Geometry* g, PrefillLayout
   L->total = L->lse_accum + lb;
   return MLA_OK;
 }
+
+// Windowed decode: schedule, slot prefix sums and split-KV partials.
+struct WindowLayout {
+  size_t num_splits, o_accum, lse_accum, total;  // (the schedule comes first)
+};
+mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, Geometry* g, WindowLayout* L) {
+  mla_status st = geometry(batch, h_q, s_q, 0, is_fp8, g);
+  if (st != MLA_OK) return st;
+  g->mode = is_fp8 ? 5 : 4;
+  g->tag = g->rpc | (g->mode << 8) | ((g->tile_tokens / kTileTokens) << 12) | (g->pair << 15);
+  size_t ob, lb;
+  workspace_layout(*g, &ob, &lb);
+  L->num_splits = align256(static_cast<size_t>(g->num_parts) * kSchedInts * sizeof(int32_t));
+  L->o_accum = L->num_splits + align256((static_cast<size_t>(g->num_problems) + 1) * sizeof(int32_t));
+  L->lse_accum = L->o_accum + ob;
+  L->total = L->lse_accum + lb;
+  return MLA_OK;
+}
+
+// Shared-prefix decode.  bf16 rows: one schedule over the prefix problems and
+// the own-key problems (`pre`, on CTA pairs).  FP8 rows: the prefix as bf16
+// rows and a table of its pages, one schedule over the prefix problems
+// (`pre`), one over the elements (`own`, on single CTAs).
+struct PrefixLayout {
+  Geometry pre, own;
+  int prefix_problems, blocks_per_elem, block_rows, prefix_slots, own_slots;
+  size_t sched, splits, own_sched, own_splits, o, lse, own_o, own_lse, table, rows, total;
+};
+mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_fp8, PrefixLayout* L) {
+  memset(L, 0, sizeof *L);
+  mla_status st = geometry(batch, h_q, s_q, 0, is_fp8, &L->own);
+  if (st != MLA_OK) return st;
+  int pairs = 0;
+  st = device_info(nullptr, nullptr, &pairs);
+  if (st != MLA_OK) return st;
+  const long long rows = static_cast<long long>(batch) * L->own.rows;
+  L->prefix_problems = static_cast<int>((rows + 127) / 128);
+  L->blocks_per_elem = is_fp8 ? 1 : (L->own.rows + 127) / 128;
+  L->block_rows = is_fp8 ? L->own.rows : (L->own.rows < 128 ? L->own.rows : 128);
+  const long long own_problems = static_cast<long long>(batch) * L->blocks_per_elem;
+  const long long np = L->prefix_problems + (is_fp8 ? 0 : own_problems);
+  if (np > kMaxProblems)
+    return fail(MLA_ERR_UNSUPPORTED, "batch*s_q*h_q = %lld query rows make %lld problems, more than the supported %d",
+                rows, np, kMaxProblems);
+  Geometry& g = L->pre;
+  g = L->own;
+  g.num_problems = static_cast<int>(np);
+  g.rows = 128;
+  g.rpc = 128;
+  g.row_groups = 1;
+  g.pair = 1;
+  g.mode = 6;
+  g.tile_tokens = 128;
+  g.tile_cost = 8;
+  const int forced = g_test_num_parts.load();
+  g.num_parts = forced > 0 ? forced : (pairs > 0 ? pairs : 1);
+  g.tag = g.rpc | (g.mode << 8) | (2 << 12) | (1 << 15);
+  // every piece takes a slot: one per problem and one more per part boundary
+  L->prefix_slots = L->prefix_problems + g.num_parts;
+  L->own_slots = static_cast<int>(own_problems) + (is_fp8 ? L->own.num_parts : g.num_parts);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  L->sched = take(static_cast<size_t>(g.num_parts) * kSchedInts * 4);
+  L->splits = take((static_cast<size_t>(np) + 1) * 4);
+  if (is_fp8) {
+    L->own_sched = take(static_cast<size_t>(L->own.num_parts) * kSchedInts * 4);
+    L->own_splits = take((static_cast<size_t>(batch) + 1) * 4);
+  }
+  L->o = take(static_cast<size_t>(L->prefix_slots) * 128 * kDv * 4);
+  L->lse = take(static_cast<size_t>(L->prefix_slots) * 128 * 4);
+  L->own_o = take(static_cast<size_t>(L->own_slots) * L->block_rows * kDv * 4);
+  L->own_lse = take(static_cast<size_t>(L->own_slots) * L->block_rows * 4);
+  if (is_fp8) {
+    L->table = take(static_cast<size_t>(prefix_pages) * 4);
+    L->rows = take(static_cast<size_t>(prefix_pages) * kPageSize * kDqk * 2);
+  }
+  L->total = at;
+  return MLA_OK;
+}
+
+// Checks that every dense decode call over a paged cache shares.
+mla_status check_paged(const void* q, const void* kvcache, const int32_t* block_table, const int32_t* cache_seqlens,
+                       const void* out, const float* lse, int num_pages, int page_size, int stride, float sm_scale,
+                       int is_fp8, const float* kv_scales) {
+  if (!q) return fail(MLA_ERR_INVALID_ARG, "q is NULL");
+  if (!kvcache) return fail(MLA_ERR_INVALID_ARG, "kvcache is NULL");
+  if (!block_table) return fail(MLA_ERR_INVALID_ARG, "block_table is NULL");
+  if (!cache_seqlens) return fail(MLA_ERR_INVALID_ARG, "cache_seqlens is NULL");
+  if (!out) return fail(MLA_ERR_INVALID_ARG, "out is NULL");
+  if (!lse) return fail(MLA_ERR_INVALID_ARG, "lse is NULL");
+  if (page_size != kPageSize) return fail(MLA_ERR_UNSUPPORTED, "page_size must be %d (got %d)", kPageSize, page_size);
+  if (num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages must be >= 1 (got %d)", num_pages);
+  if (num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages = %d exceeds 2^31 tokens", num_pages);
+  if (stride < 1) return fail(MLA_ERR_INVALID_ARG, "block_table_stride must be >= 1 (got %d)", stride);
+  if (!std::isfinite(sm_scale)) return fail(MLA_ERR_INVALID_ARG, "sm_scale is not finite");
+  if (is_fp8 != 0 && is_fp8 != 1) return fail(MLA_ERR_INVALID_ARG, "is_fp8 must be 0 or 1 (got %d)", is_fp8);
+  if (kv_scales && !is_fp8) return fail(MLA_ERR_INVALID_ARG, "kv_scales given with a bf16 cache (is_fp8 = 0)");
+  if (!aligned(q, 16)) return fail(MLA_ERR_INVALID_ARG, "q is not 16-byte aligned");
+  if (!aligned(kvcache, 16)) return fail(MLA_ERR_INVALID_ARG, "kvcache is not 16-byte aligned");
+  if (!aligned(out, 16)) return fail(MLA_ERR_INVALID_ARG, "out is not 16-byte aligned");
+  if (!aligned(lse, 4)) return fail(MLA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+  if (!aligned(block_table, 4)) return fail(MLA_ERR_INVALID_ARG, "block_table is not 4-byte aligned");
+  if (!aligned(cache_seqlens, 4)) return fail(MLA_ERR_INVALID_ARG, "cache_seqlens is not 4-byte aligned");
+  if (!aligned(kv_scales, 4)) return fail(MLA_ERR_INVALID_ARG, "kv_scales is not 4-byte aligned");
+  return MLA_OK;
+}
+mla_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (!workspace) return fail(MLA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
+  if (bytes < need) return fail(MLA_ERR_WORKSPACE, "workspace_bytes = %zu < %zu needed", bytes, need);
+  if (!aligned(workspace, 256)) return fail(MLA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  return MLA_OK;
+}
+// Tensor maps of the pair kernel over bf16 rows.
+mla_status encode_pair_maps(const void* q, long long q_rows, const void* kv, long long kv_rows, CUtensorMap* tm_q,
+                            CUtensorMap* tm_ks, CUtensorMap* tm_kv) {
+  mla_status st = encode_chunk_major_map(tm_q, q, q_rows, kNumChunks, "q");
+  if (st == MLA_OK) st = encode_chunk_major_map(tm_ks, kv, kv_rows, 3, "kvcache");
+  if (st == MLA_OK) st = encode_chunk_major_map(tm_kv, kv, kv_rows, 2, "kvcache");
+  return st;
+}
 }  // namespace
 
 extern "C" {
@@ -495,6 +619,127 @@ mla_status mla_fp8_cache_store(const void* x, int num_tokens, const int32_t* inp
   return ok();
 }
 
+mla_status mla_cache_store(const mla_cache_store_args* a, mla_stream_t stream) {
+  if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
+  if (a->num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %d)", a->num_tokens);
+  if (a->page_size != kPageSize) return fail(MLA_ERR_UNSUPPORTED, "page_size must be 64 (got %d)", a->page_size);
+  if (a->num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages must be >= 1 (got %d)", a->num_pages);
+  if (a->num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages = %d exceeds 2^31 tokens", a->num_pages);
+  if (a->is_fp8 != 0 && a->is_fp8 != 1) return fail(MLA_ERR_INVALID_ARG, "is_fp8 must be 0 or 1 (got %d)", a->is_fp8);
+  if (a->kv_scales && !a->is_fp8) return fail(MLA_ERR_INVALID_ARG, "kv_scales given with a bf16 cache (is_fp8 = 0)");
+  if (!a->kvcache) return fail(MLA_ERR_INVALID_ARG, "kvcache is NULL");
+  if (!aligned(a->kvcache, 16)) return fail(MLA_ERR_INVALID_ARG, "kvcache is not 16-byte aligned");
+  if (a->kv_scales && !aligned(a->kv_scales, 4)) return fail(MLA_ERR_INVALID_ARG, "kv_scales is not 4-byte aligned");
+  if (a->latent_stride < 0 || a->latent_stride % 8 != 0)
+    return fail(MLA_ERR_INVALID_ARG, "latent_stride must be a multiple of 8 elements (got %lld)",
+                static_cast<long long>(a->latent_stride));
+  if (a->rope_stride < 0 || a->rope_stride % 8 != 0)
+    return fail(MLA_ERR_INVALID_ARG, "rope_stride must be a multiple of 8 elements (got %lld)",
+                static_cast<long long>(a->rope_stride));
+  if (a->num_tokens == 0) return ok();
+  if (!a->latent) return fail(MLA_ERR_INVALID_ARG, "latent is NULL");
+  if (!a->rope) return fail(MLA_ERR_INVALID_ARG, "rope is NULL");
+  if (!a->slot_map) return fail(MLA_ERR_INVALID_ARG, "slot_map is NULL");
+  if (!aligned(a->latent, 16)) return fail(MLA_ERR_INVALID_ARG, "latent is not 16-byte aligned");
+  if (!aligned(a->rope, 16)) return fail(MLA_ERR_INVALID_ARG, "rope is not 16-byte aligned");
+  if (!aligned(a->slot_map, 4)) return fail(MLA_ERR_INVALID_ARG, "slot_map is not 4-byte aligned");
+  uint32_t* status = nullptr;
+  int sms = 0;
+  mla_status st = device_info(&status, &sms);
+  if (st != MLA_OK) return st;
+  SlotStoreParams p;
+  memset(&p, 0, sizeof p);
+  p.latent = static_cast<const uint16_t*>(a->latent);
+  p.rope = static_cast<const uint16_t*>(a->rope);
+  p.slots = a->slot_map;
+  p.kvcache = static_cast<uint8_t*>(a->kvcache);
+  p.kv_scales = a->kv_scales;
+  p.status = status;
+  p.latent_stride = a->latent_stride;
+  p.rope_stride = a->rope_stride;
+  p.num_tokens = a->num_tokens;
+  p.num_slots = a->num_pages * kPageSize;
+  p.is_fp8 = a->is_fp8;
+  cudaError_t e = launch_slot_store(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache store launch");
+  return ok();
+}
+
+mla_status mla_assign_pages(const mla_assign_pages_args* a, mla_stream_t stream) {
+  if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
+  if (a->batch < 1) return fail(MLA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", a->batch);
+  if (a->batch > kMaxProblems)
+    return fail(MLA_ERR_UNSUPPORTED, "batch = %d exceeds the supported %d requests", a->batch, kMaxProblems);
+  if (a->num_free < 0) return fail(MLA_ERR_INVALID_ARG, "num_free must be >= 0 (got %d)", a->num_free);
+  if (a->num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %d)", a->num_tokens);
+  if (a->num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages must be >= 1 (got %d)", a->num_pages);
+  if (a->num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages = %d exceeds 2^31 tokens", a->num_pages);
+  if (a->block_table_stride < 1)
+    return fail(MLA_ERR_INVALID_ARG, "block_table_stride must be >= 1 (got %d)", a->block_table_stride);
+  struct Arr {
+    const void* p;
+    long long n;  // int32 entries
+    const char* name;
+  };
+  const Arr in[4] = {{a->cache_lengths, a->batch, "cache_lengths"},
+                     {a->new_tokens, a->batch, "new_tokens"},
+                     {a->free_pages, a->num_free, "free_pages"},
+                     {a->free_cursor, 1, "free_cursor"}};
+  const Arr out[5] = {{a->block_table, static_cast<long long>(a->batch) * a->block_table_stride, "block_table"},
+                      {a->cache_seqlens, a->batch, "cache_seqlens"},
+                      {a->row_offsets, a->batch + 1ll, "row_offsets"},
+                      {a->slot_map, a->num_tokens, "slot_map"},
+                      {a->next_cursor, 1, "next_cursor"}};
+  for (const Arr& x : in) {
+    if (!x.p && x.n > 0) return fail(MLA_ERR_INVALID_ARG, "%s is NULL", x.name);
+    if (!aligned(x.p, 4)) return fail(MLA_ERR_INVALID_ARG, "%s is not 4-byte aligned", x.name);
+  }
+  for (const Arr& x : out) {
+    if (!x.p && x.n > 0) return fail(MLA_ERR_INVALID_ARG, "%s is NULL", x.name);
+    if (!aligned(x.p, 4)) return fail(MLA_ERR_INVALID_ARG, "%s is not 4-byte aligned", x.name);
+  }
+  // outputs overlap nothing, except that the lengths and the cursor may be
+  // updated in the very arrays they are read from
+  auto overlap = [](const Arr& x, const Arr& y) {
+    const uintptr_t xs = reinterpret_cast<uintptr_t>(x.p), ys = reinterpret_cast<uintptr_t>(y.p);
+    return x.n > 0 && y.n > 0 && xs < ys + 4 * static_cast<uintptr_t>(y.n) && ys < xs + 4 * static_cast<uintptr_t>(x.n);
+  };
+  for (int i = 0; i < 5; ++i) {
+    for (int k = 0; k < 4; ++k) {
+      const bool same = (i == 1 && k == 0 && out[i].p == in[k].p) || (i == 4 && k == 3 && out[i].p == in[k].p);
+      if (!same && overlap(out[i], in[k]))
+        return fail(MLA_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, in[k].name);
+    }
+    for (int k = 0; k < i; ++k)
+      if (overlap(out[i], out[k])) return fail(MLA_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, out[k].name);
+  }
+  uint32_t* status = nullptr;
+  int sms = 0;
+  mla_status st = device_info(&status, &sms);
+  if (st != MLA_OK) return st;
+  AssignPagesParams p;
+  memset(&p, 0, sizeof p);
+  p.cache_lengths = a->cache_lengths;
+  p.new_tokens = a->new_tokens;
+  p.free_pages = a->free_pages;
+  p.free_cursor = a->free_cursor;
+  p.block_table = a->block_table;
+  p.cache_seqlens = a->cache_seqlens;
+  p.row_offsets = a->row_offsets;
+  p.slot_map = a->num_tokens > 0 ? a->slot_map : nullptr;
+  p.next_cursor = a->next_cursor;
+  p.status = status;
+  p.batch = a->batch;
+  p.num_free = a->num_free;
+  p.block_table_stride = a->block_table_stride;
+  p.num_pages = a->num_pages;
+  p.num_tokens = a->num_tokens;
+  const bool in_place = a->cache_seqlens == a->cache_lengths || a->next_cursor == a->free_cursor;
+  cudaError_t e = launch_assign_pages(p, in_place, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "page assignment launch");
+  return ok();
+}
+
 mla_status mla_sparse_prefill_workspace_size(int s_q, int h_q, int topk, size_t* bytes) {
   if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes is NULL");
   if (topk < 1) return fail(MLA_ERR_INVALID_ARG, "topk must be >= 1 (got %d)", topk);
@@ -602,6 +847,268 @@ mla_status mla_sparse_prefill(const mla_sparse_prefill_args* a, mla_stream_t str
     e = launch_combine(cp, s, true);
     if (e != cudaSuccess) return cuda_fail(e, "combine kernel launch");
   }
+  return ok();
+}
+
+mla_status mla_window_decode_workspace_size(int batch, int h_q, int s_q, int is_fp8, size_t* bytes) {
+  if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes is NULL");
+  Geometry g{};
+  WindowLayout L{};
+  mla_status st = window_layout(batch, h_q, s_q, is_fp8, &g, &L);
+  if (st != MLA_OK) return st;
+  *bytes = L.total;
+  return ok();
+}
+
+mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t stream) {
+  if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
+  mla_status st = check_paged(a->q, a->kvcache, a->block_table, a->cache_seqlens, a->out, a->lse, a->num_pages,
+                              a->page_size, a->block_table_stride, a->sm_scale, a->is_fp8, a->kv_scales);
+  if (st != MLA_OK) return st;
+  if (a->window < 1) return fail(MLA_ERR_INVALID_ARG, "window must be >= 1 (got %d)", a->window);
+  if (a->sinks < 0) return fail(MLA_ERR_INVALID_ARG, "sinks must be >= 0 (got %d)", a->sinks);
+  Geometry g{};
+  WindowLayout L{};
+  st = window_layout(a->batch, a->h_q, a->s_q, a->is_fp8, &g, &L);
+  if (st != MLA_OK) return st;
+  st = check_workspace(a->workspace, a->workspace_bytes, L.total);
+  if (st != MLA_OK) return st;
+  uint32_t* status = nullptr;
+  st = device_info(&status, nullptr);
+  if (st != MLA_OK) return st;
+
+  CUtensorMap tm_q, tm_kv, tm_kv2;
+  const long long qrows = static_cast<long long>(a->batch) * a->s_q * a->h_q;
+  const long long cache_rows = static_cast<long long>(a->num_pages) * kPageSize;
+  if (g.pair) {
+    st = encode_pair_maps(a->q, qrows, a->kvcache, cache_rows, &tm_q, &tm_kv, &tm_kv2);
+  } else {
+    st = encode_rows_map(&tm_q, a->q, qrows, g.rpc, "q");
+    if (st == MLA_OK)
+      st = a->is_fp8 ? encode_byte_rows_map(&tm_kv, a->kvcache, cache_rows, a->kv_scales ? 640 : kFp8RowBytes, 32)
+                     : encode_rows_map(&tm_kv, a->kvcache, cache_rows, kPageSize, "kvcache");
+  }
+  if (st != MLA_OK) return st;
+
+  char* ws = static_cast<char*>(a->workspace);
+  int32_t* sched = reinterpret_cast<int32_t*>(ws);
+  int32_t* num_splits = reinterpret_cast<int32_t*>(ws + L.num_splits);
+  DecodeParams p;
+  memset(&p, 0, sizeof p);
+  p.block_table = a->block_table;
+  p.cache_seqlens = a->cache_seqlens;
+  p.sched = sched;
+  p.num_splits = num_splits;
+  p.kv_fp8 = static_cast<const uint8_t*>(a->kvcache);
+  p.out = a->out;
+  p.lse = a->lse;
+  p.o_accum = reinterpret_cast<float*>(ws + L.o_accum);
+  p.lse_accum = reinterpret_cast<float*>(ws + L.lse_accum);
+  p.status = status;
+  p.timeout_ns = watchdog_ns();
+  p.batch = a->batch;
+  p.s_q = a->s_q;
+  p.h_q = a->h_q;
+  p.num_pages = a->num_pages;
+  p.block_table_stride = a->block_table_stride;
+  p.num_problems = g.num_problems;
+  p.rows = g.rows;
+  p.row_groups = g.row_groups;
+  p.num_parts = g.num_parts;
+  p.max_slots = max_slots(g);
+  p.is_causal = 1;  // a window ends at its query token
+  p.window = a->window < kMaxWindow ? a->window : kMaxWindow;
+  p.sinks = a->sinks;
+  p.evict_first = (g.row_groups == 1 && !g.pair) ? 1 : 0;
+  p.sched_tag = g.tag;
+  p.debug_stall = g_test_debug_stall.load();
+  p.scale_log2 = a->sm_scale * 1.4426950408889634f;
+  p.kv_scales = a->kv_scales;
+  p.fp8_rope_off = a->kv_scales ? kDv : kFp8RopeOffset;
+
+  SchedSpec spec = {};
+  spec.seqlens = a->cache_seqlens;
+  spec.s_q = a->s_q;
+  spec.window = p.window;
+  spec.sinks = p.sinks;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_schedule(spec, g, sched, num_splits, s);
+  if (e != cudaSuccess) return cuda_fail(e, "schedule kernel launch");
+  e = g.pair ? launch_window_pair(tm_q, tm_kv, tm_kv2, p, s) : launch_decode(tm_q, tm_kv, p, g.rpc, g.mode, s);
+  if (e != cudaSuccess) return cuda_fail(e, "window decode kernel launch");
+  CombineParams cp;
+  memset(&cp, 0, sizeof cp);
+  cp.num_splits = num_splits;
+  cp.cache_seqlens = a->cache_seqlens;
+  cp.s_q = a->s_q;
+  cp.o_accum = p.o_accum;
+  cp.lse_accum = p.lse_accum;
+  cp.out = a->out;
+  cp.lse = a->lse;
+  cp.num_problems = g.num_problems;
+  cp.rows = g.rows;
+  cp.max_slots = p.max_slots;
+  cp.status = status;
+  e = launch_combine(cp, s, true);
+  if (e != cudaSuccess) return cuda_fail(e, "combine kernel launch");
+  return ok();
+}
+
+mla_status mla_shared_prefix_decode_workspace_size(int batch, int h_q, int s_q, int prefix_table_len, int is_fp8,
+                                                   size_t* bytes) {
+  if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes is NULL");
+  if (prefix_table_len < 1)
+    return fail(MLA_ERR_INVALID_ARG, "prefix_table_len must be >= 1 (got %d)", prefix_table_len);
+  if (prefix_table_len > kMaxPages)
+    return fail(MLA_ERR_UNSUPPORTED, "prefix_table_len = %d exceeds 2^31 tokens", prefix_table_len);
+  PrefixLayout L;
+  mla_status st = prefix_layout(batch, h_q, s_q, prefix_table_len, is_fp8, &L);
+  if (st != MLA_OK) return st;
+  *bytes = L.total;
+  return ok();
+}
+
+mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_stream_t stream) {
+  if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
+  mla_status st = check_paged(a->q, a->kvcache, a->block_table, a->cache_seqlens, a->out, a->lse, a->num_pages,
+                              a->page_size, a->block_table_stride, a->sm_scale, a->is_fp8, a->kv_scales);
+  if (st != MLA_OK) return st;
+  if (!a->prefix_table) return fail(MLA_ERR_INVALID_ARG, "prefix_table is NULL");
+  if (!a->prefix_length) return fail(MLA_ERR_INVALID_ARG, "prefix_length is NULL");
+  if (!aligned(a->prefix_table, 4)) return fail(MLA_ERR_INVALID_ARG, "prefix_table is not 4-byte aligned");
+  if (!aligned(a->prefix_length, 4)) return fail(MLA_ERR_INVALID_ARG, "prefix_length is not 4-byte aligned");
+  size_t need = 0;
+  st = mla_shared_prefix_decode_workspace_size(a->batch, a->h_q, a->s_q, a->prefix_table_len, a->is_fp8, &need);
+  if (st != MLA_OK) return st;
+  st = check_workspace(a->workspace, a->workspace_bytes, need);
+  if (st != MLA_OK) return st;
+  PrefixLayout L;
+  st = prefix_layout(a->batch, a->h_q, a->s_q, a->prefix_table_len, a->is_fp8, &L);
+  if (st != MLA_OK) return st;
+  uint32_t* status = nullptr;
+  int sms = 0;
+  st = device_info(&status, &sms);
+  if (st != MLA_OK) return st;
+
+  char* ws = static_cast<char*>(a->workspace);
+  const long long qrows = static_cast<long long>(a->batch) * L.own.rows;
+  const long long cache_rows = static_cast<long long>(a->num_pages) * kPageSize;
+  CUtensorMap tm_q, tm_ks, tm_kv, tm_own_q, tm_own_kv;
+  if (a->is_fp8) {
+    st = encode_pair_maps(a->q, qrows, ws + L.rows, static_cast<long long>(a->prefix_table_len) * kPageSize, &tm_q,
+                          &tm_ks, &tm_kv);
+    if (st == MLA_OK) st = encode_rows_map(&tm_own_q, a->q, qrows, L.own.rpc, "q");
+    if (st == MLA_OK)
+      st = encode_byte_rows_map(&tm_own_kv, a->kvcache, cache_rows, a->kv_scales ? 640 : kFp8RowBytes, 32);
+  } else {
+    st = encode_pair_maps(a->q, qrows, a->kvcache, cache_rows, &tm_q, &tm_ks, &tm_kv);
+  }
+  if (st != MLA_OK) return st;
+
+  int32_t* sched = reinterpret_cast<int32_t*>(ws + L.sched);
+  int32_t* splits = reinterpret_cast<int32_t*>(ws + L.splits);
+  int32_t* own_sched = reinterpret_cast<int32_t*>(ws + L.own_sched);
+  int32_t* own_splits = a->is_fp8 ? reinterpret_cast<int32_t*>(ws + L.own_splits) : splits + L.prefix_problems;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+
+  DecodeParams p;
+  memset(&p, 0, sizeof p);
+  p.block_table = a->block_table;
+  p.cache_seqlens = a->cache_seqlens;
+  p.sched = sched;
+  p.num_splits = splits;
+  p.o_accum = reinterpret_cast<float*>(ws + L.o);
+  p.lse_accum = reinterpret_cast<float*>(ws + L.lse);
+  p.own_o = reinterpret_cast<float*>(ws + L.own_o);
+  p.own_lse = reinterpret_cast<float*>(ws + L.own_lse);
+  p.status = status;
+  p.timeout_ns = watchdog_ns();
+  p.batch = a->batch;
+  p.s_q = a->s_q;
+  p.h_q = a->h_q;
+  p.num_pages = a->is_fp8 ? a->prefix_table_len : a->num_pages;
+  p.block_table_stride = a->block_table_stride;
+  p.num_problems = L.pre.num_problems;
+  p.rows = L.own.rows;
+  p.row_groups = 1;
+  p.num_parts = L.pre.num_parts;
+  p.max_slots = L.prefix_slots;
+  p.own_slots = L.own_slots;
+  p.block_rows = L.block_rows;
+  p.is_causal = a->is_causal ? 1 : 0;
+  p.sched_tag = L.pre.tag;
+  p.debug_stall = g_test_debug_stall.load();
+  p.scale_log2 = a->sm_scale * 1.4426950408889634f;
+  p.prefix_table = a->is_fp8 ? reinterpret_cast<const int32_t*>(ws + L.table) : a->prefix_table;
+  p.prefix_len = a->prefix_length;
+  p.prefix_pages = a->prefix_table_len;
+  p.prefix_problems = L.prefix_problems;
+  p.blocks_per_elem = L.blocks_per_elem;
+  p.total_rows = static_cast<int>(qrows);
+
+  SchedSpec spec = {};
+  spec.seqlens = a->cache_seqlens;
+  spec.s_q = a->s_q;
+  spec.prefix_len = a->prefix_length;
+  spec.prefix_problems = L.prefix_problems;
+  spec.blocks_per_elem = L.blocks_per_elem;
+  spec.always_partial = 1;
+  if (a->is_fp8) {
+    e = launch_prefix_rows(static_cast<const uint8_t*>(a->kvcache), a->kv_scales, a->prefix_table, a->prefix_length,
+                           a->prefix_table_len, a->num_pages, ws + L.rows, reinterpret_cast<int32_t*>(ws + L.table),
+                           status, sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix rows kernel launch");
+    SchedSpec own = {};
+    own.seqlens = a->cache_seqlens;
+    own.s_q = a->s_q;
+    own.always_partial = 1;
+    e = launch_schedule(own, L.own, own_sched, own_splits, s);
+    if (e != cudaSuccess) return cuda_fail(e, "schedule kernel launch");
+  }
+  e = launch_schedule(spec, L.pre, sched, splits, s);
+  if (e != cudaSuccess) return cuda_fail(e, "schedule kernel launch");
+  e = launch_prefix_pair(tm_q, tm_ks, tm_kv, p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "shared-prefix decode kernel launch");
+  if (a->is_fp8) {
+    DecodeParams o = p;
+    o.sched = own_sched;
+    o.num_splits = own_splits;
+    o.kv_fp8 = static_cast<const uint8_t*>(a->kvcache);
+    o.o_accum = p.own_o;
+    o.lse_accum = p.own_lse;
+    o.num_pages = a->num_pages;
+    o.num_problems = L.own.num_problems;
+    o.row_groups = L.own.row_groups;
+    o.num_parts = L.own.num_parts;
+    o.max_slots = L.own_slots;
+    o.always_partial = 1;
+    o.evict_first = L.own.row_groups == 1 ? 1 : 0;
+    o.sched_tag = L.own.tag;
+    o.kv_scales = a->kv_scales;
+    o.fp8_rope_off = a->kv_scales ? kDv : kFp8RopeOffset;
+    e = launch_decode(tm_own_q, tm_own_kv, o, L.own.rpc, L.own.mode, s);
+    if (e != cudaSuccess) return cuda_fail(e, "decode kernel launch");
+  }
+  PrefixCombineParams cp;
+  memset(&cp, 0, sizeof cp);
+  cp.prefix_splits = splits;
+  cp.prefix_o = p.o_accum;
+  cp.prefix_lse = p.lse_accum;
+  cp.own_splits = own_splits;
+  cp.own_o = p.own_o;
+  cp.own_lse = p.own_lse;
+  cp.block_rows = L.block_rows;
+  cp.blocks_per_elem = L.blocks_per_elem;
+  cp.rows = L.own.rows;
+  cp.total_rows = p.total_rows;
+  cp.prefix_slots = L.prefix_slots;
+  cp.own_slots = L.own_slots;
+  cp.out = a->out;
+  cp.lse = a->lse;
+  cp.status = status;
+  e = launch_prefix_combine(cp, s);
+  if (e != cudaSuccess) return cuda_fail(e, "combine kernel launch");
   return ok();
 }
 
@@ -728,6 +1235,8 @@ mla_status mla_get_device_status(mla_stream_t stream, uint32_t* flags) {
     return fail(MLA_ERR_DEVICE_BOUNDS, "a block-table entry was outside [0, num_pages) (status 0x%x)", v);
   if (v & MLA_DEVICE_BAD_SCHEDULE)
     return fail(MLA_ERR_INVALID_ARG, "the schedule did not match the decode arguments (status 0x%x)", v);
+  if (v & MLA_DEVICE_NO_ROOM)
+    return fail(MLA_ERR_DEVICE_BOUNDS, "new tokens did not get their pages or slots (status 0x%x)", v);
   return ok();
 }
 

@@ -152,7 +152,90 @@ __global__ void __launch_bounds__(kRowsPerBlock * 32) combine_kernel(const Combi
   if (lane == 0) p.lse[grow] = L;
 }
 
+// Shared-prefix merge: one warp per query row.  The row's pieces lie in two
+// runs of slots, the prefix under its block of 128 rows and its element's own
+// keys; they are merged as one list by the same formula.  An element without
+// own keys has none of the second, an empty prefix none of the first.
+__global__ void __launch_bounds__(kRowsPerBlock * 32) prefix_combine_kernel(const PrefixCombineParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr float kNegInf = -__builtin_huge_valf();
+  const int lane = threadIdx.x & 31;
+  const int64_t grow = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 5);
+  if (grow >= p.total_rows) return;
+  const int row = static_cast<int>(grow);
+  const int elem = row / p.rows, r = row % p.rows;
+  const int pp = row / 128;
+  const int op = elem * p.blocks_per_elem + r / p.block_rows;
+  const int base0 = p.prefix_splits[pp], n0 = p.prefix_splits[pp + 1] - base0;
+  // (both kinds may come from one schedule: the own slots count from the first own problem's)
+  const int base1 = p.own_splits[op] - p.own_splits[0], n1 = p.own_splits[op + 1] - p.own_splits[op];
+  if (base0 < 0 || n0 < 0 || base0 + n0 > p.prefix_slots || base1 < 0 || n1 < 0 || base1 + n1 > p.own_slots) {
+    if (lane == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
+    return;
+  }
+  const int64_t at0 = static_cast<int64_t>(base0) * 128 + row % 128;
+  const int64_t at1 = static_cast<int64_t>(base1) * p.block_rows + r % p.block_rows;
+  const int n = n0 + n1;
+  // piece i: its log-sum-exp and its 512 values
+  auto lse_of = [&](int i) {
+    return i < n0 ? p.prefix_lse[at0 + static_cast<int64_t>(i) * 128]
+                  : p.own_lse[at1 + static_cast<int64_t>(i - n0) * p.block_rows];
+  };
+  auto row_of = [&](int i) {
+    return reinterpret_cast<const float4*>((i < n0 ? p.prefix_o + (at0 + static_cast<int64_t>(i) * 128) * kDv
+                                                   : p.own_o + (at1 + static_cast<int64_t>(i - n0) * p.block_rows) * kDv) +
+                                           lane * 16);
+  };
+  float mx = kNegInf;
+  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, lse_of(i));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float L = kNegInf;
+  float acc[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  if (mx != kNegInf) {
+    float s = 0.f;
+    for (int i = lane; i < n; i += 32) s += exp2f(lse_of(i) - mx);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    L = mx + log2f(s);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float w = exp2f(lse_of(i) - L);
+      const float4* src = row_of(i);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float4 x = src[v];
+        acc[4 * v + 0] += w * x.x;
+        acc[4 * v + 1] += w * x.y;
+        acc[4 * v + 2] += w * x.z;
+        acc[4 * v + 3] += w * x.w;
+      }
+    }
+  }
+  uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + grow * kDv + lane * 16);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    out[k] = make_uint4(pack_bf16x2(acc[8 * k], acc[8 * k + 1]), pack_bf16x2(acc[8 * k + 2], acc[8 * k + 3]),
+                        pack_bf16x2(acc[8 * k + 4], acc[8 * k + 5]), pack_bf16x2(acc[8 * k + 6], acc[8 * k + 7]));
+  if (lane == 0) p.lse[grow] = L;
+}
+
 }  // namespace
+
+cudaError_t launch_prefix_combine(const PrefixCombineParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.total_rows + kRowsPerBlock - 1) / kRowsPerBlock));
+  cfg.blockDim = dim3(kRowsPerBlock * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_combine_kernel, p);
+}
 
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool pdl) {
   const int64_t rows = static_cast<int64_t>(p.num_problems) * p.rows;

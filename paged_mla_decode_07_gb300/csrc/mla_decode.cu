@@ -87,16 +87,20 @@ constexpr uint32_t kSoftmaxBar = 1;        // named barrier of the 128 softmax t
 // Kernel modes: dense decode over the bf16 cache, sparse (top-k) decode over
 // the FP8 cache, dense decode over the FP8 cache, sparse over bf16 rows (the
 // paged bf16 cache, or an unpaged KV for sparse prefill).
-constexpr int kModeDense = 0, kModeSparse = 1, kModeDenseFp8 = 2, kModeSparseBf16 = 3;
+// Windowed dense decode (first keys and a window) walks fewer pages and masks
+// more; the modes are their own so that the others keep their code.
+constexpr int kModeDense = 0, kModeSparse = 1, kModeDenseFp8 = 2, kModeSparseBf16 = 3, kModeWindow = 4,
+              kModeWindowFp8 = 5;
 
 template <int R, int MODE>
 struct Cfg {
   // Rows other than whole bf16 pages are gathered by four extra warps (FP8
   // rows dequantised, bf16 rows put into the swizzled operand layout); sparse
   // problems are (batch element, query token) pairs with their own indices
-  static constexpr bool kGather = MODE != kModeDense;
+  static constexpr bool kWindow = MODE == kModeWindow || MODE == kModeWindowFp8;
+  static constexpr bool kGather = MODE != kModeDense && MODE != kModeWindow;
   static constexpr bool kIndexed = MODE == kModeSparse || MODE == kModeSparseBf16;
-  static constexpr bool kFp8 = MODE == kModeSparse || MODE == kModeDenseFp8;
+  static constexpr bool kFp8 = MODE == kModeSparse || MODE == kModeDenseFp8 || MODE == kModeWindowFp8;
   // softmax warpgroups: with 64 rows two warpgroups split the rows
   static constexpr int kSmWG = (R == 64) ? 2 : 1;
   static constexpr int kGatherWarp0 = 4 + 4 * kSmWG;  // sparse: first FP8 gather warp
@@ -147,7 +151,7 @@ struct Cfg {
   // tile loads are the chain there) and bf16 row gathers (the in-place
   // swizzle); both measured faster that way, the 16-row dense path and the
   // FP8 gathers slower.
-  static constexpr bool kItemFull = (MODE == kModeSparseBf16) || (MODE == kModeDense && R == 64);
+  static constexpr bool kItemFull = (MODE == kModeSparseBf16) || ((MODE == kModeDense || MODE == kModeWindow) && R == 64);
   static constexpr int kFullItems = kItemFull ? 5 : 1;
   static constexpr int kNumFull = 3 * kFullItems;
   // sparse: raw FP8 rows of a tile land by row gathers in the upper chunk of
@@ -198,12 +202,16 @@ struct Bars {
 
 // Segment iterator shared by all roles: the part walks problems p0..p1 and,
 // inside each, a tile range.  All roles derive the identical sequence.
+template <bool WINDOW>
 struct Segments {
   int p0, t0, p1, t1, np, s_q, topk;
   const int32_t* seqlens;
+  int window, sinks;  // (WINDOW)
+  // pages of problem p, in the order its tiles take them
+  __device__ KeyWalk walk(int p) const { return key_walk(seqlens[p], s_q, window, sinks); }
   __device__ int last() const { return p1 < np ? p1 : np - 1; }
   __device__ void range(int p, int& tb, int& te) const {
-    int n = problem_tiles(seqlens, p, s_q, topk);
+    int n = WINDOW ? walk(p).pages : problem_tiles(seqlens, p, s_q, topk);
     tb = (p == p0) ? t0 : 0;
     te = (p == p1) ? t1 : n;
     if (te > n) te = n;
@@ -252,7 +260,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 // ---------------------------------------------------------------------------
 template <int R, int MODE>
 __device__ void producer(const CUtensorMap* tm_q, const CUtensorMap* tm_kv, const DecodeParams& p,
-                         const Segments& sg, int g, uint8_t* kv, uint8_t* qs, const Bars& bars,
+                         const Segments<Cfg<R, MODE>::kWindow>& sg, int g, uint8_t* kv, uint8_t* qs, const Bars& bars,
                          volatile uint8_t* flags, const Watchdog& wd) {
   // The whole producer warp runs this code converged; each copy is issued by
   // one elected lane (as for the MMAs, a lane issuing alone while its warp
@@ -284,9 +292,12 @@ __device__ void producer(const CUtensorMap* tm_q, const CUtensorMap* tm_kv, cons
     if (!C::kGather) {
       const int b = prob;
       const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.block_table_stride;
+      KeyWalk walk = {};
+      if (C::kWindow) walk = sg.walk(b);
       for (int j = tb; j < te; ++j, ++jt) {
-        // tile j is page j of the element
-        const int pg = j < p.block_table_stride ? bt[j] : -1;
+        // tile j is page j of the element (windowed: of its walk)
+        const int lp = C::kWindow ? walk.page(j) : j;
+        const int pg = lp < p.block_table_stride ? bt[lp] : -1;
         const bool ok = pg >= 0 && pg < p.num_pages;
         if (!ok && lane == 0) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
         uint64_t* fb = bars.full + C::kFullItems * fidx;
@@ -421,7 +432,7 @@ __device__ __forceinline__ void warp_commit(uint32_t bar) {
 }
 
 template <int R, int MODE>
-__device__ void s_issuer(const Segments& sg, uint32_t tmem, uint8_t* kv, uint8_t* qs, const Bars& bars,
+__device__ void s_issuer(const Segments<Cfg<R, MODE>::kWindow>& sg, uint32_t tmem, uint8_t* kv, uint8_t* qs, const Bars& bars,
                          const Watchdog& wd) {
   using C = Cfg<R, MODE>;
   constexpr uint32_t kIdS = idesc_bf16_f32(kTileTokens, R, 0, 0);  // A = K tile (K-major), B = Q (K-major)
@@ -495,7 +506,7 @@ done:
 }
 
 template <int R, int MODE>
-__device__ void pv_issuer(const Segments& sg, uint32_t tmem, uint8_t* kv, const Bars& bars, const Watchdog& wd) {
+__device__ void pv_issuer(const Segments<Cfg<R, MODE>::kWindow>& sg, uint32_t tmem, uint8_t* kv, const Bars& bars, const Watchdog& wd) {
   using C = Cfg<R, MODE>;
   constexpr uint32_t kIdO = idesc_bf16_f32(128, R, 1, C::kPMnMajor ? 1 : 0);  // A = V^T (MN-major), B = P
   constexpr uint64_t kHiV = smem_desc_hi(C::kKvChunkBytes, 1024);
@@ -594,7 +605,7 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }
 
 template <int R, int MODE>
-__device__ void gather_rows(const CUtensorMap* tm_rows, const DecodeParams& p, const Segments& sg, uint8_t* kv,
+__device__ void gather_rows(const CUtensorMap* tm_rows, const DecodeParams& p, const Segments<Cfg<R, MODE>::kWindow>& sg, uint8_t* kv,
                             const Bars& bars, volatile uint8_t* flags, const Watchdog& wd) {
   using C = Cfg<R, MODE>;
   using RG = Ring<C>;
@@ -668,10 +679,12 @@ __device__ void gather_rows(const CUtensorMap* tm_rows, const DecodeParams& p, c
       // page 0 standing in for an unusable page (its tokens are written as zeros)
       const int b = it.prob;
       const int L = sg.seqlens[b];
-      const int page = it.j < p.block_table_stride ? p.block_table[static_cast<int64_t>(b) * p.block_table_stride + it.j] : -1;
+      const int lp = C::kWindow ? sg.walk(b).page(it.j) : it.j;
+      const int page = lp < p.block_table_stride ? p.block_table[static_cast<int64_t>(b) * p.block_table_stride + lp] : -1;
       const bool page_ok = page >= 0 && page < p.num_pages;
       if (!page_ok && tok == 0 && h == 0) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
-      ok = page_ok && it.j * kTileTokens + tok < L;
+      const int t = lp * kTileTokens + tok;
+      ok = page_ok && t < L && (!C::kWindow || key_in_walk(t, L, p.s_q, p.window, p.sinks));
       row = (page_ok ? page : 0) * kPageSize + tok;
     }
     if (C::kFp8 && p.kv_scales) {
@@ -998,7 +1011,7 @@ __device__ __forceinline__ void half_reduce_scatter(const float (&v)[N], float* 
 }
 
 template <int R, int MODE>
-__device__ void softmax_epilogue(const DecodeParams& p, const Segments& sg, int g, int split0, uint32_t tmem,
+__device__ void softmax_epilogue(const DecodeParams& p, const Segments<Cfg<R, MODE>::kWindow>& sg, int g, int split0, uint32_t tmem,
                                  uint8_t* kv, const Bars& bars, float* aux, volatile uint8_t* flags,
                                  const Watchdog& wd) {
   using C = Cfg<R, MODE>;
@@ -1067,6 +1080,8 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments& sg, int 
 #pragma unroll
     for (int r = 0; r < RH; ++r) l[r] = 0.f;
     gsync();
+    KeyWalk walk = {};
+    if (C::kWindow) walk = sg.walk(b);
 
     for (int j = tb; j < te; ++j, ++jt) {
       const int sb = jt & 1;
@@ -1080,10 +1095,13 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments& sg, int 
         if (!group_ok(ok)) return;
       }
       tc_fence_after();
-      const int pos = j * kTileTokens + tl;  // dense: logical token of this thread
+      const int pos = (C::kWindow ? walk.page(j) : j) * kTileTokens + tl;  // dense: logical token of this thread
       // gathered modes: the gather warps' per-token flag (dense FP8: position
       // below the length and page usable); dense bf16: length and page flag
-      const bool tok_ok = C::kGather ? flags[(jt & 3) * 128 + tl] != 0 : (pos < L && flags[(jt & 3) * 128] != 0);
+      // (windowed: and seen by some query token)
+      const bool tok_ok = C::kGather ? flags[(jt & 3) * 128 + tl] != 0
+                                     : (pos < L && flags[(jt & 3) * 128] != 0 &&
+                                        (!C::kWindow || key_in_walk(pos, L, p.s_q, p.window, p.sinks)));
       if (tracer) MLA_TR(kTrSmSFull, jt);
 
       // this thread's token, its RH rows of S^T (the two halves of the warp
@@ -1104,7 +1122,9 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments& sg, int 
 
       // logits in log2 units; masked -> -inf.  Rows differ only where a causal
       // limit falls inside the tile: their limits come from shared memory.
-      const bool all_rows = tok_ok && (C::kIndexed || pos <= lim_min);
+      // (windowed: or where the window of the last row starts behind this key)
+      const bool all_rows = tok_ok && (C::kIndexed || pos <= lim_min) &&
+                            (!C::kWindow || pos < p.sinks || pos > L - 1 - p.window);
       const float sc = p.scale_log2;
       if (all_rows) {
 #pragma unroll
@@ -1115,7 +1135,14 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments& sg, int 
       } else {
 #pragma unroll
         for (int r4 = 0; r4 < RH / 4; ++r4) {
-          const int4 l4 = reinterpret_cast<const int4*>(lim_s + rh)[r4];
+          int4 l4 = reinterpret_cast<const int4*>(lim_s + rh)[r4];
+          if (C::kWindow && pos >= p.sinks) {
+            // this key has left the row's window: below every limit
+            if (pos <= l4.x - p.window) l4.x = -1;
+            if (pos <= l4.y - p.window) l4.y = -1;
+            if (pos <= l4.z - p.window) l4.z = -1;
+            if (pos <= l4.w - p.window) l4.w = -1;
+          }
           x[4 * r4] = pos <= l4.x ? x[4 * r4] * sc : kNegInf;
           x[4 * r4 + 1] = pos <= l4.y ? x[4 * r4 + 1] * sc : kNegInf;
           x[4 * r4 + 2] = pos <= l4.z ? x[4 * r4 + 2] * sc : kNegInf;
@@ -1242,7 +1269,7 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments& sg, int 
     gsync();
     // partial-result slots of this problem: none when this piece is the whole problem
     const int nsplit = p.num_splits[prob + 1] - p.num_splits[prob];
-    const bool final_out = nsplit <= 1;
+    const bool final_out = nsplit <= 1 && !p.always_partial;
     int slot = p.num_splits[prob] + (prob == sg.p0 ? split0 : 0);
     const int row0 = g * R + rb;
     bool write_ok = true;
@@ -1380,7 +1407,7 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
     g_mla_cta[3 * blockIdx.x + 2] = smid;
   }
 #endif
-  Segments sg;
+  Segments<C::kWindow> sg;
   int split0 = 0;
   // record 0 names the part count and geometry the schedule was made for;
   // only a matching schedule is read further
@@ -1399,6 +1426,8 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
   sg.s_q = p.s_q;
   sg.topk = p.topk;
   sg.seqlens = p.cache_seqlens;
+  sg.window = p.window;
+  sg.sinks = p.sinks;
   if (sg.p0 < 0 || sg.p0 > sg.np || sg.p1 < sg.p0 || sg.p1 > sg.np || sg.t0 < 0 || sg.t1 < 0) {
     if (threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
     sg.p0 = sg.np;  // nothing to do
@@ -1476,6 +1505,12 @@ size_t decode_smem_bytes(int rpc, int mode) {
     case 316: return Cfg<16, kModeSparseBf16>::kSmemBytes;
     case 332: return Cfg<32, kModeSparseBf16>::kSmemBytes;
     case 364: return Cfg<64, kModeSparseBf16>::kSmemBytes;
+    case 416: return Cfg<16, kModeWindow>::kSmemBytes;
+    case 432: return Cfg<32, kModeWindow>::kSmemBytes;
+    case 464: return Cfg<64, kModeWindow>::kSmemBytes;
+    case 516: return Cfg<16, kModeWindowFp8>::kSmemBytes;
+    case 532: return Cfg<32, kModeWindowFp8>::kSmemBytes;
+    case 564: return Cfg<64, kModeWindowFp8>::kSmemBytes;
   }
   return 0;
 }
@@ -1495,6 +1530,12 @@ cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, con
     case 316: return launch_one<16, kModeSparseBf16>(tm_q, tm_kv, p, stream);
     case 332: return launch_one<32, kModeSparseBf16>(tm_q, tm_kv, p, stream);
     case 364: return launch_one<64, kModeSparseBf16>(tm_q, tm_kv, p, stream);
+    case 416: return launch_one<16, kModeWindow>(tm_q, tm_kv, p, stream);
+    case 432: return launch_one<32, kModeWindow>(tm_q, tm_kv, p, stream);
+    case 464: return launch_one<64, kModeWindow>(tm_q, tm_kv, p, stream);
+    case 516: return launch_one<16, kModeWindowFp8>(tm_q, tm_kv, p, stream);
+    case 532: return launch_one<32, kModeWindowFp8>(tm_q, tm_kv, p, stream);
+    case 564: return launch_one<64, kModeWindowFp8>(tm_q, tm_kv, p, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -189,30 +189,122 @@ static_assert(kBCount * 8 <= kPairBarBytes, "barrier area");
 
 // Segment iterator over the part's problems (128-token tiles); every role
 // derives the identical sequence.
+//
+// Variants of the dense kernel: kPlain as scheduled by mla_get_metadata;
+// kWindowed walks the pages of the first keys and of the window; kPrefixed
+// takes a batch that shares a prefix as two kinds of problems, the prefix
+// under 128 consecutive query rows of the batch, and each element's own keys
+// under its rows, 128 at a time (the row group is part of the problem).
+constexpr int kPlain = 0, kWindowed = 1, kPrefixed = 2;
+
+template <int VAR>
 struct PairSeg {
   int p0, t0, p1, t1, np, s_q, topk;
   const int32_t* seqlens;
+  int window, sinks;                     // (kWindowed)
+  const int32_t* prefix_len;             // (kPrefixed)
+  int prefix_problems, blocks_per_elem;  // (kPrefixed)
   __device__ int last() const { return p1 < np ? p1 : np - 1; }
+  __device__ int tiles(int p) const {
+    if (VAR == kWindowed) return (key_walk(seqlens[p], s_q, window, sinks).pages + 1) / 2;
+    if (VAR == kPrefixed) {
+      const int L = p < prefix_problems ? prefix_len[0] : seqlens[(p - prefix_problems) / blocks_per_elem];
+      return L > 0 ? (L + kPairTile - 1) / kPairTile : 0;
+    }
+    return problem_tiles(seqlens, p, s_q, topk, kPairTile);
+  }
   __device__ void range(int p, int& tb, int& te) const {
-    const int n = problem_tiles(seqlens, p, s_q, topk, kPairTile);
+    const int n = tiles(p);
     tb = (p == p0) ? t0 : 0;
     te = (p == p1) ? t1 : n;
     if (te > n) te = n;
   }
 };
 
-// Page of half h (0, 1) of tile j of element b: its id, or -1 when it holds
-// no cached token or its block-table entry is unusable (flagged).
-__device__ __forceinline__ int tile_page(const DecodeParams& p, int b, int L, int j, int h, bool flag) {
-  const int pi = 2 * j + h;
-  if (pi * kPageSize >= L) return -1;
-  const int pg = pi < p.block_table_stride ? p.block_table[static_cast<int64_t>(b) * p.block_table_stride + pi] : -1;
-  if (pg < 0 || pg >= p.num_pages) {
-    if (flag) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
-    return -1;
+// What a dense problem reads and where its rows are.
+template <int VAR>
+struct PairView {
+  int L;                 // keys
+  const int32_t* table;  // page ids by logical page; NULL: page i is page i of the map
+  int table_len;
+  int64_t row0;          // query row (of the whole call) of the row group's first row
+  int rows;              // rows of the row group from there on that exist (may exceed 128)
+  int in_elem;           // row of its element that row0 is
+  bool causal;
+  KeyWalk walk;          // (kWindowed)
+
+  __device__ PairView() {}
+  __device__ PairView(const DecodeParams& p, const PairSeg<VAR>& sg, int prob, int g) {
+    if (VAR == kPrefixed) {
+      if (prob < p.prefix_problems) {
+        L = p.prefix_len[0];
+        table = p.prefix_table;
+        table_len = p.prefix_pages;
+        row0 = static_cast<int64_t>(prob) * 2 * kPairRows;
+        rows = p.total_rows - static_cast<int>(row0);
+        in_elem = 0;
+        causal = false;
+      } else {
+        const int b = (prob - p.prefix_problems) / p.blocks_per_elem, gg = (prob - p.prefix_problems) % p.blocks_per_elem;
+        L = sg.seqlens[b];
+        table = p.block_table + static_cast<int64_t>(b) * p.block_table_stride;
+        table_len = p.block_table_stride;
+        in_elem = gg * 2 * kPairRows;
+        row0 = static_cast<int64_t>(b) * p.rows + in_elem;
+        rows = p.rows - in_elem;
+        causal = p.is_causal != 0;
+      }
+    } else {
+      L = sg.seqlens[prob];
+      table = p.block_table + static_cast<int64_t>(prob) * p.block_table_stride;
+      table_len = p.block_table_stride;
+      in_elem = g * 2 * kPairRows;
+      row0 = static_cast<int64_t>(prob) * p.rows + in_elem;
+      rows = p.rows - in_elem;
+      causal = p.is_causal != 0;
+      if (VAR == kWindowed) walk = key_walk(L, sg.s_q, sg.window, sg.sinks);
+    }
   }
-  return pg;
-}
+  // logical page of half h (0, 1) of tile j; -1 past the last one
+  __device__ __forceinline__ int logical(int j, int h) const {
+    const int i = 2 * j + h;
+    if (VAR == kWindowed) return i < walk.pages ? walk.page(i) : -1;
+    return i * kPageSize < L ? i : -1;
+  }
+  // Its page id, or -1 when it holds no cached token or its block-table
+  // entry is unusable (flagged when asked).
+  __device__ __forceinline__ int page(const DecodeParams& p, int j, int h, bool flag) const {
+    const int pi = logical(j, h);
+    if (pi < 0) return -1;
+    const int pg = pi < table_len ? (VAR == kPrefixed && !table ? pi : table[pi]) : -1;
+    if (pg < 0 || pg >= p.num_pages) {
+      if (flag) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
+      return -1;
+    }
+    return pg;
+  }
+  // whether some row of the problem sees key t
+  __device__ __forceinline__ bool seen(int t, const PairSeg<VAR>& sg) const {
+    return t < L && (VAR != kWindowed || key_in_walk(t, L, sg.s_q, sg.window, sg.sinks));
+  }
+  // Tile j holds keys that no row sees beside keys that are seen: their slots
+  // may hold anything (e.g. NaN), so the value rows of those tokens are
+  // zeroed after the copy lands, before the PV MMAs.
+  __device__ __forceinline__ bool tail(int j, const PairSeg<VAR>& sg) const {
+    if (VAR == kWindowed) {
+      const int past = L - sg.s_q - sg.window;  // the last key that only the first keys' rule can show
+      for (int h = 0; h < 2; ++h) {
+        const int lp = logical(j, h);
+        if (lp < 0) continue;
+        const int first = lp * kPageSize, last = first + kPageSize - 1;
+        if (last >= L) return true;
+        if (!(sg.sinks > past || last < sg.sinks || first > past)) return true;
+      }
+      return false;
+    }
+    return L > 0 && (L & (kPageSize - 1)) != 0 && j == (L - 1) / kPairTile;
+  }
+};
 
 __device__ __forceinline__ void tma3(uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2,
                                      uint64_t policy) {
@@ -231,13 +323,6 @@ __device__ __forceinline__ void tma3_to_even(uint32_t dst, const void* map, uint
       " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
-}
-
-// Tile j of a problem of L tokens holds a page that straddles the length:
-// its slots past the length may hold anything (e.g. NaN), so the value rows
-// of those tokens are zeroed after the copy lands, before the PV MMAs.
-__device__ __forceinline__ bool tail_tile(int L, int j) {
-  return L > 0 && (L & (kPageSize - 1)) != 0 && j == (L - 1) / kPairTile;
 }
 
 // Prefetch a box of a tensor map into L2 (no shared memory involved).
@@ -321,9 +406,9 @@ __device__ __forceinline__ void warp_arrive_even(int rank, uint32_t bar_local, u
 // warp 0: Q of each segment and (dense) the score operand: the CTA's own
 // page of each tile
 // ---------------------------------------------------------------------------
-template <bool SPARSE>
+template <bool SPARSE, int VAR>
 __device__ void pair_producer_ks(const CUtensorMap* tm_q, const CUtensorMap* tm_ks, const DecodeParams& p,
-                                 const PairSeg& sg, int g, int rank, uint32_t smem, uint32_t bars, uint32_t bars_even,
+                                 const PairSeg<VAR>& sg, int g, int rank, uint32_t smem, uint32_t bars, uint32_t bars_even,
                                  const Watchdog& wd) {
   // The even CTA arms its Q and score-operand barriers with the bytes of
   // both CTAs; the odd CTA's copies complete on them directly.  A page that
@@ -341,7 +426,8 @@ __device__ void pair_producer_ks(const CUtensorMap* tm_q, const CUtensorMap* tm_
     if (q_armed > 0 && !pair_wait(bars + 8 * kBQEmpty, (q_armed - 1) & 1, wd)) goto drain;
     {
       // this CTA's 64 query rows, all nine chunks, in one copy
-      const int row0 = prob * p.rows + g * 2 * kPairRows + rank * kPairRows;
+      const int row0 = VAR == kPrefixed ? static_cast<int>(PairView<VAR>(p, sg, prob, g).row0) + rank * kPairRows
+                                        : prob * p.rows + g * 2 * kPairRows + rank * kPairRows;
       if (lane == 0) {
         if (rank == 0) {
           mbar_arrive_expect_tx_u32(bars + 8 * kBQFull, 2 * kNumChunks * kPairChunk);
@@ -355,16 +441,15 @@ __device__ void pair_producer_ks(const CUtensorMap* tm_q, const CUtensorMap* tm_
     }
     if (SPARSE) continue;  // the gather warps fill the score operand
     {
-      const int b = prob;
-      const int L = sg.seqlens[b];
+      const PairView<VAR> view(p, sg, prob, g);
       for (int j = tb; j < te; ++j, ++jt) {
-        const int pg = tile_page(p, b, L, j, rank, lane == 0);
+        const int pg = view.page(p, j, rank, lane == 0);
         const int row = pg >= 0 ? pg * kPageSize : oob_row;
         if (lane == 0) PAIR_TR(rank, 0, jt);
         // the page two tiles ahead goes to L2 now, so that its copy into shared
         // memory (which must wait for this tile's score MMAs) hits L2
         if (j + 2 < te) {
-          const int pg2 = tile_page(p, b, L, j + 2, rank, false);
+          const int pg2 = view.page(p, j + 2, rank, false);
           if (pg2 >= 0 && lane < 3) tma_prefetch3(tm_ks, 0, pg2 * kPageSize, 3 * lane);
         }
 #pragma unroll 1
@@ -406,8 +491,9 @@ drain:
 // pages of each tile, the two 128-dv blocks this CTA supplies (chunks
 // 4m + 2 rank and 4m + 2 rank + 1 for m = 0, 1), into slots 4t + 2m, 4t + 2m + 1
 // ---------------------------------------------------------------------------
-__device__ void pair_producer_kv(const CUtensorMap* tm_kv, const DecodeParams& p, const PairSeg& sg, int rank,
-                                 uint32_t smem, uint32_t bars, uint32_t bars_even, const Watchdog& wd) {
+template <int VAR>
+__device__ void pair_producer_kv(const CUtensorMap* tm_kv, const DecodeParams& p, const PairSeg<VAR>& sg, int g,
+                                 int rank, uint32_t smem, uint32_t bars, uint32_t bars_even, const Watchdog& wd) {
   // Every tile's value slots complete on the even CTA's kv_full (armed with
   // both CTAs' bytes), except on a tail tile, where each CTA's copies
   // complete on its own kv_full so that its softmax warps can zero the rows
@@ -423,12 +509,11 @@ __device__ void pair_producer_kv(const CUtensorMap* tm_kv, const DecodeParams& p
     int tb, te;
     sg.range(prob, tb, te);
     if (tb >= te) continue;
-    const int b = prob;
-    const int L = sg.seqlens[b];
+    const PairView<VAR> view(p, sg, prob, g);
     for (int j = tb; j < te; ++j, ++jt) {
-      const int pg0 = tile_page(p, b, L, j, 0, false);
-      const int pg1 = tile_page(p, b, L, j, 1, false);
-      const bool tail = tail_tile(L, j);
+      const int pg0 = view.page(p, j, 0, false);
+      const int pg1 = view.page(p, j, 1, false);
+      const bool tail = view.tail(j, sg);
       if (jt > 0 && !pair_wait(bars + 8 * kBKvEmpty, (jt - 1) & 1, wd)) goto drain;
       if (lane == 0) {
         PAIR_TR(rank, 12, jt);
@@ -493,7 +578,7 @@ struct PairIt {
   int prob, j, te;
   bool valid;
 };
-__device__ __forceinline__ PairIt pair_first_from(const PairSeg& sg, int prob) {
+__device__ __forceinline__ PairIt pair_first_from(const PairSeg<kPlain>& sg, int prob) {
   for (; prob <= sg.last(); ++prob) {
     int tb, te;
     sg.range(prob, tb, te);
@@ -501,7 +586,7 @@ __device__ __forceinline__ PairIt pair_first_from(const PairSeg& sg, int prob) {
   }
   return PairIt{0, 0, 0, false};
 }
-__device__ __forceinline__ PairIt pair_next(const PairSeg& sg, const PairIt& it) {
+__device__ __forceinline__ PairIt pair_next(const PairSeg<kPlain>& sg, const PairIt& it) {
   if (!it.valid) return it;
   if (it.j + 1 < it.te) return PairIt{it.prob, it.j + 1, it.te, true};
   return pair_first_from(sg, it.prob + 1);
@@ -509,7 +594,7 @@ __device__ __forceinline__ PairIt pair_next(const PairSeg& sg, const PairIt& it)
 
 // Cache row of the token in index slot k of problem prob, or -1 for an
 // invalid id (outside [0, length) or on an unusable page, flagged when asked).
-__device__ __forceinline__ int sparse_row(const DecodeParams& p, const PairSeg& sg, int prob, int k, bool flag) {
+__device__ __forceinline__ int sparse_row(const DecodeParams& p, const PairSeg<kPlain>& sg, int prob, int k, bool flag) {
   // (the length, the list length and the index are independent loads, in flight together)
   const int b = prob / p.s_q;
   const int L = p.flat_rows > 0 ? p.flat_rows : sg.seqlens[b];
@@ -611,7 +696,7 @@ __device__ __forceinline__ void copy_block_codes(const DecodeParams& p, int row_
 // CTAs, look the rows up three tiles ahead and prefetch them whole into L2,
 // so that the copies on the tile's critical chain hit L2.
 template <bool ROWS16>
-__device__ void pair_gather(const DecodeParams& p, const PairSeg& sg, int rank, uint32_t smem, uint32_t bars,
+__device__ void pair_gather(const DecodeParams& p, const PairSeg<kPlain>& sg, int rank, uint32_t smem, uint32_t bars,
                             const Watchdog& wd, uint32_t* flags) {
   const int g = threadIdx.x - 32 * kPairGatherWarp0;  // 0..127
   const int lane = g & 31;
@@ -790,7 +875,7 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 // this CTA's value slots of the tile are complete (its own share, written by
 // its gather warps, and its partner's copies), the PV issuer of the even CTA
 // is told.
-__device__ void pair_value_copier(const PairSeg& sg, int rank, uint32_t smem, uint32_t bars, uint32_t bars_even,
+__device__ void pair_value_copier(const PairSeg<kPlain>& sg, int rank, uint32_t smem, uint32_t bars, uint32_t bars_even,
                                   const Watchdog& wd) {
   const int lane = threadIdx.x & 31;
   const uint32_t peer = static_cast<uint32_t>(rank ^ 1);
@@ -841,8 +926,8 @@ drain:
 // ---------------------------------------------------------------------------
 // warp 1 of the even CTA: score MMAs, S = Q K^T over the pair
 // ---------------------------------------------------------------------------
-template <bool SPARSE>
-__device__ void pair_s_issuer(const PairSeg& sg, uint32_t tmem, uint32_t smem, uint32_t bars, const Watchdog& wd) {
+template <bool SPARSE, int VAR>
+__device__ void pair_s_issuer(const PairSeg<VAR>& sg, uint32_t tmem, uint32_t smem, uint32_t bars, const Watchdog& wd) {
   using C = PairCfg<SPARSE>;
   constexpr uint32_t kIdS = idesc_bf16_f32(128, kPairTile, 0, 0);
   constexpr uint64_t kHiK = smem_desc_hi(16, 1024);
@@ -898,7 +983,8 @@ done:
 // ---------------------------------------------------------------------------
 // warp 3 of the even CTA: PV MMAs, O += P V over the pair
 // ---------------------------------------------------------------------------
-__device__ void pair_pv_issuer(const PairSeg& sg, uint32_t tmem, uint32_t smem, uint32_t bars, const Watchdog& wd) {
+template <int VAR>
+__device__ void pair_pv_issuer(const PairSeg<VAR>& sg, uint32_t tmem, uint32_t smem, uint32_t bars, const Watchdog& wd) {
   constexpr uint32_t kIdO = idesc_bf16_f32(128, 256, 0, 1);  // A = P (K-major), B = V (MN-major)
   constexpr uint64_t kHiP = smem_desc_hi(16, 1024);
   constexpr uint64_t kHiV = smem_desc_hi(kPairChunk, 1024);
@@ -950,8 +1036,8 @@ done:
 // ---------------------------------------------------------------------------
 // warps 4-11: online softmax and epilogue
 // ---------------------------------------------------------------------------
-template <bool SPARSE, bool ROWS16>
-__device__ void pair_softmax(const DecodeParams& p, const PairSeg& sg, int g, int rank, int split0, uint32_t tmem,
+template <bool SPARSE, bool ROWS16, int VAR>
+__device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int g, int rank, int split0, uint32_t tmem,
                              uint32_t smem, uint32_t bars, uint32_t bars_even, float* m_s, float* red,
                              const volatile uint32_t* flags, const Watchdog& wd) {
   const int warp = threadIdx.x >> 5;
@@ -1051,16 +1137,19 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg& sg, int g, in
     int tb, te;
     sg.range(prob, tb, te);
     if (tb >= te) continue;
-    const int b = SPARSE ? prob / p.s_q : prob;
-    const int L = SPARSE ? 0 : sg.seqlens[b];  // (sparse: the validity bits, and no lengths for unpaged rows)
+    // (sparse: the validity bits, and no lengths for unpaged rows)
+    PairView<VAR> view;
+    if (!SPARSE) view = PairView<VAR>(p, sg, prob, g);
+    const int L = SPARSE ? 0 : view.L;
     // last visible key of this row (dense: bottom-right causal alignment)
-    const int lim = (!SPARSE && p.is_causal) ? L - p.s_q + grow / p.h_q : L - 1;
+    const int lim = (!SPARSE && view.causal) ? L - p.s_q + (view.in_elem + rank * kPairRows + r) / p.h_q
+                                                     : L - 1;
     float l_part = 0.f;
     for (int j = tb; j < te; ++j, ++jt) {
       const int sb = jt & 1;
       // dense: the block-table entry of this thread's page, read before the
       // wait for S so that the load overlaps it
-      const bool page_ok = SPARSE ? true : tile_page(p, b, L, j, h, false) >= 0;
+      const bool page_ok = SPARSE ? true : view.page(p, j, h, false) >= 0;
       if (!wait_all(kBSFull + sb, (jt >> 1) & 1)) return;
       tc_fence_after();
       const bool tr = (warp == 4 && lane == 0);
@@ -1087,11 +1176,15 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg& sg, int g, in
         if (!all_ok(pair_wait_thread(bars + 8 * (kBFlags + (jt & 3)), (jt >> 2) & 1, wd))) return;
         vbits = flags[4 * (jt & 3) + 2 * h + w];
       }
-      const int pos0 = j * kPairTile + h * 64 + 32 * w;
+      // first token of this thread's 32 (windowed: wherever the walk's page lies)
+      const int pos0 = VAR == kWindowed ? max(view.logical(j, h), 0) * kPageSize + 32 * w
+                                        : j * kPairTile + h * 64 + 32 * w;
       float mx = kPairNegInf;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const bool ok = SPARSE ? ((vbits >> i) & 1u) != 0 : (page_ok && pos0 + i <= lim);
+        const bool ok = SPARSE ? ((vbits >> i) & 1u) != 0
+                               : (page_ok && pos0 + i <= lim &&
+                                  (VAR != kWindowed || pos0 + i < p.sinks || pos0 + i > lim - p.window));
         x[i] = ok ? x[i] * sc : kPairNegInf;
         mx = fmaxf(mx, x[i]);
       }
@@ -1146,10 +1239,10 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg& sg, int g, in
       // 0, but a slot may hold NaN, and 0 * NaN would poison O).  Unusable
       // pages were read as zeros.  (Sparse: invalid tokens were written as
       // zeros by the gather warps.)
-      if (!SPARSE && tail_tile(L, j)) {
+      if (!SPARSE && view.tail(j, sg)) {
         if (!wait_all(kBKvFull, jt & 1)) return;
         const int tl = (q & 1) * 32 + lane;  // token of page h zeroed by this thread
-        if (page_ok && j * kPairTile + h * 64 + tl >= L) {
+        if (page_ok && !view.seen(view.logical(j, h) * kPageSize + tl, sg)) {
 #pragma unroll
           for (int s2 = 0; s2 < 2; ++s2) {
             const uint32_t rowa = smem + kPairKvOff + (4 * h + 2 * w + s2) * kPairChunk + tl * 128;
@@ -1198,16 +1291,20 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg& sg, int g, in
     const float inv = lt > 0.f ? 1.0f / lt : 0.f;
     const float lse = lt > 0.f ? m_fin + log2f(lt) : kPairNegInf;
     const int nsplit = p.num_splits[prob + 1] - p.num_splits[prob];
-    const bool final_out = nsplit <= 1;
-    const int slot = p.num_splits[prob] + (prob == sg.p0 ? split0 : 0);
-    bool write_ok = grow < p.rows;
-    if (!final_out && (slot < 0 || slot >= p.max_slots)) {
+    const bool final_out = VAR != kPrefixed && nsplit <= 1;
+    const bool own = VAR == kPrefixed && prob >= p.prefix_problems;
+    const int slot = p.num_splits[prob] + (prob == sg.p0 ? split0 : 0) - (own ? p.num_splits[p.prefix_problems] : 0);
+    bool write_ok = VAR == kPrefixed ? rank * kPairRows + r < view.rows : grow < p.rows;
+    if (!final_out && (slot < 0 || slot >= (own ? p.own_slots : p.max_slots))) {
       write_ok = false;
       if (r == 0 && hw == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
     }
     const int dv0 = 256 * w + 128 * h;
-    const int64_t orow = final_out ? static_cast<int64_t>(prob) * p.rows + grow
-                                   : static_cast<int64_t>(slot) * p.rows + grow;
+    // (prefixed: one row group; slots of 128 rows for the prefix, of block_rows for the own keys)
+    const int64_t orow = VAR == kPrefixed ? static_cast<int64_t>(slot) * (own ? p.block_rows : 2 * kPairRows) +
+                                                rank * kPairRows + r
+                         : final_out      ? static_cast<int64_t>(prob) * p.rows + grow
+                                          : static_cast<int64_t>(slot) * p.rows + grow;
 #pragma unroll 1
     for (int c = 0; c < 128; c += 16) {
       float v[16];
@@ -1228,7 +1325,7 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg& sg, int g, in
           dst[0] = lo;
           dst[1] = hi;
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.o_accum + orow * kDv + dv0 + c);
+          float4* dst = reinterpret_cast<float4*>((own ? p.own_o : p.o_accum) + orow * kDv + dv0 + c);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             dst[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
@@ -1239,7 +1336,7 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg& sg, int g, in
       if (final_out)
         p.lse[orow] = lse;
       else
-        p.lse_accum[orow] = lse;
+        (own ? p.own_lse : p.lse_accum)[orow] = lse;
     }
     tc_fence_before();
     arrive_even(kBOEmpty);
@@ -1250,7 +1347,7 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg& sg, int g, in
 // ---------------------------------------------------------------------------
 // kernel
 // ---------------------------------------------------------------------------
-template <bool SPARSE, bool ROWS16>
+template <bool SPARSE, bool ROWS16, int VAR>
 __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
     mla_decode_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
                            const __grid_constant__ CUtensorMap tm_kv, const DecodeParams p) {
@@ -1328,7 +1425,7 @@ __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
   Watchdog wd{abort_flag, p.status, p.timeout_ns};
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  PairSeg sg;
+  PairSeg<VAR> sg;
   int split0 = 0;
   if (p.sched[kSchedParts] == p.num_parts && p.sched[kSchedTag] == p.sched_tag) {
     const int32_t* sr = p.sched + static_cast<int64_t>(part) * kSchedInts;
@@ -1345,6 +1442,11 @@ __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
   sg.s_q = p.s_q;
   sg.topk = SPARSE ? p.topk : 0;
   sg.seqlens = p.cache_seqlens;
+  sg.window = p.window;
+  sg.sinks = p.sinks;
+  sg.prefix_len = p.prefix_len;
+  sg.prefix_problems = p.prefix_problems;
+  sg.blocks_per_elem = p.blocks_per_elem;
   if (sg.p0 < 0 || sg.p0 > sg.np || sg.p1 < sg.p0 || sg.p1 > sg.np || sg.t0 < 0 || sg.t1 < 0) {
     if (threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
     sg.p0 = sg.np;
@@ -1366,23 +1468,23 @@ __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
   if (warp < 4) {
     regs_to<C::kRegsCtl, C::kLaunchRegs>();
     if (warp == 0) {
-      pair_producer_ks<SPARSE>(&tm_q, &tm_ks, p, sg, g, rank, smem, bars, bars_even, wd);
+      pair_producer_ks<SPARSE, VAR>(&tm_q, &tm_ks, p, sg, g, rank, smem, bars, bars_even, wd);
     } else if (warp == 1) {
-      if (rank == 0) pair_s_issuer<SPARSE>(sg, tmem, smem, bars, wd);
+      if (rank == 0) pair_s_issuer<SPARSE, VAR>(sg, tmem, smem, bars, wd);
     } else if (warp == 2) {
-      if (SPARSE)
+      if constexpr (SPARSE)
         pair_value_copier(sg, rank, smem, bars, bars_even, wd);
       else
-        pair_producer_kv(&tm_kv, p, sg, rank, smem, bars, bars_even, wd);
+        pair_producer_kv<VAR>(&tm_kv, p, sg, g, rank, smem, bars, bars_even, wd);
     } else if (rank == 0) {
-      pair_pv_issuer(sg, tmem, smem, bars, wd);
+      pair_pv_issuer<VAR>(sg, tmem, smem, bars, wd);
     }
   } else if (warp < kPairGatherWarp0) {
     regs_to<C::kRegsSm, C::kLaunchRegs>();
-    pair_softmax<SPARSE, ROWS16>(p, sg, g, rank, split0, tmem, smem, bars, bars_even, m_s, red, flags, wd);
+    pair_softmax<SPARSE, ROWS16, VAR>(p, sg, g, rank, split0, tmem, smem, bars, bars_even, m_s, red, flags, wd);
     // the odd CTA's signal copies are complete before the pair's final sync
     if (rank == 1 && (threadIdx.x & 31) == 0) bulk_wait_all();
-  } else if (SPARSE) {
+  } else if constexpr (SPARSE) {
     regs_to<C::kRegsGather, C::kLaunchRegs>();
     pair_gather<ROWS16>(p, sg, rank, smem, bars, wd, flags);
   }
@@ -1408,11 +1510,11 @@ __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
   }
 }
 
-template <bool SPARSE, bool ROWS16>
+template <bool SPARSE, bool ROWS16, int VAR>
 cudaError_t launch_pair(const CUtensorMap& tm_q, const CUtensorMap& tm_ks, const CUtensorMap& tm_kv,
                         const DecodeParams& p, cudaStream_t stream) {
   using C = PairCfg<SPARSE>;
-  auto kern = mla_decode_pair_kernel<SPARSE, ROWS16>;
+  auto kern = mla_decode_pair_kernel<SPARSE, ROWS16, VAR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmemBytes);
   if (e != cudaSuccess) return e;
   cudaFuncAttributes fa;
@@ -1439,7 +1541,7 @@ cudaError_t launch_pair(const CUtensorMap& tm_q, const CUtensorMap& tm_ks, const
 }  // namespace
 
 int pair_cluster_capacity() {
-  auto kern = mla_decode_pair_kernel<true, false>;
+  auto kern = mla_decode_pair_kernel<true, false, kPlain>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmemBytes) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
@@ -1459,9 +1561,19 @@ int pair_cluster_capacity() {
 
 cudaError_t launch_decode_pair(const CUtensorMap& tm_q, const CUtensorMap& tm_ks, const CUtensorMap& tm_kv,
                                const DecodeParams& p, bool sparse, cudaStream_t stream) {
-  if (!sparse) return launch_pair<false, false>(tm_q, tm_ks, tm_kv, p, stream);
-  return p.rows16 ? launch_pair<true, true>(tm_q, tm_ks, tm_kv, p, stream)
-                  : launch_pair<true, false>(tm_q, tm_ks, tm_kv, p, stream);
+  if (!sparse) return launch_pair<false, false, kPlain>(tm_q, tm_ks, tm_kv, p, stream);
+  return p.rows16 ? launch_pair<true, true, kPlain>(tm_q, tm_ks, tm_kv, p, stream)
+                  : launch_pair<true, false, kPlain>(tm_q, tm_ks, tm_kv, p, stream);
+}
+
+cudaError_t launch_window_pair(const CUtensorMap& tm_q, const CUtensorMap& tm_ks, const CUtensorMap& tm_kv,
+                               const DecodeParams& p, cudaStream_t stream) {
+  return launch_pair<false, false, kWindowed>(tm_q, tm_ks, tm_kv, p, stream);
+}
+
+cudaError_t launch_prefix_pair(const CUtensorMap& tm_q, const CUtensorMap& tm_ks, const CUtensorMap& tm_kv,
+                               const DecodeParams& p, cudaStream_t stream) {
+  return launch_pair<false, false, kPrefixed>(tm_q, tm_ks, tm_kv, p, stream);
 }
 
 }  // namespace mla

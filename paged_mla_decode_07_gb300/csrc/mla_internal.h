@@ -36,6 +36,7 @@ constexpr int kSchedInts = 8;      // ints per schedule record
 enum SchedField { kSchedP0 = 0, kSchedT0 = 1, kSchedP1 = 2, kSchedT1 = 3, kSchedSplit0 = 4, kSchedParts = 5,
                   kSchedTag = 6 };
 
+constexpr int kMaxPages = ((1ll << 31) - 1) / kPageSize;  // slots are int32
 constexpr int kMaxProblems = 16384;    // metadata kernel keeps per-problem prefix sums in smem
 
 // Number of tiles of problem p: dense covers the cached tokens [0, seqlen),
@@ -48,6 +49,31 @@ __host__ __device__ inline int problem_tiles(const int32_t* cache_seqlens, int p
   int L = cache_seqlens[p];
   return L > 0 ? (L + tile_tokens - 1) / tile_tokens : 0;
 }
+
+// Pages a windowed problem reads.  Query token i sits at position L - s_q + i
+// and sees the first `sinks` keys and the last `window` up to its own, so all
+// query tokens together see [0, sinks) and [L - s_q - window + 1, L): the
+// first `head` pages, then those from page head + skip on (one run when the
+// two touch).  Page i of the walk is page i, or i + skip from `head` on.
+struct KeyWalk {
+  int pages, head, skip;
+  __host__ __device__ int page(int i) const { return i < head ? i : i + skip; }
+};
+__host__ __device__ inline KeyWalk key_walk(int L, int s_q, int window, int sinks) {
+  if (L <= 0) return KeyWalk{0, 0, 0};
+  const int total = (L + kPageSize - 1) / kPageSize;
+  const int kept = sinks < L ? sinks : L;
+  const int first = L - s_q - window + 1;  // >= -2^31: window is at most 2^30, s_q at most 1024
+  const int head = (kept + kPageSize - 1) / kPageSize;
+  if (first <= 0 || first / kPageSize <= head) return KeyWalk{total, total, 0};
+  const int w0 = first / kPageSize;
+  return KeyWalk{head + total - w0, head, w0 - head};
+}
+// Whether some query token of the element sees key t (t < L).
+__host__ __device__ inline bool key_in_walk(int t, int L, int s_q, int window, int sinks) {
+  return t < sinks || t > L - s_q - window;
+}
+constexpr int kMaxWindow = 1 << 30;  // larger windows see every key a cache can hold, as this one does
 
 // Rows per CTA for a problem with `rows` query rows sharing one key set.
 inline int rows_per_cta(int rows) { return rows > 32 ? 64 : (rows > 16 ? 32 : 16); }
@@ -97,7 +123,47 @@ struct DecodeParams {
   int rows16;                 // CTA-pair sparse decode: the rows are bf16 (1152 bytes, used as they
                               // are), 0: FP8 rows, dequantised
 
+  int window, sinks;          // windowed modes: keys before a query token it sees, first keys that stay visible
+  int always_partial;         // every piece writes a partial result, the only piece of a problem too
+
+  // shared-prefix decode on CTA pairs: problems [0, prefix_problems) are the
+  // prefix under 128 consecutive query rows each, the rest the own keys of
+  // each element under its rows, 128 at a time
+  const int32_t* prefix_table;  // [prefix_pages]; NULL: page i is row block i of the cache map
+  const int32_t* prefix_len;    // [1]
+  int prefix_pages, prefix_problems, blocks_per_elem, total_rows;
+  float* own_o;                 // partials of the own keys: [own_slots, block_rows, 512], [own_slots, block_rows]
+  float* own_lse;
+  int block_rows, own_slots;
+
   float scale_log2;           // sm_scale * log2(e)
+};
+
+// What the schedule kernel needs to know of the problems.
+struct SchedSpec {
+  const int32_t* seqlens;     // [batch]
+  int s_q, topk;
+  int window, sinks;          // window > 0: windowed problems
+  const int32_t* prefix_len;  // shared-prefix decode (see DecodeParams), else NULL
+  int prefix_problems, blocks_per_elem;
+  int always_partial;         // a problem in one piece takes a partial-result slot too
+};
+
+// Merge of the partials of shared-prefix decode: row b * rows + r has pieces
+// of the prefix under its block of 128 rows and pieces of its element's own keys.
+struct PrefixCombineParams {
+  const int32_t* prefix_splits;  // [prefix_problems + 1] slot prefix sums
+  const float* prefix_o;         // [slots, 128, 512]
+  const float* prefix_lse;       // [slots, 128]
+  const int32_t* own_splits;     // [batch * blocks_per_elem + 1]
+  const float* own_o;            // [slots, block_rows, 512]
+  const float* own_lse;          // [slots, block_rows]
+  int block_rows, blocks_per_elem;
+  int rows, total_rows;          // query rows per element, of all elements
+  int prefix_slots, own_slots;   // slots the two arrays hold
+  void* out;
+  float* lse;
+  uint32_t* status;
 };
 
 struct CombineParams {
@@ -128,10 +194,41 @@ struct IndexParams {
   uint32_t tmem_cols;         // two accumulator buffers of tmem_cols / 2 >= n_box columns
 };
 
+struct AssignPagesParams {
+  const int32_t* cache_lengths;
+  const int32_t* new_tokens;
+  const int32_t* free_pages;
+  const int32_t* free_cursor;
+  int32_t* block_table;
+  int32_t* cache_seqlens;  // NULL: not written by this launch (likewise the next three)
+  int32_t* row_offsets;
+  int32_t* slot_map;
+  int32_t* next_cursor;
+  uint32_t* status;
+  int batch, num_free, block_table_stride, num_pages, num_tokens;
+  int fill_table;          // 1: write the new block-table entries and the slots; 0: lengths and cursor only
+};
+
+// New tokens into cache rows by slot.
+struct SlotStoreParams {
+  const uint16_t* latent;  // bf16 [num_tokens, 512], rows latent_stride elements apart
+  const uint16_t* rope;    // bf16 [num_tokens, 64], rows rope_stride elements apart
+  const int32_t* slots;    // [num_tokens]
+  uint8_t* kvcache;
+  float* kv_scales;        // FP8 rows with one scale per token, else NULL
+  uint32_t* status;
+  int64_t latent_stride, rope_stride;
+  int num_tokens, num_slots;
+  int is_fp8;
+};
+
 // Kernel launchers (defined in the .cu files); return a CUDA error code.
 cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, const Geometry& g, int32_t* sched,
                             int32_t* num_splits, cudaStream_t stream);
-// mode: 0 dense bf16 cache, 1 sparse FP8 cache, 2 dense FP8 cache, 3 sparse bf16 rows
+cudaError_t launch_schedule(const SchedSpec& spec, const Geometry& g, int32_t* sched, int32_t* num_splits,
+                            cudaStream_t stream);
+// mode: 0 dense bf16 cache, 1 sparse FP8 cache, 2 dense FP8 cache, 3 sparse bf16 rows, 4 and 5 windowed dense
+// over the bf16 and the FP8 cache
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const DecodeParams& p, int rpc,
                           int mode, cudaStream_t stream);
 // CTA pairs the pair decode kernel can keep resident at once on the current
@@ -143,12 +240,26 @@ int pair_cluster_capacity();
 // FP8 rows as 128-byte boxes of one row for row gathers, tm_kv unused)
 cudaError_t launch_decode_pair(const CUtensorMap& tm_q, const CUtensorMap& tm_ks, const CUtensorMap& tm_kv,
                                const DecodeParams& p, bool sparse, cudaStream_t stream);
+// The same kernel, windowed or over a shared prefix and the elements' own keys (bf16 rows)
+cudaError_t launch_window_pair(const CUtensorMap& tm_q, const CUtensorMap& tm_ks, const CUtensorMap& tm_kv,
+                               const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_prefix_pair(const CUtensorMap& tm_q, const CUtensorMap& tm_ks, const CUtensorMap& tm_kv,
+                               const DecodeParams& p, cudaStream_t stream);
+// FP8 prefix rows to bf16 rows in `rows` (page i of the prefix at rows + 64 i),
+// `table[i]` = i or -1 for an unusable page
+cudaError_t launch_prefix_rows(const uint8_t* kvcache, const float* kv_scales, const int32_t* prefix_table,
+                               const int32_t* prefix_len, int prefix_pages, int num_pages, void* rows, int32_t* table,
+                               uint32_t* status, int sm_count, cudaStream_t stream);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool pdl);
+cudaError_t launch_prefix_combine(const PrefixCombineParams& p, cudaStream_t stream);
 size_t decode_smem_bytes(int rpc, int mode);
 cudaError_t launch_fp8_cache_store(const uint16_t* x, int num_tokens, const int32_t* row_offsets,
                                    const int32_t* cache_lengths, int batch, const int32_t* block_table,
                                    int block_table_stride, uint8_t* kvcache, int num_pages, uint32_t* status,
                                    int sm_count, cudaStream_t stream);
+cudaError_t launch_slot_store(const SlotStoreParams& p, int sm_count, cudaStream_t stream);
+// in_place: the lengths or the cursor are updated in the arrays they are read from
+cudaError_t launch_assign_pages(const AssignPagesParams& p, bool in_place, int sm_count, cudaStream_t stream);
 cudaError_t launch_index(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const IndexParams& p, int topk,
                          int32_t* out, cudaStream_t stream);
 // Sets the thread-local message returned by mla_last_error().

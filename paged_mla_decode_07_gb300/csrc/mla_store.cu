@@ -129,7 +129,140 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
   }
 }
 
+// ---------------------------------------------------------------------------
+// K7 — store through a slot map: token i (512 latent and 64 RoPE values from
+// two row-strided tensors) into cache row slots[i], in any row format.  The
+// token's place is one read instead of the search and table lookup above.
+// Memory-bound: 1152 bytes read and 1152, 656 or 644 written per token.
+// ---------------------------------------------------------------------------
+// Slot of token r, or -1 (padding, or a slot outside the cache, which is flagged).
+__device__ __forceinline__ int slot_of(const SlotStoreParams& p, int r, bool flag) {
+  const int s = __ldg(p.slots + r);
+  if (s >= p.num_slots) {
+    if (flag) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
+    return -1;
+  }
+  return s < 0 ? -1 : s;
+}
+
+// One token with a single scale over its 512 latent values: 512 codes and 64
+// RoPE values at dst, the scale at *scale_out.
+__device__ __forceinline__ void store_row_token_scale(uint8_t* dst, float* scale_out, const uint4 a, const uint4 c,
+                                                      const uint4 rp, int lane) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float scale = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+  uint32_t code[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    code[i] = e4m3x2(__fdiv_rn(v[4 * i], scale), __fdiv_rn(v[4 * i + 1], scale)) |
+              (e4m3x2(__fdiv_rn(v[4 * i + 2], scale), __fdiv_rn(v[4 * i + 3], scale)) << 16);
+  *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(code[0], code[1], code[2], code[3]);
+  if (lane < 8) *reinterpret_cast<uint4*>(dst + kDv + 16 * lane) = rp;
+  if (lane == 0) *scale_out = scale;
+}
+
+// FP8 rows, one warp per token at a time, the next token's values loaded
+// while this one is quantised.
+template <bool TOKEN_SCALE>
+__global__ void __launch_bounds__(kStoreWarps * 32) slot_store_fp8_kernel(const SlotStoreParams p) {
+  constexpr int kRow = TOKEN_SCALE ? 640 : kFp8RowBytes;
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * kStoreWarps;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto load = [&](int r, uint4& a, uint4& c, uint4& rp) {
+    const uint16_t* s = p.latent + r * p.latent_stride + 16 * lane;
+    a = ld_global_nc_v4(s);
+    c = ld_global_nc_v4(s + 8);
+    rp = lane < 8 ? ld_global_nc_v4(p.rope + r * p.rope_stride + 8 * lane) : zero;
+  };
+  int64_t r = blockIdx.x * kStoreWarps + (threadIdx.x >> 5);
+  if (r >= p.num_tokens) return;
+  uint4 a, c, rp;
+  int slot = slot_of(p, static_cast<int>(r), lane == 0);
+  load(static_cast<int>(r), a, c, rp);
+  while (true) {
+    const int64_t rn = r + warps;
+    uint4 an = zero, cn = zero, rpn = zero;
+    int slot_n = -1;
+    if (rn < p.num_tokens) {
+      slot_n = slot_of(p, static_cast<int>(rn), lane == 0);
+      load(static_cast<int>(rn), an, cn, rpn);
+    }
+    if (slot >= 0) {
+      uint8_t* dst = p.kvcache + static_cast<int64_t>(slot) * kRow;
+      if (TOKEN_SCALE)
+        store_row_token_scale(dst, p.kv_scales + slot, a, c, rp, lane);
+      else
+        store_row(dst, a, c, rp, lane);
+    }
+    if (rn >= p.num_tokens) return;
+    r = rn;
+    slot = slot_n;
+    a = an;
+    c = cn;
+    rp = rpn;
+  }
+}
+
+// bf16 rows: 72 16-byte units per token, copied as they are.
+constexpr int kRowUnits = kDqk / 8;
+constexpr int kUnitsInFlight = 4;
+
+__global__ void __launch_bounds__(kStoreWarps * 32) slot_store_bf16_kernel(const SlotStoreParams p) {
+  const int64_t units = static_cast<int64_t>(p.num_tokens) * kRowUnits;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreWarps * 32;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kStoreWarps * 32 + threadIdx.x; i0 < units;
+       i0 += step * kUnitsInFlight) {
+    uint4 v[kUnitsInFlight];
+    uint8_t* dst[kUnitsInFlight];
+#pragma unroll
+    for (int k = 0; k < kUnitsInFlight; ++k) {
+      const int64_t i = i0 + k * step;
+      dst[k] = nullptr;
+      if (i < units) {
+        const int r = static_cast<int>(i / kRowUnits), u = static_cast<int>(i % kRowUnits);
+        const int slot = slot_of(p, r, u == 0);
+        if (slot >= 0) dst[k] = p.kvcache + static_cast<int64_t>(slot) * (2 * kDqk) + 16 * u;
+        v[k] = ld_global_nc_v4(u < kDv / 8 ? p.latent + r * p.latent_stride + 8 * u
+                                           : p.rope + r * p.rope_stride + 8 * (u - kDv / 8));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kUnitsInFlight; ++k)
+      if (dst[k]) *reinterpret_cast<uint4*>(dst[k]) = v[k];
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_slot_store(const SlotStoreParams& p, int sm_count, cudaStream_t stream) {
+  if (p.num_tokens == 0) return cudaSuccess;
+  const int64_t max_grid = sm_count * 8;
+  const int threads = kStoreWarps * 32;
+  if (p.is_fp8) {
+    const int64_t need = (static_cast<int64_t>(p.num_tokens) + kStoreWarps - 1) / kStoreWarps;
+    const unsigned grid = static_cast<unsigned>(need < max_grid ? need : max_grid);
+    if (p.kv_scales)
+      slot_store_fp8_kernel<true><<<grid, threads, 0, stream>>>(p);
+    else
+      slot_store_fp8_kernel<false><<<grid, threads, 0, stream>>>(p);
+  } else {
+    const int64_t need = (static_cast<int64_t>(p.num_tokens) * kRowUnits + threads - 1) / threads;
+    slot_store_bf16_kernel<<<static_cast<unsigned>(need < max_grid ? need : max_grid), threads, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
 
 cudaError_t launch_fp8_cache_store(const uint16_t* x, int num_tokens, const int32_t* row_offsets,
                                    const int32_t* cache_lengths, int batch, const int32_t* block_table,

@@ -1,0 +1,153 @@
+"""Windowed decode with sinks on the GPU against a 64-bit reference."""
+import numpy as np
+import pytest
+import torch
+
+import paged_mla_decode_07_gb300 as mla
+from gpu_helpers import Guarded, check_guards, overrides
+from paged_reference import Cache, attend, check, i32, table
+
+pytestmark = pytest.mark.gpu
+SCALE = 576 ** -0.5
+
+
+def seen(L, s_q, i, window, sinks):
+    last = L - s_q + i
+    return [t for t in range(max(0, min(last + 1, L))) if t < sinks or t > last - window]
+
+
+def problem(fmt, h_q, s_q, lens, window, sinks, seed=0, store_all=False):
+    cache = Cache(fmt, seed, sum(-(-L // 64) for L in lens) + 3)
+    g = torch.Generator("cuda").manual_seed(seed + 1)
+    q = torch.randn(len(lens), s_q, h_q, 576, generator=g, device="cuda").to(torch.bfloat16)
+    rows, want = [], []
+    for b, L in enumerate(lens):
+        sets = [seen(L, s_q, i, window, sinks) for i in range(s_q)]
+        values, ids = cache.put(L, keep=None if store_all else set().union(*sets))
+        rows.append(ids)
+        for i in range(s_q):
+            want.append(attend(q[b, i], values[torch.tensor(sets[i], dtype=torch.long, device="cuda")], SCALE))
+    want = tuple(torch.stack([w[k] for w in want]).view(len(lens), s_q, h_q, *([512] if k != 1 else [])) for k in range(3))
+    kv, sc = cache.tensors()
+    return q, kv, sc, table(rows), i32(lens), want
+
+
+def run(q, kv, sc, bt, lens, window, sinks, flags=0, **kw):
+    b, s, h, _ = q.shape
+    g_out, g_lse = Guarded(b * s * h * 1024), Guarded(b * s * h * 4)
+    g_ws = Guarded(mla.window_decode_workspace_size(b, h_q=h, s_q=s, is_fp8=kv.dtype == torch.uint8))
+    g_ws.body.fill_(0xFF)
+    out, lse = mla.window_decode(q, kv, bt, lens, SCALE, window=window, sinks=sinks, kv_scales=sc,
+                                 out=g_out.view(torch.bfloat16, (b, s, h, 512)),
+                                 lse=g_lse.view(torch.float32, (b, s, h)), workspace=g_ws.body, **kw)
+    assert mla.device_status() == flags
+    check_guards({"out": g_out, "lse": g_lse, "workspace": g_ws}, "window_decode")
+    return out, lse
+
+
+LENS = (0, 1, 5, 63, 64, 65, 127, 128, 129, 300, 641, 1000)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 3), (64, 0), (64, 64), (100, 10), (130, 65), (256, 129),
+                                          (1000, 0), (200, 5000), (2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1)])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("h_q,s_q", [(16, 1), (128, 1), (24, 3)])
+def test_window_and_sinks(fmt, h_q, s_q, window, sinks):
+    q, kv, sc, bt, lens, want = problem(fmt, h_q, s_q, LENS, window, sinks, seed=window % 1000 + sinks % 1000)
+    check(*run(q, kv, sc, bt, lens, window, sinks), want, f"{fmt} {h_q}x{s_q} window {window} sinks {sinks}")
+
+
+@pytest.mark.parametrize("h_q,s_q", [(1, 1), (8, 1), (8, 3), (20, 1), (32, 1), (33, 1), (64, 1), (16, 4), (65, 1), (40, 2),
+                                     (128, 2), (96, 3), (100, 5), (1, 200), (512, 2)])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_row_counts(fmt, h_q, s_q):
+    window, sinks = 150, 20
+    q, kv, sc, bt, lens, want = problem(fmt, h_q, s_q, (0, 2, 64, 190, 777), window, sinks, seed=h_q * 7 + s_q)
+    check(*run(q, kv, sc, bt, lens, window, sinks), want, f"{fmt} {h_q}x{s_q}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("h_q", [16, 128])
+@pytest.mark.parametrize("parts", [1, 2, 7, 40, 300])
+def test_forced_splits(fmt, h_q, parts):
+    q, kv, sc, bt, lens, want = problem(fmt, h_q, 2, (0, 700, 64, 1500, 3), 400, 70, seed=parts)
+    with overrides(num_parts=parts):
+        got = run(q, kv, sc, bt, lens, 400, 70)
+    check(*got, want, f"{fmt} {h_q} parts {parts}")
+
+
+@pytest.mark.parametrize("fmt,h_q", [("bf16", 16), ("bf16", 128), ("fp8", 16), ("fp8_token", 128)])
+def test_many_elements(fmt, h_q):
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(0, 900, 330)]
+    q, kv, sc, bt, L, want = problem(fmt, h_q, 1, lens, 200, 4, seed=5)
+    check(*run(q, kv, sc, bt, L, 200, 4), want, f"{fmt} {h_q}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_a_window_over_everything_equals_dense_decode(fmt):
+    lens = (700, 64, 1, 1300)
+    q, kv, sc, bt, L, _ = problem(fmt, 16, 2, lens, 1 << 20, 0, seed=9)
+    got = run(q, kv, sc, bt, L, 1 << 20, 0)
+    sched, ns = mla.get_metadata(L, h_q=16, s_q=2, topk=0, is_fp8=fmt != "bf16")
+    want = mla.decode(q, kv, bt, L, SCALE, sched, ns, is_causal=True)
+    assert mla.device_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("fmt,h_q", [("bf16", 16), ("bf16", 128), ("fp8", 16), ("fp8", 128)])
+def test_an_unusable_page_is_flagged_and_masked(fmt, h_q):
+    lens, window, sinks = (900, 500), 300, 64
+    q, kv, sc, bt, L, _ = problem(fmt, h_q, 1, lens, window, sinks, seed=4)
+    lost = 900 // 64 - 1
+    bt2 = bt.clone()
+    bt2[0, lost] = kv.shape[0]
+    got = run(q, kv, sc, bt2, L, window, sinks, flags=mla.DEVICE_BAD_PAGE)
+    whole = run(q, kv, sc, bt, L, window, sinks)
+    assert torch.isfinite(got[0]).all()
+    # the other element is untouched; the masked keys lower the sum
+    assert torch.allclose(got[1][1], whole[1][1], rtol=0, atol=2.0 ** -18)
+    assert (got[1][0] < whole[1][0]).all()
+
+
+def test_short_block_table_rows_are_flagged():
+    q, kv, sc, bt, L, _ = problem("bf16", 16, 1, (900,), 300, 0, seed=4)
+    run(q, kv, sc, bt[:, :14].contiguous(), L, 300, 0, flags=mla.DEVICE_BAD_PAGE)
+
+
+def test_repeated_runs_and_graph_replays_agree():
+    q, kv, sc, bt, L, want = problem("bf16", 128, 2, (900, 130, 64, 1700), 500, 30, seed=6, store_all=True)
+    first = [t.clone() for t in run(q, kv, sc, bt, L, 500, 30)]
+    out, lse = torch.empty_like(first[0]), torch.empty_like(first[1])
+    ws = torch.empty(mla.window_decode_workspace_size(4, h_q=128, s_q=2, is_fp8=False), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mla.window_decode(q, kv, bt, L, SCALE, window=500, sinks=30, out=out, lse=lse, workspace=ws)
+    for _ in range(10):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    # the lengths are read when the graph runs
+    L.fill_(64)
+    graph.replay()
+    again = run(q, kv, sc, bt, L, 500, 30)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_two_streams_with_their_own_workspaces():
+    a = problem("bf16", 16, 1, (900, 130, 64, 1700), 500, 30, seed=6)
+    b = problem("fp8", 64, 1, (300, 1200), 100, 3, seed=7)
+    want = [run(*a[:5], 500, 30), run(*b[:5], 100, 3)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        got.append((mla.window_decode(a[0], a[1], a[3], a[4], SCALE, window=500, sinks=30, stream=streams[0]),
+                    mla.window_decode(b[0], b[1], b[3], b[4], SCALE, window=100, sinks=3, stream=streams[1].cuda_stream)))
+    torch.cuda.synchronize()
+    assert mla.device_status() == 0
+    for x, y in got:
+        for g, w in ((x, want[0]), (y, want[1])):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
