@@ -15,6 +15,7 @@ code path.  If ``libmla.so`` has not been built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional, Tuple
@@ -139,6 +140,8 @@ def library_path() -> str:
 def lib():
     """Load libmla.so (built in-tree by ``build()``); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -245,6 +248,19 @@ class _On:
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
             c.__exit__(*exc)
+
+
+# the current stream's handle without the Stream object around it (a third of the binding's time in short calls)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(dev, stream, call):
+    """call(stream handle) with the device of the tensors current, on `stream` or its current stream."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(_raw_stream(dev.index))
+    with _On(dev, stream) as handle:
+        return call(handle)
 
 
 def _cuda_tensor(t, name):
@@ -449,25 +465,25 @@ def assign_pages(cache_lengths: torch.Tensor, new_tokens: torch.Tensor, free_pag
         raise ValueError("new_tokens and block_table must have batch rows and free_cursor one entry")
     if num_tokens < 0:
         raise ValueError(f"num_tokens must be >= 0 (got {num_tokens})")
-    with _On(dev, stream) as handle:
-        def out(t, name, n):
-            if t is None:
-                return torch.empty(n, dtype=torch.int32, device=dev)
+    sizes = (num_tokens, batch, batch + 1, 1)
+    given = (slot_map, cache_seqlens, row_offsets, next_cursor)
+    for t, name, n in zip(given, ("slot_map", "cache_seqlens", "row_offsets", "next_cursor"), sizes):
+        if t is not None:
             _need(t, name, torch.int32, dev, 1)
             if t.shape[0] != n:
                 raise ValueError(f"{name} must have {n} entries (got {t.shape[0]})")
-            return t
-        cache_seqlens = out(cache_seqlens, "cache_seqlens", batch)
-        row_offsets = out(row_offsets, "row_offsets", batch + 1)
-        slot_map = out(slot_map, "slot_map", num_tokens)
-        next_cursor = out(next_cursor, "next_cursor", 1)
+
+    def call(handle):
+        slots, lens, offsets, cursor = [torch.empty(n, dtype=torch.int32, device=dev) if t is None else t
+                                        for t, n in zip(given, sizes)]
         a = AssignPagesArgs(cache_lengths.data_ptr(), new_tokens.data_ptr(), batch, free_pages.data_ptr(),
                             free_pages.shape[0], free_cursor.data_ptr(), block_table.data_ptr(),
                             block_table.shape[1], MAX_PAGES if num_pages is None else int(num_pages), num_tokens,
-                            cache_seqlens.data_ptr(), row_offsets.data_ptr(), slot_map.data_ptr(),
-                            next_cursor.data_ptr())
+                            lens.data_ptr(), offsets.data_ptr(), slots.data_ptr(), cursor.data_ptr())
         _check(lib().mla_assign_pages(ctypes.byref(a), handle))
-    return cache_seqlens, row_offsets, slot_map, next_cursor
+        return lens, offsets, slots, cursor
+
+    return _launch(dev, stream, call)
 
 
 def cache_store(latent: torch.Tensor, rope: torch.Tensor, slot_map: torch.Tensor, kvcache: torch.Tensor,
@@ -496,8 +512,7 @@ def cache_store(latent: torch.Tensor, rope: torch.Tensor, slot_map: torch.Tensor
                        rope.stride(0) if n > 1 else D_V, slot_map.data_ptr(), n, kvcache.data_ptr(),
                        kvcache.shape[0], kvcache.shape[1], int(is_fp8),
                        kv_scales.data_ptr() if kv_scales is not None else None)
-    with _On(dev, stream) as handle:
-        _check(lib().mla_cache_store(ctypes.byref(a), handle))
+    _launch(dev, stream, lambda handle: _check(lib().mla_cache_store(ctypes.byref(a), handle)))
 
 
 def sparse_prefill_workspace_size(s_q: int, h_q: int, topk: int) -> int:
@@ -578,14 +593,16 @@ def _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales):
 
 def _outputs(q, out, lse):
     batch, s_q, h_q, _ = q.shape
-    if out is None:
-        out = torch.empty((batch, s_q, h_q, D_V), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((batch, s_q, h_q), dtype=torch.float32, device=q.device)
-    _need(out, "out", torch.bfloat16, q.device)
-    _need(lse, "lse", torch.float32, q.device)
-    if out.numel() != batch * s_q * h_q * D_V or lse.numel() != batch * s_q * h_q:
-        raise ValueError("out / lse have the wrong size")
+    for t, name, dtype, shape in ((out, "out", torch.bfloat16, (batch, s_q, h_q, D_V)),
+                                  (lse, "lse", torch.float32, (batch, s_q, h_q))):
+        if t is not None:
+            _need(t, name, dtype, q.device)
+            if t.numel() != math.prod(shape):
+                raise ValueError(f"{name} has the wrong size")
+    out = torch.empty((batch, s_q, h_q, D_V), dtype=torch.bfloat16, device=q.device) if out is None else \
+        out.view(batch, s_q, h_q, D_V)
+    lse = torch.empty((batch, s_q, h_q), dtype=torch.float32, device=q.device) if lse is None else \
+        lse.view(batch, s_q, h_q)
     return out, lse
 
 
@@ -615,19 +632,22 @@ def window_decode(q: torch.Tensor, kvcache: torch.Tensor, block_table: torch.Ten
     [b, s_q, h_q, 512], lse fp32 [b, s_q, h_q], base 2)."""
     dev, is_fp8 = _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales)
     batch, s_q, h_q, _ = q.shape
-    with _On(dev, stream) as handle:
-        out, lse = _outputs(q, out, lse)
+
+    def call(handle):
+        o, z = _outputs(q, out, lse)
         n = ctypes.c_size_t()
         if workspace is None:
             _check(lib().mla_window_decode_workspace_size(batch, h_q, s_q, int(is_fp8), ctypes.byref(n)))
-        workspace = _scratch(workspace, n.value, dev)
+        ws = _scratch(workspace, n.value, dev)
         a = WindowDecodeArgs(q.data_ptr(), batch, s_q, h_q, kvcache.data_ptr(), kvcache.shape[0], kvcache.shape[1],
                              block_table.data_ptr(), block_table.shape[1], cache_seqlens.data_ptr(), float(sm_scale),
                              int(window), int(sinks), int(is_fp8),
-                             kv_scales.data_ptr() if kv_scales is not None else None, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr())
+                             kv_scales.data_ptr() if kv_scales is not None else None, ws.data_ptr(), ws.nbytes,
+                             o.data_ptr(), z.data_ptr())
         _check(lib().mla_window_decode(ctypes.byref(a), handle))
-    return out.view(batch, s_q, h_q, D_V), lse.view(batch, s_q, h_q)
+        return o, z
+
+    return _launch(dev, stream, call)
 
 
 def shared_prefix_decode_workspace_size(batch: int, *, h_q: int, s_q: int, prefix_table_len: int,
@@ -655,21 +675,24 @@ def shared_prefix_decode(q: torch.Tensor, kvcache: torch.Tensor, prefix_table: t
     if prefix_length.shape[0] != 1:
         raise ValueError("prefix_length must have one entry")
     batch, s_q, h_q, _ = q.shape
-    with _On(dev, stream) as handle:
-        out, lse = _outputs(q, out, lse)
+
+    def call(handle):
+        o, z = _outputs(q, out, lse)
         n = ctypes.c_size_t()
         if workspace is None:
             _check(lib().mla_shared_prefix_decode_workspace_size(batch, h_q, s_q, prefix_table.shape[0], int(is_fp8),
                                                                  ctypes.byref(n)))
-        workspace = _scratch(workspace, n.value, dev)
+        ws = _scratch(workspace, n.value, dev)
         a = SharedPrefixDecodeArgs(q.data_ptr(), batch, s_q, h_q, kvcache.data_ptr(), kvcache.shape[0],
                                    kvcache.shape[1], prefix_table.data_ptr(), prefix_table.shape[0],
                                    prefix_length.data_ptr(), block_table.data_ptr(), block_table.shape[1],
                                    cache_seqlens.data_ptr(), float(sm_scale), int(bool(is_causal)), int(is_fp8),
-                                   kv_scales.data_ptr() if kv_scales is not None else None, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), out.data_ptr(), lse.data_ptr())
+                                   kv_scales.data_ptr() if kv_scales is not None else None, ws.data_ptr(),
+                                   ws.nbytes, o.data_ptr(), z.data_ptr())
         _check(lib().mla_shared_prefix_decode(ctypes.byref(a), handle))
-    return out.view(batch, s_q, h_q, D_V), lse.view(batch, s_q, h_q)
+        return o, z
+
+    return _launch(dev, stream, call)
 
 
 def index_topk_workspace_size(num_tokens: int, block_table_stride: int) -> int:

@@ -283,6 +283,26 @@ mla_status prefill_layout(int s_q, int h_q, int topk, Geometry* g, PrefillLayout
   return MLA_OK;
 }
 
+// Dense and windowed decode over an FP8 cache at up to 16 query rows run on the
+// register-level kernel (mla_decode_fp8.cu), more rows on the tcgen05 ones.
+// Measured (us, windows of 2048 + 64 keys): 16 rows 54.6 against 65.8 at 64
+// elements and 21.2 against 24.4 at 8; 32 rows, which it takes as two groups,
+// 85.8 against 74.8 and 21.8 against 27.6; 64 rows 149 against 78.
+constexpr int kFp8RowsMax = 16;
+void fp8_rows_geometry(Geometry* g) {
+  g->rpc = 16;
+  g->row_groups = (g->rows + 15) / 16;
+  g->pair = 0;
+  g->mode = 7;
+  g->tile_tokens = kTileTokens;
+  g->tile_cost = 4;
+  g->overhead = 4;  // a segment's start is about a page (16 rows, 64 elements: 61.1 us against 63.2 at 8)
+  const int forced = g_test_num_parts.load();
+  g->num_parts = forced > 0 ? forced : g->sm_count / g->row_groups;
+  if (g->num_parts < 1) g->num_parts = 1;
+  g->tag = g->rpc | (g->mode << 8) | (1 << 12);
+}
+
 // Windowed decode: schedule, slot prefix sums and split-KV partials.
 struct WindowLayout {
   size_t num_splits, o_accum, lse_accum, total;  // (the schedule comes first)
@@ -291,7 +311,11 @@ mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, Geometry* g, W
   mla_status st = geometry(batch, h_q, s_q, 0, is_fp8, g);
   if (st != MLA_OK) return st;
   g->mode = is_fp8 ? 5 : 4;
-  g->tag = g->rpc | (g->mode << 8) | ((g->tile_tokens / kTileTokens) << 12) | (g->pair << 15);
+  // a segment on a CTA pair costs about four of its tiles to start and to end
+  // (48 elements x 256 rows, 17 pages: 71.6 us against 74.8 at one tile)
+  if (g->pair) g->overhead = 32;
+  if (is_fp8 && g->rows <= kFp8RowsMax) fp8_rows_geometry(g);
+  if (g->mode != 7) g->tag = g->rpc | (g->mode << 8) | ((g->tile_tokens / kTileTokens) << 12) | (g->pair << 15);
   size_t ob, lb;
   workspace_layout(*g, &ob, &lb);
   L->num_splits = align256(static_cast<size_t>(g->num_parts) * kSchedInts * sizeof(int32_t));
@@ -318,6 +342,7 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   st = device_info(nullptr, nullptr, &pairs);
   if (st != MLA_OK) return st;
   const long long rows = static_cast<long long>(batch) * L->own.rows;
+  if (is_fp8 && L->own.rows <= kFp8RowsMax) fp8_rows_geometry(&L->own);
   L->prefix_problems = static_cast<int>((rows + 127) / 128);
   L->blocks_per_elem = is_fp8 ? 1 : (L->own.rows + 127) / 128;
   L->block_rows = is_fp8 ? L->own.rows : (L->own.rows < 128 ? L->own.rows : 128);
@@ -336,6 +361,10 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   g.mode = 6;
   g.tile_tokens = 128;
   g.tile_cost = 8;
+  // a segment costs about five tiles to start and to end: with one, the parts
+  // that hold many short own-key problems ended last (64 x 128 rows, 8192
+  // shared and ~256 own keys: 250 us at one tile, 183 at three, 163 at five)
+  g.overhead = 40;
   const int forced = g_test_num_parts.load();
   g.num_parts = forced > 0 ? forced : (pairs > 0 ? pairs : 1);
   g.tag = g.rpc | (g.mode << 8) | (2 << 12) | (1 << 15);
@@ -882,7 +911,7 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   const long long cache_rows = static_cast<long long>(a->num_pages) * kPageSize;
   if (g.pair) {
     st = encode_pair_maps(a->q, qrows, a->kvcache, cache_rows, &tm_q, &tm_kv, &tm_kv2);
-  } else {
+  } else if (g.mode != 7) {
     st = encode_rows_map(&tm_q, a->q, qrows, g.rpc, "q");
     if (st == MLA_OK)
       st = a->is_fp8 ? encode_byte_rows_map(&tm_kv, a->kvcache, cache_rows, a->kv_scales ? 640 : kFp8RowBytes, 32)
@@ -934,7 +963,9 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_schedule(spec, g, sched, num_splits, s);
   if (e != cudaSuccess) return cuda_fail(e, "schedule kernel launch");
-  e = g.pair ? launch_window_pair(tm_q, tm_kv, tm_kv2, p, s) : launch_decode(tm_q, tm_kv, p, g.rpc, g.mode, s);
+  e = g.pair        ? launch_window_pair(tm_q, tm_kv, tm_kv2, p, s)
+      : g.mode == 7 ? launch_decode_fp8(a->q, p, s)
+                    : launch_decode(tm_q, tm_kv, p, g.rpc, g.mode, s);
   if (e != cudaSuccess) return cuda_fail(e, "window decode kernel launch");
   CombineParams cp;
   memset(&cp, 0, sizeof cp);
@@ -949,7 +980,8 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   cp.rows = g.rows;
   cp.max_slots = p.max_slots;
   cp.status = status;
-  e = launch_combine(cp, s, true);
+  // (a batch of a quarter of the parts or more has about five pieces per problem at most)
+  e = 4 * g.num_problems >= g.num_parts ? launch_combine(cp, s, true) : launch_window_combine(cp, s);
   if (e != cudaSuccess) return cuda_fail(e, "combine kernel launch");
   return ok();
 }
@@ -997,9 +1029,11 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   if (a->is_fp8) {
     st = encode_pair_maps(a->q, qrows, ws + L.rows, static_cast<long long>(a->prefix_table_len) * kPageSize, &tm_q,
                           &tm_ks, &tm_kv);
-    if (st == MLA_OK) st = encode_rows_map(&tm_own_q, a->q, qrows, L.own.rpc, "q");
-    if (st == MLA_OK)
-      st = encode_byte_rows_map(&tm_own_kv, a->kvcache, cache_rows, a->kv_scales ? 640 : kFp8RowBytes, 32);
+    const int row_bytes = a->kv_scales ? 640 : kFp8RowBytes;
+    if (L.own.mode != 7) {
+      if (st == MLA_OK) st = encode_rows_map(&tm_own_q, a->q, qrows, L.own.rpc, "q");
+      if (st == MLA_OK) st = encode_byte_rows_map(&tm_own_kv, a->kvcache, cache_rows, row_bytes, 32);
+    }
   } else {
     st = encode_pair_maps(a->q, qrows, a->kvcache, cache_rows, &tm_q, &tm_ks, &tm_kv);
   }
@@ -1087,7 +1121,8 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
     o.sched_tag = L.own.tag;
     o.kv_scales = a->kv_scales;
     o.fp8_rope_off = a->kv_scales ? kDv : kFp8RopeOffset;
-    e = launch_decode(tm_own_q, tm_own_kv, o, L.own.rpc, L.own.mode, s);
+    e = L.own.mode == 7 ? launch_decode_fp8(a->q, o, s)
+                        : launch_decode(tm_own_q, tm_own_kv, o, L.own.rpc, L.own.mode, s);
     if (e != cudaSuccess) return cuda_fail(e, "decode kernel launch");
   }
   PrefixCombineParams cp;

@@ -1,0 +1,692 @@
+// K9 — dense or windowed decode over an FP8 cache, 16 query rows per CTA, on
+// register-level matrix instructions.
+//
+// The same computation as the FP8 modes of the single-CTA kernel
+// (mla_decode.cu), but the FP8 rows are never written back to shared memory
+// as bf16: that kernel's load -> dequantise -> multiply chain over one set of
+// slots takes ~5.1k cycles per 64-token page, where a page's bytes at the
+// card's copy rate take ~1.9k.  Here the codes go from shared memory straight
+// into the operand registers of mma.sync:
+//     S[r, t] = Q[r, :] . K[t, :],      K[t, d] = bf16_rn(c[t, d] s_b[t])
+//     O[r, d] = sum_t (P[r, t] s_b[t]) c[t, d]          (d in block b)
+// Keys are dequantised in registers, as the format defines them.  Values are
+// not: their scale joins the probability before it is rounded to fp16 (2^-12
+// where P alone would be rounded to bf16; the rounding of the dequantised
+// value is left out, which moves the result by its half step, 2^-8 of the sum
+// of |values|, at most) and the codes are exact in fp16.  P s is kept in
+// fp16's range by a power of two per value block that follows the scales.
+//
+// At 16 rows the legacy matrix instructions (8 cycles for 16 x 8 x 16 per SM
+// quarter, measured) need 544 instructions per page, 1.1k cycles, so the
+// page's bytes remain the bound; operands in registers need no shared-memory
+// round trip, no TMEM and no cross-proxy fences.  More rows run as groups of
+// 16 that each read the pages (from L2).
+//
+// Roles (640 threads, registers split by setmaxnreg):
+//   warp 0       producer: a page is one bulk copy of its 64 whole rows,
+//                per-token scales come by cp.async
+//   warps 4-11   scores and softmax: warp w owns 16 tokens of the page and two
+//                of the four 128-dim blocks (and half of the RoPE dims), with
+//                its half of Q as operand fragments in registers; the two
+//                halves of a sum meet through shared memory, each warp taking
+//                eight of the sixteen rows on
+//   warps 12-19  values: warp w owns 64 value dims of all tokens, its 16 x 64
+//                part of O in registers
+// Score and value warps work on different pages at the same time; P (fp32)
+// passes between them through a double buffer.
+//
+// Measured: 128 elements x 4160 keys, 137 us (2.4 TB/s, 35 % of the copy
+// rate; the tcgen05 kernel 175 us): 4.4k cycles per page.  Bound by
+// instruction issue: ~3.1k warp instructions per page and SM quarter, of
+// which two codes cost 6-8 on the score side (9 cycles of the conversion and
+// arithmetic pipes, measured alone) and 2.5 on the value side.  Tried: four
+// score warps over whole rows, 5.7k cycles per page (latency); sixteen over one
+// block each, 4.5k (issue slots 65 % busy, DRAM 33 %).
+#include "mla_device.cuh"
+#include "mla_internal.h"
+
+namespace mla {
+namespace {
+
+constexpr int kRows = 16;
+constexpr int kStages = 5;
+// A stage holds the page's rows as they lie in the cache, 656 bytes each, or
+// 640 bytes each and the 64 scales behind them.  656 bytes are 4 words past a
+// multiple of the banks' width, so the operand reads below (eight rows at one
+// 16-byte column, four rows at eight 4-byte ones) touch every bank once; rows
+// of 640 bytes cost two and four passes instead.
+template <bool TOKEN_SCALE>
+struct Rows {
+  static constexpr int kRow = TOKEN_SCALE ? 640 : kFp8RowBytes;
+  static constexpr int kRope = TOKEN_SCALE ? kDv : kFp8RopeOffset;
+  static constexpr int kPage = kPageSize * kRow;
+};
+constexpr int kScaleOff = Rows<true>::kPage;  // per-token scales
+constexpr int kStageBytes = Rows<false>::kPage;
+static_assert(kScaleOff + 4 * kPageSize <= kStageBytes && kStageBytes % 128 == 0, "stage layout");
+constexpr int kPStride = 72;                 // floats per row of P: 8 rows x 4 lane groups on distinct banks
+constexpr int kPOff = kStages * kStageBytes;
+constexpr int kPBytes = kRows * kPStride * 4;
+constexpr int kAuxOff = kPOff + 2 * kPBytes;
+// aux: score sums on their way to the other half [2][8 warps][32 lanes][4], row maxima of the four
+// token groups [2][16][4], alpha [2][16], row sums [16][4], 1/sum [16], page state per stage, abort
+// flag, barriers
+constexpr int kSwapOff = kAuxOff;
+constexpr int kMaxOff = kSwapOff + 2 * 8 * 32 * 16;
+constexpr int kAlphaOff = kMaxOff + 2 * kRows * 4 * 4;
+constexpr int kSumOff = kAlphaOff + 2 * kRows * 4;
+constexpr int kInvOff = kSumOff + kRows * 4 * 4;
+constexpr int kFlagOff = kInvOff + kRows * 4;
+constexpr int kAbortOff = kFlagOff + 8 * 4;
+constexpr int kBarOff = (kAbortOff + 4 + 15) / 16 * 16;
+constexpr int kNumBars = 2 * kStages + 6;
+constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+constexpr int kThreads = 640;
+constexpr uint32_t kRegsCtl = 24, kRegsScore = 128, kRegsValue = 96, kLaunchRegs = 96;
+// setmaxnreg hands out what the block was launched with and waits for ever for more
+static_assert(kRegsCtl + 2 * kRegsScore + 2 * kRegsValue <= 5 * kLaunchRegs && kThreads * kLaunchRegs <= 65536,
+              "register split");
+// named barriers: the two warps of a token group (four barriers), the four
+// warps of a half (two)
+constexpr uint32_t kSwapBar = 1, kRowsBar = 5;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kRescale = 8.0f;             // log2 units: P <= 2^8 before the running max is raised
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Shared-memory reads and writes as plain accesses, which the compiler may
+// reorder between the (volatile) waits and arrivals: the operand reads of the
+// next products then overlap the conversions and products of the last.
+template <class T>
+__device__ __forceinline__ T lds(const uint8_t* p) {
+  return *reinterpret_cast<const T*>(p);
+}
+template <class T>
+__device__ __forceinline__ void sts(uint8_t* p, T v) {
+  *reinterpret_cast<T*>(p) = v;
+}
+// What a CTA walks: problems p0..p1 of its part and, in each, a run of pages.
+struct Walk {
+  int p0, t0, p1, t1, np;
+  __device__ int last() const { return p1 < np ? p1 : np - 1; }
+};
+__device__ __forceinline__ KeyWalk walk_of(const DecodeParams& p, int L) {
+  if (p.window > 0) return key_walk(L, p.s_q, p.window, p.sinks);
+  const int n = L > 0 ? (L + kPageSize - 1) / kPageSize : 0;
+  return KeyWalk{n, n, 0};
+}
+__device__ __forceinline__ void range(const Walk& w, int prob, const KeyWalk& k, int& tb, int& te) {
+  tb = prob == w.p0 ? w.t0 : 0;
+  te = prob == w.p1 ? min(w.t1, k.pages) : k.pages;
+}
+// Whether some query token of the element sees key t, and whether all keys of a page are seen.
+__device__ __forceinline__ bool key_seen(const DecodeParams& p, int t, int L) {
+  return t < L && (p.window <= 0 || key_in_walk(t, L, p.s_q, p.window, p.sinks));
+}
+__device__ __forceinline__ bool page_seen_whole(const DecodeParams& p, int page, int L) {
+  const int first = page * kPageSize, last = first + kPageSize - 1;
+  if (last >= L) return false;
+  if (p.window <= 0) return true;
+  const int past = L - p.s_q - p.window;
+  return p.sinks > past || last < p.sinks || first > past;
+}
+
+struct Bars {
+  uint64_t* full;     // [kStages] page landed (bulk copy's bytes, 32 lanes' scale copies)
+  uint64_t* empty;    // [kStages] 8 score + 8 value warps are done with the page
+  uint64_t* p_full;   // [2] P and alpha of a page are written (8 score warps)
+  uint64_t* p_empty;  // [2] the value warps have read them
+  uint64_t* l_full;   // 1 / row sums of a segment are written (one warp of each half)
+  uint64_t* l_empty;  // the value warps have read them
+};
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wd));
+}
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16-byte aligned bulk copy global -> shared, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint8_t* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// producer (one warp)
+// ---------------------------------------------------------------------------
+template <bool TOKEN_SCALE>
+__device__ void produce(const DecodeParams& p, const Walk& w, uint8_t* smem, const Bars& bars,
+                        const Watchdog& wd) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol = p.evict_first ? l2_policy_evict_first() : l2_policy_evict_normal();
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + kFlagOff);
+  int jt = 0;
+  for (int prob = w.p0; prob <= w.last(); ++prob) {
+    const int L = p.cache_seqlens[prob];
+    const KeyWalk k = walk_of(p, L);
+    int tb, te;
+    range(w, prob, k, tb, te);
+    const int32_t* bt = p.block_table + static_cast<int64_t>(prob) * p.block_table_stride;
+    int ids = -1;  // page ids of pages j0 .. j0 + 31 of the walk, one per lane
+    for (int j = tb; j < te; ++j, ++jt) {
+      if (((j - tb) & 31) == 0) {
+        const int lp = j + lane < te ? k.page(j + lane) : -1;
+        ids = lp >= 0 && lp < p.block_table_stride ? __ldg(bt + lp) : -1;
+      }
+      const int pg = __shfl_sync(0xffffffffu, ids, (j - tb) & 31);
+      const bool ok = pg >= 0 && pg < p.num_pages;
+      const int s = jt % kStages;
+      if (jt >= kStages && !wait_warp(bars.empty + s, ((jt / kStages) - 1) & 1, wd)) goto drain;
+      uint8_t* dst = smem + s * kStageBytes;
+      if (lane == 0) {
+        if (!ok) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
+        flags[s] = ok ? 1 : 0;
+        // (an unusable page's stage keeps what it holds: all its tokens are masked)
+        mbar_arrive_expect_tx(bars.full + s, ok ? Rows<TOKEN_SCALE>::kPage : 0);
+        if (ok)
+          bulk_load(dst, p.kv_fp8 + static_cast<int64_t>(pg) * Rows<TOKEN_SCALE>::kPage, Rows<TOKEN_SCALE>::kPage,
+                    bars.full + s, pol);
+      }
+      if (TOKEN_SCALE) {
+        if (ok) {
+          const float* src = p.kv_scales + static_cast<int64_t>(pg) * kPageSize;
+          cp_async4(smem_u32(dst + kScaleOff) + 4 * lane, src + lane);
+          cp_async4(smem_u32(dst + kScaleOff) + 4 * (lane + 32), src + lane + 32);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bars.full + s)) : "memory");
+      }
+      __syncwarp();
+    }
+  }
+drain:
+  // no copy may be in flight when the CTA ends, after a timeout either: wait
+  // (bounded) for the latest phase of each stage
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (lane == 0) {
+    for (int i = jt > kStages ? jt - kStages : 0; i < jt; ++i) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bars.full + i % kStages, (i / kStages) & 1))
+        if (global_timer_ns() - t0 > wd.limit_ns) break;
+    }
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// scores and softmax (warps 4-11)
+// ---------------------------------------------------------------------------
+// Operand order.  In an instruction's 16 products over k, lane group c
+// (lane % 4) holds k = 2c, 2c + 1, 2c + 8, 2c + 9.  The order of the dims
+// within a sum is free, so lane group c takes dims [32 c, 32 c + 32) of a
+// block, four per instruction: 16-byte reads of consecutive codes.
+template <bool TOKEN_SCALE>
+__device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& p, const Walk& w, int g, int split0,
+                       uint8_t* smem, const Bars& bars, const Watchdog& wd) {
+  const int lane = threadIdx.x & 31, sw = (threadIdx.x >> 5) - 4;
+  const int tg = sw & 3, half = sw >> 2;  // token group, half of the dims (then rows 8 half .. 8 half + 7)
+  const int r = lane >> 2, c = lane & 3;
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + kFlagOff);
+  if (p.debug_stall) {
+    // watchdog test: nothing completes this barrier before this role has run
+    const bool ok = named_bar_and(kSwapBar + tg, 64, mbar_wait(bars.l_empty, 0, wd));
+    if (!named_bar_and(kRowsBar + half, 128, ok)) return;
+  }
+  const int row = g * kRows + r + 8 * half;  // the row this lane carries through the softmax
+  int jt = 0, seg = 0;
+  for (int prob = w.p0; prob <= w.last(); ++prob) {
+    const int L = p.cache_seqlens[prob];
+    const KeyWalk walk = walk_of(p, L);
+    int tb, te;
+    range(w, prob, walk, tb, te);
+    if (tb >= te) continue;
+
+    // Q fragments of this half's dims: rows r and r + 8 of the group (zeros for rows that do not exist)
+    uint32_t qf[18][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int qr = g * kRows + r + 8 * h;
+      const bool real = qr < p.rows;
+      const uint4* src =
+          reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(prob) * p.rows + (real ? qr : 0)) * kDqk);
+#pragma unroll
+      for (int k = 0; k < 9; ++k) {
+        // two instructions' worth: block 2 half + k / 4, dims 32 c + 8 (k % 4) of it; the last RoPE dims 16 c + 8 half
+        const int at = k < 8 ? 16 * (2 * half + (k >> 2)) + 4 * c + (k & 3) : 64 + 2 * c + half;
+        const uint4 v = real ? __ldg(src + at) : make_uint4(0, 0, 0, 0);
+        qf[2 * k][h] = v.x;
+        qf[2 * k][h + 2] = v.y;
+        qf[2 * k + 1][h] = v.z;
+        qf[2 * k + 1][h + 2] = v.w;
+      }
+    }
+    const int lim = p.is_causal ? min(L - p.s_q + row / p.h_q, L - 1) : L - 1;
+    const int low = p.window > 0 ? lim - p.window : -1;  // keys up to here are outside the window
+    float m = kNegInf, l = 0.f;
+
+    for (int j = tb; j < te; ++j, ++jt) {
+      const int s = jt % kStages, buf = jt & 1;
+      bool ok = wait_warp(bars.full + s, (jt / kStages) & 1, wd);
+      const uint8_t* stage = smem + s * kStageBytes;
+      const uint8_t* keys = stage + (16 * tg + r) * Rows<TOKEN_SCALE>::kRow;  // operand column r; the next group 8 rows on
+      // scales of this lane's two key tokens for the two blocks
+      float sc[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        if (TOKEN_SCALE) {
+          sc[n][0] = sc[n][1] = lds<float>(stage + kScaleOff + 4 * (16 * tg + 8 * n + r));
+        } else {
+          const float2 v = lds<float2>(keys + 8 * n * kFp8RowBytes + kFp8ScaleOffset + 8 * half);
+          sc[n][0] = v.x;
+          sc[n][1] = v.y;
+        }
+      }
+      // [token group][row r: tokens 2c, 2c + 1; row r + 8: the same], in two
+      // parts so that four chains of products run at a time
+      float x[2][4], y[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] = y[n][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // block 2 half + k / 2, 16 codes k % 2 of this lane's 32
+        uint4 v[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          v[n] = lds<uint4>(keys + 8 * n * Rows<TOKEN_SCALE>::kRow + 128 * (2 * half + (k >> 1)) + 32 * c + 16 * (k & 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t word = i == 0 ? v[n].x : i == 1 ? v[n].y : i == 2 ? v[n].z : v[n].w;
+            mma_bf16((i & 1) ? y[n] : x[n], qf[4 * k + i], e4m3x2_scaled_bf16x2(word & 0xffffu, sc[n][k >> 1]),
+                     e4m3x2_scaled_bf16x2(word >> 16, sc[n][k >> 1]));
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint4 v =
+            lds<uint4>(keys + 8 * n * Rows<TOKEN_SCALE>::kRow + Rows<TOKEN_SCALE>::kRope + 32 * c + 16 * half);
+        mma_bf16(x[n], qf[16], v.x, v.y);
+        mma_bf16(y[n], qf[17], v.z, v.w);
+      }
+      const bool page_ok = flags[s] != 0;
+      // the other half's rows go to its warp of this token group, this half's come from there.  (A
+      // buffer is written again two pages on, after the barriers of the page between.)
+      float4* swap = reinterpret_cast<float4*>(smem + kSwapOff) + buf * 8 * 32;
+      swap[sw * 32 + lane] = half == 0 ? make_float4(x[0][2] + y[0][2], x[0][3] + y[0][3], x[1][2] + y[1][2], x[1][3] + y[1][3])
+                                       : make_float4(x[0][0] + y[0][0], x[0][1] + y[0][1], x[1][0] + y[1][0], x[1][1] + y[1][1]);
+      float z[4];  // tokens 2c, 2c + 1, 8 + 2c, 9 + 2c of the group for row r + 8 half
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        z[i] = half == 0 ? x[i >> 1][i & 1] + y[i >> 1][i & 1] : x[i >> 1][2 + (i & 1)] + y[i >> 1][2 + (i & 1)];
+      arrive_warp(bars.empty + s);  // the page is read
+      // the P buffer was last read for the page two back
+      if (jt >= 2) ok = wait_warp(bars.p_empty + buf, ((jt >> 1) - 1) & 1, wd) && ok;
+      // a warp that gave up tells its partner here and both tell their halves
+      // below: all eight leave at the same page
+      ok = named_bar_and(kSwapBar + tg, 64, ok);
+      {
+        const float4 o = swap[(sw ^ 4) * 32 + lane];
+        z[0] = (z[0] + o.x) * p.scale_log2;
+        z[1] = (z[1] + o.y) * p.scale_log2;
+        z[2] = (z[2] + o.z) * p.scale_log2;
+        z[3] = (z[3] + o.w) * p.scale_log2;
+      }
+      // mask: page usable, key at or before the row's last one, and among the first keys or in the window
+      const int first = walk.page(j) * kPageSize;
+      if (!(page_ok && first + kPageSize - 1 <= lim &&
+            (p.window <= 0 || first + kPageSize - 1 < p.sinks || first > low))) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = first + 16 * tg + 2 * c + 8 * (i >> 1) + (i & 1);
+          if (!(page_ok && t <= lim && (p.window <= 0 || t < p.sinks || t > low))) z[i] = kNegInf;
+        }
+      }
+      // row maximum: the lane groups of the warp, then the four token groups
+      float mx = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      uint8_t* tops = smem + kMaxOff + (buf * kRows + r + 8 * half) * 16;
+      if (c == 0) sts(tops + 4 * tg, mx);
+      if (!named_bar_and(kRowsBar + half, 128, ok)) return;
+      const float4 top4 = lds<float4>(tops);
+      const float top = fmaxf(fmaxf(top4.x, top4.y), fmaxf(top4.z, top4.w));
+      float alpha = 1.f;
+      if (top > m + kRescale) {  // (the first finite maximum always)
+        alpha = m == kNegInf ? 0.f : fast_exp2(m - top);
+        m = top;
+        l *= alpha;
+      }
+      if (tg == 0 && c == 0) sts(smem + kAlphaOff + (buf * kRows + r + 8 * half) * 4, alpha);
+      float pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        pr[i] = z[i] == kNegInf ? 0.f : fast_exp2(z[i] - m);
+        l += pr[i];
+      }
+      uint8_t* prow = smem + kPOff + buf * kPBytes + ((r + 8 * half) * kPStride + 16 * tg + 2 * c) * 4;
+      sts(prow, make_float2(pr[0], pr[1]));
+      sts(prow + 32, make_float2(pr[2], pr[3]));
+      arrive_warp(bars.p_full + buf);
+    }
+
+    // end of the segment: row sums over lane groups and token groups, 1 / sum for the value warps, the log-sum-exp
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (c == 0) sts(smem + kSumOff + ((r + 8 * half) * 4 + tg) * 4, l);
+    bool ok = true;
+    if (seg > 0) ok = wait_warp(bars.l_empty, (seg - 1) & 1, wd);  // the previous segment's sums are read
+    ok = named_bar_and(kSwapBar + tg, 64, ok);
+    if (!named_bar_and(kRowsBar + half, 128, ok)) return;
+    if (tg == 0) {
+      if (c == 0) {
+        const int base_slot = p.num_splits[prob], pieces = p.num_splits[prob + 1] - base_slot;
+        const bool final_out = pieces <= 1 && !p.always_partial;
+        const int slot = base_slot + (prob == w.p0 ? split0 : 0);
+        const float4 v = lds<float4>(smem + kSumOff + (r + 8 * half) * 16);
+        const float sum = (v.x + v.y) + (v.z + v.w);
+        sts(smem + kInvOff + (r + 8 * half) * 4, sum == 0.f ? 0.f : 1.f / sum);
+        const float lse = sum == 0.f ? kNegInf : m + log2f(sum);  // (NaN stays NaN)
+        if (row < p.rows) {
+          if (final_out)
+            p.lse[static_cast<int64_t>(prob) * p.rows + row] = lse;
+          else if (slot >= 0 && slot < p.max_slots)
+            p.lse_accum[static_cast<int64_t>(slot) * p.rows + row] = lse;
+        }
+      }
+      arrive_warp(bars.l_full);
+    }
+    // (the sums are written again only after the next segment's barriers)
+    ++seg;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// values (warps 12-19)
+// ---------------------------------------------------------------------------
+// Warp v owns value dims [64 v, 64 v + 64), half of block v / 2.  Lane (r, c)
+// reads four codes at dims 32 g + 4 r of tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a
+// 16-token step: column r of the instruction for code i is dim 32 g + 4 r + i, so
+// a lane ends with dims 32 g + 8 c .. + 7 of rows r and r + 8: 16-byte stores.
+template <bool TOKEN_SCALE>
+__device__ void values(const DecodeParams& p, const Walk& w, int g, int split0, uint8_t* smem, const Bars& bars,
+                       const Watchdog& wd) {
+  const int lane = threadIdx.x & 31, v = (threadIdx.x >> 5) - 12;
+  const int r = lane >> 2, c = lane & 3;
+  const int blk = v >> 1;
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + kFlagOff);
+  int jt = 0, seg = 0;
+  for (int prob = w.p0; prob <= w.last(); ++prob) {
+    const int L = p.cache_seqlens[prob];
+    const KeyWalk walk = walk_of(p, L);
+    int tb, te;
+    range(w, prob, walk, tb, te);
+    if (tb >= te) continue;
+    // O is kept at `unit` times its value, a power of two near the inverse of
+    // the block's scales, raised out of the way when a page's are 2^6 larger:
+    // P s unit is below 2^15 (P <= 2^8) and fp16 holds it to 2^-12 down to
+    // 2^-14 and to 2^-25 in absolute terms below
+    float unit = 0.f;
+    float o[2][4][4];  // [32-dim group][code i][row r: dims 8c + i, 8c + 4 + i; row r + 8]
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[a][i][e] = 0.f;
+    for (int j = tb; j < te; ++j, ++jt) {
+      const int s = jt % kStages, buf = jt & 1;
+      if (!wait_warp(bars.full + s, (jt / kStages) & 1, wd)) return;
+      const uint8_t* stage = smem + s * kStageBytes;
+      const int lp = walk.page(j);
+      const bool page_ok = flags[s] != 0;
+      const bool whole = page_ok && page_seen_whole(p, lp, L);
+      {
+        // largest scale of the block among the page's tokens that are seen
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = lane + 32 * i;
+          const float x = lds<float>(TOKEN_SCALE ? stage + kScaleOff + 4 * t
+                                                 : stage + t * kFp8RowBytes + kFp8ScaleOffset + 4 * blk);
+          if (whole || (page_ok && key_seen(p, lp * kPageSize + t, L))) big = fmaxf(big, x);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+        if (big > 0.f && !(big * unit <= 64.f && unit > 0.f)) {
+          // 2^-(exponent of big), within fp32's normal range
+          const int e = min(max(254 - static_cast<int>(__float_as_uint(big) >> 23), 1), 253);
+          const float to = __uint_as_float(static_cast<uint32_t>(e) << 23);
+          if (unit > 0.f) {
+            const float f = to / unit;
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[a][i][k] *= f;
+          }
+          unit = to;
+        }
+      }
+      if (!wait_warp(bars.p_full + buf, (jt >> 1) & 1, wd)) return;
+      const uint8_t* pa = smem + kPOff + buf * kPBytes;
+      const float a0 = lds<float>(smem + kAlphaOff + (buf * kRows + r) * 4);
+      const float a1 = lds<float>(smem + kAlphaOff + (buf * kRows + r + 8) * 4);
+      if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[a][i][0] *= a0;
+            o[a][i][1] *= a0;
+            o[a][i][2] *= a1;
+            o[a][i][3] *= a1;
+          }
+      }
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const int t = 16 * kk + 2 * c;
+        float2 x[4];  // P of rows r, r + 8 at tokens t, t + 1; then t + 8, t + 9
+        x[0] = lds<float2>(pa + (r * kPStride + t) * 4);
+        x[1] = lds<float2>(pa + ((r + 8) * kPStride + t) * 4);
+        x[2] = lds<float2>(pa + (r * kPStride + t + 8) * 4);
+        x[3] = lds<float2>(pa + ((r + 8) * kPStride + t + 8) * 4);
+        float2 sl, sh;
+        if (TOKEN_SCALE) {
+          sl = lds<float2>(stage + kScaleOff + 4 * t);
+          sh = lds<float2>(stage + kScaleOff + 4 * (t + 8));
+        } else {
+          const uint8_t* row = stage + t * kFp8RowBytes + kFp8ScaleOffset + 4 * blk;
+          sl = make_float2(lds<float>(row), lds<float>(row + kFp8RowBytes));
+          sh = make_float2(lds<float>(row + 8 * kFp8RowBytes), lds<float>(row + 9 * kFp8RowBytes));
+        }
+        // a token that no row sees may hold anything: its scale and codes become 0
+        bool k0 = true, k1 = true, k8 = true, k9 = true;
+        if (!whole) {
+          const int t0 = lp * kPageSize + t;
+          k0 = page_ok && key_seen(p, t0, L), k1 = page_ok && key_seen(p, t0 + 1, L);
+          k8 = page_ok && key_seen(p, t0 + 8, L), k9 = page_ok && key_seen(p, t0 + 9, L);
+          if (!k0) sl.x = 0.f;
+          if (!k1) sl.y = 0.f;
+          if (!k8) sh.x = 0.f;
+          if (!k9) sh.y = 0.f;
+        }
+        sl.x *= unit;
+        sl.y *= unit;
+        sh.x *= unit;
+        sh.y *= unit;
+        const uint32_t a[4] = {pack_f16x2(x[0].x * sl.x, x[0].y * sl.y), pack_f16x2(x[1].x * sl.x, x[1].y * sl.y),
+                               pack_f16x2(x[2].x * sh.x, x[2].y * sh.y), pack_f16x2(x[3].x * sh.x, x[3].y * sh.y)};
+        constexpr int kRow = Rows<TOKEN_SCALE>::kRow;
+        const uint8_t* codes = stage + t * kRow + 64 * v + 4 * r;
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          uint32_t w0 = lds<uint32_t>(codes + 32 * d), w1 = lds<uint32_t>(codes + 32 * d + kRow);
+          uint32_t w8 = lds<uint32_t>(codes + 32 * d + 8 * kRow), w9 = lds<uint32_t>(codes + 32 * d + 9 * kRow);
+          if (!whole) {
+            if (!k0) w0 = 0;
+            if (!k1) w1 = 0;
+            if (!k8) w8 = 0;
+            if (!k9) w9 = 0;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // byte i of each pair of tokens, as two fp16 values
+            const uint32_t sel = i | ((4 + i) << 4);
+            mma_f16(o[d][i], a, e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(w0, w1, sel))),
+                    e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(w8, w9, sel))));
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars.p_empty + buf);
+        mbar_arrive(bars.empty + s);
+      }
+    }
+
+    if (!wait_warp(bars.l_full, seg & 1, wd)) return;
+    const float back = unit > 0.f ? 1.f / unit : 0.f;  // (no scale above 0: O is 0)
+    const float i0 = lds<float>(smem + kInvOff + r * 4) * back, i1 = lds<float>(smem + kInvOff + (r + 8) * 4) * back;
+    arrive_warp(bars.l_empty);
+    const int base_slot = p.num_splits[prob], pieces = p.num_splits[prob + 1] - base_slot;
+    const bool final_out = pieces <= 1 && !p.always_partial;
+    const int slot = base_slot + (prob == w.p0 ? split0 : 0);
+    const bool slot_ok = final_out || (slot >= 0 && slot < p.max_slots);
+    if (!slot_ok && lane == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = g * kRows + r + 8 * h;
+      if (!slot_ok || row >= p.rows) continue;
+      const float inv = h == 0 ? i0 : i1;
+      const int64_t at = (static_cast<int64_t>(final_out ? prob : slot) * p.rows + row) * kDv + 64 * v + 8 * c;
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[i] = o[d][i][2 * h] * inv;
+          y[4 + i] = o[d][i][2 * h + 1] * inv;
+        }
+        if (final_out) {
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + 32 * d) = make_uint4(
+              pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.o_accum + at + 32 * d);
+          dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+          dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+        }
+      }
+    }
+    ++seg;
+  }
+}
+
+template <bool TOKEN_SCALE>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_rows_kernel(const __nv_bfloat16* __restrict__ q, const DecodeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kBarOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kAbortOff);
+  Bars bars{bar, bar + kStages, bar + 2 * kStages, bar + 2 * kStages + 2, bar + 2 * kStages + 4, bar + 2 * kStages + 5};
+  const int warp = threadIdx.x >> 5;
+  const int part = blockIdx.x / p.row_groups, g = blockIdx.x % p.row_groups;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bars.full + i, TOKEN_SCALE ? 1 + 32 : 1);  // the arming arrival and each lane's scale copies
+      mbar_init(bars.empty + i, 8 + 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars.p_full + i, 8);
+      mbar_init(bars.p_empty + i, 8);
+    }
+    mbar_init(bars.l_full, 2);
+    mbar_init(bars.l_empty, 8);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  Watchdog wd{abort_flag, p.status, p.timeout_ns};
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Walk w{0, 0, 0, 0, p.num_problems};
+  int split0 = 0;
+  if (p.sched[kSchedParts] == p.num_parts && p.sched[kSchedTag] == p.sched_tag) {
+    const int32_t* sr = p.sched + static_cast<int64_t>(part) * kSchedInts;
+    w.p0 = sr[kSchedP0];
+    w.t0 = sr[kSchedT0];
+    w.p1 = sr[kSchedP1];
+    w.t1 = sr[kSchedT1];
+    split0 = sr[kSchedSplit0];
+  } else {
+    w.p0 = -1;
+  }
+  if (w.p0 < 0 || w.p0 > w.np || w.p1 < w.p0 || w.p1 > w.np || w.t0 < 0 || w.t1 < 0) {
+    if (threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
+    w.p0 = w.p1 = w.np;  // nothing to do
+  }
+  if (warp < 4) {
+    regs_to<kRegsCtl, kLaunchRegs>();
+    if (warp == 0) produce<TOKEN_SCALE>(p, w, smem, bars, wd);
+  } else if (warp < 12) {
+    regs_to<kRegsScore, kLaunchRegs>();
+    scores<TOKEN_SCALE>(q, p, w, g, split0, smem, bars, wd);
+  } else {
+    regs_to<kRegsValue, kLaunchRegs>();
+    values<TOKEN_SCALE>(p, w, g, split0, smem, bars, wd);
+  }
+  __syncthreads();
+}
+
+template <bool TOKEN_SCALE>
+cudaError_t launch(const void* q, const DecodeParams& p, cudaStream_t stream) {
+  auto kern = fp8_rows_kernel<TOKEN_SCALE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.num_parts * p.row_groups);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const __nv_bfloat16*>(q), p);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_fp8(const void* q, const DecodeParams& p, cudaStream_t stream) {
+  return p.kv_scales ? launch<true>(q, p, stream) : launch<false>(q, p, stream);
+}
+
+}  // namespace mla

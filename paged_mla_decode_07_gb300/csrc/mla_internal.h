@@ -85,7 +85,8 @@ struct Geometry {
   int row_groups;    // ceil(rows / rpc)
   int num_parts;     // schedule parts (each = row_groups CTAs)
   int sm_count;
-  int mode;          // decode kernel mode: 0 dense bf16, 1 sparse FP8, 2 dense FP8, 3 sparse bf16 rows
+  int mode;          // decode kernel mode: 0 dense bf16, 1 sparse FP8, 2 dense FP8, 3 sparse bf16 rows, 4 and 5
+                     // windowed 0 and 2, 6 shared prefix on CTA pairs, 7 FP8 rows in registers
   int pair;          // 1: CTA-pair kernel (128 rows and 128-token tiles per pair), 0: one CTA per row group
   int tile_tokens;   // tokens per schedule tile (64, or 128 for the pair kernel)
   int tile_cost;     // schedule cost of one tile (quarter units of a 64-token bf16 tile)
@@ -225,6 +226,8 @@ struct SlotStoreParams {
 // Kernel launchers (defined in the .cu files); return a CUDA error code.
 cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, const Geometry& g, int32_t* sched,
                             int32_t* num_splits, cudaStream_t stream);
+// FP8 rows at 16 query rows per CTA (mla_decode_fp8.cu); window = 0: all keys
+cudaError_t launch_decode_fp8(const void* q, const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_schedule(const SchedSpec& spec, const Geometry& g, int32_t* sched, int32_t* num_splits,
                             cudaStream_t stream);
 // mode: 0 dense bf16 cache, 1 sparse FP8 cache, 2 dense FP8 cache, 3 sparse bf16 rows, 4 and 5 windowed dense
@@ -251,6 +254,7 @@ cudaError_t launch_prefix_rows(const uint8_t* kvcache, const float* kv_scales, c
                                const int32_t* prefix_len, int prefix_pages, int num_pages, void* rows, int32_t* table,
                                uint32_t* status, int sm_count, cudaStream_t stream);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool pdl);
+cudaError_t launch_window_combine(const CombineParams& p, cudaStream_t stream);
 cudaError_t launch_prefix_combine(const PrefixCombineParams& p, cudaStream_t stream);
 size_t decode_smem_bytes(int rpc, int mode);
 cudaError_t launch_fp8_cache_store(const uint16_t* x, int num_tokens, const int32_t* row_offsets,
