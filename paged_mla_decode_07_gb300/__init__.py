@@ -15,7 +15,9 @@ code path.  If ``libmla.so`` has not been built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
+import operator
 import os
 import threading
 from typing import Optional, Tuple
@@ -40,6 +42,7 @@ DEVICE_NO_ROOM = 0x8
 
 _lock = threading.Lock()
 _lib = None
+_native = None  # csrc/binding.cpp, loaded with the library
 
 
 class MLAError(RuntimeError):
@@ -139,7 +142,7 @@ def library_path() -> str:
 
 def lib():
     """Load libmla.so (built in-tree by ``build()``); raise if it is missing."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
     with _lock:
@@ -185,8 +188,30 @@ def lib():
             L.mla_shared_prefix_decode_workspace_size.restype = I
             L.mla_shared_prefix_decode.argtypes = [ctypes.POINTER(SharedPrefixDecodeArgs), P]
             L.mla_shared_prefix_decode.restype = I
-            _lib = L
+            if not os.path.exists(_build.BINDING):
+                raise RuntimeError(f"{_build.BINDING} not found: run paged_mla_decode_07_gb300.build()")
+            spec = importlib.util.spec_from_file_location("_mla_binding", _build.BINDING)
+            native = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(native)
+            _native, _lib = native, L
     return _lib
+
+
+def _plain(name: str, *args):
+    """The native binding's result for a call in its plain form, or None (see csrc/binding.cpp)."""
+    if _native is None:
+        lib()
+    r = getattr(_native, name)(*args)
+    if type(r) is int:
+        _check(r)
+    return r
+
+
+def _int32(value, name: str) -> int:
+    value = operator.index(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} = {value} does not fit 32 bits")
+    return value
 
 
 def last_error() -> str:
@@ -454,13 +479,18 @@ def assign_pages(cache_lengths: torch.Tensor, new_tokens: torch.Tensor, free_pag
     int32 [batch + 1], slot_map int32 [num_tokens], next_cursor int32 [1]); cache_seqlens may be
     given as cache_lengths and next_cursor as free_cursor, to advance them in place.
     """
+    if stream is None:
+        r = _plain("assign_pages", cache_lengths, new_tokens, free_pages, free_cursor, block_table, num_tokens, num_pages,
+                   cache_seqlens, row_offsets, slot_map, next_cursor)
+        if r is not None:
+            return r
     dev = _cuda_tensor(cache_lengths, "cache_lengths")
     _need(cache_lengths, "cache_lengths", torch.int32, dev, 1)
     _need(new_tokens, "new_tokens", torch.int32, dev, 1)
     _need(free_pages, "free_pages", torch.int32, dev, 1)
     _need(free_cursor, "free_cursor", torch.int32, dev, 1)
     _need(block_table, "block_table", torch.int32, dev, 2)
-    batch, num_tokens = cache_lengths.shape[0], int(num_tokens)
+    batch, num_tokens = cache_lengths.shape[0], _int32(num_tokens, "num_tokens")
     if new_tokens.shape[0] != batch or block_table.shape[0] != batch or free_cursor.shape[0] != 1:
         raise ValueError("new_tokens and block_table must have batch rows and free_cursor one entry")
     if num_tokens < 0:
@@ -478,7 +508,7 @@ def assign_pages(cache_lengths: torch.Tensor, new_tokens: torch.Tensor, free_pag
                                         for t, n in zip(given, sizes)]
         a = AssignPagesArgs(cache_lengths.data_ptr(), new_tokens.data_ptr(), batch, free_pages.data_ptr(),
                             free_pages.shape[0], free_cursor.data_ptr(), block_table.data_ptr(),
-                            block_table.shape[1], MAX_PAGES if num_pages is None else int(num_pages), num_tokens,
+                            block_table.shape[1], MAX_PAGES if num_pages is None else _int32(num_pages, "num_pages"), num_tokens,
                             lens.data_ptr(), offsets.data_ptr(), slots.data_ptr(), cursor.data_ptr())
         _check(lib().mla_assign_pages(ctypes.byref(a), handle))
         return lens, offsets, slots, cursor
@@ -495,6 +525,8 @@ def cache_store(latent: torch.Tensor, rope: torch.Tensor, slot_map: torch.Tensor
     (page * 64 + slot, negative: skipped), the slots distinct; kvcache bf16 [num_pages, 64, 1, 576],
     uint8 [.., 656] or, with kv_scales fp32 [num_pages, 64], uint8 [.., 640]; written in place.
     """
+    if stream is None and _plain("cache_store", latent, rope, slot_map, kvcache, kv_scales):
+        return
     dev = _cuda_tensor(latent, "latent")
     n = latent.shape[0] if latent.dim() == 2 else -1
     for t, name, width in ((latent, "latent", D_V), (rope, "rope", D_QK - D_V)):
@@ -507,6 +539,8 @@ def cache_store(latent: torch.Tensor, rope: torch.Tensor, slot_map: torch.Tensor
     _need(slot_map, "slot_map", torch.int32, dev, 1)
     if slot_map.shape[0] != n:
         raise ValueError(f"slot_map must have {n} entries (got {slot_map.shape[0]})")
+    if not isinstance(kvcache, torch.Tensor):
+        raise ValueError("kvcache must be a torch.Tensor")
     is_fp8 = _cache_format(kvcache, kv_scales, dev)
     a = CacheStoreArgs(latent.data_ptr(), latent.stride(0) if n > 1 else D_V, rope.data_ptr(),
                        rope.stride(0) if n > 1 else D_V, slot_map.data_ptr(), n, kvcache.data_ptr(),
@@ -630,6 +664,11 @@ def window_decode(q: torch.Tensor, kvcache: torch.Tensor, block_table: torch.Ten
     Arguments as decode()'s; query token i of an element of length L sits at position L - s_q + i and
     sees key t <= that position if t < sinks or t > position - window.  Returns (out bf16
     [b, s_q, h_q, 512], lse fp32 [b, s_q, h_q], base 2)."""
+    if stream is None:
+        r = _plain("window_decode", q, kvcache, block_table, cache_seqlens, sm_scale, window, sinks, kv_scales, out, lse,
+                   workspace)
+        if r is not None:
+            return r
     dev, is_fp8 = _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales)
     batch, s_q, h_q, _ = q.shape
 
@@ -641,7 +680,7 @@ def window_decode(q: torch.Tensor, kvcache: torch.Tensor, block_table: torch.Ten
         ws = _scratch(workspace, n.value, dev)
         a = WindowDecodeArgs(q.data_ptr(), batch, s_q, h_q, kvcache.data_ptr(), kvcache.shape[0], kvcache.shape[1],
                              block_table.data_ptr(), block_table.shape[1], cache_seqlens.data_ptr(), float(sm_scale),
-                             int(window), int(sinks), int(is_fp8),
+                             _int32(window, "window"), _int32(sinks, "sinks"), int(is_fp8),
                              kv_scales.data_ptr() if kv_scales is not None else None, ws.data_ptr(), ws.nbytes,
                              o.data_ptr(), z.data_ptr())
         _check(lib().mla_window_decode(ctypes.byref(a), handle))
@@ -669,6 +708,11 @@ def shared_prefix_decode(q: torch.Tensor, kvcache: torch.Tensor, prefix_table: t
     prefix_table int32 [pages] and prefix_length int32 [1] (on the device) name the shared tokens,
     block_table and cache_seqlens each element's own; every query row attends to both.  Returns (out
     bf16 [b, s_q, h_q, 512], lse fp32 [b, s_q, h_q], base 2)."""
+    if stream is None:
+        r = _plain("shared_prefix_decode", q, kvcache, prefix_table, prefix_length, block_table, cache_seqlens, sm_scale,
+                   is_causal, kv_scales, out, lse, workspace)
+        if r is not None:
+            return r
     dev, is_fp8 = _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales)
     _need(prefix_table, "prefix_table", torch.int32, dev, 1)
     _need(prefix_length, "prefix_length", torch.int32, dev, 1)

@@ -1,7 +1,9 @@
-"""Build libmla.so (the C-ABI decode library) for sm_103a with nvcc.
+"""Build libmla.so (the C-ABI decode library) for sm_103a with nvcc, and the
+native part of the Python binding with g++.
 
 Each translation unit is compiled in parallel, then linked into
-``paged_mla_decode_07_gb300/_build/libmla.so`` (in-tree, git-ignored).
+``paged_mla_decode_07_gb300/_build/libmla.so`` and ``_mla_binding.so`` beside
+it (in-tree, git-ignored).
 Usage: ``python -m paged_mla_decode_07_gb300.builder [--verbose]``.
 """
 from __future__ import annotations
@@ -11,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmla.so")
+BINDING = os.path.join(BUILD, "_mla_binding.so")
 SOURCES = ["mla_api.cu", "mla_sched.cu", "mla_decode.cu", "mla_decode_pair.cu", "mla_combine.cu", "mla_noalloc.cu",
            "mla_store.cu", "mla_index.cu", "mla_pages.cu", "mla_prefix.cu", "mla_decode_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,9 +41,9 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps() + [os.path.abspath(__file__)])
 
 
@@ -60,14 +64,38 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding():
+        import torch
+
+        inc = os.path.join(os.path.dirname(torch.__file__), "include")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
+        obj = os.path.join(BUILD, "binding.o")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               *(f"-isystem{p}" for p in (sysconfig.get_paths()["include"], inc,
+                                          os.path.join(inc, "torch", "csrc", "api", "include"), cuda)),
+               "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj, os.path.join(os.path.dirname(torch.__file__), "lib")
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj, torch_lib = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, binding_obj, f"-L{BUILD}", "-l:libmla.so", "-Wl,-rpath,$ORIGIN",
+           f"-L{torch_lib}", f"-Wl,-rpath,{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 
