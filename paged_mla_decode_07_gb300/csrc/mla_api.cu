@@ -300,12 +300,11 @@ void fp8_rows_geometry(Geometry* g) {
   const int forced = g_test_num_parts.load();
   g->num_parts = forced > 0 ? forced : g->sm_count / g->row_groups;
   if (g->num_parts < 1) g->num_parts = 1;
-  g->tag = g->rpc | (g->mode << 8) | (1 << 12);
 }
 
-// Windowed decode: schedule, slot prefix sums and split-KV partials.
+// Windowed decode: spans of the problems and split-KV partials.
 struct WindowLayout {
-  size_t num_splits, o_accum, lse_accum, total;  // (the schedule comes first)
+  size_t o_accum, lse_accum, total;  // (the spans come first)
 };
 mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, Geometry* g, WindowLayout* L) {
   mla_status st = geometry(batch, h_q, s_q, 0, is_fp8, g);
@@ -315,13 +314,11 @@ mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, Geometry* g, W
   // (48 elements x 256 rows, 17 pages: 71.6 us against 74.8 at one tile)
   if (g->pair) g->overhead = 32;
   if (is_fp8 && g->rows <= kFp8RowsMax) fp8_rows_geometry(g);
-  if (g->mode != 7) g->tag = g->rpc | (g->mode << 8) | ((g->tile_tokens / kTileTokens) << 12) | (g->pair << 15);
-  size_t ob, lb;
-  workspace_layout(*g, &ob, &lb);
-  L->num_splits = align256(static_cast<size_t>(g->num_parts) * kSchedInts * sizeof(int32_t));
-  L->o_accum = L->num_splits + align256((static_cast<size_t>(g->num_problems) + 1) * sizeof(int32_t));
-  L->lse_accum = L->o_accum + ob;
-  L->total = L->lse_accum + lb;
+  // two slots per part: the problems it starts and ends inside of
+  const size_t slots = 2 * static_cast<size_t>(g->num_parts);
+  L->o_accum = align256(static_cast<size_t>(g->num_problems) * 2 * sizeof(int32_t));
+  L->lse_accum = L->o_accum + align256(slots * g->rows * kDv * sizeof(float));
+  L->total = L->lse_accum + align256(slots * g->rows * sizeof(float));
   return MLA_OK;
 }
 
@@ -332,7 +329,7 @@ mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, Geometry* g, W
 struct PrefixLayout {
   Geometry pre, own;
   int prefix_problems, blocks_per_elem, block_rows, prefix_slots, own_slots;
-  size_t sched, splits, own_sched, own_splits, o, lse, own_o, own_lse, table, rows, total;
+  size_t spans, own_spans, o, lse, own_o, own_lse, table, rows, total;
 };
 mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_fp8, PrefixLayout* L) {
   memset(L, 0, sizeof *L);
@@ -342,7 +339,12 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   st = device_info(nullptr, nullptr, &pairs);
   if (st != MLA_OK) return st;
   const long long rows = static_cast<long long>(batch) * L->own.rows;
-  if (is_fp8 && L->own.rows <= kFp8RowsMax) fp8_rows_geometry(&L->own);
+  if (is_fp8 && L->own.rows <= kFp8RowsMax) {
+    fp8_rows_geometry(&L->own);
+  } else if (is_fp8) {
+    // the windowed mode with a window that holds every key
+    L->own.mode = 5;
+  }
   L->prefix_problems = static_cast<int>((rows + 127) / 128);
   L->blocks_per_elem = is_fp8 ? 1 : (L->own.rows + 127) / 128;
   L->block_rows = is_fp8 ? L->own.rows : (L->own.rows < 128 ? L->own.rows : 128);
@@ -367,22 +369,17 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   g.overhead = 40;
   const int forced = g_test_num_parts.load();
   g.num_parts = forced > 0 ? forced : (pairs > 0 ? pairs : 1);
-  g.tag = g.rpc | (g.mode << 8) | (2 << 12) | (1 << 15);
-  // every piece takes a slot: one per problem and one more per part boundary
-  L->prefix_slots = L->prefix_problems + g.num_parts;
-  L->own_slots = static_cast<int>(own_problems) + (is_fp8 ? L->own.num_parts : g.num_parts);
+  // every piece takes a slot: two per part and one per problem held whole
+  L->prefix_slots = 2 * g.num_parts + L->prefix_problems;
+  L->own_slots = 2 * (is_fp8 ? L->own.num_parts : g.num_parts) + static_cast<int>(own_problems);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at += align256(bytes);
     return here;
   };
-  L->sched = take(static_cast<size_t>(g.num_parts) * kSchedInts * 4);
-  L->splits = take((static_cast<size_t>(np) + 1) * 4);
-  if (is_fp8) {
-    L->own_sched = take(static_cast<size_t>(L->own.num_parts) * kSchedInts * 4);
-    L->own_splits = take((static_cast<size_t>(batch) + 1) * 4);
-  }
+  L->spans = take(static_cast<size_t>(np) * 8);
+  L->own_spans = is_fp8 ? take(static_cast<size_t>(own_problems) * 8) : L->spans + static_cast<size_t>(L->prefix_problems) * 8;
   L->o = take(static_cast<size_t>(L->prefix_slots) * 128 * kDv * 4);
   L->lse = take(static_cast<size_t>(L->prefix_slots) * 128 * 4);
   L->own_o = take(static_cast<size_t>(L->own_slots) * L->block_rows * kDv * 4);
@@ -920,14 +917,13 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   if (st != MLA_OK) return st;
 
   char* ws = static_cast<char*>(a->workspace);
-  int32_t* sched = reinterpret_cast<int32_t*>(ws);
-  int32_t* num_splits = reinterpret_cast<int32_t*>(ws + L.num_splits);
   DecodeParams p;
   memset(&p, 0, sizeof p);
   p.block_table = a->block_table;
   p.cache_seqlens = a->cache_seqlens;
-  p.sched = sched;
-  p.num_splits = num_splits;
+  p.spans = reinterpret_cast<int32_t*>(ws);
+  p.tile_cost = g.tile_cost;
+  p.overhead = g.overhead;
   p.kv_fp8 = static_cast<const uint8_t*>(a->kvcache);
   p.out = a->out;
   p.lse = a->lse;
@@ -944,45 +940,33 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   p.rows = g.rows;
   p.row_groups = g.row_groups;
   p.num_parts = g.num_parts;
-  p.max_slots = max_slots(g);
+  p.max_slots = 2 * g.num_parts;
   p.is_causal = 1;  // a window ends at its query token
   p.window = a->window < kMaxWindow ? a->window : kMaxWindow;
   p.sinks = a->sinks;
   p.evict_first = (g.row_groups == 1 && !g.pair) ? 1 : 0;
-  p.sched_tag = g.tag;
   p.debug_stall = g_test_debug_stall.load();
   p.scale_log2 = a->sm_scale * 1.4426950408889634f;
   p.kv_scales = a->kv_scales;
   p.fp8_rope_off = a->kv_scales ? kDv : kFp8RopeOffset;
 
-  SchedSpec spec = {};
-  spec.seqlens = a->cache_seqlens;
-  spec.s_q = a->s_q;
-  spec.window = p.window;
-  spec.sinks = p.sinks;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_schedule(spec, g, sched, num_splits, s);
-  if (e != cudaSuccess) return cuda_fail(e, "schedule kernel launch");
+  cudaError_t e = cudaSuccess;
   e = g.pair        ? launch_window_pair(tm_q, tm_kv, tm_kv2, p, s)
       : g.mode == 7 ? launch_decode_fp8(a->q, p, s)
                     : launch_decode(tm_q, tm_kv, p, g.rpc, g.mode, s);
   if (e != cudaSuccess) return cuda_fail(e, "window decode kernel launch");
-  CombineParams cp;
-  memset(&cp, 0, sizeof cp);
-  cp.num_splits = num_splits;
-  cp.cache_seqlens = a->cache_seqlens;
-  cp.s_q = a->s_q;
-  cp.o_accum = p.o_accum;
-  cp.lse_accum = p.lse_accum;
-  cp.out = a->out;
-  cp.lse = a->lse;
-  cp.num_problems = g.num_problems;
-  cp.rows = g.rows;
-  cp.max_slots = p.max_slots;
-  cp.status = status;
-  // (a batch of a quarter of the parts or more has about five pieces per problem at most)
-  e = 4 * g.num_problems >= g.num_parts ? launch_combine(cp, s, true) : launch_window_combine(cp, s);
-  if (e != cudaSuccess) return cuda_fail(e, "combine kernel launch");
+  MergeParams m;
+  memset(&m, 0, sizeof m);
+  m.own = MergeSide{p.spans, p.o_accum, p.lse_accum, g.rows, -1};
+  m.cache_seqlens = a->cache_seqlens;
+  m.blocks_per_elem = 1;
+  m.rows = g.rows;
+  m.batch = a->batch;
+  m.out = a->out;
+  m.lse = a->lse;
+  e = launch_merge(m, s);
+  if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
   return ok();
 }
 
@@ -1039,10 +1023,6 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   }
   if (st != MLA_OK) return st;
 
-  int32_t* sched = reinterpret_cast<int32_t*>(ws + L.sched);
-  int32_t* splits = reinterpret_cast<int32_t*>(ws + L.splits);
-  int32_t* own_sched = reinterpret_cast<int32_t*>(ws + L.own_sched);
-  int32_t* own_splits = a->is_fp8 ? reinterpret_cast<int32_t*>(ws + L.own_splits) : splits + L.prefix_problems;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
 
@@ -1050,8 +1030,9 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   memset(&p, 0, sizeof p);
   p.block_table = a->block_table;
   p.cache_seqlens = a->cache_seqlens;
-  p.sched = sched;
-  p.num_splits = splits;
+  p.spans = reinterpret_cast<int32_t*>(ws + L.spans);
+  p.tile_cost = L.pre.tile_cost;
+  p.overhead = L.pre.overhead;
   p.o_accum = reinterpret_cast<float*>(ws + L.o);
   p.lse_accum = reinterpret_cast<float*>(ws + L.lse);
   p.own_o = reinterpret_cast<float*>(ws + L.own_o);
@@ -1071,7 +1052,6 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   p.own_slots = L.own_slots;
   p.block_rows = L.block_rows;
   p.is_causal = a->is_causal ? 1 : 0;
-  p.sched_tag = L.pre.tag;
   p.debug_stall = g_test_debug_stall.load();
   p.scale_log2 = a->sm_scale * 1.4426950408889634f;
   p.prefix_table = a->is_fp8 ? reinterpret_cast<const int32_t*>(ws + L.table) : a->prefix_table;
@@ -1081,33 +1061,19 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   p.blocks_per_elem = L.blocks_per_elem;
   p.total_rows = static_cast<int>(qrows);
 
-  SchedSpec spec = {};
-  spec.seqlens = a->cache_seqlens;
-  spec.s_q = a->s_q;
-  spec.prefix_len = a->prefix_length;
-  spec.prefix_problems = L.prefix_problems;
-  spec.blocks_per_elem = L.blocks_per_elem;
-  spec.always_partial = 1;
   if (a->is_fp8) {
     e = launch_prefix_rows(static_cast<const uint8_t*>(a->kvcache), a->kv_scales, a->prefix_table, a->prefix_length,
                            a->prefix_table_len, a->num_pages, ws + L.rows, reinterpret_cast<int32_t*>(ws + L.table),
                            status, sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "prefix rows kernel launch");
-    SchedSpec own = {};
-    own.seqlens = a->cache_seqlens;
-    own.s_q = a->s_q;
-    own.always_partial = 1;
-    e = launch_schedule(own, L.own, own_sched, own_splits, s);
-    if (e != cudaSuccess) return cuda_fail(e, "schedule kernel launch");
   }
-  e = launch_schedule(spec, L.pre, sched, splits, s);
-  if (e != cudaSuccess) return cuda_fail(e, "schedule kernel launch");
   e = launch_prefix_pair(tm_q, tm_ks, tm_kv, p, s);
   if (e != cudaSuccess) return cuda_fail(e, "shared-prefix decode kernel launch");
   if (a->is_fp8) {
     DecodeParams o = p;
-    o.sched = own_sched;
-    o.num_splits = own_splits;
+    o.spans = reinterpret_cast<int32_t*>(ws + L.own_spans);
+    o.tile_cost = L.own.tile_cost;
+    o.overhead = L.own.overhead;
     o.kv_fp8 = static_cast<const uint8_t*>(a->kvcache);
     o.o_accum = p.own_o;
     o.lse_accum = p.own_lse;
@@ -1116,34 +1082,32 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
     o.row_groups = L.own.row_groups;
     o.num_parts = L.own.num_parts;
     o.max_slots = L.own_slots;
+    o.prefix_len = nullptr;
+    o.window = kMaxWindow;  // every key
     o.always_partial = 1;
     o.evict_first = L.own.row_groups == 1 ? 1 : 0;
-    o.sched_tag = L.own.tag;
     o.kv_scales = a->kv_scales;
     o.fp8_rope_off = a->kv_scales ? kDv : kFp8RopeOffset;
     e = L.own.mode == 7 ? launch_decode_fp8(a->q, o, s)
                         : launch_decode(tm_own_q, tm_own_kv, o, L.own.rpc, L.own.mode, s);
     if (e != cudaSuccess) return cuda_fail(e, "decode kernel launch");
   }
-  PrefixCombineParams cp;
-  memset(&cp, 0, sizeof cp);
-  cp.prefix_splits = splits;
-  cp.prefix_o = p.o_accum;
-  cp.prefix_lse = p.lse_accum;
-  cp.own_splits = own_splits;
-  cp.own_o = p.own_o;
-  cp.own_lse = p.own_lse;
-  cp.block_rows = L.block_rows;
-  cp.blocks_per_elem = L.blocks_per_elem;
-  cp.rows = L.own.rows;
-  cp.total_rows = p.total_rows;
-  cp.prefix_slots = L.prefix_slots;
-  cp.own_slots = L.own_slots;
-  cp.out = a->out;
-  cp.lse = a->lse;
-  cp.status = status;
-  e = launch_prefix_combine(cp, s);
-  if (e != cudaSuccess) return cuda_fail(e, "combine kernel launch");
+  MergeParams m;
+  memset(&m, 0, sizeof m);
+  m.prefix = MergeSide{p.spans, p.o_accum, p.lse_accum, 128, 2 * L.pre.num_parts};
+  const Geometry& og = a->is_fp8 ? L.own : L.pre;
+  m.own = MergeSide{reinterpret_cast<int32_t*>(ws + L.own_spans), p.own_o, p.own_lse, L.block_rows,
+                    2 * og.num_parts};
+  m.cache_seqlens = a->cache_seqlens;
+  m.prefix_len = a->prefix_length;
+  m.has_prefix = 1;
+  m.blocks_per_elem = L.blocks_per_elem;
+  m.rows = L.own.rows;
+  m.batch = a->batch;
+  m.out = a->out;
+  m.lse = a->lse;
+  e = launch_merge(m, s);
+  if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
   return ok();
 }
 

@@ -152,21 +152,38 @@ __global__ void __launch_bounds__(kRowsPerBlock * 32) combine_kernel(const Combi
   if (lane == 0) p.lse[grow] = L;
 }
 
-// Merges of windowed and shared-prefix decode, where a few rows may have many
-// pieces (a small batch is cut over all SMs): one block of 128 threads per
-// row, thread t owning dims [4 t, 4 t + 4), so that a row's pieces are read in
-// whole 2 KB lines with eight in flight per thread; the 32 log-sum-exps of a
-// round are one load of every warp and their weights reach the threads by
-// shuffles.  Bound by latency for small batches (slots, log-sum-exps, values:
-// three dependent reads) and by the partials' bytes for large ones: 96 rows of
-// 17 pieces take ~5 us less than with a warp per row that reads piece by piece.
+// ---------------------------------------------------------------------------
+// Merges of windowed and shared-prefix decode
+// ---------------------------------------------------------------------------
+// A block merges one row with all its 128 threads, thread t owning dims
+// [4 t, 4 t + 4) and eight pieces' 2 KB lines in flight, or four rows with a
+// warp each.  The first suits few rows in many pieces (a small batch is cut
+// over all SMs: 96 rows of 17 pieces take ~5 us less), the second many rows in
+// few (12288 rows of two pieces take 5 us less).  Bound by latency (spans and
+// lengths, log-sum-exps, values: three dependent reads), and by the partials'
+// bytes where there are many rows.
 constexpr int kMergeThreads = 128;
 constexpr float kMergeNegInf = -__builtin_huge_valf();
 
-// Merges n pieces of one row; lse_at(i) and values_at(i) name piece i.
-template <class LseAt, class ValuesAt>
-__device__ __forceinline__ void merge_row(int n, LseAt lse_at, ValuesAt values_at, __nv_bfloat16* out, float* lse) {
+// The pieces of problem `prob` of a side, `tiles` > 0 tiles: n of them, the
+// first in slot `slot`, the others in those of the parts behind it.  n = -1:
+// a part held the problem whole and wrote its output.
+struct Pieces {
+  int n, slot;
+  __device__ __forceinline__ int at(int i) const { return i == 0 ? slot : 2 * ((slot >> 1) + i); }
+};
+__device__ __forceinline__ Pieces find_pieces(const MergeSide& m, int prob) {
+  const int2 s = reinterpret_cast<const int2*>(m.spans)[prob];
+  const int n = s.y - (s.x >> 1) + 1;
+  if (n == 1) return m.whole_base < 0 ? Pieces{-1, 0} : Pieces{1, m.whole_base + prob};
+  return Pieces{n, s.x};
+}
+
+// Merges the pieces of one row with all threads of the block.
+template <class At>
+__device__ __forceinline__ void merge_row_block(int n, At at, __nv_bfloat16* out, float* lse) {
   const int lane = threadIdx.x & 31;
+  auto lse_at = [&](int i) { return *at(i).second; };
   const float first = lane < n ? lse_at(lane) : kMergeNegInf;  // pieces 0..31, one per lane
   float mx = first;
   for (int i = lane + 32; i < n; i += 32) mx = fmaxf(mx, lse_at(i));
@@ -189,7 +206,7 @@ __device__ __forceinline__ void merge_row(int n, LseAt lse_at, ValuesAt values_a
         float4 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (k0 + k < m) v[k] = values_at(i0 + k0 + k)[threadIdx.x];
+          if (k0 + k < m) v[k] = at(i0 + k0 + k).first[threadIdx.x];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
@@ -207,60 +224,107 @@ __device__ __forceinline__ void merge_row(int n, LseAt lse_at, ValuesAt values_a
   if (threadIdx.x == 0) *lse = L;
 }
 
-// Windowed decode: a problem in one piece wrote its rows itself; one without
-// keys has none.
-__global__ void __launch_bounds__(kMergeThreads) window_combine_kernel(const CombineParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int prob = blockIdx.x / p.rows, r = blockIdx.x % p.rows;
-  const int base = p.num_splits[prob], n = p.num_splits[prob + 1] - base;
-  if (n == 0 && p.cache_seqlens[prob] > 0) return;
-  if (base < 0 || n < 0 || n == 1 || base + n > p.max_slots) {
-    if (threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
-    return;
+// Merges the pieces of one row with one warp: lane l owns dims 128 v + 4 l .. + 3.
+template <class At>
+__device__ __forceinline__ void merge_row_warp(int n, At at, __nv_bfloat16* out, float* lse) {
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 31;
+  float mx = kMergeNegInf;
+  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, *at(i).second);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float4 acc[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = kMergeNegInf;
+  if (mx != kMergeNegInf) {
+    float sum = 0.f;
+    for (int i = lane; i < n; i += 32) sum += exp2f(*at(i).second - mx);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    L = mx + log2f(sum);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      float4 x[kAhead][4];
+      float w[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        w[i] = kMergeNegInf;
+        if (i0 + i < n) {
+          const auto piece = at(i0 + i);
+          w[i] = *piece.second;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) x[i][v] = piece.first[32 * v + lane];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (i0 + i >= n) break;
+        const float wi = exp2f(w[i] - L);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          acc[v].x += wi * x[i][v].x;
+          acc[v].y += wi * x[i][v].y;
+          acc[v].z += wi * x[i][v].z;
+          acc[v].w += wi * x[i][v].w;
+        }
+      }
+    }
   }
-  const int64_t at = static_cast<int64_t>(base) * p.rows + r;
-  merge_row(
-      n, [&](int i) { return p.lse_accum[at + static_cast<int64_t>(i) * p.rows]; },
-      [&](int i) { return reinterpret_cast<const float4*>(p.o_accum + (at + static_cast<int64_t>(i) * p.rows) * kDv); },
-      reinterpret_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(blockIdx.x) * kDv, p.lse + blockIdx.x);
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    reinterpret_cast<uint2*>(out)[32 * v + lane] =
+        make_uint2(pack_bf16x2(acc[v].x, acc[v].y), pack_bf16x2(acc[v].z, acc[v].w));
+  if (lane == 0) *lse = L;
 }
 
-// Shared-prefix decode: a row's pieces lie in two runs of slots, the prefix
-// under its block of 128 rows and its element's own keys, merged as one list.
-// An element without own keys has none of the second, an empty prefix none of
-// the first.
-__global__ void __launch_bounds__(kMergeThreads) prefix_combine_kernel(const PrefixCombineParams p) {
+struct PiecePtr {
+  const float4* first;   // the piece's 512 values
+  const float* second;   // its log-sum-exp
+};
+
+// grid: (row blocks of an element, elements); WARP_ROWS: four rows per block,
+// a warp each (then an element's rows are a multiple of four where there is a
+// prefix, so that the four lie in one block of its rows).
+template <bool WARP_ROWS>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int row = blockIdx.x;
-  const int elem = row / p.rows, r = row % p.rows;
-  const int pp = row / 128;
-  const int op = elem * p.blocks_per_elem + r / p.block_rows;
-  const int base0 = p.prefix_splits[pp], n0 = p.prefix_splits[pp + 1] - base0;
-  // (both kinds may come from one schedule: the own slots count from the first own problem's)
-  const int base1 = p.own_splits[op] - p.own_splits[0], n1 = p.own_splits[op + 1] - p.own_splits[op];
-  if (base0 < 0 || n0 < 0 || base0 + n0 > p.prefix_slots || base1 < 0 || n1 < 0 || base1 + n1 > p.own_slots) {
-    if (threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
-    return;
-  }
-  const int64_t at0 = static_cast<int64_t>(base0) * 128 + row % 128;
-  const int64_t at1 = static_cast<int64_t>(base1) * p.block_rows + r % p.block_rows;
-  merge_row(
-      n0 + n1,
-      [&](int i) {
-        return i < n0 ? p.prefix_lse[at0 + static_cast<int64_t>(i) * 128]
-                      : p.own_lse[at1 + static_cast<int64_t>(i - n0) * p.block_rows];
-      },
-      [&](int i) {
-        return reinterpret_cast<const float4*>(i < n0 ? p.prefix_o + (at0 + static_cast<int64_t>(i) * 128) * kDv
-                                                      : p.own_o + (at1 + static_cast<int64_t>(i - n0) * p.block_rows) * kDv);
-      },
-      reinterpret_cast<__nv_bfloat16*>(p.out) + static_cast<int64_t>(row) * kDv, p.lse + row);
+  const int elem = blockIdx.y;
+  const int r0 = blockIdx.x * (WARP_ROWS ? 4 : 1);  // first row of the element
+  const int own = elem * p.blocks_per_elem + r0 / p.own.rows;
+  const int64_t row0 = static_cast<int64_t>(elem) * p.rows + r0;
+  const int pre = static_cast<int>(row0 / 128);
+  const int L = p.cache_seqlens[elem], L0 = p.has_prefix ? p.prefix_len[0] : 0;
+  Pieces own_pieces = find_pieces(p.own, own), prefix_pieces{0, 0};
+  if (p.has_prefix) prefix_pieces = find_pieces(p.prefix, pre);
+  // (spans of problems without keys were not written)
+  const int n0 = L0 > 0 ? prefix_pieces.n : 0, n1 = L > 0 ? own_pieces.n : 0;
+  if (n1 < 0) return;  // one part held the problem and wrote its rows
+  const int r = r0 + (WARP_ROWS ? threadIdx.x >> 5 : 0);
+  if (r >= p.rows) return;
+  const int64_t row = static_cast<int64_t>(elem) * p.rows + r;
+  auto at = [&](int i) {
+    const bool in_prefix = i < n0;
+    const MergeSide& m = in_prefix ? p.prefix : p.own;
+    const int slot = in_prefix ? prefix_pieces.at(i) : own_pieces.at(i - n0);
+    const int64_t s = static_cast<int64_t>(slot) * m.rows + (in_prefix ? static_cast<int>(row % 128) : r % m.rows);
+    return PiecePtr{reinterpret_cast<const float4*>(m.o + s * kDv), m.lse + s};
+  };
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + row * kDv;
+  if (WARP_ROWS)
+    merge_row_warp(n0 + n1, at, out, p.lse + row);
+  else
+    merge_row_block(n0 + n1, at, out, p.lse + row);
 }
 
-template <class Params>
-cudaError_t launch_merge(void (*kernel)(const Params), const Params& p, int64_t rows, cudaStream_t stream) {
+}  // namespace
+
+cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
+  // rows enough to fill the chip four to a block, in few pieces each
+  const int64_t rows = static_cast<int64_t>(p.batch) * p.rows;
+  const bool warp_rows = rows >= 2048 && (!p.has_prefix || (p.rows % 4 == 0 && p.own.rows % 4 == 0));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  cfg.gridDim = dim3(static_cast<unsigned>(warp_rows ? (p.rows + 3) / 4 : p.rows), static_cast<unsigned>(p.batch));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -268,17 +332,7 @@ cudaError_t launch_merge(void (*kernel)(const Params), const Params& p, int64_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-}  // namespace
-
-cudaError_t launch_prefix_combine(const PrefixCombineParams& p, cudaStream_t stream) {
-  return launch_merge(prefix_combine_kernel, p, p.total_rows, stream);
-}
-
-cudaError_t launch_window_combine(const CombineParams& p, cudaStream_t stream) {
-  return launch_merge(window_combine_kernel, p, static_cast<int64_t>(p.num_problems) * p.rows, stream);
+  return warp_rows ? cudaLaunchKernelEx(&cfg, merge_kernel<true>, p) : cudaLaunchKernelEx(&cfg, merge_kernel<false>, p);
 }
 
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool pdl) {

@@ -52,6 +52,7 @@
 // with a bounded wait, and TMEM is freed.
 #include "mla_device.cuh"
 #include "mla_internal.h"
+#include "mla_schedule.cuh"
 
 namespace mla {
 
@@ -179,6 +180,7 @@ struct Cfg {
   static constexpr int kFullArrivals = kGather ? (kItemFull ? 2 : 4) : 1;
   static_assert(kPBytes <= kKvChunkBytes || !kPAlias, "P must fit in the RoPE chunk");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(schedule_scratch(kMaxProblems) <= kAuxOff, "a schedule is made where the rings will be");
   static_assert(R == 16 || R == 32 || R == 64, "rows per CTA");
   static_assert((kAuxOff + kBarBytes) % 16 == 0, "row statistics must be 16-byte aligned");
   static_assert(kTileTokens == kPageSize, "one KV tile is one page");
@@ -1011,8 +1013,8 @@ __device__ __forceinline__ void half_reduce_scatter(const float (&v)[N], float* 
 }
 
 template <int R, int MODE>
-__device__ void softmax_epilogue(const DecodeParams& p, const Segments<Cfg<R, MODE>::kWindow>& sg, int g, int split0, uint32_t tmem,
-                                 uint8_t* kv, const Bars& bars, float* aux, volatile uint8_t* flags,
+__device__ void softmax_epilogue(const DecodeParams& p, const Segments<Cfg<R, MODE>::kWindow>& sg, int g, int part, int split0,
+                                 uint32_t tmem, uint8_t* kv, const Bars& bars, float* aux, volatile uint8_t* flags,
                                  const Watchdog& wd) {
   using C = Cfg<R, MODE>;
   constexpr int RW = R / C::kSmWG;  // rows owned by this warpgroup
@@ -1268,9 +1270,17 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments<Cfg<R, MO
     }
     gsync();
     // partial-result slots of this problem: none when this piece is the whole problem
-    const int nsplit = p.num_splits[prob + 1] - p.num_splits[prob];
-    const bool final_out = nsplit <= 1 && !p.always_partial;
-    int slot = p.num_splits[prob] + (prob == sg.p0 ? split0 : 0);
+    // (windowed: slots by part, see mla_schedule.cuh)
+    bool final_out;
+    int slot;
+    if (C::kWindow) {
+      const bool whole = tb == 0 && te == walk.pages;
+      final_out = whole && !p.always_partial;
+      slot = piece_slot(whole, prob, 2 * p.num_parts, part, prob == sg.p0);
+    } else {
+      final_out = p.num_splits[prob + 1] - p.num_splits[prob] <= 1;
+      slot = p.num_splits[prob] + (prob == sg.p0 ? split0 : 0);
+    }
     const int row0 = g * R + rb;
     bool write_ok = true;
     if (!final_out && (slot < 0 || slot >= p.max_slots)) {
@@ -1409,6 +1419,13 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
 #endif
   Segments<C::kWindow> sg;
   int split0 = 0;
+  if (C::kWindow) {
+    const PartRecord r = inline_schedule(p, part, kTileTokens, smem, g == 0);
+    sg.p0 = r.p0;
+    sg.t0 = r.t0;
+    sg.p1 = r.p1;
+    sg.t1 = r.t1;
+  } else
   // record 0 names the part count and geometry the schedule was made for;
   // only a matching schedule is read further
   if (p.sched[kSchedParts] == p.num_parts && p.sched[kSchedTag] == p.sched_tag) {
@@ -1445,7 +1462,7 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
     }
   } else if (warp < C::kGatherWarp0) {
     if (C::kRegSplit) regs_to<C::kRegsSoftmax, C::kLaunchRegs>();
-    softmax_epilogue<R, MODE>(p, sg, g, split0, tmem, kv, bars, aux, flags, wd);
+    softmax_epilogue<R, MODE>(p, sg, g, part, split0, tmem, kv, bars, aux, flags, wd);
   } else if (C::kGather) {
     if (C::kRegSplit) regs_to<C::kRegsGather, C::kLaunchRegs>();
     gather_rows<R, MODE>(&tm_kv, p, sg, kv, bars, flags, wd);

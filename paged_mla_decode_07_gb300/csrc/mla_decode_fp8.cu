@@ -44,6 +44,7 @@
 // block each, 4.5k (issue slots 65 % busy, DRAM 33 %).
 #include "mla_device.cuh"
 #include "mla_internal.h"
+#include "mla_schedule.cuh"
 
 namespace mla {
 namespace {
@@ -82,6 +83,7 @@ constexpr int kBarOff = (kAbortOff + 4 + 15) / 16 * 16;
 constexpr int kNumBars = 2 * kStages + 6;
 constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(schedule_scratch(kMaxProblems) <= kPOff, "a schedule is made where the pages will be");
 constexpr int kThreads = 640;
 constexpr uint32_t kRegsCtl = 24, kRegsScore = 128, kRegsValue = 96, kLaunchRegs = 96;
 // setmaxnreg hands out what the block was launched with and waits for ever for more
@@ -241,7 +243,7 @@ drain:
 // within a sum is free, so lane group c takes dims [32 c, 32 c + 32) of a
 // block, four per instruction: 16-byte reads of consecutive codes.
 template <bool TOKEN_SCALE>
-__device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& p, const Walk& w, int g, int split0,
+__device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& p, const Walk& w, int g, int part,
                        uint8_t* smem, const Bars& bars, const Watchdog& wd) {
   const int lane = threadIdx.x & 31, sw = (threadIdx.x >> 5) - 4;
   const int tg = sw & 3, half = sw >> 2;  // token group, half of the dims (then rows 8 half .. 8 half + 7)
@@ -401,9 +403,9 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
     if (!named_bar_and(kRowsBar + half, 128, ok)) return;
     if (tg == 0) {
       if (c == 0) {
-        const int base_slot = p.num_splits[prob], pieces = p.num_splits[prob + 1] - base_slot;
-        const bool final_out = pieces <= 1 && !p.always_partial;
-        const int slot = base_slot + (prob == w.p0 ? split0 : 0);
+        const bool whole = tb == 0 && te == walk.pages;
+        const bool final_out = whole && !p.always_partial;
+        const int slot = piece_slot(whole, prob, 2 * p.num_parts, part, prob == w.p0);
         const float4 v = lds<float4>(smem + kSumOff + (r + 8 * half) * 16);
         const float sum = (v.x + v.y) + (v.z + v.w);
         sts(smem + kInvOff + (r + 8 * half) * 4, sum == 0.f ? 0.f : 1.f / sum);
@@ -430,7 +432,7 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
 // 16-token step: column r of the instruction for code i is dim 32 g + 4 r + i, so
 // a lane ends with dims 32 g + 8 c .. + 7 of rows r and r + 8: 16-byte stores.
 template <bool TOKEN_SCALE>
-__device__ void values(const DecodeParams& p, const Walk& w, int g, int split0, uint8_t* smem, const Bars& bars,
+__device__ void values(const DecodeParams& p, const Walk& w, int g, int part, uint8_t* smem, const Bars& bars,
                        const Watchdog& wd) {
   const int lane = threadIdx.x & 31, v = (threadIdx.x >> 5) - 12;
   const int r = lane >> 2, c = lane & 3;
@@ -571,9 +573,9 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int split0, 
     const float back = unit > 0.f ? 1.f / unit : 0.f;  // (no scale above 0: O is 0)
     const float i0 = lds<float>(smem + kInvOff + r * 4) * back, i1 = lds<float>(smem + kInvOff + (r + 8) * 4) * back;
     arrive_warp(bars.l_empty);
-    const int base_slot = p.num_splits[prob], pieces = p.num_splits[prob + 1] - base_slot;
-    const bool final_out = pieces <= 1 && !p.always_partial;
-    const int slot = base_slot + (prob == w.p0 ? split0 : 0);
+    const bool piece_whole = tb == 0 && te == walk.pages;
+    const bool final_out = piece_whole && !p.always_partial;
+    const int slot = piece_slot(piece_whole, prob, 2 * p.num_parts, part, prob == w.p0);
     const bool slot_ok = final_out || (slot >= 0 && slot < p.max_slots);
     if (!slot_ok && lane == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
 #pragma unroll
@@ -632,31 +634,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   Watchdog wd{abort_flag, p.status, p.timeout_ns};
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Walk w{0, 0, 0, 0, p.num_problems};
-  int split0 = 0;
-  if (p.sched[kSchedParts] == p.num_parts && p.sched[kSchedTag] == p.sched_tag) {
-    const int32_t* sr = p.sched + static_cast<int64_t>(part) * kSchedInts;
-    w.p0 = sr[kSchedP0];
-    w.t0 = sr[kSchedT0];
-    w.p1 = sr[kSchedP1];
-    w.t1 = sr[kSchedT1];
-    split0 = sr[kSchedSplit0];
-  } else {
-    w.p0 = -1;
-  }
-  if (w.p0 < 0 || w.p0 > w.np || w.p1 < w.p0 || w.p1 > w.np || w.t0 < 0 || w.t1 < 0) {
-    if (threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
-    w.p0 = w.p1 = w.np;  // nothing to do
-  }
+  const PartRecord rec = inline_schedule(p, part, kPageSize, smem, g == 0);
+  const Walk w{rec.p0, rec.t0, rec.p1, rec.t1, p.num_problems};
   if (warp < 4) {
     regs_to<kRegsCtl, kLaunchRegs>();
     if (warp == 0) produce<TOKEN_SCALE>(p, w, smem, bars, wd);
   } else if (warp < 12) {
     regs_to<kRegsScore, kLaunchRegs>();
-    scores<TOKEN_SCALE>(q, p, w, g, split0, smem, bars, wd);
+    scores<TOKEN_SCALE>(q, p, w, g, part, smem, bars, wd);
   } else {
     regs_to<kRegsValue, kLaunchRegs>();
-    values<TOKEN_SCALE>(p, w, g, split0, smem, bars, wd);
+    values<TOKEN_SCALE>(p, w, g, part, smem, bars, wd);
   }
   __syncthreads();
 }

@@ -79,6 +79,7 @@
 //   warps 12-15 (sparse) row lookups, row copies, the own value share
 #include "mla_device.cuh"
 #include "mla_internal.h"
+#include "mla_schedule.cuh"
 
 namespace mla {
 
@@ -1037,8 +1038,8 @@ done:
 // warps 4-11: online softmax and epilogue
 // ---------------------------------------------------------------------------
 template <bool SPARSE, bool ROWS16, int VAR>
-__device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int g, int rank, int split0, uint32_t tmem,
-                             uint32_t smem, uint32_t bars, uint32_t bars_even, float* m_s, float* red,
+__device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int g, int rank, int part, int split0,
+                             uint32_t tmem, uint32_t smem, uint32_t bars, uint32_t bars_even, float* m_s, float* red,
                              const volatile uint32_t* flags, const Watchdog& wd) {
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1290,10 +1291,18 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int 
     named_bar_sync(kPairSmBar, 256);  // red and m_s are reused by the next segment
     const float inv = lt > 0.f ? 1.0f / lt : 0.f;
     const float lse = lt > 0.f ? m_fin + log2f(lt) : kPairNegInf;
-    const int nsplit = p.num_splits[prob + 1] - p.num_splits[prob];
-    const bool final_out = VAR != kPrefixed && nsplit <= 1;
+    // (windowed and prefixed: slots by part, see mla_schedule.cuh)
     const bool own = VAR == kPrefixed && prob >= p.prefix_problems;
-    const int slot = p.num_splits[prob] + (prob == sg.p0 ? split0 : 0) - (own ? p.num_splits[p.prefix_problems] : 0);
+    bool final_out;
+    int slot;
+    if (VAR == kPlain) {
+      final_out = p.num_splits[prob + 1] - p.num_splits[prob] <= 1;
+      slot = p.num_splits[prob] + (prob == sg.p0 ? split0 : 0);
+    } else {
+      const bool whole = tb == 0 && te == sg.tiles(prob);
+      final_out = VAR == kWindowed && whole;
+      slot = piece_slot(whole, own ? prob - p.prefix_problems : prob, 2 * p.num_parts, part, prob == sg.p0);
+    }
     bool write_ok = VAR == kPrefixed ? rank * kPairRows + r < view.rows : grow < p.rows;
     if (!final_out && (slot < 0 || slot >= (own ? p.own_slots : p.max_slots))) {
       write_ok = false;
@@ -1427,7 +1436,14 @@ __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   PairSeg<VAR> sg;
   int split0 = 0;
-  if (p.sched[kSchedParts] == p.num_parts && p.sched[kSchedTag] == p.sched_tag) {
+  if (VAR != kPlain) {
+    static_assert(schedule_scratch(kMaxProblems) <= kPairAuxOff, "a schedule is made where the operands will be");
+    const PartRecord rec = inline_schedule(p, part, kPairTile, base, rank == 0 && g == 0);
+    sg.p0 = rec.p0;
+    sg.t0 = rec.t0;
+    sg.p1 = rec.p1;
+    sg.t1 = rec.t1;
+  } else if (p.sched[kSchedParts] == p.num_parts && p.sched[kSchedTag] == p.sched_tag) {
     const int32_t* sr = p.sched + static_cast<int64_t>(part) * kSchedInts;
     sg.p0 = sr[kSchedP0];
     sg.t0 = sr[kSchedT0];
@@ -1481,7 +1497,7 @@ __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
     }
   } else if (warp < kPairGatherWarp0) {
     regs_to<C::kRegsSm, C::kLaunchRegs>();
-    pair_softmax<SPARSE, ROWS16, VAR>(p, sg, g, rank, split0, tmem, smem, bars, bars_even, m_s, red, flags, wd);
+    pair_softmax<SPARSE, ROWS16, VAR>(p, sg, g, rank, part, split0, tmem, smem, bars, bars_even, m_s, red, flags, wd);
     // the odd CTA's signal copies are complete before the pair's final sync
     if (rank == 1 && (threadIdx.x & 31) == 0) bulk_wait_all();
   } else if constexpr (SPARSE) {

@@ -126,6 +126,9 @@ struct DecodeParams {
 
   int window, sinks;          // windowed modes: keys before a query token it sees, first keys that stay visible
   int always_partial;         // every piece writes a partial result, the only piece of a problem too
+  // windowed and shared-prefix decode make their schedules themselves (mla_schedule.cuh)
+  int tile_cost, overhead;    // schedule costs
+  int32_t* spans;             // [2 * problems] slot of the first piece, part of the last one
 
   // shared-prefix decode on CTA pairs: problems [0, prefix_problems) are the
   // prefix under 128 consecutive query rows each, the rest the own keys of
@@ -135,36 +138,41 @@ struct DecodeParams {
   int prefix_pages, prefix_problems, blocks_per_elem, total_rows;
   float* own_o;                 // partials of the own keys: [own_slots, block_rows, 512], [own_slots, block_rows]
   float* own_lse;
-  int block_rows, own_slots;
+  int block_rows, own_slots;    // (max_slots: the prefix's)
 
   float scale_log2;           // sm_scale * log2(e)
 };
 
-// What the schedule kernel needs to know of the problems.
+// What a schedule needs to know of the problems of windowed and shared-prefix decode.
 struct SchedSpec {
   const int32_t* seqlens;     // [batch]
-  int s_q, topk;
+  int s_q;
   int window, sinks;          // window > 0: windowed problems
   const int32_t* prefix_len;  // shared-prefix decode (see DecodeParams), else NULL
   int prefix_problems, blocks_per_elem;
-  int always_partial;         // a problem in one piece takes a partial-result slot too
 };
 
-// Merge of the partials of shared-prefix decode: row b * rows + r has pieces
-// of the prefix under its block of 128 rows and pieces of its element's own keys.
-struct PrefixCombineParams {
-  const int32_t* prefix_splits;  // [prefix_problems + 1] slot prefix sums
-  const float* prefix_o;         // [slots, 128, 512]
-  const float* prefix_lse;       // [slots, 128]
-  const int32_t* own_splits;     // [batch * blocks_per_elem + 1]
-  const float* own_o;            // [slots, block_rows, 512]
-  const float* own_lse;          // [slots, block_rows]
-  int block_rows, blocks_per_elem;
-  int rows, total_rows;          // query rows per element, of all elements
-  int prefix_slots, own_slots;   // slots the two arrays hold
+// One kind of problems of a merge: where its pieces are and their partials.
+struct MergeSide {
+  const int32_t* spans;       // [2 * problems of this kind]
+  const float* o;             // [slots, rows, 512]
+  const float* lse;           // [slots, rows]
+  int rows;                   // rows per slot
+  int whole_base;             // slots before those of problems held whole; -1: these write the output themselves
+};
+
+// Merge of the partials of windowed decode (`own` alone) and of shared-prefix
+// decode: row b * rows + r has pieces of the prefix under its block of 128
+// rows and pieces of its element's keys.
+struct MergeParams {
+  MergeSide own, prefix;
+  const int32_t* cache_seqlens;  // [batch] own keys
+  const int32_t* prefix_len;     // [1]
+  int has_prefix;
+  int blocks_per_elem;        // own problems per element
+  int rows, batch;            // query rows per element
   void* out;
   float* lse;
-  uint32_t* status;
 };
 
 struct CombineParams {
@@ -228,8 +236,6 @@ cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, con
                             int32_t* num_splits, cudaStream_t stream);
 // FP8 rows at 16 query rows per CTA (mla_decode_fp8.cu); window = 0: all keys
 cudaError_t launch_decode_fp8(const void* q, const DecodeParams& p, cudaStream_t stream);
-cudaError_t launch_schedule(const SchedSpec& spec, const Geometry& g, int32_t* sched, int32_t* num_splits,
-                            cudaStream_t stream);
 // mode: 0 dense bf16 cache, 1 sparse FP8 cache, 2 dense FP8 cache, 3 sparse bf16 rows, 4 and 5 windowed dense
 // over the bf16 and the FP8 cache
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const DecodeParams& p, int rpc,
@@ -254,8 +260,7 @@ cudaError_t launch_prefix_rows(const uint8_t* kvcache, const float* kv_scales, c
                                const int32_t* prefix_len, int prefix_pages, int num_pages, void* rows, int32_t* table,
                                uint32_t* status, int sm_count, cudaStream_t stream);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool pdl);
-cudaError_t launch_window_combine(const CombineParams& p, cudaStream_t stream);
-cudaError_t launch_prefix_combine(const PrefixCombineParams& p, cudaStream_t stream);
+cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
 size_t decode_smem_bytes(int rpc, int mode);
 cudaError_t launch_fp8_cache_store(const uint16_t* x, int num_tokens, const int32_t* row_offsets,
                                    const int32_t* cache_lengths, int batch, const int32_t* block_table,

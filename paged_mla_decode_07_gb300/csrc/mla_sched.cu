@@ -110,21 +110,8 @@ __device__ void block_inclusive_scan(T* v, int n, T* warp_tot) {
   __syncthreads();
 }
 
-// Tiles of problem p.
-__device__ __forceinline__ int spec_tiles(const SchedSpec& sp, int p, int tile_tokens) {
-  if (sp.prefix_len) {
-    const int L = p < sp.prefix_problems ? sp.prefix_len[0] : sp.seqlens[(p - sp.prefix_problems) / sp.blocks_per_elem];
-    return L > 0 ? (L + tile_tokens - 1) / tile_tokens : 0;
-  }
-  if (sp.window > 0) {
-    const int per = tile_tokens / kPageSize;
-    return (key_walk(sp.seqlens[p], sp.s_q, sp.window, sp.sinks).pages + per - 1) / per;
-  }
-  return problem_tiles(sp.seqlens, p, sp.s_q, sp.topk, tile_tokens);
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
-    metadata_kernel(const SchedSpec spec, int np, int num_parts,
+    metadata_kernel(const int32_t* __restrict__ cache_seqlens, int np, int s_q, int topk, int num_parts,
                     int tile_tokens, int tile_cost, int overhead, int tag, int32_t* __restrict__ sched,
                     int32_t* __restrict__ num_splits) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -141,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // 1. problem tiles (one read of cache_seqlens), costs and their prefix sums
   for (int p = tid; p < np; p += kThreads) {
-    const int n = spec_tiles(spec, p, tile_tokens);
+    const int n = problem_tiles(cache_seqlens, p, s_q, topk, tile_tokens);
     tiles[p] = n;
     pre[p + 1] = n > 0 ? static_cast<long long>(n) * tile_cost + overhead : 0;
   }
@@ -180,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int k1 = part_of(starts, num_parts, Pos{p, n - 1});
       pieces = ne_pre[k1 + 1] - ne_pre[k0];
     }
-    cnt[p] = pieces > 1 || spec.always_partial ? pieces : 0;
+    cnt[p] = pieces > 1 ? pieces : 0;
   }
   __syncthreads();
   block_inclusive_scan(cnt, np, warp_tot);
@@ -213,21 +200,12 @@ size_t metadata_smem_bytes(int np, int num_parts) {
 
 cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, const Geometry& g, int32_t* sched,
                             int32_t* num_splits, cudaStream_t stream) {
-  SchedSpec spec = {};
-  spec.seqlens = cache_seqlens;
-  spec.s_q = s_q;
-  spec.topk = topk;
-  return launch_schedule(spec, g, sched, num_splits, stream);
-}
-
-cudaError_t launch_schedule(const SchedSpec& spec, const Geometry& g, int32_t* sched, int32_t* num_splits,
-                            cudaStream_t stream) {
   size_t smem = metadata_smem_bytes(g.num_problems, g.num_parts);
   cudaError_t e = cudaFuncSetAttribute(metadata_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  metadata_kernel<<<1, kThreads, smem, stream>>>(spec, g.num_problems, g.num_parts, g.tile_tokens,
-                                                 g.tile_cost, g.overhead, g.tag, sched, num_splits);
+  metadata_kernel<<<1, kThreads, smem, stream>>>(cache_seqlens, g.num_problems, s_q, topk, g.num_parts,
+                                                 g.tile_tokens, g.tile_cost, g.overhead, g.tag, sched, num_splits);
   return cudaGetLastError();
 }
 

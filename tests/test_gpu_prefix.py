@@ -69,9 +69,11 @@ def test_forced_splits(fmt, parts):
 
 
 @pytest.mark.parametrize("fmt,h_q", [("bf16", 16), ("bf16", 128), ("fp8", 16), ("fp8_token", 64)])
-def test_many_elements(fmt, h_q):
-    own = [(i * 37) % 190 for i in range(150)]
-    case = problem(fmt, h_q, 1, 1111, own, True, seed=8)
+@pytest.mark.parametrize("n,prefix", [(150, 1111), (1200, 100)])
+def test_many_elements(fmt, h_q, n, prefix):
+    # several problems per thread of the schedule that every CTA makes
+    own = [(i * 37) % 190 for i in range(n)]
+    case = problem(fmt, h_q, 1, prefix, own, True, seed=8)
     check(*run(*case[:7], True), case[7], f"{fmt} {h_q}")
 
 

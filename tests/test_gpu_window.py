@@ -77,9 +77,11 @@ def test_forced_splits(fmt, h_q, parts):
 
 
 @pytest.mark.parametrize("fmt,h_q", [("bf16", 16), ("bf16", 128), ("fp8", 16), ("fp8_token", 128)])
-def test_many_elements(fmt, h_q):
+@pytest.mark.parametrize("n,longest", [(330, 900), (255, 200), (256, 200), (257, 200), (2500, 100)])
+def test_many_elements(fmt, h_q, n, longest):
+    # several problems per thread of the schedule that every CTA makes
     rng = np.random.default_rng(3)
-    lens = [int(x) for x in rng.integers(0, 900, 330)]
+    lens = [int(x) for x in rng.integers(0, longest, n)]
     q, kv, sc, bt, L, want = problem(fmt, h_q, 1, lens, 200, 4, seed=5)
     check(*run(q, kv, sc, bt, L, 200, 4), want, f"{fmt} {h_q}")
 
