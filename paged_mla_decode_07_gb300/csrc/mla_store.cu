@@ -145,10 +145,40 @@ __device__ __forceinline__ int slot_of(const SlotStoreParams& p, int r, bool fla
   return s < 0 ? -1 : s;
 }
 
-// One token with a single scale over its 512 latent values: 512 codes and 64
-// RoPE values at dst, the scale at *scale_out.
-__device__ __forceinline__ void store_row_token_scale(uint8_t* dst, float* scale_out, const uint4 a, const uint4 c,
-                                                      const uint4 rp, int lane) {
+// Codes of 16 values at one scale, E4M3 of the correctly rounded x / scale.
+// With r = RN(1 / scale), q0 = RN(x r) is within two units of the last place,
+// one step q + r (x - q scale) brings it within one and a second one gives the
+// correctly rounded quotient (Markstein 1990, theorem on division with a
+// correctly rounded reciprocal): five instructions per value where the divide
+// takes about ten, which bounds this kernel.  Remainders are exact while
+// x 2^-48 is above the subnormals, for every x whose code is not 0 while
+// scale >= 2^-90; scales outside [2^-90, 2^120] (infinities and NaN among
+// them) divide.
+__device__ __forceinline__ uint4 quantise16(const float (&v)[16], float scale) {
+  float y[16];
+  if (scale >= 8.077935669463161e-28f && scale <= 1.329227995784916e36f) {
+    const float r = __frcp_rn(scale);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float q = v[i] * r;
+      q = fmaf(fmaf(-q, scale, v[i]), r, q);
+      y[i] = fmaf(fmaf(-q, scale, v[i]), r, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(v[i], scale);
+  }
+  uint32_t code[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) code[i] = e4m3x2(y[4 * i], y[4 * i + 1]) | (e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
+  return make_uint4(code[0], code[1], code[2], code[3]);
+}
+
+// One token into its row: codes, RoPE values, and the scale of each 128
+// values in the row or of all 512 at *scale_out.
+template <bool TOKEN_SCALE>
+__device__ __forceinline__ void store_slot_row(uint8_t* dst, float* scale_out, const uint4 a, const uint4 c,
+                                               const uint4 rp, int lane) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
   float v[16];
 #pragma unroll
@@ -160,16 +190,15 @@ __device__ __forceinline__ void store_row_token_scale(uint8_t* dst, float* scale
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int o = TOKEN_SCALE ? 16 : 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float scale = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-  uint32_t code[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    code[i] = e4m3x2(__fdiv_rn(v[4 * i], scale), __fdiv_rn(v[4 * i + 1], scale)) |
-              (e4m3x2(__fdiv_rn(v[4 * i + 2], scale), __fdiv_rn(v[4 * i + 3], scale)) << 16);
-  *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(code[0], code[1], code[2], code[3]);
-  if (lane < 8) *reinterpret_cast<uint4*>(dst + kDv + 16 * lane) = rp;
-  if (lane == 0) *scale_out = scale;
+  *reinterpret_cast<uint4*>(dst + 16 * lane) = quantise16(v, scale);
+  if (TOKEN_SCALE) {
+    if (lane == 0) *scale_out = scale;
+  } else if ((lane & 7) == 0) {
+    *reinterpret_cast<float*>(dst + kFp8ScaleOffset + (lane >> 1)) = scale;
+  }
+  if (lane < 8) *reinterpret_cast<uint4*>(dst + (TOKEN_SCALE ? kDv : kFp8RopeOffset) + 16 * lane) = rp;
 }
 
 // FP8 rows, one warp per token at a time, the next token's values loaded
@@ -180,67 +209,60 @@ __global__ void __launch_bounds__(kStoreWarps * 32) slot_store_fp8_kernel(const 
   const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * kStoreWarps;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  auto load = [&](int r, uint4& a, uint4& c, uint4& rp) {
+  uint4 a = zero, c = zero, rp = zero;
+  int slot = -1;
+  auto load = [&](int64_t r) {
+    slot = slot_of(p, static_cast<int>(r), lane == 0);
     const uint16_t* s = p.latent + r * p.latent_stride + 16 * lane;
     a = ld_global_nc_v4(s);
     c = ld_global_nc_v4(s + 8);
-    rp = lane < 8 ? ld_global_nc_v4(p.rope + r * p.rope_stride + 8 * lane) : zero;
+    if (lane < 8) rp = ld_global_nc_v4(p.rope + r * p.rope_stride + 8 * lane);
   };
-  int64_t r = blockIdx.x * kStoreWarps + (threadIdx.x >> 5);
-  if (r >= p.num_tokens) return;
-  uint4 a, c, rp;
-  int slot = slot_of(p, static_cast<int>(r), lane == 0);
-  load(static_cast<int>(r), a, c, rp);
-  while (true) {
-    const int64_t rn = r + warps;
-    uint4 an = zero, cn = zero, rpn = zero;
-    int slot_n = -1;
-    if (rn < p.num_tokens) {
-      slot_n = slot_of(p, static_cast<int>(rn), lane == 0);
-      load(static_cast<int>(rn), an, cn, rpn);
-    }
-    if (slot >= 0) {
-      uint8_t* dst = p.kvcache + static_cast<int64_t>(slot) * kRow;
-      if (TOKEN_SCALE)
-        store_row_token_scale(dst, p.kv_scales + slot, a, c, rp, lane);
-      else
-        store_row(dst, a, c, rp, lane);
-    }
-    if (rn >= p.num_tokens) return;
-    r = rn;
-    slot = slot_n;
-    a = an;
-    c = cn;
-    rp = rpn;
+  int64_t r = static_cast<int64_t>(blockIdx.x) * kStoreWarps + (threadIdx.x >> 5);
+  if (r < p.num_tokens) load(r);
+#pragma unroll 1
+  while (r < p.num_tokens) {
+    const uint4 a0 = a, c0 = c, rp0 = rp;
+    const int slot0 = slot;
+    r += warps;
+    if (r < p.num_tokens) load(r);
+    if (slot0 >= 0)
+      store_slot_row<TOKEN_SCALE>(p.kvcache + static_cast<int64_t>(slot0) * kRow,
+                                  TOKEN_SCALE ? p.kv_scales + slot0 : nullptr, a0, c0, rp0, lane);
   }
 }
 
-// bf16 rows: 72 16-byte units per token, copied as they are.
-constexpr int kRowUnits = kDqk / 8;
-constexpr int kUnitsInFlight = 4;
-
+// bf16 rows, copied as they are: a warp takes T consecutive tokens at a time,
+// all loads issued before the first store.  Long stores run at the copy's pace
+// only if neighbouring rows are in flight together (65535 tokens alone, the
+// 151 MB take 26.5 us at T = 4, 28.7 at T = 1 and 39 with the 16-byte units of
+// all rows dealt out grid-wide; a plain copy of as many bytes takes 24.7).
+template <int T>
 __global__ void __launch_bounds__(kStoreWarps * 32) slot_store_bf16_kernel(const SlotStoreParams p) {
-  const int64_t units = static_cast<int64_t>(p.num_tokens) * kRowUnits;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreWarps * 32;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kStoreWarps * 32 + threadIdx.x; i0 < units;
-       i0 += step * kUnitsInFlight) {
-    uint4 v[kUnitsInFlight];
-    uint8_t* dst[kUnitsInFlight];
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreWarps * T;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kStoreWarps + (threadIdx.x >> 5)) * T; t0 < p.num_tokens;
+       t0 += step) {
+    uint4 a[T], c[T], rp[T];
+    int slot[T];
 #pragma unroll
-    for (int k = 0; k < kUnitsInFlight; ++k) {
-      const int64_t i = i0 + k * step;
-      dst[k] = nullptr;
-      if (i < units) {
-        const int r = static_cast<int>(i / kRowUnits), u = static_cast<int>(i % kRowUnits);
-        const int slot = slot_of(p, r, u == 0);
-        if (slot >= 0) dst[k] = p.kvcache + static_cast<int64_t>(slot) * (2 * kDqk) + 16 * u;
-        v[k] = ld_global_nc_v4(u < kDv / 8 ? p.latent + r * p.latent_stride + 8 * u
-                                           : p.rope + r * p.rope_stride + 8 * (u - kDv / 8));
-      }
+    for (int k = 0; k < T; ++k) {
+      slot[k] = -1;
+      if (t0 + k >= p.num_tokens) continue;
+      slot[k] = slot_of(p, static_cast<int>(t0) + k, lane == 0);
+      const uint16_t* s = p.latent + (t0 + k) * p.latent_stride + 8 * lane;
+      a[k] = ld_global_nc_v4(s);
+      c[k] = ld_global_nc_v4(s + 256);
+      if (lane < 8) rp[k] = ld_global_nc_v4(p.rope + (t0 + k) * p.rope_stride + 8 * lane);
     }
 #pragma unroll
-    for (int k = 0; k < kUnitsInFlight; ++k)
-      if (dst[k]) *reinterpret_cast<uint4*>(dst[k]) = v[k];
+    for (int k = 0; k < T; ++k) {
+      if (slot[k] < 0) continue;
+      uint4* dst = reinterpret_cast<uint4*>(p.kvcache + static_cast<int64_t>(slot[k]) * (2 * kDqk));
+      dst[lane] = a[k];
+      dst[32 + lane] = c[k];
+      if (lane < 8) dst[64 + lane] = rp[k];
+    }
   }
 }
 
@@ -250,16 +272,19 @@ cudaError_t launch_slot_store(const SlotStoreParams& p, int sm_count, cudaStream
   if (p.num_tokens == 0) return cudaSuccess;
   const int64_t max_grid = sm_count * 8;
   const int threads = kStoreWarps * 32;
-  if (p.is_fp8) {
-    const int64_t need = (static_cast<int64_t>(p.num_tokens) + kStoreWarps - 1) / kStoreWarps;
-    const unsigned grid = static_cast<unsigned>(need < max_grid ? need : max_grid);
-    if (p.kv_scales)
-      slot_store_fp8_kernel<true><<<grid, threads, 0, stream>>>(p);
-    else
-      slot_store_fp8_kernel<false><<<grid, threads, 0, stream>>>(p);
+  // one token per warp until every warp of a full grid has one
+  const bool four = !p.is_fp8 && p.num_tokens > max_grid * kStoreWarps;
+  const int per_block = kStoreWarps * (four ? 4 : 1);
+  const int64_t need = (static_cast<int64_t>(p.num_tokens) + per_block - 1) / per_block;
+  const unsigned grid = static_cast<unsigned>(need < max_grid ? need : max_grid);
+  if (p.is_fp8 && p.kv_scales) {
+    slot_store_fp8_kernel<true><<<grid, threads, 0, stream>>>(p);
+  } else if (p.is_fp8) {
+    slot_store_fp8_kernel<false><<<grid, threads, 0, stream>>>(p);
+  } else if (four) {
+    slot_store_bf16_kernel<4><<<grid, threads, 0, stream>>>(p);
   } else {
-    const int64_t need = (static_cast<int64_t>(p.num_tokens) * kRowUnits + threads - 1) / threads;
-    slot_store_bf16_kernel<<<static_cast<unsigned>(need < max_grid ? need : max_grid), threads, 0, stream>>>(p);
+    slot_store_bf16_kernel<1><<<grid, threads, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }

@@ -254,6 +254,20 @@ def test_cache_store_skips_padding_and_flags_slots_past_the_cache(fmt):
     run_store(latent, rope, slots, 2, fmt, flags=mla.DEVICE_BAD_PAGE)
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp8_token"])
+@pytest.mark.parametrize("power", [-133, -126, -110, -98, -97, -90, -82, -81, -60, 60, 110, 126])
+def test_cache_store_at_the_ends_of_the_range(fmt, power):
+    # scales around the limits between which the quotients are refined from a reciprocal
+    rng = np.random.default_rng(power + 200)
+    latent, rope, slots = store_case(rng, 40, 2, fmt, 0)
+    g = torch.Generator().manual_seed(power + 300)
+    m = torch.rand(40, 512, generator=g).double() * torch.where(torch.rand(40, 512, generator=g) < 0.5, -1.0, 1.0)
+    m[:, ::3] *= 2.0 ** -7
+    m[:, ::5] *= 2.0 ** -14
+    latent.copy_((m * 2.0 ** power).to(torch.bfloat16))
+    run_store(latent, rope, slots, 2, fmt)
+
+
 def test_cache_store_of_no_tokens_is_a_no_op():
     latent, rope, _ = store_case(np.random.default_rng(1), 1, 1, "bf16", 0)
     run_store(latent[:0], rope[:0], np.zeros(0, int), 2, "bf16")
