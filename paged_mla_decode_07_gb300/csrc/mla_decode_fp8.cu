@@ -10,11 +10,12 @@
 //     S[r, t] = Q[r, :] . K[t, :],      K[t, d] = bf16_rn(c[t, d] s_b[t])
 //     O[r, d] = sum_t (P[r, t] s_b[t]) c[t, d]          (d in block b)
 // Keys are dequantised in registers, as the format defines them.  Values are
-// not: their scale joins the probability before it is rounded to fp16 (2^-12
-// where P alone would be rounded to bf16; the rounding of the dequantised
-// value is left out, which moves the result by its half step, 2^-8 of the sum
-// of |values|, at most) and the codes are exact in fp16.  P s is kept in
-// fp16's range by a power of two per value block that follows the scales.
+// not: their scale joins the probability before it is rounded to bf16 and the
+// codes are exact in bf16.  The product keeps one of the two roundings that a
+// dequantised value and a rounded P would have.  bf16 and not fp16, although
+// fp16 would round less: tokens' scales may lie many orders apart (an all-zero
+// tile is stored with scale 1, its neighbours with 1e-6), and P s of the small
+// ones has to keep its bits.
 //
 // At 16 rows the legacy matrix instructions (8 cycles for 16 x 8 x 16 per SM
 // quarter, measured) need 544 instructions per page, 1.1k cycles, so the
@@ -35,11 +36,11 @@
 // Score and value warps work on different pages at the same time; P (fp32)
 // passes between them through a double buffer.
 //
-// Measured: 128 elements x 4160 keys, 137 us (2.4 TB/s, 35 % of the copy
-// rate; the tcgen05 kernel 175 us): 4.4k cycles per page.  Bound by
-// instruction issue: ~3.1k warp instructions per page and SM quarter, of
+// Measured: 128 elements x 4160 keys, 133 us (2.5 TB/s, 36 % of the copy
+// rate; the tcgen05 kernel 175 us): 4.3k cycles per page.  Bound by
+// instruction issue: ~3k warp instructions per page and SM quarter, of
 // which two codes cost 6-8 on the score side (9 cycles of the conversion and
-// arithmetic pipes, measured alone) and 2.5 on the value side.  Tried: four
+// arithmetic pipes, measured alone) and 3 on the value side.  Tried: four
 // score warps over whole rows, 5.7k cycles per page (latency); sixteen over one
 // block each, 4.5k (issue slots 65 % busy, DRAM 33 %).
 #include "mla_device.cuh"
@@ -99,16 +100,20 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// Code i of two tokens' words -> two bf16, each 2^-120 times its value: the
+// code's sign, exponent and mantissa moved to bf16's places (its subnormals
+// become bf16's).  prmt puts each code in a half's lower byte and its sign
+// (selector + 8) in all of the upper one, so one shift moves both.  (NaN codes
+// become 480: the scores are NaN for them already.)
+__device__ __forceinline__ uint32_t code_pair(uint32_t w0, uint32_t w1, int i) {
+  uint32_t v;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(v) : "r"(w0), "r"(w1), "r"(i * 0x1111 + 0xc480));
+  return (v << 4) & 0x87f087f0u;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
+// P s <= 2^8 s is held at 2^80 times its value, so O at 2^-40: scales up to
+// 2^39 stay finite and O has all its bits down to 2^-86.
+constexpr float kPScale = 1208925819614629174706176.0f;  // 2^80
+constexpr float kOScale = 1099511627776.0f;              // 2^40
 // Shared-memory reads and writes as plain accesses, which the compiler may
 // reorder between the (volatile) waits and arrivals: the operand reads of the
 // next products then overlap the conversions and products of the last.
@@ -408,7 +413,7 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
         const int slot = piece_slot(whole, prob, 2 * p.num_parts, part, prob == w.p0);
         const float4 v = lds<float4>(smem + kSumOff + (r + 8 * half) * 16);
         const float sum = (v.x + v.y) + (v.z + v.w);
-        sts(smem + kInvOff + (r + 8 * half) * 4, sum == 0.f ? 0.f : 1.f / sum);
+        sts(smem + kInvOff + (r + 8 * half) * 4, sum == 0.f ? 0.f : kOScale / sum);
         const float lse = sum == 0.f ? kNegInf : m + log2f(sum);  // (NaN stays NaN)
         if (row < p.rows) {
           if (final_out)
@@ -445,11 +450,6 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
     int tb, te;
     range(w, prob, walk, tb, te);
     if (tb >= te) continue;
-    // O is kept at `unit` times its value, a power of two near the inverse of
-    // the block's scales, raised out of the way when a page's are 2^6 larger:
-    // P s unit is below 2^15 (P <= 2^8) and fp16 holds it to 2^-12 down to
-    // 2^-14 and to 2^-25 in absolute terms below
-    float unit = 0.f;
     float o[2][4][4];  // [32-dim group][code i][row r: dims 8c + i, 8c + 4 + i; row r + 8]
 #pragma unroll
     for (int a = 0; a < 2; ++a)
@@ -464,34 +464,6 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
       const int lp = walk.page(j);
       const bool page_ok = flags[s] != 0;
       const bool whole = page_ok && page_seen_whole(p, lp, L);
-      {
-        // largest scale of the block among the page's tokens that are seen
-        float big = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = lane + 32 * i;
-          const float x = lds<float>(TOKEN_SCALE ? stage + kScaleOff + 4 * t
-                                                 : stage + t * kFp8RowBytes + kFp8ScaleOffset + 4 * blk);
-          if (whole || (page_ok && key_seen(p, lp * kPageSize + t, L))) big = fmaxf(big, x);
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-        if (big > 0.f && !(big * unit <= 64.f && unit > 0.f)) {
-          // 2^-(exponent of big), within fp32's normal range
-          const int e = min(max(254 - static_cast<int>(__float_as_uint(big) >> 23), 1), 253);
-          const float to = __uint_as_float(static_cast<uint32_t>(e) << 23);
-          if (unit > 0.f) {
-            const float f = to / unit;
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[a][i][k] *= f;
-          }
-          unit = to;
-        }
-      }
       if (!wait_warp(bars.p_full + buf, (jt >> 1) & 1, wd)) return;
       const uint8_t* pa = smem + kPOff + buf * kPBytes;
       const float a0 = lds<float>(smem + kAlphaOff + (buf * kRows + r) * 4);
@@ -535,12 +507,12 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
           if (!k8) sh.x = 0.f;
           if (!k9) sh.y = 0.f;
         }
-        sl.x *= unit;
-        sl.y *= unit;
-        sh.x *= unit;
-        sh.y *= unit;
-        const uint32_t a[4] = {pack_f16x2(x[0].x * sl.x, x[0].y * sl.y), pack_f16x2(x[1].x * sl.x, x[1].y * sl.y),
-                               pack_f16x2(x[2].x * sh.x, x[2].y * sh.y), pack_f16x2(x[3].x * sh.x, x[3].y * sh.y)};
+        sl.x *= kPScale;
+        sl.y *= kPScale;
+        sh.x *= kPScale;
+        sh.y *= kPScale;
+        const uint32_t a[4] = {pack_bf16x2(x[0].x * sl.x, x[0].y * sl.y), pack_bf16x2(x[1].x * sl.x, x[1].y * sl.y),
+                               pack_bf16x2(x[2].x * sh.x, x[2].y * sh.y), pack_bf16x2(x[3].x * sh.x, x[3].y * sh.y)};
         constexpr int kRow = Rows<TOKEN_SCALE>::kRow;
         const uint8_t* codes = stage + t * kRow + 64 * v + 4 * r;
 #pragma unroll
@@ -554,12 +526,7 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
             if (!k9) w9 = 0;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // byte i of each pair of tokens, as two fp16 values
-            const uint32_t sel = i | ((4 + i) << 4);
-            mma_f16(o[d][i], a, e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(w0, w1, sel))),
-                    e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(w8, w9, sel))));
-          }
+          for (int i = 0; i < 4; ++i) mma_bf16(o[d][i], a, code_pair(w0, w1, i), code_pair(w8, w9, i));
         }
       }
       __syncwarp();
@@ -570,8 +537,7 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
     }
 
     if (!wait_warp(bars.l_full, seg & 1, wd)) return;
-    const float back = unit > 0.f ? 1.f / unit : 0.f;  // (no scale above 0: O is 0)
-    const float i0 = lds<float>(smem + kInvOff + r * 4) * back, i1 = lds<float>(smem + kInvOff + (r + 8) * 4) * back;
+    const float i0 = lds<float>(smem + kInvOff + r * 4), i1 = lds<float>(smem + kInvOff + (r + 8) * 4);
     arrive_warp(bars.l_empty);
     const bool piece_whole = tb == 0 && te == walk.pages;
     const bool final_out = piece_whole && !p.always_partial;

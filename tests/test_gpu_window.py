@@ -16,8 +16,8 @@ def seen(L, s_q, i, window, sinks):
     return [t for t in range(max(0, min(last + 1, L))) if t < sinks or t > last - window]
 
 
-def problem(fmt, h_q, s_q, lens, window, sinks, seed=0, store_all=False):
-    cache = Cache(fmt, seed, sum(-(-L // 64) for L in lens) + 3)
+def problem(fmt, h_q, s_q, lens, window, sinks, seed=0, store_all=False, make=Cache):
+    cache = make(fmt, seed, sum(-(-L // 64) for L in lens) + 3)
     g = torch.Generator("cuda").manual_seed(seed + 1)
     q = torch.randn(len(lens), s_q, h_q, 576, generator=g, device="cuda").to(torch.bfloat16)
     rows, want = [], []
@@ -156,3 +156,44 @@ def test_two_streams_with_their_own_workspaces():
     for x, y in got:
         for g, w in ((x, want[0]), (y, want[1])):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+class FarScales(Cache):
+    """FP8 keys whose scales lie six orders apart: small values, and among them tokens with all-zero
+    tiles, which the format stores with the scale 1."""
+
+    def rows(self, n):
+        x = torch.randn(n, 512, generator=self.g, device="cuda") * 2.0 ** -20
+        x[::5] = 0
+        return self.encode(x, torch.randn(n, 64, generator=self.g, device="cuda"))
+
+    def encode(self, x, rope):
+        n = x.shape[0]
+        rope = rope.to(torch.bfloat16)
+        t = x.reshape(n, 4 if self.fmt == "fp8" else 1, -1)
+        s = t.abs().amax(-1, keepdim=True) / torch.tensor(448.0, device="cuda")
+        s = torch.where(s > 0, s, torch.ones_like(s))
+        codes = (t / s).to(torch.float8_e4m3fn)
+        lat = (codes.float() * s).to(torch.bfloat16).double().reshape(n, 512)
+        parts = [codes.view(torch.uint8).reshape(n, 512)]
+        if self.fmt == "fp8":
+            parts.append(s.reshape(n, 4).contiguous().view(torch.uint8))
+        parts.append(rope.contiguous().view(torch.uint8))
+        return torch.cat([lat, rope.double()], 1), torch.cat(parts, 1), s.reshape(n) if self.fmt == "fp8_token" else None
+
+
+class SmallCodes(FarScales):
+    """FP8 keys whose codes are subnormal but for one per tile."""
+
+    def rows(self, n):
+        x = torch.randn(n, 512, generator=self.g, device="cuda").clamp(-3, 3) * 2.0 ** -9
+        x[:, ::128] = 448.0
+        return self.encode(x * 2.0 ** -10, torch.randn(n, 64, generator=self.g, device="cuda"))
+
+
+@pytest.mark.parametrize("make", [FarScales, SmallCodes])
+@pytest.mark.parametrize("fmt", ["fp8", "fp8_token"])
+@pytest.mark.parametrize("h_q,s_q", [(8, 1), (16, 1), (20, 1), (64, 1), (128, 1), (24, 3)])
+def test_scales_and_codes_far_apart(make, fmt, h_q, s_q):
+    q, kv, sc, bt, lens, want = problem(fmt, h_q, s_q, (5, 64, 300, 777), 200, 20, seed=h_q, make=make)
+    check(*run(q, kv, sc, bt, lens, 200, 20), want, f"{fmt} {h_q}x{s_q} {make.__name__}")
