@@ -302,6 +302,10 @@ void fp8_rows_geometry(Geometry* g) {
   if (g->num_parts < 1) g->num_parts = 1;
 }
 
+// Pages of all problems of a schedule that a call may have: the sums of a
+// schedule made in the decode kernel have 31 bits for them.
+constexpr long long kMaxTilesTotal = 1ll << 28;
+
 // Windowed decode: spans of the problems and split-KV partials.
 struct WindowLayout {
   size_t o_accum, lse_accum, total;  // (the spans come first)
@@ -342,7 +346,7 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   if (is_fp8 && L->own.rows <= kFp8RowsMax) {
     fp8_rows_geometry(&L->own);
   } else if (is_fp8) {
-    // the windowed mode with a window that holds every key
+    // the windowed mode with sinks that are every key
     L->own.mode = 5;
   }
   L->prefix_problems = static_cast<int>((rows + 127) / 128);
@@ -353,6 +357,9 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   if (np > kMaxProblems)
     return fail(MLA_ERR_UNSUPPORTED, "batch*s_q*h_q = %lld query rows make %lld problems, more than the supported %d",
                 rows, np, kMaxProblems);
+  if (static_cast<long long>(L->prefix_problems) * prefix_pages > kMaxTilesTotal)
+    return fail(MLA_ERR_UNSUPPORTED, "batch*s_q*h_q = %lld query rows over a prefix table of %d entries", rows,
+                prefix_pages);
   Geometry& g = L->pre;
   g = L->own;
   g.num_problems = static_cast<int>(np);
@@ -393,7 +400,7 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
 }
 
 // Checks that every dense decode call over a paged cache shares.
-mla_status check_paged(const void* q, const void* kvcache, const int32_t* block_table, const int32_t* cache_seqlens,
+mla_status check_paged(int batch, const void* q, const void* kvcache, const int32_t* block_table, const int32_t* cache_seqlens,
                        const void* out, const float* lse, int num_pages, int page_size, int stride, float sm_scale,
                        int is_fp8, const float* kv_scales) {
   if (!q) return fail(MLA_ERR_INVALID_ARG, "q is NULL");
@@ -406,6 +413,8 @@ mla_status check_paged(const void* q, const void* kvcache, const int32_t* block_
   if (num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages must be >= 1 (got %d)", num_pages);
   if (num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages = %d exceeds 2^31 tokens", num_pages);
   if (stride < 1) return fail(MLA_ERR_INVALID_ARG, "block_table_stride must be >= 1 (got %d)", stride);
+  if (static_cast<long long>(batch) * stride > kMaxTilesTotal)
+    return fail(MLA_ERR_UNSUPPORTED, "a block table of %d x %d entries", batch, stride);
   if (!std::isfinite(sm_scale)) return fail(MLA_ERR_INVALID_ARG, "sm_scale is not finite");
   if (is_fp8 != 0 && is_fp8 != 1) return fail(MLA_ERR_INVALID_ARG, "is_fp8 must be 0 or 1 (got %d)", is_fp8);
   if (kv_scales && !is_fp8) return fail(MLA_ERR_INVALID_ARG, "kv_scales given with a bf16 cache (is_fp8 = 0)");
@@ -888,7 +897,7 @@ mla_status mla_window_decode_workspace_size(int batch, int h_q, int s_q, int is_
 
 mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t stream) {
   if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
-  mla_status st = check_paged(a->q, a->kvcache, a->block_table, a->cache_seqlens, a->out, a->lse, a->num_pages,
+  mla_status st = check_paged(a->batch, a->q, a->kvcache, a->block_table, a->cache_seqlens, a->out, a->lse, a->num_pages,
                               a->page_size, a->block_table_stride, a->sm_scale, a->is_fp8, a->kv_scales);
   if (st != MLA_OK) return st;
   if (a->window < 1) return fail(MLA_ERR_INVALID_ARG, "window must be >= 1 (got %d)", a->window);
@@ -986,7 +995,7 @@ mla_status mla_shared_prefix_decode_workspace_size(int batch, int h_q, int s_q, 
 
 mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_stream_t stream) {
   if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
-  mla_status st = check_paged(a->q, a->kvcache, a->block_table, a->cache_seqlens, a->out, a->lse, a->num_pages,
+  mla_status st = check_paged(a->batch, a->q, a->kvcache, a->block_table, a->cache_seqlens, a->out, a->lse, a->num_pages,
                               a->page_size, a->block_table_stride, a->sm_scale, a->is_fp8, a->kv_scales);
   if (st != MLA_OK) return st;
   if (!a->prefix_table) return fail(MLA_ERR_INVALID_ARG, "prefix_table is NULL");
@@ -1083,7 +1092,8 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
     o.num_parts = L.own.num_parts;
     o.max_slots = L.own_slots;
     o.prefix_len = nullptr;
-    o.window = kMaxWindow;  // every key
+    o.window = 1;
+    o.sinks = 0x7fffffff;  // every key
     o.always_partial = 1;
     o.evict_first = L.own.row_groups == 1 ? 1 : 0;
     o.kv_scales = a->kv_scales;

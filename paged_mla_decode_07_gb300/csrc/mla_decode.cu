@@ -208,9 +208,9 @@ template <bool WINDOW>
 struct Segments {
   int p0, t0, p1, t1, np, s_q, topk;
   const int32_t* seqlens;
-  int window, sinks;  // (WINDOW)
+  int window, sinks, cols;  // (WINDOW; columns of the block table)
   // pages of problem p, in the order its tiles take them
-  __device__ KeyWalk walk(int p) const { return key_walk(seqlens[p], s_q, window, sinks); }
+  __device__ KeyWalk walk(int p) const { return key_walk(seqlens[p], s_q, window, sinks, cols); }
   __device__ int last() const { return p1 < np ? p1 : np - 1; }
   __device__ void range(int p, int& tb, int& te) const {
     int n = WINDOW ? walk(p).pages : problem_tiles(seqlens, p, s_q, topk);
@@ -1445,6 +1445,7 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
   sg.seqlens = p.cache_seqlens;
   sg.window = p.window;
   sg.sinks = p.sinks;
+  sg.cols = p.block_table_stride;
   if (sg.p0 < 0 || sg.p0 > sg.np || sg.p1 < sg.p0 || sg.p1 > sg.np || sg.t0 < 0 || sg.t1 < 0) {
     if (threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
     sg.p0 = sg.np;  // nothing to do

@@ -1,4 +1,4 @@
-// K9 — dense or windowed decode over an FP8 cache, 16 query rows per CTA, on
+// K9 — windowed decode over an FP8 cache, 16 query rows per CTA, on
 // register-level matrix instructions.
 //
 // The same computation as the FP8 modes of the single-CTA kernel
@@ -131,9 +131,7 @@ struct Walk {
   __device__ int last() const { return p1 < np ? p1 : np - 1; }
 };
 __device__ __forceinline__ KeyWalk walk_of(const DecodeParams& p, int L) {
-  if (p.window > 0) return key_walk(L, p.s_q, p.window, p.sinks);
-  const int n = L > 0 ? (L + kPageSize - 1) / kPageSize : 0;
-  return KeyWalk{n, n, 0};
+  return key_walk(L, p.s_q, p.window, p.sinks, p.block_table_stride);
 }
 __device__ __forceinline__ void range(const Walk& w, int prob, const KeyWalk& k, int& tb, int& te) {
   tb = prob == w.p0 ? w.t0 : 0;
@@ -141,12 +139,11 @@ __device__ __forceinline__ void range(const Walk& w, int prob, const KeyWalk& k,
 }
 // Whether some query token of the element sees key t, and whether all keys of a page are seen.
 __device__ __forceinline__ bool key_seen(const DecodeParams& p, int t, int L) {
-  return t < L && (p.window <= 0 || key_in_walk(t, L, p.s_q, p.window, p.sinks));
+  return t < L && key_in_walk(t, L, p.s_q, p.window, p.sinks);
 }
 __device__ __forceinline__ bool page_seen_whole(const DecodeParams& p, int page, int L) {
   const int first = page * kPageSize, last = first + kPageSize - 1;
   if (last >= L) return false;
-  if (p.window <= 0) return true;
   const int past = L - p.s_q - p.window;
   return p.sinks > past || last < p.sinks || first > past;
 }
@@ -288,7 +285,7 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
       }
     }
     const int lim = p.is_causal ? min(L - p.s_q + row / p.h_q, L - 1) : L - 1;
-    const int low = p.window > 0 ? lim - p.window : -1;  // keys up to here are outside the window
+    const int low = lim - p.window;  // keys up to here are outside the window
     float m = kNegInf, l = 0.f;
 
     for (int j = tb; j < te; ++j, ++jt) {
@@ -363,11 +360,11 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
       // mask: page usable, key at or before the row's last one, and among the first keys or in the window
       const int first = walk.page(j) * kPageSize;
       if (!(page_ok && first + kPageSize - 1 <= lim &&
-            (p.window <= 0 || first + kPageSize - 1 < p.sinks || first > low))) {
+            (first + kPageSize - 1 < p.sinks || first > low))) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = first + 16 * tg + 2 * c + 8 * (i >> 1) + (i & 1);
-          if (!(page_ok && t <= lim && (p.window <= 0 || t < p.sinks || t > low))) z[i] = kNegInf;
+          if (!(page_ok && t <= lim && (t < p.sinks || t > low))) z[i] = kNegInf;
         }
       }
       // row maximum: the lane groups of the warp, then the four token groups

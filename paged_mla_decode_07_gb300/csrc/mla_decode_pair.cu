@@ -202,16 +202,17 @@ template <int VAR>
 struct PairSeg {
   int p0, t0, p1, t1, np, s_q, topk;
   const int32_t* seqlens;
+  int cols;                              // of the block table (kWindowed, kPrefixed)
   int window, sinks;                     // (kWindowed)
   const int32_t* prefix_len;             // (kPrefixed)
-  int prefix_problems, blocks_per_elem;  // (kPrefixed)
+  int prefix_pages, prefix_problems, blocks_per_elem;  // (kPrefixed)
   __device__ int last() const { return p1 < np ? p1 : np - 1; }
   __device__ int tiles(int p) const {
-    if (VAR == kWindowed) return (key_walk(seqlens[p], s_q, window, sinks).pages + 1) / 2;
-    if (VAR == kPrefixed) {
-      const int L = p < prefix_problems ? prefix_len[0] : seqlens[(p - prefix_problems) / blocks_per_elem];
-      return L > 0 ? (L + kPairTile - 1) / kPairTile : 0;
-    }
+    if (VAR == kWindowed) return (key_walk(seqlens[p], s_q, window, sinks, cols).pages + 1) / 2;
+    if (VAR == kPrefixed)
+      return ((p < prefix_problems ? pages_of(prefix_len[0], prefix_pages)
+                                   : pages_of(seqlens[(p - prefix_problems) / blocks_per_elem], cols)) +
+              1) / 2;
     return problem_tiles(seqlens, p, s_q, topk, kPairTile);
   }
   __device__ void range(int p, int& tb, int& te) const {
@@ -226,7 +227,7 @@ struct PairSeg {
 template <int VAR>
 struct PairView {
   int L;                 // keys
-  const int32_t* table;  // page ids by logical page; NULL: page i is page i of the map
+  const int32_t* table;  // page ids by logical page
   int table_len;
   int64_t row0;          // query row (of the whole call) of the row group's first row
   int rows;              // rows of the row group from there on that exist (may exceed 128)
@@ -263,13 +264,14 @@ struct PairView {
       row0 = static_cast<int64_t>(prob) * p.rows + in_elem;
       rows = p.rows - in_elem;
       causal = p.is_causal != 0;
-      if (VAR == kWindowed) walk = key_walk(L, sg.s_q, sg.window, sg.sinks);
+      if (VAR == kWindowed) walk = key_walk(L, sg.s_q, sg.window, sg.sinks, sg.cols);
     }
   }
   // logical page of half h (0, 1) of tile j; -1 past the last one
   __device__ __forceinline__ int logical(int j, int h) const {
     const int i = 2 * j + h;
     if (VAR == kWindowed) return i < walk.pages ? walk.page(i) : -1;
+    if (VAR == kPrefixed) return i <= (L - 1) / kPageSize ? i : -1;
     return i * kPageSize < L ? i : -1;
   }
   // Its page id, or -1 when it holds no cached token or its block-table
@@ -277,7 +279,7 @@ struct PairView {
   __device__ __forceinline__ int page(const DecodeParams& p, int j, int h, bool flag) const {
     const int pi = logical(j, h);
     if (pi < 0) return -1;
-    const int pg = pi < table_len ? (VAR == kPrefixed && !table ? pi : table[pi]) : -1;
+    const int pg = pi < table_len ? table[pi] : -1;
     if (pg < 0 || pg >= p.num_pages) {
       if (flag) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
       return -1;
@@ -1458,9 +1460,11 @@ __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
   sg.s_q = p.s_q;
   sg.topk = SPARSE ? p.topk : 0;
   sg.seqlens = p.cache_seqlens;
+  sg.cols = p.block_table_stride;
   sg.window = p.window;
   sg.sinks = p.sinks;
   sg.prefix_len = p.prefix_len;
+  sg.prefix_pages = p.prefix_pages;
   sg.prefix_problems = p.prefix_problems;
   sg.blocks_per_elem = p.blocks_per_elem;
   if (sg.p0 < 0 || sg.p0 > sg.np || sg.p1 < sg.p0 || sg.p1 > sg.np || sg.t0 < 0 || sg.t1 < 0) {

@@ -54,20 +54,29 @@ __host__ __device__ inline int problem_tiles(const int32_t* cache_seqlens, int p
 // and sees the first `sinks` keys and the last `window` up to its own, so all
 // query tokens together see [0, sinks) and [L - s_q - window + 1, L): the
 // first `head` pages, then those from page head + skip on (one run when the
-// two touch).  Page i of the walk is page i, or i + skip from `head` on.
+// two touch).  Page i of the walk is page i, or i + skip from `head` on.  Of
+// the pages past the `cols` columns of the block table a walk has one, whose
+// lookup reports them: a length says nothing about the memory behind it.
 struct KeyWalk {
   int pages, head, skip;
   __host__ __device__ int page(int i) const { return i < head ? i : i + skip; }
 };
-__host__ __device__ inline KeyWalk key_walk(int L, int s_q, int window, int sinks) {
+// Pages of L keys, at most one past the table.
+__host__ __device__ inline int pages_of(int L, int cols) {
+  if (L <= 0) return 0;
+  const int n = (L - 1) / kPageSize + 1;
+  return n <= cols ? n : cols + 1;
+}
+__host__ __device__ inline KeyWalk key_walk(int L, int s_q, int window, int sinks, int cols) {
   if (L <= 0) return KeyWalk{0, 0, 0};
-  const int total = (L + kPageSize - 1) / kPageSize;
-  const int kept = sinks < L ? sinks : L;
-  const int first = L - s_q - window + 1;  // >= -2^31: window is at most 2^30, s_q at most 1024
-  const int head = (kept + kPageSize - 1) / kPageSize;
-  if (first <= 0 || first / kPageSize <= head) return KeyWalk{total, total, 0};
-  const int w0 = first / kPageSize;
-  return KeyWalk{head + total - w0, head, w0 - head};
+  const int first = L - s_q - window + 1;  // > -2^31: window is at most 2^30, s_q at most 1024
+  const int head = pages_of(sinks < L ? sinks : L, cols), w0 = first / kPageSize;
+  if (first <= 0 || w0 <= head || head > cols) {
+    const int n = pages_of(L, cols);
+    return KeyWalk{n, n, 0};
+  }
+  const int total = (L - 1) / kPageSize + 1, end = (w0 > cols ? w0 : cols) + 1;
+  return KeyWalk{head + (total < end ? total : end) - w0, head, w0 - head};
 }
 // Whether some query token of the element sees key t (t < L).
 __host__ __device__ inline bool key_in_walk(int t, int L, int s_q, int window, int sinks) {
@@ -133,7 +142,7 @@ struct DecodeParams {
   // shared-prefix decode on CTA pairs: problems [0, prefix_problems) are the
   // prefix under 128 consecutive query rows each, the rest the own keys of
   // each element under its rows, 128 at a time
-  const int32_t* prefix_table;  // [prefix_pages]; NULL: page i is row block i of the cache map
+  const int32_t* prefix_table;  // [prefix_pages]
   const int32_t* prefix_len;    // [1]
   int prefix_pages, prefix_problems, blocks_per_elem, total_rows;
   float* own_o;                 // partials of the own keys: [own_slots, block_rows, 512], [own_slots, block_rows]
@@ -148,8 +157,9 @@ struct SchedSpec {
   const int32_t* seqlens;     // [batch]
   int s_q;
   int window, sinks;          // window > 0: windowed problems
+  int cols;                   // of the block table
   const int32_t* prefix_len;  // shared-prefix decode (see DecodeParams), else NULL
-  int prefix_problems, blocks_per_elem;
+  int prefix_pages, prefix_problems, blocks_per_elem;
 };
 
 // One kind of problems of a merge: where its pieces are and their partials.
@@ -234,7 +244,7 @@ struct SlotStoreParams {
 // Kernel launchers (defined in the .cu files); return a CUDA error code.
 cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, const Geometry& g, int32_t* sched,
                             int32_t* num_splits, cudaStream_t stream);
-// FP8 rows at 16 query rows per CTA (mla_decode_fp8.cu); window = 0: all keys
+// Windowed FP8 rows at 16 query rows per CTA (mla_decode_fp8.cu)
 cudaError_t launch_decode_fp8(const void* q, const DecodeParams& p, cudaStream_t stream);
 // mode: 0 dense bf16 cache, 1 sparse FP8 cache, 2 dense FP8 cache, 3 sparse bf16 rows, 4 and 5 windowed dense
 // over the bf16 and the FP8 cache

@@ -8,15 +8,15 @@ namespace mla {
 
 // Tiles of problem p.
 __device__ __forceinline__ int spec_tiles(const SchedSpec& sp, int p, int tile_tokens) {
-  if (sp.prefix_len) {
-    const int L = p < sp.prefix_problems ? sp.prefix_len[0] : sp.seqlens[(p - sp.prefix_problems) / sp.blocks_per_elem];
-    return L > 0 ? (L + tile_tokens - 1) / tile_tokens : 0;
-  }
-  if (sp.window > 0) {
-    const int per = tile_tokens / kPageSize;
-    return (key_walk(sp.seqlens[p], sp.s_q, sp.window, sp.sinks).pages + per - 1) / per;
-  }
-  return problem_tiles(sp.seqlens, p, 1, 0, tile_tokens);
+  const int per = tile_tokens / kPageSize;
+  int pages;
+  if (!sp.prefix_len)
+    pages = key_walk(sp.seqlens[p], sp.s_q, sp.window, sp.sinks, sp.cols).pages;
+  else if (p < sp.prefix_problems)
+    pages = pages_of(sp.prefix_len[0], sp.prefix_pages);
+  else
+    pages = pages_of(sp.seqlens[(p - sp.prefix_problems) / sp.blocks_per_elem], sp.cols);
+  return (pages + per - 1) / per;
 }
 
 // Windowed and shared-prefix decode make their schedule in every CTA of the
@@ -61,7 +61,9 @@ __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int
   spec.s_q = p.s_q;
   spec.window = p.window;
   spec.sinks = p.sinks;
+  spec.cols = p.block_table_stride;
   spec.prefix_len = p.prefix_len;
+  spec.prefix_pages = p.prefix_pages;
   spec.prefix_problems = p.prefix_problems;
   spec.blocks_per_elem = p.blocks_per_elem;
   auto both = [&](int i) -> long long {

@@ -138,3 +138,14 @@ def test_repeated_runs_and_graph_replays_agree():
     graph.replay()
     again = run(*case[:7], True)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("h_q", [16, 40, 128])
+@pytest.mark.parametrize("more", [1, 64, 2 ** 31 - 1])
+def test_lengths_past_the_tables(fmt, h_q, more):
+    q, kv, sc, pt, plen, bt, lens, want = problem(fmt, h_q, 1, 192, (128, 128, 128), False, seed=h_q)
+    far = i32([min(2 ** 31 - 1, 128 + more)] * 3)
+    check(*run(q, kv, sc, pt, plen, bt, far, False, flags=mla.DEVICE_BAD_PAGE), want, f"{fmt} own")
+    plen.fill_(min(2 ** 31 - 1, 192 + more))
+    check(*run(q, kv, sc, pt, plen, bt, lens, True, flags=mla.DEVICE_BAD_PAGE), want, f"{fmt} prefix")

@@ -197,3 +197,27 @@ class SmallCodes(FarScales):
 def test_scales_and_codes_far_apart(make, fmt, h_q, s_q):
     q, kv, sc, bt, lens, want = problem(fmt, h_q, s_q, (5, 64, 300, 777), 200, 20, seed=h_q, make=make)
     check(*run(q, kv, sc, bt, lens, 200, 20), want, f"{fmt} {h_q}x{s_q} {make.__name__}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("h_q,s_q", [(16, 1), (40, 1), (64, 2)])
+@pytest.mark.parametrize("window,sinks", [(100, 0), (100, 70), (100, 2 ** 31 - 1), (2 ** 31 - 1, 5)])
+def test_lengths_past_the_block_table(fmt, h_q, s_q, window, sinks):
+    """The keys that the table has pages for are attended to at the positions that the length gives
+    them; the missing ones are flagged, however many there are."""
+    cache = Cache(fmt, h_q + sinks % 100, 3 * 4 + 3)
+    lens = (2 ** 31 - 1, 2 ** 31 - 63, 192 + 1, 192 + 150)
+    g = torch.Generator("cuda").manual_seed(h_q)
+    q = torch.randn(len(lens), s_q, h_q, 576, generator=g, device="cuda").to(torch.bfloat16)
+    rows, want = [], []
+    reach = min(window, 1 << 30)
+    for b, L in enumerate(lens):
+        values, ids = cache.put(192)
+        rows.append(ids)
+        for i in range(s_q):
+            last = L - s_q + i
+            ids = [t for t in range(192) if t <= last and (t < sinks or t > last - reach)]
+            want.append(attend(q[b, i], values[torch.tensor(ids, dtype=torch.long, device="cuda")], SCALE))
+    want = tuple(torch.stack([w[k] for w in want]).view(len(lens), s_q, h_q, *([512] if k != 1 else [])) for k in range(3))
+    kv, sc = cache.tensors()
+    check(*run(q, kv, sc, table(rows), i32(lens), window, sinks, flags=mla.DEVICE_BAD_PAGE), want, f"{fmt} past the table")

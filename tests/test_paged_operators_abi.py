@@ -95,7 +95,7 @@ COMMON = [("q", None, 1, "q is NULL"), ("kvcache", None, 1, "kvcache is NULL"), 
           ("kvcache", P + 8, 1, "kvcache is not"), ("out", P + 8, 1, "out is not"), ("sm_scale", float("inf"), 1, "sm_scale"),
           ("is_fp8", 7, 1, "is_fp8"), ("kv_scales", P, 1, "kv_scales given"), ("block_table_stride", 0, 1, "stride"),
           ("batch", 0, 1, "batch"), ("s_q", 0, 1, "s_q"), ("h_q", 0, 1, "h_q"), ("h_q", 1025, 2, "1024"),
-          ("batch", 16385, 2, "16384")]
+          ("batch", 16385, 2, "16384"), ("block_table_stride", 2 ** 30, 2, "block table")]
 
 
 @pytest.mark.parametrize("field,value,status,needle", COMMON + [("window", 0, 1, "window"), ("sinks", -1, 1, "sinks")])
