@@ -315,7 +315,7 @@ mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, Geometry* g, W
   if (st != MLA_OK) return st;
   g->mode = is_fp8 ? 5 : 4;
   // a segment on a CTA pair costs about four of its tiles to start and to end
-  // (48 elements x 256 rows, 17 pages: 71.6 us against 74.8 at one tile)
+  // (64 elements x 128 rows, 33 pages: 70.7 us against 73.0 at one and a half)
   if (g->pair) g->overhead = 32;
   if (is_fp8 && g->rows <= kFp8RowsMax) fp8_rows_geometry(g);
   // two slots per part: the problems it starts and ends inside of
@@ -370,10 +370,10 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   g.mode = 6;
   g.tile_tokens = 128;
   g.tile_cost = 8;
-  // a segment costs about five tiles to start and to end: with one, the parts
-  // that hold many short own-key problems ended last (64 x 128 rows, 8192
-  // shared and ~256 own keys: 250 us at one tile, 183 at three, 163 at five)
-  g.overhead = 40;
+  // as for windows: with less, the parts that hold many short own-key problems
+  // end last (64 x 128 rows, 8192 shared and ~256 own keys: 190 us at one and a
+  // half tiles, 151 at four, 154 at five)
+  g.overhead = 32;
   const int forced = g_test_num_parts.load();
   g.num_parts = forced > 0 ? forced : (pairs > 0 ? pairs : 1);
   // every piece takes a slot: two per part and one per problem held whole

@@ -559,9 +559,10 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + 32 * d) = make_uint4(
               pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.o_accum + at + 32 * d);
-          dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-          dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+          uint32_t z[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] = __float_as_uint(y[i]);
+          st_global_v8(p.o_accum + at + 32 * d, z);
         }
       }
     }

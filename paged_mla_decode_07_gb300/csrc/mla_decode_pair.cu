@@ -1323,23 +1323,25 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int 
       tmem_ld_wait();
       if (write_ok) {
         if (final_out) {
-          uint4 lo, hi;
-          lo.x = pack_bf16x2(v[0] * inv, v[1] * inv);
-          lo.y = pack_bf16x2(v[2] * inv, v[3] * inv);
-          lo.z = pack_bf16x2(v[4] * inv, v[5] * inv);
-          lo.w = pack_bf16x2(v[6] * inv, v[7] * inv);
-          hi.x = pack_bf16x2(v[8] * inv, v[9] * inv);
-          hi.y = pack_bf16x2(v[10] * inv, v[11] * inv);
-          hi.z = pack_bf16x2(v[12] * inv, v[13] * inv);
-          hi.w = pack_bf16x2(v[14] * inv, v[15] * inv);
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDv + dv0 + c);
-          dst[0] = lo;
-          dst[1] = hi;
-        } else {
-          float4* dst = reinterpret_cast<float4*>((own ? p.own_o : p.o_accum) + orow * kDv + dv0 + c);
+          uint32_t y[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
+          for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) + orow * kDv + dv0 + c;
+          if ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) {
+            st_global_v8(dst, y);
+          } else {  // (16-byte aligned)
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+        } else {
+          float* dst = (own ? p.own_o : p.o_accum) + orow * kDv + dv0 + c;
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(v[8 * h2 + e] * inv);
+            st_global_v8(dst + 8 * h2, y);
+          }
         }
       }
     }

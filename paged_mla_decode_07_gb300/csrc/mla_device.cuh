@@ -433,6 +433,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 // Two fp32 values -> packed bf16x2 (round to nearest even); lo in the low half.
+// 32-byte store (32-byte aligned): a whole sector per thread, where threads
+// write rows apart from each other and each instruction costs a pass per row.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
