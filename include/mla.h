@@ -315,9 +315,12 @@ mla_status mla_sparse_prefill(const mla_sparse_prefill_args* args, mla_stream_t 
  * a row that sees no key gets out = 0 and lse = -inf.  Only the pages that
  * hold keys some query token sees are read, so the others need no
  * block-table entry.  A key that no query token of its element sees may hold
- * anything; one that some of them see must be finite.
- * Schedule, attention and combine are launched on `stream` by the one call;
- * device-side problems set bits in the device status word. */
+ * anything; one that some of them see must be finite, or rows of its element
+ * are not (those of other elements are).  Keys whose pages are missing from
+ * the block table, or past its columns, are left out and set
+ * MLA_DEVICE_BAD_PAGE.  FP8 scales are positive and below 2^39.
+ * The attention kernel, which makes its schedule itself, and the merge of its
+ * partial results are launched on `stream` by the one call. */
 typedef struct {
   const void* q;                  /* bf16 [batch, s_q, h_q, 576], 16-byte aligned */
   int batch, s_q, h_q;            /* s_q * h_q <= 1024 */
@@ -350,7 +353,9 @@ mla_status mla_window_decode(const mla_window_decode_args* args, mla_stream_t st
  * time, whatever elements they belong to.  The prefix may end inside a page;
  * own tokens start in pages of their own.  With an FP8 cache the prefix is
  * turned into bf16 rows in the workspace first.  Keys past a length may hold
- * anything; own keys must be finite.
+ * anything; keys that are not finite show in the rows that share them: all for
+ * the prefix, the element's for own keys.  Missing pages and FP8 scales as for
+ * mla_window_decode.
  * All launches are made on `stream` by the one call. */
 typedef struct {
   const void* q;                  /* bf16 [batch, s_q, h_q, 576], 16-byte aligned */

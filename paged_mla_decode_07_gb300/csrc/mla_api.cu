@@ -326,13 +326,13 @@ mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, Geometry* g, W
   return MLA_OK;
 }
 
-// Shared-prefix decode.  bf16 rows: one schedule over the prefix problems and
-// the own-key problems (`pre`, on CTA pairs).  FP8 rows: the prefix as bf16
-// rows and a table of its pages, one schedule over the prefix problems
-// (`pre`), one over the elements (`own`, on single CTAs).
+// Shared-prefix decode, on CTA pairs over blocks of 128 query rows (`pre`).
+// bf16 rows: the prefix and the own keys in one.  FP8 rows: the prefix alone,
+// as bf16 rows with a table of its pages; the own keys in a kernel of their
+// own (`own`).
 struct PrefixLayout {
   Geometry pre, own;
-  int prefix_problems, blocks_per_elem, block_rows, prefix_slots, own_slots;
+  int prefix_slots, own_slots;
   size_t spans, own_spans, o, lse, own_o, own_lse, table, rows, total;
 };
 mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_fp8, PrefixLayout* L) {
@@ -349,15 +349,11 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
     // the windowed mode with sinks that are every key
     L->own.mode = 5;
   }
-  L->prefix_problems = static_cast<int>((rows + 127) / 128);
-  L->blocks_per_elem = is_fp8 ? 1 : (L->own.rows + 127) / 128;
-  L->block_rows = is_fp8 ? L->own.rows : (L->own.rows < 128 ? L->own.rows : 128);
-  const long long own_problems = static_cast<long long>(batch) * L->blocks_per_elem;
-  const long long np = L->prefix_problems + (is_fp8 ? 0 : own_problems);
+  const long long np = (rows + 127) / 128;
   if (np > kMaxProblems)
     return fail(MLA_ERR_UNSUPPORTED, "batch*s_q*h_q = %lld query rows make %lld problems, more than the supported %d",
                 rows, np, kMaxProblems);
-  if (static_cast<long long>(L->prefix_problems) * prefix_pages > kMaxTilesTotal)
+  if (np * prefix_pages > kMaxTilesTotal)
     return fail(MLA_ERR_UNSUPPORTED, "batch*s_q*h_q = %lld query rows over a prefix table of %d entries", rows,
                 prefix_pages);
   Geometry& g = L->pre;
@@ -376,9 +372,9 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   g.overhead = 32;
   const int forced = g_test_num_parts.load();
   g.num_parts = forced > 0 ? forced : (pairs > 0 ? pairs : 1);
-  // every piece takes a slot: two per part and one per problem held whole
-  L->prefix_slots = 2 * g.num_parts + L->prefix_problems;
-  L->own_slots = 2 * (is_fp8 ? L->own.num_parts : g.num_parts) + static_cast<int>(own_problems);
+  // FP8: every piece takes a slot, two per part and one per problem held whole
+  L->prefix_slots = 2 * g.num_parts + (is_fp8 ? static_cast<int>(np) : 0);
+  L->own_slots = is_fp8 ? 2 * L->own.num_parts + batch : 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -386,11 +382,11 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
     return here;
   };
   L->spans = take(static_cast<size_t>(np) * 8);
-  L->own_spans = is_fp8 ? take(static_cast<size_t>(own_problems) * 8) : L->spans + static_cast<size_t>(L->prefix_problems) * 8;
+  L->own_spans = take(is_fp8 ? static_cast<size_t>(batch) * 8 : 0);
   L->o = take(static_cast<size_t>(L->prefix_slots) * 128 * kDv * 4);
   L->lse = take(static_cast<size_t>(L->prefix_slots) * 128 * 4);
-  L->own_o = take(static_cast<size_t>(L->own_slots) * L->block_rows * kDv * 4);
-  L->own_lse = take(static_cast<size_t>(L->own_slots) * L->block_rows * 4);
+  L->own_o = take(static_cast<size_t>(L->own_slots) * L->own.rows * kDv * 4);
+  L->own_lse = take(static_cast<size_t>(L->own_slots) * L->own.rows * 4);
   if (is_fp8) {
     L->table = take(static_cast<size_t>(prefix_pages) * 4);
     L->rows = take(static_cast<size_t>(prefix_pages) * kPageSize * kDqk * 2);
@@ -967,11 +963,10 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   if (e != cudaSuccess) return cuda_fail(e, "window decode kernel launch");
   MergeParams m;
   memset(&m, 0, sizeof m);
-  m.own = MergeSide{p.spans, p.o_accum, p.lse_accum, g.rows, -1};
-  m.cache_seqlens = a->cache_seqlens;
-  m.blocks_per_elem = 1;
+  m.own = MergeSide{p.spans, p.o_accum, p.lse_accum, -1};
   m.rows = g.rows;
-  m.batch = a->batch;
+  m.problems = a->batch;
+  m.total_rows = static_cast<int>(qrows);
   m.out = a->out;
   m.lse = a->lse;
   e = launch_merge(m, s);
@@ -1044,8 +1039,8 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   p.overhead = L.pre.overhead;
   p.o_accum = reinterpret_cast<float*>(ws + L.o);
   p.lse_accum = reinterpret_cast<float*>(ws + L.lse);
-  p.own_o = reinterpret_cast<float*>(ws + L.own_o);
-  p.own_lse = reinterpret_cast<float*>(ws + L.own_lse);
+  p.out = a->out;
+  p.lse = a->lse;
   p.status = status;
   p.timeout_ns = watchdog_ns();
   p.batch = a->batch;
@@ -1058,17 +1053,15 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   p.row_groups = 1;
   p.num_parts = L.pre.num_parts;
   p.max_slots = L.prefix_slots;
-  p.own_slots = L.own_slots;
-  p.block_rows = L.block_rows;
+  p.always_partial = a->is_fp8;
   p.is_causal = a->is_causal ? 1 : 0;
   p.debug_stall = g_test_debug_stall.load();
   p.scale_log2 = a->sm_scale * 1.4426950408889634f;
   p.prefix_table = a->is_fp8 ? reinterpret_cast<const int32_t*>(ws + L.table) : a->prefix_table;
   p.prefix_len = a->prefix_length;
   p.prefix_pages = a->prefix_table_len;
-  p.prefix_problems = L.prefix_problems;
-  p.blocks_per_elem = L.blocks_per_elem;
   p.total_rows = static_cast<int>(qrows);
+  p.own_keys = !a->is_fp8;
 
   if (a->is_fp8) {
     e = launch_prefix_rows(static_cast<const uint8_t*>(a->kvcache), a->kv_scales, a->prefix_table, a->prefix_length,
@@ -1084,8 +1077,8 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
     o.tile_cost = L.own.tile_cost;
     o.overhead = L.own.overhead;
     o.kv_fp8 = static_cast<const uint8_t*>(a->kvcache);
-    o.o_accum = p.own_o;
-    o.lse_accum = p.own_lse;
+    o.o_accum = reinterpret_cast<float*>(ws + L.own_o);
+    o.lse_accum = reinterpret_cast<float*>(ws + L.own_lse);
     o.num_pages = a->num_pages;
     o.num_problems = L.own.num_problems;
     o.row_groups = L.own.row_groups;
@@ -1094,7 +1087,6 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
     o.prefix_len = nullptr;
     o.window = 1;
     o.sinks = 0x7fffffff;  // every key
-    o.always_partial = 1;
     o.evict_first = L.own.row_groups == 1 ? 1 : 0;
     o.kv_scales = a->kv_scales;
     o.fp8_rope_off = a->kv_scales ? kDv : kFp8RopeOffset;
@@ -1104,16 +1096,19 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   }
   MergeParams m;
   memset(&m, 0, sizeof m);
-  m.prefix = MergeSide{p.spans, p.o_accum, p.lse_accum, 128, 2 * L.pre.num_parts};
-  const Geometry& og = a->is_fp8 ? L.own : L.pre;
-  m.own = MergeSide{reinterpret_cast<int32_t*>(ws + L.own_spans), p.own_o, p.own_lse, L.block_rows,
-                    2 * og.num_parts};
-  m.cache_seqlens = a->cache_seqlens;
-  m.prefix_len = a->prefix_length;
-  m.has_prefix = 1;
-  m.blocks_per_elem = L.blocks_per_elem;
-  m.rows = L.own.rows;
-  m.batch = a->batch;
+  m.total_rows = static_cast<int>(qrows);
+  if (a->is_fp8) {
+    m.prefix = MergeSide{p.spans, p.o_accum, p.lse_accum, 2 * L.pre.num_parts};
+    m.own = MergeSide{reinterpret_cast<int32_t*>(ws + L.own_spans), reinterpret_cast<float*>(ws + L.own_o),
+                      reinterpret_cast<float*>(ws + L.own_lse), 2 * L.own.num_parts};
+    m.has_prefix = 1;
+    m.rows = L.own.rows;
+    m.problems = a->batch;
+  } else {
+    m.own = MergeSide{p.spans, p.o_accum, p.lse_accum, -1};
+    m.rows = 128;
+    m.problems = L.pre.num_problems;
+  }
   m.out = a->out;
   m.lse = a->lse;
   e = launch_merge(m, s);

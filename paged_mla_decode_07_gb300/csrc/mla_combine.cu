@@ -159,15 +159,15 @@ __global__ void __launch_bounds__(kRowsPerBlock * 32) combine_kernel(const Combi
 // [4 t, 4 t + 4) and eight pieces' 2 KB lines in flight, or four rows with a
 // warp each.  The first suits few rows in many pieces (a small batch is cut
 // over all SMs: 96 rows of 17 pieces take ~5 us less), the second many rows in
-// few (12288 rows of two pieces take 5 us less).  Bound by latency (spans and
-// lengths, log-sum-exps, values: three dependent reads), and by the partials'
-// bytes where there are many rows.
+// few (12288 rows of two pieces take 5 us less).  Bound by latency (spans,
+// log-sum-exps, values: three dependent reads), and by the partials' bytes
+// where there are many rows.
 constexpr int kMergeThreads = 128;
 constexpr float kMergeNegInf = -__builtin_huge_valf();
 
-// The pieces of problem `prob` of a side, `tiles` > 0 tiles: n of them, the
-// first in slot `slot`, the others in those of the parts behind it.  n = -1:
-// a part held the problem whole and wrote its output.
+// The pieces of problem `prob` of a side: n of them, the first in slot `slot`,
+// the others in those of the parts behind it.  n = -1: a part held the problem
+// whole and wrote its output.
 struct Pieces {
   int n, slot;
   __device__ __forceinline__ int at(int i) const { return i == 0 ? slot : 2 * ((slot >> 1) + i); }
@@ -179,6 +179,13 @@ __device__ __forceinline__ Pieces find_pieces(const MergeSide& m, int prob) {
   return Pieces{n, s.x};
 }
 
+// Maximum, NaN if either is: a piece's log-sum-exp is NaN where a key that the row sees is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Merges the pieces of one row with all threads of the block.
 template <class At>
 __device__ __forceinline__ void merge_row_block(int n, At at, __nv_bfloat16* out, float* lse) {
@@ -186,9 +193,9 @@ __device__ __forceinline__ void merge_row_block(int n, At at, __nv_bfloat16* out
   auto lse_at = [&](int i) { return *at(i).second; };
   const float first = lane < n ? lse_at(lane) : kMergeNegInf;  // pieces 0..31, one per lane
   float mx = first;
-  for (int i = lane + 32; i < n; i += 32) mx = fmaxf(mx, lse_at(i));
+  for (int i = lane + 32; i < n; i += 32) mx = max_nan(mx, lse_at(i));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int o = 16; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float L = kMergeNegInf;
   if (mx != kMergeNegInf) {
@@ -203,18 +210,21 @@ __device__ __forceinline__ void merge_row_block(int n, At at, __nv_bfloat16* out
       const float w = lane < m ? exp2f((i0 == 0 ? first : lse_at(i0 + lane)) - L) : 0.f;
 #pragma unroll 1
       for (int k0 = 0; k0 < m; k0 += 8) {
+        // (values of a piece without keys for this row are not there)
         float4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k0 + k < m) v[k] = at(i0 + k0 + k).first[threadIdx.x];
+        float wk[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
-          if (k0 + k < m) {
-            acc.x += wk * v[k].x;
-            acc.y += wk * v[k].y;
-            acc.z += wk * v[k].z;
-            acc.w += wk * v[k].w;
+          wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+          if (k0 + k < m && wk[k] != 0.f) v[k] = at(i0 + k0 + k).first[threadIdx.x];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (k0 + k < m && wk[k] != 0.f) {
+            acc.x += wk[k] * v[k].x;
+            acc.y += wk[k] * v[k].y;
+            acc.z += wk[k] * v[k].z;
+            acc.w += wk[k] * v[k].w;
           }
         }
       }
@@ -230,9 +240,9 @@ __device__ __forceinline__ void merge_row_warp(int n, At at, __nv_bfloat16* out,
   constexpr int kAhead = 4;
   const int lane = threadIdx.x & 31;
   float mx = kMergeNegInf;
-  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, *at(i).second);
+  for (int i = lane; i < n; i += 32) mx = max_nan(mx, *at(i).second);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int o = 16; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float4 acc[4];
 #pragma unroll
   for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -261,6 +271,7 @@ __device__ __forceinline__ void merge_row_warp(int n, At at, __nv_bfloat16* out,
       for (int i = 0; i < kAhead; ++i) {
         if (i0 + i >= n) break;
         const float wi = exp2f(w[i] - L);
+        if (wi == 0.f) continue;  // (values of a piece without keys for this row are not there)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           acc[v].x += wi * x[i][v].x;
@@ -283,31 +294,26 @@ struct PiecePtr {
   const float* second;   // its log-sum-exp
 };
 
-// grid: (row blocks of an element, elements); WARP_ROWS: four rows per block,
-// a warp each (then an element's rows are a multiple of four where there is a
+// grid: (row blocks of a problem, problems); WARP_ROWS: four rows per block, a
+// warp each (then an element's rows are a multiple of four where there is a
 // prefix, so that the four lie in one block of its rows).
 template <bool WARP_ROWS>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int elem = blockIdx.y;
-  const int r0 = blockIdx.x * (WARP_ROWS ? 4 : 1);  // first row of the element
-  const int own = elem * p.blocks_per_elem + r0 / p.own.rows;
-  const int64_t row0 = static_cast<int64_t>(elem) * p.rows + r0;
-  const int pre = static_cast<int>(row0 / 128);
-  const int L = p.cache_seqlens[elem], L0 = p.has_prefix ? p.prefix_len[0] : 0;
-  Pieces own_pieces = find_pieces(p.own, own), prefix_pieces{0, 0};
-  if (p.has_prefix) prefix_pieces = find_pieces(p.prefix, pre);
-  // (spans of problems without keys were not written)
-  const int n0 = L0 > 0 ? prefix_pieces.n : 0, n1 = L > 0 ? own_pieces.n : 0;
+  const int prob = blockIdx.y;
+  const int r = blockIdx.x * (WARP_ROWS ? 4 : 1) + (WARP_ROWS ? threadIdx.x >> 5 : 0);
+  const int64_t row = static_cast<int64_t>(prob) * p.rows + r;
+  const Pieces own_pieces = find_pieces(p.own, prob);
+  Pieces prefix_pieces{0, 0};
+  if (r >= p.rows || row >= p.total_rows) return;
+  if (p.has_prefix) prefix_pieces = find_pieces(p.prefix, static_cast<int>(row / 128));
+  const int n0 = prefix_pieces.n, n1 = own_pieces.n;
   if (n1 < 0) return;  // one part held the problem and wrote its rows
-  const int r = r0 + (WARP_ROWS ? threadIdx.x >> 5 : 0);
-  if (r >= p.rows) return;
-  const int64_t row = static_cast<int64_t>(elem) * p.rows + r;
   auto at = [&](int i) {
     const bool in_prefix = i < n0;
     const MergeSide& m = in_prefix ? p.prefix : p.own;
     const int slot = in_prefix ? prefix_pieces.at(i) : own_pieces.at(i - n0);
-    const int64_t s = static_cast<int64_t>(slot) * m.rows + (in_prefix ? static_cast<int>(row % 128) : r % m.rows);
+    const int64_t s = in_prefix ? static_cast<int64_t>(slot) * 128 + row % 128 : static_cast<int64_t>(slot) * p.rows + r;
     return PiecePtr{reinterpret_cast<const float4*>(m.o + s * kDv), m.lse + s};
   };
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + row * kDv;
@@ -321,10 +327,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
 
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
   // rows enough to fill the chip four to a block, in few pieces each
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.rows;
-  const bool warp_rows = rows >= 2048 && (!p.has_prefix || (p.rows % 4 == 0 && p.own.rows % 4 == 0));
+  const bool warp_rows = p.total_rows >= 2048 && (!p.has_prefix || p.rows % 4 == 0);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(warp_rows ? (p.rows + 3) / 4 : p.rows), static_cast<unsigned>(p.batch));
+  cfg.gridDim = dim3(static_cast<unsigned>(warp_rows ? (p.rows + 3) / 4 : p.rows), static_cast<unsigned>(p.problems));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

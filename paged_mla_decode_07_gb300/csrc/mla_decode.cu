@@ -1265,8 +1265,9 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments<Cfg<R, MO
     if (tid < RW) {
       const int r = rb + tid;
       const float lt = red[r] + red[R + r] + red[2 * R + r] + red[3 * R + r];
-      inv_s[r] = lt > 0.f ? 1.0f / lt : 0.f;
-      lse_s[r] = lt > 0.f ? m_s[r] + log2f(lt) : kNegInf;
+      const bool some = C::kWindow ? lt != 0.f : lt > 0.f;  // (windowed: NaN stays NaN, through the merge too)
+      inv_s[r] = some ? 1.0f / lt : 0.f;
+      lse_s[r] = some ? m_s[r] + log2f(lt) : kNegInf;
     }
     gsync();
     // partial-result slots of this problem: none when this piece is the whole problem

@@ -193,9 +193,11 @@ static_assert(kBCount * 8 <= kPairBarBytes, "barrier area");
 //
 // Variants of the dense kernel: kPlain as scheduled by mla_get_metadata;
 // kWindowed walks the pages of the first keys and of the window; kPrefixed
-// takes a batch that shares a prefix as two kinds of problems, the prefix
-// under 128 consecutive query rows of the batch, and each element's own keys
-// under its rows, 128 at a time (the row group is part of the problem).
+// takes a batch that shares a prefix as problems of 128 consecutive query rows
+// over the prefix's tiles and then over those of the own keys of each element
+// that the rows belong to, masked to its rows.  Own keys as problems of their
+// own would read as many tiles (of 128 rows, few of them used) and pay for
+// starts, ends and partial results besides.
 constexpr int kPlain = 0, kWindowed = 1, kPrefixed = 2;
 
 template <int VAR>
@@ -205,14 +207,12 @@ struct PairSeg {
   int cols;                              // of the block table (kWindowed, kPrefixed)
   int window, sinks;                     // (kWindowed)
   const int32_t* prefix_len;             // (kPrefixed)
-  int prefix_pages, prefix_problems, blocks_per_elem;  // (kPrefixed)
+  int prefix_pages, rows, total_rows, own_keys;  // (kPrefixed)
   __device__ int last() const { return p1 < np ? p1 : np - 1; }
   __device__ int tiles(int p) const {
     if (VAR == kWindowed) return (key_walk(seqlens[p], s_q, window, sinks, cols).pages + 1) / 2;
     if (VAR == kPrefixed)
-      return ((p < prefix_problems ? pages_of(prefix_len[0], prefix_pages)
-                                   : pages_of(seqlens[(p - prefix_problems) / blocks_per_elem], cols)) +
-              1) / 2;
+      return block_tiles(p, prefix_len[0], prefix_pages, seqlens, cols, rows, total_rows, own_keys);
     return problem_tiles(seqlens, p, s_q, topk, kPairTile);
   }
   __device__ void range(int p, int& tb, int& te) const {
@@ -223,55 +223,86 @@ struct PairSeg {
   }
 };
 
-// What a dense problem reads and where its rows are.
+// What a dense problem reads and where its rows are.  kPrefixed: what the run
+// of tiles reads that seek() has come to, the prefix or an element's own keys.
 template <int VAR>
 struct PairView {
   int L;                 // keys
   const int32_t* table;  // page ids by logical page
   int table_len;
-  int64_t row0;          // query row (of the whole call) of the row group's first row
-  int rows;              // rows of the row group from there on that exist (may exceed 128)
-  int in_elem;           // row of its element that row0 is
-  bool causal;
   KeyWalk walk;          // (kWindowed)
+  // (kPrefixed) the run's tiles [j0, jn), its element (-1: the prefix), the next element and the last one
+  int j0, jn, elem, next, last;
+  bool mixed;  // (kPrefixed) the block's rows are those of several elements
 
   __device__ PairView() {}
-  __device__ PairView(const DecodeParams& p, const PairSeg<VAR>& sg, int prob, int g) {
+  __device__ PairView(const DecodeParams& p, const PairSeg<VAR>& sg, int prob) {
     if (VAR == kPrefixed) {
-      if (prob < p.prefix_problems) {
-        L = p.prefix_len[0];
-        table = p.prefix_table;
-        table_len = p.prefix_pages;
-        row0 = static_cast<int64_t>(prob) * 2 * kPairRows;
-        rows = p.total_rows - static_cast<int>(row0);
-        in_elem = 0;
-        causal = false;
-      } else {
-        const int b = (prob - p.prefix_problems) / p.blocks_per_elem, gg = (prob - p.prefix_problems) % p.blocks_per_elem;
-        L = sg.seqlens[b];
-        table = p.block_table + static_cast<int64_t>(b) * p.block_table_stride;
-        table_len = p.block_table_stride;
-        in_elem = gg * 2 * kPairRows;
-        row0 = static_cast<int64_t>(b) * p.rows + in_elem;
-        rows = p.rows - in_elem;
-        causal = p.is_causal != 0;
-      }
+      L = p.prefix_len[0];
+      table = p.prefix_table;
+      table_len = p.prefix_pages;
+      j0 = 0;
+      jn = key_tiles(L, table_len);
+      elem = -1;
+      next = block_first(prob, sg.rows);
+      last = sg.own_keys ? block_last(prob, sg.rows, sg.total_rows) : -1;
+      mixed = last > next;
     } else {
       L = sg.seqlens[prob];
       table = p.block_table + static_cast<int64_t>(prob) * p.block_table_stride;
       table_len = p.block_table_stride;
-      in_elem = g * 2 * kPairRows;
-      row0 = static_cast<int64_t>(prob) * p.rows + in_elem;
-      rows = p.rows - in_elem;
-      causal = p.is_causal != 0;
       if (VAR == kWindowed) walk = key_walk(L, sg.s_q, sg.window, sg.sinks, sg.cols);
     }
   }
+  // To the run of tile j (never backwards); true when it is another one.  All
+  // lanes of a warp together: a block of rows may hold 128 elements.
+  __device__ __forceinline__ bool seek(const DecodeParams& p, const PairSeg<VAR>& sg, int j) {
+    if (VAR != kPrefixed || j < jn) return false;
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (;;) {
+      const int len = next + lane <= last ? sg.seqlens[next + lane] : 0;
+      const int n = key_tiles(len, sg.cols);
+      int x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t found = __ballot_sync(0xffffffffu, jn + x > j);
+      if (found) {
+        const int k = __ffs(found) - 1;
+        const int end = jn + __shfl_sync(0xffffffffu, x, k);
+        L = __shfl_sync(0xffffffffu, len, k);
+        j0 = end - __shfl_sync(0xffffffffu, n, k);
+        jn = end;
+        elem = next + k;
+        next = elem + 1;
+        break;
+      }
+      jn += __shfl_sync(0xffffffffu, x, 31);
+      next += 32;
+      if (next > last) {  // (a tile of the problem lies in some run)
+        elem = last;
+        L = 0;
+        break;
+      }
+    }
+    table = p.block_table + static_cast<int64_t>(elem) * p.block_table_stride;
+    table_len = p.block_table_stride;
+    return true;
+  }
+  // The run's keys stand in the same products as rows that do not see them,
+  // rows of other elements: nothing not finite in them may reach those.
+  __device__ __forceinline__ bool guarded() const { return VAR == kPrefixed && elem >= 0 && mixed; }
   // logical page of half h (0, 1) of tile j; -1 past the last one
   __device__ __forceinline__ int logical(int j, int h) const {
+    if (VAR == kPrefixed) {
+      const int i = 2 * (j - j0) + h;
+      return i <= (L - 1) / kPageSize ? i : -1;
+    }
     const int i = 2 * j + h;
     if (VAR == kWindowed) return i < walk.pages ? walk.page(i) : -1;
-    if (VAR == kPrefixed) return i <= (L - 1) / kPageSize ? i : -1;
     return i * kPageSize < L ? i : -1;
   }
   // Its page id, or -1 when it holds no cached token or its block-table
@@ -292,7 +323,8 @@ struct PairView {
   }
   // Tile j holds keys that no row sees beside keys that are seen: their slots
   // may hold anything (e.g. NaN), so the value rows of those tokens are
-  // zeroed after the copy lands, before the PV MMAs.
+  // zeroed after the copy lands, before the PV MMAs (guarded runs: or looked
+  // through for values that are not finite).
   __device__ __forceinline__ bool tail(int j, const PairSeg<VAR>& sg) const {
     if (VAR == kWindowed) {
       const int past = L - sg.s_q - sg.window;  // the last key that only the first keys' rule can show
@@ -305,7 +337,8 @@ struct PairView {
       }
       return false;
     }
-    return L > 0 && (L & (kPageSize - 1)) != 0 && j == (L - 1) / kPairTile;
+    if (guarded()) return true;
+    return L > 0 && (L & (kPageSize - 1)) != 0 && (VAR == kPrefixed ? j - j0 : j) == (L - 1) / kPairTile;
   }
 };
 
@@ -429,7 +462,7 @@ __device__ void pair_producer_ks(const CUtensorMap* tm_q, const CUtensorMap* tm_
     if (q_armed > 0 && !pair_wait(bars + 8 * kBQEmpty, (q_armed - 1) & 1, wd)) goto drain;
     {
       // this CTA's 64 query rows, all nine chunks, in one copy
-      const int row0 = VAR == kPrefixed ? static_cast<int>(PairView<VAR>(p, sg, prob, g).row0) + rank * kPairRows
+      const int row0 = VAR == kPrefixed ? prob * 2 * kPairRows + rank * kPairRows
                                         : prob * p.rows + g * 2 * kPairRows + rank * kPairRows;
       if (lane == 0) {
         if (rank == 0) {
@@ -444,15 +477,17 @@ __device__ void pair_producer_ks(const CUtensorMap* tm_q, const CUtensorMap* tm_
     }
     if (SPARSE) continue;  // the gather warps fill the score operand
     {
-      const PairView<VAR> view(p, sg, prob, g);
+      PairView<VAR> view(p, sg, prob), ahead = view;
       for (int j = tb; j < te; ++j, ++jt) {
+        view.seek(p, sg, j);
         const int pg = view.page(p, j, rank, lane == 0);
         const int row = pg >= 0 ? pg * kPageSize : oob_row;
         if (lane == 0) PAIR_TR(rank, 0, jt);
         // the page two tiles ahead goes to L2 now, so that its copy into shared
         // memory (which must wait for this tile's score MMAs) hits L2
         if (j + 2 < te) {
-          const int pg2 = view.page(p, j + 2, rank, false);
+          ahead.seek(p, sg, j + 2);
+          const int pg2 = ahead.page(p, j + 2, rank, false);
           if (pg2 >= 0 && lane < 3) tma_prefetch3(tm_ks, 0, pg2 * kPageSize, 3 * lane);
         }
 #pragma unroll 1
@@ -495,8 +530,8 @@ drain:
 // 4m + 2 rank and 4m + 2 rank + 1 for m = 0, 1), into slots 4t + 2m, 4t + 2m + 1
 // ---------------------------------------------------------------------------
 template <int VAR>
-__device__ void pair_producer_kv(const CUtensorMap* tm_kv, const DecodeParams& p, const PairSeg<VAR>& sg, int g,
-                                 int rank, uint32_t smem, uint32_t bars, uint32_t bars_even, const Watchdog& wd) {
+__device__ void pair_producer_kv(const CUtensorMap* tm_kv, const DecodeParams& p, const PairSeg<VAR>& sg, int rank,
+                                 uint32_t smem, uint32_t bars, uint32_t bars_even, const Watchdog& wd) {
   // Every tile's value slots complete on the even CTA's kv_full (armed with
   // both CTAs' bytes), except on a tail tile, where each CTA's copies
   // complete on its own kv_full so that its softmax warps can zero the rows
@@ -512,8 +547,9 @@ __device__ void pair_producer_kv(const CUtensorMap* tm_kv, const DecodeParams& p
     int tb, te;
     sg.range(prob, tb, te);
     if (tb >= te) continue;
-    const PairView<VAR> view(p, sg, prob, g);
+    PairView<VAR> view(p, sg, prob);
     for (int j = tb; j < te; ++j, ++jt) {
+      view.seek(p, sg, j);
       const int pg0 = view.page(p, j, 0, false);
       const int pg1 = view.page(p, j, 1, false);
       const bool tail = view.tail(j, sg);
@@ -1039,6 +1075,12 @@ done:
 // ---------------------------------------------------------------------------
 // warps 4-11: online softmax and epilogue
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+  if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+  if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
+  return v;
+}
+
 template <bool SPARSE, bool ROWS16, int VAR>
 __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int g, int rank, int part, int split0,
                              uint32_t tmem, uint32_t smem, uint32_t bars, uint32_t bars_even, float* m_s, float* red,
@@ -1142,16 +1184,24 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int 
     if (tb >= te) continue;
     // (sparse: the validity bits, and no lengths for unpaged rows)
     PairView<VAR> view;
-    if (!SPARSE) view = PairView<VAR>(p, sg, prob, g);
-    const int L = SPARSE ? 0 : view.L;
+    if (!SPARSE) view = PairView<VAR>(p, sg, prob);
+    // this thread's row: its element (kPrefixed) and its query token
+    const int urow = VAR == kPrefixed ? prob * 2 * kPairRows + rank * kPairRows + r : grow;
+    const int my_elem = VAR == kPrefixed ? urow / p.rows : 0;
+    const int my_tok = SPARSE ? 0 : (VAR == kPrefixed ? urow - my_elem * p.rows : urow) / p.h_q;
     // last visible key of this row (dense: bottom-right causal alignment)
-    const int lim = (!SPARSE && view.causal) ? L - p.s_q + (view.in_elem + rank * kPairRows + r) / p.h_q
-                                                     : L - 1;
+    auto limit = [&]() {
+      if (SPARSE) return -1;
+      if (VAR == kPrefixed && view.elem != my_elem) return view.elem < 0 ? view.L - 1 : -1;
+      return p.is_causal ? view.L - p.s_q + my_tok : view.L - 1;
+    };
+    int lim = limit();
     float l_part = 0.f;
     for (int j = tb; j < te; ++j, ++jt) {
       const int sb = jt & 1;
       // dense: the block-table entry of this thread's page, read before the
       // wait for S so that the load overlaps it
+      if (VAR == kPrefixed && view.seek(p, sg, j)) lim = limit();
       const bool page_ok = SPARSE ? true : view.page(p, j, h, false) >= 0;
       if (!wait_all(kBSFull + sb, (jt >> 1) & 1)) return;
       tc_fence_after();
@@ -1181,7 +1231,16 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int 
       }
       // first token of this thread's 32 (windowed: wherever the walk's page lies)
       const int pos0 = VAR == kWindowed ? max(view.logical(j, h), 0) * kPageSize + 32 * w
-                                        : j * kPairTile + h * 64 + 32 * w;
+                                        : (VAR == kPrefixed ? j - view.j0 : j) * kPairTile + h * 64 + 32 * w;
+      // (a key with a value that is not finite has no finite score in any row,
+      // so one of each warp's rows tells; 0 x is NaN for those)
+      bool odd = false;
+      if (VAR == kPrefixed && view.guarded()) {
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z = fmaf(x[i], 0.f, z);
+        odd = __any_sync(0xffffffffu, z != 0.f);
+      }
       float mx = kPairNegInf;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -1244,13 +1303,26 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int 
       // zeros by the gather warps.)
       if (!SPARSE && view.tail(j, sg)) {
         if (!wait_all(kBKvFull, jt & 1)) return;
-        const int tl = (q & 1) * 32 + lane;  // token of page h zeroed by this thread
+        // token of page h zeroed by this thread, of those its warp has the scores of
+        const int tl = 32 * w + lane;
         if (page_ok && !view.seen(view.logical(j, h) * kPageSize + tl, sg)) {
 #pragma unroll
           for (int s2 = 0; s2 < 2; ++s2) {
-            const uint32_t rowa = smem + kPairKvOff + (4 * h + 2 * w + s2) * kPairChunk + tl * 128;
+            const uint32_t rowa = smem + kPairKvOff + (4 * h + 2 * (q & 1) + s2) * kPairChunk + tl * 128;
 #pragma unroll
             for (int u = 0; u < 8; ++u) st_shared_v4(rowa + 16 * u, 0u, 0u, 0u, 0u);
+          }
+        } else if (VAR == kPrefixed && odd) {
+          // zeros for what is not finite (the rows that see the key have NaN in P)
+#pragma unroll 1
+          for (int s2 = 0; s2 < 2; ++s2) {
+            const uint32_t rowa = smem + kPairKvOff + (4 * h + 2 * (q & 1) + s2) * kPairChunk + tl * 128;
+#pragma unroll 1
+            for (int u = 0; u < 8; ++u) {
+              const uint4 v = ld_shared_v4(rowa + 16 * u);
+              st_shared_v4(rowa + 16 * u, finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z),
+                           finite_bf16x2(v.w));
+            }
           }
         }
       }
@@ -1291,10 +1363,11 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int 
     const float lt = red[r] + red[64 + r] + red[128 + r] + red[192 + r];
     const float m_fin = m_s[r];
     named_bar_sync(kPairSmBar, 256);  // red and m_s are reused by the next segment
-    const float inv = lt > 0.f ? 1.0f / lt : 0.f;
-    const float lse = lt > 0.f ? m_fin + log2f(lt) : kPairNegInf;
+    // (windowed and prefixed: a sum that is NaN stays NaN, through the merge too)
+    const bool some = VAR == kPlain ? lt > 0.f : lt != 0.f;
+    const float inv = some ? 1.0f / lt : 0.f;
+    const float lse = some ? m_fin + log2f(lt) : kPairNegInf;
     // (windowed and prefixed: slots by part, see mla_schedule.cuh)
-    const bool own = VAR == kPrefixed && prob >= p.prefix_problems;
     bool final_out;
     int slot;
     if (VAR == kPlain) {
@@ -1302,26 +1375,27 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int 
       slot = p.num_splits[prob] + (prob == sg.p0 ? split0 : 0);
     } else {
       const bool whole = tb == 0 && te == sg.tiles(prob);
-      final_out = VAR == kWindowed && whole;
-      slot = piece_slot(whole, own ? prob - p.prefix_problems : prob, 2 * p.num_parts, part, prob == sg.p0);
+      final_out = whole && !p.always_partial;
+      slot = piece_slot(whole, prob, 2 * p.num_parts, part, prob == sg.p0);
     }
-    bool write_ok = VAR == kPrefixed ? rank * kPairRows + r < view.rows : grow < p.rows;
-    if (!final_out && (slot < 0 || slot >= (own ? p.own_slots : p.max_slots))) {
+    bool write_ok = VAR == kPrefixed ? urow < p.total_rows : grow < p.rows;
+    if (!final_out && (slot < 0 || slot >= p.max_slots)) {
       write_ok = false;
       if (r == 0 && hw == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
     }
+    // (rows of elements whose keys are in other pieces: the merge reads no values of theirs)
+    const bool write_o = write_ok && (VAR != kPrefixed || final_out || lse != kPairNegInf);
     const int dv0 = 256 * w + 128 * h;
-    // (prefixed: one row group; slots of 128 rows for the prefix, of block_rows for the own keys)
-    const int64_t orow = VAR == kPrefixed ? static_cast<int64_t>(slot) * (own ? p.block_rows : 2 * kPairRows) +
-                                                rank * kPairRows + r
-                         : final_out      ? static_cast<int64_t>(prob) * p.rows + grow
-                                          : static_cast<int64_t>(slot) * p.rows + grow;
+    // (prefixed: one row group; slots of 128 rows)
+    const int64_t orow = VAR == kPrefixed
+                             ? (final_out ? urow : static_cast<int64_t>(slot) * (2 * kPairRows) + rank * kPairRows + r)
+                             : static_cast<int64_t>(final_out ? prob : slot) * p.rows + grow;
 #pragma unroll 1
     for (int c = 0; c < 128; c += 16) {
       float v[16];
       tmem_ld_x16(tmem + lane_base + kPairOCol + 128 * w + c, v);
       tmem_ld_wait();
-      if (write_ok) {
+      if (write_o) {
         if (final_out) {
           uint32_t y[8];
 #pragma unroll
@@ -1334,7 +1408,7 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int 
             reinterpret_cast<uint4*>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
           }
         } else {
-          float* dst = (own ? p.own_o : p.o_accum) + orow * kDv + dv0 + c;
+          float* dst = p.o_accum + orow * kDv + dv0 + c;
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
             uint32_t y[8];
@@ -1349,7 +1423,7 @@ __device__ void pair_softmax(const DecodeParams& p, const PairSeg<VAR>& sg, int 
       if (final_out)
         p.lse[orow] = lse;
       else
-        (own ? p.own_lse : p.lse_accum)[orow] = lse;
+        p.lse_accum[orow] = lse;
     }
     tc_fence_before();
     arrive_even(kBOEmpty);
@@ -1467,8 +1541,9 @@ __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
   sg.sinks = p.sinks;
   sg.prefix_len = p.prefix_len;
   sg.prefix_pages = p.prefix_pages;
-  sg.prefix_problems = p.prefix_problems;
-  sg.blocks_per_elem = p.blocks_per_elem;
+  sg.rows = p.rows;
+  sg.total_rows = p.total_rows;
+  sg.own_keys = p.own_keys;
   if (sg.p0 < 0 || sg.p0 > sg.np || sg.p1 < sg.p0 || sg.p1 > sg.np || sg.t0 < 0 || sg.t1 < 0) {
     if (threadIdx.x == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
     sg.p0 = sg.np;
@@ -1497,7 +1572,7 @@ __global__ void __launch_bounds__(PairCfg<SPARSE>::kThreads, 1)
       if constexpr (SPARSE)
         pair_value_copier(sg, rank, smem, bars, bars_even, wd);
       else
-        pair_producer_kv<VAR>(&tm_kv, p, sg, g, rank, smem, bars, bars_even, wd);
+        pair_producer_kv<VAR>(&tm_kv, p, sg, rank, smem, bars, bars_even, wd);
     } else if (rank == 0) {
       pair_pv_issuer<VAR>(sg, tmem, smem, bars, wd);
     }

@@ -139,15 +139,12 @@ struct DecodeParams {
   int tile_cost, overhead;    // schedule costs
   int32_t* spans;             // [2 * problems] slot of the first piece, part of the last one
 
-  // shared-prefix decode on CTA pairs: problems [0, prefix_problems) are the
-  // prefix under 128 consecutive query rows each, the rest the own keys of
-  // each element under its rows, 128 at a time
+  // shared-prefix decode on CTA pairs: problem i is rows [128 i, 128 i + 128)
+  // of the batch over the prefix and, with own_keys, then over the own keys of
+  // each element that some of them belong to
   const int32_t* prefix_table;  // [prefix_pages]
   const int32_t* prefix_len;    // [1]
-  int prefix_pages, prefix_problems, blocks_per_elem, total_rows;
-  float* own_o;                 // partials of the own keys: [own_slots, block_rows, 512], [own_slots, block_rows]
-  float* own_lse;
-  int block_rows, own_slots;    // (max_slots: the prefix's)
+  int prefix_pages, total_rows, own_keys;
 
   float scale_log2;           // sm_scale * log2(e)
 };
@@ -159,7 +156,7 @@ struct SchedSpec {
   int window, sinks;          // window > 0: windowed problems
   int cols;                   // of the block table
   const int32_t* prefix_len;  // shared-prefix decode (see DecodeParams), else NULL
-  int prefix_pages, prefix_problems, blocks_per_elem;
+  int prefix_pages, rows, total_rows, own_keys;
 };
 
 // One kind of problems of a merge: where its pieces are and their partials.
@@ -167,20 +164,15 @@ struct MergeSide {
   const int32_t* spans;       // [2 * problems of this kind]
   const float* o;             // [slots, rows, 512]
   const float* lse;           // [slots, rows]
-  int rows;                   // rows per slot
   int whole_base;             // slots before those of problems held whole; -1: these write the output themselves
 };
 
-// Merge of the partials of windowed decode (`own` alone) and of shared-prefix
-// decode: row b * rows + r has pieces of the prefix under its block of 128
-// rows and pieces of its element's keys.
+// Merge of the partials of problems of `rows` query rows each (`own`) and,
+// where an FP8 prefix has its own, of blocks of 128 rows (`prefix`).
 struct MergeParams {
   MergeSide own, prefix;
-  const int32_t* cache_seqlens;  // [batch] own keys
-  const int32_t* prefix_len;     // [1]
   int has_prefix;
-  int blocks_per_elem;        // own problems per element
-  int rows, batch;            // query rows per element
+  int rows, problems, total_rows;
   void* out;
   float* lse;
 };

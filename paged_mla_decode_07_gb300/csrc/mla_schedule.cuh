@@ -6,17 +6,31 @@
 
 namespace mla {
 
+// Tiles of 128 keys of shared-prefix problem i: the prefix's, then those of
+// the own keys of each element that the block's rows belong to.
+__device__ __forceinline__ int block_first(int i, int rows) { return static_cast<int>(i * 128ll / rows); }
+__device__ __forceinline__ int block_last(int i, int rows, int total_rows) {
+  const long long end = i * 128ll + 128;
+  return static_cast<int>(((end < total_rows ? end : total_rows) - 1) / rows);
+}
+__device__ __forceinline__ int key_tiles(int L, int cols) { return (pages_of(L, cols) + 1) / 2; }
+__device__ __forceinline__ int block_tiles(int i, int prefix_len, int prefix_pages, const int32_t* seqlens, int cols,
+                                           int rows, int total_rows, int own_keys) {
+  int n = key_tiles(prefix_len, prefix_pages);
+  if (own_keys) {
+    const int last = block_last(i, rows, total_rows);
+#pragma unroll 8
+    for (int e = block_first(i, rows); e <= last; ++e) n += key_tiles(seqlens[e], cols);
+  }
+  return n;
+}
+
 // Tiles of problem p.
 __device__ __forceinline__ int spec_tiles(const SchedSpec& sp, int p, int tile_tokens) {
+  if (sp.prefix_len)
+    return block_tiles(p, sp.prefix_len[0], sp.prefix_pages, sp.seqlens, sp.cols, sp.rows, sp.total_rows, sp.own_keys);
   const int per = tile_tokens / kPageSize;
-  int pages;
-  if (!sp.prefix_len)
-    pages = key_walk(sp.seqlens[p], sp.s_q, sp.window, sp.sinks, sp.cols).pages;
-  else if (p < sp.prefix_problems)
-    pages = pages_of(sp.prefix_len[0], sp.prefix_pages);
-  else
-    pages = pages_of(sp.seqlens[(p - sp.prefix_problems) / sp.blocks_per_elem], sp.cols);
-  return (pages + per - 1) / per;
+  return (key_walk(sp.seqlens[p], sp.s_q, sp.window, sp.sinks, sp.cols).pages + per - 1) / per;
 }
 
 // Windowed and shared-prefix decode make their schedule in every CTA of the
@@ -38,7 +52,8 @@ __device__ __forceinline__ int spec_tiles(const SchedSpec& sp, int p, int tile_t
 // whole write partial results too, one per problem.  spans[2 i] is the slot of
 // problem i's first piece and spans[2 i + 1] the part of its last one, written
 // by the parts that hold its first and its last tile; the pieces between have
-// slots 2 k.
+// slots 2 k.  A problem without tiles lies in the range of some part (those
+// before the first one with tiles: of part 0), which writes (0, -1).
 struct PartRecord {
   int p0, t0, p1, t1;
 };
@@ -64,8 +79,9 @@ __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int
   spec.cols = p.block_table_stride;
   spec.prefix_len = p.prefix_len;
   spec.prefix_pages = p.prefix_pages;
-  spec.prefix_problems = p.prefix_problems;
-  spec.blocks_per_elem = p.blocks_per_elem;
+  spec.rows = p.rows;
+  spec.total_rows = p.total_rows;
+  spec.own_keys = p.own_keys;
   auto both = [&](int i) -> long long {
     const int n = spec_tiles(spec, i, tile_tokens);
     return n > 0 ? (static_cast<long long>(n) << 32) | 1 : 0;
@@ -152,8 +168,13 @@ __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int
   if (publish) {
     const int end = r.p1 < np ? r.p1 : np - 1;
 #pragma unroll 1
-    for (int i = r.p0 + tid; i <= end; i += blockDim.x) {
+    for (int i = (part == 0 ? 0 : r.p0) + tid; i <= end; i += blockDim.x) {
       const int n = static_cast<int>((pre[i + 1] - pre[i]) >> 32);
+      if (n == 0) {
+        p.spans[2 * i] = 0;
+        p.spans[2 * i + 1] = -1;
+        continue;
+      }
       const int tb = i == r.p0 ? r.t0 : 0, te = i == r.p1 ? r.t1 : n;
       if (tb >= te) continue;
       if (tb == 0) p.spans[2 * i] = 2 * part + (i == r.p0 ? 0 : 1);

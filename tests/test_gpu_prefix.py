@@ -149,3 +149,23 @@ def test_lengths_past_the_tables(fmt, h_q, more):
     check(*run(q, kv, sc, pt, plen, bt, far, False, flags=mla.DEVICE_BAD_PAGE), want, f"{fmt} own")
     plen.fill_(min(2 ** 31 - 1, 192 + more))
     check(*run(q, kv, sc, pt, plen, bt, lens, True, flags=mla.DEVICE_BAD_PAGE), want, f"{fmt} prefix")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("h_q,s_q", [(1, 1), (16, 1), (20, 2), (128, 1)])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_keys_that_are_not_finite_stay_in_their_element(fmt, h_q, s_q, bad):
+    """Rows of several elements share a block of the products: one element's broken keys reach no other one."""
+    own = (70, 130, 64, 5, 200, 1)
+    q, kv, sc, pt, plen, bt, lens, want = problem(fmt, h_q, s_q, 300, own, False, seed=h_q)
+    hit = 1
+    for t in (3, 129):
+        page, slot = int(bt[hit, t // 64]), t % 64
+        if fmt == "bf16":
+            kv.view(torch.int16)[page, slot, 0, 7 * t % 512] = 0x7FC0 if bad == "nan" else 0x7F80
+        else:
+            kv[page, slot, 0, 512:516].view(torch.float32).fill_(float(bad))
+    out, lse = run(q, kv, sc, pt, plen, bt, lens, False)
+    keep = [b for b in range(len(own)) if b != hit]
+    check(out[keep], lse[keep], tuple(w[keep] for w in want), f"{fmt} {h_q} beside {bad}")
+    assert bool(torch.isnan(out[hit]).any()) and not bool(torch.isfinite(lse[hit]).any() and bad == "nan")

@@ -221,3 +221,24 @@ def test_lengths_past_the_block_table(fmt, h_q, s_q, window, sinks):
     want = tuple(torch.stack([w[k] for w in want]).view(len(lens), s_q, h_q, *([512] if k != 1 else [])) for k in range(3))
     kv, sc = cache.tensors()
     check(*run(q, kv, sc, table(rows), i32(lens), window, sinks, flags=mla.DEVICE_BAD_PAGE), want, f"{fmt} past the table")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("h_q", [8, 40, 128])
+@pytest.mark.parametrize("parts", [None, 40])
+def test_a_seen_nan_is_not_lost(fmt, h_q, parts):
+    """Whole problems and split ones alike: the element's rows and their lse are NaN, the others' are right."""
+    lens = (700, 130, 300)
+    q, kv, sc, bt, L, want = problem(fmt, h_q, 1, lens, 500, 10, seed=h_q, store_all=True)
+    page, slot = int(bt[0, 650 // 64]), 650 % 64
+    if fmt == "bf16":
+        kv.view(torch.int16)[page, slot, 0, 77] = 0x7FC0
+    else:
+        kv[page, slot, 0, 512:516].view(torch.float32).fill_(float("nan"))
+    if parts:
+        with overrides(num_parts=parts):
+            out, lse = run(q, kv, sc, bt, L, 500, 10)
+    else:
+        out, lse = run(q, kv, sc, bt, L, 500, 10)
+    check(out[1:], lse[1:], tuple(w[1:] for w in want), f"{fmt} {h_q} beside NaN")
+    assert torch.isnan(out[0]).any() and torch.isnan(lse[0]).all()
