@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -54,9 +55,11 @@ constexpr int kMaxDevices = 64;
 uint32_t* g_status_ptr[kMaxDevices];
 int g_sm_count[kMaxDevices];
 int g_pair_capacity[kMaxDevices];  // co-resident CTA pairs of the pair decode kernel
+int g_cluster_capacity[kMaxDevices][4];  // clusters of 1, 2, 4, 8 CTAs resident at once
 std::mutex g_mu;
 
-mla_status device_info(uint32_t** status, int* sm_count, int* pair_capacity = nullptr) {
+mla_status device_info(uint32_t** status, int* sm_count, int* pair_capacity = nullptr,
+                       const int** cluster_capacity = nullptr) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -73,10 +76,13 @@ mla_status device_info(uint32_t** status, int* sm_count, int* pair_capacity = nu
     g_sm_count[dev] = sms;
     const int cap = pair_cluster_capacity();
     g_pair_capacity[dev] = (cap > 0 && cap < sms / 2) ? cap : sms / 2;
+    g_cluster_capacity[dev][0] = sms;
+    for (int i = 1; i < 4; ++i) g_cluster_capacity[dev][i] = window_cluster_capacity(1 << i);
   }
   if (status) *status = g_status_ptr[dev];
   if (sm_count) *sm_count = g_sm_count[dev];
   if (pair_capacity) *pair_capacity = g_pair_capacity[dev];
+  if (cluster_capacity) *cluster_capacity = g_cluster_capacity[dev];
   return MLA_OK;
 }
 
@@ -300,6 +306,29 @@ void fp8_rows_geometry(Geometry* g) {
   const int forced = g_test_num_parts.load();
   g->num_parts = forced > 0 ? forced : g->sm_count / g->row_groups;
   if (g->num_parts < 1) g->num_parts = 1;
+}
+
+// CTAs of the cluster that each problem of a windowed call is given on the
+// single-CTA kernels (mla_cluster.cuh), or 0 for a schedule over all SMs with a
+// merge kernel behind it.  A cluster is taken when all of them are resident at
+// once and the longest problem's share is at most three pages more than an even
+// share of all pages: about what a schedule costs, its segments that start and
+// end inside a problem, and the merge.  `pages` is the longest a window of this
+// call can be, the lengths being on the device.  Measured (us, cluster against
+// schedule): bf16, 16 rows, windows of 512: 4 elements 17.1 against 18.5, 34
+// 20.6 / 29.4, 60 24.8 / 29.7, 150 36.1 / 41.9; of 2048: 34 30.5 / 34.8, but 16
+// elements 29.4 / 26.0 and 100 73 / 63; 64 rows, windows of 512: 60 32.2 / 39.8;
+// FP8, 16 rows, windows of 128: 4 11.0 / 12.9, 60 13.7 / 18.8, 128 20.6 / 24.8.
+int window_cluster(const Geometry& g, int s_q, int window, int sinks, int cols, const int* capacity) {
+  if (g.pair || g_test_num_parts.load() > 0) return 0;
+  const long long reach = static_cast<long long>(window) + s_q + sinks;
+  const long long pages = std::min<long long>(cols, reach / kPageSize + 3);
+  const long long units = static_cast<long long>(g.num_problems) * g.row_groups;
+  for (int i = 3; i >= 0; --i) {
+    if (units > capacity[i] || (1 << i) > pages) continue;
+    return pages * g.sm_count <= (pages * units + 3ll * g.sm_count) << i ? 1 << i : 0;
+  }
+  return 0;
 }
 
 // Pages of all problems of a schedule that a call may have: the sums of a
@@ -905,7 +934,8 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   st = check_workspace(a->workspace, a->workspace_bytes, L.total);
   if (st != MLA_OK) return st;
   uint32_t* status = nullptr;
-  st = device_info(&status, nullptr);
+  const int* clusters = nullptr;
+  st = device_info(&status, nullptr, nullptr, &clusters);
   if (st != MLA_OK) return st;
 
   CUtensorMap tm_q, tm_kv, tm_kv2;
@@ -955,12 +985,14 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   p.kv_scales = a->kv_scales;
   p.fp8_rope_off = a->kv_scales ? kDv : kFp8RopeOffset;
 
+  p.cluster = window_cluster(g, a->s_q, p.window, a->sinks, a->block_table_stride, clusters);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   e = g.pair        ? launch_window_pair(tm_q, tm_kv, tm_kv2, p, s)
       : g.mode == 7 ? launch_decode_fp8(a->q, p, s)
                     : launch_decode(tm_q, tm_kv, p, g.rpc, g.mode, s);
   if (e != cudaSuccess) return cuda_fail(e, "window decode kernel launch");
+  if (p.cluster > 0) return ok();  // (the cluster has merged)
   MergeParams m;
   memset(&m, 0, sizeof m);
   m.own = MergeSide{p.spans, p.o_accum, p.lse_accum, -1};

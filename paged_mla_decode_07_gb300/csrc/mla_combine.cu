@@ -179,13 +179,6 @@ __device__ __forceinline__ Pieces find_pieces(const MergeSide& m, int prob) {
   return Pieces{n, s.x};
 }
 
-// Maximum, NaN if either is: a piece's log-sum-exp is NaN where a key that the row sees is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Merges the pieces of one row with all threads of the block.
 template <class At>
 __device__ __forceinline__ void merge_row_block(int n, At at, __nv_bfloat16* out, float* lse) {

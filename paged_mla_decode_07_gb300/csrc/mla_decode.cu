@@ -50,6 +50,7 @@
 // Every wait is bounded (watchdog); on expiry the CTA records
 // MLA_DEVICE_TIMEOUT, all roles unwind, in-flight copies and MMAs are drained
 // with a bounded wait, and TMEM is freed.
+#include "mla_cluster.cuh"
 #include "mla_device.cuh"
 #include "mla_internal.h"
 #include "mla_schedule.cuh"
@@ -181,6 +182,7 @@ struct Cfg {
   static_assert(kPBytes <= kKvChunkBytes || !kPAlias, "P must fit in the RoPE chunk");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert(schedule_scratch(kMaxProblems) <= kAuxOff, "a schedule is made where the rings will be");
+  static_assert(R * kDv * 4 <= kRopeOff && kMaxCluster * (R + 1) * 4 <= kNB * kKvChunkBytes, "cluster merge in the ring");
   static_assert(R == 16 || R == 32 || R == 64, "rows per CTA");
   static_assert((kAuxOff + kBarBytes) % 16 == 0, "row statistics must be 16-byte aligned");
   static_assert(kTileTokens == kPageSize, "one KV tile is one page");
@@ -440,7 +442,7 @@ __device__ void s_issuer(const Segments<Cfg<R, MODE>::kWindow>& sg, uint32_t tme
   constexpr uint32_t kIdS = idesc_bf16_f32(kTileTokens, R, 0, 0);  // A = K tile (K-major), B = Q (K-major)
   constexpr uint64_t kHiK = smem_desc_hi(16, 1024);
   const int lane = threadIdx.x & 31;
-  const uint32_t kvb = smem_u32(kv), qb = smem_u32(qs);
+  const uint32_t kvb = desc_addr(kv), qb = desc_addr(qs);
   const uint32_t full = smem_u32(bars.full), s_full = smem_u32(bars.s_full), s_empty = smem_u32(bars.s_empty);
   const uint32_t rope_empty = smem_u32(bars.rope_empty);
   const uint32_t q_full = smem_u32(bars.q_full), q_empty = smem_u32(bars.q_empty);
@@ -515,7 +517,7 @@ __device__ void pv_issuer(const Segments<Cfg<R, MODE>::kWindow>& sg, uint32_t tm
   constexpr uint64_t kHiP = smem_desc_hi(16, 1024);
   constexpr uint32_t kPStep = C::kPMnMajor ? (2048 >> 4) : (32 >> 4);  // 16 tokens of P
   const int lane = threadIdx.x & 31;
-  const uint32_t kvb = smem_u32(kv);
+  const uint32_t kvb = desc_addr(kv);
   const uint32_t p_full = smem_u32(bars.p_full), o_empty = smem_u32(bars.o_empty), o_done = smem_u32(bars.o_done);
   const uint32_t o_full = smem_u32(bars.o_full), pair_empty = smem_u32(bars.pair_empty);
   const uint32_t rope_empty = smem_u32(bars.rope_empty);
@@ -1275,7 +1277,7 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments<Cfg<R, MO
     bool final_out;
     int slot;
     if (C::kWindow) {
-      const bool whole = tb == 0 && te == walk.pages;
+      const bool whole = (tb == 0 && te == walk.pages) || p.cluster > 0;
       final_out = whole && !p.always_partial;
       slot = piece_slot(whole, prob, 2 * p.num_parts, part, prob == sg.p0);
     } else {
@@ -1301,7 +1303,10 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments<Cfg<R, MO
           const int r = 16 * q + e;
           if (write_ok && row0 + r < p.rows) {
             const float o = v[e] * inv_s[rb + r];
-            if (final_out) {
+            if (C::kWindow && p.cluster > 0) {
+              // (the ring is free: this is the CTA's only segment)
+              reinterpret_cast<float*>(kv)[(rb + r) * kDv + dv] = o;
+            } else if (final_out) {
               __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
               out[(static_cast<int64_t>(prob) * p.rows + row0 + r) * kDv + dv] = __float2bfloat16_rn(o);
             } else {
@@ -1311,7 +1316,7 @@ __device__ void softmax_epilogue(const DecodeParams& p, const Segments<Cfg<R, MO
         }
       }
     }
-    if (write_ok && tid < RW && row0 + tid < p.rows) {
+    if (write_ok && tid < RW && row0 + tid < p.rows && !(C::kWindow && p.cluster > 0)) {
       if (final_out)
         p.lse[static_cast<int64_t>(prob) * p.rows + row0 + tid] = lse_s[rb + tid];
       else
@@ -1363,8 +1368,10 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int part = blockIdx.x / p.row_groups;
-  const int g = blockIdx.x % p.row_groups;
+  // (clusters: `part` is the problem)
+  const int unit = C::kWindow && p.cluster > 0 ? blockIdx.x / p.cluster : blockIdx.x;
+  const int part = unit / p.row_groups;
+  const int g = unit % p.row_groups;
 
   if (threadIdx.x == 0) {
     mbar_init(bars.q_full, 1);
@@ -1386,8 +1393,11 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
     // copying thread (the 64 threads of a half)
     for (int k = 0; k < C::kNumRaw; ++k) mbar_init(bars.raw_full + k, (C::kIndexed && !C::kFp8) ? 64 : 2);
     *abort_flag = 0;
+    ints[10] = 0;  // (clusters: the rows' place in the ring)
     fence_barrier_init();
   }
+  // (clusters: of a CTA without pages, or one that a wait ran out in)
+  if (C::kWindow && threadIdx.x >= 128 && threadIdx.x < 128 + R) aux[3 * R + threadIdx.x - 128] = kNegInf;
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_kv);
@@ -1421,7 +1431,7 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
   Segments<C::kWindow> sg;
   int split0 = 0;
   if (C::kWindow) {
-    const PartRecord r = inline_schedule(p, part, kTileTokens, smem, g == 0);
+    const PartRecord r = p.cluster > 0 ? cluster_share(p, part) : inline_schedule(p, part, kTileTokens, smem, g == 0);
     sg.p0 = r.p0;
     sg.t0 = r.t0;
     sg.p1 = r.p1;
@@ -1475,6 +1485,15 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
 #ifdef MLA_TRACE
   if (threadIdx.x == 0 && blockIdx.x < 1024) g_mla_cta[3 * blockIdx.x + 1] = global_timer_ns();
 #endif
+  if (C::kWindow && p.cluster > 0) {
+    if (warp < kMergeFrom / 32) {
+      cluster_merge_wait();
+    } else {
+      const int64_t row = static_cast<int64_t>(part) * p.rows + g * R;
+      cluster_merge(p.cluster, ClusterSide{kv, ints + 10, aux + 3 * R}, reinterpret_cast<float*>(smem + C::kRopeOff),
+                    min(R, p.rows - g * R), reinterpret_cast<__nv_bfloat16*>(p.out) + row * kDv, p.lse + row);
+    }
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
@@ -1496,19 +1515,43 @@ cudaError_t launch_one(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const 
       return cudaErrorInvalidConfiguration;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.num_parts * p.row_groups);
+  cfg.gridDim = dim3((p.cluster > 0 ? p.cluster * p.num_problems : p.num_parts) * p.row_groups);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, tm_q, tm_kv, p);
 }
 
 }  // namespace
+
+int window_cluster_capacity(int size) {
+  using C = Cfg<64, kModeWindow>;
+  auto kern = mla_decode_kernel<64, kModeWindow>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  return n;
+}
 
 size_t decode_smem_bytes(int rpc, int mode) {
   switch (mode * 100 + rpc) {

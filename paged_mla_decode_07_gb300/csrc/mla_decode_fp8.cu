@@ -43,6 +43,7 @@
 // arithmetic pipes, measured alone) and 3 on the value side.  Tried: four
 // score warps over whole rows, 5.7k cycles per page (latency); sixteen over one
 // block each, 4.5k (issue slots 65 % busy, DRAM 33 %).
+#include "mla_cluster.cuh"
 #include "mla_device.cuh"
 #include "mla_internal.h"
 #include "mla_schedule.cuh"
@@ -80,7 +81,10 @@ constexpr int kSumOff = kAlphaOff + 2 * kRows * 4;
 constexpr int kInvOff = kSumOff + kRows * 4 * 4;
 constexpr int kFlagOff = kInvOff + kRows * 4;
 constexpr int kAbortOff = kFlagOff + 8 * 4;
-constexpr int kBarOff = (kAbortOff + 4 + 15) / 16 * 16;
+constexpr int kLseOff = kAbortOff + 4;         // [16], clusters
+constexpr int kWhereOff = kLseOff + kRows * 4;  // (clusters) offset of the rows of O
+constexpr int kBarOff = (kWhereOff + 4 + 15) / 16 * 16;
+static_assert(kRows * kDv * 4 <= kStageBytes && kMaxCluster * (kRows + 1) * 4 <= kMaxOff - kSwapOff, "cluster merge");
 constexpr int kNumBars = 2 * kStages + 6;
 constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -412,7 +416,9 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
         const float sum = (v.x + v.y) + (v.z + v.w);
         sts(smem + kInvOff + (r + 8 * half) * 4, sum == 0.f ? 0.f : kOScale / sum);
         const float lse = sum == 0.f ? kNegInf : m + log2f(sum);  // (NaN stays NaN)
-        if (row < p.rows) {
+        if (p.cluster > 0) {
+          sts(smem + kLseOff + (r + 8 * half) * 4, lse);
+        } else if (row < p.rows) {
           if (final_out)
             p.lse[static_cast<int64_t>(prob) * p.rows + row] = lse;
           else if (slot >= 0 && slot < p.max_slots)
@@ -539,7 +545,11 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
     const bool piece_whole = tb == 0 && te == walk.pages;
     const bool final_out = piece_whole && !p.always_partial;
     const int slot = piece_slot(piece_whole, prob, 2 * p.num_parts, part, prob == w.p0);
-    const bool slot_ok = final_out || (slot >= 0 && slot < p.max_slots);
+    const bool slot_ok = final_out || p.cluster > 0 || (slot >= 0 && slot < p.max_slots);
+    // (clusters: rows for the merge go to the stage that the next page would
+    // take; the value warps are at most two pages apart, so none reads it)
+    uint8_t* rows_at = smem + (jt % kStages) * kStageBytes;
+    if (p.cluster > 0 && v == 0 && lane == 0) sts(smem + kWhereOff, (jt % kStages) * kStageBytes);
     if (!slot_ok && lane == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -555,7 +565,11 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
           y[i] = o[d][i][2 * h] * inv;
           y[4 + i] = o[d][i][2 * h + 1] * inv;
         }
-        if (final_out) {
+        if (p.cluster > 0) {
+          uint8_t* dst = rows_at + ((r + 8 * h) * kDv + 64 * v + 8 * c + 32 * d) * 4;
+          sts(dst, make_float4(y[0], y[1], y[2], y[3]));
+          sts(dst + 16, make_float4(y[4], y[5], y[6], y[7]));
+        } else if (final_out) {
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + 32 * d) = make_uint4(
               pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
         } else {
@@ -579,7 +593,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kAbortOff);
   Bars bars{bar, bar + kStages, bar + 2 * kStages, bar + 2 * kStages + 2, bar + 2 * kStages + 4, bar + 2 * kStages + 5};
   const int warp = threadIdx.x >> 5;
-  const int part = blockIdx.x / p.row_groups, g = blockIdx.x % p.row_groups;
+  // (clusters: `part` is the problem)
+  const int unit = p.cluster > 0 ? blockIdx.x / p.cluster : blockIdx.x;
+  const int part = unit / p.row_groups, g = unit % p.row_groups;
+  // (clusters: of a CTA without pages, or one that a wait ran out in)
+  if (threadIdx.x >= 32 && threadIdx.x < 32 + kRows) sts(smem + kLseOff + (threadIdx.x - 32) * 4, kNegInf);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bars.full + i, TOKEN_SCALE ? 1 + 32 : 1);  // the arming arrival and each lane's scale copies
@@ -592,25 +610,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bars.l_full, 2);
     mbar_init(bars.l_empty, 8);
     *abort_flag = 0;
+    *reinterpret_cast<int*>(smem + kWhereOff) = 0;
     fence_barrier_init();
   }
   __syncthreads();
   Watchdog wd{abort_flag, p.status, p.timeout_ns};
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const PartRecord rec = inline_schedule(p, part, kPageSize, smem, g == 0);
+  const PartRecord rec = p.cluster > 0 ? cluster_share(p, part) : inline_schedule(p, part, kPageSize, smem, g == 0);
   const Walk w{rec.p0, rec.t0, rec.p1, rec.t1, p.num_problems};
   if (warp < 4) {
     regs_to<kRegsCtl, kLaunchRegs>();
     if (warp == 0) produce<TOKEN_SCALE>(p, w, smem, bars, wd);
-  } else if (warp < 12) {
-    regs_to<kRegsScore, kLaunchRegs>();
-    scores<TOKEN_SCALE>(q, p, w, g, part, smem, bars, wd);
+    __syncthreads();
+    if (p.cluster > 0) cluster_merge_wait();
   } else {
-    regs_to<kRegsValue, kLaunchRegs>();
-    values<TOKEN_SCALE>(p, w, g, part, smem, bars, wd);
+    if (warp < 12) {
+      regs_to<kRegsScore, kLaunchRegs>();
+      scores<TOKEN_SCALE>(q, p, w, g, part, smem, bars, wd);
+    } else {
+      regs_to<kRegsValue, kLaunchRegs>();
+      values<TOKEN_SCALE>(p, w, g, part, smem, bars, wd);
+    }
+    __syncthreads();
+    if (p.cluster > 0) {
+      const int64_t row = static_cast<int64_t>(part) * p.rows + g * kRows;
+      cluster_merge(p.cluster,
+                    ClusterSide{smem, reinterpret_cast<const int*>(smem + kWhereOff),
+                                reinterpret_cast<const float*>(smem + kLseOff)},
+                    reinterpret_cast<float*>(smem + kSwapOff), min(kRows, p.rows - g * kRows),
+                    static_cast<__nv_bfloat16*>(p.out) + row * kDv, p.lse + row);
+    }
   }
-  __syncthreads();
 }
 
 template <bool TOKEN_SCALE>
@@ -623,15 +654,19 @@ cudaError_t launch(const void* q, const DecodeParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.num_parts * p.row_groups);
+  cfg.gridDim = dim3((p.cluster > 0 ? p.cluster * p.num_problems : p.num_parts) * p.row_groups);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<const __nv_bfloat16*>(q), p);
 }
 

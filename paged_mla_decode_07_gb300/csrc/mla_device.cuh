@@ -337,6 +337,10 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
+// Shared address for a descriptor: in a cluster the upper bits of a shared
+// address name the CTA, and a descriptor has no room for them.
+__device__ __forceinline__ uint32_t desc_addr(const void* p) { return smem_u32(p) & 0x3ffffu; }
+
 // Descriptor of a 128-byte-swizzled operand at shared address `saddr`
 // (< 256 KB): the constant fields plus saddr >> 4; moving the start by
 // d bytes (d a multiple of 16) adds d >> 4.
@@ -433,6 +437,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 // Two fp32 values -> packed bf16x2 (round to nearest even); lo in the low half.
+// Maximum, NaN if either is: a piece's log-sum-exp is NaN where a key that the row sees is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // 32-byte store (32-byte aligned): a whole sector per thread, where threads
 // write rows apart from each other and each instruction costs a pass per row.
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {

@@ -82,6 +82,7 @@ __host__ __device__ inline KeyWalk key_walk(int L, int s_q, int window, int sink
 __host__ __device__ inline bool key_in_walk(int t, int L, int s_q, int window, int sinks) {
   return t < sinks || t > L - s_q - window;
 }
+constexpr int kMaxCluster = 8;       // CTAs of a cluster that share a windowed problem
 constexpr int kMaxWindow = 1 << 30;  // larger windows see every key a cache can hold, as this one does
 
 // Rows per CTA for a problem with `rows` query rows sharing one key set.
@@ -134,6 +135,7 @@ struct DecodeParams {
                               // are), 0: FP8 rows, dequantised
 
   int window, sinks;          // windowed modes: keys before a query token it sees, first keys that stay visible
+  int cluster;                // > 0: each problem's pages over the CTAs of a cluster of this many (mla_cluster.cuh)
   int always_partial;         // every piece writes a partial result, the only piece of a problem too
   // windowed and shared-prefix decode make their schedules themselves (mla_schedule.cuh)
   int tile_cost, overhead;    // schedule costs
@@ -263,6 +265,8 @@ cudaError_t launch_prefix_rows(const uint8_t* kvcache, const float* kv_scales, c
                                uint32_t* status, int sm_count, cudaStream_t stream);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool pdl);
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
+// Clusters of `size` single-CTA windowed kernels that are resident at once
+int window_cluster_capacity(int size);
 size_t decode_smem_bytes(int rpc, int mode);
 cudaError_t launch_fp8_cache_store(const uint16_t* x, int num_tokens, const int32_t* row_offsets,
                                    const int32_t* cache_lengths, int batch, const int32_t* block_table,

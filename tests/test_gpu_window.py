@@ -96,7 +96,11 @@ def test_a_window_over_everything_equals_dense_decode(fmt):
     assert mla.device_status() == 0
     check(*got, ref, f"{fmt} windowed")
     check(*want, ref, f"{fmt} dense")
-    if fmt == "bf16":  # the same kernel over the same pages (FP8 rows have a kernel of their own)
+    if fmt == "bf16":  # the same kernel over the same pages in the same order (FP8 rows have a kernel of their own)
+        with overrides(num_parts=1):
+            got = run(q, kv, sc, bt, L, 1 << 20, 0)
+            sched, ns = mla.get_metadata(L, h_q=16, s_q=2, topk=0, is_fp8=False)
+            want = mla.decode(q, kv, bt, L, SCALE, sched, ns, is_causal=True)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
@@ -242,3 +246,16 @@ def test_a_seen_nan_is_not_lost(fmt, h_q, parts):
         out, lse = run(q, kv, sc, bt, L, 500, 10)
     check(out[1:], lse[1:], tuple(w[1:] for w in want), f"{fmt} {h_q} beside NaN")
     assert torch.isnan(out[0]).any() and torch.isnan(lse[0]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_token"])
+@pytest.mark.parametrize("n,h_q", [(1, 16), (3, 16), (9, 40), (17, 7), (30, 16), (50, 30), (70, 16), (75, 64), (140, 16), (152, 8)])
+def test_batches_that_clusters_share(fmt, n, h_q):
+    """Few and many short windows: every size of cluster, elements without keys and with a single page among them."""
+    lens = [(37 * b * b + 11 * b) % 700 for b in range(n)]
+    lens[n // 2] = 650
+    q, kv, sc, bt, lens, want = problem(fmt, h_q, 1, lens, 300, 6, seed=n)
+    got = run(q, kv, sc, bt, lens, 300, 6)
+    check(*got, want, f"{fmt} {n} elements of {h_q} rows")
+    again = run(q, kv, sc, bt, lens, 300, 6)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
