@@ -11,6 +11,12 @@ code path.  If ``libmla.so`` has not been built, every call raises.
     out, lse = decode(q, kvcache, block_table, cache_seqlens, sm_scale,
                       sched, num_splits, is_causal=..., indices=...)
     out, lse = sparse_prefill(q, kv, indices, sm_scale)
+
+    lens, row_offsets, slots, cursor = assign_pages(cache_lengths, new_tokens, free_pages, free_cursor,
+                                                    block_table, num_tokens)
+    cache_store(latent, rope, slots, kvcache)
+    out, lse = window_decode(q, kvcache, block_table, lens, sm_scale, window=..., sinks=...)
+    out, lse = shared_prefix_decode(q, kvcache, prefix_table, prefix_length, block_table, lens, sm_scale)
 """
 from __future__ import annotations
 

@@ -289,13 +289,20 @@ mla_status prefill_layout(int s_q, int h_q, int topk, Geometry* g, PrefillLayout
   return MLA_OK;
 }
 
-// Dense and windowed decode over an FP8 cache at up to 16 query rows run on the
-// register-level kernel (mla_decode_fp8.cu), more rows on the tcgen05 ones.
-// Measured (us, windows of 2048 + 64 keys): 16 rows 54.6 against 65.8 at 64
-// elements and 21.2 against 24.4 at 8; 32 rows, which it takes as two groups,
-// 85.8 against 74.8 and 21.8 against 27.6; 64 rows 149 against 78.
-constexpr int kFp8RowsMax = 16;
-void fp8_rows_geometry(Geometry* g) {
+// The register-level kernel (mla_decode_rows.cu) takes 16 query rows per CTA and
+// reads the keys again for every 16: it runs windowed decode at up to 16 rows,
+// and at more where all groups together have few pages for each SM to read.
+// Measured (us, against the tcgen05 kernels): bf16, 128 elements x 16 rows x 4160
+// keys 110.1 / 112.0; 4 x 16 x 512 keys 12.8 / 17.2; 32 rows, 4 x 512 keys 12.9 /
+// 20.5, 30 x 512 (3.9 pages an SM) 18.5 / 24.7, 30 x 2048 (13.4) 39.0 / 35.1; 64
+// rows, 16 x 512 (4.2) 17.8 / 24.0, 30 x 512 (7.9) 28.0 / 24.7.  FP8, 128 x 16 x
+// 4160 keys 132 / 175; 64 rows, 16 x 512 19.5 / 24.0, 30 x 512 31.5 / 25.4.
+constexpr int kRowsKernelRows = 16, kRowsKernelPages = 5;
+bool rows_kernel(const Geometry& g, long long pages) {
+  return g.rows <= kRowsKernelRows ||
+         pages * g.num_problems * ((g.rows + 15) / 16) <= static_cast<long long>(kRowsKernelPages) * g.sm_count;
+}
+void rows_geometry(Geometry* g) {
   g->rpc = 16;
   g->row_groups = (g->rows + 15) / 16;
   g->pair = 0;
@@ -313,16 +320,13 @@ void fp8_rows_geometry(Geometry* g) {
 // merge kernel behind it.  A cluster is taken when all of them are resident at
 // once and the longest problem's share is at most three pages more than an even
 // share of all pages: about what a schedule costs, its segments that start and
-// end inside a problem, and the merge.  `pages` is the longest a window of this
-// call can be, the lengths being on the device.  Measured (us, cluster against
-// schedule): bf16, 16 rows, windows of 512: 4 elements 17.1 against 18.5, 34
-// 20.6 / 29.4, 60 24.8 / 29.7, 150 36.1 / 41.9; of 2048: 34 30.5 / 34.8, but 16
-// elements 29.4 / 26.0 and 100 73 / 63; 64 rows, windows of 512: 60 32.2 / 39.8;
-// FP8, 16 rows, windows of 128: 4 11.0 / 12.9, 60 13.7 / 18.8, 128 20.6 / 24.8.
-int window_cluster(const Geometry& g, int s_q, int window, int sinks, int cols, const int* capacity) {
+// end inside a problem, and the merge.  Measured (us, cluster against schedule):
+// bf16 on the tcgen05 kernel, 16 rows, windows of 512: 34 elements 20.6 / 29.4,
+// 60 24.8 / 29.7, 150 36.1 / 41.9; of 2048: 34 30.5 / 34.8, but 16 elements 29.4
+// / 26.0 and 100 73 / 63; 64 rows, windows of 512: 60 32.2 / 39.8; FP8, 16 rows,
+// windows of 128: 4 11.0 / 12.9, 60 13.7 / 18.8, 128 20.6 / 24.8.
+int window_cluster(const Geometry& g, long long pages, const int* capacity) {
   if (g.pair || g_test_num_parts.load() > 0) return 0;
-  const long long reach = static_cast<long long>(window) + s_q + sinks;
-  const long long pages = std::min<long long>(cols, reach / kPageSize + 3);
   const long long units = static_cast<long long>(g.num_problems) * g.row_groups;
   for (int i = 3; i >= 0; --i) {
     if (units > capacity[i] || (1 << i) > pages) continue;
@@ -335,18 +339,20 @@ int window_cluster(const Geometry& g, int s_q, int window, int sinks, int cols, 
 // schedule made in the decode kernel have 31 bits for them.
 constexpr long long kMaxTilesTotal = 1ll << 28;
 
-// Windowed decode: spans of the problems and split-KV partials.
+// Windowed decode: spans of the problems and split-KV partials.  `pages`: the
+// longest a window of the call can be, the lengths being on the device (the
+// layout is largest where that is too long for the register-level kernel).
 struct WindowLayout {
   size_t o_accum, lse_accum, total;  // (the spans come first)
 };
-mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, Geometry* g, WindowLayout* L) {
+mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, long long pages, Geometry* g, WindowLayout* L) {
   mla_status st = geometry(batch, h_q, s_q, 0, is_fp8, g);
   if (st != MLA_OK) return st;
   g->mode = is_fp8 ? 5 : 4;
   // a segment on a CTA pair costs about four of its tiles to start and to end
   // (64 elements x 128 rows, 33 pages: 70.7 us against 73.0 at one and a half)
   if (g->pair) g->overhead = 32;
-  if (is_fp8 && g->rows <= kFp8RowsMax) fp8_rows_geometry(g);
+  if (rows_kernel(*g, pages)) rows_geometry(g);
   // two slots per part: the problems it starts and ends inside of
   const size_t slots = 2 * static_cast<size_t>(g->num_parts);
   L->o_accum = align256(static_cast<size_t>(g->num_problems) * 2 * sizeof(int32_t));
@@ -372,8 +378,8 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   st = device_info(nullptr, nullptr, &pairs);
   if (st != MLA_OK) return st;
   const long long rows = static_cast<long long>(batch) * L->own.rows;
-  if (is_fp8 && L->own.rows <= kFp8RowsMax) {
-    fp8_rows_geometry(&L->own);
+  if (is_fp8 && L->own.rows <= kRowsKernelRows) {
+    rows_geometry(&L->own);
   } else if (is_fp8) {
     // the windowed mode with sinks that are every key
     L->own.mode = 5;
@@ -914,7 +920,7 @@ mla_status mla_window_decode_workspace_size(int batch, int h_q, int s_q, int is_
   if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes is NULL");
   Geometry g{};
   WindowLayout L{};
-  mla_status st = window_layout(batch, h_q, s_q, is_fp8, &g, &L);
+  mla_status st = window_layout(batch, h_q, s_q, is_fp8, kMaxPages, &g, &L);
   if (st != MLA_OK) return st;
   *bytes = L.total;
   return ok();
@@ -929,7 +935,9 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   if (a->sinks < 0) return fail(MLA_ERR_INVALID_ARG, "sinks must be >= 0 (got %d)", a->sinks);
   Geometry g{};
   WindowLayout L{};
-  st = window_layout(a->batch, a->h_q, a->s_q, a->is_fp8, &g, &L);
+  const long long reach = std::min<long long>(a->window, kMaxWindow) + a->s_q + a->sinks;
+  const long long pages = std::min<long long>(a->block_table_stride, reach / kPageSize + 3);
+  st = window_layout(a->batch, a->h_q, a->s_q, a->is_fp8, pages, &g, &L);
   if (st != MLA_OK) return st;
   st = check_workspace(a->workspace, a->workspace_bytes, L.total);
   if (st != MLA_OK) return st;
@@ -943,7 +951,10 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   const long long cache_rows = static_cast<long long>(a->num_pages) * kPageSize;
   if (g.pair) {
     st = encode_pair_maps(a->q, qrows, a->kvcache, cache_rows, &tm_q, &tm_kv, &tm_kv2);
-  } else if (g.mode != 7) {
+  } else if (g.mode == 7) {
+    memset(&tm_kv, 0, sizeof tm_kv);
+    if (!a->is_fp8) st = encode_rows_map(&tm_kv, a->kvcache, cache_rows, kPageSize / 2, "kvcache");
+  } else {
     st = encode_rows_map(&tm_q, a->q, qrows, g.rpc, "q");
     if (st == MLA_OK)
       st = a->is_fp8 ? encode_byte_rows_map(&tm_kv, a->kvcache, cache_rows, a->kv_scales ? 640 : kFp8RowBytes, 32)
@@ -985,11 +996,11 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   p.kv_scales = a->kv_scales;
   p.fp8_rope_off = a->kv_scales ? kDv : kFp8RopeOffset;
 
-  p.cluster = window_cluster(g, a->s_q, p.window, a->sinks, a->block_table_stride, clusters);
+  p.cluster = window_cluster(g, pages, clusters);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   e = g.pair        ? launch_window_pair(tm_q, tm_kv, tm_kv2, p, s)
-      : g.mode == 7 ? launch_decode_fp8(a->q, p, s)
+      : g.mode == 7 ? launch_decode_rows(tm_kv, a->q, p, a->is_fp8, s)
                     : launch_decode(tm_q, tm_kv, p, g.rpc, g.mode, s);
   if (e != cudaSuccess) return cuda_fail(e, "window decode kernel launch");
   if (p.cluster > 0) return ok();  // (the cluster has merged)
@@ -1122,7 +1133,7 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
     o.evict_first = L.own.row_groups == 1 ? 1 : 0;
     o.kv_scales = a->kv_scales;
     o.fp8_rope_off = a->kv_scales ? kDv : kFp8RopeOffset;
-    e = L.own.mode == 7 ? launch_decode_fp8(a->q, o, s)
+    e = L.own.mode == 7 ? launch_decode_rows(tm_q, a->q, o, true, s)
                         : launch_decode(tm_own_q, tm_own_kv, o, L.own.rpc, L.own.mode, s);
     if (e != cudaSuccess) return cuda_fail(e, "decode kernel launch");
   }

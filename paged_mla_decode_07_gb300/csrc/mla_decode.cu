@@ -1567,10 +1567,8 @@ size_t decode_smem_bytes(int rpc, int mode) {
     case 316: return Cfg<16, kModeSparseBf16>::kSmemBytes;
     case 332: return Cfg<32, kModeSparseBf16>::kSmemBytes;
     case 364: return Cfg<64, kModeSparseBf16>::kSmemBytes;
-    case 416: return Cfg<16, kModeWindow>::kSmemBytes;
     case 432: return Cfg<32, kModeWindow>::kSmemBytes;
     case 464: return Cfg<64, kModeWindow>::kSmemBytes;
-    case 516: return Cfg<16, kModeWindowFp8>::kSmemBytes;
     case 532: return Cfg<32, kModeWindowFp8>::kSmemBytes;
     case 564: return Cfg<64, kModeWindowFp8>::kSmemBytes;
   }
@@ -1592,10 +1590,8 @@ cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, con
     case 316: return launch_one<16, kModeSparseBf16>(tm_q, tm_kv, p, stream);
     case 332: return launch_one<32, kModeSparseBf16>(tm_q, tm_kv, p, stream);
     case 364: return launch_one<64, kModeSparseBf16>(tm_q, tm_kv, p, stream);
-    case 416: return launch_one<16, kModeWindow>(tm_q, tm_kv, p, stream);
     case 432: return launch_one<32, kModeWindow>(tm_q, tm_kv, p, stream);
     case 464: return launch_one<64, kModeWindow>(tm_q, tm_kv, p, stream);
-    case 516: return launch_one<16, kModeWindowFp8>(tm_q, tm_kv, p, stream);
     case 532: return launch_one<32, kModeWindowFp8>(tm_q, tm_kv, p, stream);
     case 564: return launch_one<64, kModeWindowFp8>(tm_q, tm_kv, p, stream);
   }

@@ -1,14 +1,21 @@
-// K9 — windowed decode over an FP8 cache, 16 query rows per CTA, on
-// register-level matrix instructions.
+// K9 — windowed decode, 16 query rows per CTA, on register-level matrix
+// instructions, over the bf16 cache and both FP8 caches.
 //
-// The same computation as the FP8 modes of the single-CTA kernel
-// (mla_decode.cu), but the FP8 rows are never written back to shared memory
-// as bf16: that kernel's load -> dequantise -> multiply chain over one set of
-// slots takes ~5.1k cycles per 64-token page, where a page's bytes at the
-// card's copy rate take ~1.9k.  Here the codes go from shared memory straight
-// into the operand registers of mma.sync:
-//     S[r, t] = Q[r, :] . K[t, :],      K[t, d] = bf16_rn(c[t, d] s_b[t])
-//     O[r, d] = sum_t (P[r, t] s_b[t]) c[t, d]          (d in block b)
+// Operands go from shared memory straight into the registers of mma.sync:
+//     S[r, t] = Q[r, :] . K[t, :]
+//     O[r, d] = sum_t P[r, t] V[t, d]
+// At 16 rows the legacy matrix instructions (8 cycles for 16 x 8 x 16 per SM
+// quarter, measured) need 544 instructions per page, 1.1k cycles, a third of
+// what a bf16 page's bytes take; and no TMEM, descriptors, proxy fences or
+// issuing warps stand between a copy and its results, which is what the
+// smallest calls wait for.  More rows run as groups of 16 that each read the
+// pages (from L2).
+//
+// FP8 rows are never written back to shared memory as bf16 (the tcgen05 kernel's
+// load -> dequantise -> multiply chain over one set of slots takes ~5.1k cycles
+// per page, where a page's bytes at the card's copy rate take ~1.9k):
+//     K[t, d] = bf16_rn(c[t, d] s_b[t])                 (d in block b)
+//     O[r, d] = sum_t (P[r, t] s_b[t]) c[t, d]
 // Keys are dequantised in registers, as the format defines them.  Values are
 // not: their scale joins the probability before it is rounded to bf16 and the
 // codes are exact in bf16.  The product keeps one of the two roundings that a
@@ -17,32 +24,28 @@
 // tile is stored with scale 1, its neighbours with 1e-6), and P s of the small
 // ones has to keep its bits.
 //
-// At 16 rows the legacy matrix instructions (8 cycles for 16 x 8 x 16 per SM
-// quarter, measured) need 544 instructions per page, 1.1k cycles, so the
-// page's bytes remain the bound; operands in registers need no shared-memory
-// round trip, no TMEM and no cross-proxy fences.  More rows run as groups of
-// 16 that each read the pages (from L2).
-//
 // Roles (640 threads, registers split by setmaxnreg):
-//   warp 0       producer: a page is one bulk copy of its 64 whole rows,
-//                per-token scales come by cp.async
-//   warps 4-11   scores and softmax: warp w owns 16 tokens of the page and two
-//                of the four 128-dim blocks (and half of the RoPE dims), with
-//                its half of Q as operand fragments in registers; the two
-//                halves of a sum meet through shared memory, each warp taking
-//                eight of the sixteen rows on
+//   warp 0       producer: an FP8 page is one bulk copy of its 64 whole rows
+//                (per-token scales come by cp.async), half a bf16 page nine
+//                TMA boxes
+//   warps 4-11   scores and softmax: warp w owns 16 tokens of the page and half
+//                of the dims (FP8: two of the four 128-dim blocks and half of
+//                the RoPE dims), with its half of Q as operand fragments in
+//                registers; the two halves of a sum meet through shared memory,
+//                each warp taking eight of the sixteen rows on
 //   warps 12-19  values: warp w owns 64 value dims of all tokens, its 16 x 64
 //                part of O in registers
 // Score and value warps work on different pages at the same time; P (fp32)
 // passes between them through a double buffer.
 //
-// Measured: 128 elements x 4160 keys, 133 us (2.5 TB/s, 36 % of the copy
-// rate; the tcgen05 kernel 175 us): 4.3k cycles per page.  Bound by
-// instruction issue: ~3k warp instructions per page and SM quarter, of
-// which two codes cost 6-8 on the score side (9 cycles of the conversion and
-// arithmetic pipes, measured alone) and 3 on the value side.  Tried: four
-// score warps over whole rows, 5.7k cycles per page (latency); sixteen over one
-// block each, 4.5k (issue slots 65 % busy, DRAM 33 %).
+// Measured, 128 elements x 4160 keys: bf16 110 us (5.2 TB/s, 76 % of the copy
+// rate; the tcgen05 kernel 112), FP8 132 us (2.5 TB/s, 37 %; 175): 4.3k cycles
+// per page.  FP8 is bound by instruction issue: ~3k warp instructions per page
+// and SM quarter, of which two codes cost 6-8 on the score side (9 cycles of the
+// conversion and arithmetic pipes, measured alone) and 3 on the value side.
+// Tried: four score warps over whole rows, 5.7k cycles per page (latency);
+// sixteen over one block each, 4.5k (issue slots 65 % busy, DRAM 33 %).
+// 4 elements x 512 keys: bf16 12.4 us, FP8 13.0.
 #include "mla_cluster.cuh"
 #include "mla_device.cuh"
 #include "mla_internal.h"
@@ -53,20 +56,34 @@ namespace {
 
 constexpr int kRows = 16;
 constexpr int kStages = 5;
-// A stage holds the page's rows as they lie in the cache, 656 bytes each, or
-// 640 bytes each and the 64 scales behind them.  656 bytes are 4 words past a
-// multiple of the banks' width, so the operand reads below (eight rows at one
-// 16-byte column, four rows at eight 4-byte ones) touch every bank once; rows
-// of 640 bytes cost two and four passes instead.
-template <bool TOKEN_SCALE>
+// Row formats: 656 bytes with four scales, 640 bytes and a scale per token
+// elsewhere, 576 bf16.
+constexpr int kTile = 0, kToken = 1, kBf16 = 2;
+// A stage holds a unit of a page.  FP8: all its rows as they lie in the cache
+// (with the 64 scales behind them); 656 bytes are 4 words past a multiple of
+// the banks' width, so the operand reads below (eight rows at one 16-byte
+// column, four rows at eight 4-byte ones) touch every bank once; rows of 640
+// bytes cost two and four passes instead.  bf16: half of its rows, so that two
+// and a half pages are in flight, as nine chunks of [32 rows][64 dims] with the
+// 128-byte swizzle.  (Rows copied one by one to places 1168 bytes apart: 152 us
+// where these take 110, 128 elements x 4160 keys.)
+template <int FMT>
 struct Rows {
-  static constexpr int kRow = TOKEN_SCALE ? 640 : kFp8RowBytes;
-  static constexpr int kRope = TOKEN_SCALE ? kDv : kFp8RopeOffset;
-  static constexpr int kPage = kPageSize * kRow;
+  static constexpr int kUnits = FMT == kBf16 ? 2 : 1;  // units of a page
+  static constexpr int kTokens = kPageSize / kUnits;
+  static constexpr int kRow = FMT == kBf16 ? 2 * kDqk : FMT == kToken ? 640 : kFp8RowBytes;
+  static constexpr int kBytes = kTokens * kRow;
+  static constexpr int kReaders = 8 / kUnits;  // score warps that read a unit
 };
-constexpr int kScaleOff = Rows<true>::kPage;  // per-token scales
-constexpr int kStageBytes = Rows<false>::kPage;
-static_assert(kScaleOff + 4 * kPageSize <= kStageBytes && kStageBytes % 128 == 0, "stage layout");
+// bf16: dims 8 d .. 8 d + 7 of row t of a stage
+__device__ __forceinline__ uint32_t dims_at(int t, int d) {
+  return (d >> 3) * (Rows<kBf16>::kTokens * 128) + t * 128 + (((d ^ t) & 7) << 4);
+}
+constexpr int kScaleOff = Rows<kToken>::kBytes;  // per-token scales
+constexpr int kStageBytes = Rows<kTile>::kBytes;
+static_assert(kScaleOff + 4 * kPageSize <= kStageBytes && kStageBytes % 128 == 0 &&
+                  Rows<kBf16>::kBytes <= kStageBytes && kStageBytes % 1024 == 0,
+              "stage layout");
 constexpr int kPStride = 72;                 // floats per row of P: 8 rows x 4 lane groups on distinct banks
 constexpr int kPOff = kStages * kStageBytes;
 constexpr int kPBytes = kRows * kPStride * 4;
@@ -129,6 +146,14 @@ template <class T>
 __device__ __forceinline__ void sts(uint8_t* p, T v) {
   *reinterpret_cast<T*>(p) = v;
 }
+// Four 8 x 8 blocks of 16-bit values, transposed: lane l names the 16 bytes of
+// row l % 8 of block l / 8 and gets column l / 4 of each, rows 2 (l % 4) and the next.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&v)[4], uint32_t addr) {
+  asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(addr)
+      : "memory");
+}
 // What a CTA walks: problems p0..p1 of its part and, in each, a run of pages.
 struct Walk {
   int p0, t0, p1, t1, np;
@@ -183,13 +208,13 @@ __device__ __forceinline__ void bulk_load(uint8_t* dst, const void* src, uint32_
 // ---------------------------------------------------------------------------
 // producer (one warp)
 // ---------------------------------------------------------------------------
-template <bool TOKEN_SCALE>
-__device__ void produce(const DecodeParams& p, const Walk& w, uint8_t* smem, const Bars& bars,
+template <int FMT>
+__device__ void produce(const CUtensorMap* tm_kv, const DecodeParams& p, const Walk& w, uint8_t* smem, const Bars& bars,
                         const Watchdog& wd) {
   const int lane = threadIdx.x & 31;
   const uint64_t pol = p.evict_first ? l2_policy_evict_first() : l2_policy_evict_normal();
   volatile int* flags = reinterpret_cast<volatile int*>(smem + kFlagOff);
-  int jt = 0;
+  int ut = 0;  // units
   for (int prob = w.p0; prob <= w.last(); ++prob) {
     const int L = p.cache_seqlens[prob];
     const KeyWalk k = walk_of(p, L);
@@ -197,34 +222,43 @@ __device__ void produce(const DecodeParams& p, const Walk& w, uint8_t* smem, con
     range(w, prob, k, tb, te);
     const int32_t* bt = p.block_table + static_cast<int64_t>(prob) * p.block_table_stride;
     int ids = -1;  // page ids of pages j0 .. j0 + 31 of the walk, one per lane
-    for (int j = tb; j < te; ++j, ++jt) {
+    for (int j = tb; j < te; ++j) {
       if (((j - tb) & 31) == 0) {
         const int lp = j + lane < te ? k.page(j + lane) : -1;
         ids = lp >= 0 && lp < p.block_table_stride ? __ldg(bt + lp) : -1;
       }
       const int pg = __shfl_sync(0xffffffffu, ids, (j - tb) & 31);
       const bool ok = pg >= 0 && pg < p.num_pages;
-      const int s = jt % kStages;
-      if (jt >= kStages && !wait_warp(bars.empty + s, ((jt / kStages) - 1) & 1, wd)) goto drain;
-      uint8_t* dst = smem + s * kStageBytes;
-      if (lane == 0) {
-        if (!ok) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
-        flags[s] = ok ? 1 : 0;
-        // (an unusable page's stage keeps what it holds: all its tokens are masked)
-        mbar_arrive_expect_tx(bars.full + s, ok ? Rows<TOKEN_SCALE>::kPage : 0);
-        if (ok)
-          bulk_load(dst, p.kv_fp8 + static_cast<int64_t>(pg) * Rows<TOKEN_SCALE>::kPage, Rows<TOKEN_SCALE>::kPage,
-                    bars.full + s, pol);
-      }
-      if (TOKEN_SCALE) {
-        if (ok) {
-          const float* src = p.kv_scales + static_cast<int64_t>(pg) * kPageSize;
-          cp_async4(smem_u32(dst + kScaleOff) + 4 * lane, src + lane);
-          cp_async4(smem_u32(dst + kScaleOff) + 4 * (lane + 32), src + lane + 32);
+      using R = Rows<FMT>;
+#pragma unroll 1
+      for (int unit = 0; unit < R::kUnits; ++unit, ++ut) {
+        const int s = ut % kStages;
+        if (ut >= kStages && !wait_warp(bars.empty + s, ((ut / kStages) - 1) & 1, wd)) goto drain;
+        uint8_t* dst = smem + s * kStageBytes;
+        const uint8_t* src = p.kv_fp8 + static_cast<int64_t>(ok ? pg : 0) * (R::kUnits * R::kBytes) + unit * R::kBytes;
+        if (lane == 0) {
+          if (!ok) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
+          flags[s] = ok ? 1 : 0;
+          // (an unusable page's stage keeps what it holds: all its tokens are masked)
+          mbar_arrive_expect_tx(bars.full + s, ok ? R::kBytes : 0);
+          if (ok && FMT != kBf16) bulk_load(dst, src, R::kBytes, bars.full + s, pol);
         }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bars.full + s)) : "memory");
+        if constexpr (FMT == kBf16) {
+          __syncwarp();
+          if (ok && lane < kNumChunks)
+            tma_load_3d(dst + lane * (R::kTokens * 128), tm_kv, bars.full + s, 0, lane,
+                        pg * kPageSize + unit * R::kTokens, pol);
+        }
+        if (FMT == kToken) {
+          if (ok) {
+            const float* sc = p.kv_scales + static_cast<int64_t>(pg) * kPageSize;
+            cp_async4(smem_u32(dst + kScaleOff) + 4 * lane, sc + lane);
+            cp_async4(smem_u32(dst + kScaleOff) + 4 * (lane + 32), sc + lane + 32);
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bars.full + s)) : "memory");
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
   }
 drain:
@@ -232,7 +266,7 @@ drain:
   // (bounded) for the latest phase of each stage
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (lane == 0) {
-    for (int i = jt > kStages ? jt - kStages : 0; i < jt; ++i) {
+    for (int i = ut > kStages ? ut - kStages : 0; i < ut; ++i) {
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(bars.full + i % kStages, (i / kStages) & 1))
         if (global_timer_ns() - t0 > wd.limit_ns) break;
@@ -248,7 +282,7 @@ drain:
 // (lane % 4) holds k = 2c, 2c + 1, 2c + 8, 2c + 9.  The order of the dims
 // within a sum is free, so lane group c takes dims [32 c, 32 c + 32) of a
 // block, four per instruction: 16-byte reads of consecutive codes.
-template <bool TOKEN_SCALE>
+template <int FMT>
 __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& p, const Walk& w, int g, int part,
                        uint8_t* smem, const Bars& bars, const Watchdog& wd) {
   const int lane = threadIdx.x & 31, sw = (threadIdx.x >> 5) - 4;
@@ -279,8 +313,11 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
           reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(prob) * p.rows + (real ? qr : 0)) * kDqk);
 #pragma unroll
       for (int k = 0; k < 9; ++k) {
-        // two instructions' worth: block 2 half + k / 4, dims 32 c + 8 (k % 4) of it; the last RoPE dims 16 c + 8 half
-        const int at = k < 8 ? 16 * (2 * half + (k >> 2)) + 4 * c + (k & 3) : 64 + 2 * c + half;
+        // two instructions' worth.  FP8: block 2 half + k / 4, dims 32 c + 8 (k % 4) of it; the last RoPE dims 16 c +
+        // 8 half.  bf16: of this half's 288 dims 64 (k / 2) + 16 c + 8 (k % 2); the last 256 + 8 c
+        const int at = FMT == kBf16 ? 36 * half + (k < 8 ? 8 * (k >> 1) + 2 * c + (k & 1) : 32 + c)
+                       : k < 8      ? 16 * (2 * half + (k >> 2)) + 4 * c + (k & 3)
+                                    : 64 + 2 * c + half;
         const uint4 v = real ? __ldg(src + at) : make_uint4(0, 0, 0, 0);
         qf[2 * k][h] = v.x;
         qf[2 * k][h + 2] = v.y;
@@ -293,17 +330,20 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
     float m = kNegInf, l = 0.f;
 
     for (int j = tb; j < te; ++j, ++jt) {
-      const int s = jt % kStages, buf = jt & 1;
-      bool ok = wait_warp(bars.full + s, (jt / kStages) & 1, wd);
+      using R = Rows<FMT>;
+      const int ut = R::kUnits * jt + (16 * tg) / R::kTokens;  // the unit that holds the token group
+      const int s = ut % kStages, buf = jt & 1;
+      bool ok = wait_warp(bars.full + s, (ut / kStages) & 1, wd);
       const uint8_t* stage = smem + s * kStageBytes;
-      const uint8_t* keys = stage + (16 * tg + r) * Rows<TOKEN_SCALE>::kRow;  // operand column r; the next group 8 rows on
+      // operand column r; the next group 8 rows on
+      const uint8_t* keys = stage + (16 * tg % R::kTokens + r) * R::kRow;
       // scales of this lane's two key tokens for the two blocks
       float sc[2][2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        if (TOKEN_SCALE) {
+        if (FMT == kToken) {
           sc[n][0] = sc[n][1] = lds<float>(stage + kScaleOff + 4 * (16 * tg + 8 * n + r));
-        } else {
+        } else if (FMT == kTile) {
           const float2 v = lds<float2>(keys + 8 * n * kFp8RowBytes + kFp8ScaleOffset + 8 * half);
           sc[n][0] = v.x;
           sc[n][1] = v.y;
@@ -316,12 +356,23 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[n][e] = y[n][e] = 0.f;
+      if constexpr (FMT == kBf16) {
+#pragma unroll
+        for (int k = 0; k < 9; ++k)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int d = 36 * half + (k < 8 ? 8 * (k >> 1) + 2 * c + (k & 1) : 32 + c);
+            const uint4 v = lds<uint4>(stage + dims_at(16 * (tg & 1) + 8 * n + r, d));
+            mma_bf16(x[n], qf[2 * k], v.x, v.y);
+            mma_bf16(y[n], qf[2 * k + 1], v.z, v.w);
+          }
+      } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // block 2 half + k / 2, 16 codes k % 2 of this lane's 32
         uint4 v[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          v[n] = lds<uint4>(keys + 8 * n * Rows<TOKEN_SCALE>::kRow + 128 * (2 * half + (k >> 1)) + 32 * c + 16 * (k & 1));
+          v[n] = lds<uint4>(keys + 8 * n * R::kRow + 128 * (2 * half + (k >> 1)) + 32 * c + 16 * (k & 1));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -334,9 +385,10 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const uint4 v =
-            lds<uint4>(keys + 8 * n * Rows<TOKEN_SCALE>::kRow + Rows<TOKEN_SCALE>::kRope + 32 * c + 16 * half);
+            lds<uint4>(keys + 8 * n * R::kRow + (FMT == kToken ? kDv : kFp8RopeOffset) + 32 * c + 16 * half);
         mma_bf16(x[n], qf[16], v.x, v.y);
         mma_bf16(y[n], qf[17], v.z, v.w);
+      }
       }
       const bool page_ok = flags[s] != 0;
       // the other half's rows go to its warp of this token group, this half's come from there.  (A
@@ -414,7 +466,7 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
         const int slot = piece_slot(whole, prob, 2 * p.num_parts, part, prob == w.p0);
         const float4 v = lds<float4>(smem + kSumOff + (r + 8 * half) * 16);
         const float sum = (v.x + v.y) + (v.z + v.w);
-        sts(smem + kInvOff + (r + 8 * half) * 4, sum == 0.f ? 0.f : kOScale / sum);
+        sts(smem + kInvOff + (r + 8 * half) * 4, sum == 0.f ? 0.f : (FMT == kBf16 ? 1.f : kOScale) / sum);
         const float lse = sum == 0.f ? kNegInf : m + log2f(sum);  // (NaN stays NaN)
         if (p.cluster > 0) {
           sts(smem + kLseOff + (r + 8 * half) * 4, lse);
@@ -439,7 +491,7 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
 // reads four codes at dims 32 g + 4 r of tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a
 // 16-token step: column r of the instruction for code i is dim 32 g + 4 r + i, so
 // a lane ends with dims 32 g + 8 c .. + 7 of rows r and r + 8: 16-byte stores.
-template <bool TOKEN_SCALE>
+template <int FMT>
 __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, uint8_t* smem, const Bars& bars,
                        const Watchdog& wd) {
   const int lane = threadIdx.x & 31, v = (threadIdx.x >> 5) - 12;
@@ -461,8 +513,11 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[a][i][e] = 0.f;
     for (int j = tb; j < te; ++j, ++jt) {
-      const int s = jt % kStages, buf = jt & 1;
-      if (!wait_warp(bars.full + s, (jt / kStages) & 1, wd)) return;
+      using R = Rows<FMT>;
+      const int ut = R::kUnits * jt, s = ut % kStages, buf = jt & 1;
+      const int s1 = (ut + R::kUnits - 1) % kStages;  // the page's last unit
+      if (!wait_warp(bars.full + s, (ut / kStages) & 1, wd)) return;
+      if (R::kUnits > 1 && !wait_warp(bars.full + s1, ((ut + 1) / kStages) & 1, wd)) return;
       const uint8_t* stage = smem + s * kStageBytes;
       const int lp = walk.page(j);
       const bool page_ok = flags[s] != 0;
@@ -490,11 +545,11 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
         x[1] = lds<float2>(pa + ((r + 8) * kPStride + t) * 4);
         x[2] = lds<float2>(pa + (r * kPStride + t + 8) * 4);
         x[3] = lds<float2>(pa + ((r + 8) * kPStride + t + 8) * 4);
-        float2 sl, sh;
-        if (TOKEN_SCALE) {
+        float2 sl = {}, sh = {};
+        if (FMT == kToken) {
           sl = lds<float2>(stage + kScaleOff + 4 * t);
           sh = lds<float2>(stage + kScaleOff + 4 * (t + 8));
-        } else {
+        } else if (FMT == kTile) {
           const uint8_t* row = stage + t * kFp8RowBytes + kFp8ScaleOffset + 4 * blk;
           sl = make_float2(lds<float>(row), lds<float>(row + kFp8RowBytes));
           sh = make_float2(lds<float>(row + 8 * kFp8RowBytes), lds<float>(row + 9 * kFp8RowBytes));
@@ -510,32 +565,55 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
           if (!k8) sh.x = 0.f;
           if (!k9) sh.y = 0.f;
         }
-        sl.x *= kPScale;
-        sl.y *= kPScale;
-        sh.x *= kPScale;
-        sh.y *= kPScale;
-        const uint32_t a[4] = {pack_bf16x2(x[0].x * sl.x, x[0].y * sl.y), pack_bf16x2(x[1].x * sl.x, x[1].y * sl.y),
-                               pack_bf16x2(x[2].x * sh.x, x[2].y * sh.y), pack_bf16x2(x[3].x * sh.x, x[3].y * sh.y)};
-        constexpr int kRow = Rows<TOKEN_SCALE>::kRow;
-        const uint8_t* codes = stage + t * kRow + 64 * v + 4 * r;
+        if constexpr (FMT == kBf16) {
+          const uint32_t a[4] = {pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                                 pack_bf16x2(x[3].x, x[3].y)};
+          // lane l names row l % 16 of the step's tokens (or of the 8 dims further on, from lane 16)
+          const uint32_t rows = smem_u32(smem + (kk < 2 ? s : s1) * kStageBytes);
+          const uint32_t m0 = (k0 ? 0xffffu : 0u) | (k1 ? 0xffff0000u : 0u);
+          const uint32_t m8 = (k8 ? 0xffffu : 0u) | (k9 ? 0xffff0000u : 0u);
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          uint32_t w0 = lds<uint32_t>(codes + 32 * d), w1 = lds<uint32_t>(codes + 32 * d + kRow);
-          uint32_t w8 = lds<uint32_t>(codes + 32 * d + 8 * kRow), w9 = lds<uint32_t>(codes + 32 * d + 9 * kRow);
-          if (!whole) {
-            if (!k0) w0 = 0;
-            if (!k1) w1 = 0;
-            if (!k8) w8 = 0;
-            if (!k9) w9 = 0;
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b[4];
+            ldmatrix_x4_trans(b, rows + dims_at(16 * (kk & 1) + (lane & 15), 8 * v + 2 * i + (lane >> 4)));
+            if (!whole) {
+              b[0] &= m0;
+              b[1] &= m8;
+              b[2] &= m0;
+              b[3] &= m8;
+            }
+            mma_bf16(o[i >> 1][2 * (i & 1)], a, b[0], b[1]);
+            mma_bf16(o[i >> 1][2 * (i & 1) + 1], a, b[2], b[3]);
           }
+        } else {
+          sl.x *= kPScale;
+          sl.y *= kPScale;
+          sh.x *= kPScale;
+          sh.y *= kPScale;
+          const uint32_t a[4] = {pack_bf16x2(x[0].x * sl.x, x[0].y * sl.y), pack_bf16x2(x[1].x * sl.x, x[1].y * sl.y),
+                                 pack_bf16x2(x[2].x * sh.x, x[2].y * sh.y), pack_bf16x2(x[3].x * sh.x, x[3].y * sh.y)};
+          constexpr int kRow = R::kRow;
+          const uint8_t* codes = stage + t * kRow + 64 * v + 4 * r;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_bf16(o[d][i], a, code_pair(w0, w1, i), code_pair(w8, w9, i));
+          for (int d = 0; d < 2; ++d) {
+            uint32_t w0 = lds<uint32_t>(codes + 32 * d), w1 = lds<uint32_t>(codes + 32 * d + kRow);
+            uint32_t w8 = lds<uint32_t>(codes + 32 * d + 8 * kRow), w9 = lds<uint32_t>(codes + 32 * d + 9 * kRow);
+            if (!whole) {
+              if (!k0) w0 = 0;
+              if (!k1) w1 = 0;
+              if (!k8) w8 = 0;
+              if (!k9) w9 = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_bf16(o[d][i], a, code_pair(w0, w1, i), code_pair(w8, w9, i));
+          }
         }
       }
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bars.p_empty + buf);
         mbar_arrive(bars.empty + s);
+        if (R::kUnits > 1) mbar_arrive(bars.empty + s1);
       }
     }
 
@@ -548,35 +626,51 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
     const bool slot_ok = final_out || p.cluster > 0 || (slot >= 0 && slot < p.max_slots);
     // (clusters: rows for the merge go to the stage that the next page would
     // take; the value warps are at most two pages apart, so none reads it)
-    uint8_t* rows_at = smem + (jt % kStages) * kStageBytes;
-    if (p.cluster > 0 && v == 0 && lane == 0) sts(smem + kWhereOff, (jt % kStages) * kStageBytes);
+    const int free_at = Rows<FMT>::kUnits * jt % kStages * kStageBytes;
+    uint8_t* rows_at = smem + free_at;
+    if (p.cluster > 0 && v == 0 && lane == 0) sts(smem + kWhereOff, free_at);
     if (!slot_ok && lane == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = g * kRows + r + 8 * h;
       if (!slot_ok || row >= p.rows) continue;
       const float inv = h == 0 ? i0 : i1;
-      const int64_t at = (static_cast<int64_t>(final_out ? prob : slot) * p.rows + row) * kDv + 64 * v + 8 * c;
+      const int64_t at = (static_cast<int64_t>(final_out ? prob : slot) * p.rows + row) * kDv + 64 * v;
+      if constexpr (FMT == kBf16) {
+        // dims 8 t + 2 c, 8 t + 2 c + 1
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[i] = o[d][i][2 * h] * inv;
-          y[4 + i] = o[d][i][2 * h + 1] * inv;
+        for (int t = 0; t < 8; ++t) {
+          const float y0 = o[t >> 2][t & 3][2 * h] * inv, y1 = o[t >> 2][t & 3][2 * h + 1] * inv;
+          const int d = 8 * t + 2 * c;
+          if (p.cluster > 0)
+            sts(rows_at + ((r + 8 * h) * kDv + 64 * v + d) * 4, make_float2(y0, y1));
+          else if (final_out)
+            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at + d) = pack_bf16x2(y0, y1);
+          else
+            *reinterpret_cast<float2*>(p.o_accum + at + d) = make_float2(y0, y1);
         }
-        if (p.cluster > 0) {
-          uint8_t* dst = rows_at + ((r + 8 * h) * kDv + 64 * v + 8 * c + 32 * d) * 4;
-          sts(dst, make_float4(y[0], y[1], y[2], y[3]));
-          sts(dst + 16, make_float4(y[4], y[5], y[6], y[7]));
-        } else if (final_out) {
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + 32 * d) = make_uint4(
-              pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-        } else {
-          uint32_t z[8];
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = __float_as_uint(y[i]);
-          st_global_v8(p.o_accum + at + 32 * d, z);
+        for (int d = 0; d < 2; ++d) {
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i] = o[d][i][2 * h] * inv;
+            y[4 + i] = o[d][i][2 * h + 1] * inv;
+          }
+          if (p.cluster > 0) {
+            uint8_t* dst = rows_at + ((r + 8 * h) * kDv + 64 * v + 8 * c + 32 * d) * 4;
+            sts(dst, make_float4(y[0], y[1], y[2], y[3]));
+            sts(dst + 16, make_float4(y[4], y[5], y[6], y[7]));
+          } else if (final_out) {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + 8 * c + 32 * d) = make_uint4(
+                pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+          } else {
+            uint32_t z[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = __float_as_uint(y[i]);
+            st_global_v8(p.o_accum + at + 8 * c + 32 * d, z);
+          }
         }
       }
     }
@@ -584,9 +678,9 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
   }
 }
 
-template <bool TOKEN_SCALE>
+template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp8_rows_kernel(const __nv_bfloat16* __restrict__ q, const DecodeParams p) {
+    rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __nv_bfloat16* __restrict__ q, const DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kBarOff);
@@ -600,8 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x >= 32 && threadIdx.x < 32 + kRows) sts(smem + kLseOff + (threadIdx.x - 32) * 4, kNegInf);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bars.full + i, TOKEN_SCALE ? 1 + 32 : 1);  // the arming arrival and each lane's scale copies
-      mbar_init(bars.empty + i, 8 + 8);
+      mbar_init(bars.full + i, FMT == kToken ? 1 + 32 : 1);  // the arming arrival and each lane's scale copies
+      mbar_init(bars.empty + i, Rows<FMT>::kReaders + 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars.p_full + i, 8);
@@ -621,16 +715,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Walk w{rec.p0, rec.t0, rec.p1, rec.t1, p.num_problems};
   if (warp < 4) {
     regs_to<kRegsCtl, kLaunchRegs>();
-    if (warp == 0) produce<TOKEN_SCALE>(p, w, smem, bars, wd);
+    if (warp == 0) produce<FMT>(&tm_kv, p, w, smem, bars, wd);
     __syncthreads();
     if (p.cluster > 0) cluster_merge_wait();
   } else {
     if (warp < 12) {
       regs_to<kRegsScore, kLaunchRegs>();
-      scores<TOKEN_SCALE>(q, p, w, g, part, smem, bars, wd);
+      scores<FMT>(q, p, w, g, part, smem, bars, wd);
     } else {
       regs_to<kRegsValue, kLaunchRegs>();
-      values<TOKEN_SCALE>(p, w, g, part, smem, bars, wd);
+      values<FMT>(p, w, g, part, smem, bars, wd);
     }
     __syncthreads();
     if (p.cluster > 0) {
@@ -644,9 +738,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool TOKEN_SCALE>
-cudaError_t launch(const void* q, const DecodeParams& p, cudaStream_t stream) {
-  auto kern = fp8_rows_kernel<TOKEN_SCALE>;
+template <int FMT>
+cudaError_t launch(const CUtensorMap& tm_kv, const void* q, const DecodeParams& p, cudaStream_t stream) {
+  auto kern = rows_kernel<FMT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaFuncAttributes fa;
@@ -667,13 +761,15 @@ cudaError_t launch(const void* q, const DecodeParams& p, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<const __nv_bfloat16*>(q), p);
+  return cudaLaunchKernelEx(&cfg, kern, tm_kv, static_cast<const __nv_bfloat16*>(q), p);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_fp8(const void* q, const DecodeParams& p, cudaStream_t stream) {
-  return p.kv_scales ? launch<true>(q, p, stream) : launch<false>(q, p, stream);
+cudaError_t launch_decode_rows(const CUtensorMap& tm_kv, const void* q, const DecodeParams& p, bool is_fp8,
+                               cudaStream_t stream) {
+  if (!is_fp8) return launch<kBf16>(tm_kv, q, p, stream);
+  return p.kv_scales ? launch<kToken>(tm_kv, q, p, stream) : launch<kTile>(tm_kv, q, p, stream);
 }
 
 }  // namespace mla

@@ -96,7 +96,8 @@ struct Geometry {
   int num_parts;     // schedule parts (each = row_groups CTAs)
   int sm_count;
   int mode;          // decode kernel mode: 0 dense bf16, 1 sparse FP8, 2 dense FP8, 3 sparse bf16 rows, 4 and 5
-                     // windowed 0 and 2, 6 shared prefix on CTA pairs, 7 FP8 rows in registers
+                     // windowed 0 and 2, 6 shared prefix on CTA pairs, 7 windowed, operands in
+                     // registers
   int pair;          // 1: CTA-pair kernel (128 rows and 128-token tiles per pair), 0: one CTA per row group
   int tile_tokens;   // tokens per schedule tile (64, or 128 for the pair kernel)
   int tile_cost;     // schedule cost of one tile (quarter units of a 64-token bf16 tile)
@@ -238,8 +239,10 @@ struct SlotStoreParams {
 // Kernel launchers (defined in the .cu files); return a CUDA error code.
 cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, const Geometry& g, int32_t* sched,
                             int32_t* num_splits, cudaStream_t stream);
-// Windowed FP8 rows at 16 query rows per CTA (mla_decode_fp8.cu)
-cudaError_t launch_decode_fp8(const void* q, const DecodeParams& p, cudaStream_t stream);
+// Windowed decode at 16 query rows per CTA on register-level matrix instructions (mla_decode_rows.cu)
+// (tm_kv: bf16 rows alone)
+cudaError_t launch_decode_rows(const CUtensorMap& tm_kv, const void* q, const DecodeParams& p, bool is_fp8,
+                               cudaStream_t stream);
 // mode: 0 dense bf16 cache, 1 sparse FP8 cache, 2 dense FP8 cache, 3 sparse bf16 rows, 4 and 5 windowed dense
 // over the bf16 and the FP8 cache
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const DecodeParams& p, int rpc,
