@@ -296,7 +296,7 @@ mla_status prefill_layout(int s_q, int h_q, int topk, Geometry* g, PrefillLayout
 // keys 110.1 / 112.0; 4 x 16 x 512 keys 12.8 / 17.2; 32 rows, 4 x 512 keys 12.9 /
 // 20.5, 30 x 512 (3.9 pages an SM) 18.5 / 24.7, 30 x 2048 (13.4) 39.0 / 35.1; 64
 // rows, 16 x 512 (4.2) 17.8 / 24.0, 30 x 512 (7.9) 28.0 / 24.7.  FP8, 128 x 16 x
-// 4160 keys 132 / 175; 64 rows, 16 x 512 19.5 / 24.0, 30 x 512 31.5 / 25.4.
+// 4160 keys 138 / 175; 64 rows, 16 x 512 19.5 / 24.0, 30 x 512 31.5 / 25.4.
 constexpr int kRowsKernelRows = 16, kRowsKernelPages = 5;
 bool rows_kernel(const Geometry& g, long long pages) {
   return g.rows <= kRowsKernelRows ||
@@ -315,6 +315,16 @@ void rows_geometry(Geometry* g) {
   if (g->num_parts < 1) g->num_parts = 1;
 }
 
+// CTAs of the largest clusters, one for each row group of each problem, that
+// have a page each and are resident at once; 0: none.
+int largest_cluster(const Geometry& g, long long pages, const int* capacity) {
+  if (g.pair || g_test_num_parts.load() > 0) return 0;
+  const long long units = static_cast<long long>(g.num_problems) * g.row_groups;
+  for (int i = 3; i >= 0; --i)
+    if (units <= capacity[i] && (1 << i) <= pages) return 1 << i;
+  return 0;
+}
+
 // CTAs of the cluster that each problem of a windowed call is given on the
 // single-CTA kernels (mla_cluster.cuh), or 0 for a schedule over all SMs with a
 // merge kernel behind it.  A cluster is taken when all of them are resident at
@@ -326,13 +336,9 @@ void rows_geometry(Geometry* g) {
 // / 26.0 and 100 73 / 63; 64 rows, windows of 512: 60 32.2 / 39.8; FP8, 16 rows,
 // windows of 128: 4 11.0 / 12.9, 60 13.7 / 18.8, 128 20.6 / 24.8.
 int window_cluster(const Geometry& g, long long pages, const int* capacity) {
-  if (g.pair || g_test_num_parts.load() > 0) return 0;
+  const int n = largest_cluster(g, pages, capacity);
   const long long units = static_cast<long long>(g.num_problems) * g.row_groups;
-  for (int i = 3; i >= 0; --i) {
-    if (units > capacity[i] || (1 << i) > pages) continue;
-    return pages * g.sm_count <= (pages * units + 3ll * g.sm_count) << i ? 1 << i : 0;
-  }
-  return 0;
+  return pages * g.sm_count <= (pages * units + 3ll * g.sm_count) * n ? n : 0;
 }
 
 // Pages of all problems of a schedule that a call may have: the sums of a
@@ -360,6 +366,16 @@ mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, long long page
   L->total = L->lse_accum + align256(slots * g->rows * sizeof(float));
   return MLA_OK;
 }
+
+// A small shared-prefix call runs as windowed ones do, each element over the
+// prefix and its own keys on clusters of the register-level kernel: the prefix
+// is then read for every 16 query rows, from L2.  Taken where a CTA has at most
+// 8 (FP8: 14) pages.  Measured (us, against blocks of 128 rows): bf16, 16 rows,
+// 6 elements behind 2000 keys (4.5 pages a CTA) 18.5 / 23.1, 32 (9) 26.7 / 29.5, 16
+// (9) 26.0 / 24.7, 60 (18) 42.4 / 33.6; 128 rows, 4 behind 300 14.4 / 20.5; FP8,
+// 16 rows, 6 behind 2000 20.3 / 34.8, behind 8000 (16) 46.5 / 48.7, 60 behind 2000
+// (18) 50.7 / 43.3.
+constexpr int kPrefixPagesEach = 8, kPrefixPagesEachFp8 = 14;
 
 // Shared-prefix decode, on CTA pairs over blocks of 128 query rows (`pre`).
 // bf16 rows: the prefix and the own keys in one.  FP8 rows: the prefix alone,
@@ -1050,12 +1066,55 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   if (st != MLA_OK) return st;
   uint32_t* status = nullptr;
   int sms = 0;
-  st = device_info(&status, &sms);
+  const int* clusters = nullptr;
+  st = device_info(&status, &sms, nullptr, &clusters);
   if (st != MLA_OK) return st;
 
   char* ws = static_cast<char*>(a->workspace);
   const long long qrows = static_cast<long long>(a->batch) * L.own.rows;
   const long long cache_rows = static_cast<long long>(a->num_pages) * kPageSize;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const long long pages = static_cast<long long>(a->prefix_table_len) + a->block_table_stride;
+  Geometry g = L.own;
+  rows_geometry(&g);
+  const int cluster = largest_cluster(g, pages, clusters);
+  if (cluster > 0 && pages <= (a->is_fp8 ? kPrefixPagesEachFp8 : kPrefixPagesEach) * static_cast<long long>(cluster)) {
+    CUtensorMap tm_kv;
+    memset(&tm_kv, 0, sizeof tm_kv);
+    if (!a->is_fp8) st = encode_rows_map(&tm_kv, a->kvcache, cache_rows, kPageSize / 2, "kvcache");
+    if (st != MLA_OK) return st;
+    DecodeParams p;
+    memset(&p, 0, sizeof p);
+    p.block_table = a->block_table;
+    p.cache_seqlens = a->cache_seqlens;
+    p.kv_fp8 = static_cast<const uint8_t*>(a->kvcache);
+    p.out = a->out;
+    p.lse = a->lse;
+    p.status = status;
+    p.timeout_ns = watchdog_ns();
+    p.batch = a->batch;
+    p.s_q = a->s_q;
+    p.h_q = a->h_q;
+    p.num_pages = a->num_pages;
+    p.block_table_stride = a->block_table_stride;
+    p.num_problems = g.num_problems;
+    p.rows = g.rows;
+    p.row_groups = g.row_groups;
+    p.num_parts = g.num_parts;
+    p.is_causal = a->is_causal ? 1 : 0;
+    p.window = 1;
+    p.sinks = 0x7fffffff;  // every own key
+    p.cluster = cluster;
+    p.debug_stall = g_test_debug_stall.load();
+    p.scale_log2 = a->sm_scale * 1.4426950408889634f;
+    p.kv_scales = a->kv_scales;
+    p.prefix_table = a->prefix_table;
+    p.prefix_len = a->prefix_length;
+    p.prefix_pages = a->prefix_table_len;
+    cudaError_t e = launch_decode_rows(tm_kv, a->q, p, a->is_fp8, s);
+    if (e != cudaSuccess) return cuda_fail(e, "shared-prefix decode kernel launch");
+    return ok();
+  }
   CUtensorMap tm_q, tm_ks, tm_kv, tm_own_q, tm_own_kv;
   if (a->is_fp8) {
     st = encode_pair_maps(a->q, qrows, ws + L.rows, static_cast<long long>(a->prefix_table_len) * kPageSize, &tm_q,
@@ -1070,9 +1129,7 @@ mla_status mla_shared_prefix_decode(const mla_shared_prefix_decode_args* a, mla_
   }
   if (st != MLA_OK) return st;
 
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-
   DecodeParams p;
   memset(&p, 0, sizeof p);
   p.block_table = a->block_table;

@@ -30,7 +30,8 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
 
 // This CTA's share of the pages of problem `prob`.
 __device__ __forceinline__ PartRecord cluster_share(const DecodeParams& p, int prob) {
-  const int64_t n = key_walk(p.cache_seqlens[prob], p.s_q, p.window, p.sinks, p.block_table_stride).pages;
+  const int64_t n = key_walk(p.cache_seqlens[prob], p.s_q, p.window, p.sinks, p.block_table_stride).pages +
+                    (p.prefix_len ? pages_of(p.prefix_len[0], p.prefix_pages) : 0);
   const int k = static_cast<int>(cluster_ctarank());
   return PartRecord{prob, static_cast<int>(n * k / p.cluster), prob, static_cast<int>(n * (k + 1) / p.cluster)};
 }

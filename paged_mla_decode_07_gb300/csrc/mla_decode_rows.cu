@@ -38,14 +38,14 @@
 // Score and value warps work on different pages at the same time; P (fp32)
 // passes between them through a double buffer.
 //
-// Measured, 128 elements x 4160 keys: bf16 110 us (5.2 TB/s, 76 % of the copy
-// rate; the tcgen05 kernel 112), FP8 132 us (2.5 TB/s, 37 %; 175): 4.3k cycles
-// per page.  FP8 is bound by instruction issue: ~3k warp instructions per page
-// and SM quarter, of which two codes cost 6-8 on the score side (9 cycles of the
-// conversion and arithmetic pipes, measured alone) and 3 on the value side.
-// Tried: four score warps over whole rows, 5.7k cycles per page (latency);
-// sixteen over one block each, 4.5k (issue slots 65 % busy, DRAM 33 %).
-// 4 elements x 512 keys: bf16 12.4 us, FP8 13.0.
+// Measured, 128 elements x 1.1k to 4.2k keys (3.8k on average): bf16 110 us (5.1
+// TB/s, 76 % of the copy rate; the tcgen05 kernel 112), FP8 138 us (2.4 TB/s, 35
+// %; 175), ~4.4k cycles per page.  FP8 is bound by instruction issue: ~3k warp
+// instructions per page and SM quarter, of which two codes cost 6-8 on the score
+// side (9 cycles of the conversion and arithmetic pipes, measured alone) and 3 on
+// the value side.  Tried: four score warps over whole rows, 5.7k cycles per page
+// (latency); sixteen over one block each, 4.5k (issue slots 65 % busy, DRAM 33 %).
+// 4 elements x 512 keys: bf16 12.4 us, FP8 13.4.
 #include "mla_cluster.cuh"
 #include "mla_device.cuh"
 #include "mla_internal.h"
@@ -133,6 +133,14 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w0, uint32_t w1, int i) {
 }
 // P s <= 2^8 s is held at 2^80 times its value, so O at 2^-40: scales up to
 // 2^39 stay finite and O has all its bits down to 2^-86.
+// Elements of few pages add the product of what the rounding of P s left: the
+// error against 64 bits, relative, is then 0.0023 of the result where it would be
+// 0.0026 (0.0020 over the bf16 cache, which the rounding of the values that is
+// left out does not touch; 0.0017 of it is the result's own rounding).  Elements
+// of all lengths would take 148 us where they take 132 (128 of 66 pages); the
+// condition alone costs 4 of those 132, two copies of the loop 12.
+constexpr int kFewPages = 36;
+__device__ __forceinline__ float bf16x2_half(uint32_t v, int h) { return __uint_as_float(h ? v & 0xffff0000u : v << 16); }
 constexpr float kPScale = 1208925819614629174706176.0f;  // 2^80
 constexpr float kOScale = 1099511627776.0f;              // 2^40
 // Shared-memory reads and writes as plain accesses, which the compiler may
@@ -159,10 +167,27 @@ struct Walk {
   int p0, t0, p1, t1, np;
   __device__ int last() const { return p1 < np ? p1 : np - 1; }
 };
-__device__ __forceinline__ KeyWalk walk_of(const DecodeParams& p, int L) {
-  return key_walk(L, p.s_q, p.window, p.sinks, p.block_table_stride);
-}
-__device__ __forceinline__ void range(const Walk& w, int prob, const KeyWalk& k, int& tb, int& te) {
+// The pages of an element: those of a shared prefix, if the call has one, then
+// those that its window (or, behind a prefix, every own key) needs.
+struct Keys {
+  int prefix, prefix_len, len;  // prefix pages, prefix keys, own keys
+  KeyWalk own;
+  int pages;
+  __device__ Keys(const DecodeParams& p, int prob) {
+    len = p.cache_seqlens[prob];
+    own = key_walk(len, p.s_q, p.window, p.sinks, p.block_table_stride);
+    prefix = prefix_len = 0;
+    if (p.prefix_len) {
+      prefix_len = p.prefix_len[0];
+      prefix = pages_of(prefix_len, p.prefix_pages);
+    }
+    pages = prefix + own.pages;
+  }
+  // logical page of page i, in the prefix or among the element's own
+  __device__ __forceinline__ int page(int i) const { return i < prefix ? i : own.page(i - prefix); }
+  __device__ __forceinline__ int keys(int i) const { return i < prefix ? prefix_len : len; }
+};
+__device__ __forceinline__ void range(const Walk& w, int prob, const Keys& k, int& tb, int& te) {
   tb = prob == w.p0 ? w.t0 : 0;
   te = prob == w.p1 ? min(w.t1, k.pages) : k.pages;
 }
@@ -216,16 +241,17 @@ __device__ void produce(const CUtensorMap* tm_kv, const DecodeParams& p, const W
   volatile int* flags = reinterpret_cast<volatile int*>(smem + kFlagOff);
   int ut = 0;  // units
   for (int prob = w.p0; prob <= w.last(); ++prob) {
-    const int L = p.cache_seqlens[prob];
-    const KeyWalk k = walk_of(p, L);
+    const Keys k(p, prob);
     int tb, te;
     range(w, prob, k, tb, te);
     const int32_t* bt = p.block_table + static_cast<int64_t>(prob) * p.block_table_stride;
     int ids = -1;  // page ids of pages j0 .. j0 + 31 of the walk, one per lane
     for (int j = tb; j < te; ++j) {
       if (((j - tb) & 31) == 0) {
-        const int lp = j + lane < te ? k.page(j + lane) : -1;
-        ids = lp >= 0 && lp < p.block_table_stride ? __ldg(bt + lp) : -1;
+        const int i = j + lane, lp = i < te ? k.page(i) : -1;
+        ids = -1;
+        if (lp >= 0 && lp < (i < k.prefix ? p.prefix_pages : p.block_table_stride))
+          ids = __ldg((i < k.prefix ? p.prefix_table : bt) + lp);
       }
       const int pg = __shfl_sync(0xffffffffu, ids, (j - tb) & 31);
       const bool ok = pg >= 0 && pg < p.num_pages;
@@ -297,8 +323,8 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
   const int row = g * kRows + r + 8 * half;  // the row this lane carries through the softmax
   int jt = 0, seg = 0;
   for (int prob = w.p0; prob <= w.last(); ++prob) {
-    const int L = p.cache_seqlens[prob];
-    const KeyWalk walk = walk_of(p, L);
+    const Keys walk(p, prob);
+    const int L = walk.len;
     int tb, te;
     range(w, prob, walk, tb, te);
     if (tb >= te) continue;
@@ -414,13 +440,13 @@ __device__ void scores(const __nv_bfloat16* __restrict__ q, const DecodeParams& 
         z[3] = (z[3] + o.w) * p.scale_log2;
       }
       // mask: page usable, key at or before the row's last one, and among the first keys or in the window
-      const int first = walk.page(j) * kPageSize;
-      if (!(page_ok && first + kPageSize - 1 <= lim &&
+      const int first = walk.page(j) * kPageSize, last = j < walk.prefix ? walk.prefix_len - 1 : lim;
+      if (!(page_ok && first + kPageSize - 1 <= last &&
             (first + kPageSize - 1 < p.sinks || first > low))) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = first + 16 * tg + 2 * c + 8 * (i >> 1) + (i & 1);
-          if (!(page_ok && t <= lim && (t < p.sinks || t > low))) z[i] = kNegInf;
+          if (!(page_ok && t <= last && (t < p.sinks || t > low))) z[i] = kNegInf;
         }
       }
       // row maximum: the lane groups of the warp, then the four token groups
@@ -500,11 +526,11 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
   volatile int* flags = reinterpret_cast<volatile int*>(smem + kFlagOff);
   int jt = 0, seg = 0;
   for (int prob = w.p0; prob <= w.last(); ++prob) {
-    const int L = p.cache_seqlens[prob];
-    const KeyWalk walk = walk_of(p, L);
+    const Keys walk(p, prob);
     int tb, te;
     range(w, prob, walk, tb, te);
     if (tb >= te) continue;
+    const bool few = FMT != kBf16 && walk.pages <= kFewPages;
     float o[2][4][4];  // [32-dim group][code i][row r: dims 8c + i, 8c + 4 + i; row r + 8]
 #pragma unroll
     for (int a = 0; a < 2; ++a)
@@ -521,6 +547,7 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
       const uint8_t* stage = smem + s * kStageBytes;
       const int lp = walk.page(j);
       const bool page_ok = flags[s] != 0;
+      const int L = walk.keys(j);
       const bool whole = page_ok && page_seen_whole(p, lp, L);
       if (!wait_warp(bars.p_full + buf, (jt >> 1) & 1, wd)) return;
       const uint8_t* pa = smem + kPOff + buf * kPBytes;
@@ -590,8 +617,16 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
           sl.y *= kPScale;
           sh.x *= kPScale;
           sh.y *= kPScale;
-          const uint32_t a[4] = {pack_bf16x2(x[0].x * sl.x, x[0].y * sl.y), pack_bf16x2(x[1].x * sl.x, x[1].y * sl.y),
-                                 pack_bf16x2(x[2].x * sh.x, x[2].y * sh.y), pack_bf16x2(x[3].x * sh.x, x[3].y * sh.y)};
+          x[0] = make_float2(x[0].x * sl.x, x[0].y * sl.y);
+          x[1] = make_float2(x[1].x * sl.x, x[1].y * sl.y);
+          x[2] = make_float2(x[2].x * sh.x, x[2].y * sh.y);
+          x[3] = make_float2(x[3].x * sh.x, x[3].y * sh.y);
+          uint32_t a[4], rest[4];  // P s and what its rounding left
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = pack_bf16x2(x[i].x, x[i].y);
+            if (few) rest[i] = pack_bf16x2(x[i].x - bf16x2_half(a[i], 0), x[i].y - bf16x2_half(a[i], 1));
+          }
           constexpr int kRow = R::kRow;
           const uint8_t* codes = stage + t * kRow + 64 * v + 4 * r;
 #pragma unroll
@@ -605,7 +640,11 @@ __device__ void values(const DecodeParams& p, const Walk& w, int g, int part, ui
               if (!k9) w9 = 0;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_bf16(o[d][i], a, code_pair(w0, w1, i), code_pair(w8, w9, i));
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t b0 = code_pair(w0, w1, i), b1 = code_pair(w8, w9, i);
+              mma_bf16(o[d][i], a, b0, b1);
+              if (few) mma_bf16(o[d][i], rest, b0, b1);
+            }
           }
         }
       }

@@ -10,6 +10,16 @@ pytestmark = pytest.mark.gpu
 SCALE = 576 ** -0.5
 
 
+@pytest.fixture(params=["any", "blocks"], autouse=True)
+def path(request):
+    """Every test as the call chooses its kernels, and with the blocks of 128 rows that large calls take."""
+    if request.param == "any":
+        yield
+    else:
+        with overrides(num_parts=60):
+            yield
+
+
 def problem(fmt, h_q, s_q, prefix, own, causal, seed=0):
     cache = Cache(fmt, seed, -(-prefix // 64) + sum(-(-L // 64) for L in own) + 3)
     g = torch.Generator("cuda").manual_seed(seed + 1)
