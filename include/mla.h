@@ -350,10 +350,10 @@ mla_status mla_window_decode(const mla_window_decode_args* args, mla_stream_t st
  * sees own keys <= cache_seqlens[b] - s_q + i (and always the whole prefix).
  * Results as mla_decode's over the two key sets in one softmax.  The prefix
  * is read and multiplied once for 128 query rows of the whole batch at a
- * time, whatever elements they belong to.  The prefix may end inside a page;
- * own tokens start in pages of their own.  With an FP8 cache the prefix is
- * turned into bf16 rows in the workspace first.  Keys past a length may hold
- * anything; keys that are not finite show in the rows that share them: all for
+ * time, whatever elements they belong to (calls of few pages: for 16 rows of
+ * an element); with an FP8 cache it is turned into bf16 rows in the workspace
+ * for that.  The prefix may end inside a page; own tokens start in pages of
+ * their own.  Keys past a length may hold anything; keys that are not finite show in the rows that share them: all for
  * the prefix, the element's for own keys.  Missing pages and FP8 scales as for
  * mla_window_decode.
  * All launches are made on `stream` by the one call. */

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kPagesThreads) assign_pages_kernel(const Assig
   };
 
   // new table entries, one per thread
-  if (p.fill_table) {
+  {
     const int pages = pof[p.batch];
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPagesThreads + tid; i < pages;
          i += static_cast<int64_t>(gridDim.x) * kPagesThreads) {
@@ -214,8 +214,9 @@ __global__ void __launch_bounds__(kPagesThreads) assign_pages_kernel(const Assig
 
 cudaError_t launch_assign_pages(const AssignPagesParams& p, bool in_place, int sm_count, cudaStream_t stream) {
   const size_t smem = sizeof(int) * (3 * static_cast<size_t>(p.batch) + 2);
-  cudaError_t e = cudaFuncSetAttribute(assign_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024)  // (48 KB, the scan's own among them, need no leave)
+    e = cudaFuncSetAttribute(assign_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   // one block per 2048 slots (each thread one group of four): short steps run
   // in a single block, whose in-place updates need no second launch
