@@ -1400,7 +1400,7 @@ __global__ void __launch_bounds__(Cfg<R, MODE>::kThreads, 1)
     // copying thread (the 64 threads of a half)
     for (int k = 0; k < C::kNumRaw; ++k) mbar_init(bars.raw_full + k, (C::kIndexed && !C::kFp8) ? 64 : 2);
     *abort_flag = 0;
-    ints[10] = 0;  // (clusters: the rows' place in the ring)
+    if (C::kWindow) ints[10] = 0;  // (clusters: the rows' place in the ring)
     fence_barrier_init();
   }
   // (clusters: of a CTA without pages, or one that a wait ran out in)

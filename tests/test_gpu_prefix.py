@@ -179,3 +179,20 @@ def test_keys_that_are_not_finite_stay_in_their_element(fmt, h_q, s_q, bad):
     keep = [b for b in range(len(own)) if b != hit]
     check(out[keep], lse[keep], tuple(w[keep] for w in want), f"{fmt} {h_q} beside {bad}")
     assert bool(torch.isnan(out[hit]).any()) and not bool(torch.isfinite(lse[hit]).any() and bad == "nan")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("h_q", [16, 40, 128])
+def test_lengths_below_zero_have_no_keys(fmt, h_q):
+    q, kv, sc, pt, plen, bt, lens, want = problem(fmt, h_q, 1, 100, (60, 130, 70), False, seed=h_q)
+    lens[0], lens[2] = -1, -2 ** 31
+    out, lse = run(q, kv, sc, pt, plen, bt, lens, False)
+    check(out[1:2], lse[1:2], tuple(w[1:2] for w in want), f"{fmt} {h_q}")
+    zero = lens.clone().fill_(0)
+    empty = run(q, kv, sc, pt, plen, bt, zero, False)
+    for b in (0, 2):  # (the pieces may be cut elsewhere)
+        assert torch.allclose(lse[b], empty[1][b], rtol=0, atol=2.0 ** -18)
+        assert torch.allclose(out[b].float(), empty[0][b].float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+    plen.fill_(-7)
+    out, lse = run(q, kv, sc, pt, plen, bt, lens, False)
+    assert (out[0] == 0).all() and (lse[2] == -float("inf")).all() and torch.isfinite(lse[1]).all()

@@ -253,3 +253,75 @@ def test_batches_that_clusters_share(fmt, n, h_q):
     check(*got, want, f"{fmt} {n} elements of {h_q} rows")
     again = run(q, kv, sc, bt, lens, 300, 6)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("fmt,h_q,n", [("bf16", 16, 4), ("fp8", 16, 4), ("fp8_token", 64, 3), ("bf16", 64, 40)])
+def test_clusters_are_captured_and_follow_the_lengths(fmt, h_q, n):
+    lens = [300 + 17 * b for b in range(n)]
+    q, kv, sc, bt, L, want = problem(fmt, h_q, 1, lens, 200, 3, seed=n, store_all=True)
+    out = torch.empty(n, 1, h_q, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(n, 1, h_q, device="cuda")
+    ws = torch.empty(mla.window_decode_workspace_size(n, h_q=h_q, s_q=1, is_fp8=fmt != "bf16"), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mla.window_decode(q, kv, bt, L, SCALE, window=200, sinks=3, kv_scales=sc, out=out, lse=lse, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(out, lse, want, f"{fmt} replayed")
+    for length in (0, 1, 64, 250):
+        L.fill_(length)
+        graph.replay()
+        again = run(q, kv, sc, bt, L, 200, 3)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("fmt,h_q,n,longest", [("bf16", 128, 30, 2000), ("bf16", 16, 5, 600), ("fp8", 16, 40, 5000), ("fp8", 64, 60, 3000)])
+def test_an_output_on_sixteen_bytes(fmt, h_q, n, longest):
+    """Outputs need 16-byte alignment, not more."""
+    lens = [longest - 31 * b for b in range(n)]
+    q, kv, sc, bt, L, want = problem(fmt, h_q, 1, lens, 1500, 3, seed=n)
+    room = torch.empty(n * h_q * 512 + 8, dtype=torch.bfloat16, device="cuda")
+    out = room[8:].view(n, 1, h_q, 512)
+    assert out.data_ptr() % 32 == 16
+    got = mla.window_decode(q, kv, bt, L, SCALE, window=1500, sinks=3, kv_scales=sc, out=out)
+    assert mla.device_status() == 0
+    check(*got, want, f"{fmt} at 16 bytes")
+
+
+def test_calls_on_several_streams_at_once():
+    """Every way a window is run, in turn on streams of their own with workspaces of their own."""
+    cases = []
+    for fmt, h_q, n, longest, window in (("bf16", 16, 4, 900, 300), ("fp8", 16, 100, 4000, 3500), ("bf16", 64, 40, 2000, 1500),
+                                         ("bf16", 128, 20, 3000, 2500), ("fp8_token", 64, 30, 2500, 2000)):
+        lens = [longest - 13 * b for b in range(n)]
+        q, kv, sc, bt, L, want = problem(fmt, h_q, 1, lens, window, 9, seed=n)
+        first = [t.clone() for t in run(q, kv, sc, bt, L, window, 9)]
+        check(*first, want, f"{fmt} {h_q}x{n}")
+        cases.append((q, kv, sc, bt, L, window, first, torch.cuda.Stream(),
+                      torch.empty(mla.window_decode_workspace_size(n, h_q=h_q, s_q=1, is_fp8=fmt != "bf16"), dtype=torch.uint8,
+                                  device="cuda")))
+    torch.cuda.synchronize()
+    results = [[] for _ in cases]
+    for _ in range(10):
+        for k, (q, kv, sc, bt, L, window, _, stream, ws) in enumerate(cases):
+            results[k].append(mla.window_decode(q, kv, bt, L, SCALE, window=window, sinks=9, kv_scales=sc, workspace=ws,
+                                                stream=stream))
+    torch.cuda.synchronize()
+    assert mla.device_status() == 0
+    for case, got in zip(cases, results):
+        for out, lse in got:
+            assert torch.equal(out, case[6][0]) and torch.equal(lse, case[6][1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("h_q", [16, 40, 128])
+@pytest.mark.parametrize("parts", [None, 30])
+def test_lengths_below_zero_have_no_keys(fmt, h_q, parts):
+    q, kv, sc, bt, L, want = problem(fmt, h_q, 2, (5, 130, 70, 300), 100, 4, seed=h_q)
+    L[0], L[2] = -3, -2 ** 31
+    with overrides(num_parts=parts):
+        out, lse = run(q, kv, sc, bt, L, 100, 4)
+    for b in (0, 2):
+        assert (out[b] == 0).all() and (lse[b] == -float("inf")).all()
+    keep = [1, 3]
+    check(out[keep], lse[keep], tuple(w[keep] for w in want), f"{fmt} {h_q}")
