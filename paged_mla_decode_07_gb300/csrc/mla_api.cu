@@ -417,9 +417,8 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   g.mode = 6;
   g.tile_tokens = 128;
   g.tile_cost = 8;
-  // as for windows: with less, the parts that hold many short own-key problems
-  // end last (64 x 128 rows, 8192 shared and ~256 own keys: 190 us at one and a
-  // half tiles, 151 at four, 154 at five)
+  // as for windows (64 x 128 rows behind 1000 keys: 50.9 us at two tiles, 48.5 at
+  // four, 48.2 at five and a half; 8192 keys: 140.8, 140.8, 142.5)
   g.overhead = 32;
   const int forced = g_test_num_parts.load();
   g.num_parts = forced > 0 ? forced : (pairs > 0 ? pairs : 1);
