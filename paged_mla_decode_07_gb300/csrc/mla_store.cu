@@ -153,7 +153,9 @@ __device__ __forceinline__ int slot_of(const SlotStoreParams& p, int r, bool fla
 // takes about ten, which bounds this kernel.  Remainders are exact while
 // x 2^-48 is above the subnormals, for every x whose code is not 0 while
 // scale >= 2^-90; scales outside [2^-90, 2^120] (infinities and NaN among
-// them) divide.
+// them) divide.  The remainder is taken as q scale - x: it is +0 for x = -0 and
+// for x = +0, so q - r (+0) has the sign of q, as the quotient does (with
+// x - q scale, q + r (+0) would turn -0 into +0, and the code's sign with it).
 __device__ __forceinline__ uint4 quantise16(const float (&v)[16], float scale) {
   float y[16];
   if (scale >= 8.077935669463161e-28f && scale <= 1.329227995784916e36f) {
@@ -161,8 +163,8 @@ __device__ __forceinline__ uint4 quantise16(const float (&v)[16], float scale) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float q = v[i] * r;
-      q = fmaf(fmaf(-q, scale, v[i]), r, q);
-      y[i] = fmaf(fmaf(-q, scale, v[i]), r, q);
+      q = fmaf(-r, fmaf(q, scale, -v[i]), q);
+      y[i] = fmaf(-r, fmaf(q, scale, -v[i]), q);
     }
   } else {
 #pragma unroll
