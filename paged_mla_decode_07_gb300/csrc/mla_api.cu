@@ -175,23 +175,34 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// cuTensorMapEncodeTiled(args...).  A driver call, it wants the context current
+// that a runtime call would make current: in a host thread whose first CUDA
+// call this is there is none yet, and the current device's becomes it.
+template <class... Args>
+mla_status encode_map(const char* what, Args... args) {
+  auto fn = encode_fn();
+  if (!fn) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  CUresult r = fn(args...);
+  int dev = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+    r = fn(args...);
+  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what, (int)r);
+  return MLA_OK;
+}
+
 // 576-wide bf16 rows viewed as [rows][9 chunks][64]: dim0 = 64 elements
 // (128 B, the swizzle atom width), dim1 = chunk (stride 128 B), dim2 = row
 // (stride 1152 B).  A box of {64, 1, box_rows} lands in shared memory as
 // box_rows x 128 B with the 128-byte swizzle, the canonical K-major operand
 // layout of the tcgen05 MMAs.
 mla_status encode_rows_map(CUtensorMap* map, const void* base, long long nrows, int box_rows, const char* what) {
-  auto fn = encode_fn();
-  if (!fn) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
   cuuint64_t dims[3] = {64, 9, static_cast<cuuint64_t>(nrows)};
   cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(kDqk * 2)};
   cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what, (int)r);
-  return MLA_OK;
+  return encode_map(what, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // The same 576-wide bf16 rows viewed chunk-major: dim0 = 64 elements of a
@@ -201,17 +212,13 @@ mla_status encode_rows_map(CUtensorMap* map, const void* base, long long nrows, 
 // K-major operand tiles of the tcgen05 MMAs.
 mla_status encode_chunk_major_map(CUtensorMap* map, const void* base, long long nrows, int box_chunks,
                                   const char* what) {
-  auto fn = encode_fn();
-  if (!fn) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
   cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(nrows), 9};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(kDqk * 2), 128};
   cuuint32_t box[3] = {64, 64, static_cast<cuuint32_t>(box_chunks)};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what, (int)r);
-  return MLA_OK;
+  return encode_map(what, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Cache rows as raw bytes, [rows][row_bytes] (row = page * 64 + slot, or the
@@ -220,33 +227,25 @@ mla_status encode_chunk_major_map(CUtensorMap* map, const void* base, long long 
 // row gathers require), 32 consecutive rows of a page for dense decode over
 // the FP8 cache; no swizzle: the rows land as plain 128-byte rows.
 mla_status encode_byte_rows_map(CUtensorMap* map, const void* base, long long nrows, int row_bytes, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(nrows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
   cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled(kv rows) failed with CUresult %d", (int)r);
-  return MLA_OK;
+  return encode_map("kv rows", map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // E4M3 rows of 128 bytes, [rows][128], 128-byte swizzle: a box of box_rows
 // rows lands as the canonical K-major operand of a kind::f8f6f4 MMA.
 mla_status encode_e4m3_rows_map(CUtensorMap* map, const void* base, long long nrows, int box_rows, const char* what) {
-  auto fn = encode_fn();
-  if (!fn) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
   cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(nrows)};
   cuuint64_t strides[1] = {128};
   cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what, (int)r);
-  return MLA_OK;
+  return encode_map(what, map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
