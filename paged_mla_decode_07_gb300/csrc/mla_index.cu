@@ -815,7 +815,7 @@ cudaError_t launch_index(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
   int cap = 1;
   while (cap < topk) cap <<= 1;
   const size_t smem = static_cast<size_t>((cap > kTopkThreads ? cap : kTopkThreads) + kCandCap) * sizeof(unsigned long long);
-  e = cudaFuncSetAttribute(index_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  e = allow_dynamic_smem(index_topk_kernel, smem, 20 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.num_tokens));

@@ -236,6 +236,19 @@ struct SlotStoreParams {
   int is_fp8;
 };
 
+// Lets launches of a kernel whose shared memory varies from call to call have
+// `bytes` of it beside the kernel's own (at most `own`).  48 KB in all need no
+// leave.  The limit belongs to the kernel, not to the launch, and another host
+// thread may set it between here and the launch: so every call sets the same
+// one, the most a block can have.
+template <class Kernel>
+cudaError_t allow_dynamic_smem(Kernel* kernel, size_t bytes, size_t own) {
+  constexpr size_t kFree = 48 * 1024, kMost = 227 * 1024;
+  if (bytes + own <= kFree) return cudaSuccess;
+  if (bytes + own > kMost) return cudaErrorInvalidValue;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost - own));
+}
+
 // Kernel launchers (defined in the .cu files); return a CUDA error code.
 cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, const Geometry& g, int32_t* sched,
                             int32_t* num_splits, cudaStream_t stream);

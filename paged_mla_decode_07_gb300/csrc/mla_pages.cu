@@ -214,9 +214,7 @@ __global__ void __launch_bounds__(kPagesThreads) assign_pages_kernel(const Assig
 
 cudaError_t launch_assign_pages(const AssignPagesParams& p, bool in_place, int sm_count, cudaStream_t stream) {
   const size_t smem = sizeof(int) * (3 * static_cast<size_t>(p.batch) + 2);
-  cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024)  // (48 KB, the scan's own among them, need no leave)
-    e = cudaFuncSetAttribute(assign_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_dynamic_smem(assign_pages_kernel, smem, sizeof(Scan2) * kPagesThreads / 32);
   if (e != cudaSuccess) return e;
   // one block per 2048 slots (each thread one group of four): short steps run
   // in a single block, whose in-place updates need no second launch

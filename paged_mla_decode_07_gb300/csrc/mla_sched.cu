@@ -201,8 +201,7 @@ size_t metadata_smem_bytes(int np, int num_parts) {
 cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, const Geometry& g, int32_t* sched,
                             int32_t* num_splits, cudaStream_t stream) {
   size_t smem = metadata_smem_bytes(g.num_problems, g.num_parts);
-  cudaError_t e = cudaFuncSetAttribute(metadata_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = allow_dynamic_smem(metadata_kernel, smem, 0);
   if (e != cudaSuccess) return e;
   metadata_kernel<<<1, kThreads, smem, stream>>>(cache_seqlens, g.num_problems, s_q, topk, g.num_parts,
                                                  g.tile_tokens, g.tile_cost, g.overhead, g.tag, sched, num_splits);
