@@ -12,6 +12,11 @@
 // one that the library refuses: the Python function then checks it in full,
 // switches devices and streams, and names the argument that is wrong.  A
 // library status past the refusals is returned as an int.
+//
+// Allocations and library calls run without the interpreter's lock: an
+// allocation that frees cached memory waits for the GPU, a launch into a full
+// queue waits for room in it, and what they wait for may be a host function on
+// the stream that needs the lock.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
@@ -25,6 +30,14 @@ namespace {
 
 constexpr int64_t kPage = 64, kQk = 576, kV = 512;
 constexpr int kMaxPages = ((1ll << 31) - 1) / kPage;
+
+// The interpreter's lock given up for a scope.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 // What a call's arguments have been found to be.  `ok` turns false at the
 // first one that is not plain; nothing more is read then.
@@ -80,10 +93,9 @@ struct Call {
     return reinterpret_cast<mla_stream_t>(
         c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream());
   }
-  // output argument i: the tensor given, of exactly this shape, or a new one
+  // output argument i: the tensor given, of exactly this shape, or none yet
   at::Tensor output(int i, at::ScalarType type, at::IntArrayRef shape) {
-    if (!ok) return {};
-    if (args[i] == Py_None) return at::empty(shape, options(type));
+    if (!ok || args[i] == Py_None) return {};
     const at::Tensor* t = tensor(i, type, static_cast<int>(shape.size()));
     if (!t || t->sizes() != shape) {
       ok = false;
@@ -91,9 +103,8 @@ struct Call {
     }
     return *t;
   }
-  at::Tensor workspace(int i, size_t bytes) {
-    if (!ok) return {};
-    if (args[i] == Py_None) return at::empty({static_cast<int64_t>(bytes)}, options(at::kByte));
+  at::Tensor workspace(int i) {
+    if (!ok || args[i] == Py_None) return {};
     if (!THPVariable_CheckExact(args[i])) {
       ok = false;
       return {};
@@ -101,6 +112,10 @@ struct Call {
     const at::Tensor& t = THPVariable_Unpack(args[i]);
     need(t.device().is_cuda() && t.device().index() == device && t.is_contiguous());
     return ok ? t : at::Tensor();
+  }
+  // a new tensor where none was given
+  void fill(at::Tensor& t, at::ScalarType type, at::IntArrayRef shape) const {
+    if (!t.defined()) t = at::empty(shape, options(type));
   }
 };
 
@@ -176,8 +191,8 @@ PyObject* assign_pages(PyObject*, PyObject* const* args, Py_ssize_t n) {
     a.num_tokens = c.integer(5);
     a.num_pages = c.given(6) ? c.integer(6) : kMaxPages;
     c.need(in[1]->size(0) == batch && in[4]->size(0) == batch && in[3]->size(0) == 1 && a.num_tokens >= 0);
-    const at::Tensor lens = c.output(7, at::kInt, {batch}), offsets = c.output(8, at::kInt, {batch + 1}),
-                     slots = c.output(9, at::kInt, {a.num_tokens}), cursor = c.output(10, at::kInt, {1});
+    at::Tensor lens = c.output(7, at::kInt, {batch}), offsets = c.output(8, at::kInt, {batch + 1}),
+               slots = c.output(9, at::kInt, {a.num_tokens}), cursor = c.output(10, at::kInt, {1});
     if (!c.ok) return nullptr;
     a.cache_lengths = ptr<int32_t>(*in[0]);
     a.new_tokens = ptr<int32_t>(*in[1]);
@@ -187,11 +202,20 @@ PyObject* assign_pages(PyObject*, PyObject* const* args, Py_ssize_t n) {
     a.free_cursor = ptr<int32_t>(*in[3]);
     a.block_table = ptr<int32_t>(*in[4]);
     a.block_table_stride = static_cast<int>(in[4]->size(1));
-    a.cache_seqlens = ptr<int32_t>(lens);
-    a.row_offsets = ptr<int32_t>(offsets);
-    a.slot_map = ptr<int32_t>(slots);
-    a.next_cursor = ptr<int32_t>(cursor);
-    const mla_status st = mla_assign_pages(&a, c.stream());
+    const mla_stream_t stream = c.stream();
+    mla_status st;
+    {
+      const Unlocked unlocked;
+      c.fill(lens, at::kInt, {batch});
+      c.fill(offsets, at::kInt, {batch + 1});
+      c.fill(slots, at::kInt, {a.num_tokens});
+      c.fill(cursor, at::kInt, {1});
+      a.cache_seqlens = ptr<int32_t>(lens);
+      a.row_offsets = ptr<int32_t>(offsets);
+      a.slot_map = ptr<int32_t>(slots);
+      a.next_cursor = ptr<int32_t>(cursor);
+      st = mla_assign_pages(&a, stream);
+    }
     return st == MLA_OK ? tuple_of({&lens, &offsets, &slots, &cursor}) : failed(st);
   });
 }
@@ -219,7 +243,12 @@ PyObject* cache_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
     a.kvcache = ptr(*kv);
     a.num_pages = static_cast<int>(kv->size(0));
     a.page_size = static_cast<int>(kv->size(1));
-    const mla_status st = mla_cache_store(&a, c.stream());
+    const mla_stream_t stream = c.stream();
+    mla_status st;
+    {
+      const Unlocked unlocked;
+      st = mla_cache_store(&a, stream);
+    }
     if (st != MLA_OK) return failed(st);
     Py_RETURN_TRUE;
   });
@@ -252,15 +281,24 @@ const at::Tensor* decode_io(Call& c, Args* a, int table, int lens, int scales) {
 // Outputs at arguments i and i + 1, the workspace at i + 2, then the library call.
 template <class Args, class Run>
 PyObject* decode_run(Call& c, Args* a, const at::Tensor& q, int i, size_t bytes, Run run) {
-  const at::Tensor out = c.output(i, at::kBFloat16, {q.size(0), q.size(1), q.size(2), kV});
-  const at::Tensor lse = c.output(i + 1, at::kFloat, {q.size(0), q.size(1), q.size(2)});
-  const at::Tensor ws = c.workspace(i + 2, bytes);
+  const int64_t out_shape[] = {q.size(0), q.size(1), q.size(2), kV};
+  const at::IntArrayRef rows(out_shape, 3);
+  at::Tensor out = c.output(i, at::kBFloat16, out_shape), lse = c.output(i + 1, at::kFloat, rows);
+  at::Tensor ws = c.workspace(i + 2);
   if (!c.ok) return nullptr;
-  a->workspace = ptr(ws);
-  a->workspace_bytes = ws.nbytes();
-  a->out = ptr(out);
-  a->lse = ptr<float>(lse);
-  const mla_status st = run(a, c.stream());
+  const mla_stream_t stream = c.stream();
+  mla_status st;
+  {
+    const Unlocked unlocked;
+    c.fill(out, at::kBFloat16, out_shape);
+    c.fill(lse, at::kFloat, rows);
+    c.fill(ws, at::kByte, {static_cast<int64_t>(bytes)});
+    a->workspace = ptr(ws);
+    a->workspace_bytes = ws.nbytes();
+    a->out = ptr(out);
+    a->lse = ptr<float>(lse);
+    st = run(a, stream);
+  }
   return st == MLA_OK ? tuple_of({&out, &lse}) : failed(st);
 }
 
