@@ -26,6 +26,7 @@ import math
 import operator
 import os
 import threading
+import warnings
 from typing import Optional, Tuple
 
 import torch
@@ -48,7 +49,7 @@ DEVICE_NO_ROOM = 0x8
 
 _lock = threading.Lock()
 _lib = None
-_native = None  # csrc/binding.cpp, loaded with the library
+_native = None  # csrc/binding.cpp, loaded with the library (if it was built)
 
 
 class MLAError(RuntimeError):
@@ -146,6 +147,19 @@ def library_path() -> str:
     return _build.LIB
 
 
+def _load_binding():
+    """The native binding, or None: then every call goes through ctypes."""
+    try:
+        spec = importlib.util.spec_from_file_location("_mla_binding", _build.BINDING)
+        native = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(native)
+        return native
+    except (ImportError, OSError) as e:
+        warnings.warn(f"the native binding is not used, calls go through ctypes ({e}): run "
+                      "paged_mla_decode_07_gb300.build()", RuntimeWarning, stacklevel=3)
+        return None
+
+
 def lib():
     """Load libmla.so (built in-tree by ``build()``); raise if it is missing."""
     global _lib, _native
@@ -194,12 +208,7 @@ def lib():
             L.mla_shared_prefix_decode_workspace_size.restype = I
             L.mla_shared_prefix_decode.argtypes = [ctypes.POINTER(SharedPrefixDecodeArgs), P]
             L.mla_shared_prefix_decode.restype = I
-            if not os.path.exists(_build.BINDING):
-                raise RuntimeError(f"{_build.BINDING} not found: run paged_mla_decode_07_gb300.build()")
-            spec = importlib.util.spec_from_file_location("_mla_binding", _build.BINDING)
-            native = importlib.util.module_from_spec(spec)
-            spec.loader.exec_module(native)
-            _native, _lib = native, L
+            _native, _lib = _load_binding(), L
     return _lib
 
 
@@ -207,6 +216,8 @@ def _plain(name: str, *args):
     """The native binding's result for a call in its plain form, or None (see csrc/binding.cpp)."""
     if _native is None:
         lib()
+        if _native is None:
+            return None
     r = getattr(_native, name)(*args)
     if type(r) is int:
         _check(r)

@@ -14,12 +14,15 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmla.so")
 BINDING = os.path.join(BUILD, "_mla_binding.so")
+HEADER = os.path.join(HERE, "..", "include", "mla.h")
+BINDING_SOURCE = "binding.cpp"
 SOURCES = ["mla_api.cu", "mla_sched.cu", "mla_decode.cu", "mla_decode_pair.cu", "mla_combine.cu", "mla_noalloc.cu",
            "mla_store.cu", "mla_index.cu", "mla_pages.cu", "mla_prefix.cu", "mla_decode_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -34,68 +37,89 @@ def nvcc() -> str:
     return path
 
 
-def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(HERE, "..", "include", "mla.h"))
-    return files
+def _newer(target, *sources) -> bool:
+    """target exists and is not older than its sources and this file."""
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target)
+                                          for f in (*sources, os.path.abspath(__file__)))
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, HEADER, *(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BINDING_SOURCE))
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, HEADER, os.path.join(CSRC, BINDING_SOURCE))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _deps() + [os.path.abspath(__file__)])
+    return library_up_to_date() and binding_up_to_date()
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _run(what, cmd, verbose=False):
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:  # no such program
+        raise RuntimeError(f"{what} failed: {e}") from e
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    if verbose:
+        sys.stderr.write(r.stdout + r.stderr)
+
+
+def build_library(verbose: bool = False) -> None:
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if verbose else []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        cmd = [cc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose:
-            sys.stderr.write(r.stdout + r.stderr)
+        _run(f"nvcc for {src}", [cc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
         return obj
 
-    def compile_binding():
-        import torch
-
-        inc = os.path.join(os.path.dirname(torch.__file__), "include")
-        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
-        obj = os.path.join(BUILD, "binding.o")
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-               *(f"-isystem{p}" for p in (sysconfig.get_paths()["include"], inc,
-                                          os.path.join(inc, "torch", "csrc", "api", "include"), cuda)),
-               "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
-        return obj, os.path.join(os.path.dirname(torch.__file__), "lib")
-
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(compile_binding)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        binding_obj, torch_lib = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run("link", [cc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+
+
+def compile_binding() -> str:
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    _run(f"g++ for {BINDING_SOURCE}",
+         ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(f"-isystem{p}" for p in (sysconfig.get_paths()["include"], inc,
+                                     os.path.join(inc, "torch", "csrc", "api", "include"), cuda)),
+          "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj])
+    return obj
+
+
+def link_binding(obj: str) -> None:
+    import torch
+
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, binding_obj, f"-L{BUILD}", "-l:libmla.so", "-Wl,-rpath,$ORIGIN",
-           f"-L{torch_lib}", f"-Wl,-rpath,{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    _run("link of the binding",
+         ["g++", "-shared", "-o", tmp, obj, f"-L{BUILD}", "-l:libmla.so", "-Wl,-rpath,$ORIGIN",
+          f"-L{torch_lib}", f"-Wl,-rpath,{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
     os.replace(tmp, BINDING)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Build what is not up to date.  Without the library nothing works; without the binding, which
+    needs g++ and the headers of Python and torch, the paged-cache calls go through ctypes."""
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(compile_binding) if force or not binding_up_to_date() else None
+        if force or not library_up_to_date():
+            build_library(verbose)
+        if obj is not None:
+            try:
+                link_binding(obj.result())
+            except RuntimeError as e:
+                warnings.warn(f"the native binding was not built; calls go through ctypes: {e}", RuntimeWarning, stacklevel=2)
     return LIB
 
 
