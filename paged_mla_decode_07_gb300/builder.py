@@ -2,7 +2,7 @@
 native part of the Python binding with g++.
 
 Each translation unit is compiled in parallel, then linked into
-``paged_mla_decode_07_gb300/_build/libmla.so`` and ``_mla_binding.so`` beside
+``paged_mla_decode_07_gb300/_build/libmla.so`` and ``_mla_binding.*.so`` beside
 it (in-tree, git-ignored).
 Usage: ``python -m paged_mla_decode_07_gb300.builder [--verbose]``.
 """
@@ -16,11 +16,22 @@ import sys
 import sysconfig
 import warnings
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmla.so")
-BINDING = os.path.join(BUILD, "_mla_binding.so")
+
+
+def binding_path() -> str:
+    """The binding's file.  It is compiled against the C++ types of one torch and the headers of one
+    Python, which its name states: under others it is another file, not built yet."""
+    abi = f"{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}-cxx11abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(BUILD, f"_mla_binding.{abi}.so")
+
+
+BINDING = binding_path()
 HEADER = os.path.join(HERE, "..", "include", "mla.h")
 BINDING_SOURCE = "binding.cpp"
 SOURCES = ["mla_api.cu", "mla_sched.cu", "mla_decode.cu", "mla_decode_pair.cu", "mla_combine.cu", "mla_noalloc.cu",
@@ -83,8 +94,6 @@ def build_library(verbose: bool = False) -> None:
 
 
 def compile_binding() -> str:
-    import torch
-
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     obj = os.path.join(BUILD, "binding.o")
@@ -97,8 +106,6 @@ def compile_binding() -> str:
 
 
 def link_binding(obj: str) -> None:
-    import torch
-
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
     _run("link of the binding",
