@@ -329,11 +329,16 @@ int largest_cluster(const Geometry& g, long long pages, const int* capacity) {
 // merge kernel behind it.  A cluster is taken when all of them are resident at
 // once and the longest problem's share is at most three pages more than an even
 // share of all pages: about what a schedule costs, its segments that start and
-// end inside a problem, and the merge.  Measured (us, cluster against schedule):
-// bf16 on the tcgen05 kernel, 16 rows, windows of 512: 34 elements 20.6 / 29.4,
-// 60 24.8 / 29.7, 150 36.1 / 41.9; of 2048: 34 30.5 / 34.8, but 16 elements 29.4
-// / 26.0 and 100 73 / 63; 64 rows, windows of 512: 60 32.2 / 39.8; FP8, 16 rows,
-// windows of 128: 4 11.0 / 12.9, 60 13.7 / 18.8, 128 20.6 / 24.8.
+// end inside a problem, and the merge.  Measured (us, cluster against schedule,
+// replayed, pages not in L2): the register-level kernel, 16 rows, bf16, windows
+// of 512: 4 elements 11.9 / 13.8, 60 18.9 / 23.6, 150 29.6 / 35.3; of 2048: 34
+// 26.3 / 29.4, but 16 elements 24.4 / 22.5 and 100 69.8 / 58.8; FP8, windows of
+// 128: 4 10.3 / 12.8, 60 14.2 / 19.4, 128 20.4 / 25.5; of 1024: 100 53.3 / 46.9.  64
+// rows on the tcgen05 kernels, windows of 512: 60 elements bf16 29.8 / 38.1, FP8
+// 31.8 / 40.6.  Over 330 such calls (16 to 64 rows, 1 to 150 elements, windows of
+// 128 to 4096) the side taken is within 5 % of the better one in all but 15; worst
+// 19 % (4 x 16 rows x 2048 keys of bf16: schedule 20.7, cluster 17.3) and 16 % the
+// other way (16 x 64 rows x 1024 keys of FP8: cluster 30.6, schedule 26.2).
 int window_cluster(const Geometry& g, long long pages, const int* capacity) {
   const int n = largest_cluster(g, pages, capacity);
   const long long units = static_cast<long long>(g.num_problems) * g.row_groups;

@@ -1,7 +1,8 @@
 // Small windowed calls: a problem's pages are shared out over the CTAs of one
 // thread-block cluster, and their results are merged through distributed shared
 // memory, without a schedule, partial results in global memory or a second
-// kernel (4 elements of 10 pages, FP8, 16 rows: 13.0 us for 14.4).
+// kernel (4 elements of 10 pages, 16 rows: bf16 11.9 us for 13.8, FP8 13.1 for
+// 14.4).
 #pragma once
 
 #include "mla_device.cuh"
