@@ -1560,28 +1560,6 @@ int window_cluster_capacity(int size) {
   return n;
 }
 
-size_t decode_smem_bytes(int rpc, int mode) {
-  switch (mode * 100 + rpc) {
-    case 16: return Cfg<16, kModeDense>::kSmemBytes;
-    case 32: return Cfg<32, kModeDense>::kSmemBytes;
-    case 64: return Cfg<64, kModeDense>::kSmemBytes;
-    case 116: return Cfg<16, kModeSparse>::kSmemBytes;
-    case 132: return Cfg<32, kModeSparse>::kSmemBytes;
-    case 164: return Cfg<64, kModeSparse>::kSmemBytes;
-    case 216: return Cfg<16, kModeDenseFp8>::kSmemBytes;
-    case 232: return Cfg<32, kModeDenseFp8>::kSmemBytes;
-    case 264: return Cfg<64, kModeDenseFp8>::kSmemBytes;
-    case 316: return Cfg<16, kModeSparseBf16>::kSmemBytes;
-    case 332: return Cfg<32, kModeSparseBf16>::kSmemBytes;
-    case 364: return Cfg<64, kModeSparseBf16>::kSmemBytes;
-    case 432: return Cfg<32, kModeWindow>::kSmemBytes;
-    case 464: return Cfg<64, kModeWindow>::kSmemBytes;
-    case 532: return Cfg<32, kModeWindowFp8>::kSmemBytes;
-    case 564: return Cfg<64, kModeWindowFp8>::kSmemBytes;
-  }
-  return 0;
-}
-
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const DecodeParams& p, int rpc,
                           int mode, cudaStream_t stream) {
   switch (mode * 100 + rpc) {

@@ -799,8 +799,6 @@ __global__ void __launch_bounds__(kTopkThreads, 2)
 
 }  // namespace
 
-size_t index_score_smem_bytes() { return kScoreSmem; }
-
 cudaError_t launch_index(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const IndexParams& p, int topk,
                          int32_t* out, cudaStream_t stream) {
   auto kern = p.h_idx == 64 ? (p.relu ? index_score_kernel<true, true> : index_score_kernel<false, true>)

@@ -283,7 +283,6 @@ cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool pdl
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
 // Clusters of `size` single-CTA windowed kernels that are resident at once
 int window_cluster_capacity(int size);
-size_t decode_smem_bytes(int rpc, int mode);
 cudaError_t launch_fp8_cache_store(const uint16_t* x, int num_tokens, const int32_t* row_offsets,
                                    const int32_t* cache_lengths, int batch, const int32_t* block_table,
                                    int block_table_stride, uint8_t* kvcache, int num_pages, uint32_t* status,
