@@ -723,8 +723,10 @@ def shared_prefix_decode(q: torch.Tensor, kvcache: torch.Tensor, prefix_table: t
     """Decode attention of a batch that shares a prefix, read once for the batch (mla_shared_prefix_decode).
 
     prefix_table int32 [pages] and prefix_length int32 [1] (on the device) name the shared tokens,
-    block_table and cache_seqlens each element's own; every query row attends to both.  Returns (out
-    bf16 [b, s_q, h_q, 512], lse fp32 [b, s_q, h_q], base 2)."""
+    block_table and cache_seqlens each element's own; every query row attends to both.  Tables as wide
+    as their longest entry: small calls are slower with wide ones, and over an FP8 cache each column of
+    prefix_table takes 73,728 bytes of workspace.  Returns (out bf16 [b, s_q, h_q, 512], lse fp32
+    [b, s_q, h_q], base 2)."""
     if stream is None:
         r = _plain("shared_prefix_decode", q, kvcache, prefix_table, prefix_length, block_table, cache_seqlens, sm_scale,
                    is_causal, kv_scales, out, lse, workspace)

@@ -133,12 +133,14 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w0, uint32_t w1, int i) {
 }
 // P s <= 2^8 s is held at 2^80 times its value, so O at 2^-40: scales up to
 // 2^39 stay finite and O has all its bits down to 2^-86.
-// Elements of few pages add the product of what the rounding of P s left: the
-// error against 64 bits, relative, is then 0.0023 of the result where it would be
-// 0.0026 (0.0020 over the bf16 cache, which the rounding of the values that is
-// left out does not touch; 0.0017 of it is the result's own rounding).  Elements
-// of all lengths would take 148 us where they take 132 (128 of 66 pages); the
-// condition alone costs 4 of those 132, two copies of the loop 12.
+// Elements of few pages add the product of what the rounding of P s left.  The
+// error against 64 bits, relative (0.0017 of it the result's own rounding), is
+// then 0.0022 at one page, 0.0020 at 16, 0.0019 at 36, and without it 0.0026 at
+// one, 0.0022 at 37, 0.0020 at 66, 0.0018 at 200 (bf16 cache: 0.0021, 0.0020,
+// 0.0019; 0.0019, 0.0018, 0.0018): past 36 pages no element is further off than
+// short ones are.  Elements of all lengths would take 148 us where they take
+// 132 (128 of 66 pages); the condition alone costs 4 of those 132, two copies of
+// the loop 12.
 constexpr int kFewPages = 36;
 __device__ __forceinline__ float bf16x2_half(uint32_t v, int h) { return __uint_as_float(h ? v & 0xffff0000u : v << 16); }
 constexpr float kPScale = 1208925819614629174706176.0f;  // 2^80
