@@ -258,6 +258,8 @@ def _need(t, name, dtype, device=None, ndim=None):
         raise ValueError(f"{name} must be on {device} (got {t.device})")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions (got {tuple(t.shape)})")
+    if ndim is not None and max(t.shape, default=0) >= 2 ** 31:  # (ctypes would cut the size off)
+        raise ValueError(f"a dimension of {name} does not fit 32 bits (got {tuple(t.shape)})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
