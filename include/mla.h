@@ -321,12 +321,12 @@ mla_status mla_sparse_prefill(const mla_sparse_prefill_args* args, mla_stream_t 
  * the block table, or past its columns, are left out and set
  * MLA_DEVICE_BAD_PAGE.  batch * block_table_stride is at most 2^28.
  * FP8 caches: scales are positive.  With up to 16 query rows per element (s_q *
- * h_q; in calls of few pages with more), a value enters its sum as code * scale
- * and not rounded to bf16, as K is and as mla_decode takes it, and probability *
- * scale is what is rounded to bf16, at 2^80 times its value: an element that
- * sees a key with a scale of 2^39 or more may come out not finite.  Elements of
- * at most 36 pages add what that rounding left, so an element's last bits depend on
- * its own number of pages, never on those beside it.  Error against 64 bits,
+ * h_q; in calls of few pages with more), a value enters its sum as code * scale,
+ * without the rounding to bf16 that it has in mla_decode (and as part of K), and
+ * probability * scale is what is rounded to bf16.  That product is held at 2^80
+ * times its value: an element that sees a key with a scale of 2^39 or more may
+ * come out not finite.  Elements of at most 36 pages add what that rounding
+ * left; an element's own pages alone decide on that.  Error against 64 bits,
  * relative, normal keys, at 1 / 16 / 36 / 37 / 66 / 200 pages: FP8 0.0022 /
  * 0.0020 / 0.0019 / 0.0022 / 0.0020 / 0.0018, bf16 0.0021 / 0.0020 / 0.0019 /
  * 0.0019 / 0.0018 / 0.0018 (0.0017 is the rounding of the result).

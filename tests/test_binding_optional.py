@@ -45,6 +45,7 @@ def test_a_library_that_does_not_build_is_an_error(monkeypatch, tmp_path):
     monkeypatch.setattr(builder, "LIB", str(tmp_path / "libmla.so"))
     monkeypatch.setattr(builder, "BINDING", str(tmp_path / "_mla_binding.so"))
     monkeypatch.setattr(builder, "SOURCES", ["missing.cu"])
+    monkeypatch.setattr(builder, "compile_binding", lambda: "binding.o")
     with pytest.raises(RuntimeError, match="missing.cu"):
         builder.build()
     assert not os.path.exists(builder.LIB)
