@@ -274,6 +274,98 @@ typedef struct {
 
 mla_status mla_cache_store(const mla_cache_store_args* args, mla_stream_t stream);
 
+/* FP4 cache rows: uint8 [num_pages, 64, 1, 400], per token 512 latent values
+ * in 4 bits and 64 RoPE values in bf16.
+ *   bytes [0, 256)    64 little-endian words of eight codes; word w holds dims
+ *                     8 w .. 8 w + 7: bits 4 i .. 4 i + 2 are the magnitude of
+ *                     dim i (0, 1/2, 1, 3/2, 2, 3, 4, 6: E2M1), bit 8 i + 7 the
+ *                     sign of dim i and bit 8 i + 3 that of dim 4 + i (i < 4)
+ *   bytes [256, 272)  16 scale bytes, one per 32 dims: 2^(byte - 127).  Bytes
+ *                     are 114 to 140; others are read as the nearest of these
+ *   bytes [272, 400)  64 bf16 RoPE values
+ * value = code * scale, a bf16 number; every row's latent values are finite.
+ *
+ * mla_fp4_cache_store writes token i (as mla_cache_store does, with the same
+ * rules for slots) with scale = 2^e, e the smallest integer with amax <= 6 * 2^e
+ * over the 32 values, from -13 to 13, and code = E2M1 of x / scale, rounded to
+ * nearest even and saturated at 6 (latents above 49152 are cut off there, those
+ * of a block below 2^-15 become 0; NaN is stored as 6 * scale).  Normally
+ * distributed latents come back with a relative error of 0.118 (root mean
+ * square).  Asynchronous on `stream`. */
+typedef struct {
+  const void* latent;             /* bf16 [num_tokens, 512], 16-byte aligned */
+  int64_t latent_stride;          /* elements between rows: a multiple of 8 */
+  const void* rope;               /* bf16 [num_tokens, 64], 16-byte aligned */
+  int64_t rope_stride;            /* elements between rows: a multiple of 8 */
+  const int32_t* slot_map;        /* int32 [num_tokens] */
+  int num_tokens;                 /* 0: nothing is launched */
+  void* kvcache;                  /* uint8 [num_pages,64,1,400], 16-byte aligned */
+  int num_pages, page_size;       /* page_size must be 64 */
+} mla_fp4_cache_store_args;
+
+mla_status mla_fp4_cache_store(const mla_fp4_cache_store_args* args, mla_stream_t stream);
+
+/* Row formats of a cache. */
+typedef enum {
+  MLA_CACHE_BF16 = 0,       /* 576 bf16 values */
+  MLA_CACHE_FP8 = 1,        /* 656 bytes, four scales */
+  MLA_CACHE_FP8_TOKEN = 2,  /* 640 bytes, one scale per token in kv_scales */
+  MLA_CACHE_FP4 = 3         /* 400 bytes, see mla_fp4_cache_store */
+} mla_cache_format;
+
+/* Reads cached tokens back as packed bf16 rows, as a chunked prefill needs them
+ * for its up-projection: row t of out, row_offsets[b] <= t < row_offsets[b + 1],
+ * is the token at position starts[b] + t - row_offsets[b] of request b, 512
+ * latent and 64 RoPE values.  The values are those that the row stands for:
+ * bf16 rows as they are, FP8 codes times their scale rounded to bf16, FP4
+ * values exactly.  Rows of out from row_offsets[batch] on are left as they are;
+ * offsets past num_tokens are cut off there.  A token whose page lies past
+ * block_table_stride or outside [0, num_pages) becomes a row of zeros and sets
+ * MLA_DEVICE_BAD_PAGE.  Asynchronous on `stream`. */
+typedef struct {
+  const void* kvcache;            /* as `format` says, 16-byte aligned */
+  int num_pages, page_size;       /* page_size must be 64 */
+  int format;                     /* mla_cache_format */
+  const float* kv_scales;         /* fp32 [num_pages, 64] with MLA_CACHE_FP8_TOKEN, else NULL */
+  const int32_t* block_table;     /* int32 [batch, block_table_stride] */
+  int block_table_stride;
+  int batch;
+  const int32_t* starts;          /* int32 [batch], or NULL: every request from its first token on */
+  const int32_t* row_offsets;     /* int32 [batch + 1], non-decreasing, from 0 */
+  int num_tokens;                 /* rows of out; 0: nothing is launched */
+  void* out;                      /* bf16 [num_tokens, 576], 16-byte aligned */
+} mla_cache_load_args;
+
+mla_status mla_cache_load(const mla_cache_load_args* args, mla_stream_t stream);
+
+/* Windowed decode over FP4 rows: mla_window_decode's keys, masks and results
+ * (a window of 2^30 or more sees every key: causal decode over the whole cache),
+ * with its rules for missing pages and sizes.  Latent values and their products
+ * with q are exact (q to 2^-18 of the largest value of its row), sums fp32, and
+ * probabilities are rounded to a relative 2^-9.  The RoPE values of a key that
+ * some query token sees must be finite, or rows of its element are not.  A row
+ * of q that is not finite has results that are not, other rows are as they
+ * would be.  All launches are made on `stream` by the one call. */
+typedef struct {
+  const void* q;                  /* bf16 [batch, s_q, h_q, 576], 16-byte aligned */
+  int batch, s_q, h_q;            /* s_q * h_q <= 1024 */
+  const void* kvcache;            /* uint8 [num_pages,64,1,400], 16-byte aligned */
+  int num_pages, page_size;       /* page_size must be 64 */
+  const int32_t* block_table;     /* int32 [batch, block_table_stride] */
+  int block_table_stride;
+  const int32_t* cache_seqlens;   /* int32 [batch] */
+  float sm_scale;
+  int window;                     /* >= 1 */
+  int sinks;                      /* >= 0 */
+  void* workspace;                /* >= mla_fp4_decode_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  void* out;                      /* bf16 [batch, s_q, h_q, 512], 16-byte aligned */
+  float* lse;                     /* fp32 [batch, s_q, h_q], base 2 */
+} mla_fp4_decode_args;
+
+mla_status mla_fp4_decode_workspace_size(int batch, int h_q, int s_q, size_t* bytes);
+mla_status mla_fp4_decode(const mla_fp4_decode_args* args, mla_stream_t stream);
+
 /* Sparse prefill ("flash_mla_sparse_fwd(q, kv, indices, sm_scale)" of the
  * FlashMLA article's usage section): token-level sparse attention with no
  * batch dimension and an unpaged bf16 KV with one head.  For query token i

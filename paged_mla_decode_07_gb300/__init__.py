@@ -37,6 +37,7 @@ D_QK = 576
 D_V = 512
 PAGE_SIZE = 64
 FP8_ROW_BYTES = 656
+FP4_ROW_BYTES = 400
 MAX_PAGES = (2 ** 31 - 1) // PAGE_SIZE  # slots are int32
 
 MLA_OK = 0
@@ -143,6 +144,37 @@ class SharedPrefixDecodeArgs(ctypes.Structure):
     ]
 
 
+class Fp4CacheStoreArgs(ctypes.Structure):
+    """Mirror of ``mla_fp4_cache_store_args`` in include/mla.h."""
+    _fields_ = [
+        ("latent", ctypes.c_void_p), ("latent_stride", ctypes.c_int64), ("rope", ctypes.c_void_p),
+        ("rope_stride", ctypes.c_int64), ("slot_map", ctypes.c_void_p), ("num_tokens", ctypes.c_int),
+        ("kvcache", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+    ]
+
+
+class CacheLoadArgs(ctypes.Structure):
+    """Mirror of ``mla_cache_load_args`` in include/mla.h."""
+    _fields_ = [
+        ("kvcache", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("format", ctypes.c_int), ("kv_scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int), ("batch", ctypes.c_int), ("starts", ctypes.c_void_p),
+        ("row_offsets", ctypes.c_void_p), ("num_tokens", ctypes.c_int), ("out", ctypes.c_void_p),
+    ]
+
+
+class Fp4DecodeArgs(ctypes.Structure):
+    """Mirror of ``mla_fp4_decode_args`` in include/mla.h."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("batch", ctypes.c_int), ("s_q", ctypes.c_int), ("h_q", ctypes.c_int),
+        ("kvcache", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int),
+        ("cache_seqlens", ctypes.c_void_p), ("sm_scale", ctypes.c_float), ("window", ctypes.c_int),
+        ("sinks", ctypes.c_int), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+    ]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -208,6 +240,14 @@ def lib():
             L.mla_shared_prefix_decode_workspace_size.restype = I
             L.mla_shared_prefix_decode.argtypes = [ctypes.POINTER(SharedPrefixDecodeArgs), P]
             L.mla_shared_prefix_decode.restype = I
+            L.mla_fp4_cache_store.argtypes = [ctypes.POINTER(Fp4CacheStoreArgs), P]
+            L.mla_fp4_cache_store.restype = I
+            L.mla_cache_load.argtypes = [ctypes.POINTER(CacheLoadArgs), P]
+            L.mla_cache_load.restype = I
+            L.mla_fp4_decode_workspace_size.argtypes = [I, I, I, ctypes.POINTER(S)]
+            L.mla_fp4_decode_workspace_size.restype = I
+            L.mla_fp4_decode.argtypes = [ctypes.POINTER(Fp4DecodeArgs), P]
+            L.mla_fp4_decode.restype = I
             _native, _lib = _load_binding(), L
     return _lib
 
@@ -311,6 +351,20 @@ def _cuda_tensor(t, name):
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.device
+
+
+def _is_fp4(kvcache, kv_scales, dev) -> bool:
+    """Whether a paged cache has FP4 rows, after checking it if it has."""
+    if not isinstance(kvcache, torch.Tensor):
+        raise ValueError("kvcache must be a torch.Tensor")
+    if kvcache.dtype != torch.uint8 or kvcache.dim() != 4 or kvcache.shape[3] != FP4_ROW_BYTES:
+        return False
+    _need(kvcache, "kvcache", torch.uint8, dev, 4)
+    if kvcache.shape[2] != 1:
+        raise ValueError(f"FP4 kvcache must be [pages, page_size, 1, {FP4_ROW_BYTES}] (got {tuple(kvcache.shape)})")
+    if kv_scales is not None:
+        raise ValueError("kv_scales given with an FP4 kvcache")
+    return True
 
 
 def _cache_format(kvcache, kv_scales, dev):
@@ -542,7 +596,8 @@ def cache_store(latent: torch.Tensor, rope: torch.Tensor, slot_map: torch.Tensor
     latent bf16 [num_tokens, 512] and rope bf16 [num_tokens, 64], each with any row stride that is a
     multiple of 8 values (so both may be slices of one projection); slot_map int32 [num_tokens]
     (page * 64 + slot, negative: skipped), the slots distinct; kvcache bf16 [num_pages, 64, 1, 576],
-    uint8 [.., 656] or, with kv_scales fp32 [num_pages, 64], uint8 [.., 640]; written in place.
+    uint8 [.., 656] or, with kv_scales fp32 [num_pages, 64], uint8 [.., 640]; uint8 [.., 400]: FP4 rows
+    (mla_fp4_cache_store); written in place.
     """
     if stream is None and _plain("cache_store", latent, rope, slot_map, kvcache, kv_scales):
         return
@@ -558,14 +613,67 @@ def cache_store(latent: torch.Tensor, rope: torch.Tensor, slot_map: torch.Tensor
     _need(slot_map, "slot_map", torch.int32, dev, 1)
     if slot_map.shape[0] != n:
         raise ValueError(f"slot_map must have {n} entries (got {slot_map.shape[0]})")
-    if not isinstance(kvcache, torch.Tensor):
-        raise ValueError("kvcache must be a torch.Tensor")
+    if _is_fp4(kvcache, kv_scales, dev):
+        f = Fp4CacheStoreArgs(latent.data_ptr(), latent.stride(0) if n > 1 else D_V, rope.data_ptr(),
+                              rope.stride(0) if n > 1 else D_V, slot_map.data_ptr(), n, kvcache.data_ptr(),
+                              kvcache.shape[0], kvcache.shape[1])
+        _launch(dev, stream, lambda handle: _check(lib().mla_fp4_cache_store(ctypes.byref(f), handle)))
+        return
     is_fp8 = _cache_format(kvcache, kv_scales, dev)
     a = CacheStoreArgs(latent.data_ptr(), latent.stride(0) if n > 1 else D_V, rope.data_ptr(),
                        rope.stride(0) if n > 1 else D_V, slot_map.data_ptr(), n, kvcache.data_ptr(),
                        kvcache.shape[0], kvcache.shape[1], int(is_fp8),
                        kv_scales.data_ptr() if kv_scales is not None else None)
     _launch(dev, stream, lambda handle: _check(lib().mla_cache_store(ctypes.byref(a), handle)))
+
+
+def cache_load(kvcache: torch.Tensor, block_table: torch.Tensor, row_offsets: torch.Tensor, num_tokens: int,
+               starts: Optional[torch.Tensor] = None, kv_scales: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Cached tokens as packed bf16 rows of 512 latent and 64 RoPE values (mla_cache_load).
+
+    Row t of the result, row_offsets[b] <= t < row_offsets[b + 1] (int32 [batch + 1]), is the token at
+    position starts[b] + t - row_offsets[b] of request b (starts int32 [batch]; None: 0); kvcache and
+    kv_scales in any of the formats that cache_store writes.  Returns out, bf16 [num_tokens, 576]; rows
+    from row_offsets[batch] on are not written.
+    """
+    if stream is None:
+        r = _plain("cache_load", kvcache, block_table, row_offsets, num_tokens, starts, kv_scales, out)
+        if r is not None:
+            return r
+    dev = _cuda_tensor(kvcache, "kvcache")
+    if _is_fp4(kvcache, kv_scales, dev):
+        fmt = 3
+    elif _cache_format(kvcache, kv_scales, dev):
+        fmt = 2 if kv_scales is not None else 1
+    else:
+        fmt = 0
+    _need(block_table, "block_table", torch.int32, dev, 2)
+    _need(row_offsets, "row_offsets", torch.int32, dev, 1)
+    batch, num_tokens = block_table.shape[0], _int32(num_tokens, "num_tokens")
+    if row_offsets.shape[0] != batch + 1:
+        raise ValueError("row_offsets must have one entry more than block_table has rows")
+    if num_tokens < 0:
+        raise ValueError(f"num_tokens must be >= 0 (got {num_tokens})")
+    if starts is not None:
+        _need(starts, "starts", torch.int32, dev, 1)
+        if starts.shape[0] != batch:
+            raise ValueError("starts must have batch entries")
+    if out is not None:
+        _need(out, "out", torch.bfloat16, dev, 2)
+        if tuple(out.shape) != (num_tokens, D_QK):
+            raise ValueError(f"out must be [{num_tokens}, {D_QK}] (got {tuple(out.shape)})")
+
+    def call(handle):
+        o = torch.empty((num_tokens, D_QK), dtype=torch.bfloat16, device=dev) if out is None else out
+        a = CacheLoadArgs(kvcache.data_ptr(), kvcache.shape[0], kvcache.shape[1], fmt,
+                          kv_scales.data_ptr() if kv_scales is not None else None, block_table.data_ptr(),
+                          block_table.shape[1], batch, starts.data_ptr() if starts is not None else None,
+                          row_offsets.data_ptr(), num_tokens, o.data_ptr())
+        _check(lib().mla_cache_load(ctypes.byref(a), handle))
+        return o
+
+    return _launch(dev, stream, call)
 
 
 def sparse_prefill_workspace_size(s_q: int, h_q: int, topk: int) -> int:
@@ -628,15 +736,19 @@ def sparse_prefill(q: torch.Tensor, kv: torch.Tensor, indices: torch.Tensor, sm_
     return out.view(s_q, h_q, D_V), lse.view(s_q, h_q)
 
 
-def _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales):
-    """Checks what the decode calls over a paged cache share; returns (device, is_fp8)."""
+def _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales, fp4=False):
+    """Checks what the decode calls over a paged cache share; returns (device, is_fp8: None for FP4 rows
+    where the call takes them)."""
     dev = _cuda_tensor(q, "q")
     _need(q, "q", torch.bfloat16, dev, 4)
     if q.shape[3] != D_QK:
         raise ValueError(f"q must have last dimension {D_QK} (got {q.shape[3]})")
-    if not isinstance(kvcache, torch.Tensor):
-        raise ValueError("kvcache must be a torch.Tensor")
-    is_fp8 = _cache_format(kvcache, kv_scales, dev)
+    if _is_fp4(kvcache, kv_scales, dev):
+        if not fp4:
+            raise ValueError("this call does not take an FP4 kvcache (window_decode does)")
+        is_fp8 = None
+    else:
+        is_fp8 = _cache_format(kvcache, kv_scales, dev)
     _need(block_table, "block_table", torch.int32, dev, 2)
     _need(cache_seqlens, "cache_seqlens", torch.int32, dev, 1)
     if block_table.shape[0] != q.shape[0] or cache_seqlens.shape[0] != q.shape[0]:
@@ -667,9 +779,12 @@ def _scratch(workspace, nbytes, dev):
     return workspace
 
 
-def window_decode_workspace_size(batch: int, *, h_q: int, s_q: int, is_fp8: bool) -> int:
-    """Scratch bytes of window_decode."""
+def window_decode_workspace_size(batch: int, *, h_q: int, s_q: int, is_fp8: bool, is_fp4: bool = False) -> int:
+    """Scratch bytes of window_decode; is_fp4: over FP4 rows."""
     n = ctypes.c_size_t()
+    if is_fp4:
+        _check(lib().mla_fp4_decode_workspace_size(batch, h_q, s_q, ctypes.byref(n)))
+        return n.value
     _check(lib().mla_window_decode_workspace_size(batch, h_q, s_q, int(bool(is_fp8)), ctypes.byref(n)))
     return n.value
 
@@ -678,7 +793,8 @@ def window_decode(q: torch.Tensor, kvcache: torch.Tensor, block_table: torch.Ten
                   sm_scale: float, window: int, sinks: int = 0, kv_scales: Optional[torch.Tensor] = None,
                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                   workspace: Optional[torch.Tensor] = None, stream=None):
-    """Decode attention over the first ``sinks`` and the last ``window`` keys (mla_window_decode).
+    """Decode attention over the first ``sinks`` and the last ``window`` keys (mla_window_decode; over an
+    FP4 cache, uint8 [pages, 64, 1, 400], mla_fp4_decode).
 
     Arguments as decode()'s; query token i of an element of length L sits at position L - s_q + i and
     sees key t <= that position if t < sinks or t > position - window.  Returns (out bf16
@@ -688,21 +804,24 @@ def window_decode(q: torch.Tensor, kvcache: torch.Tensor, block_table: torch.Ten
                    workspace)
         if r is not None:
             return r
-    dev, is_fp8 = _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales)
+    dev, is_fp8 = _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales, fp4=True)
     batch, s_q, h_q, _ = q.shape
 
     def call(handle):
         o, z = _outputs(q, out, lse)
-        n = ctypes.c_size_t()
+        nbytes = 0
         if workspace is None:
-            _check(lib().mla_window_decode_workspace_size(batch, h_q, s_q, int(is_fp8), ctypes.byref(n)))
-        ws = _scratch(workspace, n.value, dev)
-        a = WindowDecodeArgs(q.data_ptr(), batch, s_q, h_q, kvcache.data_ptr(), kvcache.shape[0], kvcache.shape[1],
-                             block_table.data_ptr(), block_table.shape[1], cache_seqlens.data_ptr(), float(sm_scale),
-                             _int32(window, "window"), _int32(sinks, "sinks"), int(is_fp8),
-                             kv_scales.data_ptr() if kv_scales is not None else None, ws.data_ptr(), ws.nbytes,
-                             o.data_ptr(), z.data_ptr())
-        _check(lib().mla_window_decode(ctypes.byref(a), handle))
+            nbytes = window_decode_workspace_size(batch, h_q=h_q, s_q=s_q, is_fp8=is_fp8, is_fp4=is_fp8 is None)
+        ws = _scratch(workspace, nbytes, dev)
+        common = (q.data_ptr(), batch, s_q, h_q, kvcache.data_ptr(), kvcache.shape[0], kvcache.shape[1],
+                  block_table.data_ptr(), block_table.shape[1], cache_seqlens.data_ptr(), float(sm_scale),
+                  _int32(window, "window"), _int32(sinks, "sinks"))
+        results = (ws.data_ptr(), ws.nbytes, o.data_ptr(), z.data_ptr())
+        if is_fp8 is None:
+            _check(lib().mla_fp4_decode(ctypes.byref(Fp4DecodeArgs(*common, *results)), handle))
+        else:
+            scales = kv_scales.data_ptr() if kv_scales is not None else None
+            _check(lib().mla_window_decode(ctypes.byref(WindowDecodeArgs(*common, int(is_fp8), scales, *results)), handle))
         return o, z
 
     return _launch(dev, stream, call)

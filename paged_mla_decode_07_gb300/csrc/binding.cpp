@@ -28,7 +28,7 @@
 
 namespace {
 
-constexpr int64_t kPage = 64, kQk = 576, kV = 512;
+constexpr int64_t kPage = 64, kQk = 576, kV = 512, kFp4Row = 400;
 constexpr int kMaxPages = ((1ll << 31) - 1) / kPage;
 
 // The interpreter's lock given up for a scope.
@@ -178,6 +178,17 @@ const at::Tensor* cache(Call& c, int i, int k, int* is_fp8, float** scales) {
   return c.ok ? kv : nullptr;
 }
 
+// Paged cache of FP4 rows at argument i with nothing at argument k; NULL, and
+// the call still plain, if its rows are others.
+const at::Tensor* fp4_cache(Call& c, int i, int k) {
+  if (!c.ok || !THPVariable_CheckExact(c.args[i])) return nullptr;
+  const at::Tensor& t = THPVariable_Unpack(c.args[i]);
+  if (!t.defined() || t.scalar_type() != at::kByte || t.dim() != 4 || t.size(3) != kFp4Row) return nullptr;
+  const at::Tensor* kv = c.tensor(i, at::kByte, 4);
+  c.need(kv && kv->size(2) == 1 && !c.given(k));
+  return c.ok ? kv : nullptr;
+}
+
 // (cache_lengths, new_tokens, free_pages, free_cursor, block_table, num_tokens, num_pages or None,
 //  cache_seqlens, row_offsets, slot_map, next_cursor)
 PyObject* assign_pages(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -228,7 +239,8 @@ PyObject* cache_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor* rope = c.tensor(1, at::kBFloat16, 2, true);
     const at::Tensor* slots = c.tensor(2, at::kInt, 1);
     mla_cache_store_args a{};
-    const at::Tensor* kv = cache(c, 3, 4, &a.is_fp8, &a.kv_scales);
+    const at::Tensor* fp4 = fp4_cache(c, 3, 4);
+    const at::Tensor* kv = fp4 ? fp4 : cache(c, 3, 4, &a.is_fp8, &a.kv_scales);
     if (!c.ok) return nullptr;
     const int64_t tokens = latent->size(0);
     c.need(latent->size(1) == kV && rope->size(1) == kQk - kV && rope->size(0) == tokens && slots->size(0) == tokens &&
@@ -247,20 +259,65 @@ PyObject* cache_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
     mla_status st;
     {
       const Unlocked unlocked;
-      st = mla_cache_store(&a, stream);
+      if (fp4) {
+        const mla_fp4_cache_store_args f{a.latent,     a.latent_stride, a.rope,      a.rope_stride, a.slot_map,
+                                         a.num_tokens, a.kvcache,       a.num_pages, a.page_size};
+        st = mla_fp4_cache_store(&f, stream);
+      } else {
+        st = mla_cache_store(&a, stream);
+      }
     }
     if (st != MLA_OK) return failed(st);
     Py_RETURN_TRUE;
   });
 }
 
-// What the two decode calls share: q, kvcache, block_table and cache_seqlens
-// at the given places, the common fields of their argument structs.
+// (kvcache, block_table, row_offsets, num_tokens, starts or None, kv_scales or None, out or None)
+PyObject* cache_load(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c(args, n, 7);
+    mla_cache_load_args a{};
+    int is_fp8 = 0;
+    float* scales = nullptr;
+    const at::Tensor* fp4 = fp4_cache(c, 0, 5);
+    const at::Tensor* kv = fp4 ? fp4 : cache(c, 0, 5, &is_fp8, &scales);
+    const at::Tensor* table = c.tensor(1, at::kInt, 2);
+    const at::Tensor* offsets = c.tensor(2, at::kInt, 1);
+    a.num_tokens = c.integer(3);
+    const at::Tensor* starts = c.given(4) ? c.tensor(4, at::kInt, 1) : nullptr;
+    if (!c.ok) return nullptr;
+    const int64_t batch = table->size(0);
+    c.need(offsets->size(0) == batch + 1 && (!starts || starts->size(0) == batch) && a.num_tokens >= 0);
+    at::Tensor out = c.output(6, at::kBFloat16, {a.num_tokens, kQk});
+    if (!c.ok) return nullptr;
+    a.kvcache = ptr(*kv);
+    a.num_pages = static_cast<int>(kv->size(0));
+    a.page_size = static_cast<int>(kv->size(1));
+    a.format = fp4 ? MLA_CACHE_FP4 : scales ? MLA_CACHE_FP8_TOKEN : is_fp8 ? MLA_CACHE_FP8 : MLA_CACHE_BF16;
+    a.kv_scales = scales;
+    a.block_table = ptr<int32_t>(*table);
+    a.block_table_stride = static_cast<int>(table->size(1));
+    a.batch = static_cast<int>(batch);
+    a.starts = starts ? ptr<int32_t>(*starts) : nullptr;
+    a.row_offsets = ptr<int32_t>(*offsets);
+    const mla_stream_t stream = c.stream();
+    mla_status st;
+    {
+      const Unlocked unlocked;
+      c.fill(out, at::kBFloat16, {a.num_tokens, kQk});
+      a.out = ptr(out);
+      st = mla_cache_load(&a, stream);
+    }
+    return st == MLA_OK ? THPVariable_Wrap(out) : failed(st);
+  });
+}
+
+// What the decode calls share: q, kvcache (`kv`, checked by the caller),
+// block_table and cache_seqlens at the given places, the common fields of their
+// argument structs.
 template <class Args>
-const at::Tensor* decode_io(Call& c, Args* a, int table, int lens, int scales) {
+const at::Tensor* decode_io(Call& c, Args* a, const at::Tensor* kv, int table, int lens) {
   const at::Tensor* q = c.tensor(0, at::kBFloat16, 4);
-  float* sc = nullptr;
-  const at::Tensor* kv = cache(c, 1, scales, &a->is_fp8, &sc);
   const at::Tensor* bt = c.tensor(table, at::kInt, 2);
   const at::Tensor* sl = c.tensor(lens, at::kInt, 1);
   if (!c.ok) return nullptr;
@@ -275,7 +332,6 @@ const at::Tensor* decode_io(Call& c, Args* a, int table, int lens, int scales) {
   a->block_table = ptr<int32_t>(*bt);
   a->block_table_stride = static_cast<int>(bt->size(1));
   a->cache_seqlens = ptr<int32_t>(*sl);
-  a->kv_scales = sc;
   return c.ok ? q : nullptr;
 }
 // Outputs at arguments i and i + 1, the workspace at i + 2, then the library call.
@@ -306,8 +362,21 @@ PyObject* decode_run(Call& c, Args* a, const at::Tensor& q, int i, size_t bytes,
 PyObject* window_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     Call c(args, n, 11);
+    if (const at::Tensor* kv = fp4_cache(c, 1, 7)) {
+      mla_fp4_decode_args a{};
+      const at::Tensor* q = decode_io(c, &a, kv, 2, 3);
+      a.sm_scale = c.number(4);
+      a.window = c.integer(5);
+      a.sinks = c.integer(6);
+      size_t bytes = 0;
+      if (!c.ok || mla_fp4_decode_workspace_size(a.batch, a.h_q, a.s_q, &bytes) != MLA_OK) return nullptr;
+      return decode_run(c, &a, *q, 8, bytes, mla_fp4_decode);
+    }
     mla_window_decode_args a{};
-    const at::Tensor* q = decode_io(c, &a, 2, 3, 7);
+    float* scales = nullptr;
+    const at::Tensor* kv = cache(c, 1, 7, &a.is_fp8, &scales);
+    const at::Tensor* q = decode_io(c, &a, kv, 2, 3);
+    a.kv_scales = scales;
     a.sm_scale = c.number(4);
     a.window = c.integer(5);
     a.sinks = c.integer(6);
@@ -323,7 +392,10 @@ PyObject* shared_prefix_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     Call c(args, n, 12);
     mla_shared_prefix_decode_args a{};
-    const at::Tensor* q = decode_io(c, &a, 4, 5, 8);
+    float* scales = nullptr;
+    const at::Tensor* kv = cache(c, 1, 8, &a.is_fp8, &scales);
+    const at::Tensor* q = decode_io(c, &a, kv, 4, 5);
+    a.kv_scales = scales;
     const at::Tensor* table = c.tensor(2, at::kInt, 1);
     const at::Tensor* length = c.tensor(3, at::kInt, 1);
     a.sm_scale = c.number(6);
@@ -342,7 +414,7 @@ PyObject* shared_prefix_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(assign_pages), ENTRY(cache_store), ENTRY(window_decode), ENTRY(shared_prefix_decode),
+PyMethodDef methods[] = {ENTRY(assign_pages), ENTRY(cache_store), ENTRY(cache_load), ENTRY(window_decode), ENTRY(shared_prefix_decode),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mla_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -371,6 +371,24 @@ mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, long long page
   return MLA_OK;
 }
 
+// Windowed decode over FP4 rows: 16 query rows a CTA, two CTAs an SM, tiles of
+// 128 keys.
+mla_status fp4_layout(int batch, int h_q, int s_q, Geometry* g, WindowLayout* L) {
+  mla_status st = geometry(batch, h_q, s_q, 0, 0, g);
+  if (st != MLA_OK) return st;
+  rows_geometry(g);
+  g->mode = 8;
+  g->tile_tokens = 128;
+  const int forced = g_test_num_parts.load();
+  g->num_parts = forced > 0 ? forced : 2 * g->sm_count / g->row_groups;
+  if (g->num_parts < 1) g->num_parts = 1;
+  const size_t slots = 2 * static_cast<size_t>(g->num_parts);
+  L->o_accum = align256(static_cast<size_t>(g->num_problems) * 2 * sizeof(int32_t));
+  L->lse_accum = L->o_accum + align256(slots * g->rows * kDv * sizeof(float));
+  L->total = L->lse_accum + align256(slots * g->rows * sizeof(float));
+  return MLA_OK;
+}
+
 // A small shared-prefix call runs as windowed ones do, each element over the
 // prefix and its own keys on clusters of the register-level kernel: the prefix
 // is then read for every 16 query rows, from L2.  Taken where a CTA has at most
@@ -482,6 +500,53 @@ mla_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   if (bytes < need) return fail(MLA_ERR_WORKSPACE, "workspace_bytes = %zu < %zu needed", bytes, need);
   if (!aligned(workspace, 256)) return fail(MLA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
   return MLA_OK;
+}
+// Stores through a slot map; is_fp4: FP4 rows (is_fp8 0, no scales).
+mla_status slot_store(const mla_cache_store_args& args, bool is_fp4, mla_stream_t stream) {
+  const mla_cache_store_args* a = &args;
+  if (a->num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %d)", a->num_tokens);
+  if (a->page_size != kPageSize) return fail(MLA_ERR_UNSUPPORTED, "page_size must be 64 (got %d)", a->page_size);
+  if (a->num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages must be >= 1 (got %d)", a->num_pages);
+  if (a->num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages = %d exceeds 2^31 tokens", a->num_pages);
+  if (a->is_fp8 != 0 && a->is_fp8 != 1) return fail(MLA_ERR_INVALID_ARG, "is_fp8 must be 0 or 1 (got %d)", a->is_fp8);
+  if (a->kv_scales && !a->is_fp8) return fail(MLA_ERR_INVALID_ARG, "kv_scales given with a bf16 cache (is_fp8 = 0)");
+  if (!a->kvcache) return fail(MLA_ERR_INVALID_ARG, "kvcache is NULL");
+  if (!aligned(a->kvcache, 16)) return fail(MLA_ERR_INVALID_ARG, "kvcache is not 16-byte aligned");
+  if (a->kv_scales && !aligned(a->kv_scales, 4)) return fail(MLA_ERR_INVALID_ARG, "kv_scales is not 4-byte aligned");
+  if (a->latent_stride < 0 || a->latent_stride % 8 != 0)
+    return fail(MLA_ERR_INVALID_ARG, "latent_stride must be a multiple of 8 elements (got %lld)",
+                static_cast<long long>(a->latent_stride));
+  if (a->rope_stride < 0 || a->rope_stride % 8 != 0)
+    return fail(MLA_ERR_INVALID_ARG, "rope_stride must be a multiple of 8 elements (got %lld)",
+                static_cast<long long>(a->rope_stride));
+  if (a->num_tokens == 0) return ok();
+  if (!a->latent) return fail(MLA_ERR_INVALID_ARG, "latent is NULL");
+  if (!a->rope) return fail(MLA_ERR_INVALID_ARG, "rope is NULL");
+  if (!a->slot_map) return fail(MLA_ERR_INVALID_ARG, "slot_map is NULL");
+  if (!aligned(a->latent, 16)) return fail(MLA_ERR_INVALID_ARG, "latent is not 16-byte aligned");
+  if (!aligned(a->rope, 16)) return fail(MLA_ERR_INVALID_ARG, "rope is not 16-byte aligned");
+  if (!aligned(a->slot_map, 4)) return fail(MLA_ERR_INVALID_ARG, "slot_map is not 4-byte aligned");
+  uint32_t* status = nullptr;
+  int sms = 0;
+  mla_status st = device_info(&status, &sms);
+  if (st != MLA_OK) return st;
+  SlotStoreParams p;
+  memset(&p, 0, sizeof p);
+  p.latent = static_cast<const uint16_t*>(a->latent);
+  p.rope = static_cast<const uint16_t*>(a->rope);
+  p.slots = a->slot_map;
+  p.kvcache = static_cast<uint8_t*>(a->kvcache);
+  p.kv_scales = a->kv_scales;
+  p.status = status;
+  p.latent_stride = a->latent_stride;
+  p.rope_stride = a->rope_stride;
+  p.num_tokens = a->num_tokens;
+  p.num_slots = a->num_pages * kPageSize;
+  p.is_fp8 = a->is_fp8;
+  p.is_fp4 = is_fp4;
+  cudaError_t e = launch_slot_store(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache store launch");
+  return ok();
 }
 // Tensor maps of the pair kernel over bf16 rows.
 mla_status encode_pair_maps(const void* q, long long q_rows, const void* kv, long long kv_rows, CUtensorMap* tm_q,
@@ -706,47 +771,63 @@ mla_status mla_fp8_cache_store(const void* x, int num_tokens, const int32_t* inp
 
 mla_status mla_cache_store(const mla_cache_store_args* a, mla_stream_t stream) {
   if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
+  return slot_store(*a, false, stream);
+}
+
+mla_status mla_fp4_cache_store(const mla_fp4_cache_store_args* a, mla_stream_t stream) {
+  if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
+  return slot_store(mla_cache_store_args{a->latent, a->latent_stride, a->rope, a->rope_stride, a->slot_map, a->num_tokens,
+                                         a->kvcache, a->num_pages, a->page_size, 0, nullptr},
+                    true, stream);
+}
+
+mla_status mla_cache_load(const mla_cache_load_args* a, mla_stream_t stream) {
+  if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
   if (a->num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens must be >= 0 (got %d)", a->num_tokens);
+  if (a->batch < 1) return fail(MLA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", a->batch);
+  if (a->batch > kMaxProblems)
+    return fail(MLA_ERR_UNSUPPORTED, "batch = %d exceeds the supported %d requests", a->batch, kMaxProblems);
   if (a->page_size != kPageSize) return fail(MLA_ERR_UNSUPPORTED, "page_size must be 64 (got %d)", a->page_size);
   if (a->num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages must be >= 1 (got %d)", a->num_pages);
   if (a->num_pages > kMaxPages) return fail(MLA_ERR_UNSUPPORTED, "num_pages = %d exceeds 2^31 tokens", a->num_pages);
-  if (a->is_fp8 != 0 && a->is_fp8 != 1) return fail(MLA_ERR_INVALID_ARG, "is_fp8 must be 0 or 1 (got %d)", a->is_fp8);
-  if (a->kv_scales && !a->is_fp8) return fail(MLA_ERR_INVALID_ARG, "kv_scales given with a bf16 cache (is_fp8 = 0)");
-  if (!a->kvcache) return fail(MLA_ERR_INVALID_ARG, "kvcache is NULL");
-  if (!aligned(a->kvcache, 16)) return fail(MLA_ERR_INVALID_ARG, "kvcache is not 16-byte aligned");
-  if (a->kv_scales && !aligned(a->kv_scales, 4)) return fail(MLA_ERR_INVALID_ARG, "kv_scales is not 4-byte aligned");
-  if (a->latent_stride < 0 || a->latent_stride % 8 != 0)
-    return fail(MLA_ERR_INVALID_ARG, "latent_stride must be a multiple of 8 elements (got %lld)",
-                static_cast<long long>(a->latent_stride));
-  if (a->rope_stride < 0 || a->rope_stride % 8 != 0)
-    return fail(MLA_ERR_INVALID_ARG, "rope_stride must be a multiple of 8 elements (got %lld)",
-                static_cast<long long>(a->rope_stride));
+  if (a->format < MLA_CACHE_BF16 || a->format > MLA_CACHE_FP4)
+    return fail(MLA_ERR_INVALID_ARG, "format must be a mla_cache_format (got %d)", a->format);
+  if (a->format == MLA_CACHE_FP8_TOKEN && !a->kv_scales) return fail(MLA_ERR_INVALID_ARG, "kv_scales is NULL");
+  if (a->format != MLA_CACHE_FP8_TOKEN && a->kv_scales)
+    return fail(MLA_ERR_INVALID_ARG, "kv_scales given with rows that hold their scales (format %d)", a->format);
+  if (a->block_table_stride < 1)
+    return fail(MLA_ERR_INVALID_ARG, "block_table_stride must be >= 1 (got %d)", a->block_table_stride);
+  struct Arr {
+    const void* p;
+    size_t align;
+    bool need;
+    const char* name;
+  };
+  for (const Arr& x : {Arr{a->kvcache, 16, true, "kvcache"}, Arr{a->kv_scales, 4, false, "kv_scales"},
+                       Arr{a->block_table, 4, true, "block_table"}, Arr{a->starts, 4, false, "starts"},
+                       Arr{a->row_offsets, 4, true, "row_offsets"}, Arr{a->out, 16, a->num_tokens > 0, "out"}}) {
+    if (!x.p && x.need) return fail(MLA_ERR_INVALID_ARG, "%s is NULL", x.name);
+    if (!aligned(x.p, x.align)) return fail(MLA_ERR_INVALID_ARG, "%s is not %zu-byte aligned", x.name, x.align);
+  }
   if (a->num_tokens == 0) return ok();
-  if (!a->latent) return fail(MLA_ERR_INVALID_ARG, "latent is NULL");
-  if (!a->rope) return fail(MLA_ERR_INVALID_ARG, "rope is NULL");
-  if (!a->slot_map) return fail(MLA_ERR_INVALID_ARG, "slot_map is NULL");
-  if (!aligned(a->latent, 16)) return fail(MLA_ERR_INVALID_ARG, "latent is not 16-byte aligned");
-  if (!aligned(a->rope, 16)) return fail(MLA_ERR_INVALID_ARG, "rope is not 16-byte aligned");
-  if (!aligned(a->slot_map, 4)) return fail(MLA_ERR_INVALID_ARG, "slot_map is not 4-byte aligned");
-  uint32_t* status = nullptr;
-  int sms = 0;
-  mla_status st = device_info(&status, &sms);
-  if (st != MLA_OK) return st;
-  SlotStoreParams p;
+  CacheLoadParams p;
   memset(&p, 0, sizeof p);
-  p.latent = static_cast<const uint16_t*>(a->latent);
-  p.rope = static_cast<const uint16_t*>(a->rope);
-  p.slots = a->slot_map;
-  p.kvcache = static_cast<uint8_t*>(a->kvcache);
+  int sms = 0;
+  mla_status st = device_info(&p.status, &sms);
+  if (st != MLA_OK) return st;
+  p.kvcache = static_cast<const uint8_t*>(a->kvcache);
   p.kv_scales = a->kv_scales;
-  p.status = status;
-  p.latent_stride = a->latent_stride;
-  p.rope_stride = a->rope_stride;
+  p.block_table = a->block_table;
+  p.starts = a->starts;
+  p.row_offsets = a->row_offsets;
+  p.out = static_cast<uint8_t*>(a->out);
+  p.batch = a->batch;
+  p.block_table_stride = a->block_table_stride;
+  p.num_pages = a->num_pages;
   p.num_tokens = a->num_tokens;
-  p.num_slots = a->num_pages * kPageSize;
-  p.is_fp8 = a->is_fp8;
-  cudaError_t e = launch_slot_store(p, sms, reinterpret_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "cache store launch");
+  p.format = a->format;
+  cudaError_t e = launch_cache_load(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache load launch");
   return ok();
 }
 
@@ -1029,6 +1110,81 @@ mla_status mla_window_decode(const mla_window_decode_args* a, mla_stream_t strea
   m.rows = g.rows;
   m.problems = a->batch;
   m.total_rows = static_cast<int>(qrows);
+  m.out = a->out;
+  m.lse = a->lse;
+  e = launch_merge(m, s);
+  if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
+  return ok();
+}
+
+mla_status mla_fp4_decode_workspace_size(int batch, int h_q, int s_q, size_t* bytes) {
+  if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes is NULL");
+  Geometry g{};
+  WindowLayout L{};
+  mla_status st = fp4_layout(batch, h_q, s_q, &g, &L);
+  if (st != MLA_OK) return st;
+  *bytes = L.total;
+  return ok();
+}
+
+mla_status mla_fp4_decode(const mla_fp4_decode_args* a, mla_stream_t stream) {
+  if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
+  mla_status st = check_paged(a->batch, a->q, a->kvcache, a->block_table, a->cache_seqlens, a->out, a->lse, a->num_pages,
+                              a->page_size, a->block_table_stride, a->sm_scale, 0, nullptr);
+  if (st != MLA_OK) return st;
+  if (a->window < 1) return fail(MLA_ERR_INVALID_ARG, "window must be >= 1 (got %d)", a->window);
+  if (a->sinks < 0) return fail(MLA_ERR_INVALID_ARG, "sinks must be >= 0 (got %d)", a->sinks);
+  Geometry g{};
+  WindowLayout L{};
+  st = fp4_layout(a->batch, a->h_q, a->s_q, &g, &L);
+  if (st != MLA_OK) return st;
+  st = check_workspace(a->workspace, a->workspace_bytes, L.total);
+  if (st != MLA_OK) return st;
+  DecodeParams p;
+  memset(&p, 0, sizeof p);
+  const int* clusters = nullptr;
+  st = device_info(&p.status, nullptr, nullptr, &clusters);
+  if (st != MLA_OK) return st;
+  const long long reach = std::min<long long>(a->window, kMaxWindow) + a->s_q + a->sinks;
+  const long long pages = std::min<long long>(a->block_table_stride, reach / kPageSize + 3);
+  char* ws = static_cast<char*>(a->workspace);
+  p.block_table = a->block_table;
+  p.cache_seqlens = a->cache_seqlens;
+  p.spans = reinterpret_cast<int32_t*>(ws);
+  p.tile_cost = g.tile_cost;
+  p.overhead = g.overhead;
+  p.kv_fp8 = static_cast<const uint8_t*>(a->kvcache);
+  p.out = a->out;
+  p.lse = a->lse;
+  p.o_accum = reinterpret_cast<float*>(ws + L.o_accum);
+  p.lse_accum = reinterpret_cast<float*>(ws + L.lse_accum);
+  p.timeout_ns = watchdog_ns();
+  p.batch = a->batch;
+  p.s_q = a->s_q;
+  p.h_q = a->h_q;
+  p.num_pages = a->num_pages;
+  p.block_table_stride = a->block_table_stride;
+  p.num_problems = g.num_problems;
+  p.rows = g.rows;
+  p.row_groups = g.row_groups;
+  p.num_parts = g.num_parts;
+  p.max_slots = 2 * g.num_parts;
+  p.is_causal = 1;
+  p.window = a->window < kMaxWindow ? a->window : kMaxWindow;
+  p.sinks = a->sinks;
+  p.debug_stall = g_test_debug_stall.load();
+  p.scale_log2 = a->sm_scale * 1.4426950408889634f;
+  p.cluster = window_cluster(g, pages, clusters);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_decode_fp4(a->q, p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "FP4 decode kernel launch");
+  if (p.cluster > 0) return ok();  // (the cluster has merged)
+  MergeParams m;
+  memset(&m, 0, sizeof m);
+  m.own = MergeSide{p.spans, p.o_accum, p.lse_accum, -1};
+  m.rows = g.rows;
+  m.problems = a->batch;
+  m.total_rows = a->batch * g.rows;
   m.out = a->out;
   m.lse = a->lse;
   e = launch_merge(m, s);

@@ -97,7 +97,7 @@ struct Geometry {
   int sm_count;
   int mode;          // decode kernel mode: 0 dense bf16, 1 sparse FP8, 2 dense FP8, 3 sparse bf16 rows, 4 and 5
                      // windowed 0 and 2, 6 shared prefix on CTA pairs, 7 windowed, operands in
-                     // registers
+                     // registers, 8 windowed over FP4 rows
   int pair;          // 1: CTA-pair kernel (128 rows and 128-token tiles per pair), 0: one CTA per row group
   int tile_tokens;   // tokens per schedule tile (64, or 128 for the pair kernel)
   int tile_cost;     // schedule cost of one tile (quarter units of a 64-token bf16 tile)
@@ -234,6 +234,20 @@ struct SlotStoreParams {
   int64_t latent_stride, rope_stride;
   int num_tokens, num_slots;
   int is_fp8;
+  int is_fp4;              // FP4 rows (is_fp8 is 0)
+};
+
+// Cached tokens into packed bf16 rows.
+struct CacheLoadParams {
+  const uint8_t* kvcache;
+  const float* kv_scales;      // FP8 rows with one scale per token, else NULL
+  const int32_t* block_table;
+  const int32_t* starts;       // [batch] first position of each request, or NULL: 0
+  const int32_t* row_offsets;  // [batch + 1]
+  uint8_t* out;                // bf16 [num_tokens, 576]
+  uint32_t* status;
+  int batch, block_table_stride, num_pages, num_tokens;
+  int format;                  // mla_cache_format
 };
 
 // Lets launches of a kernel whose shared memory varies from call to call have
@@ -256,6 +270,8 @@ cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, con
 // (tm_kv: bf16 rows alone)
 cudaError_t launch_decode_rows(const CUtensorMap& tm_kv, const void* q, const DecodeParams& p, bool is_fp8,
                                cudaStream_t stream);
+// Windowed decode over FP4 rows (mla_decode_fp4.cu)
+cudaError_t launch_decode_fp4(const void* q, const DecodeParams& p, cudaStream_t stream);
 // mode: 0 dense bf16 cache, 1 sparse FP8 cache, 2 dense FP8 cache, 3 sparse bf16 rows, 4 and 5 windowed dense
 // over the bf16 and the FP8 cache
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const DecodeParams& p, int rpc,
@@ -288,6 +304,7 @@ cudaError_t launch_fp8_cache_store(const uint16_t* x, int num_tokens, const int3
                                    int block_table_stride, uint8_t* kvcache, int num_pages, uint32_t* status,
                                    int sm_count, cudaStream_t stream);
 cudaError_t launch_slot_store(const SlotStoreParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_cache_load(const CacheLoadParams& p, int sm_count, cudaStream_t stream);
 // in_place: the lengths or the cursor are updated in the arrays they are read from
 cudaError_t launch_assign_pages(const AssignPagesParams& p, bool in_place, int sm_count, cudaStream_t stream);
 cudaError_t launch_index(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const IndexParams& p, int topk,

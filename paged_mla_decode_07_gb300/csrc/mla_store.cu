@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include "mla_device.cuh"
+#include "mla_fp4.cuh"
 #include "mla_internal.h"
 
 namespace mla {
@@ -234,6 +235,56 @@ __global__ void __launch_bounds__(kStoreWarps * 32) slot_store_fp8_kernel(const 
   }
 }
 
+// FP4 rows (mla_fp4.cuh): lane l quantises values [16 l, 16 l + 16), two lanes
+// share a block of 32 and its scale.  Scaling by a power of two is exact, so
+// the code's rounding is the only one.  Memory-bound: 1152 bytes read and 400
+// written per token.
+__device__ __forceinline__ void store_fp4_row(uint8_t* dst, const uint4 a, const uint4 c, const uint4 rp, int lane) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  float v[16];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+    amax = fmaxf(amax, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  const int e = fp4_exponent(amax);
+  const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] *= down;
+  reinterpret_cast<uint2*>(dst)[lane] = make_uint2(fp4_word(e2m1x8(v)), fp4_word(e2m1x8(v + 8)));
+  if ((lane & 1) == 0) dst[kFp4ScaleOffset + (lane >> 1)] = static_cast<uint8_t>(e + 127);
+  if (lane < 8) reinterpret_cast<uint4*>(dst + kFp4RopeOffset)[lane] = rp;
+}
+
+// T tokens per warp at a time, as in the bf16 rows' store below.
+template <int T>
+__global__ void __launch_bounds__(kStoreWarps * 32) slot_store_fp4_kernel(const SlotStoreParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kStoreWarps * T;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kStoreWarps + (threadIdx.x >> 5)) * T; t0 < p.num_tokens;
+       t0 += step) {
+    uint4 a[T], c[T], rp[T];
+    int slot[T];
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+      slot[k] = -1;
+      if (t0 + k >= p.num_tokens) continue;
+      slot[k] = slot_of(p, static_cast<int>(t0) + k, lane == 0);
+      const uint16_t* s = p.latent + (t0 + k) * p.latent_stride + 16 * lane;
+      a[k] = ld_global_nc_v4(s);
+      c[k] = ld_global_nc_v4(s + 8);
+      if (lane < 8) rp[k] = ld_global_nc_v4(p.rope + (t0 + k) * p.rope_stride + 8 * lane);
+    }
+#pragma unroll
+    for (int k = 0; k < T; ++k)
+      if (slot[k] >= 0)
+        store_fp4_row(p.kvcache + static_cast<int64_t>(slot[k]) * kFp4RowBytes, a[k], c[k], rp[k], lane);
+  }
+}
+
 // bf16 rows, copied as they are: a warp takes T consecutive tokens at a time,
 // all loads issued before the first store.  Long stores run at the copy's pace
 // only if neighbouring rows are in flight together (65535 tokens alone, the
@@ -275,11 +326,15 @@ cudaError_t launch_slot_store(const SlotStoreParams& p, int sm_count, cudaStream
   const int64_t max_grid = sm_count * 8;
   const int threads = kStoreWarps * 32;
   // one token per warp until every warp of a full grid has one
-  const bool four = !p.is_fp8 && p.num_tokens > max_grid * kStoreWarps;
+  const bool four = (!p.is_fp8 || p.is_fp4) && p.num_tokens > max_grid * kStoreWarps;
   const int per_block = kStoreWarps * (four ? 4 : 1);
   const int64_t need = (static_cast<int64_t>(p.num_tokens) + per_block - 1) / per_block;
   const unsigned grid = static_cast<unsigned>(need < max_grid ? need : max_grid);
-  if (p.is_fp8 && p.kv_scales) {
+  if (p.is_fp4 && four) {
+    slot_store_fp4_kernel<4><<<grid, threads, 0, stream>>>(p);
+  } else if (p.is_fp4) {
+    slot_store_fp4_kernel<1><<<grid, threads, 0, stream>>>(p);
+  } else if (p.is_fp8 && p.kv_scales) {
     slot_store_fp8_kernel<true><<<grid, threads, 0, stream>>>(p);
   } else if (p.is_fp8) {
     slot_store_fp8_kernel<false><<<grid, threads, 0, stream>>>(p);
