@@ -248,6 +248,19 @@ mla_status encode_e4m3_rows_map(CUtensorMap* map, const void* base, long long nr
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// FP4 rows as [rows][200] 16-bit words, boxes of a page's 64 rows: the codes and
+// scales (272 bytes) as they lie, or the RoPE values (128 bytes) in the 128-byte
+// swizzle of a K-major operand.
+mla_status encode_fp4_map(CUtensorMap* map, const void* base, long long nrows, bool rope) {
+  cuuint64_t dims[2] = {200, static_cast<cuuint64_t>(nrows)};
+  cuuint64_t strides[1] = {400};
+  cuuint32_t box[2] = {rope ? 64u : 136u, kPageSize};
+  cuuint32_t estr[2] = {1, 1};
+  return encode_map("kvcache", map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, rope ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 uint64_t watchdog_ns() {
@@ -371,16 +384,19 @@ mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, long long page
   return MLA_OK;
 }
 
-// Windowed decode over FP4 rows: 16 query rows a CTA, two CTAs an SM, tiles of
-// 128 keys.
+// Windowed decode over FP4 rows: 16 or 32 query rows a CTA, tiles of 128 keys.
 mla_status fp4_layout(int batch, int h_q, int s_q, Geometry* g, WindowLayout* L) {
   mla_status st = geometry(batch, h_q, s_q, 0, 0, g);
   if (st != MLA_OK) return st;
-  rows_geometry(g);
+  g->rpc = g->rows > 16 ? 32 : 16;
+  g->row_groups = (g->rows + g->rpc - 1) / g->rpc;
+  g->pair = 0;
   g->mode = 8;
   g->tile_tokens = 128;
+  g->tile_cost = 4;
+  g->overhead = 8;
   const int forced = g_test_num_parts.load();
-  g->num_parts = forced > 0 ? forced : 2 * g->sm_count / g->row_groups;
+  g->num_parts = forced > 0 ? forced : g->sm_count / g->row_groups;
   if (g->num_parts < 1) g->num_parts = 1;
   const size_t slots = 2 * static_cast<size_t>(g->num_parts);
   L->o_accum = align256(static_cast<size_t>(g->num_problems) * 2 * sizeof(int32_t));
@@ -1170,13 +1186,19 @@ mla_status mla_fp4_decode(const mla_fp4_decode_args* a, mla_stream_t stream) {
   p.num_parts = g.num_parts;
   p.max_slots = 2 * g.num_parts;
   p.is_causal = 1;
+  p.evict_first = g.row_groups == 1 ? 1 : 0;
   p.window = a->window < kMaxWindow ? a->window : kMaxWindow;
   p.sinks = a->sinks;
   p.debug_stall = g_test_debug_stall.load();
   p.scale_log2 = a->sm_scale * 1.4426950408889634f;
   p.cluster = window_cluster(g, pages, clusters);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_decode_fp4(a->q, p, s);
+  CUtensorMap tm_codes, tm_rope;
+  const long long cache_rows = static_cast<long long>(a->num_pages) * kPageSize;
+  st = encode_fp4_map(&tm_codes, a->kvcache, cache_rows, false);
+  if (st == MLA_OK) st = encode_fp4_map(&tm_rope, a->kvcache, cache_rows, true);
+  if (st != MLA_OK) return st;
+  cudaError_t e = launch_decode_fp4(tm_codes, tm_rope, a->q, p, g.rpc, s);
   if (e != cudaSuccess) return cuda_fail(e, "FP4 decode kernel launch");
   if (p.cluster > 0) return ok();  // (the cluster has merged)
   MergeParams m;

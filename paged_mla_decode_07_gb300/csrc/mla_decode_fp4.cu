@@ -2,31 +2,32 @@
 //
 // A key's latent values are E2M1 codes times powers of two, and so E5M2
 // numbers: the rows become 8-bit operands exactly, at half the shared memory
-// and half the tensor time of bf16 ones.  The other operands are split into
+// and half the operand traffic of bf16 ones.  The other operands are split into
 // 8-bit terms:
 //   q (bf16, 8 significant bits), times a power of two that puts the row's
 //     largest value into [128, 256): hi = E4M3(q), lo = E4M3(q - hi).  Exact for
 //     values down to 2^-9 of that largest one, off by 2^-18 of it below.
-//   P (fp32): three E5M2 terms of P * 2^12, each of what the last one left:
-//     relative 2^-9 (what rounding to bf16 gives) down to P = 2^-23, and the
-//     32 binades of E5M2 keep the weights of keys far below the largest one.
-// The terms stand beside each other as columns of one MMA (N = 32 and 48 for 16
-// rows, where N up to 64 costs the same time as 16) and are added in fp32 after it.
+//   P (fp32): three E5M2 terms of P * 2^8, each of what the last one left:
+//     relative 2^-9 (what rounding to bf16 gives) down to P = 2^-18, and some of
+//     it down to 2^-25: the weights of many keys far below the largest are kept.
+// The terms stand beside each other as columns of one MMA (N = 2 R and 3 R for R
+// = 16 or 32 query rows, where N up to 64 costs the same time as 16) and are
+// added in fp32 after it.
 //
-//   S^T [128 tokens, hi 16 | lo 16] = K [128, 512] Q^T     16 MMAs, K = 32
-//   S^T [128 tokens, hi 16]        += K_rope Q_rope^T      4 bf16 MMAs, K = 16
-//   O^T [128 dims, 48] x 4         += V^T P^T              16 MMAs, K = 32 tokens
+//   S^T [128 tokens, hi R | lo R] = K [128, 512] Q^T     16 MMAs, K = 32
+//   S^T [128 tokens, hi R]       += K_rope Q_rope^T      4 bf16 MMAs, K = 16
+//   O^T [128 dims, 3 R] x 4      += V^T P^T              16 MMAs, K = 32 tokens
 // with V = the same tile, read MN-major.
 //
-// One CTA has 16 query rows and 256 threads, which all do the same: convert the
-// tile whose codes wait in their registers into shared memory and issue the
-// loads of the next one; S; softmax; O.  Two CTAs share an SM, so that one
-// converts while the other's products run, and each has a whole tile (51 KB) in
-// flight: neither warp roles nor more buffers.  A tile is 128 keys, two pages
-// of the walk over sinks and window.
+// A tile is 128 keys, two pages of the walk over sinks and window.  Roles: a
+// warp copies codes and scales of the pages into a ring (and brings the pages
+// further on into L2), one copies the RoPE values into the tile, sixteen warps
+// turn codes into the tile's E5M2 values, one issues the products of S, one those
+// of O, eight have the softmax and the results.  Two tile buffers, whose chunks
+// are handed on in pairs.
 //
-// Every wait is bounded (watchdog); after one that ran out all threads of the
-// CTA leave together, with its products drained and its tensor memory freed.
+// Every wait is bounded (watchdog); after one that ran out every role leaves,
+// copies and products are drained and the tensor memory is freed.
 #include "mla_cluster.cuh"
 #include "mla_device.cuh"
 #include "mla_fp4.cuh"
@@ -36,39 +37,73 @@
 namespace mla {
 namespace {
 
-constexpr int kRows = 16;      // query rows of a CTA
-constexpr int kTile = 128;     // keys of a tile
-constexpr int kThreads = 256;  // warps w and w + 4 share the tokens 32 (w % 4) ..; rows 8 (w / 4) ..
-constexpr int kPerTok = kThreads / 16, kToks = kTile / kPerTok;  // 16 threads a token; 8 tokens a thread
-constexpr int kChunkBytes = kTile * 128;                         // 128 dims of all keys
-constexpr int kRopeOff = 4 * kChunkBytes;
-constexpr int kQOff = kRopeOff + kChunkBytes;        // hi rows, lo rows: 4 chunks of [32][128]
-constexpr int kQChunk = 2 * kRows * 128;
-constexpr int kQRopeOff = kQOff + 4 * kQChunk;       // bf16 [16][64]
-constexpr int kPOff = kQRopeOff + kRows * 128;       // [48][128 tokens]
-constexpr int kAuxOff = kPOff + 3 * kRows * 128;
-// aux: row maxima or sums of the four token groups [2][4][8], score factors [16], lse [16], barriers
-constexpr int kRedOff = kAuxOff;
-constexpr int kFactorOff = kRedOff + 2 * 4 * 8 * 4;
-constexpr int kLseOff = kFactorOff + kRows * 4;
-constexpr int kInvOff = kLseOff + kRows * 4;
-constexpr int kWeightsOff = kInvOff + kRows * 4;  // cluster merge
-constexpr int kMiscOff = kWeightsOff + kMaxCluster * (kRows + 1) * 4;  // abort flag, TMEM base, offset of O (0)
-constexpr int kBarOff = kMiscOff + 16;
-constexpr int kSmemBytes = kBarOff + 2 * 8 + 1024;  // + alignment slack
-static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs on an SM");
-static_assert(kBarOff % 8 == 0 && kAuxOff % 16 == 0, "alignment");
-constexpr uint32_t kTmemCols = 256, kSCol = 0, kOCol = 64;
-constexpr float kPScale = 4096.f;  // P <= 2^kRescale goes into its terms times this, 2^15 at most
-constexpr float kRescale = 3.f;    // log2 units that a score may pass the reference by before it is raised
+constexpr int kTile = 128;                // keys of a tile
+constexpr int kChunkBytes = kTile * 128;  // 128 dims of all keys
+constexpr int kTileBytes = 4 * kChunkBytes;
+constexpr int kRawRow = kFp4RopeOffset;   // codes and scales; 17 16-byte units, so rows lie on different banks
+constexpr int kRawBytes = kPageSize * kRawRow;
+constexpr int kConvWarps = 16, kSoftWarps = 8;
+constexpr int kThreads = 32 * (4 + kConvWarps + kSoftWarps);
+constexpr uint32_t kLaunchRegs = 72;
+constexpr int kFactors = 4;  // segments whose score factors are kept
+constexpr int kFlags = 4;    // tiles whose page states are kept
+constexpr int kAhead = 6;    // pages brought into L2 ahead of their copy
+
+template <int R>
+struct Cfg {
+  // setmaxnreg hands out what the block was launched with and waits for ever for more
+  static constexpr uint32_t kRegsCtl = 56, kRegsConv = R == 16 ? 64 : 56, kRegsSoft = R == 16 ? 96 : 112;
+  static_assert(kRegsCtl + 4 * kRegsConv + 2 * kRegsSoft <= 7 * kLaunchRegs && kThreads * kLaunchRegs <= 65536,
+                "register split");
+  static constexpr int kRaw = R == 16 ? 2 : 1;    // pages of the ring
+  static constexpr int kPBufs = R == 16 ? 2 : 1;  // buffers of P
+  static constexpr int kRows = R / 2;             // rows of a softmax thread
+  static constexpr int kRopeOff = 2 * kTileBytes;
+  static constexpr int kQOff = kRopeOff + 2 * kChunkBytes;  // hi rows, lo rows: 4 chunks of [2 R][128]
+  static constexpr int kQChunk = 2 * R * 128;
+  static constexpr int kQRopeOff = kQOff + 4 * kQChunk;  // bf16 [R][64]
+  static constexpr int kPOff = kQRopeOff + R * 128;      // [3 R / 16][128 tokens][16 rows]
+  static constexpr int kPBytes = 3 * R * 128;
+  static constexpr int kRawOff = kPOff + kPBufs * kPBytes;
+  static constexpr int kAuxOff = kRawOff + kRaw * kRawBytes;
+  // aux: row maxima or sums of the four token groups [2 tiles][2][4][R / 2], score
+  // factors [kFactors][R], lse [R], page states [kFlags][2] and [kRaw], abort flag,
+  // TMEM base, offset of O (0), barriers
+  static constexpr int kRedOff = kAuxOff;
+  static constexpr int kFactorOff = kRedOff + 2 * 4 * R * 4;
+  static constexpr int kLseOff = kFactorOff + kFactors * R * 4;
+  static constexpr int kFlagOff = kLseOff + R * 4;
+  static constexpr int kRawFlagOff = kFlagOff + kFlags * 2 * 4;
+  static constexpr int kMiscOff = kRawFlagOff + 2 * 4;
+  static constexpr int kBarOff = (kMiscOff + 12 + 7) / 8 * 8;
+  static constexpr int kNumBars = 2 * kRaw + 2 * 3 + 4 * 2 + 1;
+  // (1024 bytes of alignment; R = 32 has 16 fewer to spare and needs none: dynamic
+  // shared memory without static variables starts at its multiple, which the kernel checks)
+  static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + (R == 16 ? 1024 : 0);
+  static constexpr uint32_t kTmemCols = R == 16 ? 256 : 512;
+  static constexpr uint32_t kSCol = 0, kOCol = 4 * R;
+  static_assert(4 * R + 12 * R <= static_cast<int>(kTmemCols), "tensor memory");
+  static_assert(kBarOff % 8 == 0 && kAuxOff % 16 == 0 && kRawOff % 128 == 0, "alignment");
+  static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(schedule_scratch(kMaxProblems) <= kAuxOff, "a schedule is made where the tiles will be");
+  static_assert(kMaxCluster * (R + 1) * 4 <= kPBytes, "weights of a cluster's merge, in P's place");
+};
+constexpr float kPLog2 = 8.f;      // P is held at 2^8 times its value, 2^15 at most
+constexpr float kRescale = 7.f;    // log2 units that a score may pass the reference by before it is raised
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr uint32_t kHalfBar = 1;   // named barriers of the softmax warps of a half of the rows
 
 // kind::f8f6f4, fp32 accumulation; formats 0 E4M3, 1 E5M2
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_format, int b_format, int a_mn_major) {
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_format, int b_format, int mn_major) {
   return (1u << 4) | (static_cast<uint32_t>(a_format) << 7) | (static_cast<uint32_t>(b_format) << 10) |
-         (static_cast<uint32_t>(a_mn_major) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(mn_major) * (3u << 15)) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
+// P lies MN-major without swizzle: 128-byte blocks of 8 tokens with 16 rows
+// each, those of the next tokens behind them (leading offset), those of the next
+// 16 rows 2 KB on (stride offset): a thread writes its rows of a token at once.
+constexpr uint64_t kHiP = (static_cast<uint64_t>(128 >> 4) << 16) | (static_cast<uint64_t>(2048 >> 4) << 32) |
+                          (static_cast<uint64_t>(1) << 46);
 __device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
@@ -89,157 +124,235 @@ __device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
 }
 // An E5M2 number is the upper byte of the fp16 number of its value.
 __device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint32_t codes) { return __byte_perm(codes, 0, 0x1404); }
-__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+  if constexpr (N == 8)
+    tmem_ld_x8(taddr, v);
+  else
+    tmem_ld_x16(taddr, v);
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[16]) { tmem_st_x16(taddr, v); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
 }
 
-// Reduces eight values per lane over the warp; lane l ends with value
-// ((l >> 4) & 1) * 4 + ((l >> 3) & 1) * 2 + ((l >> 2) & 1).
-template <class Op>
-__device__ __forceinline__ float reduce8(const float (&x)[8], int lane, Op op) {
-  float a[4], b[2];
+// Reduces N values per lane over the warp; lane l ends with value l / (32 / N).
+template <int N, class Op>
+__device__ __forceinline__ float reduce_rows(const float (&x)[N], int lane, Op op) {
+  float v[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool up = lane & 16;
-    a[i] = op(up ? x[4 + i] : x[i], __shfl_xor_sync(0xffffffffu, up ? x[i] : x[4 + i], 16));
+  for (int i = 0; i < N; ++i) v[i] = x[i];
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = op(up ? v[n + i] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[n + i], o));
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const bool up = lane & 8;
-    b[i] = op(up ? a[2 + i] : a[i], __shfl_xor_sync(0xffffffffu, up ? a[i] : a[2 + i], 8));
-  }
-  const bool up = lane & 4;
-  float c = op(up ? b[1] : b[0], __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4));
-  c = op(c, __shfl_xor_sync(0xffffffffu, c, 2));
-  return op(c, __shfl_xor_sync(0xffffffffu, c, 1));
+  for (; o >= 1; o /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
 }
 
-// What a thread holds of a tile on its way from global memory: 16 bytes of
-// codes and a scale byte of eight tokens, 16 bytes of RoPE values of four.
-struct Staged {
-  uint4 code[kToks];
-  uint32_t scale[kToks];
-  uint4 rope[kToks / 2];
+struct Bars {
+  uint64_t* raw_full;   // [kRaw] codes and scales of a page have landed
+  uint64_t* raw_empty;  // [kRaw] the conversion warps have read them
+  uint64_t* rope_full;  // [2] RoPE values of a tile have landed
+  uint64_t* k_full;     // [2][2] values of a tile's pair of chunks (and of Q, before a segment's first) are written
+  uint64_t* s_full;     // [2] scores of a tile are in tensor memory
+  uint64_t* p_full;     // [2] P of a tile is written (and its scores read)
+  uint64_t* done;       // [2][2] the products of O of a pair are done: the pair (after the second P) is free
+  uint64_t* o_free;     // O of a segment has been read
 };
 
-struct Element {
+// What a CTA has of problem `prob`: pages pb .. pe of its walk.
+struct Segment {
   const int32_t* table;
-  int prob, L;
+  int L, pb, pe;
   KeyWalk walk;
 };
-
-// Page ids of pages j and j + 1 of the walk; those past `end` (no page of this
-// CTA) are -1.
-__device__ __forceinline__ int2 page_ids(const DecodeParams& p, const Element& e, int j, int end) {
-  int id[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int lp = j + i < end ? e.walk.page(j + i) : -1;
-    id[i] = lp >= 0 && lp < p.block_table_stride ? __ldg(e.table + lp) : -1;
+struct Range {
+  PartRecord rec;
+  int last;
+  __device__ bool get(const DecodeParams& p, int prob, Segment& s) const {
+    s.L = p.cache_seqlens[prob];
+    s.table = p.block_table + static_cast<int64_t>(prob) * p.block_table_stride;
+    s.walk = key_walk(s.L, p.s_q, p.window, p.sinks, p.block_table_stride);
+    const int unit = p.cluster > 0 ? 1 : 2;  // (clusters share out pages, schedules tiles)
+    s.pb = prob == rec.p0 ? unit * rec.t0 : 0;
+    s.pe = prob == rec.p1 ? min(unit * rec.t1, s.walk.pages) : s.walk.pages;
+    return s.pb < s.pe;
   }
-  return make_int2(id[0], id[1]);
+};
+// Page id of page j of the segment, -1 if it has none that is usable.
+__device__ __forceinline__ int page_id(const DecodeParams& p, const Segment& s, int j) {
+  if (j >= s.pe) return -1;
+  const int lp = s.walk.page(j);
+  const int id = lp < p.block_table_stride ? __ldg(s.table + lp) : -1;
+  return id >= 0 && id < p.num_pages ? id : -1;
 }
 
-// Whether some row sees key t, and whether every row sees all keys of a page.
+// Whether some row sees key t; whether some row sees each key of a page; whether every row sees all of them.
 __device__ __forceinline__ bool key_seen(const DecodeParams& p, int t, int L) {
   return t < L && key_in_walk(t, L, p.s_q, p.window, p.sinks);
+}
+__device__ __forceinline__ bool page_used(const DecodeParams& p, int page, int L) {
+  const int first = page * kPageSize, last = first + kPageSize - 1, past = L - p.s_q - p.window;
+  return last < L && (last < p.sinks || first > past || p.sinks > past);
 }
 __device__ __forceinline__ bool page_whole(const DecodeParams& p, int page, int L) {
   const int first = page * kPageSize, last = first + kPageSize - 1;
   if (last > L - p.s_q) return false;  // the first query token sees keys up to L - s_q
   return last < p.sinks || first > L - 1 - p.window;
 }
-__device__ __forceinline__ bool page_all_used(const DecodeParams& p, int page, int L) {
-  const int first = page * kPageSize, last = first + kPageSize - 1;
-  return last < L && (last < p.sinks || first > L - p.s_q - p.window || p.sinks > L - p.s_q - p.window);
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wd));
+}
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > wd.limit_ns) break;
 }
 
-// Issue the loads of pages j, j + 1 (page ids `id`).  Tokens that no row sees
-// are zeros, whatever their rows hold.
-__device__ __forceinline__ void stage(const DecodeParams& p, const Element& e, int j, int end, int2 id, Staged& s) {
-  const int c = threadIdx.x & 15, t0 = threadIdx.x >> 4;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int pg = h ? id.y : id.x;
-    const bool real = j + h < end && pg >= 0 && pg < p.num_pages;
-    const int lp = j + h < end ? e.walk.page(j + h) : 0;
-    const bool all = real && page_all_used(p, lp, e.L);
-    const uint8_t* base = p.kv_fp8 + static_cast<int64_t>(real ? pg : 0) * (kPageSize * kFp4RowBytes);
-#pragma unroll
-    for (int i = 0; i < kToks / 2; ++i) {
-      const int t = t0 + kPerTok * i;
-      const bool ok = all || (real && key_seen(p, lp * kPageSize + t, e.L));
-      const uint8_t* row = base + t * kFp4RowBytes;
-      s.code[4 * h + i] = ok ? ld_global_nc_v4(row + 16 * c) : zero;
-      s.scale[4 * h + i] = ok ? __ldg(row + kFp4ScaleOffset + c) : 0u;
+// ---------------------------------------------------------------------------
+// copies: codes and scales (one warp), RoPE values (one warp)
+// ---------------------------------------------------------------------------
+template <int R>
+__device__ void copy_codes(const CUtensorMap* tm, const DecodeParams& p, const Range& rg, uint8_t* smem, const Bars& bars,
+                           const Watchdog& wd) {
+  using C = Cfg<R>;
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol = p.evict_first ? l2_policy_evict_first() : l2_policy_evict_normal();
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + C::kRawFlagOff);
+  int u = 0;
+#pragma unroll 1
+  for (int prob = rg.rec.p0; prob <= rg.last; ++prob) {
+    Segment s;
+    if (!rg.get(p, prob, s)) continue;
+    int ids = -1, next = page_id(p, s, s.pb + lane);  // of 32 pages from j0 on, and of the 32 behind them
+    int j0 = s.pb - 32;
+#pragma unroll 1
+    for (int j = s.pb; j < s.pe; ++j, ++u) {
+      if (j - j0 == 32) {
+        j0 = j;
+        ids = next;
+        next = page_id(p, s, j + 32 + lane);
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, j - j0), slot = u % C::kRaw;
+      if (u >= C::kRaw && !wait_warp(bars.raw_empty + slot, ((u / C::kRaw) - 1) & 1, wd)) goto out;
+      if (lane == 0) {
+        if (id < 0) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
+        flags[slot] = id;
+        mbar_arrive_expect_tx(bars.raw_full + slot, id < 0 ? 0 : kRawBytes);
+        if (id >= 0)
+          tma_load_2d(smem + C::kRawOff + slot * kRawBytes, tm, bars.raw_full + slot, 0, id * kPageSize, pol);
+      }
+      __syncwarp();
+      // page j + kAhead into L2 (64 pages are known from j0 on); a segment's first pages come as they are copied
+      const int at = j - j0 + kAhead;
+      const int far = at < 32 ? __shfl_sync(0xffffffffu, ids, at) : __shfl_sync(0xffffffffu, next, at - 32);
+      if (lane == 0 && far >= 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                         p.kv_fp8 + static_cast<int64_t>(far) * (kPageSize * kFp4RowBytes)),
+                     "r"(kPageSize * kFp4RowBytes)
+                     : "memory");
     }
-    // RoPE: eight threads a token
+  }
+out:
+  // no copy may be in flight when the CTA ends
+  if (lane == 0)
+    for (int i = u > C::kRaw ? u - C::kRaw : 0; i < u; ++i) drain(bars.raw_full + i % C::kRaw, (i / C::kRaw) & 1, wd);
+  __syncwarp();
+}
+
+template <int R>
+__device__ void copy_rope(const CUtensorMap* tm, const DecodeParams& p, const Range& rg, uint8_t* smem, const Bars& bars,
+                          const Watchdog& wd) {
+  using C = Cfg<R>;
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol = p.evict_first ? l2_policy_evict_first() : l2_policy_evict_normal();
+  int i = 0;  // tiles
+#pragma unroll 1
+  for (int prob = rg.rec.p0; prob <= rg.last; ++prob) {
+    Segment s;
+    if (!rg.get(p, prob, s)) continue;
+    int id[2], next[2];
 #pragma unroll
-    for (int i = 0; i < kToks / 4; ++i) {
-      const int t = (threadIdx.x >> 3) + 32 * i;
-      const bool ok = all || (real && key_seen(p, lp * kPageSize + t, e.L));
-      s.rope[2 * h + i] = ok ? ld_global_nc_v4(base + t * kFp4RowBytes + kFp4RopeOffset + 16 * (threadIdx.x & 7)) : zero;
+    for (int h = 0; h < 2; ++h) next[h] = page_id(p, s, s.pb + h);
+#pragma unroll 1
+    for (int j = s.pb; j < s.pe; j += 2, ++i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        id[h] = next[h];
+        next[h] = page_id(p, s, j + 2 + h);
+      }
+      const int b = i & 1;
+      if (i >= 2 && !wait_warp(bars.s_full + b, ((i >> 1) - 1) & 1, wd)) goto out;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bars.rope_full + b, ((id[0] >= 0) + (id[1] >= 0)) * (kChunkBytes / 2));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (id[h] >= 0)
+            tma_load_2d(smem + C::kRopeOff + b * kChunkBytes + h * (kChunkBytes / 2), tm, bars.rope_full + b,
+                        kFp4RopeOffset / 2, id[h] * kPageSize, pol);
+      }
+      __syncwarp();
     }
   }
+out:
+  if (lane == 0)
+    for (int k = i > 2 ? i - 2 : 0; k < i; ++k) drain(bars.rope_full + (k & 1), (k >> 1) & 1, wd);
+  __syncwarp();
 }
 
-// Codes to E5M2 values in the 128-byte swizzle: block c of a token is the 16-byte
-// units 2 (c % 4), 2 (c % 4) + 1 of its row of chunk c / 4.  Threads of odd chunks
-// store their second unit first, so that eight of them touch all banks.
-__device__ __forceinline__ void convert(const Staged& s, uint32_t smem) {
-  const int c = threadIdx.x & 15, t0 = threadIdx.x >> 4;
-  const uint32_t chunk = smem + (c >> 2) * kChunkBytes;
-  const int u0 = 2 * (c & 3) + ((c >> 2) & 1);
-#pragma unroll
-  for (int i = 0; i < kToks; ++i) {
-    const int t = t0 + kPerTok * i;
-    const uint2 lut = fp4_lut(fp4_scale_index(s.scale[i]));
-    const uint2 a = fp4_e5m2(s.code[i].x, lut), b = fp4_e5m2(s.code[i].y, lut);
-    const uint2 d = fp4_e5m2(s.code[i].z, lut), f = fp4_e5m2(s.code[i].w, lut);
-    const uint32_t row = chunk + t * 128;
-    const bool odd = (c >> 2) & 1;
-    st_shared_v4(row + ((u0 ^ (t & 7)) << 4), odd ? d.x : a.x, odd ? d.y : a.y, odd ? f.x : b.x, odd ? f.y : b.y);
-    st_shared_v4(row + (((u0 ^ 1) ^ (t & 7)) << 4), odd ? a.x : d.x, odd ? a.y : d.y, odd ? b.x : f.x, odd ? b.y : f.y);
-  }
-#pragma unroll
-  for (int i = 0; i < kToks / 2; ++i) {
-    const int t = (threadIdx.x >> 3) + 32 * i;
-    st_shared_v4(smem + kRopeOff + t * 128 + (((threadIdx.x & 7) ^ (t & 7)) << 4), s.rope[i].x, s.rope[i].y, s.rope[i].z,
-                 s.rope[i].w);
-  }
-}
-
-// The 16 query rows: hi and lo terms, RoPE values, and what a score is to be
-// multiplied by.  16 threads a row, 32 latent and 4 RoPE dims each.
-__device__ __forceinline__ void load_queries(const __nv_bfloat16* q, const DecodeParams& p, int prob, int g, uint8_t* smem) {
-  const int r = threadIdx.x >> 4, c = threadIdx.x & 15, row = g * kRows + r;
+// ---------------------------------------------------------------------------
+// conversion warps
+// ---------------------------------------------------------------------------
+// The R query rows: hi and lo terms, RoPE values, and what a score is to be
+// multiplied by.  512 / R threads a row.
+template <int R>
+__device__ __forceinline__ void load_queries(const __nv_bfloat16* q, const DecodeParams& p, int prob, int g, uint8_t* smem,
+                                             float* factor) {
+  using C = Cfg<R>;
+  constexpr int kPer = 512 / R, kUnits = 32 / kPer, kRope = 32 / kPer;  // threads a row; 16 dims, RoPE pairs a thread
+  const int ct = threadIdx.x - 128;
+  const int r = ct / kPer, c = ct % kPer, row = g * R + r;
   const bool real = row < p.rows;
   const uint4* src = reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(prob) * p.rows + (real ? row : 0)) * kDqk);
-  uint32_t w[16];
-  uint2 rope = make_uint2(0, 0);
+  uint32_t w[8 * kUnits], rope[kRope];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = real ? __ldg(src + 4 * c + i) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < 2 * kUnits; ++i) {
+    const uint4 v = real ? __ldg(src + 2 * kUnits * c + i) : make_uint4(0, 0, 0, 0);
     w[4 * i] = v.x;
     w[4 * i + 1] = v.y;
     w[4 * i + 2] = v.z;
     w[4 * i + 3] = v.w;
   }
-  if (real) rope = __ldg(reinterpret_cast<const uint2*>(src + 64) + c);
+#pragma unroll
+  for (int i = 0; i < kRope; ++i) rope[i] = real ? __ldg(reinterpret_cast<const uint32_t*>(src + 64) + c * kRope + i) : 0u;
   auto lo_of = [](uint32_t x) { return __uint_as_float(x << 16); };
   auto hi_of = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
-  float amax = max_nan(max_nan(fabsf(lo_of(rope.x)), fabsf(hi_of(rope.x))), max_nan(fabsf(lo_of(rope.y)), fabsf(hi_of(rope.y))));
+  float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max_nan(amax, max_nan(fabsf(lo_of(w[i])), fabsf(hi_of(w[i]))));
+  for (int i = 0; i < kRope; ++i) amax = max_nan(amax, max_nan(fabsf(lo_of(rope[i])), fabsf(hi_of(rope[i]))));
 #pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int i = 0; i < 8 * kUnits; ++i) amax = max_nan(amax, max_nan(fabsf(lo_of(w[i])), fabsf(hi_of(w[i]))));
+#pragma unroll
+  for (int o = kPer / 2; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   // 2^k: the largest value to [128, 256), k within what a float's exponent holds both ways
   const int k = amax > 0.f ? min(max(134 - static_cast<int>(__float_as_uint(amax) >> 23), -120), 120) : 0;
   const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-  const uint32_t base = smem_u32(smem) + kQOff + (c >> 2) * kQChunk;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {  // 16 dims each
+  for (int u = 0; u < kUnits; ++u) {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -255,332 +368,527 @@ __device__ __forceinline__ void load_queries(const __nv_bfloat16* q, const Decod
       hi[i] = h[0] | (h[1] << 16);
       lo[i] = l[0] | (l[1] << 16);
     }
-    const uint32_t at = base + r * 128 + (((2 * (c & 3) + u) ^ (r & 7)) << 4);
+    const int d = kUnits * c + u;  // 16-byte unit of the row's 32
+    const uint32_t at = smem_u32(smem) + C::kQOff + (d >> 3) * C::kQChunk + r * 128 + (((d & 7) ^ (r & 7)) << 4);
     st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-    st_shared_v4(at + kRows * 128, lo[0], lo[1], lo[2], lo[3]);
+    st_shared_v4(at + R * 128, lo[0], lo[1], lo[2], lo[3]);
   }
-  const uint32_t at = smem_u32(smem) + kQRopeOff + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1);
-  st_shared_u32(at, pack_bf16x2(lo_of(rope.x) * up, hi_of(rope.x) * up));
-  st_shared_u32(at + 4, pack_bf16x2(lo_of(rope.y) * up, hi_of(rope.y) * up));
+#pragma unroll
+  for (int i = 0; i < kRope; ++i) {
+    const int word = kRope * c + i;
+    st_shared_u32(smem_u32(smem) + C::kQRopeOff + r * 128 + (((word >> 2) ^ (r & 7)) << 4) + 4 * (word & 3),
+                  pack_bf16x2(lo_of(rope[i]) * up, hi_of(rope[i]) * up));
+  }
   if (c == 0)  // (a row that is not finite has results that are not)
-    reinterpret_cast<float*>(smem + kFactorOff)[r] =
-        amax < __builtin_huge_valf() ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : __uint_as_float(0x7fffffffu);
+    factor[r] = amax < __builtin_huge_valf() ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23)
+                                             : __uint_as_float(0x7fffffffu);
 }
 
-__global__ void __launch_bounds__(kThreads, 2) fp4_decode_kernel(const __nv_bfloat16* __restrict__ q, const DecodeParams p) {
+// Codes to E5M2 values in the 128-byte swizzle.  The values wait in registers (16
+// rows: of the whole tile) until the products that read its buffer are done, and
+// are handed on two chunks at a time.  A thread has block c0 of chunk d and of chunk d + 2 of token t: the 16-byte units
+// 2 c0, 2 c0 + 1 of their rows (lanes are dealt out so that the stores of eight of
+// them touch all banks).  Bound by the logical and permute instructions, 64
+// lanes a clock: 36 for 32 values, ~1150 cycles for a tile.
+template <int R>
+__device__ void convert(const __nv_bfloat16* q, const DecodeParams& p, const Range& rg, int g, uint8_t* smem, const Bars& bars,
+                        const Watchdog& wd) {
+  using C = Cfg<R>;
+  constexpr int kHold = C::kRaw;  // pages whose values are held
+  const int ct = threadIdx.x - 128;
+  const int c0 = ct & 3, t = ((ct >> 2) & 3) | ((ct >> 5) << 2), d = (ct >> 4) & 1;
+  const uint32_t at = smem_u32(smem) + d * kChunkBytes + t * 128;
+  const uint32_t at0 = ((2 * c0) ^ (t & 7)) << 4, at1 = ((2 * c0 + 1) ^ (t & 7)) << 4;
+  const volatile int* flags = reinterpret_cast<const volatile int*>(smem + C::kRawFlagOff);
+  volatile int* states = reinterpret_cast<volatile int*>(smem + C::kFlagOff);
+  int u = 0, i = 0, seg = 0;
+#pragma unroll 1
+  for (int prob = rg.rec.p0; prob <= rg.last; ++prob) {
+    Segment s;
+    if (!rg.get(p, prob, s)) continue;
+    // the last products that read the queries of the segment before
+    if (i > 0 && !wait_warp(bars.s_full + ((i - 1) & 1), ((i - 1) >> 1) & 1, wd)) return;
+    load_queries<R>(q, p, prob, g, smem, reinterpret_cast<float*>(smem + C::kFactorOff) + (seg % kFactors) * R);
+    ++seg;
+#pragma unroll 1
+    for (int j = s.pb; j < s.pe; j += 2, ++i) {
+      const int b = i & 1, pages = min(2, s.pe - j);
+#pragma unroll 1
+      for (int h0 = 0; h0 < pages; h0 += kHold) {
+      uint4 out[kHold][2][2];
+#pragma unroll
+      for (int n = 0; n < kHold; ++n) {
+        const int h = h0 + n;
+        if (h >= pages) break;
+        const int slot = u % C::kRaw, lp = s.walk.page(j + h);
+        if (!wait_warp(bars.raw_full + slot, (u / C::kRaw) & 1, wd)) return;
+        ++u;
+        const bool real = flags[slot] >= 0;
+        if (ct == 0) {
+          states[2 * (i % kFlags) + h] = real;
+          if (h == 0) states[2 * (i % kFlags) + 1] = 0;
+        }
+        const uint8_t* row = smem + C::kRawOff + slot * kRawBytes + t * kRawRow;
+        uint4 code[2];
+        uint32_t scale[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          code[k] = *reinterpret_cast<const uint4*>(row + 128 * k + 64 * d + 16 * c0);
+          scale[k] = row[kFp4ScaleOffset + 8 * k + 4 * d + c0];
+        }
+        arrive_warp(bars.raw_empty + slot);
+        if (!real || !page_used(p, lp, s.L)) {
+          // a token that no row sees is zeros, whatever its row holds
+          if (!real || !key_seen(p, lp * kPageSize + t, s.L)) code[0] = code[1] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint2 lut = fp4_lut(fp4_scale_index(scale[k]));
+          const uint2 x = fp4_e5m2(code[k].x, lut), y = fp4_e5m2(code[k].y, lut);
+          const uint2 z = fp4_e5m2(code[k].z, lut), w = fp4_e5m2(code[k].w, lut);
+          out[n][k][0] = make_uint4(x.x, x.y, y.x, y.y);
+          out[n][k][1] = make_uint4(z.x, z.y, w.x, w.y);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (h0 == 0 && i >= 2 && !wait_warp(bars.done + 2 * b + k, ((i >> 1) - 1) & 1, wd)) return;
+#pragma unroll
+        for (int n = 0; n < kHold; ++n) {
+          if (h0 + n >= pages) break;
+          const uint32_t to = at + b * kTileBytes + 2 * k * kChunkBytes + (h0 + n) * (kChunkBytes / 2);
+          st_shared_v4(to + at0, out[n][k][0].x, out[n][k][0].y, out[n][k][0].z, out[n][k][0].w);
+          st_shared_v4(to + at1, out[n][k][1].x, out[n][k][1].y, out[n][k][1].z, out[n][k][1].w);
+        }
+        if (h0 + kHold < pages) continue;
+        fence_proxy_async_smem();
+        arrive_warp(bars.k_full + 2 * b + k);
+      }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// products: those of S (one warp), those of O (one warp)
+// ---------------------------------------------------------------------------
+template <int R>
+__device__ void score_products(const DecodeParams& p, const Range& rg, uint32_t tmem, uint8_t* smem, const Bars& bars,
+                               const Watchdog& wd) {
+  using C = Cfg<R>;
+  constexpr uint64_t kHi = smem_desc_hi(16, 1024);
+  const uint32_t base = desc_addr(smem);
+  const uint64_t qd = kHi | ((base + C::kQOff) >> 4), qr = kHi | ((base + C::kQRopeOff) >> 4);
+  int i = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (int prob = rg.rec.p0; prob <= rg.last && ok; ++prob) {
+    Segment s;
+    if (!rg.get(p, prob, s)) continue;
+#pragma unroll 1
+    for (int j = s.pb; j < s.pe && ok; j += 2, ++i) {
+      const int b = i & 1, ph = (i >> 1) & 1;
+      const uint64_t a = kHi | ((base + b * kTileBytes) >> 4), ar = kHi | ((base + C::kRopeOff + b * kChunkBytes) >> 4);
+      const uint32_t d = tmem + C::kSCol + 2 * R * b;
+      if (i >= 2) ok = wait_warp(bars.p_full + b, ph ^ 1, wd);  // (the scores of two tiles before have been read)
+#pragma unroll
+      for (int c = 0; c < 5; ++c) {
+        if (c == 0 || c == 2) ok = ok && wait_warp(bars.k_full + 2 * b + (c >> 1), ph, wd);
+        if (c == 4) ok = ok && wait_warp(bars.rope_full + b, ph, wd);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (c < 4 && ok)
+              umma_f8_ss(d, a + ((c * kChunkBytes + 32 * k) >> 4), qd + ((c * C::kQChunk + 32 * k) >> 4),
+                         idesc_f8(kTile, 2 * R, 1, 0, 0), c + k > 0);
+            else if (ok)
+              umma_bf16_ss_fast(d, ar + ((32 * k) >> 4), qr + ((32 * k) >> 4), idesc_bf16_f32(kTile, R, 0, 0), 1);
+          }
+          if (c == 4) umma_commit(bars.s_full + b);  // (of what has been issued, where a wait ran out too)
+        }
+        __syncwarp();
+      }
+    }
+  }
+  // products still running end (or the waits do) before the memory they use is freed
+  if (i > 0) drain(bars.s_full + ((i - 1) & 1), ((i - 1) >> 1) & 1, wd);
+}
+
+template <int R>
+__device__ void value_products(const DecodeParams& p, const Range& rg, uint32_t tmem, uint8_t* smem, const Bars& bars,
+                               const Watchdog& wd) {
+  using C = Cfg<R>;
+  constexpr uint64_t kHiV = smem_desc_hi(kChunkBytes, 1024);
+  const uint32_t base = desc_addr(smem);
+  int i = 0, seg = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (int prob = rg.rec.p0; prob <= rg.last && ok; ++prob) {
+    Segment s;
+    if (!rg.get(p, prob, s)) continue;
+    if (seg > 0) ok = wait_warp(bars.o_free, (seg - 1) & 1, wd);
+    ++seg;
+#pragma unroll 1
+    for (int j = s.pb; j < s.pe; j += 2, ++i) {
+      const int b = i & 1, steps = 2 * min(2, s.pe - j);  // (the second half of a tile of one page holds no values)
+      ok = ok && wait_warp(bars.p_full + b, (i >> 1) & 1, wd);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t a = kHiV | ((base + b * kTileBytes) >> 4);
+        const uint64_t pd = kHiP | ((base + C::kPOff + (i % C::kPBufs) * C::kPBytes) >> 4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              umma_f8_ss(tmem + C::kOCol + 3 * R * c, a + ((c * kChunkBytes + k * 32 * 128) >> 4), pd + ((512 * k) >> 4),
+                         idesc_f8(128, 3 * R, 1, 1, 1), j > s.pb || k > 0);
+          if (c & 1) umma_commit(bars.done + 2 * b + (c >> 1));
+        }
+      }
+      __syncwarp();
+    }
+  }
+  if (i > 0) drain(bars.done + 2 * ((i - 1) & 1) + 1, ((i - 1) >> 1) & 1, wd);
+}
+
+// ---------------------------------------------------------------------------
+// softmax and results: warps w and w + 4 share the tokens 32 (w % 4) .., rows R / 2 (w / 4) ..
+// ---------------------------------------------------------------------------
+template <int R>
+__device__ void softmax(const DecodeParams& p, const Range& rg, int g, int part, uint32_t tmem, uint8_t* smem,
+                        const Bars& bars, const Watchdog& wd) {
+  using C = Cfg<R>;
+  constexpr int N = C::kRows;
+  const int sw = (threadIdx.x >> 5) - 4 - kConvWarps, lane = threadIdx.x & 31, quarter = sw & 3, half = sw >> 2;
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+  const volatile int* states = reinterpret_cast<const volatile int*>(smem + C::kFlagOff);
+  float* const red2 = reinterpret_cast<float*>(smem + C::kRedOff) + 4 * N * half;
+  const auto add = [](float a, float b) { return a + b; };
+  bool ok = true;
+  if (p.debug_stall) ok = mbar_wait(bars.o_free, 0, wd);  // watchdog test: nothing completes this before this role has run
+  int i = 0, seg = 0;
+#pragma unroll 1
+  for (int prob = rg.rec.p0; prob <= rg.last; ++prob) {
+    Segment s;
+    if (!rg.get(p, prob, s)) continue;
+    const float* factor = reinterpret_cast<const float*>(smem + C::kFactorOff) + (seg % kFactors) * R + N * half;
+    ++seg;
+    float down[N], l[N], f[N];
+    uint32_t seen = 0;  // rows that have a reference
+#pragma unroll
+    for (int r = 0; r < N; ++r) down[r] = l[r] = 0.f;
+#pragma unroll 1
+    for (int j = s.pb; j < s.pe; j += 2, ++i) {
+      const int b = i & 1;
+      ok = ok && mbar_wait(bars.s_full + b, (i >> 1) & 1, wd);
+      // (the conversion warps' page states and factors are read below)
+      ok = ok && mbar_wait(bars.k_full + 2 * b, (i >> 1) & 1, wd);
+      tc_fence_after();
+      if (j == s.pb) {
+#pragma unroll
+        for (int r = 0; r < N; ++r) f[r] = factor[r];
+      }
+      // y = score - reference + kPLog2; a row's reference is the largest score of its
+      // first tile, raised where a score passes it by more than kRescale, which a
+      // vote finds: the maxima are exchanged in such tiles alone.
+      float y[N];
+      {
+        float lo[N];
+        tmem_ld(taddr + C::kSCol + 2 * R * b + N * half, y);
+        tmem_ld(taddr + C::kSCol + 2 * R * b + R + N * half, lo);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < N; ++r) y[r] = fmaf(y[r] + lo[r], f[r], down[r]);
+      }
+      const int jp = j + (quarter >> 1);
+      const bool real = states[2 * (i % kFlags) + (quarter >> 1)] != 0;
+      const int lp = jp < s.pe ? s.walk.page(jp) : 0;
+      if (!real || !page_whole(p, lp, s.L)) {
+        const int t = lp * kPageSize + 32 * (quarter & 1) + lane;
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          const int at = s.L - p.s_q + (g * R + N * half + r) / p.h_q;  // position of the row's query token
+          if (!real || t > at || t >= s.L || (t >= p.sinks && t <= at - p.window)) y[r] = kNegInf;
+        }
+      }
+      float top = y[0];
+#pragma unroll
+      for (int r = 1; r < N; ++r) top = max_nan(top, y[r]);
+      bool vote = !ok || !(top <= kRescale + kPLog2);
+      if (seen != (1u << N) - 1) {
+#pragma unroll
+        for (int r = 0; r < N; ++r) vote |= !((seen >> r) & 1) && y[r] != kNegInf;
+      }
+      const int before = C::kPBufs == 1 ? i - 1 : i - 2;  // the tile whose products free the buffer of P
+      // (the four warps of a half act and leave alike)
+      if (named_bar_or(kHalfBar + half, 128, vote)) {
+        // two buffers: a warp that is ahead passes no vote of the tile behind it
+        float* red = red2 + (i & 1) * 4 * R;
+        const float mine = reduce_rows<N>(y, lane, max_nan);
+        if (lane % (32 / N) == 0) red[N * quarter + lane / (32 / N)] = mine;
+        if (!named_bar_and(kHalfBar + half, 128, ok)) return;
+        float alpha[N];
+#pragma unroll
+        for (int r = 0; r < N; r += 4) {
+          float4 m[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m[k] = *reinterpret_cast<const float4*>(red + N * k + r);
+          alpha[r] = max_nan(max_nan(m[0].x, m[1].x), max_nan(m[2].x, m[3].x));
+          alpha[r + 1] = max_nan(max_nan(m[0].y, m[1].y), max_nan(m[2].y, m[3].y));
+          alpha[r + 2] = max_nan(max_nan(m[0].z, m[1].z), max_nan(m[2].z, m[3].z));
+          alpha[r + 3] = max_nan(max_nan(m[0].w, m[1].w), max_nan(m[2].w, m[3].w));
+        }
+        // (a row that has seen no key has no reference: its scores are the plain ones, down = 0)
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          const bool had = (seen >> r) & 1;
+          const float mx = alpha[r];
+          const float up = had ? (mx <= kPLog2 ? 0.f : mx - kPLog2) : (mx == kNegInf ? 0.f : mx - kPLog2);
+          if (mx != kNegInf) seen |= 1u << r;
+          alpha[r] = had ? fast_exp2(-up) : 1.f;
+          down[r] -= up;
+          y[r] -= up;
+          l[r] *= alpha[r];
+        }
+        if (j > s.pb) {  // O is complete up to the tile before
+          ok = mbar_wait(bars.done + 2 * ((i - 1) & 1) + 1, ((i - 1) >> 1) & 1, wd);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 12; ++c) {
+            const uint32_t col = taddr + C::kOCol + R * c + N * half;
+            float o[N];
+            tmem_ld(col, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int r = 0; r < N; ++r) o[r] *= alpha[r];
+            tmem_st(col, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      if (before >= 0) ok = ok && mbar_wait(bars.done + 2 * (before & 1) + 1, (before >> 1) & 1, wd);
+      const uint32_t pt = smem_u32(smem) + C::kPOff + (i % C::kPBufs) * C::kPBytes + (32 * quarter + lane) * 16 +
+                          (N == 8 ? 8 * half : 2048 * half);
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        y[r] = fast_exp2(y[r]);
+        l[r] += y[r];
+      }
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+        uint32_t code[N / 2];
+#pragma unroll
+        for (int r = 0; r < N; r += 2) {
+          code[r / 2] = e5m2x2(y[r], y[r + 1]);
+          if (term < 2) {
+            const uint32_t h2 = e5m2x2_to_f16x2(code[r / 2]);
+            y[r] -= f16x2_half_to_f32(h2, 0);
+            y[r + 1] -= f16x2_half_to_f32(h2, 1);
+          }
+        }
+        const uint32_t at = pt + term * (R / 16) * 2048;
+        if constexpr (N == 8)
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(code[0] | (code[1] << 16)),
+                       "r"(code[2] | (code[3] << 16))
+                       : "memory");
+        else
+          st_shared_v4(at, code[0] | (code[1] << 16), code[2] | (code[3] << 16), code[4] | (code[5] << 16),
+                       code[6] | (code[7] << 16));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      arrive_warp(bars.p_full + b);
+    }
+
+    // row sums, then the rows
+    float* red = red2 + (i & 1) * 4 * R;
+    float* const lse = reinterpret_cast<float*>(smem + C::kLseOff) + N * half;
+    {
+      const float sum = reduce_rows<N>(l, lane, add);
+      if (lane % (32 / N) == 0) red[N * quarter + lane / (32 / N)] = sum;
+      if (quarter == 0 && lane == 0) {
+#pragma unroll
+        for (int r = 0; r < N; ++r) lse[r] = down[r];
+      }
+    }
+    ok = mbar_wait(bars.done + 2 * ((i - 1) & 1) + 1, ((i - 1) >> 1) & 1, wd);
+    tc_fence_after();
+    if (!named_bar_and(kHalfBar + half, 128, ok)) return;
+    const bool whole = s.pb == 0 && s.pe == s.walk.pages;
+    const bool final_out = whole && p.cluster == 0;
+    const int slot = piece_slot(whole, prob, 2 * p.num_parts, part, prob == rg.rec.p0);
+    const bool slot_ok = final_out || p.cluster > 0 || (slot >= 0 && slot < p.max_slots);
+    if (!slot_ok && sw == 0 && lane == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
+    float* const invs = red2 + ((i + 1) & 1) * 4 * R;  // (maxima of the tile before: read)
+    if (quarter == 0 && lane < N) {  // a row per lane
+      const float sum = (red[lane] + red[N + lane]) + (red[2 * N + lane] + red[3 * N + lane]);
+      invs[lane] = sum == 0.f ? 0.f : 1.f / sum;
+      const float z = sum == 0.f ? kNegInf : log2f(sum) - lse[lane];
+      const int row = g * R + N * half + lane;
+      if (p.cluster > 0)
+        lse[lane] = z;
+      else if (row < p.rows && slot_ok)
+        (final_out ? p.lse : p.lse_accum)[static_cast<int64_t>(final_out ? prob : slot) * p.rows + row] = z;
+    }
+    named_bar_sync(kHalfBar + half, 128);
+    float inv[N];
+#pragma unroll
+    for (int r = 0; r < N; r += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(invs + r);
+      inv[r] = v.x;
+      inv[r + 1] = v.y;
+      inv[r + 2] = v.z;
+      inv[r + 3] = v.w;
+    }
+    const int rows = slot_ok ? p.rows - (g * R + N * half) : 0;  // rows from this thread's first on
+    const int64_t at = (static_cast<int64_t>(final_out ? prob : slot) * p.rows + g * R + N * half) * kDv + 32 * quarter + lane;
+    float* const shared = reinterpret_cast<float*>(smem) + N * half * kDv + 32 * quarter + lane;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float o[N];
+      {
+        float a[N], z[N];
+        const uint32_t col = taddr + C::kOCol + 3 * R * c + N * half;
+        tmem_ld(col, o);
+        tmem_ld(col + R, a);
+        tmem_ld(col + 2 * R, z);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < N; ++r) o[r] = (o[r] + (a[r] + z[r])) * inv[r];
+      }
+      if (c == 3) {
+        tc_fence_before();
+        arrive_warp(bars.o_free);
+      }
+      if (p.cluster > 0) {
+#pragma unroll
+        for (int r = 0; r < N; ++r) shared[r * kDv + 128 * c] = o[r];
+      } else if (final_out) {
+        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + at + 128 * c;
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+          if (r < rows) to[r * kDv] = __float2bfloat16_rn(o[r]);
+      } else {
+        float* to = p.o_accum + at + 128 * c;
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+          if (r < rows) to[r * kDv] = o[r];
+      }
+    }
+    if (!named_bar_and(kHalfBar + half, 128, true)) return;  // the sums have been read
+  }
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp4_decode_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_rope,
+                      const __nv_bfloat16* __restrict__ q, const DecodeParams p) {
+  using C = Cfg<R>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quarter = warp & 3, half = warp >> 2;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff);
-  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kMiscOff + 4);
-  uint64_t* bar_s = reinterpret_cast<uint64_t*>(smem + kBarOff);
-  uint64_t* bar_o = bar_s + 1;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff + 4);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  const Bars bars{bar,
+                  bar + C::kRaw,
+                  bar + 2 * C::kRaw,
+                  bar + 2 * C::kRaw + 2,
+                  bar + 2 * C::kRaw + 6,
+                  bar + 2 * C::kRaw + 8,
+                  bar + 2 * C::kRaw + 10,
+                  bar + 2 * C::kRaw + 14};
   // (clusters: `part` is the problem)
   const int unit = p.cluster > 0 ? blockIdx.x / p.cluster : blockIdx.x;
   const int part = unit / p.row_groups, g = unit % p.row_groups;
-
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const PartRecord rec = p.cluster > 0 ? cluster_share(p, part) : inline_schedule(p, part, kTile, smem, g == 0);
-  // (the schedule's scratch may reach over everything below)
+  if (C::kSmemBytes == C::kBarOff + C::kNumBars * 8 && smem != smem_raw) {
+    if (tid == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
+    return;
+  }
   if (tid == 0) {
-    mbar_init(bar_s, 1);
-    mbar_init(bar_o, 1);
+    for (int i = 0; i < C::kRaw; ++i) {
+      mbar_init(bars.raw_full + i, 1);
+      mbar_init(bars.raw_empty + i, kConvWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars.rope_full + i, 1);
+      mbar_init(bars.s_full + i, 1);
+      mbar_init(bars.p_full + i, kSoftWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bars.k_full + i, kConvWarps);
+      mbar_init(bars.done + i, 1);
+    }
+    mbar_init(bars.o_free, kSoftWarps);
     *abort_flag = 0;
-    *reinterpret_cast<volatile int*>(smem + kMiscOff + 8) = 0;
+    *reinterpret_cast<volatile int*>(smem + C::kMiscOff + 8) = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&tm_codes);
+    tma_prefetch_desc(&tm_rope);
   }
   // (clusters: of a CTA without pages, or one that a wait ran out in)
-  if (tid >= 32 && tid < 32 + kRows) reinterpret_cast<float*>(smem + kLseOff)[tid - 32] = kNegInf;
-  if (warp == 1) {
-    tmem_alloc(const_cast<uint32_t*>(tmem_slot), kTmemCols);
+  if (tid >= 32 && tid < 32 + R) reinterpret_cast<float*>(smem + C::kLseOff)[tid - 32] = kNegInf;
+  if (warp == 2) {
+    tmem_alloc(const_cast<uint32_t*>(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot, taddr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+  const uint32_t tmem = *tmem_slot;
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
-  const uint32_t sm = smem_u32(smem), dsm = desc_addr(smem);
-  if (p.debug_stall) mbar_wait(bar_o, 0, wd);  // watchdog test: nothing completes this
-
-  int tiles = 0;          // tiles whose scores are done: phase of both barriers
-  int issued_s = 0, issued_o = 0;
-  bool failed = __syncthreads_or(*abort_flag);
-  const int last = rec.p1 < p.num_problems ? rec.p1 : p.num_problems - 1;
-#pragma unroll 1
-  for (int prob = rec.p0; prob <= last && !failed; ++prob) {
-    Element e;
-    e.prob = prob;
-    e.L = p.cache_seqlens[prob];
-    e.table = p.block_table + static_cast<int64_t>(prob) * p.block_table_stride;
-    e.walk = key_walk(e.L, p.s_q, p.window, p.sinks, p.block_table_stride);
-    // this CTA's pages
-    const int unit_pages = p.cluster > 0 ? 1 : 2;
-    const int pb = prob == rec.p0 ? unit_pages * rec.t0 : 0;
-    const int pe = prob == rec.p1 ? min(unit_pages * rec.t1, e.walk.pages) : e.walk.pages;
-    if (pb >= pe) continue;
-
-    int2 id = page_ids(p, e, pb, pe);
-    load_queries(q, p, prob, g, smem);
-    Staged st;
-    stage(p, e, pb, pe, id, st);
-    int2 id_next = page_ids(p, e, pb + 2, pe);
-    float ref[8], l[8], f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ref[i] = kNegInf;
-      l[i] = 0.f;
-    }
-
-#pragma unroll 1
-    for (int j = pb; j < pe; j += 2, ++tiles) {
-      bool ok = j == pb || mbar_wait(bar_o, (tiles - 1) & 1, wd);
-      if (tid < 2 && j + tid < pe) {
-        const int pg = tid ? id.y : id.x;
-        if (pg < 0 || pg >= p.num_pages) atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
-      }
-      convert(st, sm);
-      const int2 id_now = id;
-      id = id_next;
-      if (j + 2 < pe) {
-        stage(p, e, j + 2, pe, id, st);
-        id_next = page_ids(p, e, j + 4, pe);
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      failed = __syncthreads_or(!ok);
-      if (failed) break;
-      ++issued_s;
-      if (warp == 0) {
-        tc_fence_after();
-        if (elect_one()) {
-          constexpr uint64_t kHi = smem_desc_hi(16, 1024);
-          const uint64_t a = kHi | (dsm >> 4), b = kHi | ((dsm + kQOff) >> 4);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8_ss(tmem + kSCol, a + ((c * kChunkBytes + 32 * k) >> 4), b + ((c * kQChunk + 32 * k) >> 4),
-                         idesc_f8(kTile, 2 * kRows, 1, 0, 0), c + k > 0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_bf16_ss_fast(tmem + kSCol, a + ((kRopeOff + 32 * k) >> 4),
-                              kHi | ((dsm + kQRopeOff + 32 * k) >> 4), idesc_bf16_f32(kTile, kRows, 0, 0), 1);
-          umma_commit(bar_s);
-        }
-        __syncwarp();
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = reinterpret_cast<const float*>(smem + kFactorOff)[8 * half + i];
-      ok = mbar_wait(bar_s, tiles & 1, wd);
-      tc_fence_after();
-
-      // scores of key `lp * 64 + (lane's place)` for rows 8 half .. 8 half + 7
-      float x[8];
-      {
-        float lo[8];
-        tmem_ld_x8(taddr + kSCol + 8 * half, x);
-        tmem_ld_x8(taddr + kSCol + kRows + 8 * half, lo);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (x[i] + lo[i]) * f[i];
-      }
-      const int jp = j + (quarter >> 1), pg = quarter >> 1 ? id_now.y : id_now.x;
-      const bool real = jp < pe && pg >= 0 && pg < p.num_pages;
-      const int lp = real ? e.walk.page(jp) : 0;
-      if (!real || !page_whole(p, lp, e.L)) {
-        const int t = lp * kPageSize + 32 * (quarter & 1) + lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = e.L - p.s_q + (g * kRows + 8 * half + i) / p.h_q;  // position of the row's query token
-          if (!real || t > at || t >= e.L || (t >= p.sinks && t <= at - p.window)) x[i] = kNegInf;
-        }
-      }
-      float* red = reinterpret_cast<float*>(smem + kRedOff) + 32 * half;
-      {
-        const float mx = reduce8(x, lane, max_nan);
-        if ((lane & 3) == 0) red[8 * quarter + (lane >> 2)] = mx;
-      }
-      named_bar_sync(1 + half, 128);
-      float mx[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        mx[i] = max_nan(max_nan(red[i], red[8 + i]), max_nan(red[16 + i], red[24 + i]));
-      // raise the references that scores pass by more than kRescale (all the threads of a half alike)
-      bool raise = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) raise |= !(mx[i] <= ref[i] + kRescale);
-      if (raise) {
-        float alpha[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          alpha[i] = 1.f;
-          if (!(mx[i] <= ref[i] + kRescale)) {
-            alpha[i] = ref[i] == kNegInf ? 0.f : fast_exp2(ref[i] - mx[i]);
-            ref[i] = mx[i];
-          }
-          l[i] *= alpha[i];
-        }
-        if (j > pb) {
-#pragma unroll 1
-          for (int b = 0; b < 12; ++b) {
-            const uint32_t col = taddr + kOCol + kRows * b + 8 * half;
-            float o[8];
-            tmem_ld_x8(col, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] *= alpha[i];
-            asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(col),
-                         "r"(__float_as_uint(o[0])), "r"(__float_as_uint(o[1])), "r"(__float_as_uint(o[2])),
-                         "r"(__float_as_uint(o[3])), "r"(__float_as_uint(o[4])), "r"(__float_as_uint(o[5])),
-                         "r"(__float_as_uint(o[6])), "r"(__float_as_uint(o[7]))
-                         : "memory");
-          }
-          tmem_st_wait();
-        }
-      }
-      const uint32_t pt = sm + kPOff + 8 * half * 128 + (lane & 15);
-      const int pu = 2 * quarter + (lane >> 4);
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        float v[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float pr = fast_exp2(x[i + n] - (ref[i + n] == kNegInf ? 0.f : ref[i + n]));
-          l[i + n] += pr;
-          v[n] = pr * kPScale;
-        }
-#pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          const uint32_t code = e5m2x2(v[0], v[1]);
-          const uint32_t at = pt + term * kRows * 128;
-          st_shared_u8(at + i * 128 + ((pu ^ i) << 4), code & 0xffu);
-          st_shared_u8(at + (i + 1) * 128 + ((pu ^ (i + 1)) << 4), code >> 8);
-          if (term < 2) {
-            const uint32_t h2 = e5m2x2_to_f16x2(code);
-            v[0] -= f16x2_half_to_f32(h2, 0);
-            v[1] -= f16x2_half_to_f32(h2, 1);
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      failed = __syncthreads_or(!ok);
-      if (failed) break;
-      ++issued_o;
-      if (warp == 0) {
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t a = smem_desc_hi(kChunkBytes, 1024) | (dsm >> 4);
-          const uint64_t b = smem_desc_hi(16, 1024) | ((dsm + kPOff) >> 4);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8_ss(tmem + kOCol + 3 * kRows * c, a + ((c * kChunkBytes + k * 32 * 128) >> 4), b + ((32 * k) >> 4),
-                         idesc_f8(128, 3 * kRows, 1, 1, 1), j > pb || k > 0);
-          umma_commit(bar_o);
-        }
-        __syncwarp();
-      }
-    }
-    if (failed) break;
-
-    // row sums, then the rows
-    float* red = reinterpret_cast<float*>(smem + kRedOff) + 32 * half;
-    {
-      const float sum = reduce8(l, lane, [](float a, float b) { return a + b; });
-      if ((lane & 3) == 0) red[8 * quarter + (lane >> 2)] = sum;
-    }
-    bool ok = mbar_wait(bar_o, (tiles - 1) & 1, wd);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const PartRecord rec = p.cluster > 0 ? cluster_share(p, part) : inline_schedule(p, part, kTile, smem, g == 0);
+  const Range rg{rec, rec.p1 < p.num_problems ? rec.p1 : p.num_problems - 1};
+  if (warp < 4) {
+    regs_to<C::kRegsCtl, kLaunchRegs>();
+    if (warp == 0) copy_codes<R>(&tm_codes, p, rg, smem, bars, wd);
+    if (warp == 1) score_products<R>(p, rg, tmem, smem, bars, wd);
+    if (warp == 2) copy_rope<R>(&tm_rope, p, rg, smem, bars, wd);
+    if (warp == 3) value_products<R>(p, rg, tmem, smem, bars, wd);
+    __syncthreads();
     tc_fence_after();
-    failed = __syncthreads_or(!ok);
-    if (failed) break;
-    const bool whole = pb == 0 && pe == e.walk.pages;
-    const bool final_out = whole && p.cluster == 0;
-    const int slot = piece_slot(whole, prob, 2 * p.num_parts, part, prob == rec.p0);
-    const bool slot_ok = final_out || p.cluster > 0 || (slot >= 0 && slot < p.max_slots);
-    if (!slot_ok && tid == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
-    float inv[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float sum = red[i] + red[8 + i] + red[16 + i] + red[24 + i];
-      inv[i] = sum == 0.f ? 0.f : 1.f / (sum * kPScale);
-      const int r = 8 * half + i, row = g * kRows + r;
-      if (quarter == 0 && lane == i && row < p.rows) {
-        const float z = sum == 0.f ? kNegInf : ref[i] + log2f(sum);
-        if (p.cluster > 0)
-          reinterpret_cast<float*>(smem + kLseOff)[r] = z;
-        else if (final_out)
-          p.lse[static_cast<int64_t>(prob) * p.rows + row] = z;
-        else if (slot_ok)
-          p.lse_accum[static_cast<int64_t>(slot) * p.rows + row] = z;
-      }
-    }
-    const int64_t first_row = static_cast<int64_t>(final_out ? prob : slot) * p.rows + g * kRows + 8 * half;
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      float o[8], a[8], b[8];
-      const uint32_t col = taddr + kOCol + 3 * kRows * c + 8 * half;
-      tmem_ld_x8(col, o);
-      tmem_ld_x8(col + kRows, a);
-      tmem_ld_x8(col + 2 * kRows, b);
-      tmem_ld_wait();
-      const int d = 128 * c + 32 * quarter + lane;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = (o[i] + (a[i] + b[i])) * inv[i];
-        if (p.cluster > 0) {
-          reinterpret_cast<float*>(smem)[(8 * half + i) * kDv + d] = y;
-        } else if (slot_ok && g * kRows + 8 * half + i < p.rows) {
-          if (final_out)
-            static_cast<__nv_bfloat16*>(p.out)[(first_row + i) * kDv + d] = __float2bfloat16_rn(y);
-          else
-            p.o_accum[(first_row + i) * kDv + d] = y;
-        }
-      }
-    }
-    tc_fence_before();
-    __syncthreads();  // the next segment's first products overwrite O, its queries and sums theirs
-    tc_fence_after();
-  }
-
-  if (failed) {  // products still running end (or the wait does) before the memory they use is freed
-    const uint64_t t0 = global_timer_ns();
-    while ((issued_s > 0 && !mbar_try_wait(bar_s, (issued_s - 1) & 1)) ||
-           (issued_o > 0 && !mbar_try_wait(bar_o, (issued_o - 1) & 1)))
-      if (global_timer_ns() - t0 > wd.limit_ns) break;
-  }
-  __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
-  if (p.cluster > 0) {
-    if (tid < kMergeFrom) {
-      cluster_merge_wait();
+    if (warp == 2) tmem_dealloc(tmem, C::kTmemCols);
+    if (p.cluster > 0) cluster_merge_wait();
+  } else {
+    if (warp < 4 + kConvWarps) {
+      regs_to<C::kRegsConv, kLaunchRegs>();
+      convert<R>(q, p, rg, g, smem, bars, wd);
     } else {
-      const int64_t row = static_cast<int64_t>(part) * p.rows + g * kRows;
+      regs_to<C::kRegsSoft, kLaunchRegs>();
+      softmax<R>(p, rg, g, part, tmem, smem, bars, wd);
+      tc_fence_before();
+    }
+    __syncthreads();
+    if (p.cluster > 0) {
+      const int64_t row = static_cast<int64_t>(part) * p.rows + g * R;
       cluster_merge(p.cluster,
-                    ClusterSide{smem, reinterpret_cast<const int*>(smem + kMiscOff + 8),
-                                reinterpret_cast<const float*>(smem + kLseOff)},
-                    reinterpret_cast<float*>(smem + kWeightsOff), min(kRows, p.rows - g * kRows),
+                    ClusterSide{smem, reinterpret_cast<const int*>(smem + C::kMiscOff + 8),
+                                reinterpret_cast<const float*>(smem + C::kLseOff)},
+                    reinterpret_cast<float*>(smem + C::kPOff), min(R, p.rows - g * R),
                     static_cast<__nv_bfloat16*>(p.out) + row * kDv, p.lse + row);
     }
   }
 }
 
-}  // namespace
-
-cudaError_t launch_decode_fp4(const void* q, const DecodeParams& p, cudaStream_t stream) {
-  // a schedule of very many problems is made in more shared memory than the tiles take (one CTA on an SM then)
-  const size_t schedule = p.cluster > 0 ? 0 : schedule_scratch(p.num_problems) + 1024;
-  const size_t smem = schedule > kSmemBytes ? schedule : kSmemBytes;
-  cudaError_t e = allow_dynamic_smem(fp4_decode_kernel, smem, 0);
+template <int R>
+cudaError_t launch(const CUtensorMap& tm_codes, const CUtensorMap& tm_rope, const void* q, const DecodeParams& p,
+                   cudaStream_t stream) {
+  auto kern = fp4_decode_kernel<R>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::kSmemBytes);
   if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.cluster > 0 ? p.cluster * p.num_problems : p.num_parts) * p.row_groups);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = Cfg<R>::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -591,7 +899,14 @@ cudaError_t launch_decode_fp4(const void* q, const DecodeParams& p, cudaStream_t
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fp4_decode_kernel, static_cast<const __nv_bfloat16*>(q), p);
+  return cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_rope, static_cast<const __nv_bfloat16*>(q), p);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_fp4(const CUtensorMap& tm_codes, const CUtensorMap& tm_rope, const void* q, const DecodeParams& p,
+                              int rpc, cudaStream_t stream) {
+  return rpc == 16 ? launch<16>(tm_codes, tm_rope, q, p, stream) : launch<32>(tm_codes, tm_rope, q, p, stream);
 }
 
 }  // namespace mla

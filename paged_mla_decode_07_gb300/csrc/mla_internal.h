@@ -271,7 +271,9 @@ cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, con
 cudaError_t launch_decode_rows(const CUtensorMap& tm_kv, const void* q, const DecodeParams& p, bool is_fp8,
                                cudaStream_t stream);
 // Windowed decode over FP4 rows (mla_decode_fp4.cu)
-cudaError_t launch_decode_fp4(const void* q, const DecodeParams& p, cudaStream_t stream);
+// (tm_codes: codes and scales of a page as one box, tm_rope: its RoPE values; rpc: 16 or 32 rows per CTA)
+cudaError_t launch_decode_fp4(const CUtensorMap& tm_codes, const CUtensorMap& tm_rope, const void* q, const DecodeParams& p,
+                              int rpc, cudaStream_t stream);
 // mode: 0 dense bf16 cache, 1 sparse FP8 cache, 2 dense FP8 cache, 3 sparse bf16 rows, 4 and 5 windowed dense
 // over the bf16 and the FP8 cache
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const DecodeParams& p, int rpc,
