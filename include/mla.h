@@ -366,6 +366,49 @@ typedef struct {
 mla_status mla_fp4_decode_workspace_size(int batch, int h_q, int s_q, size_t* bytes);
 mla_status mla_fp4_decode(const mla_fp4_decode_args* args, mla_stream_t stream);
 
+/* Attention over whole prompts, packed: the form of prefill before the
+ * up-projections are absorbed.  Queries and keys are 192 wide, 128 values per
+ * head and 64 RoPE values that all heads of a key share; values are 128 wide.
+ *   out[i, h] = softmax(sm_scale * q[i, h] . (k_nope[t, h'], k_rope[t])) v[t, h'],
+ *   h' = h / (h_q / h_kv)
+ * Sequence b has query rows q_offsets[b] .. q_offsets[b + 1] (n of them) and key
+ * rows k_offsets[b] .. k_offsets[b + 1] (m); either may be none.  With
+ * is_causal, query row i of the sequence sees its first m - n + i + 1 keys (the
+ * last query the last key: with context the queries are a prompt's last chunk;
+ * m < n leaves the first rows without keys), else all m.  A row without keys
+ * gets out = 0 and lse = -inf.  Rows of out and lse from q_offsets[batch] on are
+ * left as they are.  Keys and values of other sequences may hold anything; a value
+ * that is not finite shows in rows of its sequence.  Probabilities are rounded to
+ * bf16, sums are fp32, lse is base 2 as in mla_decode.
+ * All row and head strides are in elements and multiples of 8, so q, keys and
+ * values may be slices (of one up-projection, of cache rows).  Offsets that
+ * decrease, or leave the rows, are cut off or set MLA_DEVICE_BAD_SCHEDULE.
+ * All launches are made on `stream` by the one call. */
+typedef struct {
+  const void* q;                  /* bf16 [num_q, h_q, 192], 16-byte aligned (as k_nope, k_rope and v) */
+  int64_t q_stride, q_head_stride;
+  int num_q, h_q;                 /* num_q = 0: nothing is launched */
+  const void* k_nope;             /* bf16 [num_k, h_kv, 128] */
+  int64_t k_nope_stride, k_nope_head_stride;
+  const void* k_rope;             /* bf16 [num_k, 64] */
+  int64_t k_rope_stride;
+  const void* v;                  /* bf16 [num_k, h_kv, 128] */
+  int64_t v_stride, v_head_stride;
+  int num_k, h_kv;                /* h_q a multiple of h_kv */
+  const int32_t* q_offsets;       /* int32 [batch + 1], non-decreasing, from 0 */
+  const int32_t* k_offsets;       /* int32 [batch + 1], non-decreasing, from 0 */
+  int batch;
+  float sm_scale;
+  int is_causal;
+  void* workspace;                /* >= mla_prompt_attention_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  void* out;                      /* bf16 [num_q, h_q, 128], 16-byte aligned */
+  float* lse;                     /* fp32 [num_q, h_q], base 2 */
+} mla_prompt_attention_args;
+
+mla_status mla_prompt_attention_workspace_size(int num_q, int batch, size_t* bytes);
+mla_status mla_prompt_attention(const mla_prompt_attention_args* args, mla_stream_t stream);
+
 /* Sparse prefill ("flash_mla_sparse_fwd(q, kv, indices, sm_scale)" of the
  * FlashMLA article's usage section): token-level sparse attention with no
  * batch dimension and an unpaged bf16 KV with one head.  For query token i

@@ -175,6 +175,20 @@ class Fp4DecodeArgs(ctypes.Structure):
     ]
 
 
+class PromptAttentionArgs(ctypes.Structure):
+    """Mirror of ``mla_prompt_attention_args`` in include/mla.h."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("num_q", ctypes.c_int), ("h_q", ctypes.c_int), ("k_nope", ctypes.c_void_p),
+        ("k_nope_stride", ctypes.c_int64), ("k_nope_head_stride", ctypes.c_int64), ("k_rope", ctypes.c_void_p),
+        ("k_rope_stride", ctypes.c_int64), ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64), ("num_k", ctypes.c_int), ("h_kv", ctypes.c_int),
+        ("q_offsets", ctypes.c_void_p), ("k_offsets", ctypes.c_void_p), ("batch", ctypes.c_int),
+        ("sm_scale", ctypes.c_float), ("is_causal", ctypes.c_int), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+    ]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -248,6 +262,10 @@ def lib():
             L.mla_fp4_decode_workspace_size.restype = I
             L.mla_fp4_decode.argtypes = [ctypes.POINTER(Fp4DecodeArgs), P]
             L.mla_fp4_decode.restype = I
+            L.mla_prompt_attention_workspace_size.argtypes = [I, I, ctypes.POINTER(S)]
+            L.mla_prompt_attention_workspace_size.restype = I
+            L.mla_prompt_attention.argtypes = [ctypes.POINTER(PromptAttentionArgs), P]
+            L.mla_prompt_attention.restype = I
             _native, _lib = _load_binding(), L
     return _lib
 
@@ -734,6 +752,76 @@ def sparse_prefill(q: torch.Tensor, kv: torch.Tensor, indices: torch.Tensor, sm_
     a.lse = lse.data_ptr()
     _check(lib().mla_sparse_prefill(ctypes.byref(a), _stream(stream)))
     return out.view(s_q, h_q, D_V), lse.view(s_q, h_q)
+
+
+def prompt_attention_workspace_size(num_q: int, batch: int) -> int:
+    """Scratch bytes of prompt_attention."""
+    n = ctypes.c_size_t()
+    _check(lib().mla_prompt_attention_workspace_size(num_q, batch, ctypes.byref(n)))
+    return n.value
+
+
+def _heads(t, name, width, dev, heads=None):
+    """A bf16 tensor [rows, heads, width] on dev with contiguous values, its strides otherwise free."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != dev:
+        raise ValueError(f"{name} must be a bfloat16 tensor on {dev}")
+    if t.dim() != 3 or t.shape[2] != width or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [rows, {'heads' if heads is None else heads}, {width}] (got {tuple(t.shape)})")
+    if t.stride(2) != 1:
+        raise ValueError(f"the values of a head of {name} must be contiguous")
+    return t
+
+
+def prompt_attention(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
+                     k_offsets: torch.Tensor, sm_scale: float, is_causal: bool = True, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention over packed prompts (mla_prompt_attention).
+
+    q bf16 [num_q, h_q, 192] (128 values and 64 RoPE values); k_nope and v bf16 [num_k, h_kv, 128], k_rope
+    bf16 [num_k, 64] (shared by the heads), each with any row and head stride that is a multiple of 8 values
+    (slices of an up-projection, of cache rows); q_offsets and k_offsets int32 [batch + 1]: the rows of each
+    sequence.  Causal: the last query of a sequence sees its last key.  Returns (out bf16 [num_q, h_q, 128],
+    lse fp32 [num_q, h_q], base 2); rows from q_offsets[batch] on are not written."""
+    if stream is None:
+        r = _plain("prompt_attention", q, k_nope, k_rope, v, q_offsets, k_offsets, sm_scale, is_causal, out, lse, workspace)
+        if r is not None:
+            return r
+    dev = _cuda_tensor(q, "q")
+    _heads(q, "q", 192, dev)
+    _heads(k_nope, "k_nope", 128, dev)
+    num_q, h_q, _ = q.shape
+    num_k, h_kv, _ = k_nope.shape
+    _heads(v, "v", 128, dev, h_kv)
+    if isinstance(k_rope, torch.Tensor) and k_rope.dim() == 2:
+        k_rope = k_rope[:, None]
+    _heads(k_rope, "k_rope", 64, dev, 1)
+    if v.shape[0] != num_k or k_rope.shape[0] != num_k:
+        raise ValueError("k_nope, k_rope and v must have the same rows")
+    if max(num_q, num_k) >= 2 ** 31:
+        raise ValueError("the rows of q and k_nope must fit 32 bits")
+    _need(q_offsets, "q_offsets", torch.int32, dev, 1)
+    _need(k_offsets, "k_offsets", torch.int32, dev, 1)
+    if q_offsets.shape != k_offsets.shape or q_offsets.shape[0] < 2:
+        raise ValueError("q_offsets and k_offsets must have batch + 1 entries")
+    batch = q_offsets.shape[0] - 1
+    for t, name, dtype, shape in ((out, "out", torch.bfloat16, (num_q, h_q, 128)), (lse, "lse", torch.float32, (num_q, h_q))):
+        if t is not None:
+            _need(t, name, dtype, dev, len(shape))
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {shape} (got {tuple(t.shape)})")
+
+    def call(handle):
+        o = torch.empty((num_q, h_q, 128), dtype=torch.bfloat16, device=dev) if out is None else out
+        z = torch.empty((num_q, h_q), dtype=torch.float32, device=dev) if lse is None else lse
+        ws = _scratch(workspace, prompt_attention_workspace_size(num_q, batch) if workspace is None else 0, dev)
+        a = PromptAttentionArgs(q.data_ptr(), q.stride(0), q.stride(1), num_q, h_q, k_nope.data_ptr(), k_nope.stride(0),
+                                k_nope.stride(1), k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1),
+                                num_k, h_kv, q_offsets.data_ptr(), k_offsets.data_ptr(), batch, float(sm_scale),
+                                int(bool(is_causal)), ws.data_ptr(), ws.nbytes, o.data_ptr(), z.data_ptr())
+        _check(lib().mla_prompt_attention(ctypes.byref(a), handle))
+        return o, z
+
+    return _launch(dev, stream, call)
 
 
 def _decode_io(q, kvcache, block_table, cache_seqlens, kv_scales, fp4=False):

@@ -36,7 +36,7 @@ HEADER = os.path.join(HERE, "..", "include", "mla.h")
 BINDING_SOURCE = "binding.cpp"
 SOURCES = ["mla_api.cu", "mla_sched.cu", "mla_decode.cu", "mla_decode_pair.cu", "mla_combine.cu", "mla_noalloc.cu",
            "mla_store.cu", "mla_index.cu", "mla_pages.cu", "mla_prefix.cu", "mla_decode_rows.cu",
-           "mla_load.cu", "mla_decode_fp4.cu"]
+           "mla_load.cu", "mla_decode_fp4.cu", "mla_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]

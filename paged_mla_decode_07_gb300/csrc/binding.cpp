@@ -413,8 +413,68 @@ PyObject* shared_prefix_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// (q, k_nope, k_rope, v, q_offsets, k_offsets, sm_scale, is_causal, out, lse, workspace)
+PyObject* prompt_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c(args, n, 11);
+    const at::Tensor* q = c.tensor(0, at::kBFloat16, 3, true);
+    const at::Tensor* k = c.tensor(1, at::kBFloat16, 3, true);
+    const at::Tensor* rope = c.tensor(2, at::kBFloat16, 2, true);
+    const at::Tensor* v = c.tensor(3, at::kBFloat16, 3, true);
+    const at::Tensor* qo = c.tensor(4, at::kInt, 1);
+    const at::Tensor* ko = c.tensor(5, at::kInt, 1);
+    mla_prompt_attention_args a{};
+    a.sm_scale = c.number(6);
+    if (!c.ok) return nullptr;
+    a.is_causal = PyObject_IsTrue(args[7]);
+    const int64_t rows = q->size(0), heads = q->size(1);
+    c.need(a.is_causal >= 0 && q->size(2) == 192 && k->size(2) == 128 && v->sizes() == k->sizes() && rope->size(1) == 64 &&
+           rope->size(0) == k->size(0) && q->stride(2) == 1 && k->stride(2) == 1 && v->stride(2) == 1 &&
+           rope->stride(1) == 1 && qo->size(0) == ko->size(0) && qo->size(0) >= 2);
+    const int64_t out_shape[] = {rows, heads, 128};
+    const at::IntArrayRef lse_shape(out_shape, 2);
+    at::Tensor out = c.output(8, at::kBFloat16, out_shape), lse = c.output(9, at::kFloat, lse_shape);
+    at::Tensor ws = c.workspace(10);
+    size_t bytes = 0;
+    if (!c.ok || mla_prompt_attention_workspace_size(static_cast<int>(rows), static_cast<int>(qo->size(0) - 1), &bytes) != MLA_OK)
+      return nullptr;
+    a.q = ptr(*q);
+    a.q_stride = q->stride(0);
+    a.q_head_stride = q->stride(1);
+    a.num_q = static_cast<int>(rows);
+    a.h_q = static_cast<int>(heads);
+    a.k_nope = ptr(*k);
+    a.k_nope_stride = k->stride(0);
+    a.k_nope_head_stride = k->stride(1);
+    a.k_rope = ptr(*rope);
+    a.k_rope_stride = rope->stride(0);
+    a.v = ptr(*v);
+    a.v_stride = v->stride(0);
+    a.v_head_stride = v->stride(1);
+    a.num_k = static_cast<int>(k->size(0));
+    a.h_kv = static_cast<int>(k->size(1));
+    a.q_offsets = ptr<int32_t>(*qo);
+    a.k_offsets = ptr<int32_t>(*ko);
+    a.batch = static_cast<int>(qo->size(0) - 1);
+    const mla_stream_t stream = c.stream();
+    mla_status st;
+    {
+      const Unlocked unlocked;
+      c.fill(out, at::kBFloat16, out_shape);
+      c.fill(lse, at::kFloat, lse_shape);
+      c.fill(ws, at::kByte, {static_cast<int64_t>(bytes)});
+      a.workspace = ptr(ws);
+      a.workspace_bytes = ws.nbytes();
+      a.out = ptr(out);
+      a.lse = ptr<float>(lse);
+      st = mla_prompt_attention(&a, stream);
+    }
+    return st == MLA_OK ? tuple_of({&out, &lse}) : failed(st);
+  });
+}
+
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(assign_pages), ENTRY(cache_store), ENTRY(cache_load), ENTRY(window_decode), ENTRY(shared_prefix_decode),
+PyMethodDef methods[] = {ENTRY(assign_pages), ENTRY(cache_store), ENTRY(cache_load), ENTRY(prompt_attention), ENTRY(window_decode), ENTRY(shared_prefix_decode),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mla_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

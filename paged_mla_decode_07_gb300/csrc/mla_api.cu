@@ -261,6 +261,21 @@ mla_status encode_fp4_map(CUtensorMap* map, const void* base, long long nrows, b
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// bf16 rows of `heads` heads of `width` values, strides in elements: dim0 =
+// values, dim1 = head, dim2 = row; a box is 64 values of one head of 128 rows, in
+// the 128-byte swizzle.  (Strides of dimensions of size 1 are free.)
+mla_status encode_heads_map(CUtensorMap* map, const void* base, int width, long long heads, long long rows,
+                            long long head_stride, long long row_stride, const char* what) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? 2 * head_stride : 2 * width),
+                           static_cast<cuuint64_t>(rows > 1 ? 2 * row_stride : 2 * width)};
+  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode_map(what, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 uint64_t watchdog_ns() {
@@ -1211,6 +1226,96 @@ mla_status mla_fp4_decode(const mla_fp4_decode_args* a, mla_stream_t stream) {
   m.lse = a->lse;
   e = launch_merge(m, s);
   if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
+  return ok();
+}
+
+mla_status mla_prompt_attention_workspace_size(int num_q, int batch, size_t* bytes) {
+  if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes is NULL");
+  if (num_q < 0) return fail(MLA_ERR_INVALID_ARG, "num_q must be >= 0 (got %d)", num_q);
+  if (batch < 1) return fail(MLA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
+  if (batch > kMaxProblems)
+    return fail(MLA_ERR_UNSUPPORTED, "batch = %d exceeds the supported %d sequences", batch, kMaxProblems);
+  *bytes = align256(4 * (kPromptList + static_cast<size_t>(num_q / kPromptBlock + batch) * kPromptEntryInts));
+  return ok();
+}
+
+mla_status mla_prompt_attention(const mla_prompt_attention_args* a, mla_stream_t stream) {
+  if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
+  size_t need = 0;
+  mla_status st = mla_prompt_attention_workspace_size(a->num_q, a->batch, &need);
+  if (st != MLA_OK) return st;
+  if (a->num_k < 0) return fail(MLA_ERR_INVALID_ARG, "num_k must be >= 0 (got %d)", a->num_k);
+  if (a->h_q < 1) return fail(MLA_ERR_INVALID_ARG, "h_q must be >= 1 (got %d)", a->h_q);
+  if (a->h_kv < 1 || a->h_q % a->h_kv != 0)
+    return fail(MLA_ERR_INVALID_ARG, "h_q = %d must be a multiple of h_kv = %d", a->h_q, a->h_kv);
+  if (a->h_q > 1024) return fail(MLA_ERR_UNSUPPORTED, "h_q = %d exceeds 1024", a->h_q);
+  if (!std::isfinite(a->sm_scale)) return fail(MLA_ERR_INVALID_ARG, "sm_scale is not finite");
+  struct Arr {
+    const void* p;
+    size_t align;
+    bool need;
+    const char* name;
+  };
+  const bool keys = a->num_k > 0, rows = a->num_q > 0;
+  for (const Arr& x : {Arr{a->q, 16, rows, "q"}, Arr{a->k_nope, 16, keys, "k_nope"}, Arr{a->k_rope, 16, keys, "k_rope"},
+                       Arr{a->v, 16, keys, "v"}, Arr{a->q_offsets, 4, true, "q_offsets"},
+                       Arr{a->k_offsets, 4, true, "k_offsets"}, Arr{a->out, 16, rows, "out"}, Arr{a->lse, 4, rows, "lse"}}) {
+    if (!x.p && x.need) return fail(MLA_ERR_INVALID_ARG, "%s is NULL", x.name);
+    if (!aligned(x.p, x.align)) return fail(MLA_ERR_INVALID_ARG, "%s is not %zu-byte aligned", x.name, x.align);
+  }
+  struct Stride {
+    int64_t v;
+    bool used;
+    const char* name;
+  };
+  for (const Stride& x : {Stride{a->q_stride, a->num_q > 1, "q_stride"}, Stride{a->q_head_stride, a->h_q > 1, "q_head_stride"},
+                          Stride{a->k_nope_stride, a->num_k > 1, "k_nope_stride"},
+                          Stride{a->k_nope_head_stride, a->h_kv > 1, "k_nope_head_stride"},
+                          Stride{a->k_rope_stride, a->num_k > 1, "k_rope_stride"}, Stride{a->v_stride, a->num_k > 1, "v_stride"},
+                          Stride{a->v_head_stride, a->h_kv > 1, "v_head_stride"}})
+    if (x.used && (x.v < 8 || x.v % 8 != 0 || x.v >= (1ll << 38)))
+      return fail(MLA_ERR_INVALID_ARG, "%s must be a positive multiple of 8 elements (got %lld)", x.name,
+                  static_cast<long long>(x.v));
+  const long long blocks = a->num_q / kPromptBlock + static_cast<long long>(a->batch);
+  if (blocks * a->h_q >= (1ll << 31) - 4096)
+    return fail(MLA_ERR_UNSUPPORTED, "num_q = %d rows of %d heads in %d sequences", a->num_q, a->h_q, a->batch);
+  if (!rows) return ok();
+  st = check_workspace(a->workspace, a->workspace_bytes, need);
+  if (st != MLA_OK) return st;
+  PromptParams p;
+  memset(&p, 0, sizeof p);
+  int sms = 0;
+  st = device_info(&p.status, &sms);
+  if (st != MLA_OK) return st;
+  CUtensorMap tm_q, tm_k_nope, tm_k_rope, tm_v;
+  // (without keys no copy is made: their maps name q)
+  const long long nk = keys ? a->num_k : 1;
+  st = encode_heads_map(&tm_q, a->q, 192, a->h_q, a->num_q, a->q_head_stride, a->q_stride, "q");
+  if (st == MLA_OK)
+    st = encode_heads_map(&tm_k_nope, keys ? a->k_nope : a->q, 128, a->h_kv, nk, a->k_nope_head_stride, a->k_nope_stride,
+                          "k_nope");
+  if (st == MLA_OK)
+    st = encode_heads_map(&tm_v, keys ? a->v : a->q, 128, a->h_kv, nk, a->v_head_stride, a->v_stride, "v");
+  if (st == MLA_OK)
+    st = encode_heads_map(&tm_k_rope, keys ? a->k_rope : a->q, 64, 1, nk, 0, a->k_rope_stride, "k_rope");
+  if (st != MLA_OK) return st;
+  p.q_offsets = a->q_offsets;
+  p.k_offsets = a->k_offsets;
+  p.plan = static_cast<int32_t*>(a->workspace);
+  p.out = a->out;
+  p.lse = a->lse;
+  p.timeout_ns = watchdog_ns();
+  p.batch = a->batch;
+  p.num_q = a->num_q;
+  p.num_k = a->num_k;
+  p.h_q = a->h_q;
+  p.h_kv = a->h_kv;
+  p.max_blocks = static_cast<int>(blocks);
+  p.causal = a->is_causal ? 1 : 0;
+  p.debug_stall = g_test_debug_stall.load();
+  p.scale_log2 = a->sm_scale * 1.4426950408889634f;
+  cudaError_t e = launch_prompt(tm_q, tm_k_nope, tm_k_rope, tm_v, p, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
   return ok();
 }
 

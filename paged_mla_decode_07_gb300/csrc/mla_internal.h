@@ -250,6 +250,24 @@ struct CacheLoadParams {
   int format;                  // mla_cache_format
 };
 
+// Attention over packed prompts.  The workspace: a counter, the number of blocks,
+// and the list of blocks (8 ints each, 6 of them used).
+constexpr int kPromptBlock = 256;  // query rows of a block
+constexpr int kPromptCounter = 0, kPromptBlocks = 1, kPromptList = 64, kPromptEntryInts = 8;
+struct PromptParams {
+  const int32_t* q_offsets;  // [batch + 1]
+  const int32_t* k_offsets;  // [batch + 1]
+  int32_t* plan;             // workspace
+  void* out;                 // bf16 [num_q, h_q, 128]
+  float* lse;                // [num_q, h_q]
+  uint32_t* status;
+  uint64_t timeout_ns;
+  int batch, num_q, num_k, h_q, h_kv;
+  int max_blocks;            // blocks that the list has room for: as many as non-decreasing offsets can name
+  int causal, debug_stall;
+  float scale_log2;
+};
+
 // Lets launches of a kernel whose shared memory varies from call to call have
 // `bytes` of it beside the kernel's own (at most `own`).  48 KB in all need no
 // leave.  The limit belongs to the kernel, not to the launch, and another host
@@ -306,6 +324,9 @@ cudaError_t launch_fp8_cache_store(const uint16_t* x, int num_tokens, const int3
                                    int block_table_stride, uint8_t* kvcache, int num_pages, uint32_t* status,
                                    int sm_count, cudaStream_t stream);
 cudaError_t launch_slot_store(const SlotStoreParams& p, int sm_count, cudaStream_t stream);
+// (tm_q, tm_k_nope, tm_v: boxes of 64 values of one head of 128 rows; tm_k_rope: of 128 rows)
+cudaError_t launch_prompt(const CUtensorMap& tm_q, const CUtensorMap& tm_k_nope, const CUtensorMap& tm_k_rope,
+                          const CUtensorMap& tm_v, const PromptParams& p, int sm_count, cudaStream_t stream);
 cudaError_t launch_cache_load(const CacheLoadParams& p, int sm_count, cudaStream_t stream);
 // in_place: the lengths or the cursor are updated in the arrays they are read from
 cudaError_t launch_assign_pages(const AssignPagesParams& p, bool in_place, int sm_count, cudaStream_t stream);

@@ -1,0 +1,710 @@
+// K13 — attention over whole prompts, packed, causal, with grouped heads: the form
+// that MLA prefill has before its up-projections are absorbed.  Queries and keys
+// are 192 wide (128 values per head and 64 RoPE values, which a key's heads
+// share), values 128.
+//
+//   out[i, h] = sum_t softmax_t(scale q[i, h] . (k_nope[t, h'], k_rope[t])) v[t, h']
+//
+// over the keys t of i's sequence (h' = h / (heads per KV head)); causal, query i
+// of n sees the first m - n + i + 1 of m keys.
+//
+// An item is 256 query rows of one head of one sequence, two halves of 128 rows
+// (M of the MMAs), over tiles of 128 keys.  The halves share the keys and take
+// turns on the tensor pipe: while one has its softmax the other's products run.
+//   S [128, 128 keys] = Q [128, 192] K^T    12 MMAs
+//   O [128, 128]     += P [128, 128 keys] V  8 MMAs, P from tensor memory
+// Tensor memory: S and O of both halves, 512 columns; P takes the place of S.
+// Shared memory: Q 96 KB and a ring of eight 16 KB chunks (128 keys x 64 dims),
+// three for the keys of a tile and two for its values, each freed on its own.
+//
+// Bound by the tensor pipe: 20 MMAs of 64 cycles for 128 x 128 pairs of a head,
+// 10.5 MFLOP in 1280 cycles.  The softmax of a half has as long as the other
+// half's products, 1280 cycles for 128 exponentials a thread.
+//
+// Persistent: the plan kernel sorts the blocks of 256 rows of all sequences by
+// their number of key tiles, the CTAs take items from that list, longest first,
+// by a counter.  Every wait is bounded (watchdog).
+#include "mla_device.cuh"
+#include "mla_internal.h"
+
+namespace mla {
+namespace {
+
+constexpr int kHeadV = 128;
+constexpr int kBlock = kPromptBlock;  // query rows of an item
+constexpr int kHalfRows = 128, kKeys = 128;
+constexpr int kChunkBytes = 128 * 128;  // 128 rows of 64 bf16 values
+constexpr int kSlots = 8, kKChunks = 3, kVChunks = 2, kTileChunks = kKChunks + kVChunks;
+constexpr int kQOff = 0;
+constexpr int kRingOff = 2 * kKChunks * kChunkBytes;
+constexpr int kAuxOff = kRingOff + kSlots * kChunkBytes;
+constexpr int kItemInts = 8;
+constexpr int kItemOff = kAuxOff;  // [2] items
+constexpr int kMiscOff = kItemOff + 2 * kItemInts * 4;
+constexpr int kBarOff = kMiscOff + 16;
+constexpr int kNumBars = 2 * kSlots + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2 + 1;
+constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory");
+constexpr int kThreads = 384;
+constexpr uint32_t kRegsCtl = 88, kRegsSoft = 208, kLaunchRegs = 168;
+// setmaxnreg hands out what the block was launched with and waits for ever for more
+static_assert(kRegsCtl + 2 * kRegsSoft <= 3 * kLaunchRegs && kThreads * kLaunchRegs <= 65536, "register split");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSCol = 0, kOCol = 256;  // 128 columns a half
+constexpr float kRescale = 8.f;             // log2 units that a score may pass the reference by before it is raised
+constexpr float kNegInf = -__builtin_huge_valf();
+
+struct Item {
+  int q0, rows, k0, m, see, head, end;  // see: keys that row 0 sees (causal); end: no more items
+  // keys that row r sees
+  __device__ __forceinline__ int sees(int r, bool causal) const { return causal ? min(m, see + r) : m; }
+  // key tiles of half h
+  __device__ __forceinline__ int tiles(int h, bool causal) const {
+    const int n = min(rows - kHalfRows * h, kHalfRows);
+    if (n <= 0) return 0;
+    const int keys = sees(kHalfRows * h + n - 1, causal);
+    return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+  }
+};
+
+struct Bars {
+  uint64_t* full;        // [kSlots] a chunk has landed
+  uint64_t* empty;       // [kSlots] the products that read it are done
+  uint64_t* q_full;      // [2] Q of a half has landed
+  uint64_t* q_empty;     // the products that read Q of an item are done
+  uint64_t* s_full;      // [2] scores of a half are in tensor memory
+  uint64_t* p_full;      // [2] P of a half is written
+  uint64_t* o_full;      // [2] O of a half is complete
+  uint64_t* o_free;      // [2] O of a half has been read
+  uint64_t* item_full;   // [2]
+  uint64_t* item_empty;  // [2]
+  uint64_t* drained;     // all products are done
+};
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wd));
+}
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > wd.limit_ns) break;
+}
+
+// Item `n` of this CTA, as the load warp has put it into shared memory.
+__device__ __forceinline__ bool get_item(int n, uint8_t* smem, const Bars& bars, const Watchdog& wd, Item& it) {
+  if (!wait_warp(bars.item_full + (n & 1), (n >> 1) & 1, wd)) return false;
+  const volatile int* v = reinterpret_cast<const volatile int*>(smem + kItemOff) + (n & 1) * kItemInts;
+  it = Item{v[0], v[1], v[2], v[3], v[4], v[5], v[6]};
+  arrive_warp(bars.item_empty + (n & 1));
+  return !it.end;
+}
+
+// ---------------------------------------------------------------------------
+// loads, and the items (one thread)
+// ---------------------------------------------------------------------------
+struct Maps {
+  const CUtensorMap *q, *k_nope, *k_rope, *v;
+};
+__device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
+  const uint64_t pol = l2_policy_evict_normal();
+  const int group = p.h_q / p.h_kv;
+  const int total = p.plan[kPromptBlocks] * p.h_q;  // (at most 2^31 by the host's check)
+  uint64_t chunk = 0;  // chunks of keys and values so far
+  int n = 0, used = 0, loaded_q[2] = {0, 0};
+  int next = atomicAdd(p.plan + kPromptCounter, 1);
+#pragma unroll 1
+  for (;; ++n) {
+    const int at = next;
+    Item it{0, 0, 0, 0, 0, 0, 1};
+    if (at < total) {
+      const int4* e = reinterpret_cast<const int4*>(p.plan + kPromptList) + 2 * (at / p.h_q);
+      const int4 a = e[0], b = e[1];
+      it = Item{a.x, a.y, a.z, a.w, b.x, at % p.h_q, 0};
+      next = atomicAdd(p.plan + kPromptCounter, 1);
+    }
+    if (n >= 2 && !mbar_wait(bars.item_empty + (n & 1), ((n >> 1) - 1) & 1, wd)) break;
+    volatile int* v = reinterpret_cast<volatile int*>(smem + kItemOff) + (n & 1) * kItemInts;
+    v[0] = it.q0;
+    v[1] = it.rows;
+    v[2] = it.k0;
+    v[3] = it.m;
+    v[4] = it.see;
+    v[5] = it.head;
+    v[6] = it.end;
+    mbar_arrive(bars.item_full + (n & 1));
+    if (it.end) break;
+    const int nt0 = it.tiles(0, p.causal), nt1 = it.tiles(1, p.causal), nt = max(nt0, nt1);
+    if (nt == 0) continue;
+    if (used > 0 && !mbar_wait(bars.q_empty, (used - 1) & 1, wd)) break;
+    ++used;
+    auto load_q = [&](int h) {
+      mbar_arrive_expect_tx(bars.q_full + h, kKChunks * kChunkBytes);
+#pragma unroll
+      for (int c = 0; c < kKChunks; ++c)
+        tma_load_3d(smem + kQOff + (h * kKChunks + c) * kChunkBytes, tm.q, bars.q_full + h, 64 * c, it.head,
+                    it.q0 + kHalfRows * h, pol);
+      ++loaded_q[h];
+    };
+    if (nt0 > 0) load_q(0);
+    bool ok = true;
+    const int kv_head = it.head / group;
+#pragma unroll 1
+    for (int j = 0; j < nt && ok; ++j) {
+#pragma unroll 1
+      for (int c = 0; c < kTileChunks; ++c, ++chunk) {
+        const int slot = chunk % kSlots;
+        ok = chunk < kSlots || mbar_wait(bars.empty + slot, (chunk / kSlots - 1) & 1, wd);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bars.full + slot, kChunkBytes);
+        uint8_t* dst = smem + kRingOff + slot * kChunkBytes;
+        const int row = it.k0 + j * kKeys;
+        if (c < 2)
+          tma_load_3d(dst, tm.k_nope, bars.full + slot, 64 * c, kv_head, row, pol);
+        else if (c == 2)
+          tma_load_3d(dst, tm.k_rope, bars.full + slot, 0, 0, row, pol);  // (one head)
+        else {
+          // values 0 .. 63 go to the lower slot of the two (the ring's end lies between them where
+          // the first is its last): the MMAs take the second chunk a positive distance behind
+          const bool wraps = (chunk - (c - 3)) % kSlots == kSlots - 1;
+          tma_load_3d(dst, tm.v, bars.full + slot, 64 * ((c - 3) ^ (wraps ? 1 : 0)), kv_head, row, pol);
+        }
+        if (j == 0 && c == 2 && nt1 > 0) load_q(1);
+      }
+    }
+    if (!ok) break;
+  }
+  // no copy may be in flight when the CTA ends
+  for (uint64_t i = chunk > kSlots ? chunk - kSlots : 0; i < chunk; ++i) drain(bars.full + i % kSlots, (i / kSlots) & 1, wd);
+  for (int h = 0; h < 2; ++h)
+    if (loaded_q[h] > 0) drain(bars.q_full + h, (loaded_q[h] - 1) & 1, wd);
+}
+
+// ---------------------------------------------------------------------------
+// products (one warp)
+// ---------------------------------------------------------------------------
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ void products(const PromptParams& p, uint32_t tmem, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
+  const uint32_t base = desc_addr(smem);
+  constexpr uint64_t kHi = smem_desc_hi(16, 1024);
+  constexpr uint32_t kIdS = idesc_bf16_f32(kHalfRows, kKeys, 0, 0), kIdO = idesc_bf16_f32(kHalfRows, kHeadV, 0, 1);
+  uint64_t chunk = 0;  // first chunk of the item
+  int q_used[2] = {0, 0}, o_used[2] = {0, 0}, n_p[2] = {0, 0};
+  bool ok = true;
+  Item it;
+#pragma unroll 1
+  for (int n = 0; ok && get_item(n, smem, bars, wd, it); ++n) {
+    const int nt0 = it.tiles(0, p.causal), nt1 = it.tiles(1, p.causal), nt = max(nt0, nt1);
+    if (nt == 0) continue;
+    const int keys = it.sees(it.rows - 1, p.causal);
+    // S of half h, tile j
+    auto scores = [&](int h, int j) {
+      if (j >= (h ? nt1 : nt0) || !ok) return;
+      if (j == 0) ok = wait_warp(bars.q_full + h, q_used[h]++ & 1, wd);
+      const bool last_user = h == 1 || j >= nt1;
+#pragma unroll
+      for (int c = 0; c < kKChunks; ++c) {
+        const uint64_t i = chunk + static_cast<uint64_t>(j) * kTileChunks + c;
+        const int slot = static_cast<int>(i % kSlots);
+        ok = ok && wait_warp(bars.full + slot, (i / kSlots) & 1, wd);
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t a = kHi | ((base + kQOff + (h * kKChunks + c) * kChunkBytes) >> 4);
+          const uint64_t b = kHi | ((base + kRingOff + slot * kChunkBytes) >> 4);
+          if (ok) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_bf16_ss_fast(tmem + kSCol + 128 * h, a + 2 * k, b + 2 * k, kIdS, c + k > 0);
+          }
+          if (last_user) umma_commit(bars.empty + slot);
+          if (c == kKChunks - 1) umma_commit(bars.s_full + h);
+          if (c == kKChunks - 1 && last_user && j == nt - 1) umma_commit(bars.q_empty);
+        }
+        __syncwarp();
+      }
+    };
+    // O of half h, tile j
+    auto values = [&](int h, int j) {
+      const int tiles = h ? nt1 : nt0;
+      if (j >= tiles || !ok) return;
+      if (j == 0 && o_used[h] > 0) ok = wait_warp(bars.o_free + h, (o_used[h] - 1) & 1, wd);
+      if (j == 0) ++o_used[h];
+      ok = ok && wait_warp(bars.p_full + h, n_p[h]++ & 1, wd);
+      const bool last_user = h == 1 || j >= nt1;
+      const uint64_t i = chunk + static_cast<uint64_t>(j) * kTileChunks + kKChunks;
+      const int s0 = static_cast<int>(i % kSlots), s1 = static_cast<int>((i + 1) % kSlots);
+      ok = ok && wait_warp(bars.full + s0, (i / kSlots) & 1, wd) && wait_warp(bars.full + s1, ((i + 1) / kSlots) & 1, wd);
+      tc_fence_after();
+      if (elect_one()) {
+        const int first = min(s0, s1), second = max(s0, s1);
+        const uint64_t b = smem_desc_hi(0, 1024) |
+                           (static_cast<uint64_t>(((second - first) * kChunkBytes) >> 4) << 16) |
+                           ((base + kRingOff + first * kChunkBytes) >> 4);
+        const int steps = min(8, (keys - j * kKeys + 15) / 16);  // (rows behind the last key are not read)
+        if (ok) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < steps)
+              umma_bf16_ts(tmem + kOCol + 128 * h, tmem + kSCol + 128 * h + 8 * k, b + ((k * 16 * 128) >> 4), kIdO,
+                           j > 0 || k > 0);
+        }
+        if (last_user) {
+          umma_commit(bars.empty + s0);
+          umma_commit(bars.empty + s1);
+        }
+        if (j == tiles - 1) umma_commit(bars.o_full + h);
+      }
+      __syncwarp();
+    };
+    scores(0, 0);
+    scores(1, 0);
+#pragma unroll 1
+    for (int j = 0; j < nt && ok; ++j) {
+      values(0, j);
+      scores(0, j + 1);
+      values(1, j);
+      scores(1, j + 1);
+    }
+    chunk += static_cast<uint64_t>(nt) * kTileChunks;
+  }
+  // products still running end (or the waits do) before the memory they use is freed
+  if (elect_one()) umma_commit(bars.drained);
+  __syncwarp();
+  drain(bars.drained, 0, wd);
+}
+
+// ---------------------------------------------------------------------------
+// softmax and results: four warps a half, a row per thread
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ void tmem_st_words16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+__device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
+  const int sw = (threadIdx.x >> 5) - 4, half = sw >> 2, quarter = sw & 3, lane = threadIdx.x & 31;
+  const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+  const uint32_t s_at = tmem + lanes + kSCol + 128 * half, o_at = tmem + lanes + kOCol + 128 * half;
+  const int r = kHalfRows * half + 32 * quarter + lane;  // row of the item
+  const float scale = fmaxf(fabsf(p.scale_log2), 1.1754944e-38f);  // (0 would turn a masked score into NaN)
+  const bool negative = p.scale_log2 < 0.f;
+  uint64_t tile0 = 0;  // tiles of the CTA before the item
+  int n_s = 0, n_o = 0;
+  Item it;
+#pragma unroll 1
+  for (int n = 0; get_item(n, smem, bars, wd, it); ++n) {
+    const int tiles = it.tiles(half, p.causal), all_tiles = max(it.tiles(0, p.causal), it.tiles(1, p.causal));
+    const int sees = it.sees(r, p.causal), keys = it.sees(it.rows - 1, p.causal);
+    float ref = kNegInf, l = 0.f;
+    if (p.debug_stall) return;  // watchdog test: the scores are never taken
+#pragma unroll 1
+    for (int j = 0; j < tiles; ++j, ++n_s) {
+      if (!wait_warp(bars.s_full + half, n_s & 1, wd)) return;
+      tc_fence_after();
+      float x[kKeys];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float v[32];
+        tmem_ld_x32(s_at + 32 * c, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[32 * c + i] = v[i];
+      }
+      tmem_ld_wait();
+      if (negative) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
+      }
+      const int valid = sees - j * kKeys;  // of this tile's keys the row sees
+      if (__any_sync(0xffffffffu, valid < kKeys)) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i)
+          if (i >= valid) x[i] = kNegInf;
+      }
+      float m0 = max3_nan(x[0], x[1], x[2]), m1 = max3_nan(x[3], x[4], x[5]);
+      float m2 = max3_nan(x[6], x[7], x[8]), m3 = max3_nan(x[9], x[10], x[11]);
+#pragma unroll
+      for (int i = 12; i < kKeys - 4; i += 8) {
+        m0 = max3_nan(m0, x[i], x[i + 1]);
+        m1 = max3_nan(m1, x[i + 2], x[i + 3]);
+        m2 = max3_nan(m2, x[i + 4], x[i + 5]);
+        m3 = max3_nan(m3, x[i + 6], x[i + 7]);
+      }
+      m0 = max3_nan(m0, x[124], x[125]);
+      m1 = max3_nan(m1, x[126], x[127]);
+      const float top = max_nan(max_nan(m0, m1), max_nan(m2, m3)) * scale;
+      const bool raise = !(top <= ref + kRescale);
+      if (__any_sync(0xffffffffu, raise)) {
+        // (the scores' barrier follows the products of O of the tile before)
+        float alpha = 1.f;
+        if (raise) {
+          alpha = ref == kNegInf ? 1.f : fast_exp2(ref - top);
+          ref = top;
+          l *= alpha;
+        }
+        if (j > 0) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float o[16];
+            tmem_ld_x16(o_at + 16 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st_x16(o_at + 16 * c, o);
+          }
+        }
+      }
+      const float down = ref == kNegInf ? 0.f : -ref;
+      float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float2 y = fma2(make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), make_float2(scale, scale),
+                          make_float2(down, down));
+          y.x = fast_exp2(y.x);
+          y.y = fast_exp2(y.y);
+          if (i & 1)
+            sum1 = add2(sum1, y);
+          else
+            sum0 = add2(sum0, y);
+          w[i] = pack_bf16x2(y.x, y.y);
+        }
+        tmem_st_words16(s_at + 16 * c, w);
+      }
+      l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+      if ((j + 1) * kKeys > keys && j == all_tiles - 1 && (keys & 15) != 0) {
+        // Rows of V behind the last key that the products read (up to a multiple of 16)
+        // belong to other sequences, or to no one: zeros, so that no NaN of theirs
+        // meets a weight of 0.  Each half writes them.
+        const uint64_t i = (tile0 + j) * kTileChunks + kKChunks;
+        const int first = keys - j * kKeys, row = first + (threadIdx.x & 127) / 8, unit = threadIdx.x & 7;
+        bool ok = true;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          ok = ok && wait_warp(bars.full + (i + c) % kSlots, ((i + c) / kSlots) & 1, wd);
+        if (!ok) return;
+        if (row < ((first + 15) & ~15)) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            st_shared_v4(smem_u32(smem) + kRingOff + static_cast<uint32_t>((i + c) % kSlots) * kChunkBytes + row * 128 + unit * 16,
+                         0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // (the arrivals of all four warps on P's barrier hand the rows over)
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      arrive_warp(bars.p_full + half);
+    }
+    tile0 += all_tiles;
+
+    const bool real = r < it.rows;
+    const int64_t row = static_cast<int64_t>(it.q0 + r) * p.h_q + it.head;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * kHeadV;
+    if (tiles > 0) {
+      if (!wait_warp(bars.o_full + half, n_o++ & 1, wd)) return;
+      tc_fence_after();
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float o[32];
+      if (tiles > 0) {
+        tmem_ld_x32(o_at + 32 * c, o);
+        tmem_ld_wait();
+        if (c == 3) {
+          tc_fence_before();
+          arrive_warp(bars.o_free + half);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+      }
+      if (real) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = l == 0.f ? 0u : pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<uint4*>(out)[4 * c + i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
+    }
+    if (real) p.lse[row] = l == 0.f ? kNegInf : ref + log2f(l);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k_nope,
+                  const __grid_constant__ CUtensorMap tm_k_rope, const __grid_constant__ CUtensorMap tm_v,
+                  const PromptParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kMiscOff + 4);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kBarOff);
+  uint64_t* next = bar;
+  auto take = [&](int n) {
+    uint64_t* b = next;
+    next += n;
+    return b;
+  };
+  Bars bars;
+  bars.full = take(kSlots);
+  bars.empty = take(kSlots);
+  bars.q_full = take(2);
+  bars.q_empty = take(1);
+  bars.s_full = take(2);
+  bars.p_full = take(2);
+  bars.o_full = take(2);
+  bars.o_free = take(2);
+  bars.item_full = take(2);
+  bars.item_empty = take(2);
+  bars.drained = take(1);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(bars.full + i, 1);
+      mbar_init(bars.empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars.q_full + i, 1);
+      mbar_init(bars.s_full + i, 1);
+      mbar_init(bars.p_full + i, 4);
+      mbar_init(bars.o_full + i, 1);
+      mbar_init(bars.o_free + i, 4);
+      mbar_init(bars.item_full + i, 1);
+      mbar_init(bars.item_empty + i, 9);  // eight softmax warps and the products'
+    }
+    mbar_init(bars.q_empty, 1);
+    mbar_init(bars.drained, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k_nope);
+    tma_prefetch_desc(&tm_k_rope);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 2) {
+    tmem_alloc(const_cast<uint32_t*>(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Watchdog wd{abort_flag, p.status, p.timeout_ns};
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp < 4) {
+    regs_to<kRegsCtl, kLaunchRegs>();
+    if (warp == 0) {
+      if ((threadIdx.x & 31) == 0) load(Maps{&tm_q, &tm_k_nope, &tm_k_rope, &tm_v}, p, smem, bars, wd);
+      __syncwarp();
+    }
+    if (warp == 1) products(p, tmem, smem, bars, wd);
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_dealloc(tmem, kTmemCols);
+  } else {
+    regs_to<kRegsSoft, kLaunchRegs>();
+    softmax(p, tmem, smem, bars, wd);
+    tc_fence_before();
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the plan: blocks of all sequences, those with the most key tiles first
+// ---------------------------------------------------------------------------
+// A counting sort over 1024 classes of key tiles in one CTA (the order within a
+// class is free: an item's result does not depend on when it runs).  Also sets the
+// counter that the items are taken by to zero, so that each call starts it anew.
+constexpr int kPlanThreads = 1024, kClasses = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p) {
+  extern __shared__ int first[];  // [batch + 1] blocks of the sequences before
+  __shared__ int warp_sum[32], classes[kClasses], most;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // sequence b: its rows within the rows of q, its keys within those of k
+  auto clamp_to = [](int v, int most) { return min(max(v, 0), most); };
+  auto q_begin = [&](int b) { return clamp_to(p.q_offsets[b], p.num_q); };
+  auto k_begin = [&](int b) { return clamp_to(p.k_offsets[b], p.num_k); };
+  auto blocks_of = [&](int b) { return (max(q_begin(b + 1) - q_begin(b), 0) + kBlock - 1) / kBlock; };
+  const int per = (p.batch + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    first[b] = mine;
+    mine += blocks_of(b);
+  }
+  int x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  if (tid == 0) most = 0;
+  classes[tid] = 0;
+  __syncthreads();
+  if (warp == 0) {
+    int t = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += y;
+    }
+    warp_sum[lane] = t;
+  }
+  __syncthreads();
+  const int before = x - mine + (warp > 0 ? warp_sum[warp - 1] : 0);
+  for (int b = b0; b < b1; ++b) first[b] += before;
+  int total = warp_sum[31];
+  if (tid == 0) first[p.batch] = total;
+  __syncthreads();
+  // (offsets that decrease may name more blocks than the list has room for)
+  if (total > p.max_blocks) {
+    if (tid == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
+    total = 0;
+  }
+  // block i: its entry and its key tiles
+  auto entry = [&](int i, int4& a, int& see) {
+    int lo = 0, hi = p.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= i)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int q0 = q_begin(lo), n = q_begin(lo + 1) - q0, k0 = k_begin(lo), m = max(k_begin(lo + 1) - k0, 0);
+    const int at = (i - first[lo]) * kBlock, rows = min(kBlock, n - at);
+    a = make_int4(q0 + at, rows, k0, m);
+    see = m - n + at + 1;
+    const int keys = p.causal ? min(m, see + rows - 1) : m;
+    return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+  };
+  int longest = 0;
+  for (int i = tid; i < total; i += kPlanThreads) {
+    int4 a;
+    int see;
+    longest = max(longest, entry(i, a, see));
+  }
+  atomicMax(&most, longest);
+  __syncthreads();
+  int shift = 0;
+  while ((most >> shift) >= kClasses) ++shift;
+  for (int i = tid; i < total; i += kPlanThreads) {
+    int4 a;
+    int see;
+    atomicAdd(&classes[kClasses - 1 - (entry(i, a, see) >> shift)], 1);
+  }
+  __syncthreads();
+  // places of the classes, the longest first
+  int c = classes[tid], z = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, z, o);
+    if (lane >= o) z += y;
+  }
+  if (lane == 31) warp_sum[warp] = z;
+  __syncthreads();
+  if (warp == 0) {
+    int t = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += y;
+    }
+    warp_sum[lane] = t;
+  }
+  __syncthreads();
+  classes[tid] = z - c + (warp > 0 ? warp_sum[warp - 1] : 0);
+  __syncthreads();
+  int4* list = reinterpret_cast<int4*>(p.plan + kPromptList);
+  for (int i = tid; i < total; i += kPlanThreads) {
+    int4 a;
+    int see;
+    const int tiles = entry(i, a, see);
+    const int at = atomicAdd(&classes[kClasses - 1 - (tiles >> shift)], 1);
+    list[2 * at] = a;
+    list[2 * at + 1] = make_int4(see, 0, 0, 0);
+  }
+  if (tid == 0) {
+    p.plan[kPromptCounter] = 0;
+    p.plan[kPromptBlocks] = total;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(const CUtensorMap& tm_q, const CUtensorMap& tm_k_nope, const CUtensorMap& tm_k_rope,
+                          const CUtensorMap& tm_v, const PromptParams& p, int sm_count, cudaStream_t stream) {
+  const size_t scratch = (static_cast<size_t>(p.batch) + 1) * sizeof(int);
+  cudaError_t e = allow_dynamic_smem(plan_kernel, scratch, 8192);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, prompt_kernel);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = scratch;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, plan_kernel, p);
+  if (e != cudaSuccess) return e;
+  const int64_t items = static_cast<int64_t>(p.max_blocks) * p.h_q;
+  cfg.gridDim = dim3(static_cast<unsigned>(items < sm_count ? items : sm_count));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  return cudaLaunchKernelEx(&cfg, prompt_kernel, tm_q, tm_k_nope, tm_k_rope, tm_v, p);
+}
+
+}  // namespace mla
