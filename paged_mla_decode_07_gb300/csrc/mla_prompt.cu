@@ -42,7 +42,7 @@ constexpr int kItemInts = 8;
 constexpr int kItemOff = kAuxOff;  // [2] items
 constexpr int kMiscOff = kItemOff + 2 * kItemInts * 4;
 constexpr int kBarOff = kMiscOff + 16;
-constexpr int kNumBars = 2 * kSlots + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2 + 1;
+constexpr int kNumBars = 2 * kSlots + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2 + 2;
 constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr int kThreads = 384;
@@ -74,11 +74,11 @@ struct Bars {
   uint64_t* q_empty;     // the products that read Q of an item are done
   uint64_t* s_full;      // [2] scores of a half are in tensor memory
   uint64_t* p_full;      // [2] P of a half is written
-  uint64_t* o_full;      // [2] O of a half is complete
+  uint64_t* pv_done;     // [2] the products of O of a half's tile are done
   uint64_t* o_free;      // [2] O of a half has been read
   uint64_t* item_full;   // [2]
   uint64_t* item_empty;  // [2]
-  uint64_t* drained;     // all products are done
+  uint64_t* drained;     // [2] all products of S, of O, are done
 };
 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
@@ -113,7 +113,7 @@ __device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const
   const uint64_t pol = l2_policy_evict_normal();
   const int group = p.h_q / p.h_kv;
   const int total = p.plan[kPromptBlocks] * p.h_q;  // (at most 2^31 by the host's check)
-  uint64_t chunk = 0;  // chunks of keys and values so far
+  uint32_t chunk = 0;  // chunks of keys and values so far
   int n = 0, used = 0, loaded_q[2] = {0, 0};
   int next = atomicAdd(p.plan + kPromptCounter, 1);
 #pragma unroll 1
@@ -178,13 +178,13 @@ __device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const
     if (!ok) break;
   }
   // no copy may be in flight when the CTA ends
-  for (uint64_t i = chunk > kSlots ? chunk - kSlots : 0; i < chunk; ++i) drain(bars.full + i % kSlots, (i / kSlots) & 1, wd);
+  for (uint32_t i = chunk > kSlots ? chunk - kSlots : 0; i < chunk; ++i) drain(bars.full + i % kSlots, (i / kSlots) & 1, wd);
   for (int h = 0; h < 2; ++h)
     if (loaded_q[h] > 0) drain(bars.q_full + h, (loaded_q[h] - 1) & 1, wd);
 }
 
 // ---------------------------------------------------------------------------
-// products (one warp)
+// products: those of S (one warp), those of O (one warp)
 // ---------------------------------------------------------------------------
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -196,93 +196,109 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
-__device__ void products(const PromptParams& p, uint32_t tmem, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
+__device__ void score_products(const PromptParams& p, uint32_t tmem, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
   const uint32_t base = desc_addr(smem);
   constexpr uint64_t kHi = smem_desc_hi(16, 1024);
-  constexpr uint32_t kIdS = idesc_bf16_f32(kHalfRows, kKeys, 0, 0), kIdO = idesc_bf16_f32(kHalfRows, kHeadV, 0, 1);
-  uint64_t chunk = 0;  // first chunk of the item
-  int q_used[2] = {0, 0}, o_used[2] = {0, 0}, n_p[2] = {0, 0};
+  constexpr uint32_t kIdS = idesc_bf16_f32(kHalfRows, kKeys, 0, 0);
+  uint32_t chunk = 0;  // first chunk of the tile
+  int items[2] = {0, 0}, tiles[2] = {0, 0};
   bool ok = true;
   Item it;
 #pragma unroll 1
   for (int n = 0; ok && get_item(n, smem, bars, wd, it); ++n) {
     const int nt0 = it.tiles(0, p.causal), nt1 = it.tiles(1, p.causal), nt = max(nt0, nt1);
-    if (nt == 0) continue;
-    const int keys = it.sees(it.rows - 1, p.causal);
-    // S of half h, tile j
-    auto scores = [&](int h, int j) {
-      if (j >= (h ? nt1 : nt0) || !ok) return;
-      if (j == 0) ok = wait_warp(bars.q_full + h, q_used[h]++ & 1, wd);
-      const bool last_user = h == 1 || j >= nt1;
-#pragma unroll
-      for (int c = 0; c < kKChunks; ++c) {
-        const uint64_t i = chunk + static_cast<uint64_t>(j) * kTileChunks + c;
-        const int slot = static_cast<int>(i % kSlots);
-        ok = ok && wait_warp(bars.full + slot, (i / kSlots) & 1, wd);
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t a = kHi | ((base + kQOff + (h * kKChunks + c) * kChunkBytes) >> 4);
-          const uint64_t b = kHi | ((base + kRingOff + slot * kChunkBytes) >> 4);
-          if (ok) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16_ss_fast(tmem + kSCol + 128 * h, a + 2 * k, b + 2 * k, kIdS, c + k > 0);
-          }
-          if (last_user) umma_commit(bars.empty + slot);
-          if (c == kKChunks - 1) umma_commit(bars.s_full + h);
-          if (c == kKChunks - 1 && last_user && j == nt - 1) umma_commit(bars.q_empty);
-        }
-        __syncwarp();
-      }
-    };
-    // O of half h, tile j
-    auto values = [&](int h, int j) {
-      const int tiles = h ? nt1 : nt0;
-      if (j >= tiles || !ok) return;
-      if (j == 0 && o_used[h] > 0) ok = wait_warp(bars.o_free + h, (o_used[h] - 1) & 1, wd);
-      if (j == 0) ++o_used[h];
-      ok = ok && wait_warp(bars.p_full + h, n_p[h]++ & 1, wd);
-      const bool last_user = h == 1 || j >= nt1;
-      const uint64_t i = chunk + static_cast<uint64_t>(j) * kTileChunks + kKChunks;
-      const int s0 = static_cast<int>(i % kSlots), s1 = static_cast<int>((i + 1) % kSlots);
-      ok = ok && wait_warp(bars.full + s0, (i / kSlots) & 1, wd) && wait_warp(bars.full + s1, ((i + 1) / kSlots) & 1, wd);
-      tc_fence_after();
-      if (elect_one()) {
-        const int first = min(s0, s1), second = max(s0, s1);
-        const uint64_t b = smem_desc_hi(0, 1024) |
-                           (static_cast<uint64_t>(((second - first) * kChunkBytes) >> 4) << 16) |
-                           ((base + kRingOff + first * kChunkBytes) >> 4);
-        const int steps = min(8, (keys - j * kKeys + 15) / 16);  // (rows behind the last key are not read)
-        if (ok) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < steps)
-              umma_bf16_ts(tmem + kOCol + 128 * h, tmem + kSCol + 128 * h + 8 * k, b + ((k * 16 * 128) >> 4), kIdO,
-                           j > 0 || k > 0);
-        }
-        if (last_user) {
-          umma_commit(bars.empty + s0);
-          umma_commit(bars.empty + s1);
-        }
-        if (j == tiles - 1) umma_commit(bars.o_full + h);
-      }
-      __syncwarp();
-    };
-    scores(0, 0);
-    scores(1, 0);
 #pragma unroll 1
-    for (int j = 0; j < nt && ok; ++j) {
-      values(0, j);
-      scores(0, j + 1);
-      values(1, j);
-      scores(1, j + 1);
+    for (int j = 0; j < nt && ok; ++j, chunk += kTileChunks) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (j >= (h ? nt1 : nt0)) continue;
+        const bool last_user = h == 1 || j >= nt1;
+        if (j == 0) ok = ok && wait_warp(bars.q_full + h, items[h]++ & 1, wd);
+        // P, which lies where S will, has been read
+        ok = ok && (tiles[h] == 0 || wait_warp(bars.pv_done + h, (tiles[h] - 1) & 1, wd));
+        ++tiles[h];
+        const uint32_t d = tmem + kSCol + 128 * h;
+        const uint32_t q_at = base + kQOff + h * kKChunks * kChunkBytes;
+#pragma unroll
+        for (int c = 0; c < kKChunks; ++c) {
+          const uint32_t slot = (chunk + c) % kSlots;
+          if (h == 0 || j >= nt0) ok = ok && wait_warp(bars.full + slot, ((chunk + c) / kSlots) & 1, wd);
+          if (c == 0 || h == 0) tc_fence_after();
+          if (elect_one()) {
+            const uint64_t a = kHi | ((q_at + c * kChunkBytes) >> 4);
+            const uint64_t b = kHi | ((base + kRingOff + slot * kChunkBytes) >> 4);
+            if (ok) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) umma_bf16_ss_fast(d, a + 2 * k, b + 2 * k, kIdS, c + k > 0);
+            }
+            if (last_user) umma_commit(bars.empty + slot);
+            if (c == kKChunks - 1) {
+              umma_commit(bars.s_full + h);
+              if (last_user && j == nt - 1) umma_commit(bars.q_empty);
+            }
+          }
+          __syncwarp();
+        }
+      }
     }
-    chunk += static_cast<uint64_t>(nt) * kTileChunks;
   }
-  // products still running end (or the waits do) before the memory they use is freed
+  // products still running end (or the wait does) before the memory they use is freed
   if (elect_one()) umma_commit(bars.drained);
   __syncwarp();
   drain(bars.drained, 0, wd);
+}
+
+__device__ void value_products(const PromptParams& p, uint32_t tmem, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
+  const uint32_t base = desc_addr(smem);
+  constexpr uint32_t kIdO = idesc_bf16_f32(kHalfRows, kHeadV, 0, 1);
+  uint32_t chunk = kKChunks;  // first chunk of the tile's values
+  int items[2] = {0, 0}, tiles[2] = {0, 0};
+  bool ok = true;
+  Item it;
+#pragma unroll 1
+  for (int n = 0; ok && get_item(n, smem, bars, wd, it); ++n) {
+    const int nt0 = it.tiles(0, p.causal), nt1 = it.tiles(1, p.causal), nt = max(nt0, nt1);
+    const int keys = it.sees(it.rows - 1, p.causal);
+#pragma unroll 1
+    for (int j = 0; j < nt && ok; ++j, chunk += kTileChunks) {
+      const uint32_t s0 = chunk % kSlots, s1 = (chunk + 1) % kSlots;
+      const uint32_t first = min(s0, s1), gap = max(s0, s1) - first;
+      const uint64_t b = smem_desc_hi(0, 1024) | (static_cast<uint64_t>(gap * kChunkBytes >> 4) << 16) |
+                         ((base + kRingOff + first * kChunkBytes) >> 4);
+      const int steps = min(8, (keys - j * kKeys + 15) / 16);  // (rows behind the last key are not read)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (j >= (h ? nt1 : nt0)) continue;
+        const bool last_user = h == 1 || j >= nt1;
+        if (j == 0) {
+          ok = ok && (items[h] == 0 || wait_warp(bars.o_free + h, (items[h] - 1) & 1, wd));
+          ++items[h];
+        }
+        if (h == 0 || j >= nt0)
+          ok = ok && wait_warp(bars.full + s0, (chunk / kSlots) & 1, wd) && wait_warp(bars.full + s1, ((chunk + 1) / kSlots) & 1, wd);
+        ok = ok && wait_warp(bars.p_full + h, tiles[h]++ & 1, wd);
+        tc_fence_after();
+        if (elect_one()) {
+          if (ok) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < steps)
+                umma_bf16_ts(tmem + kOCol + 128 * h, tmem + kSCol + 128 * h + 8 * k, b + ((k * 16 * 128) >> 4), kIdO,
+                             j > 0 || k > 0);
+          }
+          umma_commit(bars.pv_done + h);
+          if (last_user) {
+            umma_commit(bars.empty + s0);
+            umma_commit(bars.empty + s1);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  if (elect_one()) umma_commit(bars.drained + 1);
+  __syncwarp();
+  drain(bars.drained + 1, 0, wd);
 }
 
 // ---------------------------------------------------------------------------
@@ -325,8 +341,8 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
   const int r = kHalfRows * half + 32 * quarter + lane;  // row of the item
   const float scale = fmaxf(fabsf(p.scale_log2), 1.1754944e-38f);  // (0 would turn a masked score into NaN)
   const bool negative = p.scale_log2 < 0.f;
-  uint64_t tile0 = 0;  // tiles of the CTA before the item
-  int n_s = 0, n_o = 0;
+  uint32_t tile0 = 0;  // tiles of the CTA before the item
+  int n_s = 0;
   Item it;
 #pragma unroll 1
   for (int n = 0; get_item(n, smem, bars, wd, it); ++n) {
@@ -414,7 +430,7 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
         // Rows of V behind the last key that the products read (up to a multiple of 16)
         // belong to other sequences, or to no one: zeros, so that no NaN of theirs
         // meets a weight of 0.  Each half writes them.
-        const uint64_t i = (tile0 + j) * kTileChunks + kKChunks;
+        const uint32_t i = (tile0 + j) * kTileChunks + kKChunks;
         const int first = keys - j * kKeys, row = first + (threadIdx.x & 127) / 8, unit = threadIdx.x & 7;
         bool ok = true;
 #pragma unroll
@@ -424,7 +440,7 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
         if (row < ((first + 15) & ~15)) {
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            st_shared_v4(smem_u32(smem) + kRingOff + static_cast<uint32_t>((i + c) % kSlots) * kChunkBytes + row * 128 + unit * 16,
+            st_shared_v4(smem_u32(smem) + kRingOff + ((i + c) % kSlots) * kChunkBytes + row * 128 + unit * 16,
                          0, 0, 0, 0);
         }
         fence_proxy_async_smem();  // (the arrivals of all four warps on P's barrier hand the rows over)
@@ -439,7 +455,7 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
     const int64_t row = static_cast<int64_t>(it.q0 + r) * p.h_q + it.head;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * kHeadV;
     if (tiles > 0) {
-      if (!wait_warp(bars.o_full + half, n_o++ & 1, wd)) return;
+      if (!wait_warp(bars.pv_done + half, (n_s - 1) & 1, wd)) return;
       tc_fence_after();
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -494,11 +510,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   bars.q_empty = take(1);
   bars.s_full = take(2);
   bars.p_full = take(2);
-  bars.o_full = take(2);
+  bars.pv_done = take(2);
   bars.o_free = take(2);
   bars.item_full = take(2);
   bars.item_empty = take(2);
-  bars.drained = take(1);
+  bars.drained = take(2);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(bars.full + i, 1);
@@ -508,13 +524,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars.q_full + i, 1);
       mbar_init(bars.s_full + i, 1);
       mbar_init(bars.p_full + i, 4);
-      mbar_init(bars.o_full + i, 1);
+      mbar_init(bars.pv_done + i, 1);
+      mbar_init(bars.drained + i, 1);
       mbar_init(bars.o_free + i, 4);
       mbar_init(bars.item_full + i, 1);
-      mbar_init(bars.item_empty + i, 9);  // eight softmax warps and the products'
+      mbar_init(bars.item_empty + i, 10);  // eight softmax warps and two of products
     }
     mbar_init(bars.q_empty, 1);
-    mbar_init(bars.drained, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
@@ -539,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((threadIdx.x & 31) == 0) load(Maps{&tm_q, &tm_k_nope, &tm_k_rope, &tm_v}, p, smem, bars, wd);
       __syncwarp();
     }
-    if (warp == 1) products(p, tmem, smem, bars, wd);
+    if (warp == 1) score_products(p, tmem, smem, bars, wd);
+    if (warp == 3) value_products(p, tmem, smem, bars, wd);
     __syncthreads();
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tmem, kTmemCols);
