@@ -186,19 +186,36 @@ __device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const
 // ---------------------------------------------------------------------------
 // products: those of S (one warp), those of O (one warp)
 // ---------------------------------------------------------------------------
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The warps that issue share their schedulers with the softmax warps, so the code
+// between two MMAs has to be short (with a wait, an election and 64-bit
+// descriptors for every four of them an MMA took 100 cycles to issue, where it
+// runs for 64): descriptors are their lower words, the upper word being constant,
+// and all MMAs of a tile are issued from one elected thread at a time.
+constexpr uint32_t kDescHi = static_cast<uint32_t>(smem_desc_hi(0, 1024) >> 32);
+__host__ __device__ constexpr uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return (saddr >> 4) | ((lbo_bytes >> 4) << 16);
+}
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHi));
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHi));
 }
 
 __device__ void score_products(const PromptParams& p, uint32_t tmem, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
-  const uint32_t base = desc_addr(smem);
-  constexpr uint64_t kHi = smem_desc_hi(16, 1024);
+  const uint32_t base = desc_addr(smem), bars_empty = smem_u32(bars.empty);
+  const uint32_t q_lo = desc_lo(base + kQOff, 16), ring_lo = desc_lo(base + kRingOff, 16);
   constexpr uint32_t kIdS = idesc_bf16_f32(kHalfRows, kKeys, 0, 0);
   uint32_t chunk = 0;  // first chunk of the tile
   int items[2] = {0, 0}, tiles[2] = {0, 0};
@@ -217,28 +234,33 @@ __device__ void score_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
         // P, which lies where S will, has been read
         ok = ok && (tiles[h] == 0 || wait_warp(bars.pv_done + h, (tiles[h] - 1) & 1, wd));
         ++tiles[h];
-        const uint32_t d = tmem + kSCol + 128 * h;
-        const uint32_t q_at = base + kQOff + h * kKChunks * kChunkBytes;
+        if (h == 0 || j >= nt0) {
 #pragma unroll
-        for (int c = 0; c < kKChunks; ++c) {
-          const uint32_t slot = (chunk + c) % kSlots;
-          if (h == 0 || j >= nt0) ok = ok && wait_warp(bars.full + slot, ((chunk + c) / kSlots) & 1, wd);
-          if (c == 0 || h == 0) tc_fence_after();
-          if (elect_one()) {
-            const uint64_t a = kHi | ((q_at + c * kChunkBytes) >> 4);
-            const uint64_t b = kHi | ((base + kRingOff + slot * kChunkBytes) >> 4);
-            if (ok) {
+          for (int c = 0; c < kKChunks; ++c)
+            ok = ok && wait_warp(bars.full + (chunk + c) % kSlots, ((chunk + c) / kSlots) & 1, wd);
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t s0 = chunk % kSlots, s1 = (chunk + 1) % kSlots, s2 = (chunk + 2) % kSlots;
+          if (ok) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) umma_bf16_ss_fast(d, a + 2 * k, b + 2 * k, kIdS, c + k > 0);
-            }
-            if (last_user) umma_commit(bars.empty + slot);
-            if (c == kKChunks - 1) {
-              umma_commit(bars.s_full + h);
-              if (last_user && j == nt - 1) umma_commit(bars.q_empty);
+            for (int c = 0; c < kKChunks; ++c) {
+              const uint32_t b = ring_lo + (c == 0 ? s0 : c == 1 ? s1 : s2) * (kChunkBytes >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_ss(tmem + kSCol + 128 * h, q_lo + (((h * kKChunks + c) * kChunkBytes) >> 4) + 2 * k, b + 2 * k, kIdS,
+                        c + k > 0);
             }
           }
-          __syncwarp();
+          umma_commit(bars.s_full + h);
+          if (last_user) {
+            umma_commit_u32(bars_empty + 8 * s0);
+            umma_commit_u32(bars_empty + 8 * s1);
+            umma_commit_u32(bars_empty + 8 * s2);
+            if (j == nt - 1) umma_commit(bars.q_empty);
+          }
         }
+        __syncwarp();
       }
     }
   }
@@ -263,8 +285,7 @@ __device__ void value_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
     for (int j = 0; j < nt && ok; ++j, chunk += kTileChunks) {
       const uint32_t s0 = chunk % kSlots, s1 = (chunk + 1) % kSlots;
       const uint32_t first = min(s0, s1), gap = max(s0, s1) - first;
-      const uint64_t b = smem_desc_hi(0, 1024) | (static_cast<uint64_t>(gap * kChunkBytes >> 4) << 16) |
-                         ((base + kRingOff + first * kChunkBytes) >> 4);
+      const uint32_t b = desc_lo(base + kRingOff + first * kChunkBytes, gap * kChunkBytes);
       const int steps = min(8, (keys - j * kKeys + 15) / 16);  // (rows behind the last key are not read)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -283,8 +304,7 @@ __device__ void value_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               if (k < steps)
-                umma_bf16_ts(tmem + kOCol + 128 * h, tmem + kSCol + 128 * h + 8 * k, b + ((k * 16 * 128) >> 4), kIdO,
-                             j > 0 || k > 0);
+                umma_ts(tmem + kOCol + 128 * h, tmem + kSCol + 128 * h + 8 * k, b + ((k * 16 * 128) >> 4), kIdO, j > 0 || k > 0);
           }
           umma_commit(bars.pv_done + h);
           if (last_user) {
