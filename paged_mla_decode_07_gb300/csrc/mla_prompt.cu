@@ -231,14 +231,15 @@ __device__ void score_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
         if (j >= (h ? nt1 : nt0)) continue;
         const bool last_user = h == 1 || j >= nt1;
         if (j == 0) ok = ok && wait_warp(bars.q_full + h, items[h]++ & 1, wd);
-        // P, which lies where S will, has been read
-        ok = ok && (tiles[h] == 0 || wait_warp(bars.pv_done + h, (tiles[h] - 1) & 1, wd));
-        ++tiles[h];
         if (h == 0 || j >= nt0) {
 #pragma unroll
           for (int c = 0; c < kKChunks; ++c)
             ok = ok && wait_warp(bars.full + (chunk + c) % kSlots, ((chunk + c) / kSlots) & 1, wd);
         }
+        // P, which lies where S will, has been read (the last wait: each takes about a hundred
+        // cycles, and this one ends last)
+        ok = ok && (tiles[h] == 0 || wait_warp(bars.pv_done + h, (tiles[h] - 1) & 1, wd));
+        ++tiles[h];
         tc_fence_after();
         if (elect_one()) {
           const uint32_t s0 = chunk % kSlots, s1 = (chunk + 1) % kSlots, s2 = (chunk + 2) % kSlots;
