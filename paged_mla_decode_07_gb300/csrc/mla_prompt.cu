@@ -115,17 +115,17 @@ __device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const
   const int total = p.plan[kPromptBlocks] * p.h_q;  // (at most 2^31 by the host's check)
   uint32_t chunk = 0;  // chunks of keys and values so far
   int n = 0, used = 0, loaded_q[2] = {0, 0};
-  int next = atomicAdd(p.plan + kPromptCounter, 1);
+  auto fetch = [&]() {
+    const int at = atomicAdd(p.plan + kPromptCounter, 1);
+    if (at >= total) return Item{0, 0, 0, 0, 0, 0, 1};
+    const int4* e = reinterpret_cast<const int4*>(p.plan + kPromptList) + 2 * (at / p.h_q);
+    const int4 a = e[0], b = e[1];
+    return Item{a.x, a.y, a.z, a.w, b.x, at % p.h_q, 0};
+  };
+  Item next = fetch();
 #pragma unroll 1
   for (;; ++n) {
-    const int at = next;
-    Item it{0, 0, 0, 0, 0, 0, 1};
-    if (at < total) {
-      const int4* e = reinterpret_cast<const int4*>(p.plan + kPromptList) + 2 * (at / p.h_q);
-      const int4 a = e[0], b = e[1];
-      it = Item{a.x, a.y, a.z, a.w, b.x, at % p.h_q, 0};
-      next = atomicAdd(p.plan + kPromptCounter, 1);
-    }
+    const Item it = next;  // (the next one is on its way while this one's tiles are loaded)
     if (n >= 2 && !mbar_wait(bars.item_empty + (n & 1), ((n >> 1) - 1) & 1, wd)) break;
     volatile int* v = reinterpret_cast<volatile int*>(smem + kItemOff) + (n & 1) * kItemInts;
     v[0] = it.q0;
@@ -137,6 +137,7 @@ __device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const
     v[6] = it.end;
     mbar_arrive(bars.item_full + (n & 1));
     if (it.end) break;
+    next = fetch();
     const int nt0 = it.tiles(0, p.causal), nt1 = it.tiles(1, p.causal), nt = max(nt0, nt1);
     if (nt == 0) continue;
     if (used > 0 && !mbar_wait(bars.q_empty, (used - 1) & 1, wd)) break;
@@ -362,6 +363,7 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
   const int r = kHalfRows * half + 32 * quarter + lane;  // row of the item
   const float scale = fmaxf(fabsf(p.scale_log2), 1.1754944e-38f);  // (0 would turn a masked score into NaN)
   const bool negative = p.scale_log2 < 0.f;
+  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
   uint32_t tile0 = 0;  // tiles of the CTA before the item
   int n_s = 0;
   Item it;
@@ -499,9 +501,14 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           w[i] = l == 0.f ? 0u : pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+        if (wide) {  // whole sectors: each store instruction costs a pass per row
+          st_global_v8(out + 32 * c, {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]});
+          st_global_v8(out + 32 * c + 16, {w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]});
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<uint4*>(out)[4 * c + i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(out)[4 * c + i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
       }
     }
     if (real) p.lse[row] = l == 0.f ? kNegInf : ref + log2f(l);
