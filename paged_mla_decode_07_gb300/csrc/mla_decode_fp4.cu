@@ -102,15 +102,25 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_format, int 
 // P lies MN-major without swizzle: 128-byte blocks of 8 tokens with 16 rows
 // each, those of the next tokens behind them (leading offset), those of the next
 // 16 rows 2 KB on (stride offset): a thread writes its rows of a token at once.
-constexpr uint64_t kHiP = (static_cast<uint64_t>(128 >> 4) << 16) | (static_cast<uint64_t>(2048 >> 4) << 32) |
-                          (static_cast<uint64_t>(1) << 46);
-__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+constexpr uint32_t kDescHiP = (2048u >> 4) | (1u << 14);
+// Descriptors as words: the code between two MMAs has to be short where the warp
+// that issues them shares its scheduler with busy ones.
+__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                           bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %6};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHi), "r"(b_hi));
+}
+__device__ __forceinline__ void umma_bf16_words(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, 1, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(kDescHi));
 }
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -476,9 +486,8 @@ template <int R>
 __device__ void score_products(const DecodeParams& p, const Range& rg, uint32_t tmem, uint8_t* smem, const Bars& bars,
                                const Watchdog& wd) {
   using C = Cfg<R>;
-  constexpr uint64_t kHi = smem_desc_hi(16, 1024);
   const uint32_t base = desc_addr(smem);
-  const uint64_t qd = kHi | ((base + C::kQOff) >> 4), qr = kHi | ((base + C::kQRopeOff) >> 4);
+  const uint32_t qd = desc_lo(base + C::kQOff, 16), qr = desc_lo(base + C::kQRopeOff, 16);
   int i = 0;
   bool ok = true;
 #pragma unroll 1
@@ -488,24 +497,26 @@ __device__ void score_products(const DecodeParams& p, const Range& rg, uint32_t 
 #pragma unroll 1
     for (int j = s.pb; j < s.pe && ok; j += 2, ++i) {
       const int b = i & 1, ph = (i >> 1) & 1;
-      const uint64_t a = kHi | ((base + b * kTileBytes) >> 4), ar = kHi | ((base + C::kRopeOff + b * kChunkBytes) >> 4);
+      const uint32_t a = desc_lo(base + b * kTileBytes, 16), ar = desc_lo(base + C::kRopeOff + b * kChunkBytes, 16);
       const uint32_t d = tmem + C::kSCol + 2 * R * b;
       if (i >= 2) ok = wait_warp(bars.p_full + b, ph ^ 1, wd);  // (the scores of two tiles before have been read)
 #pragma unroll
-      for (int c = 0; c < 5; ++c) {
-        if (c == 0 || c == 2) ok = ok && wait_warp(bars.k_full + 2 * b + (c >> 1), ph, wd);
-        if (c == 4) ok = ok && wait_warp(bars.rope_full + b, ph, wd);
+      for (int part = 0; part < 3; ++part) {  // two chunks, two chunks, RoPE
+        ok = ok && wait_warp(part < 2 ? bars.k_full + 2 * b + part : bars.rope_full + b, ph, wd);
         tc_fence_after();
         if (elect_one()) {
+          if (ok && part < 2) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (c < 4 && ok)
-              umma_f8_ss(d, a + ((c * kChunkBytes + 32 * k) >> 4), qd + ((c * C::kQChunk + 32 * k) >> 4),
-                         idesc_f8(kTile, 2 * R, 1, 0, 0), c + k > 0);
-            else if (ok)
-              umma_bf16_ss_fast(d, ar + ((32 * k) >> 4), qr + ((32 * k) >> 4), idesc_bf16_f32(kTile, R, 0, 0), 1);
+            for (int c = 2 * part; c < 2 * part + 2; ++c)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_f8_ss(d, a + ((c * kChunkBytes + 32 * k) >> 4), qd + ((c * C::kQChunk + 32 * k) >> 4), kDescHi,
+                           idesc_f8(kTile, 2 * R, 1, 0, 0), c + k > 0);
+          } else if (ok) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_bf16_words(d, ar + 2 * k, qr + 2 * k, idesc_bf16_f32(kTile, R, 0, 0));
           }
-          if (c == 4) umma_commit(bars.s_full + b);  // (of what has been issued, where a wait ran out too)
+          if (part == 2) umma_commit(bars.s_full + b);  // (of what has been issued, where a wait ran out too)
         }
         __syncwarp();
       }
@@ -519,7 +530,6 @@ template <int R>
 __device__ void value_products(const DecodeParams& p, const Range& rg, uint32_t tmem, uint8_t* smem, const Bars& bars,
                                const Watchdog& wd) {
   using C = Cfg<R>;
-  constexpr uint64_t kHiV = smem_desc_hi(kChunkBytes, 1024);
   const uint32_t base = desc_addr(smem);
   int i = 0, seg = 0;
   bool ok = true;
@@ -536,14 +546,14 @@ __device__ void value_products(const DecodeParams& p, const Range& rg, uint32_t 
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t a = kHiV | ((base + b * kTileBytes) >> 4);
-        const uint64_t pd = kHiP | ((base + C::kPOff + (i % C::kPBufs) * C::kPBytes) >> 4);
+        const uint32_t a = desc_lo(base + b * kTileBytes, kChunkBytes);
+        const uint32_t pd = desc_lo(base + C::kPOff + (i % C::kPBufs) * C::kPBytes, 128);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (k < steps)
-              umma_f8_ss(tmem + C::kOCol + 3 * R * c, a + ((c * kChunkBytes + k * 32 * 128) >> 4), pd + ((512 * k) >> 4),
+              umma_f8_ss(tmem + C::kOCol + 3 * R * c, a + ((c * kChunkBytes + k * 32 * 128) >> 4), pd + ((512 * k) >> 4), kDescHiP,
                          idesc_f8(128, 3 * R, 1, 1, 1), j > s.pb || k > 0);
           if (c & 1) umma_commit(bars.done + 2 * b + (c >> 1));
         }

@@ -350,6 +350,13 @@ __host__ __device__ constexpr uint64_t smem_desc_hi(uint32_t lbo_bytes, uint32_t
          (static_cast<uint64_t>(2) << 61);
 }
 
+// The same in words, for issue loops that share a scheduler with busy warps: the
+// upper word (stride offset 1024) is constant, the lower one is the start and the
+// leading offset.
+constexpr uint32_t kDescHi = static_cast<uint32_t>(smem_desc_hi(0, 1024) >> 32);
+__host__ __device__ constexpr uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return (saddr >> 4) | ((lbo_bytes >> 4) << 16);
+}
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far
 // has completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {

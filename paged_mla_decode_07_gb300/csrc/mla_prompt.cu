@@ -192,10 +192,6 @@ __device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const
 // descriptors for every four of them an MMA took 100 cycles to issue, where it
 // runs for 64): descriptors are their lower words, the upper word being constant,
 // and all MMAs of a tile are issued from one elected thread at a time.
-constexpr uint32_t kDescHi = static_cast<uint32_t>(smem_desc_hi(0, 1024) >> 32);
-__host__ __device__ constexpr uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
-  return (saddr >> 4) | ((lbo_bytes >> 4) << 16);
-}
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
