@@ -8,10 +8,14 @@
 // scale, which is a bf16 number.
 //
 // Memory-bound: a row of 400 to 1152 bytes read and 1152 bytes written per
-// token.  A warp takes kTokens consecutive tokens: it finds the request of the
-// first by a search 32 requests wide (three reads deep for 16384 requests) and
-// goes on from there, and issues the loads of all of them before the first
-// store.  Lane l holds dims 16 l .. 16 l + 15 and, up to lane 7, eight RoPE values.
+// token, behind four reads that depend on each other (the offsets, by a search 32
+// requests wide, the start, the page, the row): a warp has one token, or two of
+// long calls, in a grid that fills the chip several times over, so that the reads
+// of many tokens overlap.  Lane k of a warp finds the row of its token k; then lane
+// l holds dims 16 l .. 16 l + 15 and, up to lane 7, eight RoPE values.  110304
+// tokens of FP8 rows take 40.0 us (5.0 TB/s; a copy of as many bytes 40.1), 30001
+// of FP4 rows 17.5 (a launch alone 7.3); with four tokens a warp in a grid of eight
+// blocks an SM 41.1 and 21.7, one token there 42.0 and 21.6.
 #include "mla_device.cuh"
 #include "mla_fp4.cuh"
 #include "mla_internal.h"
@@ -50,31 +54,29 @@ __global__ void __launch_bounds__(kLoadWarps * 32) cache_load_kernel(const Cache
   const int total = min(__ldg(p.row_offsets + p.batch), p.num_tokens);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kLoadWarps * T;
   for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kLoadWarps + (threadIdx.x >> 5)) * T; t0 < total; t0 += step) {
+    // lane k finds the row of token k: its request, its page
     int b = request_of(p.row_offsets, p.batch, static_cast<int>(t0), lane);
-    const int first = __ldg(p.row_offsets + b);
-    int next = __ldg(p.row_offsets + b + 1);
-    int64_t pos = (p.starts ? __ldg(p.starts + b) : 0) + (t0 - first);
-    // rows and their places
-    int64_t row[T];
-#pragma unroll
-    for (int k = 0; k < T; ++k) {
-      row[k] = -1;
-      if (t0 + k >= total) continue;
-      while (t0 + k >= next && b + 1 < p.batch) {  // the next request with tokens
+    int64_t mine = -1;
+    const int64_t t = t0 + lane;
+    if (lane < T && t < total) {
+      int first = __ldg(p.row_offsets + b), next = __ldg(p.row_offsets + b + 1);
+      while (t >= next && b + 1 < p.batch) {
         ++b;
+        first = next;
         next = __ldg(p.row_offsets + b + 1);
-        pos = p.starts ? __ldg(p.starts + b) : 0;
       }
-      const int64_t page_at = pos / kPageSize;
+      const int64_t pos = (p.starts ? __ldg(p.starts + b) : 0) + (t - first), page_at = pos / kPageSize;
       int page = -1;
       if (pos >= 0 && page_at < p.block_table_stride)
         page = __ldg(p.block_table + static_cast<int64_t>(b) * p.block_table_stride + page_at);
       if (page >= 0 && page < p.num_pages)
-        row[k] = static_cast<int64_t>(page) * kPageSize + pos % kPageSize;
-      else if (lane == 0)
+        mine = static_cast<int64_t>(page) * kPageSize + pos % kPageSize;
+      else
         atomicOr(p.status, MLA_DEVICE_BAD_PAGE);
-      ++pos;
     }
+    int64_t row[T];
+#pragma unroll
+    for (int k = 0; k < T; ++k) row[k] = __shfl_sync(0xffffffffu, mine, k);
     const uint4 zero = make_uint4(0, 0, 0, 0);
     uint4 a[T], c[T], rope[T];
     float scale[T];
@@ -125,13 +127,13 @@ __global__ void __launch_bounds__(kLoadWarps * 32) cache_load_kernel(const Cache
 
 template <int FMT>
 cudaError_t launch(const CacheLoadParams& p, int sm_count, cudaStream_t stream) {
-  // one token per warp until every warp of a full grid has one
-  const int64_t most = 8ll * sm_count;
-  const bool four = p.num_tokens > most * kLoadWarps;
-  const int64_t per = kLoadWarps * (four ? 4 : 1), need = (p.num_tokens + per - 1) / per;
+  // one token per warp until every warp of the grid has one
+  const int64_t most = 64ll * sm_count;
+  const bool two = p.num_tokens > most * kLoadWarps;
+  const int64_t per = kLoadWarps * (two ? 2 : 1), need = (p.num_tokens + per - 1) / per;
   const unsigned grid = static_cast<unsigned>(need < most ? need : most);
-  if (four)
-    cache_load_kernel<FMT, 4><<<grid, kLoadWarps * 32, 0, stream>>>(p);
+  if (two)
+    cache_load_kernel<FMT, 2><<<grid, kLoadWarps * 32, 0, stream>>>(p);
   else
     cache_load_kernel<FMT, 1><<<grid, kLoadWarps * 32, 0, stream>>>(p);
   return cudaGetLastError();
