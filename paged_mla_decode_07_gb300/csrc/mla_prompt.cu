@@ -42,7 +42,7 @@ constexpr int kItemInts = 8;
 constexpr int kItemOff = kAuxOff;  // [2] items
 constexpr int kMiscOff = kItemOff + 2 * kItemInts * 4;
 constexpr int kBarOff = kMiscOff + 16;
-constexpr int kNumBars = 2 * kSlots + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2 + 2;
+constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2;
 constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr int kThreads = 384;
@@ -71,7 +71,7 @@ struct Bars {
   uint64_t* full;        // [kSlots] a chunk has landed
   uint64_t* empty;       // [kSlots] the products that read it are done
   uint64_t* q_full;      // [2] Q of a half has landed
-  uint64_t* q_empty;     // the products that read Q of an item are done
+  uint64_t* q_empty;     // [2] the products that read Q of a half are done
   uint64_t* s_full;      // [2] scores of a half are in tensor memory
   uint64_t* p_full;      // [2] P of a half is written
   uint64_t* pv_done;     // [2] the products of O of a half's tile are done
@@ -106,6 +106,14 @@ __device__ __forceinline__ bool get_item(int n, uint8_t* smem, const Bars& bars,
 // ---------------------------------------------------------------------------
 // loads, and the items (one thread)
 // ---------------------------------------------------------------------------
+// Brings a box into L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 struct Maps {
   const CUtensorMap *q, *k_nope, *k_rope, *v;
 };
@@ -114,7 +122,7 @@ __device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const
   const int group = p.h_q / p.h_kv;
   const int total = p.plan[kPromptBlocks] * p.h_q;  // (at most 2^31 by the host's check)
   uint32_t chunk = 0;  // chunks of keys and values so far
-  int n = 0, used = 0, loaded_q[2] = {0, 0};
+  int n = 0;
   auto fetch = [&]() {
     const int at = atomicAdd(p.plan + kPromptCounter, 1);
     if (at >= total) return Item{0, 0, 0, 0, 0, 0, 1};
@@ -138,19 +146,12 @@ __device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const
     mbar_arrive(bars.item_full + (n & 1));
     if (it.end) break;
     next = fetch();
+    if (!next.end)
+      for (int h = 0; h < 2; ++h)
+        if (next.tiles(h, p.causal) > 0)
+          for (int c = 0; c < kKChunks; ++c) tma_prefetch_3d(tm.q, 64 * c, next.head, next.q0 + kHalfRows * h);
     const int nt0 = it.tiles(0, p.causal), nt1 = it.tiles(1, p.causal), nt = max(nt0, nt1);
     if (nt == 0) continue;
-    if (used > 0 && !mbar_wait(bars.q_empty, (used - 1) & 1, wd)) break;
-    ++used;
-    auto load_q = [&](int h) {
-      mbar_arrive_expect_tx(bars.q_full + h, kKChunks * kChunkBytes);
-#pragma unroll
-      for (int c = 0; c < kKChunks; ++c)
-        tma_load_3d(smem + kQOff + (h * kKChunks + c) * kChunkBytes, tm.q, bars.q_full + h, 64 * c, it.head,
-                    it.q0 + kHalfRows * h, pol);
-      ++loaded_q[h];
-    };
-    if (nt0 > 0) load_q(0);
     bool ok = true;
     const int kv_head = it.head / group;
 #pragma unroll 1
@@ -173,15 +174,45 @@ __device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const
           const bool wraps = (chunk - (c - 3)) % kSlots == kSlots - 1;
           tma_load_3d(dst, tm.v, bars.full + slot, 64 * ((c - 3) ^ (wraps ? 1 : 0)), kv_head, row, pol);
         }
-        if (j == 0 && c == 2 && nt1 > 0) load_q(1);
       }
     }
     if (!ok) break;
   }
   // no copy may be in flight when the CTA ends
   for (uint32_t i = chunk > kSlots ? chunk - kSlots : 0; i < chunk; ++i) drain(bars.full + i % kSlots, (i / kSlots) & 1, wd);
-  for (int h = 0; h < 2; ++h)
-    if (loaded_q[h] > 0) drain(bars.q_full + h, (loaded_q[h] - 1) & 1, wd);
+}
+
+// Q of both halves (one warp): each as soon as the half's last products of the
+// item before are done, so that one half starts on an item while the other ends
+// the last one.
+__device__ void load_queries(const CUtensorMap* tm, const PromptParams& p, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
+  const uint64_t pol = l2_policy_evict_normal();
+  const int lane = threadIdx.x & 31;
+  int loads[2] = {0, 0};
+  bool ok = true;
+  Item it;
+#pragma unroll 1
+  for (int n = 0; ok && get_item(n, smem, bars, wd, it); ++n) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (it.tiles(h, p.causal) == 0) continue;
+      ok = ok && (loads[h] == 0 || wait_warp(bars.q_empty + h, (loads[h] - 1) & 1, wd));
+      if (!ok) break;
+      ++loads[h];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bars.q_full + h, kKChunks * kChunkBytes);
+#pragma unroll
+        for (int c = 0; c < kKChunks; ++c)
+          tma_load_3d(smem + kQOff + (h * kKChunks + c) * kChunkBytes, tm, bars.q_full + h, 64 * c, it.head,
+                      it.q0 + kHalfRows * h, pol);
+      }
+      __syncwarp();
+    }
+  }
+  if (lane == 0)
+    for (int h = 0; h < 2; ++h)
+      if (loads[h] > 0) drain(bars.q_full + h, (loads[h] - 1) & 1, wd);
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -251,11 +282,11 @@ __device__ void score_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
             }
           }
           umma_commit(bars.s_full + h);
+          if (j == (h ? nt1 : nt0) - 1) umma_commit(bars.q_empty + h);
           if (last_user) {
             umma_commit_u32(bars_empty + 8 * s0);
             umma_commit_u32(bars_empty + 8 * s1);
             umma_commit_u32(bars_empty + 8 * s2);
-            if (j == nt - 1) umma_commit(bars.q_empty);
           }
         }
         __syncwarp();
@@ -531,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bars.full = take(kSlots);
   bars.empty = take(kSlots);
   bars.q_full = take(2);
-  bars.q_empty = take(1);
+  bars.q_empty = take(2);
   bars.s_full = take(2);
   bars.p_full = take(2);
   bars.pv_done = take(2);
@@ -546,15 +577,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars.q_full + i, 1);
+      mbar_init(bars.q_empty + i, 1);
       mbar_init(bars.s_full + i, 1);
       mbar_init(bars.p_full + i, 4);
       mbar_init(bars.pv_done + i, 1);
       mbar_init(bars.drained + i, 1);
       mbar_init(bars.o_free + i, 4);
       mbar_init(bars.item_full + i, 1);
-      mbar_init(bars.item_empty + i, 10);  // eight softmax warps and two of products
+      mbar_init(bars.item_empty + i, 11);  // eight softmax warps, two of products, the one that loads Q
     }
-    mbar_init(bars.q_empty, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
@@ -579,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((threadIdx.x & 31) == 0) load(Maps{&tm_q, &tm_k_nope, &tm_k_rope, &tm_v}, p, smem, bars, wd);
       __syncwarp();
     }
+    if (warp == 2) load_queries(&tm_q, p, smem, bars, wd);
     if (warp == 1) score_products(p, tmem, smem, bars, wd);
     if (warp == 3) value_products(p, tmem, smem, bars, wd);
     __syncthreads();
