@@ -382,7 +382,9 @@ mla_status mla_fp4_decode(const mla_fp4_decode_args* args, mla_stream_t stream);
  * bf16, sums are fp32, lse is base 2 as in mla_decode.
  * All row and head strides are in elements and multiples of 8, so q, keys and
  * values may be slices (of one up-projection, of cache rows).  Offsets that
- * decrease, or leave the rows, are cut off or set MLA_DEVICE_BAD_SCHEDULE.
+ * leave the rows are cut off there; results of offsets that decrease are
+ * invalid, and set MLA_DEVICE_BAD_SCHEDULE where they name more blocks of 256
+ * query rows than num_q / 256 + batch.
  * All launches are made on `stream` by the one call. */
 typedef struct {
   const void* q;                  /* bf16 [num_q, h_q, 192], 16-byte aligned (as k_nope, k_rope and v) */

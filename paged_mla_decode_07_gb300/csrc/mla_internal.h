@@ -264,6 +264,7 @@ struct PromptParams {
   uint64_t timeout_ns;
   int batch, num_q, num_k, h_q, h_kv;
   int max_blocks;            // blocks that the list has room for: as many as non-decreasing offsets can name
+  int planned;               // 1: items by the plan; 0: item i is CTA i's
   int causal, debug_stall;
   float scale_log2;
 };

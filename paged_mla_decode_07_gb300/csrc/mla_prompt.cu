@@ -23,7 +23,8 @@
 //
 // Persistent: the plan kernel sorts the blocks of 256 rows of all sequences by
 // their number of key tiles, the CTAs take items from that list, longest first,
-// by a counter.  Every wait is bounded (watchdog).
+// by a counter.  Calls with no more items than SMs have no plan: each CTA finds its
+// one item itself.  Every wait is bounded (watchdog).
 #include "mla_device.cuh"
 #include "mla_internal.h"
 
@@ -117,20 +118,61 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, 
 struct Maps {
   const CUtensorMap *q, *k_nope, *k_rope, *v;
 };
-__device__ void load(const Maps& tm, const PromptParams& p, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
+// Sequence b: its rows within those of q, its keys within those of k.
+struct Sequence {
+  int q0, n, k0, m;
+  __device__ __forceinline__ Sequence(const PromptParams& p, int b) {
+    auto clamp = [](int v, int most) { return min(max(v, 0), most); };
+    q0 = clamp(p.q_offsets[b], p.num_q);
+    n = max(clamp(p.q_offsets[b + 1], p.num_q) - q0, 0);
+    k0 = clamp(p.k_offsets[b], p.num_k);
+    m = max(clamp(p.k_offsets[b + 1], p.num_k) - k0, 0);
+  }
+  __device__ __forceinline__ int blocks() const { return (n + kBlock - 1) / kBlock; }
+};
+
+// Block `at` of all sequences' (one warp), for calls without a plan.  The last
+// CTA counts them all: offsets that decrease may name more than the call has CTAs for.
+__device__ __forceinline__ Item find_block(const PromptParams& p, int at) {
+  const int lane = threadIdx.x & 31;
+  const bool count = blockIdx.x == gridDim.x - 1;
+  int before = 0;  // blocks of the sequences up to b0
+  Item it{0, 0, 0, 0, 0, 0, 1};
+  for (int b0 = 0; b0 < p.batch && (it.end || count); b0 += 32) {
+    const int b = b0 + lane, n = b < p.batch ? Sequence(p, b).blocks() : 0;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const uint32_t has = __ballot_sync(0xffffffffu, before + sum > at);
+    if (has && it.end) {
+      const int k = __ffs(has) - 1;
+      const Sequence s(p, b0 + k);
+      const int row = (at - before - __shfl_sync(0xffffffffu, sum - n, k)) * kBlock;
+      it = Item{s.q0 + row, min(kBlock, s.n - row), s.k0, s.m, s.m - s.n + row + 1, 0, 0};
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (count && lane == 0 && before > p.max_blocks) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
+  return it;
+}
+
+__device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
   const uint64_t pol = l2_policy_evict_normal();
   const int group = p.h_q / p.h_kv;
-  const int total = p.plan[kPromptBlocks] * p.h_q;  // (at most 2^31 by the host's check)
+  const int total = p.planned ? p.plan[kPromptBlocks] * p.h_q : 0;  // (below 2^31 by the host's check)
   uint32_t chunk = 0;  // chunks of keys and values so far
   int n = 0;
   auto fetch = [&]() {
-    const int at = atomicAdd(p.plan + kPromptCounter, 1);
+    const int at = p.planned ? atomicAdd(p.plan + kPromptCounter, 1) : 0;
     if (at >= total) return Item{0, 0, 0, 0, 0, 0, 1};
     const int4* e = reinterpret_cast<const int4*>(p.plan + kPromptList) + 2 * (at / p.h_q);
     const int4 a = e[0], b = e[1];
     return Item{a.x, a.y, a.z, a.w, b.x, at % p.h_q, 0};
   };
-  Item next = fetch();
+  Item next = p.planned ? fetch() : own;
 #pragma unroll 1
   for (;; ++n) {
     const Item it = next;  // (the next one is on its way while this one's tiles are loaded)
@@ -607,7 +649,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     regs_to<kRegsCtl, kLaunchRegs>();
     if (warp == 0) {
-      if ((threadIdx.x & 31) == 0) load(Maps{&tm_q, &tm_k_nope, &tm_k_rope, &tm_v}, p, smem, bars, wd);
+      Item own{0, 0, 0, 0, 0, 0, 1};
+      if (!p.planned) {
+        own = find_block(p, blockIdx.x / p.h_q);
+        own.head = blockIdx.x % p.h_q;
+      }
+      if ((threadIdx.x & 31) == 0) load(Maps{&tm_q, &tm_k_nope, &tm_k_rope, &tm_v}, p, own, smem, bars, wd);
       __syncwarp();
     }
     if (warp == 2) load_queries(&tm_q, p, smem, bars, wd);
@@ -638,16 +685,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // sequence b: its rows within the rows of q, its keys within those of k
-  auto clamp_to = [](int v, int most) { return min(max(v, 0), most); };
-  auto q_begin = [&](int b) { return clamp_to(p.q_offsets[b], p.num_q); };
-  auto k_begin = [&](int b) { return clamp_to(p.k_offsets[b], p.num_k); };
-  auto blocks_of = [&](int b) { return (max(q_begin(b + 1) - q_begin(b), 0) + kBlock - 1) / kBlock; };
   const int per = (p.batch + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
   int mine = 0;
   for (int b = b0; b < b1; ++b) {
     first[b] = mine;
-    mine += blocks_of(b);
+    mine += Sequence(p, b).blocks();
   }
   int x = mine;
 #pragma unroll
@@ -689,11 +731,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
       else
         hi = mid - 1;
     }
-    const int q0 = q_begin(lo), n = q_begin(lo + 1) - q0, k0 = k_begin(lo), m = max(k_begin(lo + 1) - k0, 0);
-    const int at = (i - first[lo]) * kBlock, rows = min(kBlock, n - at);
-    a = make_int4(q0 + at, rows, k0, m);
-    see = m - n + at + 1;
-    const int keys = p.causal ? min(m, see + rows - 1) : m;
+    const Sequence s(p, lo);
+    const int at = (i - first[lo]) * kBlock, rows = min(kBlock, s.n - at);
+    a = make_int4(s.q0 + at, rows, s.k0, s.m);
+    see = s.m - s.n + at + 1;
+    const int keys = p.causal ? min(s.m, see + rows - 1) : s.m;
     return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
   };
   int longest = 0;
@@ -751,7 +793,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
 }  // namespace
 
 cudaError_t launch_prompt(const CUtensorMap& tm_q, const CUtensorMap& tm_k_nope, const CUtensorMap& tm_k_rope,
-                          const CUtensorMap& tm_v, const PromptParams& p, int sm_count, cudaStream_t stream) {
+                          const CUtensorMap& tm_v, const PromptParams& params, int sm_count, cudaStream_t stream) {
+  PromptParams p = params;
+  const int64_t items = static_cast<int64_t>(p.max_blocks) * p.h_q;
+  p.planned = items > sm_count;
   const size_t scratch = (static_cast<size_t>(p.batch) + 1) * sizeof(int);
   cudaError_t e = allow_dynamic_smem(plan_kernel, scratch, 8192);
   if (e != cudaSuccess) return e;
@@ -762,18 +807,19 @@ cudaError_t launch_prompt(const CUtensorMap& tm_q, const CUtensorMap& tm_k_nope,
   if (e != cudaSuccess) return e;
   if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = scratch;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, plan_kernel, p);
-  if (e != cudaSuccess) return e;
-  const int64_t items = static_cast<int64_t>(p.max_blocks) * p.h_q;
+  if (p.planned) {
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = scratch;
+    e = cudaLaunchKernelEx(&cfg, plan_kernel, p);
+    if (e != cudaSuccess) return e;
+  }
   cfg.gridDim = dim3(static_cast<unsigned>(items < sm_count ? items : sm_count));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
