@@ -384,7 +384,7 @@ mla_status mla_fp4_decode(const mla_fp4_decode_args* args, mla_stream_t stream);
  * values may be slices (of one up-projection, of cache rows).  Offsets that
  * leave the rows are cut off there; results of offsets that decrease are
  * invalid, and set MLA_DEVICE_BAD_SCHEDULE where they name more blocks of 256
- * query rows than num_q / 256 + batch.
+ * query rows than others could.
  * All launches are made on `stream` by the one call. */
 typedef struct {
   const void* q;                  /* bf16 [num_q, h_q, 192], 16-byte aligned (as k_nope, k_rope and v) */
@@ -408,7 +408,7 @@ typedef struct {
   float* lse;                     /* fp32 [num_q, h_q], base 2 */
 } mla_prompt_attention_args;
 
-mla_status mla_prompt_attention_workspace_size(int num_q, int batch, size_t* bytes);
+mla_status mla_prompt_attention_workspace_size(int num_q, int num_k, int h_q, int batch, size_t* bytes);
 mla_status mla_prompt_attention(const mla_prompt_attention_args* args, mla_stream_t stream);
 
 /* Sparse prefill ("flash_mla_sparse_fwd(q, kv, indices, sm_scale)" of the

@@ -262,7 +262,7 @@ def lib():
             L.mla_fp4_decode_workspace_size.restype = I
             L.mla_fp4_decode.argtypes = [ctypes.POINTER(Fp4DecodeArgs), P]
             L.mla_fp4_decode.restype = I
-            L.mla_prompt_attention_workspace_size.argtypes = [I, I, ctypes.POINTER(S)]
+            L.mla_prompt_attention_workspace_size.argtypes = [I, I, I, I, ctypes.POINTER(S)]
             L.mla_prompt_attention_workspace_size.restype = I
             L.mla_prompt_attention.argtypes = [ctypes.POINTER(PromptAttentionArgs), P]
             L.mla_prompt_attention.restype = I
@@ -754,10 +754,10 @@ def sparse_prefill(q: torch.Tensor, kv: torch.Tensor, indices: torch.Tensor, sm_
     return out.view(s_q, h_q, D_V), lse.view(s_q, h_q)
 
 
-def prompt_attention_workspace_size(num_q: int, batch: int) -> int:
+def prompt_attention_workspace_size(num_q: int, num_k: int, h_q: int, batch: int) -> int:
     """Scratch bytes of prompt_attention."""
     n = ctypes.c_size_t()
-    _check(lib().mla_prompt_attention_workspace_size(num_q, batch, ctypes.byref(n)))
+    _check(lib().mla_prompt_attention_workspace_size(num_q, num_k, h_q, batch, ctypes.byref(n)))
     return n.value
 
 
@@ -813,7 +813,7 @@ def prompt_attention(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor
     def call(handle):
         o = torch.empty((num_q, h_q, 128), dtype=torch.bfloat16, device=dev) if out is None else out
         z = torch.empty((num_q, h_q), dtype=torch.float32, device=dev) if lse is None else lse
-        ws = _scratch(workspace, prompt_attention_workspace_size(num_q, batch) if workspace is None else 0, dev)
+        ws = _scratch(workspace, prompt_attention_workspace_size(num_q, num_k, h_q, batch) if workspace is None else 0, dev)
         a = PromptAttentionArgs(q.data_ptr(), q.stride(0), q.stride(1), num_q, h_q, k_nope.data_ptr(), k_nope.stride(0),
                                 k_nope.stride(1), k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1),
                                 num_k, h_kv, q_offsets.data_ptr(), k_offsets.data_ptr(), batch, float(sm_scale),

@@ -436,7 +436,8 @@ PyObject* prompt_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     at::Tensor out = c.output(8, at::kBFloat16, out_shape), lse = c.output(9, at::kFloat, lse_shape);
     at::Tensor ws = c.workspace(10);
     size_t bytes = 0;
-    if (!c.ok || mla_prompt_attention_workspace_size(static_cast<int>(rows), static_cast<int>(qo->size(0) - 1), &bytes) != MLA_OK)
+    if (!c.ok || mla_prompt_attention_workspace_size(static_cast<int>(rows), static_cast<int>(k->size(0)), static_cast<int>(heads),
+                                                     static_cast<int>(qo->size(0) - 1), &bytes) != MLA_OK)
       return nullptr;
     a.q = ptr(*q);
     a.q_stride = q->stride(0);

@@ -498,6 +498,48 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
   return MLA_OK;
 }
 
+// Attention over packed prompts: blocks of 256 query rows (as many as
+// non-decreasing offsets can name), one item for each of their heads.  Calls with
+// more items than SMs take them from a plan.  In others an item's key tiles are
+// shared out over as many CTAs as there are SMs for it, up to 16, while each has 512
+// keys of an average sequence (the lengths are on the device): a run less than that
+// is worth its merge.  Measured (us, one run / shared out): 1 sequence x 16 heads, 512
+// queries behind 8192 keys 138 / 69, behind 32768 491 / 188, 1 query behind 8192 120
+// / 36; 200 queries of one head 138 / 28; but 256 behind 256 keys, 2 sequences x 16
+// heads, 21.6 / 27.8.
+struct PromptLayout {
+  int blocks, planned, splits;
+  size_t o_part, lse_part, total;  // (the list comes first)
+};
+mla_status prompt_layout(int num_q, int num_k, int h_q, int batch, PromptLayout* L) {
+  if (num_q < 0) return fail(MLA_ERR_INVALID_ARG, "num_q must be >= 0 (got %d)", num_q);
+  if (num_k < 0) return fail(MLA_ERR_INVALID_ARG, "num_k must be >= 0 (got %d)", num_k);
+  if (h_q < 1) return fail(MLA_ERR_INVALID_ARG, "h_q must be >= 1 (got %d)", h_q);
+  if (h_q > 1024) return fail(MLA_ERR_UNSUPPORTED, "h_q = %d exceeds 1024", h_q);
+  if (batch < 1) return fail(MLA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
+  if (batch > kMaxProblems)
+    return fail(MLA_ERR_UNSUPPORTED, "batch = %d exceeds the supported %d sequences", batch, kMaxProblems);
+  const long long some = std::min(batch, num_q);  // sequences with rows
+  const long long blocks = (num_q - some) / kPromptBlock + some, items = blocks * h_q;
+  if (items >= (1ll << 31) - 4096)
+    return fail(MLA_ERR_UNSUPPORTED, "num_q = %d rows of %d heads in %d sequences", num_q, h_q, batch);
+  int sms = 0;
+  mla_status st = device_info(nullptr, &sms);
+  if (st != MLA_OK) return st;
+  L->blocks = static_cast<int>(blocks);
+  L->planned = items > sms ? 1 : 0;
+  L->splits = 1;
+  if (!L->planned && items > 0)
+    L->splits = static_cast<int>(std::max(1ll, std::min(std::min<long long>(sms / items, 16), num_k / batch / 512ll)));
+  size_t at = align256(4 * (kPromptList + static_cast<size_t>(blocks) * kPromptEntryInts));
+  if (L->splits > 1) at = std::max(at, align256(static_cast<size_t>(items) * 16));
+  const size_t runs = L->splits > 1 ? static_cast<size_t>(items) * L->splits : 0;
+  L->o_part = at;
+  L->lse_part = L->o_part + runs * kPromptBlock * 128 * sizeof(float);
+  L->total = L->lse_part + align256(runs * kPromptBlock * sizeof(float));
+  return MLA_OK;
+}
+
 // Checks that every dense decode call over a paged cache shares.
 mla_status check_paged(int batch, const void* q, const void* kvcache, const int32_t* block_table, const int32_t* cache_seqlens,
                        const void* out, const float* lse, int num_pages, int page_size, int stride, float sm_scale,
@@ -1229,26 +1271,19 @@ mla_status mla_fp4_decode(const mla_fp4_decode_args* a, mla_stream_t stream) {
   return ok();
 }
 
-mla_status mla_prompt_attention_workspace_size(int num_q, int batch, size_t* bytes) {
+mla_status mla_prompt_attention_workspace_size(int num_q, int num_k, int h_q, int batch, size_t* bytes) {
   if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes is NULL");
-  if (num_q < 0) return fail(MLA_ERR_INVALID_ARG, "num_q must be >= 0 (got %d)", num_q);
-  if (batch < 1) return fail(MLA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
-  if (batch > kMaxProblems)
-    return fail(MLA_ERR_UNSUPPORTED, "batch = %d exceeds the supported %d sequences", batch, kMaxProblems);
-  *bytes = align256(4 * (kPromptList + static_cast<size_t>(num_q / kPromptBlock + batch) * kPromptEntryInts));
+  PromptLayout L;
+  mla_status st = prompt_layout(num_q, num_k, h_q, batch, &L);
+  if (st != MLA_OK) return st;
+  *bytes = L.total;
   return ok();
 }
 
 mla_status mla_prompt_attention(const mla_prompt_attention_args* a, mla_stream_t stream) {
   if (!a) return fail(MLA_ERR_INVALID_ARG, "args is NULL");
-  size_t need = 0;
-  mla_status st = mla_prompt_attention_workspace_size(a->num_q, a->batch, &need);
-  if (st != MLA_OK) return st;
-  if (a->num_k < 0) return fail(MLA_ERR_INVALID_ARG, "num_k must be >= 0 (got %d)", a->num_k);
-  if (a->h_q < 1) return fail(MLA_ERR_INVALID_ARG, "h_q must be >= 1 (got %d)", a->h_q);
   if (a->h_kv < 1 || a->h_q % a->h_kv != 0)
     return fail(MLA_ERR_INVALID_ARG, "h_q = %d must be a multiple of h_kv = %d", a->h_q, a->h_kv);
-  if (a->h_q > 1024) return fail(MLA_ERR_UNSUPPORTED, "h_q = %d exceeds 1024", a->h_q);
   if (!std::isfinite(a->sm_scale)) return fail(MLA_ERR_INVALID_ARG, "sm_scale is not finite");
   struct Arr {
     const void* p;
@@ -1276,11 +1311,11 @@ mla_status mla_prompt_attention(const mla_prompt_attention_args* a, mla_stream_t
     if (x.used && (x.v < 8 || x.v % 8 != 0 || x.v >= (1ll << 38)))
       return fail(MLA_ERR_INVALID_ARG, "%s must be a positive multiple of 8 elements (got %lld)", x.name,
                   static_cast<long long>(x.v));
-  const long long blocks = a->num_q / kPromptBlock + static_cast<long long>(a->batch);
-  if (blocks * a->h_q >= (1ll << 31) - 4096)
-    return fail(MLA_ERR_UNSUPPORTED, "num_q = %d rows of %d heads in %d sequences", a->num_q, a->h_q, a->batch);
+  PromptLayout L;
+  mla_status st = prompt_layout(a->num_q, a->num_k, a->h_q, a->batch, &L);
+  if (st != MLA_OK) return st;
   if (!rows) return ok();
-  st = check_workspace(a->workspace, a->workspace_bytes, need);
+  st = check_workspace(a->workspace, a->workspace_bytes, L.total);
   if (st != MLA_OK) return st;
   PromptParams p;
   memset(&p, 0, sizeof p);
@@ -1310,7 +1345,11 @@ mla_status mla_prompt_attention(const mla_prompt_attention_args* a, mla_stream_t
   p.num_k = a->num_k;
   p.h_q = a->h_q;
   p.h_kv = a->h_kv;
-  p.max_blocks = static_cast<int>(blocks);
+  p.max_blocks = L.blocks;
+  p.planned = L.planned;
+  p.splits = L.splits;
+  p.o_part = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + L.o_part);
+  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + L.lse_part);
   p.causal = a->is_causal ? 1 : 0;
   p.debug_stall = g_test_debug_stall.load();
   p.scale_log2 = a->sm_scale * 1.4426950408889634f;

@@ -251,7 +251,8 @@ struct CacheLoadParams {
 };
 
 // Attention over packed prompts.  The workspace: a counter, the number of blocks,
-// and the list of blocks (8 ints each, 6 of them used).
+// and the list of blocks (8 ints each, 5 of them used); without a plan and with
+// splits, the items (4 ints each) and the partial results.
 constexpr int kPromptBlock = 256;  // query rows of a block
 constexpr int kPromptCounter = 0, kPromptBlocks = 1, kPromptList = 64, kPromptEntryInts = 8;
 struct PromptParams {
@@ -264,7 +265,10 @@ struct PromptParams {
   uint64_t timeout_ns;
   int batch, num_q, num_k, h_q, h_kv;
   int max_blocks;            // blocks that the list has room for: as many as non-decreasing offsets can name
-  int planned;               // 1: items by the plan; 0: item i is CTA i's
+  int planned;               // 1: items by the plan; 0: item i belongs to CTAs i * splits ..
+  int splits;                // CTAs that share an item's key tiles (1 with a plan)
+  float* o_part;             // their results, [items * splits][256 rows][128]
+  float* lse_part;           // [items * splits][256 rows]
   int causal, debug_stall;
   float scale_log2;
 };

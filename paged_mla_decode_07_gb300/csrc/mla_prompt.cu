@@ -24,7 +24,9 @@
 // Persistent: the plan kernel sorts the blocks of 256 rows of all sequences by
 // their number of key tiles, the CTAs take items from that list, longest first,
 // by a counter.  Calls with no more items than SMs have no plan: each CTA finds its
-// one item itself.  Every wait is bounded (watchdog).
+// one item itself, or where there are several SMs for an item a run of its key
+// tiles, and the merge kernel joins the runs' results.  Every wait is bounded
+// (watchdog).
 #include "mla_device.cuh"
 #include "mla_internal.h"
 
@@ -39,7 +41,7 @@ constexpr int kSlots = 8, kKChunks = 3, kVChunks = 2, kTileChunks = kKChunks + k
 constexpr int kQOff = 0;
 constexpr int kRingOff = 2 * kKChunks * kChunkBytes;
 constexpr int kAuxOff = kRingOff + kSlots * kChunkBytes;
-constexpr int kItemInts = 8;
+constexpr int kItemInts = 10;
 constexpr int kItemOff = kAuxOff;  // [2] items
 constexpr int kMiscOff = kItemOff + 2 * kItemInts * 4;
 constexpr int kBarOff = kMiscOff + 16;
@@ -57,6 +59,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 
 struct Item {
   int q0, rows, k0, m, see, head, end;  // see: keys that row 0 sees (causal); end: no more items
+  int j0 = 0, j1 = 1 << 30;             // key tiles of this run of the item
   // keys that row r sees
   __device__ __forceinline__ int sees(int r, bool causal) const { return causal ? min(m, see + r) : m; }
   // key tiles of half h
@@ -66,6 +69,8 @@ struct Item {
     const int keys = sees(kHalfRows * h + n - 1, causal);
     return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
   }
+  // end of this run's tiles of half h: it has some if that is past j0
+  __device__ __forceinline__ int stop(int h, bool causal) const { return min(tiles(h, causal), j1); }
 };
 
 struct Bars {
@@ -99,7 +104,7 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, const Watc
 __device__ __forceinline__ bool get_item(int n, uint8_t* smem, const Bars& bars, const Watchdog& wd, Item& it) {
   if (!wait_warp(bars.item_full + (n & 1), (n >> 1) & 1, wd)) return false;
   const volatile int* v = reinterpret_cast<const volatile int*>(smem + kItemOff) + (n & 1) * kItemInts;
-  it = Item{v[0], v[1], v[2], v[3], v[4], v[5], v[6]};
+  it = Item{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8]};
   arrive_warp(bars.item_empty + (n & 1));
   return !it.end;
 }
@@ -185,6 +190,8 @@ __device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uin
     v[4] = it.see;
     v[5] = it.head;
     v[6] = it.end;
+    v[7] = it.j0;
+    v[8] = it.j1;
     mbar_arrive(bars.item_full + (n & 1));
     if (it.end) break;
     next = fetch();
@@ -192,12 +199,11 @@ __device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uin
       for (int h = 0; h < 2; ++h)
         if (next.tiles(h, p.causal) > 0)
           for (int c = 0; c < kKChunks; ++c) tma_prefetch_3d(tm.q, 64 * c, next.head, next.q0 + kHalfRows * h);
-    const int nt0 = it.tiles(0, p.causal), nt1 = it.tiles(1, p.causal), nt = max(nt0, nt1);
-    if (nt == 0) continue;
+    const int nt = max(it.stop(0, p.causal), it.stop(1, p.causal));
     bool ok = true;
     const int kv_head = it.head / group;
 #pragma unroll 1
-    for (int j = 0; j < nt && ok; ++j) {
+    for (int j = it.j0; j < nt && ok; ++j) {
 #pragma unroll 1
       for (int c = 0; c < kTileChunks; ++c, ++chunk) {
         const int slot = chunk % kSlots;
@@ -237,7 +243,7 @@ __device__ void load_queries(const CUtensorMap* tm, const PromptParams& p, uint8
   for (int n = 0; ok && get_item(n, smem, bars, wd, it); ++n) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (it.tiles(h, p.causal) == 0) continue;
+      if (it.stop(h, p.causal) <= it.j0) continue;
       ok = ok && (loads[h] == 0 || wait_warp(bars.q_empty + h, (loads[h] - 1) & 1, wd));
       if (!ok) break;
       ++loads[h];
@@ -293,14 +299,14 @@ __device__ void score_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
   Item it;
 #pragma unroll 1
   for (int n = 0; ok && get_item(n, smem, bars, wd, it); ++n) {
-    const int nt0 = it.tiles(0, p.causal), nt1 = it.tiles(1, p.causal), nt = max(nt0, nt1);
+    const int nt0 = it.stop(0, p.causal), nt1 = it.stop(1, p.causal), nt = max(nt0, nt1);
 #pragma unroll 1
-    for (int j = 0; j < nt && ok; ++j, chunk += kTileChunks) {
+    for (int j = it.j0; j < nt && ok; ++j, chunk += kTileChunks) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (j >= (h ? nt1 : nt0)) continue;
         const bool last_user = h == 1 || j >= nt1;
-        if (j == 0) ok = ok && wait_warp(bars.q_full + h, items[h]++ & 1, wd);
+        if (j == it.j0) ok = ok && wait_warp(bars.q_full + h, items[h]++ & 1, wd);
         if (h == 0 || j >= nt0) {
 #pragma unroll
           for (int c = 0; c < kKChunks; ++c)
@@ -350,10 +356,10 @@ __device__ void value_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
   Item it;
 #pragma unroll 1
   for (int n = 0; ok && get_item(n, smem, bars, wd, it); ++n) {
-    const int nt0 = it.tiles(0, p.causal), nt1 = it.tiles(1, p.causal), nt = max(nt0, nt1);
+    const int nt0 = it.stop(0, p.causal), nt1 = it.stop(1, p.causal), nt = max(nt0, nt1);
     const int keys = it.sees(it.rows - 1, p.causal);
 #pragma unroll 1
-    for (int j = 0; j < nt && ok; ++j, chunk += kTileChunks) {
+    for (int j = it.j0; j < nt && ok; ++j, chunk += kTileChunks) {
       const uint32_t s0 = chunk % kSlots, s1 = (chunk + 1) % kSlots;
       const uint32_t first = min(s0, s1), gap = max(s0, s1) - first;
       const uint32_t b = desc_lo(base + kRingOff + first * kChunkBytes, gap * kChunkBytes);
@@ -362,7 +368,7 @@ __device__ void value_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
       for (int h = 0; h < 2; ++h) {
         if (j >= (h ? nt1 : nt0)) continue;
         const bool last_user = h == 1 || j >= nt1;
-        if (j == 0) {
+        if (j == it.j0) {
           ok = ok && (items[h] == 0 || wait_warp(bars.o_free + h, (items[h] - 1) & 1, wd));
           ++items[h];
         }
@@ -375,7 +381,7 @@ __device__ void value_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               if (k < steps)
-                umma_ts(tmem + kOCol + 128 * h, tmem + kSCol + 128 * h + 8 * k, b + ((k * 16 * 128) >> 4), kIdO, j > 0 || k > 0);
+                umma_ts(tmem + kOCol + 128 * h, tmem + kSCol + 128 * h + 8 * k, b + ((k * 16 * 128) >> 4), kIdO, j > it.j0 || k > 0);
           }
           umma_commit(bars.pv_done + h);
           if (last_user) {
@@ -438,12 +444,13 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
   Item it;
 #pragma unroll 1
   for (int n = 0; get_item(n, smem, bars, wd, it); ++n) {
-    const int tiles = it.tiles(half, p.causal), all_tiles = max(it.tiles(0, p.causal), it.tiles(1, p.causal));
+    const int stop = it.stop(half, p.causal), all_tiles = max(it.tiles(0, p.causal), it.tiles(1, p.causal));
+    const bool some = stop > it.j0;
     const int sees = it.sees(r, p.causal), keys = it.sees(it.rows - 1, p.causal);
     float ref = kNegInf, l = 0.f;
     if (p.debug_stall) return;  // watchdog test: the scores are never taken
 #pragma unroll 1
-    for (int j = 0; j < tiles; ++j, ++n_s) {
+    for (int j = it.j0; j < stop; ++j, ++n_s) {
       if (!wait_warp(bars.s_full + half, n_s & 1, wd)) return;
       tc_fence_after();
       float x[kKeys];
@@ -486,7 +493,7 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
           ref = top;
           l *= alpha;
         }
-        if (j > 0) {
+        if (j > it.j0) {
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             float o[16];
@@ -522,7 +529,7 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
         // Rows of V behind the last key that the products read (up to a multiple of 16)
         // belong to other sequences, or to no one: zeros, so that no NaN of theirs
         // meets a weight of 0.  Each half writes them.
-        const uint32_t i = (tile0 + j) * kTileChunks + kKChunks;
+        const uint32_t i = (tile0 + j - it.j0) * kTileChunks + kKChunks;
         const int first = keys - j * kKeys, row = first + (threadIdx.x & 127) / 8, unit = threadIdx.x & 7;
         bool ok = true;
 #pragma unroll
@@ -541,12 +548,12 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
       tc_fence_before();
       arrive_warp(bars.p_full + half);
     }
-    tile0 += all_tiles;
+    tile0 += max(max(it.stop(0, p.causal), it.stop(1, p.causal)) - it.j0, 0);
 
     const bool real = r < it.rows;
     const int64_t row = static_cast<int64_t>(it.q0 + r) * p.h_q + it.head;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * kHeadV;
-    if (tiles > 0) {
+    if (some) {
       if (!wait_warp(bars.pv_done + half, (n_s - 1) & 1, wd)) return;
       tc_fence_after();
     }
@@ -554,7 +561,7 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       float o[32];
-      if (tiles > 0) {
+      if (some) {
         tmem_ld_x32(o_at + 32 * c, o);
         tmem_ld_wait();
         if (c == 3) {
@@ -565,7 +572,14 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = 0.f;
       }
-      if (real) {
+      if (p.splits > 1) {
+        if (real && some) {
+          float4* to = reinterpret_cast<float4*>(p.o_part + (static_cast<int64_t>(blockIdx.x) * kBlock + r) * kHeadV + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            to[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+        }
+      } else if (real) {
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -580,7 +594,12 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
         }
       }
     }
-    if (real) p.lse[row] = l == 0.f ? kNegInf : ref + log2f(l);
+    const float z = l == 0.f ? kNegInf : ref + log2f(l);
+    if (p.splits > 1) {
+      p.lse_part[static_cast<int64_t>(blockIdx.x) * kBlock + r] = z;
+    } else if (real) {
+      p.lse[row] = z;
+    }
   }
 }
 
@@ -651,8 +670,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       Item own{0, 0, 0, 0, 0, 0, 1};
       if (!p.planned) {
-        own = find_block(p, blockIdx.x / p.h_q);
-        own.head = blockIdx.x % p.h_q;
+        const int item = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+        own = find_block(p, item / p.h_q);
+        own.head = item % p.h_q;
+        if (p.splits > 1) {
+          const int nt = max(own.tiles(0, p.causal), own.tiles(1, p.causal));
+          own.j0 = nt * split / p.splits;
+          own.j1 = nt * (split + 1) / p.splits;
+          // for the merge (an item without a block: no rows)
+          if (split == 0 && (threadIdx.x & 31) == 0)
+            reinterpret_cast<int4*>(p.plan)[item] = make_int4(own.q0, own.rows, own.head, 0);
+        }
       }
       if ((threadIdx.x & 31) == 0) load(Maps{&tm_q, &tm_k_nope, &tm_k_rope, &tm_v}, p, own, smem, bars, wd);
       __syncwarp();
@@ -669,6 +697,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
   }
+}
+
+// Joins the runs of an item's rows: a warp per row, four dims per lane.
+constexpr int kMergeWarps = 8, kMaxSplits = 16;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) prompt_merge_kernel(const PromptParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, r = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int4 item = reinterpret_cast<const int4*>(p.plan)[blockIdx.y];
+  if (r >= item.y) return;
+  const int64_t part = static_cast<int64_t>(blockIdx.y) * p.splits * kBlock + r;
+  float z[kMaxSplits], top = kNegInf;
+#pragma unroll
+  for (int k = 0; k < kMaxSplits; ++k) {
+    z[k] = k < p.splits ? p.lse_part[part + k * kBlock] : kNegInf;
+    top = max_nan(top, z[k]);
+  }
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = kNegInf;
+  if (top != kNegInf) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) sum += exp2f(z[k] - top);
+    total = top + log2f(sum);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) {
+      if (z[k] == kNegInf) continue;  // (no values are there)
+      const float4 v = reinterpret_cast<const float4*>(p.o_part + (part + k * kBlock) * kHeadV)[lane];
+      const float w = exp2f(z[k] - total);
+      o.x += w * v.x;
+      o.y += w * v.y;
+      o.z += w * v.z;
+      o.w += w * v.w;
+    }
+  }
+  const int64_t row = static_cast<int64_t>(item.x + r) * p.h_q + item.z;
+  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kHeadV)[lane] =
+      make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  if (lane == 0) p.lse[row] = total;
 }
 
 // ---------------------------------------------------------------------------
@@ -793,10 +861,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
 }  // namespace
 
 cudaError_t launch_prompt(const CUtensorMap& tm_q, const CUtensorMap& tm_k_nope, const CUtensorMap& tm_k_rope,
-                          const CUtensorMap& tm_v, const PromptParams& params, int sm_count, cudaStream_t stream) {
-  PromptParams p = params;
+                          const CUtensorMap& tm_v, const PromptParams& p, int sm_count, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(p.max_blocks) * p.h_q;
-  p.planned = items > sm_count;
   const size_t scratch = (static_cast<size_t>(p.batch) + 1) * sizeof(int);
   cudaError_t e = allow_dynamic_smem(plan_kernel, scratch, 8192);
   if (e != cudaSuccess) return e;
@@ -820,10 +886,15 @@ cudaError_t launch_prompt(const CUtensorMap& tm_q, const CUtensorMap& tm_k_nope,
     e = cudaLaunchKernelEx(&cfg, plan_kernel, p);
     if (e != cudaSuccess) return e;
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(items < sm_count ? items : sm_count));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.planned ? sm_count : items * p.splits));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
-  return cudaLaunchKernelEx(&cfg, prompt_kernel, tm_q, tm_k_nope, tm_k_rope, tm_v, p);
+  e = cudaLaunchKernelEx(&cfg, prompt_kernel, tm_q, tm_k_nope, tm_k_rope, tm_v, p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  cfg.gridDim = dim3(kBlock / kMergeWarps, static_cast<unsigned>(items));
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prompt_merge_kernel, p);
 }
 
 }  // namespace mla

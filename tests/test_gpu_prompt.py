@@ -64,7 +64,7 @@ def run(args, scale=SCALE, causal=True, flags=0, pad=0):
     g_out, g_lse = Guarded(n * h * 256), Guarded(n * h * 4)
     g_out.body.fill_(0xA5)
     g_lse.body.fill_(0xA5)
-    g_ws = Guarded(mla.prompt_attention_workspace_size(n, batch))
+    g_ws = Guarded(mla.prompt_attention_workspace_size(n, args[1].shape[0], h, batch))
     g_ws.body.fill_(0xFF)
     out, lse = mla.prompt_attention(*args, scale, is_causal=causal, out=g_out.view(torch.bfloat16, (n, h, 128)),
                                     lse=g_lse.view(torch.float32, (n, h)), workspace=g_ws.body)
@@ -98,6 +98,14 @@ def test_queries_and_keys(n, m, causal):
 @pytest.mark.parametrize("h_q,h_kv", [(1, 1), (3, 3), (16, 16), (16, 4), (8, 1), (20, 5), (128, 128)])
 def test_heads(h_q, h_kv):
     compare(inputs(h_q, h_kv, [(70, 70), (200, 330), (1, 40)], seed=h_q + h_kv), f"{h_q} {h_kv}")
+
+
+@pytest.mark.parametrize("n,m", [(1, 700), (1, 5000), (7, 9001), (100, 513), (200, 2000), (300, 4000), (256, 20000)])
+@pytest.mark.parametrize("heads", [1, 16, 60])
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_rows_behind_many_keys(n, m, heads, causal):
+    # an item's keys shared out over several CTAs, whose results are merged
+    compare(inputs(heads, 1, [(n, m), (0, 3), (2, 300)], seed=n + m), f"{n} {m} {heads}", causal=causal)
 
 
 @pytest.mark.parametrize("gap", [0, 8, 64])
@@ -223,6 +231,23 @@ def test_empty_calls():
     out, lse = mla.prompt_attention(q, k_nope[:0], k_rope[:0], v[:0], qo, i32([0, 0]), SCALE)
     assert (out == 0).all() and (lse == -math.inf).all()
     assert mla.device_status() == 0
+
+
+def test_workspaces_are_checked():
+    args = inputs(1, 1, [(20, 3000)], seed=13)  # (5 CTAs share the one item's keys)
+    need = mla.prompt_attention_workspace_size(20, 3000, 1, 1)
+    assert need > 5 * 256 * 129 * 4
+    for ws in (torch.empty(need - 1, dtype=torch.uint8, device="cuda"), torch.empty(need + 16, dtype=torch.uint8, device="cuda")[16:]):
+        with pytest.raises(ValueError, match="workspace"):
+            mla.prompt_attention(*args, SCALE, workspace=ws)
+    with pytest.raises(ValueError, match="k_rope must be"):
+        mla.prompt_attention(args[0], args[1], args[2][:, :32], *args[3:], SCALE)
+    with pytest.raises(ValueError, match="multiple of h_kv"):
+        mla.prompt_attention(args[0].expand(-1, 3, -1).contiguous(), args[1].expand(-1, 2, -1).contiguous(), args[2],
+                             args[3].expand(-1, 2, -1).contiguous(), *args[4:], SCALE)
+    with pytest.raises(ValueError, match="positive multiple of 8"):
+        mla.prompt_attention(args[0].expand(-1, 2, -1).contiguous(), args[1].expand(-1, 2, -1), args[2],
+                             args[3].expand(-1, 2, -1), *args[4:], SCALE)
 
 
 def test_watchdog_reports_an_expired_wait():
