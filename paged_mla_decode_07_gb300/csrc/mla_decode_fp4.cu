@@ -26,6 +26,20 @@
 // of O, eight have the softmax and the results.  Two tile buffers, whose chunks
 // are handed on in pairs.
 //
+// What bounds it: not memory (64 x 16 rows over 2048 to 16384 keys take 73 us, 3.2
+// TB/s, where the rows' bytes take 35) but the chain of a tile through its buffer,
+// 3.3k cycles a tile: stores of the values, products of S, softmax, products of O,
+// the next values.  In it the products (1540 cycles of operand reads at the 128
+// bytes a clock of shared memory) and the stores share that bandwidth, ~3000 cycles
+// of it a tile.  More buffers have no room (a tile of E5M2 values is 64 KB); the
+// same tiles in bf16 would be twice that and twice the operand traffic.  Measured
+// on the way (us, that call): all threads doing everything, two CTAs an SM, codes
+// prefetched in registers, 120 (the loads' scoreboards are those of the other
+// steps); roles with eight conversion warps 122, products of S and O from one warp in
+// whichever order is ready 124, maxima exchanged in raised tiles alone 115, sixteen
+// conversion warps, P by rows and a warp each for S and O 87, values held in
+// registers until their buffer is free 83, row sums by lanes 81 (cold caches).
+//
 // Every wait is bounded (watchdog); after one that ran out every role leaves,
 // copies and products are drained and the tensor memory is freed.
 #include "mla_cluster.cuh"
