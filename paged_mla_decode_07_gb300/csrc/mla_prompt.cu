@@ -107,11 +107,15 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, const Watc
     if (global_timer_ns() - t0 > wd.limit_ns) break;
 }
 
-// Item `n` of this CTA, as the load warp has put it into shared memory.
+// Item `n` of this CTA, as the load warp has put it into shared memory.  Each lane
+// reads a word, the shuffles use them: the arrival behind them is behind the reads.
 __device__ __forceinline__ bool get_item(int n, uint8_t* smem, const Bars& bars, const Watchdog& wd, Item& it) {
   if (!wait_warp(bars.item_full + (n & 1), (n >> 1) & 1, wd)) return false;
+  const int lane = threadIdx.x & 31;
   const volatile int* v = reinterpret_cast<const volatile int*>(smem + kItemOff) + (n & 1) * kItemInts;
-  it = Item{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8]};
+  const int word = v[lane < kItemInts ? lane : 0];
+  auto at = [&](int i) { return __shfl_sync(0xffffffffu, word, i); };
+  it = Item{at(0), at(1), at(2), at(3), at(4), at(5), at(6), at(7), at(8)};
   arrive_warp(bars.item_empty + (n & 1));
   return !it.end;
 }
