@@ -460,6 +460,11 @@ __device__ void convert(const __nv_bfloat16* q, const DecodeParams& p, const Ran
           code[k] = *reinterpret_cast<const uint4*>(row + 128 * k + 64 * d + 16 * c0);
           scale[k] = row[kFp4ScaleOffset + 8 * k + 4 * d + c0];
         }
+        // The slot is handed back behind an instruction that uses each read (the branch; the
+        // fence in it is not needed): an arrival right behind the reads has let the next
+        // page's copy overtake them, where there is one slot and pages are in L2.
+        if (__any_sync(0xffffffffu, (code[0].x ^ code[1].x) + (scale[0] ^ scale[1]) == 0x9e3779b9u)) __threadfence_block();
+        arrive_warp(bars.raw_empty + slot);
         if (!real || !page_used(p, lp, s.L)) {
           // a token that no row sees is zeros, whatever its row holds
           if (!real || !key_seen(p, lp * kPageSize + t, s.L)) code[0] = code[1] = make_uint4(0, 0, 0, 0);
@@ -472,10 +477,6 @@ __device__ void convert(const __nv_bfloat16* q, const DecodeParams& p, const Ran
           out[n][k][0] = make_uint4(x.x, x.y, y.x, y.y);
           out[n][k][1] = make_uint4(z.x, z.y, w.x, w.y);
         }
-        // Behind the instructions that use what was read: an arrival right behind the reads
-        // has let the next page's copy overtake them (one ring slot, pages in L2: a few
-        // words of a page in hundreds of calls).
-        arrive_warp(bars.raw_empty + slot);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {

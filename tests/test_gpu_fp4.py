@@ -210,3 +210,111 @@ def test_an_unusable_page_is_flagged_and_masked(h_q):
     assert torch.allclose(got[1][1], whole[1][1], rtol=0, atol=2.0 ** -18)
     assert (got[1][0] < whole[1][0]).all()
     run(q, kv, sc, bt[:, :14].contiguous(), L, window, 0, flags=mla.DEVICE_BAD_PAGE)  # a table too short
+
+
+@pytest.mark.parametrize("h_q,s_q,window", [(16, 1, 1 << 30), (128, 1, 1 << 30), (128, 2, 1000), (40, 1, 700)])
+def test_repeated_calls_are_equal(h_q, s_q, window):
+    # pages that lie in L2 come back faster than they are read: no word of a page may be the next one's
+    lens = [int(x) for x in np.random.default_rng(7).integers(50, 5000, 40)]
+    q, kv, sc, bt, L, want = fp4_problem(h_q, s_q, lens, window, 16, seed=11)
+    first = run(q, kv, sc, bt, L, window, 16)
+    check(*first, want, f"{h_q}x{s_q}")
+    for _ in range(200):
+        out, lse = mla.window_decode(q, kv.view(torch.uint8).view(-1, PAGE, 1, ROW), bt, L, SCALE, window=window, sinks=16)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert mla.device_status() == 0
+
+
+def test_captured_calls_and_other_streams():
+    q, kv, sc, bt, L, want = fp4_problem(32, 1, (700, 64, 3000), 500, 4, seed=12)
+    kv = kv.view(torch.uint8).view(-1, PAGE, 1, ROW)
+    first = run(q, kv, sc, bt, L, 500, 4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = mla.window_decode(q, kv, bt, L, SCALE, window=500, sinks=4)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [mla.window_decode(q, kv, bt, L, SCALE, window=500, sinks=4, stream=s) for s in streams for _ in range(5)]
+    graph.replay()
+    torch.cuda.synchronize()
+    for o, z in [*got, (out, lse)]:
+        assert torch.equal(o, first[0]) and torch.equal(z, first[1])
+
+
+def test_refusals_name_the_argument():
+    q, kv, sc, bt, L, _ = fp4_problem(16, 1, (100,), 50, 0, seed=1)
+    kv = kv.view(torch.uint8).view(-1, PAGE, 1, ROW)
+    with pytest.raises(ValueError, match="kv_scales given with an FP4 kvcache"):
+        mla.window_decode(q, kv, bt, L, SCALE, window=5, kv_scales=torch.ones(kv.shape[:2], device="cuda"))
+    with pytest.raises(ValueError, match="does not take an FP4 kvcache"):
+        mla.shared_prefix_decode(q, kv, bt[0], L, bt, L, SCALE)
+    with pytest.raises(ValueError, match="page_size"):
+        mla.window_decode(q, kv.view(-1, 32, 1, ROW), bt, L, SCALE, window=5)
+    with pytest.raises(ValueError, match="out must be"):
+        mla.cache_load(kv, bt, i32([0, 5]), 5, out=torch.empty(4, 576, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="row_offsets must have"):
+        mla.cache_load(kv, bt, i32([0, 5, 6]), 5)
+    with pytest.raises(ValueError, match="starts must have"):
+        mla.cache_load(kv, bt, i32([0, 5]), 5, starts=i32([0, 1]))
+
+
+@pytest.mark.parametrize("h_q", [16, 128])
+def test_watchdog_reports_an_expired_wait(h_q):
+    from gpu_helpers import env
+    q, kv, sc, bt, L, want = fp4_problem(h_q, 1, (900, 300), 1 << 30, 0, seed=2)
+    for parts in (None, 3):  # clusters, a schedule
+        with env(MLA_WATCHDOG_NS=20_000_000), overrides(debug_stall=True, num_parts=parts):
+            mla.window_decode(q, kv.view(torch.uint8).view(-1, PAGE, 1, ROW), bt, L, SCALE, window=1 << 30)
+            torch.cuda.synchronize()
+        assert mla.device_status() & mla.DEVICE_TIMEOUT
+        check(*run(q, kv, sc, bt, L, 1 << 30, 0), want, "after a timeout")
+
+
+def test_rows_that_are_not_finite_stay_alone():
+    q, kv, sc, bt, L, _ = fp4_problem(16, 1, (300, 700), 1 << 30, 0, seed=3)
+    want = run(q, kv, sc, bt, L, 1 << 30, 0)
+    q[0, 0, 5, 100] = float("nan")
+    q[1, 0, 7, 570] = float("inf")
+    out, lse = run(q, kv, sc, bt, L, 1 << 30, 0)
+    keep = torch.ones(2, 1, 16, dtype=torch.bool, device="cuda")
+    keep[0, 0, 5] = keep[1, 0, 7] = False
+    assert torch.isnan(out[~keep]).all() and torch.isnan(lse[~keep]).all()
+    assert torch.equal(out[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+
+
+@pytest.mark.parametrize("spread", [1e-3, 20.0])
+def test_query_magnitudes(spread):
+    # rows of q of any size, values of a row 2^12 apart: split into two 8-bit terms
+    q, kv, sc, bt, L, _ = fp4_problem(16, 1, (500,), 1 << 30, 0, seed=4)
+    q.mul_(spread * torch.exp2(torch.randint(-12, 1, q.shape, device="cuda").float()).to(torch.bfloat16))
+    out, lse = run(q, kv, sc, bt, L, 1 << 30, 0)
+    rows = mla.cache_load(kv.view(torch.uint8).view(-1, PAGE, 1, ROW), bt, i32([0, 500]), 500).double()
+    want_out, want_lse, mean = attend(q[0, 0], rows, SCALE)
+    # a term of q is off by 2^-18 of its row's largest value, 576 of them meet keys of about one, then the scale
+    off = 2.0 ** -18 * q.abs().max().item() * 576 * rows.abs().mean().item() * SCALE
+    assert (lse[0, 0].double() - want_lse).abs().max().item() <= off + 2.0 ** -9
+    assert ((out[0, 0].double() - want_out).abs() <= (2.0 ** -8 + 2 * off + 2.0 ** -9) * mean + 2.0 ** -8 * want_out.abs()).all()
+
+
+def test_weights_far_below_the_largest():
+    # one key 2^14 above 6000 others, which together have a third of its weight
+    n = 6000
+    cache = Fp4Cache("fp4", 5, -(-n // PAGE) + 1)
+    values, ids = cache.put(n)
+    kv = cache.raw.view(-1, PAGE, 1, ROW)
+    q = torch.zeros(1, 1, 16, 576, device="cuda", dtype=torch.bfloat16)
+    top = values[1234, 512:]
+    q[0, 0, :, 512:] = top.to(torch.bfloat16)
+    scale = (14.2 * np.log(2.0)) / float(top @ top)
+    rows = torch.cat([values[:, :512], torch.zeros(n, 64, device="cuda", dtype=torch.float64)], 1)
+    raw = cache.raw.view(-1, ROW)
+    slots = torch.tensor(ids, device="cuda").repeat_interleave(PAGE)[:n] * PAGE + torch.arange(n, device="cuda") % PAGE
+    raw[slots, 272:] = 0  # the others' RoPE values: scores of 0
+    raw[slots[1234], 272:] = top.to(torch.bfloat16).view(torch.uint8)
+    rows[1234, 512:] = top.to(torch.bfloat16).double()
+    out, lse = mla.window_decode(q, kv, table([ids]), i32([n]), scale, window=1 << 30)
+    want = attend(q[0, 0], rows, scale)
+    assert abs(float(torch.exp2(want[1][0] - 14.2)) - 1.32) < 0.02
+    check(out, lse, tuple(w[None, None] for w in want), "small weights")
+    assert mla.device_status() == 0

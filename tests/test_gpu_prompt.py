@@ -198,6 +198,18 @@ def test_repeated_runs_are_equal_and_a_graph_replays():
     assert mla.device_status() == 0
 
 
+def test_repeated_calls_are_equal():
+    # short and long items, several thousand: no field of one may be the next one's
+    g = torch.Generator().manual_seed(3)
+    lens = [(int(n), int(n + c)) for n, c in torch.randint(1, 400, (300, 2), generator=g).tolist()] + [(1500, 1500)]
+    args = inputs(16, 16, lens, seed=14)
+    want = mla.prompt_attention(*args, SCALE)
+    for _ in range(100):
+        got = mla.prompt_attention(*args, SCALE)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert mla.device_status() == 0
+
+
 def test_bad_offsets_are_flagged_or_cut_off():
     q, k_nope, k_rope, v, _, _ = inputs(2, 2, [(100, 100)], seed=9)
     # past the rows: cut off there
