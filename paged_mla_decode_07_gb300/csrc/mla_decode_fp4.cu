@@ -517,10 +517,13 @@ __device__ void score_products(const DecodeParams& p, const Range& rg, uint32_t 
       const int b = i & 1, ph = (i >> 1) & 1;
       const uint32_t a = desc_lo(base + b * kTileBytes, 16), ar = desc_lo(base + C::kRopeOff + b * kChunkBytes, 16);
       const uint32_t d = tmem + C::kSCol + 2 * R * b;
-      if (i >= 2) ok = wait_warp(bars.p_full + b, ph ^ 1, wd);  // (the scores of two tiles before have been read)
+      // the scores of two tiles before have been read, the RoPE values are there (each wait takes
+      // about a hundred cycles: those that end early come first)
+      if (i >= 2) ok = wait_warp(bars.p_full + b, ph ^ 1, wd);
+      ok = ok && wait_warp(bars.rope_full + b, ph, wd);
 #pragma unroll
       for (int part = 0; part < 3; ++part) {  // two chunks, two chunks, RoPE
-        ok = ok && wait_warp(part < 2 ? bars.k_full + 2 * b + part : bars.rope_full + b, ph, wd);
+        if (part < 2) ok = ok && wait_warp(bars.k_full + 2 * b + part, ph, wd);
         tc_fence_after();
         if (elect_one()) {
           if (ok && part < 2) {
@@ -611,9 +614,11 @@ __device__ void softmax(const DecodeParams& p, const Range& rg, int g, int part,
 #pragma unroll 1
     for (int j = s.pb; j < s.pe; j += 2, ++i) {
       const int b = i & 1;
-      ok = ok && mbar_wait(bars.s_full + b, (i >> 1) & 1, wd);
-      // (the conversion warps' page states and factors are read below)
+      // (the conversion warps' page states and factors are read below; two buffers of P: this
+      // tile's is free where its scores are to come)
       ok = ok && mbar_wait(bars.k_full + 2 * b, (i >> 1) & 1, wd);
+      if (C::kPBufs == 2 && i >= 2) ok = ok && mbar_wait(bars.done + 2 * b + 1, ((i >> 1) - 1) & 1, wd);
+      ok = ok && mbar_wait(bars.s_full + b, (i >> 1) & 1, wd);
       tc_fence_after();
       if (j == s.pb) {
 #pragma unroll
@@ -650,7 +655,6 @@ __device__ void softmax(const DecodeParams& p, const Range& rg, int g, int part,
 #pragma unroll
         for (int r = 0; r < N; ++r) vote |= !((seen >> r) & 1) && y[r] != kNegInf;
       }
-      const int before = C::kPBufs == 1 ? i - 1 : i - 2;  // the tile whose products free the buffer of P
       // (the four warps of a half act and leave alike)
       if (named_bar_or(kHalfBar + half, 128, vote)) {
         // two buffers: a warp that is ahead passes no vote of the tile behind it
@@ -697,7 +701,7 @@ __device__ void softmax(const DecodeParams& p, const Range& rg, int g, int part,
           tmem_st_wait();
         }
       }
-      if (before >= 0) ok = ok && mbar_wait(bars.done + 2 * (before & 1) + 1, (before >> 1) & 1, wd);
+      if (C::kPBufs == 1 && i > 0) ok = ok && mbar_wait(bars.done + 2 * ((i - 1) & 1) + 1, ((i - 1) >> 1) & 1, wd);
       const uint32_t pt = smem_u32(smem) + C::kPOff + (i % C::kPBufs) * C::kPBytes + (32 * quarter + lane) * 16 +
                           (N == 8 ? 8 * half : 2048 * half);
 #pragma unroll
