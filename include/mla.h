@@ -342,7 +342,8 @@ mla_status mla_cache_load(const mla_cache_load_args* args, mla_stream_t stream);
  * (a window of 2^30 or more sees every key: causal decode over the whole cache),
  * with its rules for missing pages and sizes.  Latent values and their products
  * with q are exact (q to 2^-18 of the largest value of its row), sums fp32, and
- * probabilities are rounded to a relative 2^-9.  The RoPE values of a key that
+ * probabilities are rounded to a relative 2^-9 (those under 2^-18 of the row's
+ * largest to 2^-25 of that).  The RoPE values of a key that
  * some query token sees must be finite, or rows of its element are not.  A row
  * of q that is not finite has results that are not, other rows are as they
  * would be.  All launches are made on `stream` by the one call. */

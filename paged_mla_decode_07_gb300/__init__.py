@@ -17,6 +17,9 @@ code path.  If ``libmla.so`` has not been built, every call raises.
     cache_store(latent, rope, slots, kvcache)
     out, lse = window_decode(q, kvcache, block_table, lens, sm_scale, window=..., sinks=...)
     out, lse = shared_prefix_decode(q, kvcache, prefix_table, prefix_length, block_table, lens, sm_scale)
+
+    rows = cache_load(kvcache, block_table, k_offsets, num_tokens)
+    out, lse = prompt_attention(q, k_nope, k_rope, v, q_offsets, k_offsets, sm_scale)
 """
 from __future__ import annotations
 
