@@ -181,17 +181,29 @@ __device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uin
   const int total = p.planned ? p.plan[kPromptBlocks] * p.h_q : 0;  // (below 2^31 by the host's check)
   uint32_t chunk = 0;  // chunks of keys and values so far
   int n = 0;
-  auto fetch = [&]() {
-    const int at = p.planned ? atomicAdd(p.plan + kPromptCounter, 1) : 0;
-    if (at >= total) return Item{0, 0, 0, 0, 0, 0, 1};
-    const int4* e = reinterpret_cast<const int4*>(p.plan + kPromptList) + 2 * (at / p.h_q);
-    const int4 a = e[0], b = e[1];
-    return Item{a.x, a.y, a.z, a.w, b.x, at % p.h_q, 0};
+  // An item is taken late, while the last two tiles of the one before are loaded: one
+  // taken earlier waits for its turn here where another CTA is free (8 chunks of 256 to
+  // 1023 queries behind up to 8192 keys, 16 heads: 231 us for 214).
+  int ticket = total;
+  int4 e0, e1;
+  auto take = [&]() {
+    if (p.planned) ticket = atomicAdd(p.plan + kPromptCounter, 1);
   };
-  Item next = p.planned ? fetch() : own;
+  auto look = [&]() {
+    if (ticket >= total) return;
+    const int4* e = reinterpret_cast<const int4*>(p.plan + kPromptList) + 2 * (ticket / p.h_q);
+    e0 = e[0];
+    e1 = e[1];
+  };
+  auto item = [&]() {
+    return ticket >= total ? Item{0, 0, 0, 0, 0, 0, 1} : Item{e0.x, e0.y, e0.z, e0.w, e1.x, ticket % p.h_q, 0};
+  };
+  take();
+  look();
+  Item next = p.planned ? item() : own;
 #pragma unroll 1
   for (;; ++n) {
-    const Item it = next;  // (the next one is on its way while this one's tiles are loaded)
+    const Item it = next;
     if (n >= 2 && !mbar_wait(bars.item_empty + (n & 1), ((n >> 1) - 1) & 1, wd)) break;
     volatile int* v = reinterpret_cast<volatile int*>(smem + kItemOff) + (n & 1) * kItemInts;
     v[0] = it.q0;
@@ -205,19 +217,16 @@ __device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uin
     v[8] = it.j1;
     mbar_arrive(bars.item_full + (n & 1));
     if (it.end) break;
-    next = fetch();
-    if (!next.end)
-      for (int h = 0; h < 2; ++h)
-        if (next.tiles(h, p.causal) > 0)
-          for (int c = 0; c < kKChunks; ++c) tma_prefetch_3d(tm.q, 64 * c, next.head, next.q0 + kHalfRows * h);
-    const int nt = max(it.stop(0, p.causal), it.stop(1, p.causal));
+    const int nt = max(it.stop(0, p.causal), it.stop(1, p.causal)), late = max(it.j0, nt - 2);
     bool ok = true;
     const int kv_head = it.head / group;
 #pragma unroll 1
     for (int j = it.j0; j < nt && ok; ++j) {
+      if (j == late) take();
 #pragma unroll 1
       for (int c = 0; c < kTileChunks; ++c, ++chunk) {
         const int slot = chunk % kSlots;
+        if (c == 2 && j == nt - 1) look();
         ok = chunk < kSlots || mbar_wait(bars.empty + slot, (chunk / kSlots - 1) & 1, wd);
         if (!ok) break;
         mbar_arrive_expect_tx(bars.full + slot, kChunkBytes);
@@ -236,6 +245,15 @@ __device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uin
       }
     }
     if (!ok) break;
+    if (nt <= it.j0) {
+      take();
+      look();
+    }
+    next = item();
+    if (!next.end)
+      for (int h = 0; h < 2; ++h)
+        if (next.tiles(h, p.causal) > 0)
+          for (int c = 0; c < kKChunks; ++c) tma_prefetch_3d(tm.q, 64 * c, next.head, next.q0 + kHalfRows * h);
   }
   // no copy may be in flight when the CTA ends
   for (uint32_t i = chunk > kSlots ? chunk - kSlots : 0; i < chunk; ++i) drain(bars.full + i % kSlots, (i / kSlots) & 1, wd);
