@@ -284,7 +284,7 @@ __device__ void copy_codes(const CUtensorMap* tm, const DecodeParams& p, const R
       // page j + kAhead into L2 (64 pages are known from j0 on); a segment's first pages come as they are copied
       const int at = j - j0 + kAhead;
       const int far = at < 32 ? __shfl_sync(0xffffffffu, ids, at) : __shfl_sync(0xffffffffu, next, at - 32);
-      if (lane == 0 && far >= 0)
+      if (lane == 0 && far >= 0 && u >= C::kRaw)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                          p.kv_fp8 + static_cast<int64_t>(far) * (kPageSize * kFp4RowBytes)),
                      "r"(kPageSize * kFp4RowBytes)

@@ -116,6 +116,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// The same in half the instructions, for kernels whose roles wait at many places.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if (i & 31) continue;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    const bool late = now - t0 > wd.limit_ns;
+    if (late) wd.trip(MLA_DEVICE_TIMEOUT);
+    if (late || wd.aborted()) return false;
+  }
+  return true;
+}
+
 // Named barrier for a subset of warps (ids 1..15; id 0 is __syncthreads).
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

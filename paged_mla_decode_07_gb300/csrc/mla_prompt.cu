@@ -95,7 +95,7 @@ struct Bars {
 };
 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wd));
+  return __all_sync(0xffffffffu, mbar_wait_short(bar, parity, wd));
 }
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   __syncwarp();
@@ -204,7 +204,7 @@ __device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uin
 #pragma unroll 1
   for (;; ++n) {
     const Item it = next;
-    if (n >= 2 && !mbar_wait(bars.item_empty + (n & 1), ((n >> 1) - 1) & 1, wd)) break;
+    if (n >= 2 && !mbar_wait_short(bars.item_empty + (n & 1), ((n >> 1) - 1) & 1, wd)) break;
     volatile int* v = reinterpret_cast<volatile int*>(smem + kItemOff) + (n & 1) * kItemInts;
     v[0] = it.q0;
     v[1] = it.rows;
@@ -227,7 +227,7 @@ __device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uin
       for (int c = 0; c < kTileChunks; ++c, ++chunk) {
         const int slot = chunk % kSlots;
         if (c == 2 && j == nt - 1) look();
-        ok = chunk < kSlots || mbar_wait(bars.empty + slot, (chunk / kSlots - 1) & 1, wd);
+        ok = chunk < kSlots || mbar_wait_short(bars.empty + slot, (chunk / kSlots - 1) & 1, wd);
         if (!ok) break;
         mbar_arrive_expect_tx(bars.full + slot, kChunkBytes);
         uint8_t* dst = smem + kRingOff + slot * kChunkBytes;
@@ -321,7 +321,8 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
 __device__ void score_products(const PromptParams& p, uint32_t tmem, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
   const uint32_t base = desc_addr(smem), bars_empty = smem_u32(bars.empty);
   const uint32_t q_lo = desc_lo(base + kQOff, 16), ring_lo = desc_lo(base + kRingOff, 16);
-  constexpr uint32_t kIdS = idesc_bf16_f32(kHalfRows, kKeys, 0, 0);
+  // (a negative scale: the products are those of -Q, bit 13)
+  const uint32_t id_s = idesc_bf16_f32(kHalfRows, kKeys, 0, 0) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
   uint32_t chunk = 0;  // first chunk of the tile
   int items[2] = {0, 0}, tiles[2] = {0, 0};
   bool ok = true;
@@ -354,7 +355,7 @@ __device__ void score_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
               const uint32_t b = ring_lo + (c == 0 ? s0 : c == 1 ? s1 : s2) * (kChunkBytes >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                umma_ss(tmem + kSCol + 128 * h, q_lo + (((h * kKChunks + c) * kChunkBytes) >> 4) + 2 * k, b + 2 * k, kIdS,
+                umma_ss(tmem + kSCol + 128 * h, q_lo + (((h * kKChunks + c) * kChunkBytes) >> 4) + 2 * k, b + 2 * k, id_s,
                         c + k > 0);
             }
           }
@@ -466,7 +467,6 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
   const uint32_t s_at = tmem + lanes + kSCol + 128 * half, o_at = tmem + lanes + kOCol + 128 * half;
   const int r = kHalfRows * half + 32 * quarter + lane;  // row of the item
   const float scale = fmaxf(fabsf(p.scale_log2), 1.1754944e-38f);  // (0 would turn a masked score into NaN)
-  const bool negative = p.scale_log2 < 0.f;
   const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
   uint32_t tile0 = 0;  // tiles of the CTA before the item
   int n_s = 0;
@@ -491,15 +491,16 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
         for (int i = 0; i < 32; ++i) x[32 * c + i] = v[i];
       }
       tmem_ld_wait();
-      if (negative) {
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) x[i] = -x[i];
-      }
       const int valid = sees - j * kKeys;  // of this tile's keys the row sees
       if (__any_sync(0xffffffffu, valid < kKeys)) {
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i)
-          if (i >= valid) x[i] = kNegInf;
+        for (int c = 0; c < 4; ++c) {
+          const int v = valid - 32 * c;
+          const uint32_t keep = v >= 32 ? ~0u : v <= 0 ? 0u : (1u << v) - 1;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(keep & (1u << i))) x[32 * c + i] = kNegInf;
+        }
       }
       float m0 = max3_nan(x[0], x[1], x[2]), m1 = max3_nan(x[3], x[4], x[5]);
       float m2 = max3_nan(x[6], x[7], x[8]), m3 = max3_nan(x[9], x[10], x[11]);
@@ -587,7 +588,7 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
       tc_fence_after();
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       float o[32];
       if (some) {

@@ -36,10 +36,11 @@ __device__ __forceinline__ int spec_tiles(const SchedSpec& sp, int p, int tile_t
 // Windowed and shared-prefix decode make their schedule in every CTA of the
 // decode kernel instead of in a kernel before it, which adds 5.3 us to a chain
 // of 20 (4 elements, 10 pages).  Code that runs once per launch is bound by its
-// instruction fetches, barriers and dependent loads (~1.2k cycles for each scan
-// or search; 7.7k in all when it counted the slots of split problems as the
-// schedule kernel does), so it is kept to one scan and one search: a CTA needs
-// its own part's ends, and the slots of partial results are named by part.
+// instruction fetches, barriers and dependent loads (~1.2k cycles for a scan or a
+// binary search; 7.7k in all when it counted the slots of split problems as the
+// schedule kernel does), so it is kept to one scan, behind which the thread whose
+// problems hold an end of the part finds it: a CTA needs its own part's ends, and
+// the slots of partial results are named by part.
 //
 // The cut: problem i is a start-up cost and tiles of tile_cost each, parts are
 // equal shares of all costs, as in mla_sched.cu.  A share smaller than a
@@ -68,9 +69,10 @@ __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int
                                                       unsigned char* scratch, bool publish) {
   const int np = p.num_problems, parts = p.num_parts, tid = threadIdx.x;
   const int lane = tid & 31, w = tid >> 5, warps = blockDim.x >> 5;
-  // tiles (high word) and problems with tiles (low word) of the problems before
-  long long* pre = reinterpret_cast<long long*>(scratch);  // [np + 1]
-  long long* warp_tot = pre + np + 1;                      // [warps]
+  // tiles (high word) and problems with tiles (low word), of each problem and of each warp's
+  long long* held = reinterpret_cast<long long*>(scratch);  // [np], read by the thread that wrote it
+  long long* warp_tot = held + np + 1;                      // [warps <= 32]
+  int* const found = reinterpret_cast<int*>(warp_tot + 32);  // [2][2]
   SchedSpec spec = {};
   spec.seqlens = p.cache_seqlens;
   spec.s_q = p.s_q;
@@ -92,7 +94,7 @@ __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int
 #pragma unroll 1
   for (int i = b0; i < b1; ++i) {
     const long long v = both(i);
-    pre[i] = mine;
+    held[i] = v;
     mine += v;
   }
   long long x = mine;
@@ -112,10 +114,7 @@ __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int
   const long long total = __shfl_sync(0xffffffffu, t, 31);
   x -= mine;
   if (w > 0) x += __shfl_sync(0xffffffffu, t, w - 1);
-#pragma unroll 1
-  for (int i = b0; i < b1; ++i) pre[i] += x;
-  if (tid == 0) pre[np] = total;
-  __syncthreads();
+  // (x: those before this thread's run)
 
   // shares in costs, or in tiles
   long long tile_cost = p.tile_cost, overhead = p.overhead;
@@ -126,7 +125,7 @@ __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int
   }
   const long long all = cost_of(total);
   const bool small = all < (1ll << 31);  // 32-bit divisions
-  int pos[2][2];
+  const long long starts = cost_of(x), ends = cost_of(x + mine);
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     const int k = part + e;
@@ -139,37 +138,30 @@ __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int
     } else {
       at = all / parts * k + all % parts * k / parts;
     }
-    int lo = np, tile = 0;
-    if (at < all) {
-      // the last problem that starts at or before `at` (of those without tiles the last)
-      lo = 0;
-      int hi = np - 1;
+    if (at >= all) {
+      if (tid == 0) {
+        found[2 * e] = np;
+        found[2 * e + 1] = 0;
+      }
+    } else if (starts <= at && at < ends) {  // one thread's run holds it
+      int i = b0;
+      long long before = x;
 #pragma unroll 1
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cost_of(pre[mid]) <= at)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      const long long o = at - cost_of(pre[lo]) - overhead;
-      if (o > 0)
-        tile = small ? static_cast<int>(static_cast<unsigned>(o) / static_cast<unsigned>(tile_cost))
-                     : static_cast<int>(o / tile_cost);
-      if (tile >= static_cast<int>((pre[lo + 1] - pre[lo]) >> 32)) {
-        ++lo;
-        tile = 0;
-      }
+      for (; i + 1 < b1 && cost_of(before + held[i]) <= at; ++i) before += held[i];
+      const long long o = at - cost_of(before) - overhead;
+      found[2 * e] = i;
+      found[2 * e + 1] = o <= 0 ? 0
+                         : small ? static_cast<int>(static_cast<unsigned>(o) / static_cast<unsigned>(tile_cost))
+                                 : static_cast<int>(o / tile_cost);
     }
-    pos[e][0] = lo;
-    pos[e][1] = tile;
   }
-  const PartRecord r{pos[0][0], pos[0][1], pos[1][0], pos[1][1]};
+  __syncthreads();
+  const PartRecord r{found[0], found[1], found[2], found[3]};
   if (publish) {
-    const int end = r.p1 < np ? r.p1 : np - 1;
+    const int first = part == 0 ? 0 : r.p0, end = r.p1 < np ? r.p1 : np - 1;
 #pragma unroll 1
-    for (int i = (part == 0 ? 0 : r.p0) + tid; i <= end; i += blockDim.x) {
-      const int n = static_cast<int>((pre[i + 1] - pre[i]) >> 32);
+    for (int i = max(b0, first); i < min(b1, end + 1); ++i) {
+      const int n = static_cast<int>(held[i] >> 32);
       if (n == 0) {
         p.spans[2 * i] = 0;
         p.spans[2 * i + 1] = -1;
