@@ -251,8 +251,10 @@ __device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uin
     }
     next = item();
     if (!next.end)
+#pragma unroll 1
       for (int h = 0; h < 2; ++h)
         if (next.tiles(h, p.causal) > 0)
+#pragma unroll 1
           for (int c = 0; c < kKChunks; ++c) tma_prefetch_3d(tm.q, 64 * c, next.head, next.q0 + kHalfRows * h);
   }
   // no copy may be in flight when the CTA ends
@@ -265,20 +267,21 @@ __device__ void load(const Maps& tm, const PromptParams& p, const Item& own, uin
 __device__ void load_queries(const CUtensorMap* tm, const PromptParams& p, uint8_t* smem, const Bars& bars, const Watchdog& wd) {
   const uint64_t pol = l2_policy_evict_normal();
   const int lane = threadIdx.x & 31;
-  int loads[2] = {0, 0};
+  uint32_t loaded = 0, phase = 3;  // bit h: some were loaded; the parity to wait for (first: that before the first phase)
   bool ok = true;
   Item it;
 #pragma unroll 1
   for (int n = 0; ok && get_item(n, smem, bars, wd, it); ++n) {
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       if (it.stop(h, p.causal) <= it.j0) continue;
-      ok = ok && (loads[h] == 0 || wait_warp(bars.q_empty + h, (loads[h] - 1) & 1, wd));
+      ok = ok && wait_warp(bars.q_empty + h, (phase >> h) & 1, wd);
       if (!ok) break;
-      ++loads[h];
+      phase ^= 1u << h;
+      loaded |= 1u << h;
       if (lane == 0) {
         mbar_arrive_expect_tx(bars.q_full + h, kKChunks * kChunkBytes);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kKChunks; ++c)
           tma_load_3d(smem + kQOff + (h * kKChunks + c) * kChunkBytes, tm, bars.q_full + h, 64 * c, it.head,
                       it.q0 + kHalfRows * h, pol);
@@ -287,8 +290,9 @@ __device__ void load_queries(const CUtensorMap* tm, const PromptParams& p, uint8
     }
   }
   if (lane == 0)
-    for (int h = 0; h < 2; ++h)
-      if (loads[h] > 0) drain(bars.q_full + h, (loads[h] - 1) & 1, wd);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h)  // (the last load's parity: `phase` has passed it)
+      if ((loaded >> h) & 1) drain(bars.q_full + h, (phase >> h) & 1, wd);
   __syncwarp();
 }
 
@@ -381,7 +385,7 @@ __device__ void value_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
   const uint32_t base = desc_addr(smem);
   constexpr uint32_t kIdO = idesc_bf16_f32(kHalfRows, kHeadV, 0, 1);
   uint32_t chunk = kKChunks;  // first chunk of the tile's values
-  int items[2] = {0, 0}, tiles[2] = {0, 0};
+  uint32_t o_phase = 3, p_phase = 0;  // bit h: the parity to wait for (of the first O: the phase before the first)
   bool ok = true;
   Item it;
 #pragma unroll 1
@@ -394,17 +398,18 @@ __device__ void value_products(const PromptParams& p, uint32_t tmem, uint8_t* sm
       const uint32_t first = min(s0, s1), gap = max(s0, s1) - first;
       const uint32_t b = desc_lo(base + kRingOff + first * kChunkBytes, gap * kChunkBytes);
       const int steps = min(8, (keys - j * kKeys + 15) / 16);  // (rows behind the last key are not read)
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         if (j >= (h ? nt1 : nt0)) continue;
         const bool last_user = h == 1 || j >= nt1;
         if (j == it.j0) {
-          ok = ok && (items[h] == 0 || wait_warp(bars.o_free + h, (items[h] - 1) & 1, wd));
-          ++items[h];
+          ok = ok && wait_warp(bars.o_free + h, (o_phase >> h) & 1, wd);
+          o_phase ^= 1u << h;
         }
         if (h == 0 || j >= nt0)
           ok = ok && wait_warp(bars.full + s0, (chunk / kSlots) & 1, wd) && wait_warp(bars.full + s1, ((chunk + 1) / kSlots) & 1, wd);
-        ok = ok && wait_warp(bars.p_full + h, tiles[h]++ & 1, wd);
+        ok = ok && wait_warp(bars.p_full + h, (p_phase >> h) & 1, wd);
+        p_phase ^= 1u << h;
         tc_fence_after();
         if (elect_one()) {
           if (ok) {
@@ -562,12 +567,12 @@ __device__ void softmax(const PromptParams& p, uint32_t tmem, uint8_t* smem, con
         const uint32_t i = (tile0 + j - it.j0) * kTileChunks + kKChunks;
         const int first = keys - j * kKeys, row = first + (threadIdx.x & 127) / 8, unit = threadIdx.x & 7;
         bool ok = true;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c)
           ok = ok && wait_warp(bars.full + (i + c) % kSlots, ((i + c) / kSlots) & 1, wd);
         if (!ok) return;
         if (row < ((first + 15) & ~15)) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 2; ++c)
             st_shared_v4(smem_u32(smem) + kRingOff + ((i + c) % kSlots) * kChunkBytes + row * 128 + unit * 16,
                          0, 0, 0, 0);
