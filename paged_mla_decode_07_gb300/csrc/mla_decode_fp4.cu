@@ -874,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const PartRecord rec = p.cluster > 0 ? cluster_share(p, part) : inline_schedule(p, part, kTile, smem, g == 0);
+  const PartRecord rec = p.cluster > 0 ? cluster_share(p, part) : inline_schedule<false>(p, part, kTile, smem, g == 0);
   const Range rg{rec, rec.p1 < p.num_problems ? rec.p1 : p.num_problems - 1};
   if (warp < 4) {
     regs_to<C::kRegsCtl, kLaunchRegs>();

@@ -25,9 +25,10 @@ __device__ __forceinline__ int block_tiles(int i, int prefix_len, int prefix_pag
   return n;
 }
 
-// Tiles of problem p.
+// Tiles of problem p (PREFIX: the kernel takes calls with a shared prefix).
+template <bool PREFIX>
 __device__ __forceinline__ int spec_tiles(const SchedSpec& sp, int p, int tile_tokens) {
-  if (sp.prefix_len)
+  if (PREFIX && sp.prefix_len)
     return block_tiles(p, sp.prefix_len[0], sp.prefix_pages, sp.seqlens, sp.cols, sp.rows, sp.total_rows, sp.own_keys);
   const int per = tile_tokens / kPageSize;
   return (key_walk(sp.seqlens[p], sp.s_q, sp.window, sp.sinks, sp.cols).pages + per - 1) / per;
@@ -65,6 +66,7 @@ __host__ __device__ constexpr size_t schedule_scratch(int np) { return (static_c
 // All threads of the block; scratch: schedule_scratch() bytes of shared
 // memory, 8-byte aligned, that the async proxy may write again after this
 // returns.  `publish` makes this CTA write its part's spans.
+template <bool PREFIX = true>
 __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int part, int tile_tokens,
                                                       unsigned char* scratch, bool publish) {
   const int np = p.num_problems, parts = p.num_parts, tid = threadIdx.x;
@@ -85,7 +87,7 @@ __device__ __forceinline__ PartRecord inline_schedule(const DecodeParams& p, int
   spec.total_rows = p.total_rows;
   spec.own_keys = p.own_keys;
   auto both = [&](int i) -> long long {
-    const int n = spec_tiles(spec, i, tile_tokens);
+    const int n = spec_tiles<PREFIX>(spec, i, tile_tokens);
     return n > 0 ? (static_cast<long long>(n) << 32) | 1 : 0;
   };
   // each thread's run of problems, then the scan over threads
