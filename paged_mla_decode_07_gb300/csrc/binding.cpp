@@ -475,7 +475,8 @@ PyObject* prompt_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(assign_pages), ENTRY(cache_store), ENTRY(cache_load), ENTRY(prompt_attention), ENTRY(window_decode), ENTRY(shared_prefix_decode),
+PyMethodDef methods[] = {ENTRY(assign_pages), ENTRY(cache_store), ENTRY(cache_load), ENTRY(prompt_attention),
+                         ENTRY(window_decode), ENTRY(shared_prefix_decode),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mla_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -504,8 +504,8 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
 // shared out over as many CTAs as there are SMs for it, up to 16, while each has 512
 // keys of an average sequence (the lengths are on the device): a run less than that
 // is worth its merge.  Measured (us, one run / shared out): 1 sequence x 16 heads, 512
-// queries behind 8192 keys 138 / 69, behind 32768 491 / 188, 1 query behind 8192 120
-// / 36; 200 queries of one head 138 / 28; but 256 behind 256 keys, 2 sequences x 16
+// queries behind 8192 keys 138 / 59, behind 32768 491 / 148, 1 query behind 8192 120
+// / 35; 200 queries of one head 138 / 28; but 256 behind 256 keys, 2 sequences x 16
 // heads, 21.6 / 27.8.
 struct PromptLayout {
   int blocks, planned, splits;

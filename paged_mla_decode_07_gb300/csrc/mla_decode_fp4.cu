@@ -28,8 +28,8 @@
 //
 // What bounds it: not memory (64 x 16 rows over 2048 to 16384 keys take 73 us, 3.2
 // TB/s, where the rows' bytes take 35) but the chain of a tile through its buffer,
-// 3.3k cycles a tile: stores of the values, products of S, softmax, products of O,
-// the next values.  In it the products (1540 cycles of operand reads at the 128
+// 3.3k cycles a tile (32 rows: 4.5k): stores of the values, products of S, softmax,
+// products of O, the next values.  In it the products (1540 cycles of operand reads at the 128
 // bytes a clock of shared memory) and the stores share that bandwidth, ~3000 cycles
 // of it a tile.  More buffers have no room (a tile of E5M2 values is 64 KB); the
 // same tiles in bf16 would be twice that and twice the operand traffic.  Measured
@@ -38,7 +38,12 @@
 // steps); roles with eight conversion warps 122, products of S and O from one warp in
 // whichever order is ready 124, maxima exchanged in raised tiles alone 115, sixteen
 // conversion warps, P by rows and a warp each for S and O 87, values held in
-// registers until their buffer is free 83, row sums by lanes 81 (cold caches).
+// registers until their buffer is free 83, row sums by lanes 81 (cold caches).  32
+// rows (32 x 128 rows over 1001 to 8191 keys): 157, with the same steps 101, waits that
+// end early first and L2 brought in behind the first pages 97 (92 in a row of calls).
+// Not kept there: two pages of codes at once in runs of 32 tokens, one RoPE buffer and
+// a page held as codes, which shorten the chain to 4.0k and spill (91; 128 x 16 rows of
+// a window 87 for 86); in runs of 16 tokens the copies bound it (114).
 //
 // Every wait is bounded (watchdog); after one that ran out every role leaves,
 // copies and products are drained and the tensor memory is freed.

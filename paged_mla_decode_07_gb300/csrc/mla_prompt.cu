@@ -20,13 +20,23 @@
 // Bound by the tensor pipe: 20 MMAs of 64 cycles for 128 x 128 pairs of a head,
 // 10.5 MFLOP in 1280 cycles, and by the chain of a half: products of S (780 cycles
 // and ~150 of latency), softmax (1380), products of O (520 and ~250).  16384 tokens
-// x 16 heads take 835 to 870 us, 1580 to 1650 TFLOP/s: 84 to 87 % of the library's
-// bf16 rate in bursts, 97 % of its sustained one (tensor pipe active 70.5 %).  128
-// heads of their own keys are bound by memory: no two of the 152 items that run at
-// a time share keys (5.4 TB/s).  On the way: products from one warp 1242 TFLOP/s,
-// from a warp each for S and O 1281, all of a tile's from one election with 32-bit
-// descriptors 1429, the wait for O's products last 1573, Q of each half reloaded on
-// its own 1619.
+// x 16 heads take 825 to 860 us, 1600 to 1670 TFLOP/s: 85 to 88 % of the library's
+// bf16 rate in bursts, 97 % of its sustained one (tensor pipe active 70.5 %).  On the
+// way: products from one warp 1242 TFLOP/s, from a warp each for S and O 1281, all of
+// a tile's from one election with 32-bit descriptors 1429, the wait for O's products
+// last 1573, Q of each half reloaded on its own 1619.
+//
+// Short prompts are bound by what lies between two items of a CTA, which is code
+// that runs once an item, at the rate that its instructions are fetched (the roles
+// of 12 warps do not fit the first caches): 32 prompts of 256 rows x 128 heads took
+// 207 us, with a loop over the results 194, waits of half the length, masks from bits
+// and the sign of the scale in the products 189, the products of O and the loads of Q
+// written once for both halves 185 (not those of S: 16384 tokens 830 -> 925).  5
+// prompts of 333 to 4096 rows x 128 heads take 1085 us, 955 where 16 heads share
+// their keys: no two of the 152 items that run at a time do otherwise, and 6 GB come
+// from memory.  Not kept there: keys and values brought into L2 one to four tiles
+// ahead (1120 to 1160), heads in groups whose keys fit L2 (1232), results transposed
+// in registers to store whole lines (32 x 256 rows: 202).
 //
 // Persistent: the plan kernel sorts the blocks of 256 rows of all sequences by
 // their number of key tiles, the CTAs take items from that list, longest first,
