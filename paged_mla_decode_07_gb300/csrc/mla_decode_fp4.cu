@@ -40,7 +40,8 @@
 // conversion warps, P by rows and a warp each for S and O 87, values held in
 // registers until their buffer is free 83, row sums by lanes 81 (cold caches).  32
 // rows (32 x 128 rows over 1001 to 8191 keys): 157, with the same steps 101, waits that
-// end early first and L2 brought in behind the first pages 97 (92 in a row of calls).
+// end early first and L2 brought in behind the first pages 97 (92 in a row of calls),
+// four pages ahead at once for one page six ahead 91.
 // Not kept there: two pages of codes at once in runs of 32 tokens, one RoPE buffer and
 // a page held as codes, which shorten the chain to 4.0k and spill (91; 128 x 16 rows of
 // a window 87 for 86); in runs of 16 tokens the copies bound it (114).
@@ -66,7 +67,7 @@ constexpr int kThreads = 32 * (4 + kConvWarps + kSoftWarps);
 constexpr uint32_t kLaunchRegs = 72;
 constexpr int kFactors = 4;  // segments whose score factors are kept
 constexpr int kFlags = 4;    // tiles whose page states are kept
-constexpr int kAhead = 6;    // pages brought into L2 ahead of their copy
+constexpr int kAhead = 4;    // pages brought into L2 ahead of their copy
 
 template <int R>
 struct Cfg {
@@ -268,7 +269,7 @@ __device__ void copy_codes(const CUtensorMap* tm, const DecodeParams& p, const R
     Segment s;
     if (!rg.get(p, prob, s)) continue;
     int ids = -1, next = page_id(p, s, s.pb + lane);  // of 32 pages from j0 on, and of the 32 behind them
-    int j0 = s.pb - 32;
+    int j0 = s.pb - 32, far = 0;  // far: the first page that has not been brought into L2
 #pragma unroll 1
     for (int j = s.pb; j < s.pe; ++j, ++u) {
       if (j - j0 == 32) {
@@ -286,14 +287,18 @@ __device__ void copy_codes(const CUtensorMap* tm, const DecodeParams& p, const R
           tma_load_2d(smem + C::kRawOff + slot * kRawBytes, tm, bars.raw_full + slot, 0, id * kPageSize, pol);
       }
       __syncwarp();
-      // page j + kAhead into L2 (64 pages are known from j0 on); a segment's first pages come as they are copied
-      const int at = j - j0 + kAhead;
-      const int far = at < 32 ? __shfl_sync(0xffffffffu, ids, at) : __shfl_sync(0xffffffffu, next, at - 32);
-      if (lane == 0 && far >= 0 && u >= C::kRaw)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                         p.kv_fp8 + static_cast<int64_t>(far) * (kPageSize * kFp4RowBytes)),
-                     "r"(kPageSize * kFp4RowBytes)
-                     : "memory");
+      // pages up to j + kAhead into L2 (64 are known from j0 on), the first ones behind the copies of a whole ring
+      if (u >= C::kRaw - 1) {
+        const int page = max(far, j + 1) + lane, at = page - j0;
+        const int low = __shfl_sync(0xffffffffu, ids, at & 31), high = __shfl_sync(0xffffffffu, next, at & 31);
+        const int ahead = at < 32 ? low : high;
+        if (page <= j + kAhead && ahead >= 0)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                           p.kv_fp8 + static_cast<int64_t>(ahead) * (kPageSize * kFp4RowBytes)),
+                       "r"(kPageSize * kFp4RowBytes)
+                       : "memory");
+        far = j + kAhead + 1;
+      }
     }
   }
 out:
