@@ -122,6 +122,18 @@ def test_many_sequences(n):
     compare(inputs(2, 2, lens, seed=n), f"{n} sequences")
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_items_without_keys_among_others(causal):
+    # several items per CTA, some of no tiles at all, some with tiles in one half alone
+    lens = [(130, 0), (1, 1), (257, 900), (0, 50), (300, 2), (256, 0), (100, 400)] * 12
+    compare(inputs(8, 4, lens, seed=15), "items without keys", causal=causal)
+
+
+@pytest.mark.parametrize("heads,lens", [(1, [(5, 4000)]), (16, [(300, 500)] * 20)])
+def test_negative_scales_of_long_and_of_many_items(heads, lens):
+    compare(inputs(heads, 1, lens, seed=16), f"{heads} heads, scale -0.1", scale=-0.1)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.1, 3.0, 1e-4])
 def test_scales(scale):
     # 3.0: scores of hundreds, one key takes all of a row; negative: the smallest product is the largest score
@@ -262,8 +274,9 @@ def test_workspaces_are_checked():
                              args[3].expand(-1, 2, -1), *args[4:], SCALE)
 
 
-def test_watchdog_reports_an_expired_wait():
-    args = inputs(2, 2, [(300, 300)], seed=12)
+@pytest.mark.parametrize("heads", [2, 128])  # (one item a CTA; items from a list)
+def test_watchdog_reports_an_expired_wait(heads):
+    args = inputs(heads, 2, [(300, 300)], seed=12)
     from gpu_helpers import env
     with env(MLA_WATCHDOG_NS=20_000_000), overrides(debug_stall=True):
         mla.prompt_attention(*args, SCALE)
