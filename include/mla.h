@@ -342,11 +342,11 @@ mla_status mla_cache_load(const mla_cache_load_args* args, mla_stream_t stream);
  * (a window of 2^30 or more sees every key: causal decode over the whole cache),
  * with its rules for missing pages and sizes.  Latent values and their products
  * with q are exact (q to 2^-18 of the largest value of its row), sums fp32, and
- * probabilities are rounded to a relative 2^-9 (those under 2^-18 of the row's
- * largest to 2^-25 of that).  The RoPE values of a key that
- * some query token sees must be finite, or rows of its element are not.  A row
- * of q that is not finite has results that are not, other rows are as they
- * would be.  All launches are made on `stream` by the one call. */
+ * a probability is off by the larger of 2^-9 of itself and 2^-33 of the row's
+ * largest (of n keys that far below it out may so lose n * 2^-33 of their mean
+ * |v|; lse does not).  The RoPE values of a key that some query token sees must
+ * be finite, or rows of its element are not.  A row of q that is not finite has
+ * results that are not, other rows are as they would be.  All launches are made on `stream` by the one call. */
 typedef struct {
   const void* q;                  /* bf16 [batch, s_q, h_q, 576], 16-byte aligned */
   int batch, s_q, h_q;            /* s_q * h_q <= 1024 */

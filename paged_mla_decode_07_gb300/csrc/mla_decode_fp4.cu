@@ -7,9 +7,12 @@
 //   q (bf16, 8 significant bits), times a power of two that puts the row's
 //     largest value into [128, 256): hi = E4M3(q), lo = E4M3(q - hi).  Exact for
 //     values down to 2^-9 of that largest one, off by 2^-18 of it below.
-//   P (fp32): three E5M2 terms of P * 2^8, each of what the last one left:
-//     relative 2^-9 (what rounding to bf16 gives) down to P = 2^-18, and some of
-//     it down to 2^-25: the weights of many keys far below the largest are kept.
+//   P (fp32): three E5M2 terms of P * 2^8, each of what the last one left, times
+//     16 more (E5M2 leaves an eighth at most): off by the larger of 2^-9 of
+//     itself (what rounding to bf16 gives) and 2^-33 of the row's largest.  The
+//     sum l has P itself, so what the terms lost would be missing from O alone:
+//     with one factor for the three weights under 2^-25 were 0 in O, 2.5 % of a
+//     row that has 2^20 such keys behind one large one.
 // The terms stand beside each other as columns of one MMA (N = 2 R and 3 R for R
 // = 16 or 32 query rows, where N up to 64 costs the same time as 16) and are
 // added in fp32 after it.
@@ -109,6 +112,7 @@ struct Cfg {
   static_assert(kMaxCluster * (R + 1) * 4 <= kPBytes, "weights of a cluster's merge, in P's place");
 };
 constexpr float kPLog2 = 8.f;      // P is held at 2^8 times its value, 2^15 at most
+constexpr float kPStep = 16.f;     // and its second and third term at 16 times what the one before left: 2^11 of 2^15
 constexpr float kRescale = 7.f;    // log2 units that a score may pass the reference by before it is raised
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr uint32_t kHalfBar = 1;   // named barriers of the softmax warps of a half of the rows
@@ -727,8 +731,8 @@ __device__ void softmax(const DecodeParams& p, const Range& rg, int g, int part,
           code[r / 2] = e5m2x2(y[r], y[r + 1]);
           if (term < 2) {
             const uint32_t h2 = e5m2x2_to_f16x2(code[r / 2]);
-            y[r] -= f16x2_half_to_f32(h2, 0);
-            y[r + 1] -= f16x2_half_to_f32(h2, 1);
+            y[r] = (y[r] - f16x2_half_to_f32(h2, 0)) * kPStep;
+            y[r + 1] = (y[r + 1] - f16x2_half_to_f32(h2, 1)) * kPStep;
           }
         }
         const uint32_t at = pt + term * (R / 16) * 2048;
@@ -799,7 +803,7 @@ __device__ void softmax(const DecodeParams& p, const Range& rg, int g, int part,
         tmem_ld(col + 2 * R, z);
         tmem_ld_wait();
 #pragma unroll
-        for (int r = 0; r < N; ++r) o[r] = (o[r] + (a[r] + z[r])) * inv[r];
+        for (int r = 0; r < N; ++r) o[r] = fmaf(fmaf(z[r], 1.f / kPStep, a[r]), 1.f / kPStep, o[r]) * inv[r];
       }
       if (c == 3) {
         tc_fence_before();
