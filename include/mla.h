@@ -341,7 +341,7 @@ mla_status mla_cache_load(const mla_cache_load_args* args, mla_stream_t stream);
 /* Windowed decode over FP4 rows: mla_window_decode's keys, masks and results
  * (a window of 2^30 or more sees every key: causal decode over the whole cache),
  * with its rules for missing pages and sizes.  Latent values and their products
- * with q are exact (q to 2^-18 of the largest value of its row), sums fp32, and
+ * with q are exact (q to 2^-21 of the largest value of its row), sums fp32, and
  * a probability is off by the larger of 2^-9 of itself and 2^-33 of the row's
  * largest (of n keys that far below it out may so lose n * 2^-33 of their mean
  * |v|; lse does not).  The RoPE values of a key that some query token sees must

@@ -5,8 +5,8 @@
 // and half the operand traffic of bf16 ones.  The other operands are split into
 // 8-bit terms:
 //   q (bf16, 8 significant bits), times a power of two that puts the row's
-//     largest value into [128, 256): hi = E4M3(q), lo = E4M3(q - hi).  Exact for
-//     values down to 2^-9 of that largest one, off by 2^-18 of it below.
+//     largest value into [128, 256): hi = E4M3(q), lo = E4M3(16 (q - hi)).  Exact
+//     for values down to 2^-14 of that largest one, off by 2^-21 of it below.
 //   P (fp32): three E5M2 terms of P * 2^8, each of what the last one left, times
 //     16 more (E5M2 leaves an eighth at most): off by the larger of 2^-9 of
 //     itself (what rounding to bf16 gives) and 2^-33 of the row's largest.  The
@@ -113,6 +113,7 @@ struct Cfg {
 };
 constexpr float kPLog2 = 8.f;      // P is held at 2^8 times its value, 2^15 at most
 constexpr float kPStep = 16.f;     // and its second and third term at 16 times what the one before left: 2^11 of 2^15
+constexpr float kQStep = 16.f;     // the second term of q is held at 16 times what the first left (8 of 256 at most)
 constexpr float kRescale = 7.f;    // log2 units that a score may pass the reference by before it is raised
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr uint32_t kHalfBar = 1;   // named barriers of the softmax warps of a half of the rows
@@ -401,7 +402,7 @@ __device__ __forceinline__ void load_queries(const __nv_bfloat16* q, const Decod
         const float x0 = lo_of(x) * up, x1 = hi_of(x) * up;
         h[n] = e4m3x2(x0, x1);
         const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(h[n]));
-        l[n] = e4m3x2(x0 - f16x2_half_to_f32(f, 0), x1 - f16x2_half_to_f32(f, 1));
+        l[n] = e4m3x2((x0 - f16x2_half_to_f32(f, 0)) * kQStep, (x1 - f16x2_half_to_f32(f, 1)) * kQStep);
       }
       hi[i] = h[0] | (h[1] << 16);
       lo[i] = l[0] | (l[1] << 16);
@@ -648,7 +649,7 @@ __device__ void softmax(const DecodeParams& p, const Range& rg, int g, int part,
         tmem_ld(taddr + C::kSCol + 2 * R * b + R + N * half, lo);
         tmem_ld_wait();
 #pragma unroll
-        for (int r = 0; r < N; ++r) y[r] = fmaf(y[r] + lo[r], f[r], down[r]);
+        for (int r = 0; r < N; ++r) y[r] = fmaf(fmaf(lo[r], 1.f / kQStep, y[r]), f[r], down[r]);
       }
       const int jp = j + (quarter >> 1);
       const bool real = states[2 * (i % kFlags) + (quarter >> 1)] != 0;

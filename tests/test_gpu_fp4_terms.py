@@ -1,4 +1,5 @@
-"""Decode over FP4 rows: what its 8-bit terms hold of the weights, where one key has nearly all of a row's."""
+"""Decode over FP4 rows: what its 8-bit terms hold of the weights and of q, where one key has nearly all of a
+row's weight and where a row of q has values far below its largest."""
 import math
 
 import pytest
@@ -47,3 +48,30 @@ def test_many_small_weights_under_one_large_one(h_q, pages):
     assert (worst <= 1.0).all(), f"error by gap, of the bound: {worst.tolist()}"
     # (the scale's own rounding: 2^-23 of a gap)
     assert ((lse[0, 0].double() - (gaps.double() + torch.log2(total))).abs() <= 2.0 ** -12).all()
+
+
+@pytest.mark.parametrize("h_q", [16, 32])
+@pytest.mark.parametrize("size", [-40, 0, 30])
+def test_queries_far_below_their_rows_largest(h_q, size):
+    """A row of q whose largest value is a power of two that meets zeros, the others 2^-10 of it with their last
+    bit set: one key's score is 511 times that value."""
+    latent = torch.ones(PAGE, 512, device="cuda", dtype=torch.bfloat16)
+    latent[:, 0] = 0.0
+    kv = cache(latent, torch.zeros(PAGE, 64, device="cuda", dtype=torch.bfloat16))
+    q = torch.zeros(1, 1, h_q, 576, device="cuda", dtype=torch.bfloat16)
+    small = 2.0 ** size * torch.tensor([2.0 ** -e * (1 + odd * 2.0 ** -7) for e in (7, 8, 9, 10, 11, 12, 13, 14)
+                                        for odd in (1, 127)], device="cuda", dtype=torch.float64)
+    small = small.repeat(h_q // 16)
+    q[0, 0, :, :512] = small[:, None].to(torch.bfloat16)
+    q[0, 0, :, 0] = 2.0 ** size
+    assert torch.equal(q[0, 0, :, 1].double(), small)
+    scale = 2.0 ** -size
+    out, lse = mla.window_decode(q, kv, i32([[0]]), i32([1]), scale, window=ALL)
+    assert mla.device_status() == 0
+    want = 511 * small * scale / math.log(2.0)
+    # q is off by 2^-21 of its row's largest value, each of the 511 by as much; fp32 sums.  lse is made of the
+    # score less 8 and of log2(2^8): a score of less than 4 is rounded to the step of numbers up to 8 in
+    # the difference, 2^-21, by half of it at most, and lse is rounded from the two as far again: 2^-21 in all
+    # (the row of 2^-14 * (1 + 127 / 128) has every one of its values off by the whole 2^-21, on one side).
+    bound = 511 * 2.0 ** -21 / math.log(2.0) + 2.0 ** -20 * want + 2.0 ** -21
+    assert ((lse[0, 0].double() - want).abs() <= bound).all(), ((lse[0, 0].double() - want).abs() / bound).tolist()
