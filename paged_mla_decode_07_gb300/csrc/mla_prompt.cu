@@ -799,10 +799,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int per = (p.batch + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+  // Offsets that decrease may name more blocks than the list has room for, and more than
+  // 32 bits hold (16384 sequences of 2^26 rows and of none in turn: 2^31): sums of threads
+  // and of warps stop one past the room, so that none of the 32 that are added passes 2^29.
+  const int past = p.max_blocks + 1;
   int mine = 0;
   for (int b = b0; b < b1; ++b) {
     first[b] = mine;
-    mine += Sequence(p, b).blocks();
+    mine = min(mine + Sequence(p, b).blocks(), past);
   }
   int x = mine;
 #pragma unroll
@@ -810,7 +814,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
     const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) warp_sum[warp] = x;
+  if (lane == 31) warp_sum[warp] = min(x, past);
   if (tid == 0) most = 0;
   classes[tid] = 0;
   __syncthreads();
@@ -829,7 +833,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PromptParams p
   int total = warp_sum[31];
   if (tid == 0) first[p.batch] = total;
   __syncthreads();
-  // (offsets that decrease may name more blocks than the list has room for)
   if (total > p.max_blocks) {
     if (tid == 0) atomicOr(p.status, MLA_DEVICE_BAD_SCHEDULE);
     total = 0;
