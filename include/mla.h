@@ -390,7 +390,7 @@ mla_status mla_fp4_decode(const mla_fp4_decode_args* args, mla_stream_t stream);
 typedef struct {
   const void* q;                  /* bf16 [num_q, h_q, 192], 16-byte aligned (as k_nope, k_rope and v) */
   int64_t q_stride, q_head_stride;
-  int num_q, h_q;                 /* num_q = 0: nothing is launched */
+  int num_q, h_q;                 /* num_q = 0: nothing is launched; num_q, num_k <= 2^31 - 512 */
   const void* k_nope;             /* bf16 [num_k, h_kv, 128] */
   int64_t k_nope_stride, k_nope_head_stride;
   const void* k_rope;             /* bf16 [num_k, 64] */

@@ -514,6 +514,10 @@ struct PromptLayout {
 mla_status prompt_layout(int num_q, int num_k, int h_q, int batch, PromptLayout* L) {
   if (num_q < 0) return fail(MLA_ERR_INVALID_ARG, "num_q must be >= 0 (got %d)", num_q);
   if (num_k < 0) return fail(MLA_ERR_INVALID_ARG, "num_k must be >= 0 (got %d)", num_k);
+  // (the kernels round rows up to blocks of 256 and keys up to tiles of 128 in 32 bits)
+  constexpr int kMostRows = INT32_MAX - 511;
+  if (num_q > kMostRows) return fail(MLA_ERR_UNSUPPORTED, "num_q = %d exceeds the supported %d rows", num_q, kMostRows);
+  if (num_k > kMostRows) return fail(MLA_ERR_UNSUPPORTED, "num_k = %d exceeds the supported %d rows", num_k, kMostRows);
   if (h_q < 1) return fail(MLA_ERR_INVALID_ARG, "h_q must be >= 1 (got %d)", h_q);
   if (h_q > 1024) return fail(MLA_ERR_UNSUPPORTED, "h_q = %d exceeds 1024", h_q);
   if (batch < 1) return fail(MLA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
