@@ -86,6 +86,27 @@ mla_status device_info(uint32_t** status, int* sm_count, int* pair_capacity = nu
   return MLA_OK;
 }
 
+// Readies a kernel on the current device, once.
+enum Ready { kReadyFp4Rows16, kReadyFp4Rows32, kReadyPrompt, kReadyKinds };
+bool g_ready[kMaxDevices][kReadyKinds];
+
+mla_status make_ready(Ready kind) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev < 0 || dev >= kMaxDevices) return fail(MLA_ERR_UNSUPPORTED, "device ordinal %d too large", dev);
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_ready[dev][kind]) return MLA_OK;
+  KernelRegs regs{};
+  e = kind == kReadyPrompt ? ready_prompt(&regs) : ready_decode_fp4(kind == kReadyFp4Rows16 ? 16 : 32, &regs);
+  if (e != cudaSuccess) return cuda_fail(e, kind == kReadyPrompt ? "prompt attention setup" : "FP4 decode setup");
+  if (regs.have != regs.want)
+    return fail(MLA_ERR_CUDA, "%s was compiled with %d registers a thread, its register split is for %d", regs.kernel,
+                regs.have, regs.want);
+  g_ready[dev][kind] = true;
+  return MLA_OK;
+}
+
 // The CTA-pair decode kernel for problems of more than 64 rows, dense over
 // the bf16 cache or sparse over FP8 or bf16 rows (mla_decode_pair.cu).
 constexpr bool kPairDecode = true;
@@ -1253,6 +1274,8 @@ mla_status mla_fp4_decode(const mla_fp4_decode_args* a, mla_stream_t stream) {
   p.debug_stall = g_test_debug_stall.load();
   p.scale_log2 = a->sm_scale * 1.4426950408889634f;
   p.cluster = window_cluster(g, pages, clusters);
+  st = make_ready(g.rpc == 16 ? kReadyFp4Rows16 : kReadyFp4Rows32);
+  if (st != MLA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CUtensorMap tm_codes, tm_rope;
   const long long cache_rows = static_cast<long long>(a->num_pages) * kPageSize;
@@ -1325,6 +1348,8 @@ mla_status mla_prompt_attention(const mla_prompt_attention_args* a, mla_stream_t
   memset(&p, 0, sizeof p);
   int sms = 0;
   st = device_info(&p.status, &sms);
+  if (st != MLA_OK) return st;
+  st = make_ready(kReadyPrompt);
   if (st != MLA_OK) return st;
   CUtensorMap tm_q, tm_k_nope, tm_k_rope, tm_v;
   // (without keys no copy is made: their maps name q)

@@ -931,13 +931,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int R>
 cudaError_t launch(const CUtensorMap& tm_codes, const CUtensorMap& tm_rope, const void* q, const DecodeParams& p,
                    cudaStream_t stream) {
-  auto kern = fp4_decode_kernel<R>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.cluster > 0 ? p.cluster * p.num_problems : p.num_parts) * p.row_groups);
   cfg.blockDim = dim3(kThreads);
@@ -952,7 +945,18 @@ cudaError_t launch(const CUtensorMap& tm_codes, const CUtensorMap& tm_rope, cons
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_rope, static_cast<const __nv_bfloat16*>(q), p);
+  return cudaLaunchKernelEx(&cfg, fp4_decode_kernel<R>, tm_codes, tm_rope, static_cast<const __nv_bfloat16*>(q), p);
+}
+
+template <int R>
+cudaError_t ready(KernelRegs* regs) {
+  auto kern = fp4_decode_kernel<R>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e == cudaSuccess) *regs = KernelRegs{R == 16 ? "fp4_decode_kernel<16>" : "fp4_decode_kernel<32>", fa.numRegs, kLaunchRegs};
+  return e;
 }
 
 }  // namespace
@@ -961,5 +965,7 @@ cudaError_t launch_decode_fp4(const CUtensorMap& tm_codes, const CUtensorMap& tm
                               int rpc, cudaStream_t stream) {
   return rpc == 16 ? launch<16>(tm_codes, tm_rope, q, p, stream) : launch<32>(tm_codes, tm_rope, q, p, stream);
 }
+
+cudaError_t ready_decode_fp4(int rpc, KernelRegs* regs) { return rpc == 16 ? ready<16>(regs) : ready<32>(regs); }
 
 }  // namespace mla

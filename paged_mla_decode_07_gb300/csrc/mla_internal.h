@@ -286,6 +286,14 @@ cudaError_t allow_dynamic_smem(Kernel* kernel, size_t bytes, size_t own) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost - own));
 }
 
+// What a kernel that hands registers from warp to warp was compiled with, and what
+// its split is for (setmaxnreg waits for ever for more than there are).  Read, and the
+// kernel's shared memory allowed, once per device, before its first launch there.
+struct KernelRegs {
+  const char* kernel;
+  int have, want;
+};
+
 // Kernel launchers (defined in the .cu files); return a CUDA error code.
 cudaError_t launch_metadata(const int32_t* cache_seqlens, int s_q, int topk, const Geometry& g, int32_t* sched,
                             int32_t* num_splits, cudaStream_t stream);
@@ -295,8 +303,10 @@ cudaError_t launch_decode_rows(const CUtensorMap& tm_kv, const void* q, const De
                                cudaStream_t stream);
 // Windowed decode over FP4 rows (mla_decode_fp4.cu)
 // (tm_codes: codes and scales of a page as one box, tm_rope: its RoPE values; rpc: 16 or 32 rows per CTA)
+// (the current device has had ready_decode_fp4)
 cudaError_t launch_decode_fp4(const CUtensorMap& tm_codes, const CUtensorMap& tm_rope, const void* q, const DecodeParams& p,
                               int rpc, cudaStream_t stream);
+cudaError_t ready_decode_fp4(int rpc, KernelRegs* regs);
 // mode: 0 dense bf16 cache, 1 sparse FP8 cache, 2 dense FP8 cache, 3 sparse bf16 rows, 4 and 5 windowed dense
 // over the bf16 and the FP8 cache
 cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const DecodeParams& p, int rpc,
@@ -330,8 +340,10 @@ cudaError_t launch_fp8_cache_store(const uint16_t* x, int num_tokens, const int3
                                    int sm_count, cudaStream_t stream);
 cudaError_t launch_slot_store(const SlotStoreParams& p, int sm_count, cudaStream_t stream);
 // (tm_q, tm_k_nope, tm_v: boxes of 64 values of one head of 128 rows; tm_k_rope: of 128 rows)
+// (the current device has had ready_prompt)
 cudaError_t launch_prompt(const CUtensorMap& tm_q, const CUtensorMap& tm_k_nope, const CUtensorMap& tm_k_rope,
                           const CUtensorMap& tm_v, const PromptParams& p, int sm_count, cudaStream_t stream);
+cudaError_t ready_prompt(KernelRegs* regs);
 cudaError_t launch_cache_load(const CacheLoadParams& p, int sm_count, cudaStream_t stream);
 // in_place: the lengths or the cursor are updated in the arrays they are read from
 cudaError_t launch_assign_pages(const AssignPagesParams& p, bool in_place, int sm_count, cudaStream_t stream);

@@ -912,14 +912,7 @@ cudaError_t launch_prompt(const CUtensorMap& tm_q, const CUtensorMap& tm_k_nope,
                           const CUtensorMap& tm_v, const PromptParams& p, int sm_count, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(p.max_blocks) * p.h_q;
   const size_t scratch = (static_cast<size_t>(p.batch) + 1) * sizeof(int);
-  cudaError_t e = allow_dynamic_smem(plan_kernel, scratch, 8192);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, prompt_kernel);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -943,6 +936,17 @@ cudaError_t launch_prompt(const CUtensorMap& tm_q, const CUtensorMap& tm_k_nope,
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, prompt_merge_kernel, p);
+}
+
+cudaError_t ready_prompt(KernelRegs* regs) {
+  cudaError_t e = allow_dynamic_smem(plan_kernel, (kMaxProblems + 1) * sizeof(int), 8192);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, prompt_kernel);
+  if (e == cudaSuccess) *regs = KernelRegs{"prompt_kernel", fa.numRegs, kLaunchRegs};
+  return e;
 }
 
 }  // namespace mla
