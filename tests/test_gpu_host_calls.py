@@ -47,3 +47,15 @@ def test_prompt_attention_asks_for_no_attributes(heads, launches):
     rope = torch.zeros(10, 64, device="cuda", dtype=torch.bfloat16)
     off = i32([0, 10])
     checked(runtime_calls(lambda: mla.prompt_attention(q, k, rope, k, off, off, 0.1)), launches)
+
+
+@pytest.mark.parametrize("batch,h_q,keys,window,launches", [
+    (100, 16, 600, 512, 1), (4, 16, 2100, 2048, 1), (30, 128, 1100, 1024, 1),  # on clusters
+    (16, 16, 4200, 4096, 2), (2, 256, 4200, 4096, 2), (200, 16, 600, 512, 2)])  # a schedule and a merge
+def test_fp4_decode_takes_the_side_that_was_measured_faster(batch, h_q, keys, window, launches):
+    pages = -(-keys // 64)
+    q = torch.zeros(batch, 1, h_q, 576, device="cuda", dtype=torch.bfloat16)
+    kv = torch.zeros(pages, 64, 1, 400, device="cuda", dtype=torch.uint8)
+    table, lens = torch.arange(pages, device="cuda", dtype=torch.int32).repeat(batch, 1), i32([keys] * batch)
+    names = runtime_calls(lambda: mla.window_decode(q, kv, table, lens, 0.1, window=window))
+    checked(names, 4 * launches)
