@@ -376,9 +376,9 @@ int largest_cluster(const Geometry& g, long long pages, const int* capacity) {
 // CTAs of the cluster that each problem of a windowed call is given on the
 // single-CTA kernels (mla_cluster.cuh), or 0 for a schedule over all SMs with a
 // merge kernel behind it.  A cluster is taken when all of them are resident at
-// once and the longest problem's share is at most `slack` pages more than an even
+// once and the longest problem's share is at most three pages more than an even
 // share of all pages: about what a schedule costs, its segments that start and
-// end inside a problem, and the merge.  The kernels over bf16 and FP8 rows: three.  Measured (us, cluster against schedule,
+// end inside a problem, and the merge.  Measured (us, cluster against schedule,
 // replayed, pages not in L2): the register-level kernel, 16 rows, bf16, windows
 // of 512: 4 elements 11.9 / 13.8, 60 18.9 / 23.6, 150 29.6 / 35.3; of 2048: 34
 // 26.3 / 29.4, but 16 elements 24.4 / 22.5 and 100 69.8 / 58.8; FP8, windows of
@@ -388,10 +388,10 @@ int largest_cluster(const Geometry& g, long long pages, const int* capacity) {
 // 128 to 4096) the side taken is within 5 % of the better one in all but 15; worst
 // 19 % (4 x 16 rows x 2048 keys of bf16: schedule 20.7, cluster 17.3) and 16 % the
 // other way (16 x 64 rows x 1024 keys of FP8: cluster 30.6, schedule 26.2).
-int window_cluster(const Geometry& g, long long pages, const int* capacity, long long slack = 3) {
+int window_cluster(const Geometry& g, long long pages, const int* capacity) {
   const int n = largest_cluster(g, pages, capacity);
   const long long units = static_cast<long long>(g.num_problems) * g.row_groups;
-  return pages * g.sm_count <= (pages * units + slack * g.sm_count) * n ? n : 0;
+  return pages * g.sm_count <= (pages * units + 3ll * g.sm_count) * n ? n : 0;
 }
 
 // Pages of all problems of a schedule that a call may have: the sums of a
@@ -420,22 +420,32 @@ mla_status window_layout(int batch, int h_q, int s_q, int is_fp8, long long page
   return MLA_OK;
 }
 
+// CTAs of a problem's cluster over FP4 rows, as window_cluster gives them for the other
+// kernels: taken where the longest problem's share is at most eight pages more than four
+// fifths of an even share.  Eight: a page here is a third of a bf16 one's bytes and half
+// a tile.  Four fifths: the even share is that of problems which are all as long as one
+// can be, and where lengths differ the schedule has less than that for each SM.  Measured
+// (us, cluster against schedule, replayed, pages not in L2): 16 rows, windows of 512, 4
+// elements 12.7 / 15.0, 100 20.1 / 25.5; of 4096, 16 25.7 / 23.4; 32 elements of 1001 to
+// 8191 keys 38.5 / 30.4; 128 rows, 16 windows of 512 20.1 / 28.6, 30 of 1024 34.7 / 39.1, 38
+// elements of 1 to 16384 keys 280 / 152; 256 rows, 2 of 4096 31.9 / 26.5.  Of 579 such calls
+// (8 to 256 rows, 1 to 150 elements, even and ragged lengths up to 16384) the side taken is
+// within 5 % of the better one in all but 28 (with three pages and a whole share in all but
+// 123, the worst at 1.85 times); worst 23 % (76 elements x 32 rows of 1 to 4096 keys: cluster
+// 53.1, schedule 43.2).  The capacity that is asked of another kernel is this one's too (76,
+// 36 and 15 clusters of 2, 4 and 8: one CTA an SM).
+int fp4_cluster(const Geometry& g, long long pages, const int* capacity) {
+  const int n = largest_cluster(g, pages, capacity);
+  const long long units = static_cast<long long>(g.num_problems) * g.row_groups;
+  return 5 * pages * g.sm_count <= (4 * pages * units + 5 * 8ll * g.sm_count) * n ? n : 0;
+}
+
 // Windowed decode over FP4 rows: 16 or 32 query rows a CTA, tiles of 128 keys.  A
 // segment's start and end cost about two tiles, for either number of rows (us at 0 /
 // 4 / 8 / 16 / 32 quarters of a 64-key tile: 64 x 16 rows of 2048 to 16384 keys 75.6 /
 // 72.2 / 72.5 / 74.4 / 76.6, 200 x 16 in windows of 1000 49.7 / 47.0 / 45.9 / 47.3 / 48.0,
 // 32 x 128 rows 97.1 / 93.6 / 94.7 / 95.1 / 102.3, 48 x 256 in windows of 1000 89.3 / 85.5
 // / 84.1 / 83.8 / 90.0, 40 x 60 rows 60.9 / 51.1 / 48.0 / 50.2 / 53.8).
-// A cluster is taken up to eight pages past an even share (window_cluster): a page is a
-// third of a bf16 one's bytes and half a tile.  Measured (us, cluster against schedule,
-// replayed, pages not in L2): 16 rows, windows of 512, 4 elements 12.7 / 15.0, 100 20.1 /
-// 25.5; of 2048, 4 15.5 / 18.1, 16 18.6 / 18.7; of 4096, 16 25.7 / 23.4; 128 rows, 16 of 512
-// 20.1 / 28.6, 30 of 1024 34.7 / 39.1; 256 rows, 2 of 4096 31.9 / 26.5.  Of 375 such calls (8
-// to 256 rows, 1 to 150 elements of even and of ragged lengths) the side taken is within 5 %
-// of the better one in all but 16 (with three pages in all but 67); worst 33 % (75 elements x
-// 64 rows of 1 to 3000 keys: cluster 65.4, schedule 49.0).  The capacity that is asked of
-// another kernel is this one's too (76, 36 and 15 clusters of 2, 4 and 8: one CTA an SM).
-constexpr int kFp4ClusterSlack = 8;
 mla_status fp4_layout(int batch, int h_q, int s_q, Geometry* g, WindowLayout* L) {
   mla_status st = geometry(batch, h_q, s_q, 0, 0, g);
   if (st != MLA_OK) return st;
@@ -1288,7 +1298,7 @@ mla_status mla_fp4_decode(const mla_fp4_decode_args* a, mla_stream_t stream) {
   p.sinks = a->sinks;
   p.debug_stall = g_test_debug_stall.load();
   p.scale_log2 = a->sm_scale * 1.4426950408889634f;
-  p.cluster = window_cluster(g, pages, clusters, kFp4ClusterSlack);
+  p.cluster = fp4_cluster(g, pages, clusters);
   st = make_ready(g.rpc == 16 ? kReadyFp4Rows16 : kReadyFp4Rows32);
   if (st != MLA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -51,7 +51,8 @@ def test_prompt_attention_asks_for_no_attributes(heads, launches):
 
 @pytest.mark.parametrize("batch,h_q,keys,window,launches", [
     (100, 16, 600, 512, 1), (4, 16, 2100, 2048, 1), (30, 128, 1100, 1024, 1),  # on clusters
-    (16, 16, 4200, 4096, 2), (2, 256, 4200, 4096, 2), (200, 16, 600, 512, 2)])  # a schedule and a merge
+    (16, 16, 4200, 4096, 2), (2, 256, 4200, 4096, 2), (200, 16, 600, 512, 2), (32, 16, 8191, 1 << 30, 2),
+    (100, 16, 8191, 1 << 30, 2), (38, 128, 16384, 1 << 30, 2)])  # a schedule and a merge
 def test_fp4_decode_takes_the_side_that_was_measured_faster(batch, h_q, keys, window, launches):
     pages = -(-keys // 64)
     q = torch.zeros(batch, 1, h_q, 576, device="cuda", dtype=torch.bfloat16)
