@@ -552,7 +552,10 @@ mla_status prefix_layout(int batch, int h_q, int s_q, int prefix_pages, int is_f
 // is worth its merge.  Measured (us, one run / shared out): 1 sequence x 16 heads, 512
 // queries behind 8192 keys 138 / 59, behind 32768 491 / 148, 1 query behind 8192 120
 // / 35; 200 queries of one head 138 / 28; but 256 behind 256 keys, 2 sequences x 16
-// heads, 21.6 / 27.8.
+// heads, 21.6 / 27.8.  Every item has the same number of CTAs, so up to half of the SMs
+// have none (32 items: 128 of 152 work), and 256 rows, of which a sequence of one query
+// fills one: its products are those of 256 (512 queries behind 32768 keys are 1.6 times
+// their floor of 91 us, one query behind 8192 3.5 times its 10).
 struct PromptLayout {
   int blocks, planned, splits;
   size_t o_part, lse_part, total;  // (the list comes first)

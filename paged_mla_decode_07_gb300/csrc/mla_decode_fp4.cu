@@ -30,11 +30,13 @@
 // are handed on in pairs.
 //
 // What bounds it: not memory (64 x 16 rows over 2048 to 16384 keys take 73 us, 3.2
-// TB/s, where the rows' bytes take 35) but the chain of a tile through its buffer,
-// 3.3k cycles a tile (32 rows: 4.5k): stores of the values, products of S, softmax,
-// products of O, the next values.  In it the products (1540 cycles of operand reads at the 128
-// bytes a clock of shared memory) and the stores share that bandwidth, ~3000 cycles
-// of it a tile.  More buffers have no room (a tile of E5M2 values is 64 KB); the
+// TB/s, where the rows' bytes take 35) but 1.74 us for each of a CTA's 30 tiles (32
+// rows: 2.7), 14 us of start, end and merge of any call, and 4.6 us for each segment
+// behind a CTA's first (32 rows: 5; from calls of one, two and four equal segments a
+// CTA).  A tile's time is the chain through its buffer, 3.3k cycles (32 rows: 4.5k):
+// stores of the values, products of S, softmax, products of O, the next values.  In it
+// the products (1540 cycles of operand reads at the 128 bytes a clock of shared memory)
+// and the stores share that bandwidth, ~2800 cycles of it.  More buffers have no room (a tile of E5M2 values is 64 KB); the
 // same tiles in bf16 would be twice that and twice the operand traffic.  Measured
 // on the way (us, that call): all threads doing everything, two CTAs an SM, codes
 // prefetched in registers, 120 (the loads' scoreboards are those of the other
@@ -48,6 +50,8 @@
 // Not kept there: two pages of codes at once in runs of 32 tokens, one RoPE buffer and
 // a page held as codes, which shorten the chain to 4.0k and spill (91; 128 x 16 rows of
 // a window 87 for 86); in runs of 16 tokens the copies bound it (114).
+// With more than 32 rows every 32 of them convert and multiply a page again: 64 x 64
+// rows take 159 us, 64 x 128 rows 293, where the kernels over bf16 rows take 155 and 185.
 //
 // Every wait is bounded (watchdog); after one that ran out every role leaves,
 // copies and products are drained and the tensor memory is freed.
