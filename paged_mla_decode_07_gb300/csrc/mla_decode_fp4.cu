@@ -6,7 +6,7 @@
 // 8-bit terms:
 //   q (bf16, 8 significant bits), times a power of two that puts the row's
 //     largest value into [128, 256): hi = E4M3(q), lo = E4M3(16 (q - hi)).  Exact
-//     for values down to 2^-14 of that largest one, off by 2^-21 of it below.
+//     for values down to 2^-13 of that largest one, off by 2^-21 of it below.
 //   P (fp32): three E5M2 terms of P * 2^8, each of what the last one left, times
 //     16 more (E5M2 leaves an eighth at most): off by the larger of 2^-9 of
 //     itself (what rounding to bf16 gives) and 2^-33 of the row's largest.  The
